@@ -110,6 +110,13 @@ __device__ __forceinline__ uint4 silu_mul8(const float (&gv)[8], const float (&u
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Element types (lowbit_type of the C ABI) as they are stored and widened.
+typedef __bf16 bf16_t;
+template <int TYPE> struct Elem;
+template <> struct Elem<1> { typedef float type; };
+template <> struct Elem<2> { typedef _Float16 type; };
+template <> struct Elem<3> { typedef bf16_t type; };
+
 // y[0 .. count) = 0 by the threads gid = 0, stride, 2 stride, ... of a grid:
 // 16-byte stores (y is 16-byte aligned), then the count % 4 tail.
 __device__ __forceinline__ void zero_f32(float* y, int64_t count, int64_t gid, int64_t stride) {
@@ -217,6 +224,51 @@ size_t lm_head_workspace_bytes(int64_t n, int64_t k, int64_t b);
 hipError_t launch_lm_head(int fmt, const uint8_t* codes, const uint16_t* scales, int64_t n,
                           int64_t k, const uint16_t* x, int64_t b, float* y, int32_t* idx,
                           float* val, void* ws, hipStream_t st);
+
+// norms around a block with its gate and residual (arguments as in the C ABI)
+struct NormArgs {
+  const void* y;
+  const void* r;
+  void* r_out;
+  void* x_out;
+  const float *post_w, *post_b, *pre_w, *pre_b;
+  const void* gate;
+  int64_t ldy, ldr, ldro, ldx, ldg, m, k;
+  int y_type, r_type, x_type, gate_type, post, pre;
+  float scale, eps;
+};
+hipError_t launch_norm_residual(const NormArgs& a, hipStream_t st);
+
+// logits on their way to a token (arguments as in the C ABI)
+struct LogitsArgs {
+  const void* y;
+  const int32_t *tokens, *prompt_len, *total_len;
+  const float *repetition, *frequency, *presence;
+  const int32_t* bias_ids;
+  const float* bias_vals;
+  const int32_t *bias_len, *mask, *mask_row;
+  float* out;
+  int32_t* idx;
+  float* val;
+  int64_t ldy, n, b, tcap, ldt, bcap, ldb, mask_rows, ldm, ldo;
+  int y_type;
+};
+size_t logits_workspace_bytes(int64_t n, int64_t b);
+hipError_t launch_logits_process(const LogitsArgs& a, void* ws, hipStream_t st);
+
+// low-rank adapters beside a projection (arguments as in the C ABI)
+struct LoraArgs {
+  const void* x;
+  const int32_t* ids;
+  const void *a, *b;
+  const int32_t* ranks;
+  const float* scales;
+  void* y;
+  int64_t ldx, ldy, m, n, k, r, slots;
+  int x_type, y_type;
+};
+size_t lora_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_t r, int64_t slots);
+hipError_t launch_lora_accumulate(const LoraArgs& a, void* ws, hipStream_t st);
 
 hipError_t launch_gemm(int fmt, const uint8_t* codes, const uint16_t* scales, int64_t n,
                        int64_t k, const uint16_t* x, int64_t m, void* y, bool out_f32,

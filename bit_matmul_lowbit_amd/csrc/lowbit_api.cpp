@@ -30,6 +30,7 @@ namespace {
 
 constexpr int64_t kMaxElems = int64_t(1) << 40;
 constexpr int64_t kMaxK = int64_t(1) << 22;
+constexpr int64_t kMaxRows = int64_t(1) << 22;
 
 bool fmt_ok(int fmt) { return fmt == LOWBIT_FMT_Q1_G128 || fmt == LOWBIT_FMT_T2_G128; }
 
@@ -41,9 +42,31 @@ bool shape_ok(int64_t n, int64_t k) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+bool type_ok(int t) { return t == LOWBIT_F32 || t == LOWBIT_F16 || t == LOWBIT_BF16; }
+
+bool aligned_to_elem(const void* p, int type) {
+  return (reinterpret_cast<uintptr_t>(p) & (type == LOWBIT_F32 ? 3u : 1u)) == 0;
+}
+
+// rows of k elements at stride ld: no overlap, and every offset below 2^40
+bool rows_ok(int64_t m, int64_t k, int64_t ld) { return ld >= k && ld <= kMaxElems / m; }
+
 int64_t padded(int64_t n) { return (n + 15) / 16 * 16; }
 
 int hip_status(hipError_t e) { return e == hipSuccess ? LOWBIT_OK : LOWBIT_ERR_HIP; }
+
+bool logits_shape_ok(int64_t n, int64_t b) {
+  return n >= 1 && n <= (int64_t(1) << 31) - 1 && b >= 1 && b <= 65535 && n <= kMaxElems / b;
+}
+
+bool lora_shape_ok(int64_t m, int64_t n, int64_t k, int64_t r, int64_t slots) {
+  return m >= 1 && m <= kMaxRows && n >= 1 && n <= (int64_t(1) << 31) - 1 && k >= 8 && k <= kMaxK &&
+         k % 8 == 0 && r >= 8 && r <= 256 && r % 8 == 0 && slots >= 1 && slots <= 4096 &&
+         n <= kMaxElems / m && k <= kMaxElems / m && r * n <= kMaxElems / slots &&
+         r * k <= kMaxElems / slots;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 }  // namespace
 
@@ -329,6 +352,173 @@ int lowbit_base3_to_t2(const uint8_t* base3, const uint16_t* scales_rm, int64_t 
     return LOWBIT_ERR_ALIGN;
   return hip_status(lowbit::launch_base3_to_t2(base3, scales_rm, n, k,
                                                static_cast<uint8_t*>(codes), scales, stream));
+}
+
+int lowbit_norm_residual(const void* y, int y_type, int64_t ldy, const void* r, int r_type,
+                         int64_t ldr, void* r_out, int64_t ldro, void* x_out, int x_type,
+                         int64_t ldx, int64_t m, int64_t k, int post, const float* post_w,
+                         const float* post_b, const void* gate, int gate_type, int64_t ldg,
+                         float scale, int pre, const float* pre_w, const float* pre_b, float eps,
+                         hipStream_t stream) {
+  if (!r || (!r_out && !x_out) || !type_ok(r_type)) return LOWBIT_ERR_ARG;
+  if (y && (!type_ok(y_type) || post < LOWBIT_NORM_NONE || post > LOWBIT_NORM_LAYER))
+    return LOWBIT_ERR_ARG;
+  if (x_out && (!type_ok(x_type) || pre < LOWBIT_NORM_NONE || pre > LOWBIT_NORM_LAYER))
+    return LOWBIT_ERR_ARG;
+  if (y && gate && !type_ok(gate_type)) return LOWBIT_ERR_ARG;
+  if (!(eps >= 0.0f)) return LOWBIT_ERR_ARG;
+  if (m < 1 || m > kMaxRows || k < 1 || k > kMaxK) return LOWBIT_ERR_SHAPE;
+  if (!rows_ok(m, k, ldr) || (y && !rows_ok(m, k, ldy)) || (r_out && !rows_ok(m, k, ldro)) ||
+      (x_out && !rows_ok(m, k, ldx)) || (y && gate && ldg != 0 && !rows_ok(m, k, ldg)))
+    return LOWBIT_ERR_SHAPE;
+  // in place means row on row: another stride would write rows not yet read
+  if (r_out == r && ldro != ldr && m > 1) return LOWBIT_ERR_ARG;
+  if (x_out && (x_out == r || x_out == y || x_out == r_out)) return LOWBIT_ERR_ARG;
+  if (r_out && r_out == y) return LOWBIT_ERR_ARG;
+  if (!aligned_to_elem(r, r_type) || (y && !aligned_to_elem(y, y_type)) ||
+      (r_out && !aligned_to_elem(r_out, r_type)) || (x_out && !aligned_to_elem(x_out, x_type)) ||
+      (y && gate && !aligned_to_elem(gate, gate_type)) || !aligned_to_elem(post_w, LOWBIT_F32) ||
+      !aligned_to_elem(post_b, LOWBIT_F32) || !aligned_to_elem(pre_w, LOWBIT_F32) ||
+      !aligned_to_elem(pre_b, LOWBIT_F32))
+    return LOWBIT_ERR_ALIGN;
+  lowbit::NormArgs a = {};
+  a.y = y;
+  a.r = r;
+  a.r_out = r_out;
+  a.x_out = x_out;
+  // what is not used is cleared, so that the kernels see one form of it
+  a.post = y ? post : LOWBIT_NORM_NONE;
+  a.pre = x_out ? pre : LOWBIT_NORM_NONE;
+  a.post_w = a.post ? post_w : nullptr;
+  a.post_b = a.post ? post_b : nullptr;
+  a.pre_w = a.pre ? pre_w : nullptr;
+  a.pre_b = a.pre ? pre_b : nullptr;
+  a.gate = y ? gate : nullptr;
+  a.ldy = ldy;
+  a.ldr = ldr;
+  a.ldro = ldro;
+  a.ldx = ldx;
+  a.ldg = ldg;
+  a.m = m;
+  a.k = k;
+  a.y_type = y ? y_type : r_type;
+  a.r_type = r_type;
+  a.x_type = x_out ? x_type : LOWBIT_F32;
+  a.gate_type = a.gate ? gate_type : LOWBIT_F32;
+  a.scale = scale;
+  a.eps = eps;
+  return hip_status(lowbit::launch_norm_residual(a, stream));
+}
+
+size_t lowbit_logits_workspace_bytes(int64_t n, int64_t b) {
+  return logits_shape_ok(n, b) ? lowbit::logits_workspace_bytes(n, b) : 0;
+}
+
+int lowbit_logits_process(const void* y, int y_type, int64_t ldy, int64_t n, int64_t b,
+                          const int32_t* tokens, int64_t tcap, int64_t ldt,
+                          const int32_t* prompt_len, const int32_t* total_len,
+                          const float* repetition, const float* frequency, const float* presence,
+                          const int32_t* bias_ids, const float* bias_vals, int64_t bcap, int64_t ldb,
+                          const int32_t* bias_len, const int32_t* mask, int64_t mask_rows,
+                          int64_t ldm, const int32_t* mask_row, float* out, int64_t ldo,
+                          int32_t* idx, float* val, void* workspace, size_t workspace_bytes,
+                          hipStream_t stream) {
+  if (!y || !type_ok(y_type) || (!out && !idx) || (val && !idx)) return LOWBIT_ERR_ARG;
+  if (!bias_ids != !bias_vals) return LOWBIT_ERR_ARG;
+  if (!logits_shape_ok(n, b) || !rows_ok(b, n, ldy) || (out && !rows_ok(b, n, ldo)))
+    return LOWBIT_ERR_SHAPE;
+  constexpr int64_t kMaxList = int64_t(1) << 30;
+  if (tokens && (tcap < 0 || tcap >= kMaxList || !rows_ok(b, tcap, ldt))) return LOWBIT_ERR_SHAPE;
+  if (bias_ids && (bcap < 0 || bcap >= kMaxList || !rows_ok(b, bcap, ldb))) return LOWBIT_ERR_SHAPE;
+  if (mask) {
+    if (mask_rows < 1 || mask_rows > kMaxElems || !rows_ok(mask_rows, (n + 31) / 32, ldm))
+      return LOWBIT_ERR_SHAPE;
+  }
+  // in place means row on row, in one type
+  if (out && out == y && (y_type != LOWBIT_F32 || (ldo != ldy && b > 1))) return LOWBIT_ERR_ARG;
+  if (!aligned_to_elem(y, y_type) || !aligned4(tokens) || !aligned4(prompt_len) ||
+      !aligned4(total_len) || !aligned4(repetition) || !aligned4(frequency) || !aligned4(presence) ||
+      !aligned4(bias_ids) || !aligned4(bias_vals) || !aligned4(bias_len) || !aligned4(mask) ||
+      !aligned4(mask_row) || !aligned4(out) || !aligned4(idx) || !aligned4(val))
+    return LOWBIT_ERR_ALIGN;
+  if (idx) {
+    if (!workspace || workspace_bytes < lowbit::logits_workspace_bytes(n, b))
+      return LOWBIT_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return LOWBIT_ERR_ALIGN;
+  }
+  lowbit::LogitsArgs a = {};
+  a.y = y;
+  // an empty list is no list
+  if (tokens && tcap > 0) {
+    a.tokens = tokens;
+    a.prompt_len = prompt_len;
+    a.total_len = total_len;
+    a.tcap = tcap;
+    a.ldt = ldt;
+  }
+  a.repetition = repetition;
+  a.frequency = frequency;
+  a.presence = presence;
+  if (bias_ids && bcap > 0) {
+    a.bias_ids = bias_ids;
+    a.bias_vals = bias_vals;
+    a.bias_len = bias_len;
+    a.bcap = bcap;
+    a.ldb = ldb;
+  }
+  a.mask = mask;
+  a.mask_row = mask_row;
+  a.mask_rows = mask_rows;
+  a.ldm = ldm;
+  a.out = out;
+  a.ldo = ldo;
+  a.idx = idx;
+  a.val = val;
+  a.y_type = y_type;
+  a.ldy = ldy;
+  a.n = n;
+  a.b = b;
+  return hip_status(lowbit::launch_logits_process(a, workspace, stream));
+}
+
+size_t lowbit_lora_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_t r, int64_t slots) {
+  return lora_shape_ok(m, n, k, r, slots) ? lowbit::lora_workspace_bytes(m, n, k, r, slots) : 0;
+}
+
+int lowbit_lora_accumulate(const void* x, int x_type, int64_t ldx, const int32_t* ids, int64_t m,
+                           int64_t n, int64_t k, int64_t r, int64_t slots, const void* a,
+                           const void* b, const int32_t* ranks, const float* scales, void* y,
+                           int y_type, int64_t ldy, void* workspace, size_t workspace_bytes,
+                           hipStream_t stream) {
+  if (!x || !ids || !a || !b || !y) return LOWBIT_ERR_ARG;
+  if (x_type != LOWBIT_F16 && x_type != LOWBIT_BF16) return LOWBIT_ERR_ARG;
+  if (y_type != LOWBIT_F32 && !(y_type == LOWBIT_BF16 && x_type == LOWBIT_BF16)) return LOWBIT_ERR_ARG;
+  if (!lora_shape_ok(m, n, k, r, slots) || !rows_ok(m, k, ldx) || !rows_ok(m, n, ldy))
+    return LOWBIT_ERR_SHAPE;
+  if (!aligned16(x) || ldx % 8 != 0 || !aligned16(a) || !aligned16(b) || !aligned4(ids) ||
+      !aligned4(ranks) || !aligned4(scales) || !aligned_to_elem(y, y_type))
+    return LOWBIT_ERR_ALIGN;
+  if (!workspace || workspace_bytes < lowbit::lora_workspace_bytes(m, n, k, r, slots))
+    return LOWBIT_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return LOWBIT_ERR_ALIGN;
+  lowbit::LoraArgs q = {};
+  q.x = x;
+  q.ids = ids;
+  q.a = a;
+  q.b = b;
+  q.ranks = ranks;
+  q.scales = scales;
+  q.y = y;
+  q.ldx = ldx;
+  q.ldy = ldy;
+  q.m = m;
+  q.n = n;
+  q.k = k;
+  q.r = r;
+  q.slots = slots;
+  q.x_type = x_type;
+  q.y_type = y_type;
+  return hip_status(lowbit::launch_lora_accumulate(q, workspace, stream));
 }
 
 }  // extern "C"

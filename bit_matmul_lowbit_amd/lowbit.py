@@ -28,7 +28,11 @@ SYMBOLS = [
     "lowbit_gemv", "lowbit_gemv_noalloc", "lowbit_gemm", "lowbit_gemm_f32", "lowbit_silu_mul",
     "lowbit_ffn_workspace_bytes", "lowbit_ffn", "lowbit_embed", "lowbit_argmax_workspace_bytes",
     "lowbit_argmax", "lowbit_lm_head_workspace_bytes", "lowbit_lm_head",
+    "lowbit_norm_residual", "lowbit_logits_workspace_bytes", "lowbit_logits_process",
+    "lowbit_lora_workspace_bytes", "lowbit_lora_accumulate",
 ]
+
+NORMS = {"none": 0, "rms": 1, "layer": 2}
 
 
 # ceiling probes (include/lowbit_probes.h): context for the roofline only
@@ -62,6 +66,7 @@ def load() -> ctypes.CDLL:
 
     lib = ctypes.CDLL(LIB_PATH)
     p, i64, sz, i = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
+    f = ctypes.c_float
     sig = {
         "lowbit_version": ([], i),
         "lowbit_status_str": ([i], ctypes.c_char_p),
@@ -86,6 +91,14 @@ def load() -> ctypes.CDLL:
         "lowbit_argmax": ([p, i64, i64, p, p, p, sz, p], i),
         "lowbit_lm_head_workspace_bytes": ([i, i64, i64, i64], sz),
         "lowbit_lm_head": ([i, p, p, i64, i64, p, i64, p, p, p, p, sz, p], i),
+        "lowbit_norm_residual": ([p, i, i64, p, i, i64, p, i64, p, i, i64, i64, i64, i, p, p, p, i,
+                                  i64, f, i, p, p, f, p], i),
+        "lowbit_logits_workspace_bytes": ([i64, i64], sz),
+        "lowbit_logits_process": ([p, i, i64, i64, i64, p, i64, i64, p, p, p, p, p, p, p, i64, i64, p, p,
+                                   i64, i64, p, p, i64, p, p, p, sz, p], i),
+        "lowbit_lora_workspace_bytes": ([i64, i64, i64, i64, i64], sz),
+        "lowbit_lora_accumulate": ([p, i, i64, p, i64, i64, i64, i64, i64, p, p, p, p, p, i, i64, p, sz,
+                                    p], i),
         "lowbit_quantize_t2": ([p, i64, i64, p, p, p], i),
         "lowbit_base3_bytes": ([i64, i64], sz),
         "lowbit_t2_to_base3": ([p, p, i64, i64, p, p, p], i),
@@ -534,6 +547,258 @@ def lowbit_base3_to_t2(b3, scales_rm, n: int, k: int, codes=None, scales=None, s
                                      _dev(scales, (torch.float16, torch.int16), "scales"),
                                      _stream(stream)), "lowbit_base3_to_t2")
     return codes, scales
+
+
+# ---------------------------------------------------------------------------
+# operators beside the products.  They take row strides, run on the device
+# their tensors are on (also when it is not the current one) and pass plain
+# integers, since a decode step makes many such calls.
+
+_types = {}
+
+
+def _type_codes():
+    """torch dtype -> lowbit_type, filled on first use (importing this module
+    loads nothing)."""
+    if not _types:
+        import torch
+
+        _types.update({torch.float32: 1, torch.float16: 2, torch.bfloat16: 3})
+    return _types
+
+
+def _float_rows(t, name, shape=None, device=None):
+    """(pointer, type code, row stride, rows, columns) of a 1-D or 2-D
+    FP32 / FP16 / BF16 device tensor whose rows are contiguous."""
+    code = _type_codes().get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected float32, float16 or bfloat16")
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    dims = t.dim()
+    if dims == 2:
+        m, k = t.shape
+        ld, unit = t.stride()
+        if m == 1:
+            ld = k
+    elif dims == 1:
+        m, k, unit = 1, t.shape[0], t.stride(0)
+        ld = k
+    else:
+        raise ValueError(f"{name} must have one or two dimensions")
+    if unit != 1 and k != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    if shape is not None and (m, k) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return t.data_ptr(), code, ld, m, k
+
+
+def _vector(t, dtype, count, name, device):
+    """Pointer of a contiguous device vector of at least `count` elements, or
+    None (NULL) for None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor of {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.numel() < count:
+        raise ValueError(f"{name} holds {t.numel()} elements, needs at least {count}")
+    return t.data_ptr()
+
+
+def _lists(t, dtype, b, name, device):
+    """(pointer, columns, row stride) of a [b][columns] device tensor with
+    contiguous rows, or (None, 0, 0) for None."""
+    if t is None:
+        return None, 0, 0
+    if t.dtype != dtype or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor of {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dim() != 2 or (b is not None and t.shape[0] != b):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {b} rows")
+    cols = t.shape[1]
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return t.data_ptr(), cols, max(ld, cols) if t.shape[0] == 1 else ld
+
+
+def _call(where, device, stream, *args, keep=()):
+    """Call library function `where` on `stream` (default: the device's
+    current one) with `device` current.  `keep`: tensors allocated here that
+    the kernels use; the allocator is told when the stream is not the one
+    they belong to."""
+    import torch
+
+    index = device.index
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        raw = stream.cuda_stream
+        for t in keep:
+            t.record_stream(stream)
+    fn = getattr(load(), where)
+    if index == torch._C._cuda_getDevice():
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, raw)
+    if status != 0:
+        raise LowbitError(status, where)
+
+
+def lowbit_norm_residual(y, r, post="none", post_w=None, post_b=None, gate=None, scale=1.0,
+                         pre=None, pre_w=None, pre_b=None, eps=1e-6, r_out=None, x_out=None,
+                         x_dtype=None, stream=None):
+    """r' = r + scale * gate * post(y) and x = pre(r'), one launch; returns
+    (r_out, x_out).
+
+    y [m][k] (a block's output) or None: then r is only normed.  r [m][k]: the
+    residual stream, updated in place unless r_out is given.  post / pre:
+    "none", "rms" or "layer" with FP32 weights and biases [k] (None: 1 and
+    0); pre=None makes no x.  gate: [k] for every row or [m][k].  x_out is
+    allocated with x_dtype (FP16, as lowbit_gemv reads it, if not given)."""
+    import torch
+
+    rp, rt, ldr, m, k = _float_rows(r, "r")
+    dev, shape = r.device, (m, k)
+    f32 = torch.float32
+    yp = yt = ldy = gp = gt = ldg = rop = ldro = 0
+    post_c = pre_c = 0
+    if y is not None:
+        post_c = NORMS[post]
+        yp, yt, ldy, _, _ = _float_rows(y, "y", shape, dev)
+        if gate is not None:
+            if gate.dim() == 1:
+                gp, gt, _, _, _ = _float_rows(gate, "gate", (1, k), dev)
+            else:
+                gp, gt, ldg, _, _ = _float_rows(gate, "gate", shape, dev)
+        if r_out is None:
+            r_out, rop, ldro = r, rp, ldr
+        else:
+            rop, rot, ldro, _, _ = _float_rows(r_out, "r_out", shape, dev)
+            if rot != rt:
+                raise TypeError("r_out must have the type of r")
+    elif r_out is not None:
+        raise ValueError("r_out needs y")
+    xp = xt = ldx = 0
+    if pre is not None:
+        pre_c = NORMS[pre]
+        if x_out is None:
+            x_out = torch.empty(r.shape, dtype=x_dtype or torch.float16, device=dev)
+        xp, xt, ldx, _, _ = _float_rows(x_out, "x_out", shape, dev)
+    elif x_out is not None:
+        raise ValueError("x_out needs pre")
+    _call("lowbit_norm_residual", dev, stream, yp, yt, ldy, rp, rt, ldr, rop, ldro, xp, xt, ldx, m, k,
+          post_c, _vector(post_w, f32, k, "post_w", dev), _vector(post_b, f32, k, "post_b", dev),
+          gp, gt, ldg, scale, pre_c, _vector(pre_w, f32, k, "pre_w", dev),
+          _vector(pre_b, f32, k, "pre_b", dev), eps, keep=() if x_out is None else (x_out,))
+    return (r_out if y is not None else r), x_out
+
+
+def lowbit_logits_workspace_bytes(n: int, b: int) -> int:
+    return int(load().lowbit_logits_workspace_bytes(n, b))
+
+
+def lowbit_logits_process(y, tokens=None, prompt_len=None, total_len=None, repetition=None,
+                          frequency=None, presence=None, bias_ids=None, bias_vals=None,
+                          bias_len=None, mask=None, mask_row=None, out=None, top1=True, idx=None,
+                          val=None, workspace=None, stream=None):
+    """Biases, penalties for repeated tokens and a grammar mask on logits y
+    [b][n], with the top-1 of the result; returns (out, idx, val).
+
+    out [b][n] FP32 takes the processed logits (y itself: in place; None: they
+    are not stored); idx int32 [b] and val FP32 [b] take the top-1 unless
+    top1 is False.  tokens int32 [b][.] with prompt_len / total_len int32 [b];
+    repetition / frequency / presence FP32 [b]; bias_ids int32 and bias_vals
+    FP32 [b][.] with bias_len int32 [b]; mask int32 [rows][>= n / 32] with
+    mask_row int32 [b]."""
+    import torch
+
+    yp, yt, ldy, b, n = _float_rows(y, "y")
+    dev, f32, i32 = y.device, torch.float32, torch.int32
+    tp, tcap, ldt = _lists(tokens, i32, b, "tokens", dev)
+    bp, bcap, ldb = _lists(bias_ids, i32, b, "bias_ids", dev)
+    bv, bvcap, ldbv = _lists(bias_vals, f32, b, "bias_vals", dev)
+    if bcap != bvcap or (b > 1 and ldb != ldbv):
+        raise ValueError("bias_ids and bias_vals must have one shape and row stride")
+    mp, words, ldm = _lists(mask, i32, None if mask_row is not None else b, "mask", dev)
+    if mask is not None and words < (n + 31) // 32:
+        raise ValueError(f"mask has {words} words a row, needs {(n + 31) // 32}")
+    op = ldo = 0
+    if out is not None:
+        op, ot, ldo, _, _ = _float_rows(out, "out", (b, n), dev)
+        if out.dtype != f32:
+            raise TypeError("out must be float32")
+    need = 0
+    made = ()
+    if top1:
+        if idx is None:
+            idx = torch.empty(b, dtype=i32, device=dev)
+            made += (idx,)
+        if val is None:
+            val = torch.empty(b, dtype=f32, device=dev)
+            made += (val,)
+        if workspace is None:
+            need = lowbit_logits_workspace_bytes(n, b)
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+            made += (workspace,)
+        need = workspace.numel()
+    elif idx is not None or val is not None:
+        raise ValueError("idx and val need top1")
+    _call("lowbit_logits_process", dev, stream, yp, yt, ldy, n, b, tp, tcap, ldt,
+          _vector(prompt_len, i32, b, "prompt_len", dev), _vector(total_len, i32, b, "total_len", dev),
+          _vector(repetition, f32, b, "repetition", dev), _vector(frequency, f32, b, "frequency", dev),
+          _vector(presence, f32, b, "presence", dev), bp, bv, bcap, ldb,
+          _vector(bias_len, i32, b, "bias_len", dev), mp, 0 if mask is None else mask.shape[0], ldm,
+          _vector(mask_row, i32, b, "mask_row", dev), op, ldo, _vector(idx, i32, b, "idx", dev),
+          _vector(val, f32, b, "val", dev),
+          _vector(workspace, torch.uint8, 0, "workspace", dev) if top1 else None, need, keep=made)
+    return out, idx, val
+
+
+def lowbit_lora_workspace_bytes(m: int, n: int, k: int, r: int, slots: int) -> int:
+    return int(load().lowbit_lora_workspace_bytes(m, n, k, r, slots))
+
+
+def lowbit_lora_accumulate(x, ids, a, b, y, ranks=None, scales=None, workspace=None, stream=None):
+    """y[i] += scales[s] * B[s] (A[s] x[i]) with s = ids[i], in place; returns y.
+
+    x [m][k] FP16 or BF16, ids int32 [m] (outside [0, slots): no adapter), a
+    [slots][r][k] and b [slots][n][r] in x's type, ranks int32 [slots], scales
+    FP32 [slots], y [m][n] FP32 (or BF16 with BF16 x); rows of x and y may be
+    strided (a slice of a fused projection's output)."""
+    import torch
+
+    xp, xt, ldx, m, k = _float_rows(x, "x")
+    dev = x.device
+    yp, yt, ldy, ym, n = _float_rows(y, "y", None, dev)
+    if ym != m:
+        raise ValueError(f"y has {ym} rows, x has {m}")
+    if a.dim() != 3 or b.dim() != 3:
+        raise ValueError("a must be [slots][r][k] and b [slots][n][r]")
+    slots, r, _ = a.shape
+    if a.shape[2] != k or tuple(b.shape) != (slots, n, r):
+        raise ValueError(f"a {tuple(a.shape)} and b {tuple(b.shape)} do not fit x {tuple(x.shape)} "
+                         f"and y {tuple(y.shape)}")
+    need = workspace.numel() if workspace is not None else 0
+    made = ()
+    if workspace is None:
+        need = lowbit_lora_workspace_bytes(m, n, k, r, slots)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        made = (workspace,)
+    _call("lowbit_lora_accumulate", dev, stream, xp, xt, ldx, _vector(ids, torch.int32, m, "ids", dev), m,
+          n, k, r, slots, _vector(a, x.dtype, 0, "a", dev), _vector(b, x.dtype, 0, "b", dev),
+          _vector(ranks, torch.int32, slots, "ranks", dev),
+          _vector(scales, torch.float32, slots, "scales", dev), yp, yt, ldy,
+          _vector(workspace, torch.uint8, 0, "workspace", dev), need, keep=made)
+    return y
 
 
 # ---------------------------------------------------------------------------

@@ -80,7 +80,8 @@
  *   - Shapes: n >= 1, k >= 128 and k % 128 == 0, n*k < 2^40; GEMV batch
  *     1 <= b <= 8; GEMM m >= 1.
  *   - Alignment: codes, scales, x, y, w and workspace pointers must be 16-byte
- *     aligned (torch's allocator gives 256).
+ *     aligned (torch's allocator gives 256), unless an entry point says
+ *     otherwise.
  *   - Buffers of one call must not overlap, except that read-only inputs may
  *     alias each other.  Calls on different streams that share an output or
  *     a workspace race.
@@ -112,6 +113,21 @@ typedef enum {
   LOWBIT_ERR_WORKSPACE = 6,   /* workspace missing or smaller than required  */
   LOWBIT_ERR_SCRATCH = 7      /* needs more than lowbit_gemv_noalloc's scratch */
 } lowbit_status;
+
+/* Element types of the operators that take more than one. */
+typedef enum {
+  LOWBIT_F32 = 1, /* FP32 */
+  LOWBIT_F16 = 2, /* FP16 (IEEE binary16) */
+  LOWBIT_BF16 = 3 /* BF16 */
+} lowbit_type;
+
+/* Normalisation of lowbit_norm_residual. */
+typedef enum {
+  LOWBIT_NORM_NONE = 0, /* v unchanged                                        */
+  LOWBIT_NORM_RMS = 1,  /* v / sqrt(mean(v^2) + eps) * w + b                  */
+  LOWBIT_NORM_LAYER = 2 /* (v - mean(v)) / sqrt(var(v) + eps) * w + b,
+                           var(v) = mean((v - mean(v))^2)                     */
+} lowbit_norm;
 
 /* Library ABI version (this header describes version 1). */
 int lowbit_version(void);
@@ -363,6 +379,123 @@ int lowbit_lm_head(int fmt, const void* codes, const uint16_t* scales, int64_t n
                    const uint16_t* x_fp16, int64_t b, float* y_f32, int32_t* idx_out,
                    float* val_out, void* workspace, size_t workspace_bytes,
                    hipStream_t stream);
+
+/* The norms around a block, its gate and the residual add, in one pass
+ * [P2 "Como funciona la compresion": every projection of a block is
+ * low-bit; what lies between two blocks is not and is done here].  Row i of
+ * m rows of k elements:
+ *   u     = norm_post(y[i])                 (u = 0 when y is NULL)
+ *   r'    = r[i] + scale * gate[i] * u      (gate = 1 when NULL)
+ *   r_out[i] = r' rounded to r_type         (skipped when r_out is NULL)
+ *   x_out[i] = norm_pre(r') rounded to x_type   (skipped when x_out is NULL)
+ * norm_pre sees r' in FP32, not its rounded copy.  All arithmetic is FP32
+ * with one rounding (nearest-even) per stored value; the sums of a row are
+ * added in a fixed order, so equal inputs give equal outputs.
+ *   y      : [m] rows of k at stride ldy, y_type (what lowbit_ffn,
+ *            lowbit_gemv or lowbit_gemm gave), read-only, or NULL; with y
+ *            NULL, post, post_w, post_b, gate and scale are not used
+ *   r      : [m] rows at stride ldr, r_type: the residual stream
+ *   r_out  : [m] rows at stride ldro, r_type, or NULL; may be r itself
+ *            (same pointer and stride)
+ *   x_out  : [m] rows at stride ldx, x_type, or NULL: the next block's x
+ *   post, pre           : a lowbit_norm each
+ *   post_w, post_b, pre_w, pre_b : [k] FP32, or NULL (w = 1, b = 0); not
+ *            used with LOWBIT_NORM_NONE
+ *   gate   : gate_type; one row of k for every i when ldg is 0, else [m]
+ *            rows at stride ldg; or NULL
+ * Strides count elements and are at least k (or 0 for ldg).  1 <= m <= 2^22,
+ * 1 <= k <= 2^22, m * stride < 2^40.  At least one of r_out and x_out is
+ * given.  Pointers need their element's alignment only; rows whose
+ * pointers and strides are multiples of 16 bytes are read 16 bytes at a
+ * time.  eps >= 0. */
+int lowbit_norm_residual(const void* y, int y_type, int64_t ldy, const void* r, int r_type,
+                         int64_t ldr, void* r_out, int64_t ldro, void* x_out, int x_type,
+                         int64_t ldx, int64_t m, int64_t k, int post, const float* post_w,
+                         const float* post_b, const void* gate, int gate_type, int64_t ldg,
+                         float scale, int pre, const float* pre_w, const float* pre_b, float eps,
+                         hipStream_t stream);
+
+/* Workspace bytes lowbit_logits_process needs to find the top-1 for (n, b);
+ * 0 on a bad shape. */
+size_t lowbit_logits_workspace_bytes(int64_t n, int64_t b);
+
+/* Logits on their way to a token: biases, penalties for repeated tokens and
+ * a grammar's mask, with the top-1 of the result, in one pass over y
+ * [P5 "Detalles tecnicos": decode is checked by top-1 token match].  For
+ * token t of row i, in this order and each operation rounded to FP32:
+ *   v = y[i][t] + bias            bias: the sum of row i's entries with id t,
+ *                                 in the list's order
+ *   t anywhere in row i's tokens: v = v > 0 ? v / repetition : v * repetition
+ *   t after the prompt, c times:  v = (v - frequency * c) - presence
+ *   the mask's bit for t is 0:    v = -inf (whatever v was, NaN too)
+ *   y         : [b] rows of n logits at stride ldy, y_type (read-only)
+ *   tokens    : [b] rows of tcap int32 at stride ldt, or NULL (no penalties);
+ *               of row i the first total_len[i] count (all if total_len is
+ *               NULL), the first prompt_len[i] of them as prompt (none if
+ *               NULL); lengths are cut to [0, tcap], ids outside [0, n) are
+ *               passed over
+ *   repetition, frequency, presence : [b] FP32, or NULL (1, 0, 0)
+ *   bias_ids, bias_vals : [b] rows of bcap entries at stride ldb, or both
+ *               NULL; of row i the first bias_len[i] count (all if NULL); ids
+ *               outside [0, n) are passed over
+ *   mask      : mask_rows rows of at least ceil(n / 32) int32 words at
+ *               stride ldm, bit t % 32 of word t / 32 for token t (1:
+ *               allowed), or NULL.  Row i follows mask row mask_row[i] (i if
+ *               mask_row is NULL); a negative one: row i is not masked, one
+ *               past the last: nothing is allowed
+ *   out       : [b] rows of n FP32 at stride ldo (device, written), or NULL;
+ *               may be y itself (FP32, same stride)
+ *   idx       : [b] int32 (device, written), or NULL: the lowest allowed
+ *               token of the largest value, NaN counting as largest, -0 equal
+ *               to +0; -1 if the mask allows nothing
+ *   val       : [b] FP32 or NULL: the value at idx (a zero as +0), -inf if
+ *               the mask allows nothing; not written without idx
+ *   workspace : lowbit_logits_workspace_bytes(n, b) bytes, contents ignored
+ *               on entry; not used (NULL allowed) without idx
+ * At least one of out and idx is given.  n < 2^31, b <= 65535, tcap, bcap
+ * < 2^30.  Pointers other than the workspace need their element's alignment
+ * only.  Equal inputs give equal bits. */
+int lowbit_logits_process(const void* y, int y_type, int64_t ldy, int64_t n, int64_t b,
+                          const int32_t* tokens, int64_t tcap, int64_t ldt,
+                          const int32_t* prompt_len, const int32_t* total_len,
+                          const float* repetition, const float* frequency, const float* presence,
+                          const int32_t* bias_ids, const float* bias_vals, int64_t bcap, int64_t ldb,
+                          const int32_t* bias_len, const int32_t* mask, int64_t mask_rows,
+                          int64_t ldm, const int32_t* mask_row, float* out, int64_t ldo,
+                          int32_t* idx, float* val, void* workspace, size_t workspace_bytes,
+                          hipStream_t stream);
+
+/* Workspace bytes lowbit_lora_accumulate needs; 0 on a bad shape. */
+size_t lowbit_lora_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_t r, int64_t slots);
+
+/* Low-rank adapters of many requests beside a shared projection  [P2 "Como
+ * funciona la compresion": the projections are low-bit and frozen; what is
+ * learned on top of them is kept apart]: adds to y, which holds W.x of
+ * lowbit_gemv, lowbit_gemm or lowbit_gemm_f32, for every row i with an
+ * adapter s = ids[i]
+ *   y[i][o] += scales[s] * sum_{j < ranks[s]} B[s][o][j] sum_k A[s][j][k] x[i][k]
+ *   x      : [m] rows of k at stride ldx, x_type FP16 or BF16 (read-only)
+ *   ids    : [m] int32: the row's adapter; a row whose id is outside
+ *            [0, slots) is left as it is
+ *   a, b   : [slots][r][k] and [slots][n][r], x_type
+ *   ranks  : [slots] int32 or NULL (r); cut to [0, r].  Entries of A and B at
+ *            or past the rank are not used
+ *   scales : [slots] FP32 or NULL (1)
+ *   y      : [m] rows of n at stride ldy, read and written in place: FP32,
+ *            or, with BF16 x, BF16
+ * Products are of the stored values, sums and the result of the first
+ * product are FP32 (or pairs that hold as much), and y is rounded once.  No
+ * atomics; equal inputs give equal bits.  Rows may come in any order and
+ * adapters be shared by any of them.
+ * 1 <= m <= 2^22, n < 2^31, k a multiple of 8, r a multiple of 8 up to 256,
+ * 1 <= slots <= 4096, every extent below 2^40 elements.  x, a, b and
+ * workspace are 16-byte aligned, ldx is a multiple of 8; y needs its
+ * element's alignment only. */
+int lowbit_lora_accumulate(const void* x, int x_type, int64_t ldx, const int32_t* ids, int64_t m,
+                           int64_t n, int64_t k, int64_t r, int64_t slots, const void* a,
+                           const void* b, const int32_t* ranks, const float* scales, void* y,
+                           int y_type, int64_t ldy, void* workspace, size_t workspace_bytes,
+                           hipStream_t stream);
 
 #ifdef __cplusplus
 }
