@@ -1,17 +1,64 @@
 // Low-rank adapters of many requests beside a shared low-bit projection:
 //   v[i][j]  = scale[s] * sum_k A[s][j][k] x[i][k],  s = ids[i], j < rank[s]
 //   y[i][o] += sum_j B[s][o][j] v[i][j]
-// The first product ("shrink") leaves v in the workspace as FP32, the second
-// ("expand") adds to y in place.  No atomics: every v and every y element has
-// one writer.
 //
 // [P2] 7minutos.es, "PrismML lanza Bonsai 27B ...", "Como funciona la
 //      compresion": every projection of the model is a frozen low-bit matrix;
 //      what is learned on top of it lives in such adapters.
+//
+// Rows are grouped by adapter, so that an adapter's matrices meet all of its
+// rows at once.  An item is up to 64 rows of one adapter (32 where r > 128).
+// With m <= 64 every work-group finds its item itself: the ids of all rows
+// fit one wave, and ballots pick out the rows that share one (no launch, no
+// memory).  More rows are sorted by one work-group first (lora_plan_kernel).
+//
+// Both products run on v_mfma_f32_16x16x32 with operands straight from
+// memory: A and B are stored with the contracted index innermost, so a
+// lane's 8 operand values are 16 contiguous bytes.
+//   A operand (16 x 32): lane l holds row l % 16, 8 values at 8 (l / 16)
+//   B operand (32 x 16): lane l holds column l % 16, 8 values at 8 (l / 16)
+//   D (16 x 16): lane l, register e holds row 4 (l / 16) + e, column l % 16
+//
+// shrink: v^T = A x^T, one work-group per (16 rows of an item, up to 64 of
+// its ranks, slice of k); its eight waves split the slice and are summed
+// through LDS.  The slices' FP32 sums go to the workspace.
+// expand: y^T += B v^T, one work-group per (item, 256 outputs).  v is summed
+// over the slices, scaled, and split into 16-bit pieces whose sum holds it to
+// FP32's precision or nearly (FP16: two pieces of a row scaled by a power of
+// two, 22 bits; BF16: three pieces, 24 bits), since a single 16-bit v would
+// be the least exact value of the whole sum.  No atomics anywhere: every
+// value has one writer and its sum one order.
 #include "common.h"
 
 namespace lowbit {
 namespace {
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kInlineRows = 64;  // rows whose grouping one wave finds by itself
+constexpr int kShrinkWaves = 8;
+constexpr int kTilesN = 4;                 // 16-output tiles of a wave in expand
+constexpr int kWaveN = 16 * kTilesN;       // 64 outputs per wave
+constexpr int kBlockN = 4 * kWaveN;        // 256 outputs per work-group
+constexpr int kMaxSlots = 4096;
+
+template <int XT> struct Mma;
+template <> struct Mma<2> {
+  static constexpr int pieces = 2;
+  static __device__ __forceinline__ f32x4 run(uint4 a, uint4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  }
+};
+template <> struct Mma<3> {
+  static constexpr int pieces = 3;
+  static __device__ __forceinline__ f32x4 run(uint4 a, uint4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  }
+};
 
 __device__ __forceinline__ int rank_of(const LoraArgs& a, int64_t s) {
   if (!a.ranks) return (int)a.r;
@@ -19,71 +66,471 @@ __device__ __forceinline__ int rank_of(const LoraArgs& a, int64_t s) {
   return v < 0 ? 0 : (v > (int)a.r ? (int)a.r : v);
 }
 
-// one wave per (row, j)
-template <int XT>
-__global__ __launch_bounds__(256) void lora_shrink_kernel(LoraArgs a, float* __restrict__ v) {
-  typedef typename Elem<XT>::type T;
-  const int64_t i = blockIdx.x;
-  const int64_t s = a.ids[i];
-  if (s < 0 || s >= a.slots) return;
-  const int rank = rank_of(a, s);
-  const T* x = static_cast<const T*>(a.x) + i * a.ldx;
-  const int lane = threadIdx.x & 63;
-  for (int j = threadIdx.x >> 6; j < rank; j += 4) {
-    const T* w = static_cast<const T*>(a.a) + (s * a.r + j) * a.k;
-    float acc = 0.0f;
-    for (int64_t c = lane; c < a.k; c += 64) acc += (float)w[c] * (float)x[c];
+// the row's adapter, or -1 for a row that nothing is added to
+__device__ __forceinline__ int slot_of(const LoraArgs& a, int64_t i) {
+  const int s = a.ids[i];
+  return s >= 0 && s < a.slots && rank_of(a, s) > 0 ? s : -1;
+}
+
+__device__ __forceinline__ int lanes_below(uint64_t mask) {
+  return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
+                                        __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
+}
+
+// What the plan of more than kInlineRows rows holds, at the head of the
+// workspace: the number of items, the items, and the rows in item order.
+struct Item {
+  int slot, start, count, unused;
+};
+struct Plan {
+  int* items_used;
+  Item* items;
+  int* rows;
+};
+
+// Item number `item`: its adapter and row count (0: there is none), and its
+// rows in rows[0 .. count) (LDS).  Ends in a barrier if there is one.
+template <bool INLINE>
+__device__ __forceinline__ int find_item(const LoraArgs& a, const Plan& plan, int item, int tm,
+                                         int* rows, int* slot) {
+  int count = 0;
+  if constexpr (INLINE) {
+    const int lane = threadIdx.x & 63;
+    const int s = lane < a.m ? slot_of(a, lane) : -1;
+    uint64_t left = __ballot(s >= 0);
+    uint64_t mine = 0;
+    int seen = 0;
+    while (left) {
+      const int ls = __builtin_amdgcn_readlane(s, __builtin_ctzll(left));
+      const uint64_t same = __ballot(s == ls);
+      const int n = __popcll(same), parts = (n + tm - 1) / tm;
+      if (item < seen + parts) {
+        const int first = (item - seen) * tm;
+        count = n - first < tm ? n - first : tm;
+        *slot = ls;
+        mine = same;
+        const int at = lanes_below(mine) - first;
+        if (threadIdx.x < 64 && ((mine >> lane) & 1) && at >= 0 && at < count) rows[at] = lane;
+        break;
+      }
+      seen += parts;
+      left &= ~same;
+    }
+  } else {
+    if (item < *plan.items_used) {
+      const Item it = plan.items[item];
+      count = it.count;
+      *slot = it.slot;
+      if ((int)threadIdx.x < count) rows[threadIdx.x] = plan.rows[it.start + threadIdx.x];
+    }
+  }
+  if (count) __syncthreads();
+  return count;
+}
+
+// Rows sorted by adapter, in one work-group: a histogram over the adapters
+// (LDS; the rows of a wave that share one add to it once), its prefix sums,
+// then each row's place.  Rows of one adapter keep nearly their order; which
+// one they get changes no result, each row being a column of its own.
+__global__ __launch_bounds__(1024) void lora_plan_kernel(LoraArgs a, Plan plan, int tm) {
+  __shared__ int cnt[kMaxSlots];
+  __shared__ uint64_t wave_sum[16];
+  const int tid = threadIdx.x, lane = tid & 63;
+  for (int s = tid; s < a.slots; s += 1024) cnt[s] = 0;
+  __syncthreads();
+  const int64_t steps = (a.m + 1023) / 1024;
+  for (int64_t t = 0; t < steps; ++t) {
+    const int64_t i = t * 1024 + tid;
+    const int s = i < a.m ? slot_of(a, i) : -1;
+    uint64_t left = __ballot(s >= 0);
+    while (left) {
+      const int leader = __builtin_ctzll(left);
+      const uint64_t same = __ballot(s == __builtin_amdgcn_readlane(s, leader));
+      if (lane == leader) atomicAdd(&cnt[s], __popcll(same));
+      left &= ~same;
+    }
+  }
+  __syncthreads();
+  // exclusive prefix sums over the adapters: rows (low half), items (high)
+  uint64_t own[4], sum = 0;
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1) acc += __shfl_xor(acc, off, 64);
-    if (lane == 0) v[i * a.r + j] = a.scales ? acc * a.scales[s] : acc;
+  for (int u = 0; u < 4; ++u) {
+    const int s = tid * 4 + u;
+    const int n = s < a.slots ? cnt[s] : 0;
+    own[u] = (uint64_t)(uint32_t)n | ((uint64_t)(uint32_t)((n + tm - 1) / tm) << 32);
+    sum += own[u];
+  }
+  uint64_t inc = sum;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const uint64_t o = __shfl_up(inc, off, 64);
+    if (lane >= off) inc += o;
+  }
+  if (lane == 63) wave_sum[tid >> 6] = inc;
+  __syncthreads();
+  uint64_t base = inc - sum;
+  for (int w = 0; w < (tid >> 6); ++w) base += wave_sum[w];
+  if (tid == 1023) *plan.items_used = (int)((base + sum) >> 32);
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int s = tid * 4 + u;
+    if (s < a.slots) {
+      const int n = (int)(uint32_t)own[u], start = (int)(uint32_t)base, it = (int)(base >> 32);
+      for (int p = 0; p * tm < n; ++p)
+        plan.items[it + p] = Item{s, start + p * tm, n - p * tm < tm ? n - p * tm : tm, 0};
+      cnt[s] = start;
+    }
+    base += own[u];
+  }
+  __syncthreads();
+  for (int64_t t = 0; t < steps; ++t) {
+    const int64_t i = t * 1024 + tid;
+    const int s = i < a.m ? slot_of(a, i) : -1;
+    uint64_t left = __ballot(s >= 0);
+    while (left) {
+      const int leader = __builtin_ctzll(left);
+      const uint64_t same = __ballot(s == __builtin_amdgcn_readlane(s, leader));
+      int at = 0;
+      if (lane == leader) at = atomicAdd(&cnt[s], __popcll(same));
+      at = __builtin_amdgcn_readlane(at, leader);
+      if ((same >> lane) & 1) plan.rows[at + lanes_below(same)] = (int)i;
+      left &= ~same;
+    }
   }
 }
 
-// one thread per (row, output), the outputs of a row over gridDim.y work-groups
-template <int XT, int YT>
-__global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs a, const float* __restrict__ v) {
-  typedef typename Elem<XT>::type T;
-  typedef typename Elem<YT>::type Y;
-  const int64_t i = blockIdx.x;
-  const int64_t s = a.ids[i];
-  if (s < 0 || s >= a.slots) return;
-  const int rank = rank_of(a, s);
-  if (rank == 0) return;
-  Y* y = static_cast<Y*>(a.y) + i * a.ldy;
-  for (int64_t o = (int64_t)blockIdx.y * 256 + threadIdx.x; o < a.n; o += (int64_t)gridDim.y * 256) {
-    const T* w = static_cast<const T*>(a.b) + (s * a.n + o) * a.r;
-    float acc = 0.0f;
-    for (int j = 0; j < rank; ++j) acc += (float)w[j] * v[i * a.r + j];
-    y[o] = (Y)((float)y[o] + acc);
+// v[slice][row][j] for 16 rows of an item and RT * 16 ranks: blockIdx.x =
+// item * subs + (16-row part of the item), y = part of the ranks, z = slice.
+// Rows past the item's and ranks past the adapter's repeat the last one (each
+// is a row or column of the MFMA of its own) and are not stored.
+template <int XT, int RT, bool INLINE>
+__global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs a, Plan plan, int tm, int subs,
+                                                          float* __restrict__ v) {
+  __shared__ int rows[64];
+  __shared__ f32x4 red[kShrinkWaves][RT][64];
+  const int item = blockIdx.x / subs, sub = blockIdx.x % subs;
+  int slot = 0;
+  const int count = find_item<INLINE>(a, plan, item, tm, rows, &slot);
+  const int here = count - sub * 16 < 16 ? count - sub * 16 : 16;
+  if (here <= 0) return;
+  const int rank = rank_of(a, slot), r0 = (int)blockIdx.y * RT * 16;
+  if (r0 >= rank) return;
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = lane & 15, q = lane >> 4;
+  const int64_t row = rows[sub * 16 + (c < here ? c : here - 1)];
+  const uint16_t* xp = static_cast<const uint16_t*>(a.x) + row * a.ldx + q * 8;
+  const uint16_t* ap[RT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    const int j = r0 + t * 16 + c;
+    ap[t] = static_cast<const uint16_t*>(a.a) + ((int64_t)slot * a.r + (j < rank ? j : rank - 1)) * a.k +
+            q * 8;
   }
+  const int steps = (int)((a.k + 31) / 32);
+  const int parts = kShrinkWaves * (int)gridDim.z;
+  const int per = (steps + parts - 1) / parts;
+  const int s0 = ((int)blockIdx.z * kShrinkWaves + wave) * per;
+  const int s1 = s0 + per < steps ? s0 + per : steps;
+  const int full = (int)(a.k / 32);  // steps in which every lane has its 8 values
+
+  f32x4 acc[RT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t) acc[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  constexpr int U = RT == 1 ? 8 : 4;  // steps whose loads are in flight together
+  int s = s0;
+  for (; s + U <= s1 && s + U <= full; s += U) {
+    uint4 xr[U], ar[U][RT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      xr[u] = *reinterpret_cast<const uint4*>(xp + (int64_t)(s + u) * 32);
+#pragma unroll
+      for (int t = 0; t < RT; ++t) ar[u][t] = *reinterpret_cast<const uint4*>(ap[t] + (int64_t)(s + u) * 32);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int t = 0; t < RT; ++t) acc[t] = Mma<XT>::run(ar[u][t], xr[u], acc[t]);
+  }
+  for (; s < s1; ++s) {
+    uint4 xr = make_uint4(0, 0, 0, 0), ar[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) ar[t] = xr;
+    if (s * 32 + q * 8 < a.k) {
+      xr = *reinterpret_cast<const uint4*>(xp + (int64_t)s * 32);
+#pragma unroll
+      for (int t = 0; t < RT; ++t) ar[t] = *reinterpret_cast<const uint4*>(ap[t] + (int64_t)s * 32);
+    }
+#pragma unroll
+    for (int t = 0; t < RT; ++t) acc[t] = Mma<XT>::run(ar[t], xr, acc[t]);
+  }
+#pragma unroll
+  for (int t = 0; t < RT; ++t) red[wave][t][lane] = acc[t];
+  __syncthreads();
+  if (threadIdx.x < RT * 64) {
+    const int t = threadIdx.x >> 6;
+    f32x4 sum = red[0][t][lane];
+#pragma unroll
+    for (int w = 1; w < kShrinkWaves; ++w) sum += red[w][t][lane];
+    const int j = r0 + t * 16 + q * 4;
+    // j .. j + 3 lie in the row (r is a multiple of 8); what is past the rank is not read
+    if (c < here && j < rank)
+      *reinterpret_cast<f32x4*>(v + ((int64_t)blockIdx.z * a.m + row) * a.r + j) = sum;
+  }
+}
+
+// FP32 value -> its pieces; `scale` is a power of two (1 for BF16)
+__device__ __forceinline__ void split(float v, float scale, _Float16 (&p)[2]) {
+  v *= scale;
+  p[0] = (_Float16)v;
+  const float rest = v - (float)p[0];
+  p[1] = __builtin_isfinite((float)p[0]) ? (_Float16)rest : (_Float16)0.0f;
+}
+__device__ __forceinline__ void split(float v, float, bf16_t (&p)[3]) {
+  p[0] = (bf16_t)v;
+  const bool fine = __builtin_isfinite((float)p[0]);
+  const float rest = fine ? v - (float)p[0] : 0.0f;
+  p[1] = (bf16_t)rest;
+  p[2] = (bf16_t)(rest - (float)p[1]);
+}
+
+// largest of 16 consecutive lanes
+__device__ __forceinline__ float max16(float v) {
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, 64));
+  return v;
+}
+
+// Y[i][n0 .. n0 + 16) as they are stored (16 values of a lane)
+template <int YT>
+struct Out16 {
+  typename Elem<YT>::type e[16];
+};
+
+// One item, 256 outputs.  Tile t of a wave holds outputs 16 q + 4 t + e at D's
+// row 4 q + e, so that a lane's four tiles are 16 consecutive outputs of its
+// row (64 bytes of FP32, 32 of BF16), read and written 16 bytes at a time.
+template <int XT, int YT, bool INLINE>
+__global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs a, Plan plan, int tm, int slices,
+                                                          const float* __restrict__ v) {
+  constexpr int P = Mma<XT>::pieces;
+  typedef typename Elem<XT>::type X;
+  typedef typename Elem<YT>::type Y;
+  extern __shared__ uint4 dyn[];
+  __shared__ int rows[64];
+  __shared__ float unscale[64];
+  X* pieces = reinterpret_cast<X*>(dyn);  // [P][tm][pitch]
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int c = lane & 15, q = lane >> 4;
+
+  for (int item = blockIdx.y;; item += gridDim.y) {
+    int slot = 0;
+    const int count = find_item<INLINE>(a, plan, item, tm, rows, &slot);
+    if (!count) return;
+    const int rank = rank_of(a, slot);
+    const int chunks = (rank + 31) / 32, pitch = chunks * 32 + 8;  // 16 bytes past: other banks
+    const float scale = a.scales ? a.scales[slot] : 1.0f;
+    const int subs = (count + 15) / 16;
+
+    // v of the item's rows, 16 lanes to a row
+    for (int sub = 0; sub < subs; ++sub) {
+      const int at = sub * 16 + (tid >> 4), j0 = (tid & 15) * 4;
+      const bool live = at < count;
+      const float* vr = v + (int64_t)rows[live ? at : 0] * a.r;
+      f32x4 val[4];
+      float top = 0.0f;
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const int j = j0 + h * 64;
+        val[h] = (f32x4){0.f, 0.f, 0.f, 0.f};
+        if (live && j < rank) {
+          for (int z = 0; z < slices; ++z)
+            val[h] += *reinterpret_cast<const f32x4*>(vr + (int64_t)z * a.m * a.r + j);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            val[h][e] = j + e < rank ? val[h][e] * scale : 0.0f;
+            const float m = fabsf(val[h][e]);
+            if (m <= 3.4028235e38f) top = fmaxf(top, m);
+          }
+        }
+      }
+      float up = 1.0f;
+      if constexpr (XT == 2) {
+        top = max16(top);
+        // the row's largest value to [2^13, 2^14): far from FP16's ends on both sides
+        int ex = top > 0.0f ? 13 - ilogbf(top) : 0;
+        ex = ex > 120 ? 120 : ex;
+        up = ldexpf(1.0f, ex);
+        if ((tid & 15) == 0 && live) unscale[at] = ldexpf(1.0f, -ex);
+      }
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const int j = j0 + h * 64;
+        if (j < chunks * 32) {
+          X p[4][P];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) split(val[h][e], up, p[e]);
+#pragma unroll
+          for (int w = 0; w < P; ++w) {
+            X o[4] = {p[0][w], p[1][w], p[2][w], p[3][w]};
+            __builtin_memcpy(pieces + (w * tm + at) * pitch + j, o, 8);
+          }
+        }
+      }
+    }
+    __syncthreads();
+
+    for (int64_t n0 = ((int64_t)blockIdx.x * 4 + wave) * kWaveN; n0 < a.n;
+         n0 += (int64_t)gridDim.x * kBlockN) {
+      f32x4 acc[4][kTilesN];
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int t = 0; t < kTilesN; ++t) acc[s][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+      for (int rc = 0; rc < chunks; ++rc) {
+        const int j = rc * 32 + q * 8;
+        uint4 w[kTilesN];
+#pragma unroll
+        for (int t = 0; t < kTilesN; ++t) {
+          const int64_t o = n0 + (c >> 2) * (4 * kTilesN) + t * 4 + (c & 3);
+          w[t] = make_uint4(0, 0, 0, 0);
+          if (o < a.n && j < rank)
+            w[t] = *reinterpret_cast<const uint4*>(static_cast<const X*>(a.b) +
+                                                   ((int64_t)slot * a.n + o) * a.r + j);
+        }
+        if (rank - j < 8) {  // entries past the rank may hold anything
+          uint32_t keep[4];
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            const int left = rank - j - 2 * d;
+            keep[d] = left >= 2 ? 0xFFFFFFFFu : (left == 1 ? 0xFFFFu : 0u);
+          }
+#pragma unroll
+          for (int t = 0; t < kTilesN; ++t) {
+            w[t].x &= keep[0];
+            w[t].y &= keep[1];
+            w[t].z &= keep[2];
+            w[t].w &= keep[3];
+          }
+        }
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          if (s < subs) {
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+              const uint4 b = *reinterpret_cast<const uint4*>(pieces + (p * tm + s * 16 + c) * pitch + j);
+#pragma unroll
+              for (int t = 0; t < kTilesN; ++t) acc[s][t] = Mma<XT>::run(w[t], b, acc[s][t]);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const int at = s * 16 + c;
+        if (at < count) {
+          const float un = XT == 2 ? unscale[at] : 1.0f;
+          const int64_t o = n0 + q * 16;
+          Y* yp = static_cast<Y*>(a.y) + (int64_t)rows[at] * a.ldy + o;
+          if (o + 16 <= a.n) {
+            Out16<YT> z;
+            __builtin_memcpy(&z, yp, sizeof(z));
+#pragma unroll
+            for (int u = 0; u < 16; ++u) z.e[u] = (Y)((float)z.e[u] + acc[s][u >> 2][u & 3] * un);
+            __builtin_memcpy(yp, &z, sizeof(z));
+          } else {
+#pragma unroll
+            for (int u = 0; u < 16; ++u)
+              if (o + u < a.n) yp[u] = (Y)((float)yp[u] + acc[s][u >> 2][u & 3] * un);
+          }
+        }
+      }
+    }
+    __syncthreads();  // the next item's rows and pieces
+  }
+}
+
+int64_t round256(int64_t v) { return (v + 255) / 256 * 256; }
+
+// rows of an item: as many as keep its pieces within 64 KB of LDS
+int item_rows(int64_t r) { return r > 128 ? 32 : 64; }
+
+int64_t max_items(int64_t m, int64_t slots, int64_t tm) {
+  // every item but an adapter's last is full
+  const int64_t most = slots + m / tm;
+  return most < m ? most : m;
+}
+
+int64_t plan_bytes(int64_t m, int64_t slots, int64_t tm) {
+  return m <= kInlineRows ? 0 : 256 + round256(max_items(m, slots, tm) * 16) + round256(m * 4);
+}
+
+int ranks_per_block(int64_t m, int64_t r) {
+  // few rows: many work-groups of 16 ranks, each reading x again (from the
+  // cache); many rows: x, the larger operand, is read once per 64 ranks
+  if (m <= kInlineRows || r <= 16) return 1;
+  return r <= 32 ? 2 : 4;
+}
+
+// k in slices until there are about as many work-groups as compute units; a
+// wave keeps at least 64 of k, and the expand kernel sums at most 16 slices
+int64_t slices_of(int64_t m, int64_t k, int64_t r, int64_t slots) {
+  const int tm = item_rows(r), rt = ranks_per_block(m, r);
+  const int64_t items = max_items(m, slots, tm), units = items > (m + 15) / 16 ? items : (m + 15) / 16;
+  const int64_t groups = (r + rt * 16 - 1) / (rt * 16);
+  int64_t s = 256 / (units * groups);
+  const int64_t most = k / (64 * kShrinkWaves);
+  s = s < most ? s : most;
+  return s < 1 ? 1 : (s > 16 ? 16 : s);
+}
+
+template <int XT, int YT, bool INLINE>
+hipError_t launch(const LoraArgs& a, const Plan& plan, float* v, hipStream_t st) {
+  const int tm = item_rows(a.r), rt = ranks_per_block(a.m, a.r);
+  const int64_t items = max_items(a.m, a.slots, tm);
+  const int64_t rows = a.m < tm ? a.m : tm;
+  const int subs = (int)((rows + 15) / 16);
+  const int slices = (int)slices_of(a.m, a.k, a.r, a.slots);
+  const dim3 gs((unsigned)(items * subs), (unsigned)((a.r + rt * 16 - 1) / (rt * 16)), (unsigned)slices);
+  if (rt == 1)
+    hipLaunchKernelGGL((lora_shrink_kernel<XT, 1, INLINE>), gs, dim3(512), 0, st, a, plan, tm, subs, v);
+  else if (rt == 2)
+    hipLaunchKernelGGL((lora_shrink_kernel<XT, 2, INLINE>), gs, dim3(512), 0, st, a, plan, tm, subs, v);
+  else
+    hipLaunchKernelGGL((lora_shrink_kernel<XT, 4, INLINE>), gs, dim3(512), 0, st, a, plan, tm, subs, v);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t tiles = (a.n + kBlockN - 1) / kBlockN;
+  const dim3 ge((unsigned)(tiles < 8192 ? tiles : 8192), (unsigned)(items < 32768 ? items : 32768));
+  const size_t lds = (size_t)Mma<XT>::pieces * tm * ((a.r + 31) / 32 * 32 + 8) * 2;
+  hipLaunchKernelGGL((lora_expand_kernel<XT, YT, INLINE>), ge, dim3(256), lds, st, a, plan, tm, slices, v);
+  return hipGetLastError();
 }
 
 }  // namespace
 
 size_t lora_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_t r, int64_t slots) {
   (void)n;
-  (void)k;
-  (void)slots;
-  return (size_t)((m * r * 4 + 255) / 256 * 256);
+  return (size_t)(plan_bytes(m, slots, item_rows(r)) + round256(slices_of(m, k, r, slots) * m * r * 4));
 }
 
 hipError_t launch_lora_accumulate(const LoraArgs& a, void* ws, hipStream_t st) {
-  float* v = static_cast<float*>(ws);
-  const int64_t tiles = (a.n + 255) / 256;
-  const dim3 gs((unsigned)a.m), ge((unsigned)a.m, (unsigned)(tiles < 1024 ? tiles : 1024));
-  if (a.x_type == 2)
-    hipLaunchKernelGGL(lora_shrink_kernel<2>, gs, dim3(256), 0, st, a, v);
-  else
-    hipLaunchKernelGGL(lora_shrink_kernel<3>, gs, dim3(256), 0, st, a, v);
-  hipError_t e = hipGetLastError();
+  const int tm = item_rows(a.r);
+  char* base = static_cast<char*>(ws);
+  float* v = reinterpret_cast<float*>(base + plan_bytes(a.m, a.slots, tm));
+  Plan plan = {};
+  if (a.m <= kInlineRows) {
+    if (a.x_type == 2) return launch<2, 1, true>(a, plan, v, st);
+    return a.y_type == 1 ? launch<3, 1, true>(a, plan, v, st) : launch<3, 3, true>(a, plan, v, st);
+  }
+  plan.items_used = reinterpret_cast<int*>(base);
+  plan.items = reinterpret_cast<Item*>(base + 256);
+  plan.rows = reinterpret_cast<int*>(base + 256 + round256(max_items(a.m, a.slots, tm) * 16));
+  hipLaunchKernelGGL(lora_plan_kernel, dim3(1), dim3(1024), 0, st, a, plan, tm);
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (a.x_type == 2)
-    hipLaunchKernelGGL((lora_expand_kernel<2, 1>), ge, dim3(256), 0, st, a, v);
-  else if (a.y_type == 1)
-    hipLaunchKernelGGL((lora_expand_kernel<3, 1>), ge, dim3(256), 0, st, a, v);
-  else
-    hipLaunchKernelGGL((lora_expand_kernel<3, 3>), ge, dim3(256), 0, st, a, v);
-  return hipGetLastError();
+  if (a.x_type == 2) return launch<2, 1, false>(a, plan, v, st);
+  return a.y_type == 1 ? launch<3, 1, false>(a, plan, v, st) : launch<3, 3, false>(a, plan, v, st);
 }
 
 }  // namespace lowbit
