@@ -5,10 +5,239 @@
 // [P2] 7minutos.es, "PrismML lanza Bonsai 27B ...", "Como funciona la
 //      compresion": the projections of a block are low-bit; the norms and the
 //      residual stream between them are not.
+//
+// A row of y and r is read once and held in registers (8 elements per thread
+// and step, raw, as they were loaded) while its sums are formed: the
+// deviations of a layer norm are summed in a second sweep over the registers,
+// which keeps a small variance beside a large mean.  A row belongs to one
+// work-group, or to one wave where rows are short and many; rows longer than
+// the registers of a work-group hold are read again for every sum.
 #include "common.h"
 
 namespace lowbit {
 namespace {
+
+// 8 elements as they lie in memory, S bytes each
+template <int S>
+struct Raw8 {
+  uint32_t d[2 * S];
+};
+
+// Elements [c, c + 8) of a row at p + i0: 16-byte loads at any element
+// alignment; past `k` nothing is read and zeros stand.
+template <int S>
+__device__ __forceinline__ Raw8<S> load8(const void* p, int64_t i0, int c, int k) {
+  Raw8<S> r;
+  const char* at = static_cast<const char*>(p) + (i0 + c) * S;
+  if (c + 8 <= k) {
+    __builtin_memcpy(&r, at, sizeof(r));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 2 * S; ++j) r.d[j] = 0u;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (c + j < k) {
+        if constexpr (S == 4) {
+          __builtin_memcpy(&r.d[j], at + j * 4, 4);
+        } else {
+          uint16_t h;
+          __builtin_memcpy(&h, at + j * 2, 2);
+          r.d[j >> 1] |= (uint32_t)h << ((j & 1) * 16);
+        }
+      }
+    }
+  }
+  return r;
+}
+
+template <int S>
+__device__ __forceinline__ void widen(const Raw8<S>& r, int type, float (&v)[8]) {
+  if constexpr (S == 4) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __builtin_bit_cast(float, r.d[j]);
+  } else if (type == 2) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      v[j] = (float)__builtin_bit_cast(_Float16, (uint16_t)(r.d[j >> 1] >> ((j & 1) * 16)));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      v[j] = __builtin_bit_cast(float, (j & 1) ? r.d[j >> 1] & 0xFFFF0000u : r.d[j >> 1] << 16);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store8_as(void* p, int64_t i0, int c, int k, const float (&v)[8]) {
+  T o[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) o[j] = (T)v[j];
+  T* at = static_cast<T*>(p) + i0 + c;
+  if (c + 8 <= k) {
+    __builtin_memcpy(at, o, sizeof(o));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + j < k) at[j] = o[j];
+  }
+}
+
+__device__ __forceinline__ void store8(void* p, int type, int64_t i0, int c, int k, const float (&v)[8]) {
+  if (type == 1) store8_as<float>(p, i0, c, k, v);
+  else if (type == 2) store8_as<_Float16>(p, i0, c, k, v);
+  else store8_as<bf16_t>(p, i0, c, k, v);
+}
+
+// FP32 vector of k elements, or `none` everywhere where it is not given
+__device__ __forceinline__ void vector8(const float* p, float none, int c, int k, float (&v)[8]) {
+  if (p) {
+    widen<4>(load8<4>(p, 0, c, k), 1, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = none;
+  }
+}
+
+// Sum over the wave in every lane: DPP adds within 16 lanes and across the
+// halves (no LDS round trip), the same order for every row.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS,
+                                                                   0xF, false));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v = dpp_add<0x111, 0xF>(v);  // row_shr:1
+  v = dpp_add<0x112, 0xF>(v);  // row_shr:2
+  v = dpp_add<0x114, 0xF>(v);  // row_shr:4
+  v = dpp_add<0x118, 0xF>(v);  // row_shr:8: lane 15 of each row holds the row's sum
+  v = dpp_add<0x142, 0xA>(v);  // row_bcast:15 into rows 1 and 3
+  v = dpp_add<0x143, 0xC>(v);  // row_bcast:31 into rows 2 and 3
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
+
+// Sum over the threads that share a row.  Consecutive sums of a work-group
+// use the two halves of `red` in turn, so that one barrier each is enough.
+template <bool WAVE>
+__device__ __forceinline__ float row_sum(float v, float (*red)[16], int& turn) {
+  v = wave_sum(v);
+  if constexpr (WAVE) return v;
+  if ((threadIdx.x & 63) == 0) red[turn][threadIdx.x >> 6] = v;
+  __syncthreads();
+  const int waves = (int)blockDim.x >> 6;
+  float s = red[turn][0];
+  for (int w = 1; w < waves; ++w) s += red[turn][w];
+  turn ^= 1;
+  return s;
+}
+
+// Rows of up to threads * NV * 8 elements in registers.  SY, SR: bytes per
+// element of y and r.
+template <bool WAVE, int SY, int SR, int NV>
+__global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(NormArgs a) {
+  __shared__ float red[2][16];
+  const int threads = WAVE ? 64 : (int)blockDim.x;
+  const int t = WAVE ? threadIdx.x & 63 : threadIdx.x;
+  const int64_t i = WAVE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : (int64_t)blockIdx.x;
+  if (WAVE && i >= a.m) return;
+  const int k = (int)a.k;
+  const float inv_k = 1.0f / (float)k;
+  int turn = 0;
+
+  Raw8<SY> yr[NV];
+  Raw8<SR> rr[NV];
+  float v[NV][8];
+#pragma unroll
+  for (int n = 0; n < NV; ++n) {
+    const int c = (n * threads + t) * 8;
+    if (a.y) yr[n] = load8<SY>(a.y, i * a.ldy, c, k);
+    rr[n] = load8<SR>(a.r, i * a.ldr, c, k);
+  }
+  if (a.y) {
+    float u[NV][8];
+#pragma unroll
+    for (int n = 0; n < NV; ++n) widen<SY>(yr[n], a.y_type, u[n]);
+    float mean = 0.0f, rs = 1.0f;
+    if (a.post == 2) {
+      float s = 0.0f;
+#pragma unroll
+      for (int n = 0; n < NV; ++n)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s += u[n][j];
+      mean = row_sum<WAVE>(s, red, turn) * inv_k;
+    }
+    if (a.post != 0) {
+      float s = 0.0f;
+#pragma unroll
+      for (int n = 0; n < NV; ++n)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float d = (n * threads + t) * 8 + j < k ? u[n][j] - mean : 0.0f;
+          s += d * d;
+        }
+      rs = 1.0f / sqrtf(row_sum<WAVE>(s, red, turn) * inv_k + a.eps);
+    }
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+      const int c = (n * threads + t) * 8;
+      if (c < k) {
+        if (a.post != 0) {
+          float w[8], b[8];
+          vector8(a.post_w, 1.0f, c, k, w);
+          vector8(a.post_b, 0.0f, c, k, b);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) u[n][j] = (u[n][j] - mean) * rs * w[j] + b[j];
+        }
+        if (a.gate) {
+          float g[8];
+          if (a.gate_type == 1) widen<4>(load8<4>(a.gate, i * a.ldg, c, k), 1, g);
+          else widen<2>(load8<2>(a.gate, i * a.ldg, c, k), a.gate_type, g);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) u[n][j] *= g[j];
+        }
+      }
+      widen<SR>(rr[n], a.r_type, v[n]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[n][j] += a.scale * u[n][j];
+      if (a.r_out && c < k) store8(a.r_out, a.r_type, i * a.ldro, c, k, v[n]);
+    }
+  } else {
+#pragma unroll
+    for (int n = 0; n < NV; ++n) widen<SR>(rr[n], a.r_type, v[n]);
+  }
+  if (!a.x_out) return;
+  float mean = 0.0f, rs = 1.0f;
+  if (a.pre == 2) {
+    float s = 0.0f;
+#pragma unroll
+    for (int n = 0; n < NV; ++n)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += (n * threads + t) * 8 + j < k ? v[n][j] : 0.0f;
+    mean = row_sum<WAVE>(s, red, turn) * inv_k;
+  }
+  if (a.pre != 0) {
+    float s = 0.0f;
+#pragma unroll
+    for (int n = 0; n < NV; ++n)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float d = (n * threads + t) * 8 + j < k ? v[n][j] - mean : 0.0f;
+        s += d * d;
+      }
+    rs = 1.0f / sqrtf(row_sum<WAVE>(s, red, turn) * inv_k + a.eps);
+  }
+#pragma unroll
+  for (int n = 0; n < NV; ++n) {
+    const int c = (n * threads + t) * 8;
+    if (c >= k) continue;
+    if (a.pre != 0) {
+      float w[8], b[8];
+      vector8(a.pre_w, 1.0f, c, k, w);
+      vector8(a.pre_b, 0.0f, c, k, b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[n][j] = (v[n][j] - mean) * rs * w[j] + b[j];
+    }
+    store8(a.x_out, a.x_type, i * a.ldx, c, k, v[n]);
+  }
+}
 
 template <int TYPE>
 __device__ __forceinline__ float load1(const void* p, int64_t i) {
@@ -25,23 +254,11 @@ __device__ __forceinline__ void store_any(void* p, int type, int64_t i, float v)
   else static_cast<bf16_t*>(p)[i] = (bf16_t)v;
 }
 
-// sum over the work-group, the same in every thread; `red` holds one float
-// per wave and is free again when the call returns
-__device__ __forceinline__ float block_sum(float v, float* red) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  float s = 0.0f;
-  for (int w = 0; w < (int)(blockDim.x >> 6); ++w) s += red[w];
-  __syncthreads();
-  return s;
-}
-
-// One work-group per row, any k, stride and alignment: nothing of the row is
-// kept, each pass over it reads it again.
-__global__ __launch_bounds__(256) void norm_rows_kernel(NormArgs a) {
-  __shared__ float red[4];
+// Rows longer than a work-group's registers: nothing is kept, each sum reads
+// the row again (a row of 2^22 would not fit a compute unit in any form).
+__global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
+  __shared__ float red[2][16];
+  int turn = 0;
   const int64_t i = blockIdx.x;
   const float inv_k = 1.0f / (float)a.k;
   const int64_t iy = i * a.ldy, ir = i * a.ldr, ig = i * a.ldg;
@@ -50,15 +267,15 @@ __global__ __launch_bounds__(256) void norm_rows_kernel(NormArgs a) {
   if (a.post != 0) {
     if (a.post == 2) {
       float s = 0.0f;
-      for (int64_t c = threadIdx.x; c < a.k; c += 256) s += load_any(a.y, a.y_type, iy + c);
-      mean_y = block_sum(s, red) * inv_k;
+      for (int64_t c = threadIdx.x; c < a.k; c += 1024) s += load_any(a.y, a.y_type, iy + c);
+      mean_y = row_sum<false>(s, red, turn) * inv_k;
     }
     float s = 0.0f;
-    for (int64_t c = threadIdx.x; c < a.k; c += 256) {
+    for (int64_t c = threadIdx.x; c < a.k; c += 1024) {
       const float d = load_any(a.y, a.y_type, iy + c) - mean_y;
       s += d * d;
     }
-    rs_y = 1.0f / sqrtf(block_sum(s, red) * inv_k + a.eps);
+    rs_y = 1.0f / sqrtf(row_sum<false>(s, red, turn) * inv_k + a.eps);
   }
   auto residual = [&](int64_t c) {
     float v = load_any(a.r, a.r_type, ir + c);
@@ -78,17 +295,17 @@ __global__ __launch_bounds__(256) void norm_rows_kernel(NormArgs a) {
   if (a.pre != 0) {
     if (a.pre == 2) {
       float s = 0.0f;
-      for (int64_t c = threadIdx.x; c < a.k; c += 256) s += residual(c);
-      mean_r = block_sum(s, red) * inv_k;
+      for (int64_t c = threadIdx.x; c < a.k; c += 1024) s += residual(c);
+      mean_r = row_sum<false>(s, red, turn) * inv_k;
     }
     float s = 0.0f;
-    for (int64_t c = threadIdx.x; c < a.k; c += 256) {
+    for (int64_t c = threadIdx.x; c < a.k; c += 1024) {
       const float d = residual(c) - mean_r;
       s += d * d;
     }
-    rs_r = 1.0f / sqrtf(block_sum(s, red) * inv_k + a.eps);
+    rs_r = 1.0f / sqrtf(row_sum<false>(s, red, turn) * inv_k + a.eps);
   }
-  for (int64_t c = threadIdx.x; c < a.k; c += 256) {
+  for (int64_t c = threadIdx.x; c < a.k; c += 1024) {
     const float v = residual(c);
     if (a.r_out) store_any(a.r_out, a.r_type, i * a.ldro + c, v);
     if (a.x_out) {
@@ -103,10 +320,31 @@ __global__ __launch_bounds__(256) void norm_rows_kernel(NormArgs a) {
   }
 }
 
+template <bool WAVE, int NV>
+hipError_t launch_as(const NormArgs& a, dim3 grid, dim3 block, hipStream_t st) {
+  const bool y4 = a.y_type == 1, r4 = a.r_type == 1;
+  if (y4 && r4) hipLaunchKernelGGL((norm_kernel<WAVE, 4, 4, NV>), grid, block, 0, st, a);
+  else if (y4) hipLaunchKernelGGL((norm_kernel<WAVE, 4, 2, NV>), grid, block, 0, st, a);
+  else if (r4) hipLaunchKernelGGL((norm_kernel<WAVE, 2, 4, NV>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((norm_kernel<WAVE, 2, 2, NV>), grid, block, 0, st, a);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_norm_residual(const NormArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL(norm_rows_kernel, dim3((unsigned)a.m), dim3(256), 0, st, a);
+  const int64_t chunks = (a.k + 7) / 8;
+  // short rows, many of them: one wave each, no barriers
+  if (chunks <= 128 && a.m >= 1024) {
+    const dim3 grid((unsigned)((a.m + 3) / 4));
+    return chunks <= 64 ? launch_as<true, 1>(a, grid, dim3(256), st) : launch_as<true, 2>(a, grid, dim3(256), st);
+  }
+  const dim3 grid((unsigned)a.m);
+  auto block = [&](int64_t nv) { return dim3((unsigned)((chunks + nv * 64 - 1) / (nv * 64) * 64)); };
+  if (chunks <= 1024) return launch_as<false, 1>(a, grid, block(1), st);
+  if (chunks <= 2048) return launch_as<false, 2>(a, grid, block(2), st);
+  if (chunks <= 4096) return launch_as<false, 4>(a, grid, block(4), st);
+  hipLaunchKernelGGL(norm_long_kernel, grid, dim3(1024), 0, st, a);
   return hipGetLastError();
 }
 
