@@ -12,12 +12,19 @@ namespace lowbit {
 // all bits flipped, positive: sign bit set); a NaN with a clear sign bit
 // sorts above +inf, so NaN wins as it does for numpy's and torch's argmax.
 
-__device__ __forceinline__ uint64_t argmax_key(float v, int64_t i) {
+__device__ __forceinline__ uint32_t ordered_bits(float v) {
   uint32_t u = __builtin_bit_cast(uint32_t, v);
   if (__builtin_isnan(v)) u = 0x7FC00000u;  // every NaN the same, above +inf
   if (v == 0.0f) u = 0u;                    // -0 and +0 are equal values
-  u = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-  return ((uint64_t)u << 32) | (uint64_t)(0xFFFFFFFFu - (uint32_t)i);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+__device__ __forceinline__ uint64_t argmax_pack(uint32_t ordered, int64_t i) {
+  return ((uint64_t)ordered << 32) | (uint64_t)(0xFFFFFFFFu - (uint32_t)i);
+}
+
+__device__ __forceinline__ uint64_t argmax_key(float v, int64_t i) {
+  return argmax_pack(ordered_bits(v), i);
 }
 
 __device__ __forceinline__ uint64_t wave_max(uint64_t k) {
