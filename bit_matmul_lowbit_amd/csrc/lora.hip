@@ -7,7 +7,7 @@
 //      what is learned on top of it lives in such adapters.
 //
 // Rows are grouped by adapter, so that an adapter's matrices meet all of its
-// rows at once.  An item is up to 64 rows of one adapter (32 where r > 128).
+// rows at once.  An item is up to 32 rows of one adapter (16 where m <= 16).
 // With m <= 64 every work-group finds its item itself: the ids of all rows
 // fit one wave, and ballots pick out the rows that share one (no launch, no
 // memory).  More rows are sorted by one work-group first (lora_plan_kernel).
@@ -22,7 +22,8 @@
 // shrink: v^T = A x^T, one work-group per (16 rows of an item, up to 64 of
 // its ranks, slice of k); its eight waves split the slice and are summed
 // through LDS.  The slices' FP32 sums go to the workspace.
-// expand: y^T += B v^T, one work-group per (item, 256 outputs).  v is summed
+// expand: y^T += B v^T, one work-group per (item, share of the outputs, 256 at
+// a time).  v is summed
 // over the slices, scaled, and split into 16-bit pieces whose sum holds it to
 // FP32's precision or nearly (FP16: two pieces of a row scaled by a power of
 // two, 22 bits; BF16: three pieces, 24 bits), since a single 16-bit v would
@@ -38,11 +39,13 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kInlineRows = 64;  // rows whose grouping one wave finds by itself
+constexpr int kItemRows = 32;    // most rows of an item
 constexpr int kShrinkWaves = 8;
 constexpr int kTilesN = 4;                 // 16-output tiles of a wave in expand
 constexpr int kWaveN = 16 * kTilesN;       // 64 outputs per wave
 constexpr int kBlockN = 4 * kWaveN;        // 256 outputs per work-group
 constexpr int kMaxSlots = 4096;
+constexpr int kMaxSlices = 8;              // slices of k at most
 
 template <int XT> struct Mma;
 template <> struct Mma<2> {
@@ -206,7 +209,7 @@ __global__ __launch_bounds__(1024) void lora_plan_kernel(LoraArgs a, Plan plan, 
 template <int XT, int RT, bool INLINE>
 __global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs a, Plan plan, int tm, int subs,
                                                           float* __restrict__ v) {
-  __shared__ int rows[64];
+  __shared__ int rows[kItemRows];
   __shared__ f32x4 red[kShrinkWaves][RT][64];
   const int item = blockIdx.x / subs, sub = blockIdx.x % subs;
   int slot = 0;
@@ -232,37 +235,41 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs a, Plan plan,
   const int per = (steps + parts - 1) / parts;
   const int s0 = ((int)blockIdx.z * kShrinkWaves + wave) * per;
   const int s1 = s0 + per < steps ? s0 + per : steps;
-  const int full = (int)(a.k / 32);  // steps in which every lane has its 8 values
+  const bool ragged = a.k % 32 != 0;  // the last step's upper lanes have no k
 
   f32x4 acc[RT];
 #pragma unroll
   for (int t = 0; t < RT; ++t) acc[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
-  constexpr int U = RT == 1 ? 8 : 4;  // steps whose loads are in flight together
-  int s = s0;
-  for (; s + U <= s1 && s + U <= full; s += U) {
-    uint4 xr[U], ar[U][RT];
+  // a ring of U steps, each reloaded as soon as it is used; past the slice
+  // the last step is loaded again and not used
+  constexpr int U = RT == 4 ? 4 : 8;
+  uint4 xr[U], ar[U][RT];
+  auto load = [&](int u, int s) __attribute__((always_inline)) {
+    s = s < s1 ? s : s1 - 1;
+    int64_t at = (int64_t)s * 32;
+    if (ragged && at + q * 8 >= a.k) at = a.k - 8 - q * 8;
+    xr[u] = *reinterpret_cast<const uint4*>(xp + at);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      xr[u] = *reinterpret_cast<const uint4*>(xp + (int64_t)(s + u) * 32);
+    for (int t = 0; t < RT; ++t) ar[u][t] = *reinterpret_cast<const uint4*>(ap[t] + at);
+  };
+  if (s0 < s1) {
 #pragma unroll
-      for (int t = 0; t < RT; ++t) ar[u][t] = *reinterpret_cast<const uint4*>(ap[t] + (int64_t)(s + u) * 32);
+    for (int u = 0; u < U; ++u) load(u, s0 + u);
+    for (int s = s0; s < s1; s += U) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (s + u < s1) {
+          if (ragged && s + u == steps - 1 && (s + u) * 32 + q * 8 >= a.k) {
+            xr[u] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int t = 0; t < RT; ++t) ar[u][t] = xr[u];
+          }
+#pragma unroll
+          for (int t = 0; t < RT; ++t) acc[t] = Mma<XT>::run(ar[u][t], xr[u], acc[t]);
+          load(u, s + U + u);
+        }
+      }
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int t = 0; t < RT; ++t) acc[t] = Mma<XT>::run(ar[u][t], xr[u], acc[t]);
-  }
-  for (; s < s1; ++s) {
-    uint4 xr = make_uint4(0, 0, 0, 0), ar[RT];
-#pragma unroll
-    for (int t = 0; t < RT; ++t) ar[t] = xr;
-    if (s * 32 + q * 8 < a.k) {
-      xr = *reinterpret_cast<const uint4*>(xp + (int64_t)s * 32);
-#pragma unroll
-      for (int t = 0; t < RT; ++t) ar[t] = *reinterpret_cast<const uint4*>(ap[t] + (int64_t)s * 32);
-    }
-#pragma unroll
-    for (int t = 0; t < RT; ++t) acc[t] = Mma<XT>::run(ar[t], xr, acc[t]);
   }
 #pragma unroll
   for (int t = 0; t < RT; ++t) red[wave][t][lane] = acc[t];
@@ -301,26 +308,71 @@ __device__ __forceinline__ float max16(float v) {
   return v;
 }
 
-// Y[i][n0 .. n0 + 16) as they are stored (16 values of a lane)
+// 16 consecutive outputs of a row, as they are stored
 template <int YT>
 struct Out16 {
-  typename Elem<YT>::type e[16];
+  uint32_t d[YT == 1 ? 16 : 8];
 };
 
-// One item, 256 outputs.  Tile t of a wave holds outputs 16 q + 4 t + e at D's
-// row 4 q + e, so that a lane's four tiles are 16 consecutive outputs of its
-// row (64 bytes of FP32, 32 of BF16), read and written 16 bytes at a time.
-template <int XT, int YT, bool INLINE>
-__global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs a, Plan plan, int tm, int slices,
+// + add * un, rounded once
+__device__ __forceinline__ void add16(Out16<1>& z, const f32x4 (&add)[kTilesN], float un) {
+#pragma unroll
+  for (int u = 0; u < 16; ++u)
+    z.d[u] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, z.d[u]) + add[u >> 2][u & 3] * un);
+}
+__device__ __forceinline__ void add16(Out16<3>& z, const f32x4 (&add)[kTilesN], float un) {
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const float lo = __builtin_bit_cast(float, z.d[u] << 16) + add[u >> 1][2 * (u & 1)] * un;
+    const float hi = __builtin_bit_cast(float, z.d[u] & 0xFFFF0000u) + add[u >> 1][2 * (u & 1) + 1] * un;
+    z.d[u] = (uint32_t)__builtin_bit_cast(uint16_t, (bf16_t)lo) |
+             ((uint32_t)__builtin_bit_cast(uint16_t, (bf16_t)hi) << 16);
+  }
+}
+
+// the outputs that lie in the row, one by one (its last ones)
+__device__ __forceinline__ void load_tail(Out16<1>& z, const float* p, int64_t n) {
+#pragma unroll
+  for (int u = 0; u < 16; ++u)
+    if (u < n) z.d[u] = __builtin_bit_cast(uint32_t, p[u]);
+}
+__device__ __forceinline__ void load_tail(Out16<3>& z, const bf16_t* p, int64_t n) {
+  const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const uint32_t lo = 2 * u < n ? h[2 * u] : 0u, hi = 2 * u + 1 < n ? h[2 * u + 1] : 0u;
+    z.d[u] = lo | (hi << 16);
+  }
+}
+__device__ __forceinline__ void store_tail(const Out16<1>& z, float* p, int64_t n) {
+#pragma unroll
+  for (int u = 0; u < 16; ++u)
+    if (u < n) p[u] = __builtin_bit_cast(float, z.d[u]);
+}
+__device__ __forceinline__ void store_tail(const Out16<3>& z, bf16_t* p, int64_t n) {
+  uint16_t* h = reinterpret_cast<uint16_t*>(p);
+#pragma unroll
+  for (int u = 0; u < 16; ++u)
+    if (u < n) h[u] = (uint16_t)(z.d[u >> 1] >> ((u & 1) * 16));
+}
+
+// One item (SUBS * 16 rows at most), every gridDim.x-th 256 outputs.  Tile t
+// of a wave holds output 16 q + 4 t + e at D's row 4 q + e, so that a lane's
+// four tiles are 16 consecutive outputs of its row (64 bytes of FP32, 32 of
+// BF16), read and written 16 bytes at a time.  The first outputs and the
+// first 32 ranks of B are on their way while v is made ready; further ones
+// are requested before the outputs of the step are stored.
+template <int XT, int YT, bool INLINE, int SUBS>
+__global__ __launch_bounds__(256, SUBS == 1 ? 4 : 3) void lora_expand_kernel(LoraArgs a, Plan plan, int tm, int slices,
                                                           const float* __restrict__ v) {
   constexpr int P = Mma<XT>::pieces;
   typedef typename Elem<XT>::type X;
   typedef typename Elem<YT>::type Y;
   extern __shared__ uint4 dyn[];
-  __shared__ int rows[64];
-  __shared__ float unscale[64];
+  __shared__ int rows[kItemRows];
+  __shared__ float unscale[kItemRows];
   X* pieces = reinterpret_cast<X*>(dyn);  // [P][tm][pitch]
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 15, q = lane >> 4;
 
   for (int item = blockIdx.y;; item += gridDim.y) {
@@ -328,12 +380,48 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs a, Plan plan,
     const int count = find_item<INLINE>(a, plan, item, tm, rows, &slot);
     if (!count) return;
     const int rank = rank_of(a, slot);
-    const int chunks = (rank + 31) / 32, pitch = chunks * 32 + 8;  // 16 bytes past: other banks
     const float scale = a.scales ? a.scales[slot] : 1.0f;
-    const int subs = (count + 15) / 16;
+    const int chunks = (rank + 31) / 32, pitch = chunks * 32 + 8;  // 16 bytes past: other banks
+    const X* bs = static_cast<const X*>(a.b) + (int64_t)slot * a.n * a.r;
+    Y* yrow[SUBS];
+#pragma unroll
+    for (int s = 0; s < SUBS; ++s)
+      yrow[s] = static_cast<Y*>(a.y) + (int64_t)rows[s * 16 + c < count ? s * 16 + c : 0] * a.ldy;
+
+    uint4 w[2][kTilesN];
+    // B's rows from n0 on: a uniform base and 32-bit offsets
+    auto load_w = [&](uint4 (&d)[kTilesN], int64_t n0, int rc) __attribute__((always_inline)) {
+      int j = rc * 32 + q * 8;
+      j = j < (int)a.r ? j : (int)a.r - 8;  // past r: any, masked below
+      const int last = a.n - n0 < kWaveN ? (int)(a.n - n0) - 1 : kWaveN - 1;
+      const X* base = bs + n0 * a.r;
+#pragma unroll
+      for (int t = 0; t < kTilesN; ++t) {
+        const int o = (c >> 2) * (4 * kTilesN) + t * 4 + (c & 3);
+        // an output past the last is not stored
+        d[t] = *reinterpret_cast<const uint4*>(base + (uint32_t)((o < last ? o : last) * (int)a.r + j));
+      }
+    };
+    Out16<YT> z[SUBS] = {};
+    auto load_y = [&](int64_t n0) __attribute__((always_inline)) {
+      const int64_t o = n0 + q * 16;
+#pragma unroll
+      for (int s = 0; s < SUBS; ++s) {
+        if (s * 16 + c < count) {
+          if (o + 16 <= a.n) __builtin_memcpy(&z[s], yrow[s] + o, sizeof(z[s]));
+          else load_tail(z[s], yrow[s] + o, a.n - o);
+        }
+      }
+    };
+    const int64_t step = (int64_t)gridDim.x * kBlockN;
+    int64_t n0 = ((int64_t)blockIdx.x * 4 + wave) * kWaveN;
+    if (n0 < a.n) {
+      load_w(w[0], n0, 0);
+      load_y(n0);
+    }
 
     // v of the item's rows, 16 lanes to a row
-    for (int sub = 0; sub < subs; ++sub) {
+    for (int sub = 0; sub * 16 < count; ++sub) {
       const int at = sub * 16 + (tid >> 4), j0 = (tid & 15) * 4;
       const bool live = at < count;
       const float* vr = v + (int64_t)rows[live ? at : 0] * a.r;
@@ -344,8 +432,18 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs a, Plan plan,
         const int j = j0 + h * 64;
         val[h] = (f32x4){0.f, 0.f, 0.f, 0.f};
         if (live && j < rank) {
-          for (int z = 0; z < slices; ++z)
-            val[h] += *reinterpret_cast<const f32x4*>(vr + (int64_t)z * a.m * a.r + j);
+          // four slices at a time (all loads out before the first add)
+#pragma unroll 1
+          for (int u0 = 0; u0 < slices; u0 += 4) {
+            f32x4 part[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              part[u] = *reinterpret_cast<const f32x4*>(
+                  vr + (int64_t)(u0 + u < slices ? u0 + u : u0) * a.m * a.r + j);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              if (u0 + u < slices) val[h] += part[u];
+          }
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             val[h][e] = j + e < rank ? val[h][e] * scale : 0.0f;
@@ -371,78 +469,74 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs a, Plan plan,
 #pragma unroll
           for (int e = 0; e < 4; ++e) split(val[h][e], up, p[e]);
 #pragma unroll
-          for (int w = 0; w < P; ++w) {
-            X o[4] = {p[0][w], p[1][w], p[2][w], p[3][w]};
-            __builtin_memcpy(pieces + (w * tm + at) * pitch + j, o, 8);
+          for (int u = 0; u < P; ++u) {
+            X o[4] = {p[0][u], p[1][u], p[2][u], p[3][u]};
+            __builtin_memcpy(pieces + (u * tm + at) * pitch + j, o, 8);
           }
         }
       }
     }
     __syncthreads();
 
-    for (int64_t n0 = ((int64_t)blockIdx.x * 4 + wave) * kWaveN; n0 < a.n;
-         n0 += (int64_t)gridDim.x * kBlockN) {
-      f32x4 acc[4][kTilesN];
+    for (; n0 < a.n; n0 += step) {
+      f32x4 acc[SUBS][kTilesN];
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
+      for (int s = 0; s < SUBS; ++s)
 #pragma unroll
         for (int t = 0; t < kTilesN; ++t) acc[s][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
-      for (int rc = 0; rc < chunks; ++rc) {
+      auto multiply = [&](uint4 (&d)[kTilesN], int rc) __attribute__((always_inline)) {
         const int j = rc * 32 + q * 8;
-        uint4 w[kTilesN];
-#pragma unroll
-        for (int t = 0; t < kTilesN; ++t) {
-          const int64_t o = n0 + (c >> 2) * (4 * kTilesN) + t * 4 + (c & 3);
-          w[t] = make_uint4(0, 0, 0, 0);
-          if (o < a.n && j < rank)
-            w[t] = *reinterpret_cast<const uint4*>(static_cast<const X*>(a.b) +
-                                                   ((int64_t)slot * a.n + o) * a.r + j);
-        }
-        if (rank - j < 8) {  // entries past the rank may hold anything
+        if (rc * 32 + 32 > rank) {  // entries past the rank may hold anything
           uint32_t keep[4];
 #pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            const int left = rank - j - 2 * d;
-            keep[d] = left >= 2 ? 0xFFFFFFFFu : (left == 1 ? 0xFFFFu : 0u);
+          for (int h = 0; h < 4; ++h) {
+            const int left = rank - j - 2 * h;
+            keep[h] = left >= 2 ? 0xFFFFFFFFu : (left == 1 ? 0xFFFFu : 0u);
           }
 #pragma unroll
           for (int t = 0; t < kTilesN; ++t) {
-            w[t].x &= keep[0];
-            w[t].y &= keep[1];
-            w[t].z &= keep[2];
-            w[t].w &= keep[3];
+            d[t].x &= keep[0];
+            d[t].y &= keep[1];
+            d[t].z &= keep[2];
+            d[t].w &= keep[3];
           }
         }
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          if (s < subs) {
+        for (int s = 0; s < SUBS; ++s) {
+          if (s * 16 < count) {
 #pragma unroll
             for (int p = 0; p < P; ++p) {
               const uint4 b = *reinterpret_cast<const uint4*>(pieces + (p * tm + s * 16 + c) * pitch + j);
 #pragma unroll
-              for (int t = 0; t < kTilesN; ++t) acc[s][t] = Mma<XT>::run(w[t], b, acc[s][t]);
+              for (int t = 0; t < kTilesN; ++t) acc[s][t] = Mma<XT>::run(d[t], b, acc[s][t]);
             }
           }
         }
+      };
+      for (int rc = 0; rc < chunks; rc += 2) {
+        if (rc + 1 < chunks) load_w(w[1], n0, rc + 1);
+        multiply(w[0], rc);
+        if (rc + 1 < chunks) {
+          if (rc + 2 < chunks) load_w(w[0], n0, rc + 2);
+          multiply(w[1], rc + 1);
+        }
       }
+      Out16<YT> sum[SUBS];
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const int at = s * 16 + c;
-        if (at < count) {
-          const float un = XT == 2 ? unscale[at] : 1.0f;
-          const int64_t o = n0 + q * 16;
-          Y* yp = static_cast<Y*>(a.y) + (int64_t)rows[at] * a.ldy + o;
-          if (o + 16 <= a.n) {
-            Out16<YT> z;
-            __builtin_memcpy(&z, yp, sizeof(z));
+      for (int s = 0; s < SUBS; ++s) {
+        sum[s] = z[s];
+        add16(sum[s], acc[s], XT == 2 ? unscale[s * 16 + c < count ? s * 16 + c : 0] : 1.0f);
+      }
+      if (n0 + step < a.n) {
+        load_w(w[0], n0 + step, 0);
+        load_y(n0 + step);
+      }
+      const int64_t o = n0 + q * 16;
 #pragma unroll
-            for (int u = 0; u < 16; ++u) z.e[u] = (Y)((float)z.e[u] + acc[s][u >> 2][u & 3] * un);
-            __builtin_memcpy(yp, &z, sizeof(z));
-          } else {
-#pragma unroll
-            for (int u = 0; u < 16; ++u)
-              if (o + u < a.n) yp[u] = (Y)((float)yp[u] + acc[s][u >> 2][u & 3] * un);
-          }
+      for (int s = 0; s < SUBS; ++s) {
+        if (s * 16 + c < count) {
+          if (o + 16 <= a.n) __builtin_memcpy(yrow[s] + o, &sum[s], sizeof(sum[s]));
+          else store_tail(sum[s], yrow[s] + o, a.n - o);
         }
       }
     }
@@ -452,8 +546,7 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs a, Plan plan,
 
 int64_t round256(int64_t v) { return (v + 255) / 256 * 256; }
 
-// rows of an item: as many as keep its pieces within 64 KB of LDS
-int item_rows(int64_t r) { return r > 128 ? 32 : 64; }
+int item_rows(int64_t m) { return m <= 16 ? 16 : kItemRows; }
 
 int64_t max_items(int64_t m, int64_t slots, int64_t tm) {
   // every item but an adapter's last is full
@@ -473,20 +566,20 @@ int ranks_per_block(int64_t m, int64_t r) {
 }
 
 // k in slices until there are about as many work-groups as compute units; a
-// wave keeps at least 64 of k, and the expand kernel sums at most 16 slices
+// wave keeps at least 64 of k
 int64_t slices_of(int64_t m, int64_t k, int64_t r, int64_t slots) {
-  const int tm = item_rows(r), rt = ranks_per_block(m, r);
+  const int tm = item_rows(m), rt = ranks_per_block(m, r);
   const int64_t items = max_items(m, slots, tm), units = items > (m + 15) / 16 ? items : (m + 15) / 16;
   const int64_t groups = (r + rt * 16 - 1) / (rt * 16);
   int64_t s = 256 / (units * groups);
   const int64_t most = k / (64 * kShrinkWaves);
   s = s < most ? s : most;
-  return s < 1 ? 1 : (s > 16 ? 16 : s);
+  return s < 1 ? 1 : (s > kMaxSlices ? kMaxSlices : s);
 }
 
 template <int XT, int YT, bool INLINE>
 hipError_t launch(const LoraArgs& a, const Plan& plan, float* v, hipStream_t st) {
-  const int tm = item_rows(a.r), rt = ranks_per_block(a.m, a.r);
+  const int tm = item_rows(a.m), rt = ranks_per_block(a.m, a.r);
   const int64_t items = max_items(a.m, a.slots, tm);
   const int64_t rows = a.m < tm ? a.m : tm;
   const int subs = (int)((rows + 15) / 16);
@@ -500,10 +593,17 @@ hipError_t launch(const LoraArgs& a, const Plan& plan, float* v, hipStream_t st)
     hipLaunchKernelGGL((lora_shrink_kernel<XT, 4, INLINE>), gs, dim3(512), 0, st, a, plan, tm, subs, v);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  // Work-groups for eight to a compute unit; one takes several 256 outputs
+  // where there are more, so that finding its rows and making v ready (a
+  // chain of four memory latencies) is paid once for all of them.
   const int64_t tiles = (a.n + kBlockN - 1) / kBlockN;
-  const dim3 ge((unsigned)(tiles < 8192 ? tiles : 8192), (unsigned)(items < 32768 ? items : 32768));
+  const int64_t want = (2048 + items - 1) / items;
+  const dim3 ge((unsigned)(tiles < want ? tiles : want), (unsigned)(items < 32768 ? items : 32768));
   const size_t lds = (size_t)Mma<XT>::pieces * tm * ((a.r + 31) / 32 * 32 + 8) * 2;
-  hipLaunchKernelGGL((lora_expand_kernel<XT, YT, INLINE>), ge, dim3(256), lds, st, a, plan, tm, slices, v);
+  if (INLINE && tm == 16)
+    hipLaunchKernelGGL((lora_expand_kernel<XT, YT, INLINE, 1>), ge, dim3(256), lds, st, a, plan, tm, slices, v);
+  else
+    hipLaunchKernelGGL((lora_expand_kernel<XT, YT, INLINE, 2>), ge, dim3(256), lds, st, a, plan, tm, slices, v);
   return hipGetLastError();
 }
 
@@ -511,11 +611,11 @@ hipError_t launch(const LoraArgs& a, const Plan& plan, float* v, hipStream_t st)
 
 size_t lora_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_t r, int64_t slots) {
   (void)n;
-  return (size_t)(plan_bytes(m, slots, item_rows(r)) + round256(slices_of(m, k, r, slots) * m * r * 4));
+  return (size_t)(plan_bytes(m, slots, item_rows(m)) + round256(slices_of(m, k, r, slots) * m * r * 4));
 }
 
 hipError_t launch_lora_accumulate(const LoraArgs& a, void* ws, hipStream_t st) {
-  const int tm = item_rows(a.r);
+  const int tm = item_rows(a.m);
   char* base = static_cast<char*>(ws);
   float* v = reinterpret_cast<float*>(base + plan_bytes(a.m, a.slots, tm));
   Plan plan = {};
