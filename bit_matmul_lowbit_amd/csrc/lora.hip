@@ -12,23 +12,24 @@
 // fit one wave, and ballots pick out the rows that share one (no launch, no
 // memory).  More rows are sorted by one work-group first (lora_plan_kernel).
 //
-// Both products run on v_mfma_f32_16x16x32 with operands straight from
-// memory: A and B are stored with the contracted index innermost, so a
-// lane's 8 operand values are 16 contiguous bytes.
+// Both products run on v_mfma_f32_16x16x32.
 //   A operand (16 x 32): lane l holds row l % 16, 8 values at 8 (l / 16)
 //   B operand (32 x 16): lane l holds column l % 16, 8 values at 8 (l / 16)
 //   D (16 x 16): lane l, register e holds row 4 (l / 16) + e, column l % 16
 //
 // shrink: v^T = A x^T, one work-group per (16 rows of an item, up to 64 of
 // its ranks, slice of k); its eight waves split the slice and are summed
-// through LDS.  The slices' FP32 sums go to the workspace.
-// expand: y^T += B v^T, one work-group per (item, share of the outputs, 256 at
-// a time).  v is summed
-// over the slices, scaled, and split into 16-bit pieces whose sum holds it to
-// FP32's precision or nearly (FP16: two pieces of a row scaled by a power of
-// two, 22 bits; BF16: three pieces, 24 bits), since a single 16-bit v would
-// be the least exact value of the whole sum.  No atomics anywhere: every
-// value has one writer and its sum one order.
+// through LDS.  The slices' FP32 sums go to the workspace.  Operands taken
+// straight from memory would have neighbouring lanes in 16 different rows,
+// and such loads run at a quarter of the rate of contiguous ones; a wave
+// loads 128 contiguous bytes of a row by eight lanes instead and passes them
+// to the lanes that need them through LDS of its own.
+// expand: y += v B^T, one work-group per (item, share of the outputs, 256 at a
+// time).  v is summed over the slices, scaled, and split into 16-bit pieces
+// whose sum holds it to FP32's precision or nearly (FP16: two pieces of a row
+// scaled by a power of two, 22 bits; BF16: three pieces, 24 bits), since a
+// single 16-bit v would be the least exact value of the whole sum.  No
+// atomics anywhere: every value has one writer and its sum one order.
 #include "common.h"
 
 namespace lowbit {
@@ -131,74 +132,93 @@ __device__ __forceinline__ int find_item(const LoraArgs& a, const Plan& plan, in
   return count;
 }
 
-// Rows sorted by adapter, in one work-group: a histogram over the adapters
-// (LDS; the rows of a wave that share one add to it once), its prefix sums,
-// then each row's place.  Rows of one adapter keep nearly their order; which
-// one they get changes no result, each row being a column of its own.
-__global__ __launch_bounds__(1024) void lora_plan_kernel(LoraArgs a, Plan plan, int tm) {
+// inclusive prefix sum over the wave's lanes, by DPP
+__device__ __forceinline__ int wave_scan(int v) {
+#define LOWBIT_SCAN(CTRL, ROWS) v += __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false)
+  LOWBIT_SCAN(0x111, 0xF);  // row_shr:1
+  LOWBIT_SCAN(0x112, 0xF);  // row_shr:2
+  LOWBIT_SCAN(0x114, 0xF);  // row_shr:4
+  LOWBIT_SCAN(0x118, 0xF);  // row_shr:8
+  LOWBIT_SCAN(0x142, 0xA);  // row_bcast:15 into rows 1 and 3
+  LOWBIT_SCAN(0x143, 0xC);  // row_bcast:31 into rows 2 and 3
+#undef LOWBIT_SCAN
+  return v;
+}
+
+// Rows sorted by adapter, in one work-group: each row takes the next place
+// among its adapter's (a counter in LDS), prefix sums over the adapters give
+// each adapter's first place.  Rows of one adapter keep nearly their order;
+// which place one gets changes no result, each row being a row of the products
+// of its own.  A wave whose rows share one adapter, as in a long prompt, adds
+// to the counter once.  The work-group's first 4096 rows keep their places in
+// registers, later ones in `place`.
+__global__ __launch_bounds__(1024) void lora_plan_kernel(LoraArgs a, Plan plan, int tm, int* place) {
+  constexpr int kHeld = 4;
   __shared__ int cnt[kMaxSlots];
-  __shared__ uint64_t wave_sum[16];
-  const int tid = threadIdx.x, lane = tid & 63;
+  __shared__ int wave_rows[16], wave_items[16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int slot[kHeld], at[kHeld];
+#pragma unroll
+  for (int t = 0; t < kHeld; ++t) slot[t] = t * 1024 + tid < a.m ? slot_of(a, t * 1024 + tid) : -1;
   for (int s = tid; s < a.slots; s += 1024) cnt[s] = 0;
   __syncthreads();
-  const int64_t steps = (a.m + 1023) / 1024;
-  for (int64_t t = 0; t < steps; ++t) {
-    const int64_t i = t * 1024 + tid;
-    const int s = i < a.m ? slot_of(a, i) : -1;
-    uint64_t left = __ballot(s >= 0);
-    while (left) {
-      const int leader = __builtin_ctzll(left);
-      const uint64_t same = __ballot(s == __builtin_amdgcn_readlane(s, leader));
-      if (lane == leader) atomicAdd(&cnt[s], __popcll(same));
-      left &= ~same;
+  auto take = [&](int s) __attribute__((always_inline)) {
+    const int s0 = __builtin_amdgcn_readfirstlane(s);
+    if (__ballot(s == s0) == ~0ull) {
+      if (s0 < 0) return 0;
+      int first = 0;
+      if (lane == 0) first = atomicAdd(&cnt[s0], 64);
+      return __builtin_amdgcn_readfirstlane(first) + lane;
     }
+    return s >= 0 ? atomicAdd(&cnt[s], 1) : 0;
+  };
+  const int64_t steps = (a.m + 1023) / 1024;
+#pragma unroll
+  for (int t = 0; t < kHeld; ++t)
+    if (t < steps) at[t] = take(slot[t]);
+  for (int64_t t = kHeld; t < steps; ++t) {
+    const int64_t i = t * 1024 + tid;
+    const int p = take(i < a.m ? slot_of(a, i) : -1);
+    if (i < a.m) place[i] = p;
   }
   __syncthreads();
-  // exclusive prefix sums over the adapters: rows (low half), items (high)
-  uint64_t own[4], sum = 0;
+  int own[4], rows = 0, items = 0;
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
-    const int s = tid * 4 + u;
-    const int n = s < a.slots ? cnt[s] : 0;
-    own[u] = (uint64_t)(uint32_t)n | ((uint64_t)(uint32_t)((n + tm - 1) / tm) << 32);
-    sum += own[u];
+    own[u] = tid * 4 + u < a.slots ? cnt[tid * 4 + u] : 0;
+    rows += own[u];
+    items += (own[u] + tm - 1) / tm;
   }
-  uint64_t inc = sum;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const uint64_t o = __shfl_up(inc, off, 64);
-    if (lane >= off) inc += o;
+  const int rows_to = wave_scan(rows), items_to = wave_scan(items);
+  if (lane == 63) {
+    wave_rows[wave] = rows_to;
+    wave_items[wave] = items_to;
   }
-  if (lane == 63) wave_sum[tid >> 6] = inc;
   __syncthreads();
-  uint64_t base = inc - sum;
-  for (int w = 0; w < (tid >> 6); ++w) base += wave_sum[w];
-  if (tid == 1023) *plan.items_used = (int)((base + sum) >> 32);
+  int start = rows_to - rows, it = items_to - items;
+  for (int w = 0; w < wave; ++w) {
+    start += wave_rows[w];
+    it += wave_items[w];
+  }
+  if (tid == 1023) *plan.items_used = it + items;
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int s = tid * 4 + u;
     if (s < a.slots) {
-      const int n = (int)(uint32_t)own[u], start = (int)(uint32_t)base, it = (int)(base >> 32);
-      for (int p = 0; p * tm < n; ++p)
-        plan.items[it + p] = Item{s, start + p * tm, n - p * tm < tm ? n - p * tm : tm, 0};
+      for (int p = 0; p < own[u]; p += tm)
+        plan.items[it++] = Item{s, start + p, own[u] - p < tm ? own[u] - p : tm, 0};
       cnt[s] = start;
+      start += own[u];
     }
-    base += own[u];
   }
   __syncthreads();
-  for (int64_t t = 0; t < steps; ++t) {
+#pragma unroll
+  for (int t = 0; t < kHeld; ++t)
+    if (slot[t] >= 0) plan.rows[cnt[slot[t]] + at[t]] = t * 1024 + tid;
+  for (int64_t t = kHeld; t < steps; ++t) {
     const int64_t i = t * 1024 + tid;
     const int s = i < a.m ? slot_of(a, i) : -1;
-    uint64_t left = __ballot(s >= 0);
-    while (left) {
-      const int leader = __builtin_ctzll(left);
-      const uint64_t same = __ballot(s == __builtin_amdgcn_readlane(s, leader));
-      int at = 0;
-      if (lane == leader) at = atomicAdd(&cnt[s], __popcll(same));
-      at = __builtin_amdgcn_readlane(at, leader);
-      if ((same >> lane) & 1) plan.rows[at + lanes_below(same)] = (int)i;
-      left &= ~same;
-    }
+    if (s >= 0) plan.rows[cnt[s] + place[i]] = (int)i;
   }
 }
 
@@ -209,8 +229,13 @@ __global__ __launch_bounds__(1024) void lora_plan_kernel(LoraArgs a, Plan plan, 
 template <int XT, int RT, bool INLINE>
 __global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs a, Plan plan, int tm, int subs,
                                                           float* __restrict__ v) {
+  constexpr int T = 1 + RT;                 // 16-row tiles of a step: x, then A's
+  constexpr int U = RT == 4 ? 2 : RT == 2 ? 3 : 4;  // steps in flight
   __shared__ int rows[kItemRows];
-  __shared__ f32x4 red[kShrinkWaves][RT][64];
+  // per wave, a step of each tile: 16 rows of 8 pieces of 16 bytes, piece p of
+  // row i at p ^ (i & 7) (the lanes of a read then fall into different banks);
+  // afterwards the waves' sums
+  __shared__ uint4 stage[kShrinkWaves][T][16][8];
   const int item = blockIdx.x / subs, sub = blockIdx.x % subs;
   int slot = 0;
   const int count = find_item<INLINE>(a, plan, item, tm, rows, &slot);
@@ -219,70 +244,89 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs a, Plan plan,
   const int rank = rank_of(a, slot), r0 = (int)blockIdx.y * RT * 16;
   if (r0 >= rank) return;
 
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = lane & 15, q = lane >> 4;
-  const int64_t row = rows[sub * 16 + (c < here ? c : here - 1)];
-  const uint16_t* xp = static_cast<const uint16_t*>(a.x) + row * a.ldx + q * 8;
-  const uint16_t* ap[RT];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, q = lane >> 4;    // as an operand's lane
+  const int lr = lane >> 3, lp = lane & 7;   // as a loading lane: rows lr and lr + 8, piece lp
+  const uint16_t* xp[2];
 #pragma unroll
-  for (int t = 0; t < RT; ++t) {
-    const int j = r0 + t * 16 + c;
-    ap[t] = static_cast<const uint16_t*>(a.a) + ((int64_t)slot * a.r + (j < rank ? j : rank - 1)) * a.k +
-            q * 8;
+  for (int h = 0; h < 2; ++h) {
+    const int at = lr + 8 * h;
+    xp[h] = static_cast<const uint16_t*>(a.x) + (int64_t)rows[sub * 16 + (at < here ? at : here - 1)] * a.ldx;
   }
-  const int steps = (int)((a.k + 31) / 32);
+  const uint16_t* ap = static_cast<const uint16_t*>(a.a) + (int64_t)slot * a.r * a.k;
+  uint32_t aoff[RT][2];
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int j = r0 + t * 16 + lr + 8 * h;
+      aoff[t][h] = (uint32_t)(j < rank ? j : rank - 1) * (uint32_t)a.k;
+    }
+  const int k = (int)a.k, steps = (k + 63) / 64;
   const int parts = kShrinkWaves * (int)gridDim.z;
   const int per = (steps + parts - 1) / parts;
   const int s0 = ((int)blockIdx.z * kShrinkWaves + wave) * per;
   const int s1 = s0 + per < steps ? s0 + per : steps;
-  const bool ragged = a.k % 32 != 0;  // the last step's upper lanes have no k
 
   f32x4 acc[RT];
 #pragma unroll
   for (int t = 0; t < RT; ++t) acc[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
-  // a ring of U steps, each reloaded as soon as it is used; past the slice
-  // the last step is loaded again and not used
-  constexpr int U = RT == 4 ? 4 : 8;
-  uint4 xr[U], ar[U][RT];
+  uint4 in[U][T][2];
   auto load = [&](int u, int s) __attribute__((always_inline)) {
-    s = s < s1 ? s : s1 - 1;
-    int64_t at = (int64_t)s * 32;
-    if (ragged && at + q * 8 >= a.k) at = a.k - 8 - q * 8;
-    xr[u] = *reinterpret_cast<const uint4*>(xp + at);
+    int at = s * 64 + lp * 8;
+    at = at < k ? at : k - 8;  // pieces past k are zeroed below
 #pragma unroll
-    for (int t = 0; t < RT; ++t) ar[u][t] = *reinterpret_cast<const uint4*>(ap[t] + at);
+    for (int h = 0; h < 2; ++h) {
+      in[u][0][h] = *reinterpret_cast<const uint4*>(xp[h] + at);
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+        in[u][1 + t][h] = *reinterpret_cast<const uint4*>(ap + (aoff[t][h] + (uint32_t)at));
+    }
   };
-  if (s0 < s1) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) load(u, s0 + u);
-    for (int s = s0; s < s1; s += U) {
+  for (int u = 0; u < U; ++u)
+    if (s0 + u < s1) load(u, s0 + u);
+  for (int s = s0; s < s1; s += U) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (s + u < s1) {
-          if (ragged && s + u == steps - 1 && (s + u) * 32 + q * 8 >= a.k) {
-            xr[u] = make_uint4(0, 0, 0, 0);
+    for (int u = 0; u < U; ++u) {
+      if (s + u < s1) {
+        if ((s + u) * 64 + 64 > k && (s + u) * 64 + lp * 8 >= k) {
 #pragma unroll
-            for (int t = 0; t < RT; ++t) ar[u][t] = xr[u];
-          }
-#pragma unroll
-          for (int t = 0; t < RT; ++t) acc[t] = Mma<XT>::run(ar[u][t], xr[u], acc[t]);
-          load(u, s + U + u);
+          for (int t = 0; t < T; ++t) in[u][t][0] = in[u][t][1] = make_uint4(0, 0, 0, 0);
         }
+        // a wave's LDS accesses are carried out in their order; the empty asm
+        // statements keep the compiler to it
+        __asm__ volatile("" ::: "memory");
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) stage[wave][t][lr + 8 * h][lp ^ (lr & 7)] = in[u][t][h];
+        __asm__ volatile("" ::: "memory");
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const uint4 b = stage[wave][0][c][(w * 4 + q) ^ (c & 7)];
+#pragma unroll
+          for (int t = 0; t < RT; ++t)
+            acc[t] = Mma<XT>::run(stage[wave][1 + t][c][(w * 4 + q) ^ (c & 7)], b, acc[t]);
+        }
+        if (s + U + u < s1) load(u, s + U + u);
       }
     }
   }
+  __syncthreads();
+  f32x4(*red)[RT][64] = reinterpret_cast<f32x4(*)[RT][64]>(&stage[0][0][0][0]);
 #pragma unroll
   for (int t = 0; t < RT; ++t) red[wave][t][lane] = acc[t];
   __syncthreads();
   if (threadIdx.x < RT * 64) {
-    const int t = threadIdx.x >> 6;
+    const int t = wave;
     f32x4 sum = red[0][t][lane];
 #pragma unroll
     for (int w = 1; w < kShrinkWaves; ++w) sum += red[w][t][lane];
     const int j = r0 + t * 16 + q * 4;
     // j .. j + 3 lie in the row (r is a multiple of 8); what is past the rank is not read
     if (c < here && j < rank)
-      *reinterpret_cast<f32x4*>(v + ((int64_t)blockIdx.z * a.m + row) * a.r + j) = sum;
+      *reinterpret_cast<f32x4*>(v + ((int64_t)blockIdx.z * a.m + rows[sub * 16 + c]) * a.r + j) = sum;
   }
 }
 
@@ -308,62 +352,72 @@ __device__ __forceinline__ float max16(float v) {
   return v;
 }
 
-// 16 consecutive outputs of a row, as they are stored
+// largest magnitude of the finite ones of four values
+__device__ __forceinline__ float finite_max(f32x4 v) {
+  float top = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) top = fabsf(v[e]) <= 3.4028235e38f ? fmaxf(top, fabsf(v[e])) : top;
+  return top;
+}
+
+// four consecutive outputs of a row, as they are stored
 template <int YT>
-struct Out16 {
-  uint32_t d[YT == 1 ? 16 : 8];
+struct Out4 {
+  uint32_t d[YT == 1 ? 4 : 2];
 };
 
 // + add * un, rounded once
-__device__ __forceinline__ void add16(Out16<1>& z, const f32x4 (&add)[kTilesN], float un) {
+__device__ __forceinline__ Out4<1> add4(Out4<1> z, float a0, float a1, float a2, float a3) {
+  const float add[4] = {a0, a1, a2, a3};
 #pragma unroll
-  for (int u = 0; u < 16; ++u)
-    z.d[u] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, z.d[u]) + add[u >> 2][u & 3] * un);
+  for (int u = 0; u < 4; ++u)
+    z.d[u] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, z.d[u]) + add[u]);
+  return z;
 }
-__device__ __forceinline__ void add16(Out16<3>& z, const f32x4 (&add)[kTilesN], float un) {
+__device__ __forceinline__ Out4<3> add4(Out4<3> z, float a0, float a1, float a2, float a3) {
+  const float add[4] = {a0, a1, a2, a3};
 #pragma unroll
-  for (int u = 0; u < 8; ++u) {
-    const float lo = __builtin_bit_cast(float, z.d[u] << 16) + add[u >> 1][2 * (u & 1)] * un;
-    const float hi = __builtin_bit_cast(float, z.d[u] & 0xFFFF0000u) + add[u >> 1][2 * (u & 1) + 1] * un;
+  for (int u = 0; u < 2; ++u) {
+    const float lo = __builtin_bit_cast(float, z.d[u] << 16) + add[2 * u];
+    const float hi = __builtin_bit_cast(float, z.d[u] & 0xFFFF0000u) + add[2 * u + 1];
     z.d[u] = (uint32_t)__builtin_bit_cast(uint16_t, (bf16_t)lo) |
              ((uint32_t)__builtin_bit_cast(uint16_t, (bf16_t)hi) << 16);
   }
+  return z;
 }
 
-// the outputs that lie in the row, one by one (its last ones)
-__device__ __forceinline__ void load_tail(Out16<1>& z, const float* p, int64_t n) {
+// the first n < 4 of them (a row's last outputs)
+__device__ __forceinline__ void load_tail(Out4<1>& z, const float* p, int n) {
 #pragma unroll
-  for (int u = 0; u < 16; ++u)
+  for (int u = 0; u < 3; ++u)
     if (u < n) z.d[u] = __builtin_bit_cast(uint32_t, p[u]);
 }
-__device__ __forceinline__ void load_tail(Out16<3>& z, const bf16_t* p, int64_t n) {
+__device__ __forceinline__ void load_tail(Out4<3>& z, const bf16_t* p, int n) {
   const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
-#pragma unroll
-  for (int u = 0; u < 8; ++u) {
-    const uint32_t lo = 2 * u < n ? h[2 * u] : 0u, hi = 2 * u + 1 < n ? h[2 * u + 1] : 0u;
-    z.d[u] = lo | (hi << 16);
-  }
+  z.d[0] = n > 0 ? h[0] : 0u;
+  if (n > 1) z.d[0] |= (uint32_t)h[1] << 16;
+  z.d[1] = n > 2 ? h[2] : 0u;
 }
-__device__ __forceinline__ void store_tail(const Out16<1>& z, float* p, int64_t n) {
+__device__ __forceinline__ void store_tail(const Out4<1>& z, float* p, int n) {
 #pragma unroll
-  for (int u = 0; u < 16; ++u)
+  for (int u = 0; u < 3; ++u)
     if (u < n) p[u] = __builtin_bit_cast(float, z.d[u]);
 }
-__device__ __forceinline__ void store_tail(const Out16<3>& z, bf16_t* p, int64_t n) {
+__device__ __forceinline__ void store_tail(const Out4<3>& z, bf16_t* p, int n) {
   uint16_t* h = reinterpret_cast<uint16_t*>(p);
 #pragma unroll
-  for (int u = 0; u < 16; ++u)
+  for (int u = 0; u < 3; ++u)
     if (u < n) h[u] = (uint16_t)(z.d[u >> 1] >> ((u & 1) * 16));
 }
 
-// One item (SUBS * 16 rows at most), every gridDim.x-th 256 outputs.  Tile t
-// of a wave holds output 16 q + 4 t + e at D's row 4 q + e, so that a lane's
-// four tiles are 16 consecutive outputs of its row (64 bytes of FP32, 32 of
-// BF16), read and written 16 bytes at a time.  The first outputs and the
-// first 32 ranks of B are on their way while v is made ready; further ones
-// are requested before the outputs of the step are stored.
+// One item (SUBS * 16 rows at most), every gridDim.x-th 256 outputs.  Column c
+// of a wave's tile t is output 4 c + t, so that a lane's four tiles are four
+// consecutive outputs and 16 lanes read and write 256 contiguous bytes of an
+// FP32 row (128 of BF16).  The first outputs and the first 32 ranks of B are
+// on their way while v is made ready; further ones are requested before the
+// outputs of the step are stored.
 template <int XT, int YT, bool INLINE, int SUBS>
-__global__ __launch_bounds__(256, SUBS == 1 ? 4 : 3) void lora_expand_kernel(LoraArgs a, Plan plan, int tm, int slices,
+__global__ __launch_bounds__(256, SUBS == 1 || YT == 3 ? 3 : 2) void lora_expand_kernel(LoraArgs a, Plan plan, int tm, int slices,
                                                           const float* __restrict__ v) {
   constexpr int P = Mma<XT>::pieces;
   typedef typename Elem<XT>::type X;
@@ -383,10 +437,12 @@ __global__ __launch_bounds__(256, SUBS == 1 ? 4 : 3) void lora_expand_kernel(Lor
     const float scale = a.scales ? a.scales[slot] : 1.0f;
     const int chunks = (rank + 31) / 32, pitch = chunks * 32 + 8;  // 16 bytes past: other banks
     const X* bs = static_cast<const X*>(a.b) + (int64_t)slot * a.n * a.r;
-    Y* yrow[SUBS];
-#pragma unroll
-    for (int s = 0; s < SUBS; ++s)
-      yrow[s] = static_cast<Y*>(a.y) + (int64_t)rows[s * 16 + c < count ? s * 16 + c : 0] * a.ldy;
+    // where row 4 q + e of a part has its outputs n0 + 4 c ...; made anew at
+    // each use (kept, the pointers would cost a wave of occupancy)
+    auto yrow = [&](int s, int e, int64_t n0) __attribute__((always_inline)) {
+      const int at = s * 16 + q * 4 + e;
+      return static_cast<Y*>(a.y) + ((int64_t)rows[at < count ? at : 0] * a.ldy + n0 + c * 4);
+    };
 
     uint4 w[2][kTilesN];
     // B's rows from n0 on: a uniform base and 32-bit offsets
@@ -397,40 +453,49 @@ __global__ __launch_bounds__(256, SUBS == 1 ? 4 : 3) void lora_expand_kernel(Lor
       const X* base = bs + n0 * a.r;
 #pragma unroll
       for (int t = 0; t < kTilesN; ++t) {
-        const int o = (c >> 2) * (4 * kTilesN) + t * 4 + (c & 3);
+        const int o = c * kTilesN + t;
         // an output past the last is not stored
         d[t] = *reinterpret_cast<const uint4*>(base + (uint32_t)((o < last ? o : last) * (int)a.r + j));
       }
     };
-    Out16<YT> z[SUBS] = {};
+    Out4<YT> z[SUBS][4] = {};
     auto load_y = [&](int64_t n0) __attribute__((always_inline)) {
-      const int64_t o = n0 + q * 16;
+      const int64_t left = a.n - n0 - c * 4;
 #pragma unroll
-      for (int s = 0; s < SUBS; ++s) {
-        if (s * 16 + c < count) {
-          if (o + 16 <= a.n) __builtin_memcpy(&z[s], yrow[s] + o, sizeof(z[s]));
-          else load_tail(z[s], yrow[s] + o, a.n - o);
-        }
-      }
+      for (int s = 0; s < SUBS; ++s)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (s * 16 + q * 4 + e < count) {
+            const Y* at = yrow(s, e, n0);
+            if (left >= 4) __builtin_memcpy(&z[s][e], at, sizeof(z[s][e]));
+            else load_tail(z[s][e], at, (int)left);
+          }
     };
     const int64_t step = (int64_t)gridDim.x * kBlockN;
     int64_t n0 = ((int64_t)blockIdx.x * 4 + wave) * kWaveN;
-    if (n0 < a.n) {
-      load_w(w[0], n0, 0);
-      load_y(n0);
-    }
+    // B in a ring of two: its (outputs, 32 ranks) pieces in the order in which
+    // they are used, two of them ahead
+    int64_t pn = n0;
+    int prc = 0;
+    auto request = [&](uint4 (&d)[kTilesN]) __attribute__((always_inline)) {
+      if (pn >= a.n) return;
+      load_w(d, pn, prc);
+      if (++prc == chunks) {
+        prc = 0;
+        pn += step;
+      }
+    };
+    request(w[0]);
+    if (n0 < a.n) load_y(n0);
+    request(w[1]);
 
-    // v of the item's rows, 16 lanes to a row
+    // v of the item's rows, 16 lanes to a row, 64 ranks at a time
     for (int sub = 0; sub * 16 < count; ++sub) {
       const int at = sub * 16 + (tid >> 4), j0 = (tid & 15) * 4;
       const bool live = at < count;
       const float* vr = v + (int64_t)rows[live ? at : 0] * a.r;
-      f32x4 val[4];
-      float top = 0.0f;
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        const int j = j0 + h * 64;
-        val[h] = (f32x4){0.f, 0.f, 0.f, 0.f};
+      auto inner = [&](int j) __attribute__((always_inline)) {
+        f32x4 sum = (f32x4){0.f, 0.f, 0.f, 0.f};
         if (live && j < rank) {
           // four slices at a time (all loads out before the first add)
 #pragma unroll 1
@@ -442,18 +507,19 @@ __global__ __launch_bounds__(256, SUBS == 1 ? 4 : 3) void lora_expand_kernel(Lor
                   vr + (int64_t)(u0 + u < slices ? u0 + u : u0) * a.m * a.r + j);
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-              if (u0 + u < slices) val[h] += part[u];
+              if (u0 + u < slices) sum += part[u];
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            val[h][e] = j + e < rank ? val[h][e] * scale : 0.0f;
-            const float m = fabsf(val[h][e]);
-            if (m <= 3.4028235e38f) top = fmaxf(top, m);
-          }
+          for (int e = 0; e < 4; ++e) sum[e] = j + e < rank ? sum[e] * scale : 0.0f;
         }
-      }
+        return sum;
+      };
+      const f32x4 first = inner(j0);
       float up = 1.0f;
       if constexpr (XT == 2) {
+        float top = finite_max(first);
+#pragma unroll 1
+        for (int j = j0 + 64; j < rank; j += 64) top = fmaxf(top, finite_max(inner(j)));
         top = max16(top);
         // the row's largest value to [2^13, 2^14): far from FP16's ends on both sides
         int ex = top > 0.0f ? 13 - ilogbf(top) : 0;
@@ -461,84 +527,84 @@ __global__ __launch_bounds__(256, SUBS == 1 ? 4 : 3) void lora_expand_kernel(Lor
         up = ldexpf(1.0f, ex);
         if ((tid & 15) == 0 && live) unscale[at] = ldexpf(1.0f, -ex);
       }
+#pragma unroll 1
+      for (int j = j0; j < chunks * 32; j += 64) {
+        const f32x4 val = j == j0 ? first : inner(j);
+        X p[4][P];
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        const int j = j0 + h * 64;
-        if (j < chunks * 32) {
-          X p[4][P];
+        for (int e = 0; e < 4; ++e) split(val[e], up, p[e]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) split(val[h][e], up, p[e]);
-#pragma unroll
-          for (int u = 0; u < P; ++u) {
-            X o[4] = {p[0][u], p[1][u], p[2][u], p[3][u]};
-            __builtin_memcpy(pieces + (u * tm + at) * pitch + j, o, 8);
-          }
+        for (int u = 0; u < P; ++u) {
+          X o[4] = {p[0][u], p[1][u], p[2][u], p[3][u]};
+          __builtin_memcpy(pieces + (u * tm + at) * pitch + j, o, 8);
         }
       }
     }
     __syncthreads();
 
-    for (; n0 < a.n; n0 += step) {
-      f32x4 acc[SUBS][kTilesN];
+    f32x4 acc[SUBS][kTilesN];
+    int rc = 0;
+    // one piece of B; with the last ranks of an output, y is written
+    auto advance = [&](uint4 (&d)[kTilesN]) __attribute__((always_inline)) {
+      if (rc == 0) {
+#pragma unroll
+        for (int s = 0; s < SUBS; ++s)
+#pragma unroll
+          for (int t = 0; t < kTilesN; ++t) acc[s][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+      }
+      const int j = rc * 32 + q * 8;
+      if (rc * 32 + 32 > rank) {  // entries past the rank may hold anything
+        uint32_t keep[4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const int left = rank - j - 2 * h;
+          keep[h] = left >= 2 ? 0xFFFFFFFFu : (left == 1 ? 0xFFFFu : 0u);
+        }
+#pragma unroll
+        for (int t = 0; t < kTilesN; ++t) {
+          d[t].x &= keep[0];
+          d[t].y &= keep[1];
+          d[t].z &= keep[2];
+          d[t].w &= keep[3];
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < SUBS; ++s) {
+        if (s * 16 < count) {
+#pragma unroll
+          for (int p = 0; p < P; ++p) {
+            const uint4 b = *reinterpret_cast<const uint4*>(pieces + (p * tm + s * 16 + c) * pitch + j);
+#pragma unroll
+            for (int t = 0; t < kTilesN; ++t) acc[s][t] = Mma<XT>::run(b, d[t], acc[s][t]);
+          }
+        }
+      }
+      request(d);
+      if (++rc < chunks) return;
+      rc = 0;
 #pragma unroll
       for (int s = 0; s < SUBS; ++s)
 #pragma unroll
-        for (int t = 0; t < kTilesN; ++t) acc[s][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
-      auto multiply = [&](uint4 (&d)[kTilesN], int rc) __attribute__((always_inline)) {
-        const int j = rc * 32 + q * 8;
-        if (rc * 32 + 32 > rank) {  // entries past the rank may hold anything
-          uint32_t keep[4];
+        for (int e = 0; e < 4; ++e) {
+          const float un = XT == 2 ? unscale[s * 16 + q * 4 + e] : 1.0f;
+          z[s][e] = add4(z[s][e], acc[s][0][e] * un, acc[s][1][e] * un, acc[s][2][e] * un, acc[s][3][e] * un);
+        }
+      const int64_t left = a.n - n0 - c * 4;
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            const int left = rank - j - 2 * h;
-            keep[h] = left >= 2 ? 0xFFFFFFFFu : (left == 1 ? 0xFFFFu : 0u);
+      for (int s = 0; s < SUBS; ++s)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (s * 16 + q * 4 + e < count) {
+            Y* at = yrow(s, e, n0);
+            if (left >= 4) __builtin_memcpy(at, &z[s][e], sizeof(z[s][e]));
+            else store_tail(z[s][e], at, (int)left);
           }
-#pragma unroll
-          for (int t = 0; t < kTilesN; ++t) {
-            d[t].x &= keep[0];
-            d[t].y &= keep[1];
-            d[t].z &= keep[2];
-            d[t].w &= keep[3];
-          }
-        }
-#pragma unroll
-        for (int s = 0; s < SUBS; ++s) {
-          if (s * 16 < count) {
-#pragma unroll
-            for (int p = 0; p < P; ++p) {
-              const uint4 b = *reinterpret_cast<const uint4*>(pieces + (p * tm + s * 16 + c) * pitch + j);
-#pragma unroll
-              for (int t = 0; t < kTilesN; ++t) acc[s][t] = Mma<XT>::run(d[t], b, acc[s][t]);
-            }
-          }
-        }
-      };
-      for (int rc = 0; rc < chunks; rc += 2) {
-        if (rc + 1 < chunks) load_w(w[1], n0, rc + 1);
-        multiply(w[0], rc);
-        if (rc + 1 < chunks) {
-          if (rc + 2 < chunks) load_w(w[0], n0, rc + 2);
-          multiply(w[1], rc + 1);
-        }
-      }
-      Out16<YT> sum[SUBS];
-#pragma unroll
-      for (int s = 0; s < SUBS; ++s) {
-        sum[s] = z[s];
-        add16(sum[s], acc[s], XT == 2 ? unscale[s * 16 + c < count ? s * 16 + c : 0] : 1.0f);
-      }
-      if (n0 + step < a.n) {
-        load_w(w[0], n0 + step, 0);
-        load_y(n0 + step);
-      }
-      const int64_t o = n0 + q * 16;
-#pragma unroll
-      for (int s = 0; s < SUBS; ++s) {
-        if (s * 16 + c < count) {
-          if (o + 16 <= a.n) __builtin_memcpy(yrow[s] + o, &sum[s], sizeof(sum[s]));
-          else store_tail(sum[s], yrow[s] + o, a.n - o);
-        }
-      }
+      n0 += step;
+      if (n0 < a.n) load_y(n0);
+    };
+    while (n0 < a.n) {
+      advance(w[0]);
+      if (n0 < a.n) advance(w[1]);
     }
     __syncthreads();  // the next item's rows and pieces
   }
@@ -565,13 +631,13 @@ int ranks_per_block(int64_t m, int64_t r) {
   return r <= 32 ? 2 : 4;
 }
 
-// k in slices until there are about as many work-groups as compute units; a
-// wave keeps at least 64 of k
+// k in slices until there are about two work-groups per compute unit; a wave
+// keeps at least 64 of k
 int64_t slices_of(int64_t m, int64_t k, int64_t r, int64_t slots) {
   const int tm = item_rows(m), rt = ranks_per_block(m, r);
   const int64_t items = max_items(m, slots, tm), units = items > (m + 15) / 16 ? items : (m + 15) / 16;
   const int64_t groups = (r + rt * 16 - 1) / (rt * 16);
-  int64_t s = 256 / (units * groups);
+  int64_t s = (512 + units * groups - 1) / (units * groups);
   const int64_t most = k / (64 * kShrinkWaves);
   s = s < most ? s : most;
   return s < 1 ? 1 : (s > kMaxSlices ? kMaxSlices : s);
@@ -593,12 +659,14 @@ hipError_t launch(const LoraArgs& a, const Plan& plan, float* v, hipStream_t st)
     hipLaunchKernelGGL((lora_shrink_kernel<XT, 4, INLINE>), gs, dim3(512), 0, st, a, plan, tm, subs, v);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  // Work-groups for eight to a compute unit; one takes several 256 outputs
-  // where there are more, so that finding its rows and making v ready (a
-  // chain of four memory latencies) is paid once for all of them.
-  const int64_t tiles = (a.n + kBlockN - 1) / kBlockN;
-  const int64_t want = (2048 + items - 1) / items;
-  const dim3 ge((unsigned)(tiles < want ? tiles : want), (unsigned)(items < 32768 ? items : 32768));
+  // Work-groups: as many as run at once (three to a compute unit) where two
+  // shares of the outputs each are enough for that, else four times as many.  One that
+  // takes several shares finds its rows and makes v ready (a chain of four
+  // memory latencies) once for all of them.
+  const int64_t tiles = (a.n + kBlockN - 1) / kBlockN, all = tiles * items;
+  int64_t each = all <= 1536 ? (all + 767) / 768 : (all + 3071) / 3072;
+  each = each < tiles ? each : tiles;
+  const dim3 ge((unsigned)((tiles + each - 1) / each), (unsigned)(items < 32768 ? items : 32768));
   const size_t lds = (size_t)Mma<XT>::pieces * tm * ((a.r + 31) / 32 * 32 + 8) * 2;
   if (INLINE && tm == 16)
     hipLaunchKernelGGL((lora_expand_kernel<XT, YT, INLINE, 1>), ge, dim3(256), lds, st, a, plan, tm, slices, v);
@@ -626,7 +694,8 @@ hipError_t launch_lora_accumulate(const LoraArgs& a, void* ws, hipStream_t st) {
   plan.items_used = reinterpret_cast<int*>(base);
   plan.items = reinterpret_cast<Item*>(base + 256);
   plan.rows = reinterpret_cast<int*>(base + 256 + round256(max_items(a.m, a.slots, tm) * 16));
-  hipLaunchKernelGGL(lora_plan_kernel, dim3(1), dim3(1024), 0, st, a, plan, tm);
+  hipLaunchKernelGGL(lora_plan_kernel, dim3(1), dim3(1024), 0, st, a, plan, tm,
+                     reinterpret_cast<int*>(v));
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (a.x_type == 2) return launch<2, 1, false>(a, plan, v, st);
