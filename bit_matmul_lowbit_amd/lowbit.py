@@ -550,104 +550,115 @@ def lowbit_base3_to_t2(b3, scales_rm, n: int, k: int, codes=None, scales=None, s
 
 
 # ---------------------------------------------------------------------------
-# operators beside the products.  They take row strides, run on the device
-# their tensors are on (also when it is not the current one) and pass plain
-# integers, since a decode step makes many such calls.
+# operators beside the products.  They take row strides and run on the device
+# their tensors are on (also when it is not the current one).  A decode step
+# makes many such calls, so the checks are written for few attribute reads: the
+# common case passes one condition, and what fails it is named afterwards.
 
-_types = {}
-
-
-def _type_codes():
-    """torch dtype -> lowbit_type, filled on first use (importing this module
-    loads nothing)."""
-    if not _types:
-        import torch
-
-        _types.update({torch.float32: 1, torch.float16: 2, torch.bfloat16: 3})
-    return _types
+_types = {}      # torch dtype -> lowbit_type
+_torch = None
 
 
-def _float_rows(t, name, shape=None, device=None):
-    """(pointer, type code, row stride, rows, columns) of a 1-D or 2-D
-    FP32 / FP16 / BF16 device tensor whose rows are contiguous."""
-    code = _type_codes().get(t.dtype)
+def _first_use():
+    """Import torch and fill the type table (importing this module loads
+    nothing)."""
+    global _torch
+    import torch
+
+    _types.update({torch.float32: 1, torch.float16: 2, torch.bfloat16: 3})
+    _torch = torch
+    return torch
+
+
+def _float_rows(t, shape, dev, name):
+    """(pointer, type code, row stride) of a device tensor [m][k] (or [k], one
+    row) of FP32 / FP16 / BF16 with contiguous rows."""
+    code = _types.get(t.dtype)
+    if t.dim() == 2:
+        ld, unit = t.stride()
+        if code and unit == 1 and t.shape == shape and t.get_device() == dev:
+            return t.data_ptr(), code, ld if shape[0] > 1 else shape[1]
+        got = tuple(t.shape)
+    else:
+        unit = t.stride(-1) if t.dim() else 1
+        got = (1,) + tuple(t.shape)
     if code is None:
         raise TypeError(f"{name} has dtype {t.dtype}, expected float32, float16 or bfloat16")
     if not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
-    dims = t.dim()
-    if dims == 2:
-        m, k = t.shape
-        ld, unit = t.stride()
-        if m == 1:
-            ld = k
-    elif dims == 1:
-        m, k, unit = 1, t.shape[0], t.stride(0)
-        ld = k
-    else:
-        raise ValueError(f"{name} must have one or two dimensions")
-    if unit != 1 and k != 1:
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    if got != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if unit != 1 and shape[1] != 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
-    if shape is not None and (m, k) != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    return t.data_ptr(), code, ld, m, k
+    ld = t.stride(0) if t.dim() == 2 else shape[1]
+    return t.data_ptr(), code, ld if shape[0] > 1 else shape[1]
 
 
-def _vector(t, dtype, count, name, device):
-    """Pointer of a contiguous device vector of at least `count` elements, or
+def _shape2(t, name):
+    """Shape of t as (rows, columns); its device index."""
+    dev = t.get_device()
+    if dev < 0:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    shape = t.shape
+    if len(shape) == 1:
+        shape = (1, shape[0])
+    elif len(shape) != 2:
+        raise ValueError(f"{name} must have one or two dimensions")
+    return shape, dev
+
+
+def _vector(t, dtype, count, name, dev):
+    """Pointer of a contiguous device tensor of at least `count` elements, or
     None (NULL) for None."""
     if t is None:
         return None
+    if t.dtype is dtype and t.get_device() == dev and t.numel() >= count and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor of {dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.numel() < count:
-        raise ValueError(f"{name} holds {t.numel()} elements, needs at least {count}")
-    return t.data_ptr()
+    raise ValueError(f"{name} holds {t.numel()} elements, needs at least {count}")
 
 
-def _lists(t, dtype, b, name, device):
+def _lists(t, dtype, b, name, dev):
     """(pointer, columns, row stride) of a [b][columns] device tensor with
     contiguous rows, or (None, 0, 0) for None."""
     if t is None:
         return None, 0, 0
     if t.dtype != dtype or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor of {dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
     if t.dim() != 2 or (b is not None and t.shape[0] != b):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {b} rows")
-    cols = t.shape[1]
+    rows, cols = t.shape
     ld, unit = t.stride()
     if unit != 1 and cols > 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
-    return t.data_ptr(), cols, max(ld, cols) if t.shape[0] == 1 else ld
+    return t.data_ptr(), cols, ld if rows > 1 else max(ld, cols)
 
 
-def _call(where, device, stream, *args, keep=()):
-    """Call library function `where` on `stream` (default: the device's
-    current one) with `device` current.  `keep`: tensors allocated here that
-    the kernels use; the allocator is told when the stream is not the one
+def _call(where, dev, stream, args, keep=()):
+    """Call library function `where` on `stream` (default: the current one of
+    device `dev`) with that device current.  `keep`: tensors allocated here
+    that the kernels use; the allocator is told when the stream is not the one
     they belong to."""
-    import torch
-
-    index = device.index
+    fn = getattr(_lib or load(), where)
     if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(index)
+        raw = _torch._C._cuda_getCurrentRawStream(dev)
     else:
         raw = stream.cuda_stream
         for t in keep:
             t.record_stream(stream)
-    fn = getattr(load(), where)
-    if index == torch._C._cuda_getDevice():
+    if dev == _torch._C._cuda_getDevice():
         status = fn(*args, raw)
     else:
-        with torch.cuda.device(index):
+        with _torch.cuda.device(dev):
             status = fn(*args, raw)
     if status != 0:
         raise LowbitError(status, where)
@@ -664,41 +675,41 @@ def lowbit_norm_residual(y, r, post="none", post_w=None, post_b=None, gate=None,
     "none", "rms" or "layer" with FP32 weights and biases [k] (None: 1 and
     0); pre=None makes no x.  gate: [k] for every row or [m][k].  x_out is
     allocated with x_dtype (FP16, as lowbit_gemv reads it, if not given)."""
-    import torch
-
-    rp, rt, ldr, m, k = _float_rows(r, "r")
-    dev, shape = r.device, (m, k)
+    torch = _torch or _first_use()
+    shape, dev = _shape2(r, "r")
+    m, k = shape
+    rp, rt, ldr = _float_rows(r, shape, dev, "r")
     f32 = torch.float32
-    yp = yt = ldy = gp = gt = ldg = rop = ldro = 0
-    post_c = pre_c = 0
+    yp = yt = ldy = gp = gt = ldg = rop = ldro = xp = xt = ldx = post_c = pre_c = 0
+    made = ()
     if y is not None:
         post_c = NORMS[post]
-        yp, yt, ldy, _, _ = _float_rows(y, "y", shape, dev)
+        yp, yt, ldy = _float_rows(y, shape, dev, "y")
         if gate is not None:
             if gate.dim() == 1:
-                gp, gt, _, _, _ = _float_rows(gate, "gate", (1, k), dev)
+                gp, gt, _ = _float_rows(gate, (1, k), dev, "gate")
             else:
-                gp, gt, ldg, _, _ = _float_rows(gate, "gate", shape, dev)
+                gp, gt, ldg = _float_rows(gate, shape, dev, "gate")
         if r_out is None:
             r_out, rop, ldro = r, rp, ldr
         else:
-            rop, rot, ldro, _, _ = _float_rows(r_out, "r_out", shape, dev)
+            rop, rot, ldro = _float_rows(r_out, shape, dev, "r_out")
             if rot != rt:
                 raise TypeError("r_out must have the type of r")
     elif r_out is not None:
         raise ValueError("r_out needs y")
-    xp = xt = ldx = 0
     if pre is not None:
         pre_c = NORMS[pre]
         if x_out is None:
-            x_out = torch.empty(r.shape, dtype=x_dtype or torch.float16, device=dev)
-        xp, xt, ldx, _, _ = _float_rows(x_out, "x_out", shape, dev)
+            x_out = torch.empty(r.shape, dtype=x_dtype or torch.float16, device=r.device)
+            made = (x_out,)
+        xp, xt, ldx = _float_rows(x_out, shape, dev, "x_out")
     elif x_out is not None:
         raise ValueError("x_out needs pre")
-    _call("lowbit_norm_residual", dev, stream, yp, yt, ldy, rp, rt, ldr, rop, ldro, xp, xt, ldx, m, k,
-          post_c, _vector(post_w, f32, k, "post_w", dev), _vector(post_b, f32, k, "post_b", dev),
-          gp, gt, ldg, scale, pre_c, _vector(pre_w, f32, k, "pre_w", dev),
-          _vector(pre_b, f32, k, "pre_b", dev), eps, keep=() if x_out is None else (x_out,))
+    _call("lowbit_norm_residual", dev, stream,
+          (yp, yt, ldy, rp, rt, ldr, rop, ldro, xp, xt, ldx, m, k, post_c,
+           _vector(post_w, f32, k, "post_w", dev), _vector(post_b, f32, k, "post_b", dev), gp, gt, ldg, scale,
+           pre_c, _vector(pre_w, f32, k, "pre_w", dev), _vector(pre_b, f32, k, "pre_b", dev), eps), made)
     return (r_out if y is not None else r), x_out
 
 
@@ -719,47 +730,53 @@ def lowbit_logits_process(y, tokens=None, prompt_len=None, total_len=None, repet
     repetition / frequency / presence FP32 [b]; bias_ids int32 and bias_vals
     FP32 [b][.] with bias_len int32 [b]; mask int32 [rows][>= n / 32] with
     mask_row int32 [b]."""
-    import torch
-
-    yp, yt, ldy, b, n = _float_rows(y, "y")
-    dev, f32, i32 = y.device, torch.float32, torch.int32
+    torch = _torch or _first_use()
+    f32, i32 = torch.float32, torch.int32
+    shape, dev = _shape2(y, "y")
+    b, n = shape
+    yp, yt, ldy = _float_rows(y, shape, dev, "y")
     tp, tcap, ldt = _lists(tokens, i32, b, "tokens", dev)
-    bp, bcap, ldb = _lists(bias_ids, i32, b, "bias_ids", dev)
-    bv, bvcap, ldbv = _lists(bias_vals, f32, b, "bias_vals", dev)
-    if bcap != bvcap or (b > 1 and ldb != ldbv):
-        raise ValueError("bias_ids and bias_vals must have one shape and row stride")
-    mp, words, ldm = _lists(mask, i32, None if mask_row is not None else b, "mask", dev)
-    if mask is not None and words < (n + 31) // 32:
-        raise ValueError(f"mask has {words} words a row, needs {(n + 31) // 32}")
+    bp = bv = None
+    bcap = ldb = 0
+    if bias_ids is not None or bias_vals is not None:
+        bp, bcap, ldb = _lists(bias_ids, i32, b, "bias_ids", dev)
+        bv, bvcap, ldbv = _lists(bias_vals, f32, b, "bias_vals", dev)
+        if bp is None or bv is None or bcap != bvcap or ldb != ldbv:
+            raise ValueError("bias_ids and bias_vals must have one shape and row stride")
+    mp, rows, ldm = None, 0, 0
+    if mask is not None:
+        mp, words, ldm = _lists(mask, i32, None if mask_row is not None else b, "mask", dev)
+        rows = mask.shape[0]
+        if words < (n + 31) // 32:
+            raise ValueError(f"mask has {words} words a row, needs {(n + 31) // 32}")
     op = ldo = 0
     if out is not None:
-        op, ot, ldo, _, _ = _float_rows(out, "out", (b, n), dev)
-        if out.dtype != f32:
+        op, ot, ldo = _float_rows(out, shape, dev, "out")
+        if ot != 1:
             raise TypeError("out must be float32")
+    ip = vp = wp = None
     need = 0
     made = ()
     if top1:
         if idx is None:
-            idx = torch.empty(b, dtype=i32, device=dev)
+            idx = torch.empty(b, dtype=i32, device=y.device)
             made += (idx,)
         if val is None:
-            val = torch.empty(b, dtype=f32, device=dev)
+            val = torch.empty(b, dtype=f32, device=y.device)
             made += (val,)
         if workspace is None:
-            need = lowbit_logits_workspace_bytes(n, b)
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+            workspace = torch.empty(max(lowbit_logits_workspace_bytes(n, b), 16), dtype=torch.uint8, device=y.device)
             made += (workspace,)
-        need = workspace.numel()
+        ip, vp = _vector(idx, i32, b, "idx", dev), _vector(val, f32, b, "val", dev)
+        wp, need = _vector(workspace, torch.uint8, 0, "workspace", dev), workspace.numel()
     elif idx is not None or val is not None:
         raise ValueError("idx and val need top1")
-    _call("lowbit_logits_process", dev, stream, yp, yt, ldy, n, b, tp, tcap, ldt,
-          _vector(prompt_len, i32, b, "prompt_len", dev), _vector(total_len, i32, b, "total_len", dev),
-          _vector(repetition, f32, b, "repetition", dev), _vector(frequency, f32, b, "frequency", dev),
-          _vector(presence, f32, b, "presence", dev), bp, bv, bcap, ldb,
-          _vector(bias_len, i32, b, "bias_len", dev), mp, 0 if mask is None else mask.shape[0], ldm,
-          _vector(mask_row, i32, b, "mask_row", dev), op, ldo, _vector(idx, i32, b, "idx", dev),
-          _vector(val, f32, b, "val", dev),
-          _vector(workspace, torch.uint8, 0, "workspace", dev) if top1 else None, need, keep=made)
+    _call("lowbit_logits_process", dev, stream,
+          (yp, yt, ldy, n, b, tp, tcap, ldt, _vector(prompt_len, i32, b, "prompt_len", dev),
+           _vector(total_len, i32, b, "total_len", dev), _vector(repetition, f32, b, "repetition", dev),
+           _vector(frequency, f32, b, "frequency", dev), _vector(presence, f32, b, "presence", dev), bp, bv, bcap,
+           ldb, _vector(bias_len, i32, b, "bias_len", dev), mp, rows, ldm,
+           _vector(mask_row, i32, b, "mask_row", dev), op, ldo, ip, vp, wp, need), made)
     return out, idx, val
 
 
@@ -774,30 +791,26 @@ def lowbit_lora_accumulate(x, ids, a, b, y, ranks=None, scales=None, workspace=N
     [slots][r][k] and b [slots][n][r] in x's type, ranks int32 [slots], scales
     FP32 [slots], y [m][n] FP32 (or BF16 with BF16 x); rows of x and y may be
     strided (a slice of a fused projection's output)."""
-    import torch
-
-    xp, xt, ldx, m, k = _float_rows(x, "x")
-    dev = x.device
-    yp, yt, ldy, ym, n = _float_rows(y, "y", None, dev)
-    if ym != m:
-        raise ValueError(f"y has {ym} rows, x has {m}")
+    torch = _torch or _first_use()
+    shape, dev = _shape2(x, "x")
+    m, k = shape
+    xp, xt, ldx = _float_rows(x, shape, dev, "x")
     if a.dim() != 3 or b.dim() != 3:
         raise ValueError("a must be [slots][r][k] and b [slots][n][r]")
-    slots, r, _ = a.shape
-    if a.shape[2] != k or tuple(b.shape) != (slots, n, r):
-        raise ValueError(f"a {tuple(a.shape)} and b {tuple(b.shape)} do not fit x {tuple(x.shape)} "
-                         f"and y {tuple(y.shape)}")
-    need = workspace.numel() if workspace is not None else 0
+    slots, n, r = b.shape
+    if a.shape != (slots, r, k):
+        raise ValueError(f"a {tuple(a.shape)} does not fit x {tuple(x.shape)} and b {tuple(b.shape)}")
+    yp, yt, ldy = _float_rows(y, (m, n), dev, "y")
     made = ()
     if workspace is None:
         need = lowbit_lora_workspace_bytes(m, n, k, r, slots)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
         made = (workspace,)
-    _call("lowbit_lora_accumulate", dev, stream, xp, xt, ldx, _vector(ids, torch.int32, m, "ids", dev), m,
-          n, k, r, slots, _vector(a, x.dtype, 0, "a", dev), _vector(b, x.dtype, 0, "b", dev),
-          _vector(ranks, torch.int32, slots, "ranks", dev),
-          _vector(scales, torch.float32, slots, "scales", dev), yp, yt, ldy,
-          _vector(workspace, torch.uint8, 0, "workspace", dev), need, keep=made)
+    _call("lowbit_lora_accumulate", dev, stream,
+          (xp, xt, ldx, _vector(ids, torch.int32, m, "ids", dev), m, n, k, r, slots,
+           _vector(a, x.dtype, 0, "a", dev), _vector(b, x.dtype, 0, "b", dev),
+           _vector(ranks, torch.int32, slots, "ranks", dev), _vector(scales, torch.float32, slots, "scales", dev),
+           yp, yt, ldy, _vector(workspace, torch.uint8, 0, "workspace", dev), workspace.numel()), made)
     return y
 
 
