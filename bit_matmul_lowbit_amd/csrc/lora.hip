@@ -17,6 +17,7 @@
 //   B operand (32 x 16): lane l holds column l % 16, 8 values at 8 (l / 16)
 //   D (16 x 16): lane l, register e holds row 4 (l / 16) + e, column l % 16
 //
+// A small call does both in one launch (lora_small_kernel), others in two:
 // shrink: v^T = A x^T, one work-group per (16 rows of an item, up to 64 of
 // its ranks, slice of k); its eight waves split the slice and are summed
 // through LDS.  The slices' FP32 sums go to the workspace.  Operands taken
@@ -222,28 +223,22 @@ __global__ __launch_bounds__(1024) void lora_plan_kernel(LoraArgs a, Plan plan, 
   }
 }
 
-// v[slice][row][j] for 16 rows of an item and RT * 16 ranks: blockIdx.x =
-// item * subs + (16-row part of the item), y = part of the ranks, z = slice.
-// Rows past the item's and ranks past the adapter's repeat the last one (each
-// is a row or column of the MFMA of its own) and are not stored.
-template <int XT, int RT, bool INLINE>
-__global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs a, Plan plan, int tm, int subs,
-                                                          float* __restrict__ v) {
-  constexpr int T = 1 + RT;                 // 16-row tiles of a step: x, then A's
-  constexpr int U = RT == 4 ? 2 : RT == 2 ? 3 : 4;  // steps in flight
-  __shared__ int rows[kItemRows];
-  // per wave, a step of each tile: 16 rows of 8 pieces of 16 bytes, piece p of
-  // row i at p ^ (i & 7) (the lanes of a read then fall into different banks);
-  // afterwards the waves' sums
-  __shared__ uint4 stage[kShrinkWaves][T][16][8];
-  const int item = blockIdx.x / subs, sub = blockIdx.x % subs;
-  int slot = 0;
-  const int count = find_item<INLINE>(a, plan, item, tm, rows, &slot);
-  const int here = count - sub * 16 < 16 ? count - sub * 16 : 16;
-  if (here <= 0) return;
-  const int rank = rank_of(a, slot), r0 = (int)blockIdx.y * RT * 16;
-  if (r0 >= rank) return;
-
+// The first product for 16 rows and RT * 16 ranks from r0 on, over part `part`
+// of `parts` of k for this wave: the work-group's waves are summed, and thread
+// 64 t + lane (t < RT) returns v[row lane % 16][r0 + 16 t + 4 (lane / 16) ..+3]
+// of the parts of all its waves.  Rows past the `here` given ones and ranks
+// past the adapter's repeat the last one (each is a row or column of the MFMA
+// of its own) and are not to be used.
+//
+// `stage`, per wave: a step of each tile, 16 rows of 8 pieces of 16 bytes,
+// piece p of row i at p ^ (i & 7) (the lanes of a read then fall into
+// different banks); afterwards the waves' sums.  The call ends with reads of
+// it.
+template <int XT, int RT>
+__device__ __forceinline__ f32x4 shrink16(const LoraArgs& a, int slot, int rank, int r0, const int* rows,
+                                          int here, uint4 (*stage)[1 + RT][16][8], int part, int parts) {
+  constexpr int T = 1 + RT;                          // 16-row tiles of a step: x, then A's
+  constexpr int U = RT == 4 ? 2 : RT == 2 ? 3 : 4;   // steps in flight
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, q = lane >> 4;    // as an operand's lane
   const int lr = lane >> 3, lp = lane & 7;   // as a loading lane: rows lr and lr + 8, piece lp
@@ -251,7 +246,7 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs a, Plan plan,
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int at = lr + 8 * h;
-    xp[h] = static_cast<const uint16_t*>(a.x) + (int64_t)rows[sub * 16 + (at < here ? at : here - 1)] * a.ldx;
+    xp[h] = static_cast<const uint16_t*>(a.x) + (int64_t)rows[at < here ? at : here - 1] * a.ldx;
   }
   const uint16_t* ap = static_cast<const uint16_t*>(a.a) + (int64_t)slot * a.r * a.k;
   uint32_t aoff[RT][2];
@@ -263,9 +258,8 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs a, Plan plan,
       aoff[t][h] = (uint32_t)(j < rank ? j : rank - 1) * (uint32_t)a.k;
     }
   const int k = (int)a.k, steps = (k + 63) / 64;
-  const int parts = kShrinkWaves * (int)gridDim.z;
   const int per = (steps + parts - 1) / parts;
-  const int s0 = ((int)blockIdx.z * kShrinkWaves + wave) * per;
+  const int s0 = part * per;
   const int s1 = s0 + per < steps ? s0 + per : steps;
 
   f32x4 acc[RT];
@@ -318,16 +312,35 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs a, Plan plan,
 #pragma unroll
   for (int t = 0; t < RT; ++t) red[wave][t][lane] = acc[t];
   __syncthreads();
-  if (threadIdx.x < RT * 64) {
-    const int t = wave;
-    f32x4 sum = red[0][t][lane];
-#pragma unroll
-    for (int w = 1; w < kShrinkWaves; ++w) sum += red[w][t][lane];
-    const int j = r0 + t * 16 + q * 4;
-    // j .. j + 3 lie in the row (r is a multiple of 8); what is past the rank is not read
-    if (c < here && j < rank)
-      *reinterpret_cast<f32x4*>(v + ((int64_t)blockIdx.z * a.m + rows[sub * 16 + c]) * a.r + j) = sum;
+  f32x4 sum = (f32x4){0.f, 0.f, 0.f, 0.f};
+  if (wave < RT) {
+    sum = red[0][wave][lane];
+    for (int w = 1; w < (int)blockDim.x >> 6; ++w) sum += red[w][wave][lane];
   }
+  return sum;
+}
+
+// v[slice][row][j] for 16 rows of an item and RT * 16 ranks: blockIdx.x =
+// item * subs + (16-row part of the item), y = part of the ranks, z = slice.
+template <int XT, int RT, bool INLINE>
+__global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs a, Plan plan, int tm, int subs,
+                                                          float* __restrict__ v) {
+  __shared__ int rows[kItemRows];
+  __shared__ uint4 stage[kShrinkWaves][1 + RT][16][8];
+  const int item = blockIdx.x / subs, sub = blockIdx.x % subs;
+  int slot = 0;
+  const int count = find_item<INLINE>(a, plan, item, tm, rows, &slot);
+  const int here = count - sub * 16 < 16 ? count - sub * 16 : 16;
+  if (here <= 0) return;
+  const int rank = rank_of(a, slot), r0 = (int)blockIdx.y * RT * 16;
+  if (r0 >= rank) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const f32x4 sum = shrink16<XT, RT>(a, slot, rank, r0, rows + sub * 16, here, stage,
+                                     (int)blockIdx.z * kShrinkWaves + wave, kShrinkWaves * (int)gridDim.z);
+  const int c = threadIdx.x & 15, j = r0 + wave * 16 + ((threadIdx.x >> 4) & 3) * 4;
+  // j .. j + 3 lie in the row (r is a multiple of 8); what is past the rank is not read
+  if (wave < RT && c < here && j < rank)
+    *reinterpret_cast<f32x4*>(v + ((int64_t)blockIdx.z * a.m + rows[sub * 16 + c]) * a.r + j) = sum;
 }
 
 // FP32 value -> its pieces; `scale` is a power of two (1 for BF16)
@@ -410,204 +423,248 @@ __device__ __forceinline__ void store_tail(const Out4<3>& z, bf16_t* p, int n) {
     if (u < n) h[u] = (uint16_t)(z.d[u >> 1] >> ((u & 1) * 16));
 }
 
-// One item (SUBS * 16 rows at most), every gridDim.x-th 256 outputs.  Column c
-// of a wave's tile t is output 4 c + t, so that a lane's four tiles are four
-// consecutive outputs and 16 lanes read and write 256 contiguous bytes of an
-// FP32 row (128 of BF16).  The first outputs and the first 32 ranks of B are
-// on their way while v is made ready; further ones are requested before the
-// outputs of the step are stored.
-template <int XT, int YT, bool INLINE, int SUBS>
-__global__ __launch_bounds__(256, SUBS == 1 || YT == 3 ? 3 : 2) void lora_expand_kernel(LoraArgs a, Plan plan, int tm, int slices,
-                                                          const float* __restrict__ v) {
+// The second product for an item of up to SUBS * 16 rows: share `share` of
+// `shares` of the outputs, WAVES * 64 at a time.  Column c of a wave's tile t
+// is output 4 c + t, so that a lane's four tiles are four consecutive outputs
+// and 16 lanes read and write 256 contiguous bytes of an FP32 row (128 of
+// BF16).  The first outputs and the first ranks of B are on their way while v
+// is made ready: first() brings about what inner(row, j), four sums of v from
+// rank j on, needs.
+template <int XT, int YT, int SUBS, int WAVES, class First, class Inner>
+__device__ __forceinline__ void expand_item(const LoraArgs& a, int slot, int count, int rank, const int* rows,
+                                            float* unscale, typename Elem<XT>::type* pieces, int tm, int share,
+                                            int shares, First first, Inner inner) {
   constexpr int P = Mma<XT>::pieces;
   typedef typename Elem<XT>::type X;
   typedef typename Elem<YT>::type Y;
-  extern __shared__ uint4 dyn[];
-  __shared__ int rows[kItemRows];
-  __shared__ float unscale[kItemRows];
-  X* pieces = reinterpret_cast<X*>(dyn);  // [P][tm][pitch]
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 15, q = lane >> 4;
+  const float scale = a.scales ? a.scales[slot] : 1.0f;
+  const int chunks = (rank + 31) / 32, pitch = chunks * 32 + 8;  // 16 bytes past: other banks
+  const X* bs = static_cast<const X*>(a.b) + (int64_t)slot * a.n * a.r;
+  // where row 4 q + e of a part has its outputs n0 + 4 c ...; made anew at
+  // each use (kept, the pointers would cost a wave of occupancy)
+  auto yrow = [&](int s, int e, int64_t n0) __attribute__((always_inline)) {
+    const int at = s * 16 + q * 4 + e;
+    return static_cast<Y*>(a.y) + ((int64_t)rows[at < count ? at : 0] * a.ldy + n0 + c * 4);
+  };
 
+  uint4 w[2][kTilesN];
+  // B's rows from n0 on: a uniform base and 32-bit offsets
+  auto load_w = [&](uint4 (&d)[kTilesN], int64_t n0, int rc) __attribute__((always_inline)) {
+    int j = rc * 32 + q * 8;
+    j = j < (int)a.r ? j : (int)a.r - 8;  // past r: any, masked below
+    const int last = a.n - n0 < kWaveN ? (int)(a.n - n0) - 1 : kWaveN - 1;
+    const X* base = bs + n0 * a.r;
+#pragma unroll
+    for (int t = 0; t < kTilesN; ++t) {
+      const int o = c * kTilesN + t;
+      // an output past the last is not stored
+      d[t] = *reinterpret_cast<const uint4*>(base + (uint32_t)((o < last ? o : last) * (int)a.r + j));
+    }
+  };
+  Out4<YT> z[SUBS][4] = {};
+  auto load_y = [&](int64_t n0) __attribute__((always_inline)) {
+    const int64_t left = a.n - n0 - c * 4;
+#pragma unroll
+    for (int s = 0; s < SUBS; ++s)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (s * 16 + q * 4 + e < count) {
+          const Y* at = yrow(s, e, n0);
+          if (left >= 4) __builtin_memcpy(&z[s][e], at, sizeof(z[s][e]));
+          else load_tail(z[s][e], at, (int)left);
+        }
+  };
+  const int64_t step = (int64_t)shares * (WAVES * kWaveN);
+  int64_t n0 = ((int64_t)share * WAVES + wave) * kWaveN;
+  // B in a ring of two: its (outputs, 32 ranks) pieces in the order in which
+  // they are used, two of them ahead
+  int64_t pn = n0;
+  int prc = 0;
+  auto request = [&](uint4 (&d)[kTilesN]) __attribute__((always_inline)) {
+    if (pn >= a.n) return;
+    load_w(d, pn, prc);
+    if (++prc == chunks) {
+      prc = 0;
+      pn += step;
+    }
+  };
+  request(w[0]);
+  if (n0 < a.n) load_y(n0);
+  request(w[1]);
+
+  first();
+  // v of the item's rows, 16 lanes to a row, 64 ranks at a time
+  for (int sub = 0; sub * 16 < count; ++sub) {
+    if (WAVES > 4 && wave >= 4) break;  // 256 threads are 16 rows
+    const int at = sub * 16 + (tid >> 4), j0 = (tid & 15) * 4;
+    const bool live = at < count;
+    auto scaled = [&](int j) __attribute__((always_inline)) {
+      f32x4 sum = (f32x4){0.f, 0.f, 0.f, 0.f};
+      if (live && j < rank) {
+        sum = inner(at, j);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] = j + e < rank ? sum[e] * scale : 0.0f;
+      }
+      return sum;
+    };
+    const f32x4 head = scaled(j0);
+    float up = 1.0f;
+    if constexpr (XT == 2) {
+      float top = finite_max(head);
+#pragma unroll 1
+      for (int j = j0 + 64; j < rank; j += 64) top = fmaxf(top, finite_max(scaled(j)));
+      top = max16(top);
+      // the row's largest value to [2^13, 2^14): far from FP16's ends on both sides
+      int ex = top > 0.0f ? 13 - ilogbf(top) : 0;
+      ex = ex > 120 ? 120 : ex;
+      up = ldexpf(1.0f, ex);
+      if ((tid & 15) == 0 && live) unscale[at] = ldexpf(1.0f, -ex);
+    }
+#pragma unroll 1
+    for (int j = j0; j < chunks * 32; j += 64) {
+      const f32x4 val = j == j0 ? head : scaled(j);
+      X p[4][P];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) split(val[e], up, p[e]);
+#pragma unroll
+      for (int u = 0; u < P; ++u) {
+        X o[4] = {p[0][u], p[1][u], p[2][u], p[3][u]};
+        __builtin_memcpy(pieces + (u * tm + at) * pitch + j, o, 8);
+      }
+    }
+  }
+  __syncthreads();
+
+  f32x4 acc[SUBS][kTilesN];
+  int rc = 0;
+  // one piece of B; with the last ranks of an output, y is written
+  auto advance = [&](uint4 (&d)[kTilesN]) __attribute__((always_inline)) {
+    if (rc == 0) {
+#pragma unroll
+      for (int s = 0; s < SUBS; ++s)
+#pragma unroll
+        for (int t = 0; t < kTilesN; ++t) acc[s][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    }
+    const int j = rc * 32 + q * 8;
+    if (rc * 32 + 32 > rank) {  // entries past the rank may hold anything
+      uint32_t keep[4];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const int left = rank - j - 2 * h;
+        keep[h] = left >= 2 ? 0xFFFFFFFFu : (left == 1 ? 0xFFFFu : 0u);
+      }
+#pragma unroll
+      for (int t = 0; t < kTilesN; ++t) {
+        d[t].x &= keep[0];
+        d[t].y &= keep[1];
+        d[t].z &= keep[2];
+        d[t].w &= keep[3];
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < SUBS; ++s) {
+      if (s * 16 < count) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          const uint4 b = *reinterpret_cast<const uint4*>(pieces + (p * tm + s * 16 + c) * pitch + j);
+#pragma unroll
+          for (int t = 0; t < kTilesN; ++t) acc[s][t] = Mma<XT>::run(b, d[t], acc[s][t]);
+        }
+      }
+    }
+    request(d);
+    if (++rc < chunks) return;
+    rc = 0;
+#pragma unroll
+    for (int s = 0; s < SUBS; ++s)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float un = XT == 2 ? unscale[s * 16 + q * 4 + e] : 1.0f;
+        z[s][e] = add4(z[s][e], acc[s][0][e] * un, acc[s][1][e] * un, acc[s][2][e] * un, acc[s][3][e] * un);
+      }
+    const int64_t left = a.n - n0 - c * 4;
+#pragma unroll
+    for (int s = 0; s < SUBS; ++s)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (s * 16 + q * 4 + e < count) {
+          Y* at = yrow(s, e, n0);
+          if (left >= 4) __builtin_memcpy(at, &z[s][e], sizeof(z[s][e]));
+          else store_tail(z[s][e], at, (int)left);
+        }
+    n0 += step;
+    if (n0 < a.n) load_y(n0);
+  };
+  while (n0 < a.n) {
+    advance(w[0]);
+    if (n0 < a.n) advance(w[1]);
+  }
+}
+
+// One item, every gridDim.x-th 256 outputs.
+template <int XT, int YT, bool INLINE, int SUBS>
+__global__ __launch_bounds__(256, SUBS == 1 || YT == 3 ? 3 : 2) void lora_expand_kernel(
+    LoraArgs a, Plan plan, int tm, int slices, const float* __restrict__ v) {
+  extern __shared__ uint4 dyn[];  // pieces of v: [pieces][tm][pitch]
+  __shared__ int rows[kItemRows];
+  __shared__ float unscale[kItemRows];
   for (int item = blockIdx.y;; item += gridDim.y) {
     int slot = 0;
     const int count = find_item<INLINE>(a, plan, item, tm, rows, &slot);
     if (!count) return;
-    const int rank = rank_of(a, slot);
-    const float scale = a.scales ? a.scales[slot] : 1.0f;
-    const int chunks = (rank + 31) / 32, pitch = chunks * 32 + 8;  // 16 bytes past: other banks
-    const X* bs = static_cast<const X*>(a.b) + (int64_t)slot * a.n * a.r;
-    // where row 4 q + e of a part has its outputs n0 + 4 c ...; made anew at
-    // each use (kept, the pointers would cost a wave of occupancy)
-    auto yrow = [&](int s, int e, int64_t n0) __attribute__((always_inline)) {
-      const int at = s * 16 + q * 4 + e;
-      return static_cast<Y*>(a.y) + ((int64_t)rows[at < count ? at : 0] * a.ldy + n0 + c * 4);
-    };
-
-    uint4 w[2][kTilesN];
-    // B's rows from n0 on: a uniform base and 32-bit offsets
-    auto load_w = [&](uint4 (&d)[kTilesN], int64_t n0, int rc) __attribute__((always_inline)) {
-      int j = rc * 32 + q * 8;
-      j = j < (int)a.r ? j : (int)a.r - 8;  // past r: any, masked below
-      const int last = a.n - n0 < kWaveN ? (int)(a.n - n0) - 1 : kWaveN - 1;
-      const X* base = bs + n0 * a.r;
-#pragma unroll
-      for (int t = 0; t < kTilesN; ++t) {
-        const int o = c * kTilesN + t;
-        // an output past the last is not stored
-        d[t] = *reinterpret_cast<const uint4*>(base + (uint32_t)((o < last ? o : last) * (int)a.r + j));
-      }
-    };
-    Out4<YT> z[SUBS][4] = {};
-    auto load_y = [&](int64_t n0) __attribute__((always_inline)) {
-      const int64_t left = a.n - n0 - c * 4;
-#pragma unroll
-      for (int s = 0; s < SUBS; ++s)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (s * 16 + q * 4 + e < count) {
-            const Y* at = yrow(s, e, n0);
-            if (left >= 4) __builtin_memcpy(&z[s][e], at, sizeof(z[s][e]));
-            else load_tail(z[s][e], at, (int)left);
-          }
-    };
-    const int64_t step = (int64_t)gridDim.x * kBlockN;
-    int64_t n0 = ((int64_t)blockIdx.x * 4 + wave) * kWaveN;
-    // B in a ring of two: its (outputs, 32 ranks) pieces in the order in which
-    // they are used, two of them ahead
-    int64_t pn = n0;
-    int prc = 0;
-    auto request = [&](uint4 (&d)[kTilesN]) __attribute__((always_inline)) {
-      if (pn >= a.n) return;
-      load_w(d, pn, prc);
-      if (++prc == chunks) {
-        prc = 0;
-        pn += step;
-      }
-    };
-    request(w[0]);
-    if (n0 < a.n) load_y(n0);
-    request(w[1]);
-
-    // v of the item's rows, 16 lanes to a row, 64 ranks at a time
-    for (int sub = 0; sub * 16 < count; ++sub) {
-      const int at = sub * 16 + (tid >> 4), j0 = (tid & 15) * 4;
-      const bool live = at < count;
-      const float* vr = v + (int64_t)rows[live ? at : 0] * a.r;
-      auto inner = [&](int j) __attribute__((always_inline)) {
-        f32x4 sum = (f32x4){0.f, 0.f, 0.f, 0.f};
-        if (live && j < rank) {
-          // four slices at a time (all loads out before the first add)
+    auto inner = [&](int at, int j) __attribute__((always_inline)) {
+      const float* vr = v + (int64_t)rows[at] * a.r + j;
+      f32x4 sum = (f32x4){0.f, 0.f, 0.f, 0.f};
+      // four slices at a time (all loads out before the first add)
 #pragma unroll 1
-          for (int u0 = 0; u0 < slices; u0 += 4) {
-            f32x4 part[4];
+      for (int u0 = 0; u0 < slices; u0 += 4) {
+        f32x4 part[4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-              part[u] = *reinterpret_cast<const f32x4*>(
-                  vr + (int64_t)(u0 + u < slices ? u0 + u : u0) * a.m * a.r + j);
+        for (int u = 0; u < 4; ++u)
+          part[u] = *reinterpret_cast<const f32x4*>(vr + (int64_t)(u0 + u < slices ? u0 + u : u0) * a.m * a.r);
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-              if (u0 + u < slices) sum += part[u];
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sum[e] = j + e < rank ? sum[e] * scale : 0.0f;
-        }
-        return sum;
-      };
-      const f32x4 first = inner(j0);
-      float up = 1.0f;
-      if constexpr (XT == 2) {
-        float top = finite_max(first);
-#pragma unroll 1
-        for (int j = j0 + 64; j < rank; j += 64) top = fmaxf(top, finite_max(inner(j)));
-        top = max16(top);
-        // the row's largest value to [2^13, 2^14): far from FP16's ends on both sides
-        int ex = top > 0.0f ? 13 - ilogbf(top) : 0;
-        ex = ex > 120 ? 120 : ex;
-        up = ldexpf(1.0f, ex);
-        if ((tid & 15) == 0 && live) unscale[at] = ldexpf(1.0f, -ex);
+        for (int u = 0; u < 4; ++u)
+          if (u0 + u < slices) sum += part[u];
       }
-#pragma unroll 1
-      for (int j = j0; j < chunks * 32; j += 64) {
-        const f32x4 val = j == j0 ? first : inner(j);
-        X p[4][P];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) split(val[e], up, p[e]);
-#pragma unroll
-        for (int u = 0; u < P; ++u) {
-          X o[4] = {p[0][u], p[1][u], p[2][u], p[3][u]};
-          __builtin_memcpy(pieces + (u * tm + at) * pitch + j, o, 8);
-        }
-      }
-    }
-    __syncthreads();
-
-    f32x4 acc[SUBS][kTilesN];
-    int rc = 0;
-    // one piece of B; with the last ranks of an output, y is written
-    auto advance = [&](uint4 (&d)[kTilesN]) __attribute__((always_inline)) {
-      if (rc == 0) {
-#pragma unroll
-        for (int s = 0; s < SUBS; ++s)
-#pragma unroll
-          for (int t = 0; t < kTilesN; ++t) acc[s][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
-      }
-      const int j = rc * 32 + q * 8;
-      if (rc * 32 + 32 > rank) {  // entries past the rank may hold anything
-        uint32_t keep[4];
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const int left = rank - j - 2 * h;
-          keep[h] = left >= 2 ? 0xFFFFFFFFu : (left == 1 ? 0xFFFFu : 0u);
-        }
-#pragma unroll
-        for (int t = 0; t < kTilesN; ++t) {
-          d[t].x &= keep[0];
-          d[t].y &= keep[1];
-          d[t].z &= keep[2];
-          d[t].w &= keep[3];
-        }
-      }
-#pragma unroll
-      for (int s = 0; s < SUBS; ++s) {
-        if (s * 16 < count) {
-#pragma unroll
-          for (int p = 0; p < P; ++p) {
-            const uint4 b = *reinterpret_cast<const uint4*>(pieces + (p * tm + s * 16 + c) * pitch + j);
-#pragma unroll
-            for (int t = 0; t < kTilesN; ++t) acc[s][t] = Mma<XT>::run(b, d[t], acc[s][t]);
-          }
-        }
-      }
-      request(d);
-      if (++rc < chunks) return;
-      rc = 0;
-#pragma unroll
-      for (int s = 0; s < SUBS; ++s)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float un = XT == 2 ? unscale[s * 16 + q * 4 + e] : 1.0f;
-          z[s][e] = add4(z[s][e], acc[s][0][e] * un, acc[s][1][e] * un, acc[s][2][e] * un, acc[s][3][e] * un);
-        }
-      const int64_t left = a.n - n0 - c * 4;
-#pragma unroll
-      for (int s = 0; s < SUBS; ++s)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (s * 16 + q * 4 + e < count) {
-            Y* at = yrow(s, e, n0);
-            if (left >= 4) __builtin_memcpy(at, &z[s][e], sizeof(z[s][e]));
-            else store_tail(z[s][e], at, (int)left);
-          }
-      n0 += step;
-      if (n0 < a.n) load_y(n0);
+      return sum;
     };
-    while (n0 < a.n) {
-      advance(w[0]);
-      if (n0 < a.n) advance(w[1]);
-    }
+    expand_item<XT, YT, SUBS, 4>(a, slot, count, rank_of(a, slot), rows, unscale,
+                                 reinterpret_cast<typename Elem<XT>::type*>(dyn), tm, (int)blockIdx.x,
+                                 (int)gridDim.x, [] {}, inner);
     __syncthreads();  // the next item's rows and pieces
   }
+}
+
+// Both products in one launch, for few rows with small adapters: every
+// work-group forms its item's v by itself (reading all of A, which the cache
+// then holds) and goes on to its 512 outputs.
+template <int XT, int YT, int RT>
+__global__ __launch_bounds__(512) void lora_small_kernel(LoraArgs a) {
+  constexpr int kWaves = 8, kPitch = RT * 16 + 4;
+  __shared__ int rows[16];
+  __shared__ float unscale[16];
+  __shared__ uint4 stage[kWaves][1 + RT][16][8];
+  __shared__ __align__(16) float inner_v[16][kPitch];
+  __shared__ uint4 pieces[Mma<XT>::pieces * 16 * ((RT * 16 + 31) / 32 * 32 + 8) / 8];
+  int slot = 0;
+  const int count = find_item<true>(a, Plan{}, (int)blockIdx.y, 16, rows, &slot);
+  if (!count) return;
+  const int rank = rank_of(a, slot);
+  auto first = [&]() __attribute__((always_inline)) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const f32x4 sum = shrink16<XT, RT>(a, slot, rank, 0, rows, count, stage, wave, kWaves);
+    if (wave < RT)
+      *reinterpret_cast<f32x4*>(&inner_v[threadIdx.x & 15][wave * 16 + ((threadIdx.x >> 4) & 3) * 4]) = sum;
+    __syncthreads();
+  };
+  auto inner = [&](int at, int j) __attribute__((always_inline)) {
+    return *reinterpret_cast<const f32x4*>(&inner_v[at][j]);
+  };
+  expand_item<XT, YT, 1, kWaves>(a, slot, count, rank, rows, unscale,
+                                 reinterpret_cast<typename Elem<XT>::type*>(pieces), 16, (int)blockIdx.x,
+                                 (int)gridDim.x, first, inner);
 }
 
 int64_t round256(int64_t v) { return (v + 255) / 256 * 256; }
@@ -643,6 +700,26 @@ int64_t slices_of(int64_t m, int64_t k, int64_t r, int64_t slots) {
   return s < 1 ? 1 : (s > kMaxSlices ? kMaxSlices : s);
 }
 
+// One launch instead of two pays while reading all of A costs a work-group
+// less than the launch and the way of v through memory, and while the
+// work-groups all run at once (one to a compute unit).  Measured as a graph,
+// one launch against two: 1 x 2048 -> 6144, r 16 (64 KB) 7.0 : 7.9 us; 16 rows,
+// r 32 (128 KB) 9.4 : 13.5; 1 x 5120 -> 5120, r 16 (160 KB) 9.1 : 8.6; 4 x 2048
+// -> 34816, r 32 (272 work-groups) 14.8 : 9.9.
+bool small_ok(const LoraArgs& a) {
+  return a.m <= 16 && a.r <= 64 && a.r * a.k * 2 <= (128 << 10) &&
+         max_items(a.m, a.slots, 16) * ((a.n + 511) / 512) <= 256;
+}
+
+template <int XT, int YT>
+hipError_t launch_small(const LoraArgs& a, hipStream_t st) {
+  const dim3 grid((unsigned)((a.n + 511) / 512), (unsigned)max_items(a.m, a.slots, 16));
+  if (a.r <= 16) hipLaunchKernelGGL((lora_small_kernel<XT, YT, 1>), grid, dim3(512), 0, st, a);
+  else if (a.r <= 32) hipLaunchKernelGGL((lora_small_kernel<XT, YT, 2>), grid, dim3(512), 0, st, a);
+  else hipLaunchKernelGGL((lora_small_kernel<XT, YT, 4>), grid, dim3(512), 0, st, a);
+  return hipGetLastError();
+}
+
 template <int XT, int YT, bool INLINE>
 hipError_t launch(const LoraArgs& a, const Plan& plan, float* v, hipStream_t st) {
   const int tm = item_rows(a.m), rt = ranks_per_block(a.m, a.r);
@@ -660,9 +737,9 @@ hipError_t launch(const LoraArgs& a, const Plan& plan, float* v, hipStream_t st)
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   // Work-groups: as many as run at once (three to a compute unit) where two
-  // shares of the outputs each are enough for that, else four times as many.  One that
-  // takes several shares finds its rows and makes v ready (a chain of four
-  // memory latencies) once for all of them.
+  // shares of the outputs each are enough for that, else four times as many.
+  // One that takes several shares finds its rows and makes v ready (a chain of
+  // four memory latencies) once for all of them.
   const int64_t tiles = (a.n + kBlockN - 1) / kBlockN, all = tiles * items;
   int64_t each = all <= 1536 ? (all + 767) / 768 : (all + 3071) / 3072;
   each = each < tiles ? each : tiles;
@@ -687,6 +764,10 @@ hipError_t launch_lora_accumulate(const LoraArgs& a, void* ws, hipStream_t st) {
   char* base = static_cast<char*>(ws);
   float* v = reinterpret_cast<float*>(base + plan_bytes(a.m, a.slots, tm));
   Plan plan = {};
+  if (small_ok(a)) {
+    if (a.x_type == 2) return launch_small<2, 1>(a, st);
+    return a.y_type == 1 ? launch_small<3, 1>(a, st) : launch_small<3, 3>(a, st);
+  }
   if (a.m <= kInlineRows) {
     if (a.x_type == 2) return launch<2, 1, true>(a, plan, v, st);
     return a.y_type == 1 ? launch<3, 1, true>(a, plan, v, st) : launch<3, 3, true>(a, plan, v, st);
