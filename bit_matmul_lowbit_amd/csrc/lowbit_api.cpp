@@ -56,7 +56,8 @@ int64_t padded(int64_t n) { return (n + 15) / 16 * 16; }
 int hip_status(hipError_t e) { return e == hipSuccess ? LOWBIT_OK : LOWBIT_ERR_HIP; }
 
 bool logits_shape_ok(int64_t n, int64_t b) {
-  return n >= 1 && n <= (int64_t(1) << 31) - 1 && b >= 1 && b <= 65535 && n <= kMaxElems / b;
+  // the grid's threads (one per 16 logits) stay below 2^32
+  return n >= 1 && n <= (int64_t(1) << 31) - 1 && b >= 1 && b <= 65535 && n <= (int64_t(1) << 35) / b;
 }
 
 bool lora_shape_ok(int64_t m, int64_t n, int64_t k, int64_t r, int64_t slots) {
@@ -367,7 +368,8 @@ int lowbit_norm_residual(const void* y, int y_type, int64_t ldy, const void* r, 
     return LOWBIT_ERR_ARG;
   if (y && gate && !type_ok(gate_type)) return LOWBIT_ERR_ARG;
   if (!(eps >= 0.0f)) return LOWBIT_ERR_ARG;
-  if (m < 1 || m > kMaxRows || k < 1 || k > kMaxK) return LOWBIT_ERR_SHAPE;
+  // a work-group of up to 1024 threads per row: the grid's threads stay below 2^32
+  if (m < 1 || m > kMaxRows / 2 || k < 1 || k > kMaxK) return LOWBIT_ERR_SHAPE;
   if (!rows_ok(m, k, ldr) || (y && !rows_ok(m, k, ldy)) || (r_out && !rows_ok(m, k, ldro)) ||
       (x_out && !rows_ok(m, k, ldx)) || (y && gate && ldg != 0 && !rows_ok(m, k, ldg)))
     return LOWBIT_ERR_SHAPE;

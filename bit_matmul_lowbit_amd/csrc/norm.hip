@@ -28,24 +28,28 @@ struct Raw8 {
 template <int S>
 __device__ __forceinline__ Raw8<S> load8(const void* p, int64_t i0, int c, int k) {
   Raw8<S> r;
-  const char* at = static_cast<const char*>(p) + (i0 + c) * S;
+  const char* row = static_cast<const char*>(p) + i0 * S;
   if (c + 8 <= k) {
-    __builtin_memcpy(&r, at, sizeof(r));
+    __builtin_memcpy(&r, row + (int64_t)c * S, sizeof(r));
   } else {
-#pragma unroll
-    for (int j = 0; j < 2 * S; ++j) r.d[j] = 0u;
+    // one by one, all on their way together; past the row its last element is
+    // read again and dropped
+    uint32_t e[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      if (c + j < k) {
-        if constexpr (S == 4) {
-          __builtin_memcpy(&r.d[j], at + j * 4, 4);
-        } else {
-          uint16_t h;
-          __builtin_memcpy(&h, at + j * 2, 2);
-          r.d[j >> 1] |= (uint32_t)h << ((j & 1) * 16);
-        }
+      const int64_t at = (int64_t)(c + j < k ? c + j : k - 1) * S;
+      if constexpr (S == 4) {
+        __builtin_memcpy(&e[j], row + at, 4);
+      } else {
+        uint16_t h;
+        __builtin_memcpy(&h, row + at, 2);
+        e[j] = h;
       }
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) e[j] = c + j < k ? e[j] : 0u;
+#pragma unroll
+    for (int j = 0; j < 2 * S; ++j) r.d[j] = S == 4 ? e[j] : e[2 * (j & 3)] | (e[2 * (j & 3) + 1] << 16);
   }
   return r;
 }
@@ -115,25 +119,35 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 
 // Sum over the threads that share a row.  Consecutive sums of a work-group
-// use the two halves of `red` in turn, so that one barrier each is enough.
+// use the two halves of `red` in turn, so that one barrier each is enough; the
+// places of waves that the work-group does not have hold zeros (row_sum_init).
+__device__ __forceinline__ void row_sum_init(float (*red)[16]) {
+  if (threadIdx.x < 32 && (threadIdx.x & 15) >= (blockDim.x >> 6)) red[threadIdx.x >> 4][threadIdx.x & 15] = 0.0f;
+}
 template <bool WAVE>
 __device__ __forceinline__ float row_sum(float v, float (*red)[16], int& turn) {
   v = wave_sum(v);
   if constexpr (WAVE) return v;
   if ((threadIdx.x & 63) == 0) red[turn][threadIdx.x >> 6] = v;
   __syncthreads();
-  const int waves = (int)blockDim.x >> 6;
-  float s = red[turn][0];
-  for (int w = 1; w < waves; ++w) s += red[turn][w];
+  float4 w[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) w[q] = *reinterpret_cast<const float4*>(&red[turn][q * 4]);
+  float s = 0.0f;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) s += (w[q].x + w[q].y) + (w[q].z + w[q].w);
   turn ^= 1;
   return s;
 }
 
 // Rows of up to threads * NV * 8 elements in registers.  SY, SR: bytes per
-// element of y and r.
-template <bool WAVE, int SY, int SR, int NV>
+// element of y and r.  AHEAD: weights and gate are fetched with the
+// row, not when they are needed, which takes two memory latencies off a small
+// call and occupancy off a large one.
+template <bool WAVE, int SY, int SR, int NV, bool AHEAD>
 __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(NormArgs a) {
-  __shared__ float red[2][16];
+  __shared__ __align__(16) float red[2][16];
+  if constexpr (!WAVE) row_sum_init(red);
   const int threads = WAVE ? 64 : (int)blockDim.x;
   const int t = WAVE ? threadIdx.x & 63 : threadIdx.x;
   const int64_t i = WAVE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : (int64_t)blockIdx.x;
@@ -150,6 +164,27 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(NormArgs a) {
     const int c = (n * threads + t) * 8;
     if (a.y) yr[n] = load8<SY>(a.y, i * a.ldy, c, k);
     rr[n] = load8<SR>(a.r, i * a.ldr, c, k);
+  }
+  float post_w[NV][8], post_b[NV][8], gate[NV][8], pre_w[NV][8], pre_b[NV][8];
+  auto gate8 = [&](int n) __attribute__((always_inline)) {
+    const int c = (n * threads + t) * 8;
+    if (a.gate_type == 1) widen<4>(load8<4>(a.gate, i * a.ldg, c, k), 1, gate[n]);
+    else widen<2>(load8<2>(a.gate, i * a.ldg, c, k), a.gate_type, gate[n]);
+  };
+  if constexpr (AHEAD) {
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+      const int c = (n * threads + t) * 8;
+      if (a.post != 0) {
+        vector8(a.post_w, 1.0f, c, k, post_w[n]);
+        vector8(a.post_b, 0.0f, c, k, post_b[n]);
+      }
+      if (a.pre != 0) {
+        vector8(a.pre_w, 1.0f, c, k, pre_w[n]);
+        vector8(a.pre_b, 0.0f, c, k, pre_b[n]);
+      }
+      if (a.gate) gate8(n);
+    }
   }
   if (a.y) {
     float u[NV][8];
@@ -180,18 +215,17 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(NormArgs a) {
       const int c = (n * threads + t) * 8;
       if (c < k) {
         if (a.post != 0) {
-          float w[8], b[8];
-          vector8(a.post_w, 1.0f, c, k, w);
-          vector8(a.post_b, 0.0f, c, k, b);
+          if constexpr (!AHEAD) {
+            vector8(a.post_w, 1.0f, c, k, post_w[n]);
+            vector8(a.post_b, 0.0f, c, k, post_b[n]);
+          }
 #pragma unroll
-          for (int j = 0; j < 8; ++j) u[n][j] = (u[n][j] - mean) * rs * w[j] + b[j];
+          for (int j = 0; j < 8; ++j) u[n][j] = (u[n][j] - mean) * rs * post_w[n][j] + post_b[n][j];
         }
         if (a.gate) {
-          float g[8];
-          if (a.gate_type == 1) widen<4>(load8<4>(a.gate, i * a.ldg, c, k), 1, g);
-          else widen<2>(load8<2>(a.gate, i * a.ldg, c, k), a.gate_type, g);
+          if constexpr (!AHEAD) gate8(n);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) u[n][j] *= g[j];
+          for (int j = 0; j < 8; ++j) u[n][j] *= gate[n][j];
         }
       }
       widen<SR>(rr[n], a.r_type, v[n]);
@@ -229,11 +263,12 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(NormArgs a) {
     const int c = (n * threads + t) * 8;
     if (c >= k) continue;
     if (a.pre != 0) {
-      float w[8], b[8];
-      vector8(a.pre_w, 1.0f, c, k, w);
-      vector8(a.pre_b, 0.0f, c, k, b);
+      if constexpr (!AHEAD) {
+        vector8(a.pre_w, 1.0f, c, k, pre_w[n]);
+        vector8(a.pre_b, 0.0f, c, k, pre_b[n]);
+      }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[n][j] = (v[n][j] - mean) * rs * w[j] + b[j];
+      for (int j = 0; j < 8; ++j) v[n][j] = (v[n][j] - mean) * rs * pre_w[n][j] + pre_b[n][j];
     }
     store8(a.x_out, a.x_type, i * a.ldx, c, k, v[n]);
   }
@@ -257,7 +292,8 @@ __device__ __forceinline__ void store_any(void* p, int type, int64_t i, float v)
 // Rows longer than a work-group's registers: nothing is kept, each sum reads
 // the row again (a row of 2^22 would not fit a compute unit in any form).
 __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
-  __shared__ float red[2][16];
+  __shared__ __align__(16) float red[2][16];
+  row_sum_init(red);
   int turn = 0;
   const int64_t i = blockIdx.x;
   const float inv_k = 1.0f / (float)a.k;
@@ -320,13 +356,13 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
   }
 }
 
-template <bool WAVE, int NV>
+template <bool WAVE, int NV, bool AHEAD>
 hipError_t launch_as(const NormArgs& a, dim3 grid, dim3 block, hipStream_t st) {
   const bool y4 = a.y_type == 1, r4 = a.r_type == 1;
-  if (y4 && r4) hipLaunchKernelGGL((norm_kernel<WAVE, 4, 4, NV>), grid, block, 0, st, a);
-  else if (y4) hipLaunchKernelGGL((norm_kernel<WAVE, 4, 2, NV>), grid, block, 0, st, a);
-  else if (r4) hipLaunchKernelGGL((norm_kernel<WAVE, 2, 4, NV>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((norm_kernel<WAVE, 2, 2, NV>), grid, block, 0, st, a);
+  if (y4 && r4) hipLaunchKernelGGL((norm_kernel<WAVE, 4, 4, NV, AHEAD>), grid, block, 0, st, a);
+  else if (y4) hipLaunchKernelGGL((norm_kernel<WAVE, 4, 2, NV, AHEAD>), grid, block, 0, st, a);
+  else if (r4) hipLaunchKernelGGL((norm_kernel<WAVE, 2, 4, NV, AHEAD>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((norm_kernel<WAVE, 2, 2, NV, AHEAD>), grid, block, 0, st, a);
   return hipGetLastError();
 }
 
@@ -334,16 +370,22 @@ hipError_t launch_as(const NormArgs& a, dim3 grid, dim3 block, hipStream_t st) {
 
 hipError_t launch_norm_residual(const NormArgs& a, hipStream_t st) {
   const int64_t chunks = (a.k + 7) / 8;
+  const bool many = a.m >= 1024;
   // short rows, many of them: one wave each, no barriers
-  if (chunks <= 128 && a.m >= 1024) {
+  if (chunks <= 128 && many) {
     const dim3 grid((unsigned)((a.m + 3) / 4));
-    return chunks <= 64 ? launch_as<true, 1>(a, grid, dim3(256), st) : launch_as<true, 2>(a, grid, dim3(256), st);
+    return chunks <= 64 ? launch_as<true, 1, false>(a, grid, dim3(256), st)
+                        : launch_as<true, 2, false>(a, grid, dim3(256), st);
   }
   const dim3 grid((unsigned)a.m);
   auto block = [&](int64_t nv) { return dim3((unsigned)((chunks + nv * 64 - 1) / (nv * 64) * 64)); };
-  if (chunks <= 1024) return launch_as<false, 1>(a, grid, block(1), st);
-  if (chunks <= 2048) return launch_as<false, 2>(a, grid, block(2), st);
-  if (chunks <= 4096) return launch_as<false, 4>(a, grid, block(4), st);
+  // Many long rows: 16 elements a thread, so that more work-groups of fewer
+  // waves share a compute unit (16384 x 5120 BF16: 144 us, with 8 elements 184,
+  // with 32 161; 4096 x 4096 27 each way).
+  if (chunks <= 1024 && !(many && chunks > 512))
+    return many ? launch_as<false, 1, false>(a, grid, block(1), st) : launch_as<false, 1, true>(a, grid, block(1), st);
+  if (chunks <= 2048) return launch_as<false, 2, false>(a, grid, block(2), st);
+  if (chunks <= 4096) return launch_as<false, 4, false>(a, grid, block(4), st);
   hipLaunchKernelGGL(norm_long_kernel, grid, dim3(1024), 0, st, a);
   return hipGetLastError();
 }

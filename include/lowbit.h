@@ -403,7 +403,7 @@ int lowbit_lm_head(int fmt, const void* codes, const uint16_t* scales, int64_t n
  *            used with LOWBIT_NORM_NONE
  *   gate   : gate_type; one row of k for every i when ldg is 0, else [m]
  *            rows at stride ldg; or NULL
- * Strides count elements and are at least k (or 0 for ldg).  1 <= m <= 2^22,
+ * Strides count elements and are at least k (or 0 for ldg).  1 <= m <= 2^21,
  * 1 <= k <= 2^22, m * stride < 2^40.  At least one of r_out and x_out is
  * given.  Pointers need their element's alignment only; rows whose
  * pointers and strides are multiples of 16 bytes are read 16 bytes at a
@@ -452,8 +452,8 @@ size_t lowbit_logits_workspace_bytes(int64_t n, int64_t b);
  *               the mask allows nothing; not written without idx
  *   workspace : lowbit_logits_workspace_bytes(n, b) bytes, contents ignored
  *               on entry; not used (NULL allowed) without idx
- * At least one of out and idx is given.  n < 2^31, b <= 65535, tcap, bcap
- * < 2^30.  Pointers other than the workspace need their element's alignment
+ * At least one of out and idx is given.  n < 2^31, b <= 65535, n * b <= 2^35,
+ * tcap, bcap < 2^30.  Pointers other than the workspace need their element's alignment
  * only.  Equal inputs give equal bits. */
 int lowbit_logits_process(const void* y, int y_type, int64_t ldy, int64_t n, int64_t b,
                           const int32_t* tokens, int64_t tcap, int64_t ldt,
