@@ -556,18 +556,19 @@ def lowbit_base3_to_t2(b3, scales_rm, n: int, k: int, codes=None, scales=None, s
 # common case passes one condition, and what fails it is named afterwards.
 
 _types = {}      # torch dtype -> lowbit_type
-_torch = None
+_torch = _raw_stream = _current_device = _f32 = _i32 = None
 
 
 def _first_use():
-    """Import torch and fill the type table (importing this module loads
-    nothing)."""
-    global _torch
+    """Import torch and fill the tables (importing this module loads nothing)."""
+    global _torch, _raw_stream, _current_device, _f32, _i32
     import torch
 
+    load()
     _types.update({torch.float32: 1, torch.float16: 2, torch.bfloat16: 3})
+    _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    _f32, _i32 = torch.float32, torch.int32
     _torch = torch
-    return torch
 
 
 def _float_rows(t, shape, dev, name):
@@ -610,10 +611,7 @@ def _shape2(t, name):
 
 
 def _vector(t, dtype, count, name, dev):
-    """Pointer of a contiguous device tensor of at least `count` elements, or
-    None (NULL) for None."""
-    if t is None:
-        return None
+    """Pointer of a contiguous device tensor of at least `count` elements."""
     if t.dtype is dtype and t.get_device() == dev and t.numel() >= count and t.is_contiguous():
         return t.data_ptr()
     if t.dtype != dtype or not t.is_cuda:
@@ -627,9 +625,12 @@ def _vector(t, dtype, count, name, dev):
 
 def _lists(t, dtype, b, name, dev):
     """(pointer, columns, row stride) of a [b][columns] device tensor with
-    contiguous rows, or (None, 0, 0) for None."""
-    if t is None:
-        return None, 0, 0
+    contiguous rows (any number of them for b None)."""
+    if t.dtype is dtype and t.dim() == 2 and t.get_device() == dev:
+        rows, cols = t.shape
+        ld, unit = t.stride()
+        if unit == 1 and (b is None or rows == b):
+            return t.data_ptr(), cols, ld if rows > 1 else max(ld, cols)
     if t.dtype != dtype or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor of {dtype}")
     if t.get_device() != dev:
@@ -643,19 +644,19 @@ def _lists(t, dtype, b, name, dev):
     return t.data_ptr(), cols, ld if rows > 1 else max(ld, cols)
 
 
-def _call(where, dev, stream, args, keep=()):
+def _call(where, dev, stream, args, made=()):
     """Call library function `where` on `stream` (default: the current one of
-    device `dev`) with that device current.  `keep`: tensors allocated here
+    device `dev`) with that device current.  `made`: tensors allocated here
     that the kernels use; the allocator is told when the stream is not the one
     they belong to."""
-    fn = getattr(_lib or load(), where)
+    fn = getattr(_lib, where)
     if stream is None:
-        raw = _torch._C._cuda_getCurrentRawStream(dev)
+        raw = _raw_stream(dev)
     else:
         raw = stream.cuda_stream
-        for t in keep:
+        for t in made:
             t.record_stream(stream)
-    if dev == _torch._C._cuda_getDevice():
+    if dev == _current_device():
         status = fn(*args, raw)
     else:
         with _torch.cuda.device(dev):
@@ -675,11 +676,11 @@ def lowbit_norm_residual(y, r, post="none", post_w=None, post_b=None, gate=None,
     "none", "rms" or "layer" with FP32 weights and biases [k] (None: 1 and
     0); pre=None makes no x.  gate: [k] for every row or [m][k].  x_out is
     allocated with x_dtype (FP16, as lowbit_gemv reads it, if not given)."""
-    torch = _torch or _first_use()
+    if _torch is None:
+        _first_use()
     shape, dev = _shape2(r, "r")
     m, k = shape
     rp, rt, ldr = _float_rows(r, shape, dev, "r")
-    f32 = torch.float32
     yp = yt = ldy = gp = gt = ldg = rop = ldro = xp = xt = ldx = post_c = pre_c = 0
     made = ()
     if y is not None:
@@ -701,15 +702,19 @@ def lowbit_norm_residual(y, r, post="none", post_w=None, post_b=None, gate=None,
     if pre is not None:
         pre_c = NORMS[pre]
         if x_out is None:
-            x_out = torch.empty(r.shape, dtype=x_dtype or torch.float16, device=r.device)
+            x_out = _torch.empty(r.shape, dtype=x_dtype or _torch.float16, device=r.device)
             made = (x_out,)
         xp, xt, ldx = _float_rows(x_out, shape, dev, "x_out")
     elif x_out is not None:
         raise ValueError("x_out needs pre")
     _call("lowbit_norm_residual", dev, stream,
           (yp, yt, ldy, rp, rt, ldr, rop, ldro, xp, xt, ldx, m, k, post_c,
-           _vector(post_w, f32, k, "post_w", dev), _vector(post_b, f32, k, "post_b", dev), gp, gt, ldg, scale,
-           pre_c, _vector(pre_w, f32, k, "pre_w", dev), _vector(pre_b, f32, k, "pre_b", dev), eps), made)
+           None if post_w is None else _vector(post_w, _f32, k, "post_w", dev),
+           None if post_b is None else _vector(post_b, _f32, k, "post_b", dev),
+           gp, gt, ldg, scale, pre_c,
+           None if pre_w is None else _vector(pre_w, _f32, k, "pre_w", dev),
+           None if pre_b is None else _vector(pre_b, _f32, k, "pre_b", dev),
+           eps), made)
     return (r_out if y is not None else r), x_out
 
 
@@ -730,22 +735,24 @@ def lowbit_logits_process(y, tokens=None, prompt_len=None, total_len=None, repet
     repetition / frequency / presence FP32 [b]; bias_ids int32 and bias_vals
     FP32 [b][.] with bias_len int32 [b]; mask int32 [rows][>= n / 32] with
     mask_row int32 [b]."""
-    torch = _torch or _first_use()
-    f32, i32 = torch.float32, torch.int32
+    if _torch is None:
+        _first_use()
     shape, dev = _shape2(y, "y")
     b, n = shape
     yp, yt, ldy = _float_rows(y, shape, dev, "y")
-    tp, tcap, ldt = _lists(tokens, i32, b, "tokens", dev)
+    tp, tcap, ldt = _lists(tokens, _i32, b, "tokens", dev) if tokens is not None else (None, 0, 0)
     bp = bv = None
     bcap = ldb = 0
     if bias_ids is not None or bias_vals is not None:
-        bp, bcap, ldb = _lists(bias_ids, i32, b, "bias_ids", dev)
-        bv, bvcap, ldbv = _lists(bias_vals, f32, b, "bias_vals", dev)
-        if bp is None or bv is None or bcap != bvcap or ldb != ldbv:
+        if bias_ids is None or bias_vals is None:
+            raise ValueError("bias_ids and bias_vals go together")
+        bp, bcap, ldb = _lists(bias_ids, _i32, b, "bias_ids", dev)
+        bv, bvcap, ldbv = _lists(bias_vals, _f32, b, "bias_vals", dev)
+        if bcap != bvcap or ldb != ldbv:
             raise ValueError("bias_ids and bias_vals must have one shape and row stride")
     mp, rows, ldm = None, 0, 0
     if mask is not None:
-        mp, words, ldm = _lists(mask, i32, None if mask_row is not None else b, "mask", dev)
+        mp, words, ldm = _lists(mask, _i32, None if mask_row is not None else b, "mask", dev)
         rows = mask.shape[0]
         if words < (n + 31) // 32:
             raise ValueError(f"mask has {words} words a row, needs {(n + 31) // 32}")
@@ -759,24 +766,31 @@ def lowbit_logits_process(y, tokens=None, prompt_len=None, total_len=None, repet
     made = ()
     if top1:
         if idx is None:
-            idx = torch.empty(b, dtype=i32, device=y.device)
+            idx = _torch.empty(b, dtype=_i32, device=y.device)
             made += (idx,)
         if val is None:
-            val = torch.empty(b, dtype=f32, device=y.device)
+            val = _torch.empty(b, dtype=_f32, device=y.device)
             made += (val,)
         if workspace is None:
-            workspace = torch.empty(max(lowbit_logits_workspace_bytes(n, b), 16), dtype=torch.uint8, device=y.device)
+            need = lowbit_logits_workspace_bytes(n, b)
+            workspace = _torch.empty(max(need, 16), dtype=_torch.uint8, device=y.device)
             made += (workspace,)
-        ip, vp = _vector(idx, i32, b, "idx", dev), _vector(val, f32, b, "val", dev)
-        wp, need = _vector(workspace, torch.uint8, 0, "workspace", dev), workspace.numel()
+        ip, vp = _vector(idx, _i32, b, "idx", dev), _vector(val, _f32, b, "val", dev)
+        wp, need = _vector(workspace, _torch.uint8, 0, "workspace", dev), workspace.numel()
     elif idx is not None or val is not None:
         raise ValueError("idx and val need top1")
     _call("lowbit_logits_process", dev, stream,
-          (yp, yt, ldy, n, b, tp, tcap, ldt, _vector(prompt_len, i32, b, "prompt_len", dev),
-           _vector(total_len, i32, b, "total_len", dev), _vector(repetition, f32, b, "repetition", dev),
-           _vector(frequency, f32, b, "frequency", dev), _vector(presence, f32, b, "presence", dev), bp, bv, bcap,
-           ldb, _vector(bias_len, i32, b, "bias_len", dev), mp, rows, ldm,
-           _vector(mask_row, i32, b, "mask_row", dev), op, ldo, ip, vp, wp, need), made)
+          (yp, yt, ldy, n, b, tp, tcap, ldt,
+           None if prompt_len is None else _vector(prompt_len, _i32, b, "prompt_len", dev),
+           None if total_len is None else _vector(total_len, _i32, b, "total_len", dev),
+           None if repetition is None else _vector(repetition, _f32, b, "repetition", dev),
+           None if frequency is None else _vector(frequency, _f32, b, "frequency", dev),
+           None if presence is None else _vector(presence, _f32, b, "presence", dev),
+           bp, bv, bcap, ldb,
+           None if bias_len is None else _vector(bias_len, _i32, b, "bias_len", dev),
+           mp, rows, ldm,
+           None if mask_row is None else _vector(mask_row, _i32, b, "mask_row", dev),
+           op, ldo, ip, vp, wp, need), made)
     return out, idx, val
 
 
@@ -791,7 +805,8 @@ def lowbit_lora_accumulate(x, ids, a, b, y, ranks=None, scales=None, workspace=N
     [slots][r][k] and b [slots][n][r] in x's type, ranks int32 [slots], scales
     FP32 [slots], y [m][n] FP32 (or BF16 with BF16 x); rows of x and y may be
     strided (a slice of a fused projection's output)."""
-    torch = _torch or _first_use()
+    if _torch is None:
+        _first_use()
     shape, dev = _shape2(x, "x")
     m, k = shape
     xp, xt, ldx = _float_rows(x, shape, dev, "x")
@@ -804,13 +819,14 @@ def lowbit_lora_accumulate(x, ids, a, b, y, ranks=None, scales=None, workspace=N
     made = ()
     if workspace is None:
         need = lowbit_lora_workspace_bytes(m, n, k, r, slots)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
+        workspace = _torch.empty(max(need, 16), dtype=_torch.uint8, device=x.device)
         made = (workspace,)
     _call("lowbit_lora_accumulate", dev, stream,
-          (xp, xt, ldx, _vector(ids, torch.int32, m, "ids", dev), m, n, k, r, slots,
+          (xp, xt, ldx, _vector(ids, _i32, m, "ids", dev), m, n, k, r, slots,
            _vector(a, x.dtype, 0, "a", dev), _vector(b, x.dtype, 0, "b", dev),
-           _vector(ranks, torch.int32, slots, "ranks", dev), _vector(scales, torch.float32, slots, "scales", dev),
-           yp, yt, ldy, _vector(workspace, torch.uint8, 0, "workspace", dev), workspace.numel()), made)
+           None if ranks is None else _vector(ranks, _i32, slots, "ranks", dev),
+           None if scales is None else _vector(scales, _f32, slots, "scales", dev),
+           yp, yt, ldy, _vector(workspace, _torch.uint8, 0, "workspace", dev), workspace.numel()), made)
     return y
 
 
