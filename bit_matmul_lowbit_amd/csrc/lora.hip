@@ -7,7 +7,8 @@
 //      what is learned on top of it lives in such adapters.
 //
 // Rows are grouped by adapter, so that an adapter's matrices meet all of its
-// rows at once.  An item is up to 32 rows of one adapter (16 where m <= 16).
+// rows at once.  An item is up to 32 rows of one adapter (16 where adapters
+// have few rows).
 // With m <= 64 every work-group finds its item itself: the ids of all rows
 // fit one wave, and ballots pick out the rows that share one (no launch, no
 // memory).  More rows are sorted by one work-group first (lora_plan_kernel).
@@ -83,27 +84,29 @@ __device__ __forceinline__ int lanes_below(uint64_t mask) {
 }
 
 // What the plan of more than kInlineRows rows holds, at the head of the
-// workspace: the number of items, the items, and the rows in item order.
+// workspace: the number of items, the items, and their rows, tm places to an
+// item.  All three are found by the item's number alone, so that they are read
+// in one memory latency.
 struct Item {
-  int slot, start, count, unused;
+  int slot, count, rank;
+  float scale;
 };
 struct Plan {
   int* items_used;
   Item* items;
   int* rows;
+  int most;  // items there is room for
 };
 
-// Item number `item`: its adapter and row count (0: there is none), and its
-// rows in rows[0 .. count) (LDS).  Ends in a barrier if there is one.
+// Item number `item` (tm rows at most): its count is 0 if there is none; its
+// rows go to rows[0 .. count) (LDS).  Ends in a barrier if there is one.
 template <bool INLINE>
-__device__ __forceinline__ int find_item(const LoraArgs& a, const Plan& plan, int item, int tm,
-                                         int* rows, int* slot) {
-  int count = 0;
+__device__ __forceinline__ Item find_item(const LoraArgs& a, const Plan& plan, int item, int tm, int* rows) {
+  Item it = {0, 0, 0, 1.0f};
   if constexpr (INLINE) {
     const int lane = threadIdx.x & 63;
     const int s = lane < a.m ? slot_of(a, lane) : -1;
     uint64_t left = __ballot(s >= 0);
-    uint64_t mine = 0;
     int seen = 0;
     while (left) {
       const int ls = __builtin_amdgcn_readlane(s, __builtin_ctzll(left));
@@ -111,26 +114,28 @@ __device__ __forceinline__ int find_item(const LoraArgs& a, const Plan& plan, in
       const int n = __popcll(same), parts = (n + tm - 1) / tm;
       if (item < seen + parts) {
         const int first = (item - seen) * tm;
-        count = n - first < tm ? n - first : tm;
-        *slot = ls;
-        mine = same;
-        const int at = lanes_below(mine) - first;
-        if (threadIdx.x < 64 && ((mine >> lane) & 1) && at >= 0 && at < count) rows[at] = lane;
+        it.count = n - first < tm ? n - first : tm;
+        it.slot = ls;
+        it.rank = rank_of(a, ls);
+        if (a.scales) it.scale = a.scales[ls];
+        const int at = lanes_below(same) - first;
+        if (threadIdx.x < 64 && ((same >> lane) & 1) && at >= 0 && at < it.count) rows[at] = lane;
         break;
       }
       seen += parts;
       left &= ~same;
     }
-  } else {
-    if (item < *plan.items_used) {
-      const Item it = plan.items[item];
-      count = it.count;
-      *slot = it.slot;
-      if ((int)threadIdx.x < count) rows[threadIdx.x] = plan.rows[it.start + threadIdx.x];
+  } else if (item < plan.most) {
+    const int used = *plan.items_used;
+    const Item got = plan.items[item];
+    const int row = plan.rows[item * tm + (threadIdx.x & (tm - 1))];
+    if (item < used) {
+      it = got;
+      if ((int)threadIdx.x < it.count) rows[threadIdx.x] = row;
     }
   }
-  if (count) __syncthreads();
-  return count;
+  if (it.count) __syncthreads();
+  return it;
 }
 
 // inclusive prefix sum over the wave's lanes, by DPP
@@ -147,17 +152,17 @@ __device__ __forceinline__ int wave_scan(int v) {
 }
 
 // Rows sorted by adapter, in one work-group: each row takes the next place
-// among its adapter's (a counter in LDS), prefix sums over the adapters give
-// each adapter's first place.  Rows of one adapter keep nearly their order;
-// which place one gets changes no result, each row being a row of the products
-// of its own.  A wave whose rows share one adapter, as in a long prompt, adds
-// to the counter once.  The work-group's first 4096 rows keep their places in
-// registers, later ones in `place`.
+// among its adapter's (a counter in LDS); a prefix sum over the adapters'
+// items gives each adapter's first item.  Rows of one adapter keep nearly
+// their order; which place one gets changes no result, each row being a row
+// of the products of its own.  A wave whose rows share one adapter, as in a
+// long prompt, adds to the counter once.  The work-group's first 4096 rows
+// keep their places in registers, later ones in `place`.
 __global__ __launch_bounds__(1024) void lora_plan_kernel(LoraArgs a, Plan plan, int tm, int* place) {
   constexpr int kHeld = 4;
-  __shared__ int cnt[kMaxSlots];
-  __shared__ int wave_rows[16], wave_items[16];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  __shared__ int cnt[kMaxSlots], first[kMaxSlots];
+  __shared__ int wave_items[16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int slot[kHeld], at[kHeld];
 #pragma unroll
   for (int t = 0; t < kHeld; ++t) slot[t] = t * 1024 + tid < a.m ? slot_of(a, t * 1024 + tid) : -1;
@@ -167,9 +172,9 @@ __global__ __launch_bounds__(1024) void lora_plan_kernel(LoraArgs a, Plan plan, 
     const int s0 = __builtin_amdgcn_readfirstlane(s);
     if (__ballot(s == s0) == ~0ull) {
       if (s0 < 0) return 0;
-      int first = 0;
-      if (lane == 0) first = atomicAdd(&cnt[s0], 64);
-      return __builtin_amdgcn_readfirstlane(first) + lane;
+      int got = 0;
+      if (lane == 0) got = atomicAdd(&cnt[s0], 64);
+      return __builtin_amdgcn_readfirstlane(got) + lane;
     }
     return s >= 0 ? atomicAdd(&cnt[s], 1) : 0;
   };
@@ -183,43 +188,39 @@ __global__ __launch_bounds__(1024) void lora_plan_kernel(LoraArgs a, Plan plan, 
     if (i < a.m) place[i] = p;
   }
   __syncthreads();
-  int own[4], rows = 0, items = 0;
+  int own[4], items = 0;
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
-    own[u] = tid * 4 + u < a.slots ? cnt[tid * 4 + u] : 0;
-    rows += own[u];
-    items += (own[u] + tm - 1) / tm;
+    own[u] = tid * 4 + u < a.slots ? (cnt[tid * 4 + u] + tm - 1) / tm : 0;
+    items += own[u];
   }
-  const int rows_to = wave_scan(rows), items_to = wave_scan(items);
-  if (lane == 63) {
-    wave_rows[wave] = rows_to;
-    wave_items[wave] = items_to;
+  const int items_to = wave_scan(items);
+  if (lane == 63) wave_items[wave] = items_to;
+  __syncthreads();
+  const int waves_to = wave_scan(lane < 16 ? wave_items[lane] : 0);
+  int it = items_to - items + (wave ? __builtin_amdgcn_readlane(waves_to, wave - 1) : 0);
+  if (tid == 0) *plan.items_used = __builtin_amdgcn_readlane(waves_to, 15);
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    if (tid * 4 + u < a.slots) first[tid * 4 + u] = it;
+    it += own[u];
   }
   __syncthreads();
-  int start = rows_to - rows, it = items_to - items;
-  for (int w = 0; w < wave; ++w) {
-    start += wave_rows[w];
-    it += wave_items[w];
-  }
-  if (tid == 1023) *plan.items_used = it + items;
-#pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int s = tid * 4 + u;
-    if (s < a.slots) {
-      for (int p = 0; p < own[u]; p += tm)
-        plan.items[it++] = Item{s, start + p, own[u] - p < tm ? own[u] - p : tm, 0};
-      cnt[s] = start;
-      start += own[u];
+  auto put = [&](int s, int p, int i) __attribute__((always_inline)) {
+    const int item = first[s] + p / tm, at = p % tm;
+    plan.rows[item * tm + at] = i;
+    if (at == 0) {
+      const int left = cnt[s] - p;
+      plan.items[item] = Item{s, left < tm ? left : tm, rank_of(a, s), a.scales ? a.scales[s] : 1.0f};
     }
-  }
-  __syncthreads();
+  };
 #pragma unroll
   for (int t = 0; t < kHeld; ++t)
-    if (slot[t] >= 0) plan.rows[cnt[slot[t]] + at[t]] = t * 1024 + tid;
+    if (slot[t] >= 0) put(slot[t], at[t], t * 1024 + tid);
   for (int64_t t = kHeld; t < steps; ++t) {
     const int64_t i = t * 1024 + tid;
     const int s = i < a.m ? slot_of(a, i) : -1;
-    if (s >= 0) plan.rows[cnt[s] + place[i]] = (int)i;
+    if (s >= 0) put(s, place[i], (int)i);
   }
 }
 
@@ -328,14 +329,13 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs a, Plan plan,
   __shared__ int rows[kItemRows];
   __shared__ uint4 stage[kShrinkWaves][1 + RT][16][8];
   const int item = blockIdx.x / subs, sub = blockIdx.x % subs;
-  int slot = 0;
-  const int count = find_item<INLINE>(a, plan, item, tm, rows, &slot);
-  const int here = count - sub * 16 < 16 ? count - sub * 16 : 16;
+  const Item it = find_item<INLINE>(a, plan, item, tm, rows);
+  const int here = it.count - sub * 16 < 16 ? it.count - sub * 16 : 16;
   if (here <= 0) return;
-  const int rank = rank_of(a, slot), r0 = (int)blockIdx.y * RT * 16;
+  const int rank = it.rank, r0 = (int)blockIdx.y * RT * 16;
   if (r0 >= rank) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const f32x4 sum = shrink16<XT, RT>(a, slot, rank, r0, rows + sub * 16, here, stage,
+  const f32x4 sum = shrink16<XT, RT>(a, it.slot, rank, r0, rows + sub * 16, here, stage,
                                      (int)blockIdx.z * kShrinkWaves + wave, kShrinkWaves * (int)gridDim.z);
   const int c = threadIdx.x & 15, j = r0 + wave * 16 + ((threadIdx.x >> 4) & 3) * 4;
   // j .. j + 3 lie in the row (r is a multiple of 8); what is past the rank is not read
@@ -431,15 +431,16 @@ __device__ __forceinline__ void store_tail(const Out4<3>& z, bf16_t* p, int n) {
 // is made ready: first() brings about what inner(row, j), four sums of v from
 // rank j on, needs.
 template <int XT, int YT, int SUBS, int WAVES, class First, class Inner>
-__device__ __forceinline__ void expand_item(const LoraArgs& a, int slot, int count, int rank, const int* rows,
-                                            float* unscale, typename Elem<XT>::type* pieces, int tm, int share,
+__device__ __forceinline__ void expand_item(const LoraArgs& a, const Item& it, const int* rows, float* unscale,
+                                            typename Elem<XT>::type* pieces, int tm, int share,
                                             int shares, First first, Inner inner) {
   constexpr int P = Mma<XT>::pieces;
   typedef typename Elem<XT>::type X;
   typedef typename Elem<YT>::type Y;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 15, q = lane >> 4;
-  const float scale = a.scales ? a.scales[slot] : 1.0f;
+  const int slot = it.slot, count = it.count, rank = it.rank;
+  const float scale = it.scale;
   const int chunks = (rank + 31) / 32, pitch = chunks * 32 + 8;  // 16 bytes past: other banks
   const X* bs = static_cast<const X*>(a.b) + (int64_t)slot * a.n * a.r;
   // where row 4 q + e of a part has its outputs n0 + 4 c ...; made anew at
@@ -611,9 +612,8 @@ __global__ __launch_bounds__(256, SUBS == 1 || YT == 3 ? 3 : 2) void lora_expand
   __shared__ int rows[kItemRows];
   __shared__ float unscale[kItemRows];
   for (int item = blockIdx.y;; item += gridDim.y) {
-    int slot = 0;
-    const int count = find_item<INLINE>(a, plan, item, tm, rows, &slot);
-    if (!count) return;
+    const Item it = find_item<INLINE>(a, plan, item, tm, rows);
+    if (!it.count) return;
     auto inner = [&](int at, int j) __attribute__((always_inline)) {
       const float* vr = v + (int64_t)rows[at] * a.r + j;
       f32x4 sum = (f32x4){0.f, 0.f, 0.f, 0.f};
@@ -630,7 +630,7 @@ __global__ __launch_bounds__(256, SUBS == 1 || YT == 3 ? 3 : 2) void lora_expand
       }
       return sum;
     };
-    expand_item<XT, YT, SUBS, 4>(a, slot, count, rank_of(a, slot), rows, unscale,
+    expand_item<XT, YT, SUBS, 4>(a, it, rows, unscale,
                                  reinterpret_cast<typename Elem<XT>::type*>(dyn), tm, (int)blockIdx.x,
                                  (int)gridDim.x, [] {}, inner);
     __syncthreads();  // the next item's rows and pieces
@@ -648,13 +648,11 @@ __global__ __launch_bounds__(512) void lora_small_kernel(LoraArgs a) {
   __shared__ uint4 stage[kWaves][1 + RT][16][8];
   __shared__ __align__(16) float inner_v[16][kPitch];
   __shared__ uint4 pieces[Mma<XT>::pieces * 16 * ((RT * 16 + 31) / 32 * 32 + 8) / 8];
-  int slot = 0;
-  const int count = find_item<true>(a, Plan{}, (int)blockIdx.y, 16, rows, &slot);
-  if (!count) return;
-  const int rank = rank_of(a, slot);
+  const Item it = find_item<true>(a, Plan{}, (int)blockIdx.y, 16, rows);
+  if (!it.count) return;
   auto first = [&]() __attribute__((always_inline)) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const f32x4 sum = shrink16<XT, RT>(a, slot, rank, 0, rows, count, stage, wave, kWaves);
+    const f32x4 sum = shrink16<XT, RT>(a, it.slot, it.rank, 0, rows, it.count, stage, wave, kWaves);
     if (wave < RT)
       *reinterpret_cast<f32x4*>(&inner_v[threadIdx.x & 15][wave * 16 + ((threadIdx.x >> 4) & 3) * 4]) = sum;
     __syncthreads();
@@ -662,14 +660,16 @@ __global__ __launch_bounds__(512) void lora_small_kernel(LoraArgs a) {
   auto inner = [&](int at, int j) __attribute__((always_inline)) {
     return *reinterpret_cast<const f32x4*>(&inner_v[at][j]);
   };
-  expand_item<XT, YT, 1, kWaves>(a, slot, count, rank, rows, unscale,
+  expand_item<XT, YT, 1, kWaves>(a, it, rows, unscale,
                                  reinterpret_cast<typename Elem<XT>::type*>(pieces), 16, (int)blockIdx.x,
                                  (int)gridDim.x, first, inner);
 }
 
 int64_t round256(int64_t v) { return (v + 255) / 256 * 256; }
 
-int item_rows(int64_t m) { return m <= 16 ? 16 : kItemRows; }
+// Rows of an item at most: 32 halve the reads of an adapter that many rows
+// share; with few rows to an adapter the second 16 would be empty work-groups.
+int item_rows(int64_t m, int64_t slots) { return m <= kInlineRows || m <= 16 * slots ? 16 : kItemRows; }
 
 int64_t max_items(int64_t m, int64_t slots, int64_t tm) {
   // every item but an adapter's last is full
@@ -678,23 +678,29 @@ int64_t max_items(int64_t m, int64_t slots, int64_t tm) {
 }
 
 int64_t plan_bytes(int64_t m, int64_t slots, int64_t tm) {
-  return m <= kInlineRows ? 0 : 256 + round256(max_items(m, slots, tm) * 16) + round256(m * 4);
+  return m <= kInlineRows ? 0 : 256 + round256(max_items(m, slots, tm) * (16 + tm * 4));
 }
 
-int ranks_per_block(int64_t m, int64_t r) {
-  // few rows: many work-groups of 16 ranks, each reading x again (from the
-  // cache); many rows: x, the larger operand, is read once per 64 ranks
-  if (m <= kInlineRows || r <= 16) return 1;
+// 16-row units of the first product: of all items, as many as there can be
+int64_t shrink_units(int64_t m, int64_t slots) {
+  const int64_t items = max_items(m, slots, item_rows(m, slots)), rows = (m + 15) / 16;
+  return items > rows ? items : rows;
+}
+
+// Ranks a work-group of the first product takes, in 16s.  Few rows: 16, for
+// many work-groups, each reading x again (from the cache); many rows: x, the
+// larger operand, is read once per 64 ranks.
+int ranks_per_block(int64_t m, int64_t r, int64_t slots) {
+  if (r <= 16 || shrink_units(m, slots) * ((r + 15) / 16) <= 256) return 1;
   return r <= 32 ? 2 : 4;
 }
 
-// k in slices until there are about two work-groups per compute unit; a wave
-// keeps at least 64 of k
+// k in slices as long as all work-groups run at once (two to a compute unit,
+// one where each takes 64 ranks); a wave keeps at least 64 of k
 int64_t slices_of(int64_t m, int64_t k, int64_t r, int64_t slots) {
-  const int tm = item_rows(m), rt = ranks_per_block(m, r);
-  const int64_t items = max_items(m, slots, tm), units = items > (m + 15) / 16 ? items : (m + 15) / 16;
-  const int64_t groups = (r + rt * 16 - 1) / (rt * 16);
-  int64_t s = (512 + units * groups - 1) / (units * groups);
+  const int rt = ranks_per_block(m, r, slots);
+  const int64_t groups = shrink_units(m, slots) * ((r + rt * 16 - 1) / (rt * 16));
+  int64_t s = (rt == 4 ? 256 : 512) / groups;
   const int64_t most = k / (64 * kShrinkWaves);
   s = s < most ? s : most;
   return s < 1 ? 1 : (s > kMaxSlices ? kMaxSlices : s);
@@ -722,7 +728,7 @@ hipError_t launch_small(const LoraArgs& a, hipStream_t st) {
 
 template <int XT, int YT, bool INLINE>
 hipError_t launch(const LoraArgs& a, const Plan& plan, float* v, hipStream_t st) {
-  const int tm = item_rows(a.m), rt = ranks_per_block(a.m, a.r);
+  const int tm = item_rows(a.m, a.slots), rt = ranks_per_block(a.m, a.r, a.slots);
   const int64_t items = max_items(a.m, a.slots, tm);
   const int64_t rows = a.m < tm ? a.m : tm;
   const int subs = (int)((rows + 15) / 16);
@@ -745,7 +751,7 @@ hipError_t launch(const LoraArgs& a, const Plan& plan, float* v, hipStream_t st)
   each = each < tiles ? each : tiles;
   const dim3 ge((unsigned)((tiles + each - 1) / each), (unsigned)(items < 32768 ? items : 32768));
   const size_t lds = (size_t)Mma<XT>::pieces * tm * ((a.r + 31) / 32 * 32 + 8) * 2;
-  if (INLINE && tm == 16)
+  if (tm == 16)
     hipLaunchKernelGGL((lora_expand_kernel<XT, YT, INLINE, 1>), ge, dim3(256), lds, st, a, plan, tm, slices, v);
   else
     hipLaunchKernelGGL((lora_expand_kernel<XT, YT, INLINE, 2>), ge, dim3(256), lds, st, a, plan, tm, slices, v);
@@ -756,11 +762,11 @@ hipError_t launch(const LoraArgs& a, const Plan& plan, float* v, hipStream_t st)
 
 size_t lora_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_t r, int64_t slots) {
   (void)n;
-  return (size_t)(plan_bytes(m, slots, item_rows(m)) + round256(slices_of(m, k, r, slots) * m * r * 4));
+  return (size_t)(plan_bytes(m, slots, item_rows(m, slots)) + round256(slices_of(m, k, r, slots) * m * r * 4));
 }
 
 hipError_t launch_lora_accumulate(const LoraArgs& a, void* ws, hipStream_t st) {
-  const int tm = item_rows(a.m);
+  const int tm = item_rows(a.m, a.slots);
   char* base = static_cast<char*>(ws);
   float* v = reinterpret_cast<float*>(base + plan_bytes(a.m, a.slots, tm));
   Plan plan = {};
@@ -774,7 +780,8 @@ hipError_t launch_lora_accumulate(const LoraArgs& a, void* ws, hipStream_t st) {
   }
   plan.items_used = reinterpret_cast<int*>(base);
   plan.items = reinterpret_cast<Item*>(base + 256);
-  plan.rows = reinterpret_cast<int*>(base + 256 + round256(max_items(a.m, a.slots, tm) * 16));
+  plan.most = (int)max_items(a.m, a.slots, tm);
+  plan.rows = reinterpret_cast<int*>(base + 256 + (int64_t)plan.most * 16);
   hipLaunchKernelGGL(lora_plan_kernel, dim3(1), dim3(1024), 0, st, a, plan, tm,
                      reinterpret_cast<int*>(v));
   const hipError_t e = hipGetLastError();
