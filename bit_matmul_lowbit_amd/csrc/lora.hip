@@ -259,16 +259,16 @@ __device__ __forceinline__ f32x4 shrink16(const LoraArgs& a, int slot, int rank,
       aoff[t][h] = (uint32_t)(j < rank ? j : rank - 1) * (uint32_t)a.k;
     }
   const int k = (int)a.k, steps = (k + 63) / 64;
-  const int per = (steps + parts - 1) / parts;
-  const int s0 = part * per;
-  const int s1 = s0 + per < steps ? s0 + per : steps;
+  // steps part, part + parts, ...: the waves that run together read
+  // neighbouring 128 bytes
+  const int mine = part < steps ? (steps - part + parts - 1) / parts : 0;
 
   f32x4 acc[RT];
 #pragma unroll
   for (int t = 0; t < RT; ++t) acc[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
   uint4 in[U][T][2];
-  auto load = [&](int u, int s) __attribute__((always_inline)) {
-    int at = s * 64 + lp * 8;
+  auto load = [&](int u, int i) __attribute__((always_inline)) {
+    int at = (part + i * parts) * 64 + lp * 8;
     at = at < k ? at : k - 8;  // pieces past k are zeroed below
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -280,12 +280,13 @@ __device__ __forceinline__ f32x4 shrink16(const LoraArgs& a, int slot, int rank,
   };
 #pragma unroll
   for (int u = 0; u < U; ++u)
-    if (s0 + u < s1) load(u, s0 + u);
-  for (int s = s0; s < s1; s += U) {
+    if (u < mine) load(u, u);
+  for (int i = 0; i < mine; i += U) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (s + u < s1) {
-        if ((s + u) * 64 + 64 > k && (s + u) * 64 + lp * 8 >= k) {
+      if (i + u < mine) {
+        const int s = part + (i + u) * parts;
+        if (s * 64 + 64 > k && s * 64 + lp * 8 >= k) {
 #pragma unroll
           for (int t = 0; t < T; ++t) in[u][t][0] = in[u][t][1] = make_uint4(0, 0, 0, 0);
         }
@@ -304,7 +305,7 @@ __device__ __forceinline__ f32x4 shrink16(const LoraArgs& a, int slot, int rank,
           for (int t = 0; t < RT; ++t)
             acc[t] = Mma<XT>::run(stage[wave][1 + t][c][(w * 4 + q) ^ (c & 7)], b, acc[t]);
         }
-        if (s + U + u < s1) load(u, s + U + u);
+        if (i + U + u < mine) load(u, i + U + u);
       }
     }
   }
