@@ -231,11 +231,17 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(NormArgs a) {
       widen<SR>(rr[n], a.r_type, v[n]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[n][j] += a.scale * u[n][j];
-      if (a.r_out && c < k) store8(a.r_out, a.r_type, i * a.ldro, c, k, v[n]);
     }
   } else {
 #pragma unroll
     for (int n = 0; n < NV; ++n) widen<SR>(rr[n], a.r_type, v[n]);
+  }
+  if (a.r_out) {
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+      const int c = (n * threads + t) * 8;
+      if (c < k) store8(a.r_out, a.r_type, i * a.ldro, c, k, v[n]);
+    }
   }
   if (!a.x_out) return;
   float mean = 0.0f, rs = 1.0f;

@@ -252,3 +252,60 @@ def test_graph_replays_with_growing_lengths():
         _same(out, want)
         _same(idx, widx)
         _same(val, wval)
+
+
+def test_offsets_past_32_bits():
+    import torch
+
+    n, ld = 5003, (1 << 28) + 3  # 20 rows: 5.4e9 logits, 21 GB
+    d = _case(20, n, 64, 5, True, 41)
+    want, widx, wval, _ = plain64.logits_process(**d)
+    wide = torch.empty(20, ld, device="cuda")
+    y = wide[:, 77:77 + n]
+    y.copy_(_dev(d["y"]))
+    _, idx, val = _run(d, y=y, out=y)
+    _same(y, want)
+    _same(idx, widx)
+    _same(val, wval)
+
+
+@pytest.mark.parametrize("b", [3, 40])
+def test_more_biases_than_threads_and_than_lds_holds(b):
+    """Long lists of biases: later entries are not kept by a thread, and past
+    256 in one part the list itself is searched."""
+    import torch
+
+    n = 20000
+    for nbias, top in ((1500, n), (700, 900), (3000, 3000)):
+        g = np.random.default_rng(nbias)
+        d = _case(b, n, 50, nbias, True, nbias)
+        d["bias_ids"] = g.integers(0, top, (b, nbias)).astype(np.int32)
+        d["bias_len"][:] = nbias
+        out = torch.empty((b, n), dtype=torch.float32, device="cuda")
+        _, idx, val = _run(d, out=out)
+        want, widx, wval, _ = plain64.logits_process(**d)
+        _same(out, want)
+        _same(idx, widx)
+        _same(val, wval)
+
+
+@pytest.mark.parametrize("b,n", [(64, 151936), (400, 20001), (70, 60000)])
+def test_long_lists_of_tokens(b, n):
+    """The large parts: lists of 16384 tokens and more."""
+    import torch
+
+    g = np.random.default_rng(b)
+    hist = 16500
+    d = dict(y=(g.integers(-40, 41, (b, n)) / 8).astype(np.float32),
+             tokens=(g.random((b, hist)) ** 4 * n).astype(np.int32),
+             total_len=g.integers(0, hist + 1, b).astype(np.int32), repetition=np.full(b, 2.0, np.float32),
+             frequency=np.full(b, 0.25, np.float32), presence=np.full(b, 0.5, np.float32))
+    d["prompt_len"] = (d["total_len"] // 2).astype(np.int32)
+    rows = g.choice(b, 4, replace=False)
+    out = torch.empty((b, n), dtype=torch.float32, device="cuda")
+    _, idx, val = _run(d, out=out)
+    want, widx, wval, _ = plain64.logits_process(**{k: v[rows] for k, v in d.items()})
+    _same(out[rows], want)
+    _same(idx[rows], widx)
+    _same(val[rows], wval)
+    assert torch.equal(idx.long(), out.max(dim=1).indices) or torch.equal(out.max(dim=1).values, val)

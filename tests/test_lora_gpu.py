@@ -52,7 +52,10 @@ def _check(got, want, bound):
 
 SHAPES = [(1, 128, 1, 8, 1), (1, 2048, 6144, 16, 8), (8, 1280, 700, 64, 16), (3, 8, 17, 8, 2), (16, 5120, 130, 24, 3),
           (17, 136, 1000, 40, 5), (64, 384, 515, 128, 70), (65, 640, 333, 16, 4), (200, 2176, 257, 40, 24),
-          (7, 17408, 64, 256, 2), (300, 256, 1025, 32, 300), (1030, 128, 96, 8, 3)]
+          (7, 17408, 64, 256, 2), (300, 256, 1025, 32, 300), (1030, 128, 96, 8, 3),
+          # one launch with 32 and 64 ranks; several items of one adapter; more rows than a plan keeps in registers
+          (9, 512, 300, 32, 4), (12, 256, 700, 64, 5), (16, 640, 129, 48, 16), (40, 384, 300, 128, 3),
+          (64, 256, 100, 16, 1), (5000, 64, 40, 8, 2), (9000, 8, 16, 8, 700)]
 
 
 @pytest.mark.parametrize("m,k,n,r,slots", SHAPES)
@@ -198,3 +201,33 @@ def test_guards_graph_and_stream(m):
     y[:m] = y0
     graph.replay()
     _check(y[:m], *_want(d, y0.cpu().double().numpy(), "f32"))
+
+
+def test_offsets_past_32_bits():
+    import torch
+
+    m, k, n, ld = 70, 128, 300, (1 << 26) + 64  # 70 rows: 4.7e9 elements, 9.4 GB
+    d = _case(m, k, n, 16, 3, "bf16", "bf16", seed=40)
+    y0 = d["y"].cpu().double().numpy()
+    want = _want(d, y0, "bf16")
+    wide = torch.empty(m, ld, dtype=torch.bfloat16, device="cuda")
+    wide[:, 5:5 + n] = d["y"]
+    wide[:, ld - 200:ld - 72] = d["x"]
+    d["y"], d["x"] = wide[:, 5:5 + n], wide[:, ld - 200:ld - 72]
+    _check(lowbit.lowbit_lora_accumulate(**d), *want)
+
+
+def test_two_streams_with_their_own_workspaces():
+    import torch
+
+    cases = [_case(m, 1280, 3000, 32, 9, "f16", "f32", seed=m) for m in (8, 200)]
+    wants = [_want(d, d["y"].cpu().double().numpy(), "f32") for d in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for d, s in zip(cases, streams):
+        with torch.cuda.stream(s):
+            lowbit.lowbit_lora_accumulate(**d)
+    torch.cuda.synchronize()
+    for d, want in zip(cases, wants):
+        _check(d["y"], *want)

@@ -215,3 +215,34 @@ def test_graph_and_stream():
         graph.replay()
         torch.cuda.synchronize()
         _check(d, r_out, x_out)
+
+
+def test_offsets_past_32_bits():
+    import torch
+
+    m, k, ld = 40, 1280, (1 << 27) + 8  # 40 rows: 5.4e9 elements, 10.7 GB
+    d = _case(m, k, "f16", "f16", "f16", "rms", "layer", "channel", 15)
+    wide = torch.empty(m, ld, dtype=torch.float16, device="cuda")
+    places = {"y": 8, "r": 1 << 20, "x": ld - k - 1}
+    y, r, x = (wide[:, o:o + k] for o in places.values())
+    y.copy_(d["y"][0])
+    r.copy_(d["r"][0])
+    got = _call(d, y=y, r=r, x_out=x)
+    _check(d, *got)
+
+
+@pytest.mark.parametrize("k", [640, 40000])
+def test_c_interface_copies_the_residual_without_y(k):
+    """y NULL: r' is r, and goes to r_out where that is given."""
+    import torch
+
+    r = torch.randn(3, k, device="cuda")
+    r_out = torch.full_like(r, 7.0)
+    x = torch.empty(3, k, dtype=torch.float16, device="cuda")
+    args = (None, 0, 0, r.data_ptr(), 1, k, r_out.data_ptr(), k, x.data_ptr(), 2, k, 3, k, 0, None, None, None, 0, 0, 1.0,
+            1, None, None, 1e-6, torch.cuda.current_stream().cuda_stream)
+    assert lowbit.load().lowbit_norm_residual(*args) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(r_out, r)
+    want = plain64.norm(r.cpu().double().numpy(), "rms")
+    assert (np.abs(x.cpu().double().numpy() - want) <= plain64.rounding(want, "float16") + 1e-5).all()
