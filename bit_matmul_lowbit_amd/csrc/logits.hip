@@ -12,6 +12,13 @@
 // part reads the row's tokens, which come from the cache.  The few tokens
 // with a bias are left out of that pass and taken one by one after it, so
 // that the pass itself holds no table of biases.
+//
+// What bounds it.  Large calls: the logits read and written, and the tokens,
+// read once by every part.  64 x 151936 with lists of up to 32768, 300 biases, a
+// mask, logits written: 29.9 us and 4 to 5 for the rows' ends (86 MB of logits,
+// mask and lists; without tokens 24 in all, without biases too 20).  Small calls:
+// a launch and the latencies of lengths, tokens and logits: 1 x 151936, the token
+// alone, 4.7 + 1.7 us; 8 x 151936 with everything 9.4 + 2.6 us.
 #include "argmax.h"
 #include "common.h"
 
