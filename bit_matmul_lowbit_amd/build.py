@@ -1,14 +1,17 @@
-"""Build liblowbit.so (HIP, gfx950) in-tree with hipcc.
+"""Build liblowbit.so (HIP, gfx950) in-tree with hipcc, and the Python
+binding's argument module (_marshal.so, host code against torch's headers)
+with g++.
 
 Run ``python -m bit_matmul_lowbit_amd.build`` or call ``build()``.  Every call
-recompiles.  The library is placed next to this file so that it travels with
-the source tree.
+recompiles.  Both are placed next to this file so that they travel with the
+source tree.
 """
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -30,17 +33,39 @@ FLAGS = [
 ]
 
 
-def build(verbose: bool = False) -> str:
-    srcs = [os.path.join(CSRC, s) for s in SOURCES]
-    tmp = LIB + ".tmp"
-    cmd = [HIPCC, *FLAGS, "-I", os.path.join(ROOT, "include"), "-o", tmp, *srcs]
+MARSHAL = os.path.join(HERE, "_marshal.so")
+CXX = os.environ.get("CXX", "g++")
+
+
+def _run(cmd, out: str, verbose: bool) -> None:
+    """Run a compiler that writes out + ".tmp", and move that to `out`."""
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError("hipcc failed building liblowbit.so")
-    os.replace(tmp, LIB)
+        raise RuntimeError(f"{cmd[0]} failed building {os.path.basename(out)}")
+    os.replace(out + ".tmp", out)
+
+
+def build_marshal(verbose: bool = False) -> str:
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    inc, lib = os.path.join(root, "include"), os.path.join(root, "lib")
+    # the torch libraries are found by their names, being loaded by then
+    _run([CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", inc,
+          "-I", os.path.join(inc, "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"],
+          "-o", MARSHAL + ".tmp", os.path.join(CSRC, "marshal.cpp"), "-L", lib, "-ltorch_python", "-ltorch_cpu",
+          "-lc10"], MARSHAL, verbose)
+    return MARSHAL
+
+
+def build(verbose: bool = False) -> str:
+    build_marshal(verbose)
+    srcs = [os.path.join(CSRC, s) for s in SOURCES]
+    _run([HIPCC, *FLAGS, "-I", os.path.join(ROOT, "include"), "-o", LIB + ".tmp", *srcs], LIB, verbose)
     return LIB
 
 

@@ -552,96 +552,27 @@ def lowbit_base3_to_t2(b3, scales_rm, n: int, k: int, codes=None, scales=None, s
 # ---------------------------------------------------------------------------
 # operators beside the products.  They take row strides and run on the device
 # their tensors are on (also when it is not the current one).  A decode step
-# makes many such calls, so the checks are written for few attribute reads: the
-# common case passes one condition, and what fails it is named afterwards.
+# makes many such calls, so the checks of a tensor are one call of the compiled
+# module _marshal each.
 
-_types = {}      # torch dtype -> lowbit_type
-_torch = _raw_stream = _current_device = _f32 = _i32 = None
+_F32, _I32, _U8 = 1, 4, 5  # its type codes
+_torch = _m = _raw_stream = _current_device = None
 
 
 def _first_use():
-    """Import torch and fill the tables (importing this module loads nothing)."""
-    global _torch, _raw_stream, _current_device, _f32, _i32
+    """Load torch, the library and the argument module (importing this module
+    loads nothing)."""
+    global _torch, _m, _raw_stream, _current_device
     import torch
 
     load()
-    _types.update({torch.float32: 1, torch.float16: 2, torch.bfloat16: 3})
+    try:
+        from . import _marshal
+    except ImportError as e:
+        raise RuntimeError("bit_matmul_lowbit_amd/_marshal.so is missing or does not fit this torch: build it with "
+                           "`python -m bit_matmul_lowbit_amd.build` (or __graft_entry__.build())") from e
     _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-    _f32, _i32 = torch.float32, torch.int32
-    _torch = torch
-
-
-def _float_rows(t, shape, dev, name):
-    """(pointer, type code, row stride) of a device tensor [m][k] (or [k], one
-    row) of FP32 / FP16 / BF16 with contiguous rows."""
-    code = _types.get(t.dtype)
-    if t.dim() == 2:
-        ld, unit = t.stride()
-        if code and unit == 1 and t.shape == shape and t.get_device() == dev:
-            return t.data_ptr(), code, ld if shape[0] > 1 else shape[1]
-        got = tuple(t.shape)
-    else:
-        unit = t.stride(-1) if t.dim() else 1
-        got = (1,) + tuple(t.shape)
-    if code is None:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected float32, float16 or bfloat16")
-    if not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
-    if got != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if unit != 1 and shape[1] != 1:
-        raise ValueError(f"{name}: the elements of a row must be contiguous")
-    ld = t.stride(0) if t.dim() == 2 else shape[1]
-    return t.data_ptr(), code, ld if shape[0] > 1 else shape[1]
-
-
-def _shape2(t, name):
-    """Shape of t as (rows, columns); its device index."""
-    dev = t.get_device()
-    if dev < 0:
-        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
-    shape = t.shape
-    if len(shape) == 1:
-        shape = (1, shape[0])
-    elif len(shape) != 2:
-        raise ValueError(f"{name} must have one or two dimensions")
-    return shape, dev
-
-
-def _vector(t, dtype, count, name, dev):
-    """Pointer of a contiguous device tensor of at least `count` elements."""
-    if t.dtype is dtype and t.get_device() == dev and t.numel() >= count and t.is_contiguous():
-        return t.data_ptr()
-    if t.dtype != dtype or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA (HIP) tensor of {dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    raise ValueError(f"{name} holds {t.numel()} elements, needs at least {count}")
-
-
-def _lists(t, dtype, b, name, dev):
-    """(pointer, columns, row stride) of a [b][columns] device tensor with
-    contiguous rows (any number of them for b None)."""
-    if t.dtype is dtype and t.dim() == 2 and t.get_device() == dev:
-        rows, cols = t.shape
-        ld, unit = t.stride()
-        if unit == 1 and (b is None or rows == b):
-            return t.data_ptr(), cols, ld if rows > 1 else max(ld, cols)
-    if t.dtype != dtype or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA (HIP) tensor of {dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
-    if t.dim() != 2 or (b is not None and t.shape[0] != b):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {b} rows")
-    rows, cols = t.shape
-    ld, unit = t.stride()
-    if unit != 1 and cols > 1:
-        raise ValueError(f"{name}: the elements of a row must be contiguous")
-    return t.data_ptr(), cols, ld if rows > 1 else max(ld, cols)
+    _torch, _m = torch, _marshal
 
 
 def _call(where, dev, stream, args, made=()):
@@ -678,23 +609,23 @@ def lowbit_norm_residual(y, r, post="none", post_w=None, post_b=None, gate=None,
     allocated with x_dtype (FP16, as lowbit_gemv reads it, if not given)."""
     if _torch is None:
         _first_use()
-    shape, dev = _shape2(r, "r")
-    m, k = shape
-    rp, rt, ldr = _float_rows(r, shape, dev, "r")
+    rows, vector = _m.rows, _m.vector
+    m, k, dev = _m.shape("r", r)
+    rp, rt, ldr = rows("r", r, m, k, dev)
     yp = yt = ldy = gp = gt = ldg = rop = ldro = xp = xt = ldx = post_c = pre_c = 0
     made = ()
     if y is not None:
         post_c = NORMS[post]
-        yp, yt, ldy = _float_rows(y, shape, dev, "y")
+        yp, yt, ldy = rows("y", y, m, k, dev)
         if gate is not None:
             if gate.dim() == 1:
-                gp, gt, _ = _float_rows(gate, (1, k), dev, "gate")
+                gp, gt, _ = rows("gate", gate, 1, k, dev)
             else:
-                gp, gt, ldg = _float_rows(gate, shape, dev, "gate")
+                gp, gt, ldg = rows("gate", gate, m, k, dev)
         if r_out is None:
             r_out, rop, ldro = r, rp, ldr
         else:
-            rop, rot, ldro = _float_rows(r_out, shape, dev, "r_out")
+            rop, rot, ldro = rows("r_out", r_out, m, k, dev)
             if rot != rt:
                 raise TypeError("r_out must have the type of r")
     elif r_out is not None:
@@ -704,17 +635,13 @@ def lowbit_norm_residual(y, r, post="none", post_w=None, post_b=None, gate=None,
         if x_out is None:
             x_out = _torch.empty(r.shape, dtype=x_dtype or _torch.float16, device=r.device)
             made = (x_out,)
-        xp, xt, ldx = _float_rows(x_out, shape, dev, "x_out")
+        xp, xt, ldx = rows("x_out", x_out, m, k, dev)
     elif x_out is not None:
         raise ValueError("x_out needs pre")
     _call("lowbit_norm_residual", dev, stream,
           (yp, yt, ldy, rp, rt, ldr, rop, ldro, xp, xt, ldx, m, k, post_c,
-           None if post_w is None else _vector(post_w, _f32, k, "post_w", dev),
-           None if post_b is None else _vector(post_b, _f32, k, "post_b", dev),
-           gp, gt, ldg, scale, pre_c,
-           None if pre_w is None else _vector(pre_w, _f32, k, "pre_w", dev),
-           None if pre_b is None else _vector(pre_b, _f32, k, "pre_b", dev),
-           eps), made)
+           vector("post_w", post_w, _F32, k, dev), vector("post_b", post_b, _F32, k, dev), gp, gt, ldg, scale,
+           pre_c, vector("pre_w", pre_w, _F32, k, dev), vector("pre_b", pre_b, _F32, k, dev), eps), made)
     return (r_out if y is not None else r), x_out
 
 
@@ -737,28 +664,23 @@ def lowbit_logits_process(y, tokens=None, prompt_len=None, total_len=None, repet
     mask_row int32 [b]."""
     if _torch is None:
         _first_use()
-    shape, dev = _shape2(y, "y")
-    b, n = shape
-    yp, yt, ldy = _float_rows(y, shape, dev, "y")
-    tp, tcap, ldt = _lists(tokens, _i32, b, "tokens", dev) if tokens is not None else (None, 0, 0)
-    bp = bv = None
-    bcap = ldb = 0
-    if bias_ids is not None or bias_vals is not None:
-        if bias_ids is None or bias_vals is None:
-            raise ValueError("bias_ids and bias_vals go together")
-        bp, bcap, ldb = _lists(bias_ids, _i32, b, "bias_ids", dev)
-        bv, bvcap, ldbv = _lists(bias_vals, _f32, b, "bias_vals", dev)
-        if bcap != bvcap or ldb != ldbv:
-            raise ValueError("bias_ids and bias_vals must have one shape and row stride")
-    mp, rows, ldm = None, 0, 0
-    if mask is not None:
-        mp, words, ldm = _lists(mask, _i32, None if mask_row is not None else b, "mask", dev)
-        rows = mask.shape[0]
+    rows, vector, lists = _m.rows, _m.vector, _m.lists
+    b, n, dev = _m.shape("y", y)
+    yp, yt, ldy = rows("y", y, b, n, dev)
+    tp, tcap, ldt = lists("tokens", tokens, _I32, b, dev)
+    bp, bcap, ldb = lists("bias_ids", bias_ids, _I32, b, dev)
+    bv, bvcap, ldbv = lists("bias_vals", bias_vals, _F32, b, dev)
+    if (bp is None) != (bv is None) or bcap != bvcap or ldb != ldbv:
+        raise ValueError("bias_ids and bias_vals go together, with one shape and row stride")
+    mp, words, ldm = lists("mask", mask, _I32, b if mask_row is None else -1, dev)
+    mask_rows = 0
+    if mp is not None:
+        mask_rows = mask.shape[0]
         if words < (n + 31) // 32:
             raise ValueError(f"mask has {words} words a row, needs {(n + 31) // 32}")
     op = ldo = 0
     if out is not None:
-        op, ot, ldo = _float_rows(out, shape, dev, "out")
+        op, ot, ldo = rows("out", out, b, n, dev)
         if ot != 1:
             raise TypeError("out must be float32")
     ip = vp = wp = None
@@ -766,31 +688,26 @@ def lowbit_logits_process(y, tokens=None, prompt_len=None, total_len=None, repet
     made = ()
     if top1:
         if idx is None:
-            idx = _torch.empty(b, dtype=_i32, device=y.device)
+            idx = _torch.empty(b, dtype=_torch.int32, device=y.device)
             made += (idx,)
         if val is None:
-            val = _torch.empty(b, dtype=_f32, device=y.device)
+            val = _torch.empty(b, dtype=_torch.float32, device=y.device)
             made += (val,)
         if workspace is None:
             need = lowbit_logits_workspace_bytes(n, b)
             workspace = _torch.empty(max(need, 16), dtype=_torch.uint8, device=y.device)
             made += (workspace,)
-        ip, vp = _vector(idx, _i32, b, "idx", dev), _vector(val, _f32, b, "val", dev)
-        wp, need = _vector(workspace, _torch.uint8, 0, "workspace", dev), workspace.numel()
+        ip, vp = vector("idx", idx, _I32, b, dev), vector("val", val, _F32, b, dev)
+        wp, need = vector("workspace", workspace, _U8, 0, dev), workspace.numel()
     elif idx is not None or val is not None:
         raise ValueError("idx and val need top1")
     _call("lowbit_logits_process", dev, stream,
           (yp, yt, ldy, n, b, tp, tcap, ldt,
-           None if prompt_len is None else _vector(prompt_len, _i32, b, "prompt_len", dev),
-           None if total_len is None else _vector(total_len, _i32, b, "total_len", dev),
-           None if repetition is None else _vector(repetition, _f32, b, "repetition", dev),
-           None if frequency is None else _vector(frequency, _f32, b, "frequency", dev),
-           None if presence is None else _vector(presence, _f32, b, "presence", dev),
-           bp, bv, bcap, ldb,
-           None if bias_len is None else _vector(bias_len, _i32, b, "bias_len", dev),
-           mp, rows, ldm,
-           None if mask_row is None else _vector(mask_row, _i32, b, "mask_row", dev),
-           op, ldo, ip, vp, wp, need), made)
+           vector("prompt_len", prompt_len, _I32, b, dev), vector("total_len", total_len, _I32, b, dev),
+           vector("repetition", repetition, _F32, b, dev), vector("frequency", frequency, _F32, b, dev),
+           vector("presence", presence, _F32, b, dev), bp, bv, bcap, ldb,
+           vector("bias_len", bias_len, _I32, b, dev), mp, mask_rows, ldm,
+           vector("mask_row", mask_row, _I32, b, dev), op, ldo, ip, vp, wp, need), made)
     return out, idx, val
 
 
@@ -807,26 +724,25 @@ def lowbit_lora_accumulate(x, ids, a, b, y, ranks=None, scales=None, workspace=N
     strided (a slice of a fused projection's output)."""
     if _torch is None:
         _first_use()
-    shape, dev = _shape2(x, "x")
-    m, k = shape
-    xp, xt, ldx = _float_rows(x, shape, dev, "x")
+    rows, vector = _m.rows, _m.vector
+    m, k, dev = _m.shape("x", x)
+    xp, xt, ldx = rows("x", x, m, k, dev)
     if a.dim() != 3 or b.dim() != 3:
         raise ValueError("a must be [slots][r][k] and b [slots][n][r]")
     slots, n, r = b.shape
     if a.shape != (slots, r, k):
         raise ValueError(f"a {tuple(a.shape)} does not fit x {tuple(x.shape)} and b {tuple(b.shape)}")
-    yp, yt, ldy = _float_rows(y, (m, n), dev, "y")
+    yp, yt, ldy = rows("y", y, m, n, dev)
     made = ()
     if workspace is None:
         need = lowbit_lora_workspace_bytes(m, n, k, r, slots)
         workspace = _torch.empty(max(need, 16), dtype=_torch.uint8, device=x.device)
         made = (workspace,)
     _call("lowbit_lora_accumulate", dev, stream,
-          (xp, xt, ldx, _vector(ids, _i32, m, "ids", dev), m, n, k, r, slots,
-           _vector(a, x.dtype, 0, "a", dev), _vector(b, x.dtype, 0, "b", dev),
-           None if ranks is None else _vector(ranks, _i32, slots, "ranks", dev),
-           None if scales is None else _vector(scales, _f32, slots, "scales", dev),
-           yp, yt, ldy, _vector(workspace, _torch.uint8, 0, "workspace", dev), workspace.numel()), made)
+          (xp, xt, ldx, vector("ids", ids, _I32, m, dev), m, n, k, r, slots,
+           vector("a", a, xt, 0, dev), vector("b", b, xt, 0, dev),
+           vector("ranks", ranks, _I32, slots, dev), vector("scales", scales, _F32, slots, dev),
+           yp, yt, ldy, vector("workspace", workspace, _U8, 0, dev), workspace.numel()), made)
     return y
 
 

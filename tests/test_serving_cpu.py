@@ -101,6 +101,22 @@ def test_binding_rejects_host_tensors_and_wrong_types():
         lowbit.lowbit_norm_residual(None, torch.zeros(2, 128, dtype=torch.int32), pre="rms")
     with pytest.raises(TypeError):
         lowbit.lowbit_logits_process(torch.zeros(2, 100))
+    with pytest.raises(TypeError, match="not list"):
+        lowbit.lowbit_logits_process([1.0, 2.0])
     with pytest.raises(TypeError):
         lowbit.lowbit_lora_accumulate(x, torch.zeros(2, dtype=torch.int32), torch.zeros(1, 8, 128), torch.zeros(1, 4, 8),
                                       torch.zeros(2, 4))
+
+
+def test_argument_module_counts_its_arguments():
+    from bit_matmul_lowbit_amd import _marshal
+
+    for f in (_marshal.shape, _marshal.rows, _marshal.vector, _marshal.lists):
+        with pytest.raises(TypeError, match="expected"):
+            f("name")
+    assert _marshal.vector("name", None, 1, 5, 0) is None
+    assert _marshal.lists("name", None, 4, 5, 0) == (None, 0, 0)
+    with pytest.raises(TypeError):
+        _marshal.rows("name", None, 1, 1, 0)
+    with pytest.raises(TypeError):
+        _marshal.vector("name", 5, "f32", 1, 0)
