@@ -27,13 +27,27 @@ __device__ __forceinline__ uint64_t argmax_key(float v, int64_t i) {
   return argmax_pack(ordered_bits(v), i);
 }
 
+// One step of wave_max: the larger of the own key and the one that the DPP
+// control brings from another lane (0, below every key, where it brings none).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint64_t dpp_max(uint64_t k) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)k, CTRL, ROWS, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(k >> 32), CTRL, ROWS, 0xF, false);
+  const uint64_t o = ((uint64_t)hi << 32) | lo;
+  return o > k ? o : k;
+}
+
+// largest key of the wave, in every lane
 __device__ __forceinline__ uint64_t wave_max(uint64_t k) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) {
-    const uint64_t o = __shfl_xor(k, off, 64);
-    k = o > k ? o : k;
-  }
-  return k;
+  k = dpp_max<0x111, 0xF>(k);  // row_shr:1
+  k = dpp_max<0x112, 0xF>(k);  // row_shr:2
+  k = dpp_max<0x114, 0xF>(k);  // row_shr:4
+  k = dpp_max<0x118, 0xF>(k);  // row_shr:8: lane 15 of each row of 16 has the row's
+  k = dpp_max<0x142, 0xA>(k);  // row_bcast:15 into rows 1 and 3
+  k = dpp_max<0x143, 0xC>(k);  // row_bcast:31 into rows 2 and 3: lane 63 has the wave's
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)k, 63);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(k >> 32), 63);
+  return ((uint64_t)hi << 32) | lo;
 }
 
 // block-wide maximum of one key per thread (256 threads)

@@ -235,7 +235,7 @@ __global__ __launch_bounds__(1024) void lora_plan_kernel(LoraArgs a, Plan plan, 
 // piece p of row i at p ^ (i & 7) (the lanes of a read then fall into
 // different banks); afterwards the waves' sums.  The call ends with reads of
 // it.
-template <int XT, int RT>
+template <int XT, int RT, int WAVES>
 __device__ __forceinline__ f32x4 shrink16(const LoraArgs& a, int slot, int rank, int r0, const int* rows,
                                           int here, uint4 (*stage)[1 + RT][16][8], int part, int parts) {
   constexpr int T = 1 + RT;                          // 16-row tiles of a step: x, then A's
@@ -317,7 +317,8 @@ __device__ __forceinline__ f32x4 shrink16(const LoraArgs& a, int slot, int rank,
   f32x4 sum = (f32x4){0.f, 0.f, 0.f, 0.f};
   if (wave < RT) {
     sum = red[0][wave][lane];
-    for (int w = 1; w < (int)blockDim.x >> 6; ++w) sum += red[w][wave][lane];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) sum += red[w][wave][lane];
   }
   return sum;
 }
@@ -336,7 +337,7 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs a, Plan plan,
   const int rank = it.rank, r0 = (int)blockIdx.y * RT * 16;
   if (r0 >= rank) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const f32x4 sum = shrink16<XT, RT>(a, it.slot, rank, r0, rows + sub * 16, here, stage,
+  const f32x4 sum = shrink16<XT, RT, kShrinkWaves>(a, it.slot, rank, r0, rows + sub * 16, here, stage,
                                      (int)blockIdx.z * kShrinkWaves + wave, kShrinkWaves * (int)gridDim.z);
   const int c = threadIdx.x & 15, j = r0 + wave * 16 + ((threadIdx.x >> 4) & 3) * 4;
   // j .. j + 3 lie in the row (r is a multiple of 8); what is past the rank is not read
@@ -359,12 +360,13 @@ __device__ __forceinline__ void split(float v, float, bf16_t (&p)[3]) {
   p[2] = (bf16_t)(rest - (float)p[1]);
 }
 
-// largest of 16 consecutive lanes
-__device__ __forceinline__ float max16(float v) {
-#pragma unroll
-  for (int off = 8; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, 64));
-  return v;
+// largest of 16 consecutive lanes, in each of them
+template <int ROR>
+__device__ __forceinline__ float max_ror(float v) {
+  return fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x120 + ROR,
+                                                                        0xF, 0xF, true)));
 }
+__device__ __forceinline__ float max16(float v) { return max_ror<1>(max_ror<2>(max_ror<4>(max_ror<8>(v)))); }
 
 // largest magnitude of the finite ones of four values
 __device__ __forceinline__ float finite_max(f32x4 v) {
@@ -653,7 +655,7 @@ __global__ __launch_bounds__(512) void lora_small_kernel(LoraArgs a) {
   if (!it.count) return;
   auto first = [&]() __attribute__((always_inline)) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const f32x4 sum = shrink16<XT, RT>(a, it.slot, it.rank, 0, rows, it.count, stage, wave, kWaves);
+    const f32x4 sum = shrink16<XT, RT, kWaves>(a, it.slot, it.rank, 0, rows, it.count, stage, wave, kWaves);
     if (wave < RT)
       *reinterpret_cast<f32x4*>(&inner_v[threadIdx.x & 15][wave * 16 + ((threadIdx.x >> 4) & 3) * 4]) = sum;
     __syncthreads();
