@@ -9,9 +9,9 @@
 // Rows are grouped by adapter, so that an adapter's matrices meet all of its
 // rows at once.  An item is up to 32 rows of one adapter (16 where adapters
 // have few rows).
-// With m <= 64 every work-group finds its item itself: the ids of all rows
-// fit one wave, and ballots pick out the rows that share one (no launch, no
-// memory).  More rows are sorted by one work-group first (lora_plan_kernel).
+// Up to 64 rows, a lane to a row, are grouped by the first wave of every
+// work-group for itself (no launch, no memory); more are sorted by one
+// work-group first (lora_plan_kernel).
 //
 // Both products run on v_mfma_f32_16x16x32.
 //   A operand (16 x 32): lane l holds row l % 16, 8 values at 8 (l / 16)
@@ -41,7 +41,7 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kInlineRows = 64;  // rows whose grouping one wave finds by itself
+constexpr int kInlineRows = 64;  // rows that one wave groups by itself
 constexpr int kItemRows = 32;    // most rows of an item
 constexpr int kShrinkWaves = 8;
 constexpr int kTilesN = 4;                 // 16-output tiles of a wave in expand
@@ -83,8 +83,7 @@ __device__ __forceinline__ int lanes_below(uint64_t mask) {
                                         __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
 }
 
-// What the plan of more than kInlineRows rows holds, at the head of the
-// workspace: the number of items, the items, and their rows, tm places to an
+// What a plan holds, at the head of the workspace: the number of items, the items, and their rows, tm places to an
 // item.  All three are found by the item's number alone, so that they are read
 // in one memory latency.
 struct Item {
@@ -98,46 +97,6 @@ struct Plan {
   int most;  // items there is room for
 };
 
-// Item number `item` (tm rows at most): its count is 0 if there is none; its
-// rows go to rows[0 .. count) (LDS).  Ends in a barrier if there is one.
-template <bool INLINE>
-__device__ __forceinline__ Item find_item(const LoraArgs& a, const Plan& plan, int item, int tm, int* rows) {
-  Item it = {0, 0, 0, 1.0f};
-  if constexpr (INLINE) {
-    const int lane = threadIdx.x & 63;
-    const int s = lane < a.m ? slot_of(a, lane) : -1;
-    uint64_t left = __ballot(s >= 0);
-    int seen = 0;
-    while (left) {
-      const int ls = __builtin_amdgcn_readlane(s, __builtin_ctzll(left));
-      const uint64_t same = __ballot(s == ls);
-      const int n = __popcll(same), parts = (n + tm - 1) / tm;
-      if (item < seen + parts) {
-        const int first = (item - seen) * tm;
-        it.count = n - first < tm ? n - first : tm;
-        it.slot = ls;
-        it.rank = rank_of(a, ls);
-        if (a.scales) it.scale = a.scales[ls];
-        const int at = lanes_below(same) - first;
-        if (threadIdx.x < 64 && ((same >> lane) & 1) && at >= 0 && at < it.count) rows[at] = lane;
-        break;
-      }
-      seen += parts;
-      left &= ~same;
-    }
-  } else if (item < plan.most) {
-    const int used = *plan.items_used;
-    const Item got = plan.items[item];
-    const int row = plan.rows[item * tm + (threadIdx.x & (tm - 1))];
-    if (item < used) {
-      it = got;
-      if ((int)threadIdx.x < it.count) rows[threadIdx.x] = row;
-    }
-  }
-  if (it.count) __syncthreads();
-  return it;
-}
-
 // inclusive prefix sum over the wave's lanes, by DPP
 __device__ __forceinline__ int wave_scan(int v) {
 #define LOWBIT_SCAN(CTRL, ROWS) v += __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false)
@@ -149,6 +108,68 @@ __device__ __forceinline__ int wave_scan(int v) {
   LOWBIT_SCAN(0x143, 0xC);  // row_bcast:31 into rows 2 and 3
 #undef LOWBIT_SCAN
   return v;
+}
+
+// What a work-group shares of its item.
+struct Found {
+  Item it;
+  int rows[kItemRows];
+};
+
+// Item number `item` (tm rows at most), in every thread: its count is 0 if
+// there is none; its rows are in found.rows (LDS).  The call holds a barrier.
+// INLINE: the first wave finds it among up to 64 rows, a lane to a row: a ballot
+// for each bit of the adapters' numbers gives every lane the rows of its own,
+// the first row of each stands for the adapter's items, and a prefix sum
+// numbers them.  (Passing the adapters one by one took up to 0.3 us for each.)
+// Otherwise: from the plan.
+template <bool INLINE>
+__device__ __forceinline__ Item find_item(const LoraArgs& a, const Plan& plan, int item, int tm, Found& found) {
+  if (threadIdx.x < 64) {
+    const int lane = threadIdx.x;
+    Item it = {0, 0, 0, 1.0f};
+    if constexpr (INLINE) {
+      const int m = (int)a.m;
+      const int s = lane < m ? slot_of(a, lane) : -1;
+      uint64_t same = __ballot(s >= 0);  // the rows of this lane's adapter, by the bits of its number
+      for (int bit = 0; bit < 32 - __builtin_clz((int)a.slots | 1); ++bit) {
+        const bool on = (s >> bit) & 1;
+        const uint64_t all_on = __ballot(on);
+        same &= on ? all_on : ~all_on;
+      }
+      const int all = __popcll(same), before = lanes_below(same);
+      const int parts = s >= 0 && before == 0 ? (all + tm - 1) / tm : 0;
+      const int end = wave_scan(parts);
+      const uint64_t hit = __ballot(item < end && item >= end - parts);
+      if (hit) {
+        const int leader = __builtin_ctzll(hit);
+        const int first = (item - __builtin_amdgcn_readlane(end - parts, leader)) * tm;
+        const int left = __builtin_amdgcn_readlane(all, leader) - first;
+        it.slot = __builtin_amdgcn_readlane(s, leader);
+        it.count = left < tm ? left : tm;
+        it.rank = rank_of(a, it.slot);
+        const int at = before - first;
+        if (s == it.slot && at >= 0 && at < it.count) found.rows[at] = lane;
+      }
+    } else if (item < plan.most) {
+      const int used = *plan.items_used;
+      const Item got = plan.items[item];
+      const int row = plan.rows[item * tm + (lane & (tm - 1))];
+      if (item < used) {
+        it = got;
+        if (lane < it.count) found.rows[lane] = row;
+      }
+    }
+    if (lane == 0) found.it = it;
+  }
+  __syncthreads();
+  Item it;
+  it.slot = __builtin_amdgcn_readfirstlane(found.it.slot);
+  it.count = __builtin_amdgcn_readfirstlane(found.it.count);
+  it.rank = __builtin_amdgcn_readfirstlane(found.it.rank);
+  // (asked for here, it is there when v is)
+  it.scale = INLINE ? (a.scales ? a.scales[it.slot] : 1.0f) : found.it.scale;
+  return it;
 }
 
 // Rows sorted by adapter, in one work-group: each row takes the next place
@@ -328,10 +349,11 @@ __device__ __forceinline__ f32x4 shrink16(const LoraArgs& a, int slot, int rank,
 template <int XT, int RT, bool INLINE>
 __global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs a, Plan plan, int tm, int subs,
                                                           float* __restrict__ v) {
-  __shared__ int rows[kItemRows];
+  __shared__ Found found;
+  const int* rows = found.rows;
   __shared__ uint4 stage[kShrinkWaves][1 + RT][16][8];
   const int item = blockIdx.x / subs, sub = blockIdx.x % subs;
-  const Item it = find_item<INLINE>(a, plan, item, tm, rows);
+  const Item it = find_item<INLINE>(a, plan, item, tm, found);
   const int here = it.count - sub * 16 < 16 ? it.count - sub * 16 : 16;
   if (here <= 0) return;
   const int rank = it.rank, r0 = (int)blockIdx.y * RT * 16;
@@ -612,10 +634,11 @@ template <int XT, int YT, bool INLINE, int SUBS>
 __global__ __launch_bounds__(256, SUBS == 1 || YT == 3 ? 3 : 2) void lora_expand_kernel(
     LoraArgs a, Plan plan, int tm, int slices, const float* __restrict__ v) {
   extern __shared__ uint4 dyn[];  // pieces of v: [pieces][tm][pitch]
-  __shared__ int rows[kItemRows];
+  __shared__ Found found;
+  const int* rows = found.rows;
   __shared__ float unscale[kItemRows];
   for (int item = blockIdx.y;; item += gridDim.y) {
-    const Item it = find_item<INLINE>(a, plan, item, tm, rows);
+    const Item it = find_item<INLINE>(a, plan, item, tm, found);
     if (!it.count) return;
     auto inner = [&](int at, int j) __attribute__((always_inline)) {
       const float* vr = v + (int64_t)rows[at] * a.r + j;
@@ -646,12 +669,13 @@ __global__ __launch_bounds__(256, SUBS == 1 || YT == 3 ? 3 : 2) void lora_expand
 template <int XT, int YT, int RT>
 __global__ __launch_bounds__(512) void lora_small_kernel(LoraArgs a) {
   constexpr int kWaves = 8, kPitch = RT * 16 + 4;
-  __shared__ int rows[16];
+  __shared__ Found found;
+  const int* rows = found.rows;
   __shared__ float unscale[16];
   __shared__ uint4 stage[kWaves][1 + RT][16][8];
   __shared__ __align__(16) float inner_v[16][kPitch];
   __shared__ uint4 pieces[Mma<XT>::pieces * 16 * ((RT * 16 + 31) / 32 * 32 + 8) / 8];
-  const Item it = find_item<true>(a, Plan{}, (int)blockIdx.y, 16, rows);
+  const Item it = find_item<true>(a, Plan{}, (int)blockIdx.y, 16, found);
   if (!it.count) return;
   auto first = [&]() __attribute__((always_inline)) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -761,6 +785,12 @@ hipError_t launch(const LoraArgs& a, const Plan& plan, float* v, hipStream_t st)
   return hipGetLastError();
 }
 
+template <bool INLINE>
+hipError_t launch_typed(const LoraArgs& a, const Plan& plan, float* v, hipStream_t st) {
+  if (a.x_type == 2) return launch<2, 1, INLINE>(a, plan, v, st);
+  return a.y_type == 1 ? launch<3, 1, INLINE>(a, plan, v, st) : launch<3, 3, INLINE>(a, plan, v, st);
+}
+
 }  // namespace
 
 size_t lora_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_t r, int64_t slots) {
@@ -777,10 +807,7 @@ hipError_t launch_lora_accumulate(const LoraArgs& a, void* ws, hipStream_t st) {
     if (a.x_type == 2) return launch_small<2, 1>(a, st);
     return a.y_type == 1 ? launch_small<3, 1>(a, st) : launch_small<3, 3>(a, st);
   }
-  if (a.m <= kInlineRows) {
-    if (a.x_type == 2) return launch<2, 1, true>(a, plan, v, st);
-    return a.y_type == 1 ? launch<3, 1, true>(a, plan, v, st) : launch<3, 3, true>(a, plan, v, st);
-  }
+  if (a.m <= kInlineRows) return launch_typed<true>(a, plan, v, st);
   plan.items_used = reinterpret_cast<int*>(base);
   plan.items = reinterpret_cast<Item*>(base + 256);
   plan.most = (int)max_items(a.m, a.slots, tm);
@@ -789,8 +816,7 @@ hipError_t launch_lora_accumulate(const LoraArgs& a, void* ws, hipStream_t st) {
                      reinterpret_cast<int*>(v));
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (a.x_type == 2) return launch<2, 1, false>(a, plan, v, st);
-  return a.y_type == 1 ? launch<3, 1, false>(a, plan, v, st) : launch<3, 3, false>(a, plan, v, st);
+  return launch_typed<false>(a, plan, v, st);
 }
 
 }  // namespace lowbit
