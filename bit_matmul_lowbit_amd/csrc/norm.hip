@@ -14,9 +14,9 @@
 // the registers of a work-group hold are read again for every sum.
 //
 // What bounds it: memory.  16384 x 5120, everything BF16, a norm on both sides:
-// 141 to 149 us for 671 MB (4.5 to 4.75 TB/s; a large copy reaches 4.8).  Small
-// calls are a launch and two or three latencies: 1 x 2048 2.4 us, 8 x 5120 with
-// a gate 4.6 us, 777 x 1283 with layer norms 7.6 us.
+// 141 to 150 us for 671 MB (4.5 to 4.75 TB/s; a large copy reaches 4.8).  Small
+// calls are a launch and two or three latencies: 1 x 2048 2.3 us, 8 x 5120 with
+// a gate 4.5 us, 777 x 1283 with layer norms 7.0 us.
 #include "common.h"
 
 namespace lowbit {
