@@ -572,21 +572,28 @@ def _first_use():
         raise RuntimeError("bit_matmul_lowbit_amd/_marshal.so is missing or does not fit this torch: build it with "
                            "`python -m bit_matmul_lowbit_amd.build` (or __graft_entry__.build())") from e
     _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-    _torch, _m = torch, _marshal
+    _m = _marshal
+    _torch = torch  # last: it says that all of them are there
 
 
-def _call(where, dev, stream, args, made=()):
-    """Call library function `where` on `stream` (default: the current one of
-    device `dev`) with that device current.  `made`: tensors allocated here
-    that the kernels use; the allocator is told when the stream is not the one
-    they belong to."""
-    fn = getattr(_lib, where)
+def _empty(shape, dtype, device, stream):
+    """A tensor made for a call on `stream` (None: the current one).  It is that
+    stream's memory: what the current one freed may still be in use by work
+    that waits there.  The current stream, where the caller reads it, is noted
+    with the allocator."""
     if stream is None:
-        raw = _raw_stream(dev)
-    else:
-        raw = stream.cuda_stream
-        for t in made:
-            t.record_stream(stream)
+        return _torch.empty(shape, dtype=dtype, device=device)
+    with _torch.cuda.stream(stream):
+        t = _torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(_torch.cuda.current_stream(device))
+    return t
+
+
+def _call(where, dev, stream, args):
+    """Call library function `where` on `stream` (default: the current one of
+    device `dev`) with that device current."""
+    fn = getattr(_lib, where)
+    raw = _raw_stream(dev) if stream is None else stream.cuda_stream
     if dev == _current_device():
         status = fn(*args, raw)
     else:
@@ -594,6 +601,11 @@ def _call(where, dev, stream, args, made=()):
             status = fn(*args, raw)
     if status != 0:
         raise LowbitError(status, where)
+
+
+def _same_device(stream, dev):
+    if stream is not None and stream.device_index != dev:
+        raise ValueError(f"stream is one of cuda:{stream.device_index}, expected cuda:{dev}")
 
 
 def lowbit_norm_residual(y, r, post="none", post_w=None, post_b=None, gate=None, scale=1.0,
@@ -611,9 +623,9 @@ def lowbit_norm_residual(y, r, post="none", post_w=None, post_b=None, gate=None,
         _first_use()
     rows, vector = _m.rows, _m.vector
     m, k, dev = _m.shape("r", r)
+    _same_device(stream, dev)
     rp, rt, ldr = rows("r", r, m, k, dev)
     yp = yt = ldy = gp = gt = ldg = rop = ldro = xp = xt = ldx = post_c = pre_c = 0
-    made = ()
     if y is not None:
         post_c = NORMS[post]
         yp, yt, ldy = rows("y", y, m, k, dev)
@@ -633,15 +645,14 @@ def lowbit_norm_residual(y, r, post="none", post_w=None, post_b=None, gate=None,
     if pre is not None:
         pre_c = NORMS[pre]
         if x_out is None:
-            x_out = _torch.empty(r.shape, dtype=x_dtype or _torch.float16, device=r.device)
-            made = (x_out,)
+            x_out = _empty(r.shape, x_dtype or _torch.float16, r.device, stream)
         xp, xt, ldx = rows("x_out", x_out, m, k, dev)
     elif x_out is not None:
         raise ValueError("x_out needs pre")
     _call("lowbit_norm_residual", dev, stream,
           (yp, yt, ldy, rp, rt, ldr, rop, ldro, xp, xt, ldx, m, k, post_c,
            vector("post_w", post_w, _F32, k, dev), vector("post_b", post_b, _F32, k, dev), gp, gt, ldg, scale,
-           pre_c, vector("pre_w", pre_w, _F32, k, dev), vector("pre_b", pre_b, _F32, k, dev), eps), made)
+           pre_c, vector("pre_w", pre_w, _F32, k, dev), vector("pre_b", pre_b, _F32, k, dev), eps))
     return (r_out if y is not None else r), x_out
 
 
@@ -666,6 +677,7 @@ def lowbit_logits_process(y, tokens=None, prompt_len=None, total_len=None, repet
         _first_use()
     rows, vector, lists = _m.rows, _m.vector, _m.lists
     b, n, dev = _m.shape("y", y)
+    _same_device(stream, dev)
     yp, yt, ldy = rows("y", y, b, n, dev)
     tp, tcap, ldt = lists("tokens", tokens, _I32, b, dev)
     bp, bcap, ldb = lists("bias_ids", bias_ids, _I32, b, dev)
@@ -685,18 +697,14 @@ def lowbit_logits_process(y, tokens=None, prompt_len=None, total_len=None, repet
             raise TypeError("out must be float32")
     ip = vp = wp = None
     need = 0
-    made = ()
     if top1:
         if idx is None:
-            idx = _torch.empty(b, dtype=_torch.int32, device=y.device)
-            made += (idx,)
+            idx = _empty(b, _torch.int32, y.device, stream)
         if val is None:
-            val = _torch.empty(b, dtype=_torch.float32, device=y.device)
-            made += (val,)
+            val = _empty(b, _torch.float32, y.device, stream)
         if workspace is None:
             need = lowbit_logits_workspace_bytes(n, b)
-            workspace = _torch.empty(max(need, 16), dtype=_torch.uint8, device=y.device)
-            made += (workspace,)
+            workspace = _empty(max(need, 16), _torch.uint8, y.device, stream)
         ip, vp = vector("idx", idx, _I32, b, dev), vector("val", val, _F32, b, dev)
         wp, need = vector("workspace", workspace, _U8, 0, dev), workspace.numel()
     elif idx is not None or val is not None:
@@ -707,7 +715,7 @@ def lowbit_logits_process(y, tokens=None, prompt_len=None, total_len=None, repet
            vector("repetition", repetition, _F32, b, dev), vector("frequency", frequency, _F32, b, dev),
            vector("presence", presence, _F32, b, dev), bp, bv, bcap, ldb,
            vector("bias_len", bias_len, _I32, b, dev), mp, mask_rows, ldm,
-           vector("mask_row", mask_row, _I32, b, dev), op, ldo, ip, vp, wp, need), made)
+           vector("mask_row", mask_row, _I32, b, dev), op, ldo, ip, vp, wp, need))
     return out, idx, val
 
 
@@ -726,6 +734,7 @@ def lowbit_lora_accumulate(x, ids, a, b, y, ranks=None, scales=None, workspace=N
         _first_use()
     rows, vector = _m.rows, _m.vector
     m, k, dev = _m.shape("x", x)
+    _same_device(stream, dev)
     xp, xt, ldx = rows("x", x, m, k, dev)
     if a.dim() != 3 or b.dim() != 3:
         raise ValueError("a must be [slots][r][k] and b [slots][n][r]")
@@ -733,16 +742,14 @@ def lowbit_lora_accumulate(x, ids, a, b, y, ranks=None, scales=None, workspace=N
     if a.shape != (slots, r, k):
         raise ValueError(f"a {tuple(a.shape)} does not fit x {tuple(x.shape)} and b {tuple(b.shape)}")
     yp, yt, ldy = rows("y", y, m, n, dev)
-    made = ()
     if workspace is None:
         need = lowbit_lora_workspace_bytes(m, n, k, r, slots)
-        workspace = _torch.empty(max(need, 16), dtype=_torch.uint8, device=x.device)
-        made = (workspace,)
+        workspace = _empty(max(need, 16), _torch.uint8, x.device, stream)
     _call("lowbit_lora_accumulate", dev, stream,
           (xp, xt, ldx, vector("ids", ids, _I32, m, dev), m, n, k, r, slots,
            vector("a", a, xt, 0, dev), vector("b", b, xt, 0, dev),
            vector("ranks", ranks, _I32, slots, dev), vector("scales", scales, _F32, slots, dev),
-           yp, yt, ldy, vector("workspace", workspace, _U8, 0, dev), workspace.numel()), made)
+           yp, yt, ldy, vector("workspace", workspace, _U8, 0, dev), workspace.numel()))
     return y
 
 

@@ -93,3 +93,39 @@ def test_the_plain_calls_pass():
 def test_refusals(call, over, error):
     with pytest.raises(error):
         call(**over())
+
+
+class _OtherDevice:
+    device_index = 1
+    cuda_stream = 0
+
+
+@pytest.mark.parametrize("call", [_norm, _logits, _lora])
+def test_a_stream_of_another_device_is_refused(call):
+    with pytest.raises(ValueError):
+        call(stream=_OtherDevice())
+
+
+@pytest.mark.parametrize("op", ["norm", "logits"])
+def test_outputs_on_another_stream_do_not_reuse_its_memory(op):
+    """What the current stream freed may still be written by work that waits
+    there: a call on another stream gets other memory for its outputs."""
+    import torch
+
+    side = torch.cuda.Stream()
+    r, y = _f(4, 200000), _f(70000, 64)
+    torch.cuda.synchronize()
+
+    def run():
+        if op == "norm":
+            return lowbit.lowbit_norm_residual(None, r, pre="rms", x_dtype=torch.float32, stream=side)[1:]
+        return lowbit.lowbit_logits_process(y[:60000], stream=side)[1:]
+
+    sizes = [t.numel() for t in run()]
+    torch.cuda.synchronize()
+    freed = [torch.empty(n, dtype=torch.float32, device="cuda") for n in sizes]
+    held = {t.data_ptr() for t in freed}
+    del freed
+    outs = run()
+    torch.cuda.synchronize()
+    assert not held & {t.data_ptr() for t in outs}
