@@ -453,7 +453,7 @@ size_t lowbit_logits_workspace_bytes(int64_t n, int64_t b);
  *   workspace : lowbit_logits_workspace_bytes(n, b) bytes, contents ignored
  *               on entry; not used (NULL allowed) without idx
  * At least one of out and idx is given.  n < 2^31, b <= 65535, n * b <= 2^35,
- * tcap, bcap < 2^30.  Pointers other than the workspace need their element's alignment
+ * tcap < 2^30, bcap <= 16384.  Pointers other than the workspace need their element's alignment
  * only.  Equal inputs give equal bits. */
 int lowbit_logits_process(const void* y, int y_type, int64_t ldy, int64_t n, int64_t b,
                           const int32_t* tokens, int64_t tcap, int64_t ldt,

@@ -54,7 +54,12 @@ LOGITS = dict(y=GOOD, yt=F32, ldy=100, n=100, b=2, tok=GOOD, tcap=10, ldt=10, pl
     (dict(bv=NULL), ARG), (dict(bi=NULL), ARG), (dict(out=GOOD, yt=BF16), ARG), (dict(out=GOOD, ldo=200), ARG),
     (dict(n=0), SHAPE), (dict(n=1 << 31), SHAPE), (dict(b=0), SHAPE), (dict(b=65536), SHAPE), (dict(ldy=99), SHAPE),
     (dict(ldo=99), SHAPE), (dict(tcap=-1), SHAPE), (dict(ldt=9), SHAPE), (dict(tcap=1 << 30, ldt=1 << 30), SHAPE),
-    (dict(ldb=3), SHAPE), (dict(bcap=-2), SHAPE), (dict(ldm=3), SHAPE), (dict(rows=0), SHAPE),
+    (dict(ldb=3), SHAPE), (dict(bcap=-2), SHAPE), (dict(bcap=16385, ldb=16385), SHAPE), (dict(ldm=3), SHAPE),
+    (dict(rows=0), SHAPE),
+    # n * b of 2^35 passes (the address is then refused), more does not
+    (dict(n=1 << 20, b=1 << 15, ldy=1 << 20, ldo=1 << 20, ldm=1 << 15, rows=1 << 15, idx=NULL, val=NULL,
+          y=P(0x10002)), ALIGN),
+    (dict(n=(1 << 20) + 1, b=1 << 15, ldy=1 << 21, ldo=1 << 21), SHAPE),
     (dict(y=P(0x10002)), ALIGN), (dict(tok=P(0x10002)), ALIGN), (dict(mask=P(0x10001)), ALIGN),
     (dict(ws=NULL), WS), (dict(wsb=8), WS), (dict(ws=P(0x10008)), ALIGN),
 ])
