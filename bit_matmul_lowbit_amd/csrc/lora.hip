@@ -782,7 +782,7 @@ hipError_t launch(const LoraArgs& a, const Plan& plan, float* v, hipStream_t st)
   // One that takes several shares finds its rows and makes v ready (a chain of
   // four memory latencies) once for all of them.
   const int64_t tiles = (a.n + kBlockN - 1) / kBlockN, all = tiles * items;
-  int64_t each = all <= 1536 ? (all + 767) / 768 : (all + 3071) / 3072;
+  int64_t each = all <= 1536 ? (all + 767) / 768 : (all + 2999) / 3000;
   each = each < tiles ? each : tiles;
   const dim3 ge((unsigned)((tiles + each - 1) / each), (unsigned)(items < 32768 ? items : 32768));
   const size_t lds = (size_t)Mma<XT>::pieces * tm * ((a.r + 31) / 32 * 32 + 8) * 2;
