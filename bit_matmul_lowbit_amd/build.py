@@ -1,5 +1,5 @@
 """Build liblowbit.so (HIP, gfx950) in-tree with hipcc, and the Python
-binding's argument module (_marshal.so, host code against torch's headers)
+binding's compiled part (_marshal.so, host code against torch's headers)
 with g++.
 
 Run ``python -m bit_matmul_lowbit_amd.build`` or call ``build()``.  Every call
@@ -35,6 +35,7 @@ FLAGS = [
 
 MARSHAL = os.path.join(HERE, "_marshal.so")
 CXX = os.environ.get("CXX", "g++")
+ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 
 
 def _run(cmd, out: str, verbose: bool) -> None:
@@ -57,6 +58,7 @@ def build_marshal(verbose: bool = False) -> str:
     _run([CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", inc,
           "-I", os.path.join(inc, "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"],
+          "-I", os.path.join(ROOT, "include"), "-I", os.path.join(ROCM, "include"), "-D__HIP_PLATFORM_AMD__",
           "-o", MARSHAL + ".tmp", os.path.join(CSRC, "marshal.cpp"), "-L", lib, "-ltorch_python", "-ltorch_cpu",
           "-lc10"], MARSHAL, verbose)
     return MARSHAL

@@ -552,60 +552,46 @@ def lowbit_base3_to_t2(b3, scales_rm, n: int, k: int, codes=None, scales=None, s
 # ---------------------------------------------------------------------------
 # operators beside the products.  They take row strides and run on the device
 # their tensors are on (also when it is not the current one).  A decode step
-# makes many such calls, so the checks of a tensor are one call of the compiled
-# module _marshal each.
+# makes many such calls, so the compiled module _marshal checks the tensors and
+# calls the library.
 
-_F32, _I32, _U8 = 1, 4, 5  # its type codes
-_torch = _m = _raw_stream = _current_device = None
+_m = None
+_codes = {}  # torch type -> its code there
+
+
+def _empty(shape, code, dev, stream):
+    """A tensor made for a call on `stream`, which need not be the current one.
+    It is that stream's memory: what the current one freed may still be in use
+    by work that waits there.  The current stream, where the caller reads it, is
+    noted with the allocator."""
+    import torch
+
+    dtype = next(t for t, c in _codes.items() if c == code)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=f"cuda:{dev}")
+    t.record_stream(torch.cuda.current_stream(dev))
+    return t
 
 
 def _first_use():
-    """Load torch, the library and the argument module (importing this module
+    """Load torch, the library and the compiled module (importing this module
     loads nothing)."""
-    global _torch, _m, _raw_stream, _current_device
+    global _m
     import torch
 
-    load()
+    lib = load()
     try:
         from . import _marshal
     except ImportError as e:
         raise RuntimeError("bit_matmul_lowbit_amd/_marshal.so is missing or does not fit this torch: build it with "
                            "`python -m bit_matmul_lowbit_amd.build` (or __graft_entry__.build())") from e
-    _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    _codes.update({torch.float32: 1, torch.float16: 2, torch.bfloat16: 3, torch.int32: 4, torch.uint8: 5})
+    _marshal.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in
+                    ("lowbit_norm_residual", "lowbit_logits_workspace_bytes", "lowbit_logits_process",
+                     "lowbit_lora_workspace_bytes", "lowbit_lora_accumulate")),
+                  torch._C._cuda_getCurrentRawStream, _empty, LowbitError)
     _m = _marshal
-    _torch = torch  # last: it says that all of them are there
-
-
-def _empty(shape, dtype, device, stream):
-    """A tensor made for a call on `stream` (None: the current one).  It is that
-    stream's memory: what the current one freed may still be in use by work
-    that waits there.  The current stream, where the caller reads it, is noted
-    with the allocator."""
-    if stream is None:
-        return _torch.empty(shape, dtype=dtype, device=device)
-    with _torch.cuda.stream(stream):
-        t = _torch.empty(shape, dtype=dtype, device=device)
-    t.record_stream(_torch.cuda.current_stream(device))
-    return t
-
-
-def _call(where, dev, stream, args):
-    """Call library function `where` on `stream` (default: the current one of
-    device `dev`) with that device current."""
-    fn = getattr(_lib, where)
-    raw = _raw_stream(dev) if stream is None else stream.cuda_stream
-    if dev == _current_device():
-        status = fn(*args, raw)
-    else:
-        with _torch.cuda.device(dev):
-            status = fn(*args, raw)
-    if status != 0:
-        raise LowbitError(status, where)
-
-
-def _same_device(stream, dev):
-    if stream is not None and stream.device_index != dev:
-        raise ValueError(f"stream is one of cuda:{stream.device_index}, expected cuda:{dev}")
+    return _m
 
 
 def lowbit_norm_residual(y, r, post="none", post_w=None, post_b=None, gate=None, scale=1.0,
@@ -619,41 +605,12 @@ def lowbit_norm_residual(y, r, post="none", post_w=None, post_b=None, gate=None,
     "none", "rms" or "layer" with FP32 weights and biases [k] (None: 1 and
     0); pre=None makes no x.  gate: [k] for every row or [m][k].  x_out is
     allocated with x_dtype (FP16, as lowbit_gemv reads it, if not given)."""
-    if _torch is None:
-        _first_use()
-    rows, vector = _m.rows, _m.vector
-    m, k, dev = _m.shape("r", r)
-    _same_device(stream, dev)
-    rp, rt, ldr = rows("r", r, m, k, dev)
-    yp = yt = ldy = gp = gt = ldg = rop = ldro = xp = xt = ldx = post_c = pre_c = 0
-    if y is not None:
-        post_c = NORMS[post]
-        yp, yt, ldy = rows("y", y, m, k, dev)
-        if gate is not None:
-            if gate.dim() == 1:
-                gp, gt, _ = rows("gate", gate, 1, k, dev)
-            else:
-                gp, gt, ldg = rows("gate", gate, m, k, dev)
-        if r_out is None:
-            r_out, rop, ldro = r, rp, ldr
-        else:
-            rop, rot, ldro = rows("r_out", r_out, m, k, dev)
-            if rot != rt:
-                raise TypeError("r_out must have the type of r")
-    elif r_out is not None:
-        raise ValueError("r_out needs y")
-    if pre is not None:
-        pre_c = NORMS[pre]
-        if x_out is None:
-            x_out = _empty(r.shape, x_dtype or _torch.float16, r.device, stream)
-        xp, xt, ldx = rows("x_out", x_out, m, k, dev)
-    elif x_out is not None:
-        raise ValueError("x_out needs pre")
-    _call("lowbit_norm_residual", dev, stream,
-          (yp, yt, ldy, rp, rt, ldr, rop, ldro, xp, xt, ldx, m, k, post_c,
-           vector("post_w", post_w, _F32, k, dev), vector("post_b", post_b, _F32, k, dev), gp, gt, ldg, scale,
-           pre_c, vector("pre_w", pre_w, _F32, k, dev), vector("pre_b", pre_b, _F32, k, dev), eps))
-    return (r_out if y is not None else r), x_out
+    m = _m or _first_use()
+    x_code = 2 if x_dtype is None else _codes.get(x_dtype, 0)
+    if not 1 <= x_code <= 3:
+        raise TypeError("x_dtype must be float32, float16 or bfloat16")
+    return m.norm(y, r, NORMS[post] if y is not None else 0, post_w, post_b, gate, scale,
+                  NORMS[pre] if pre is not None else -1, pre_w, pre_b, eps, r_out, x_out, x_code, stream)
 
 
 def lowbit_logits_workspace_bytes(n: int, b: int) -> int:
@@ -673,50 +630,8 @@ def lowbit_logits_process(y, tokens=None, prompt_len=None, total_len=None, repet
     repetition / frequency / presence FP32 [b]; bias_ids int32 and bias_vals
     FP32 [b][.] with bias_len int32 [b]; mask int32 [rows][>= n / 32] with
     mask_row int32 [b]."""
-    if _torch is None:
-        _first_use()
-    rows, vector, lists = _m.rows, _m.vector, _m.lists
-    b, n, dev = _m.shape("y", y)
-    _same_device(stream, dev)
-    yp, yt, ldy = rows("y", y, b, n, dev)
-    tp, tcap, ldt = lists("tokens", tokens, _I32, b, dev)
-    bp, bcap, ldb = lists("bias_ids", bias_ids, _I32, b, dev)
-    bv, bvcap, ldbv = lists("bias_vals", bias_vals, _F32, b, dev)
-    if (bp is None) != (bv is None) or bcap != bvcap or ldb != ldbv:
-        raise ValueError("bias_ids and bias_vals go together, with one shape and row stride")
-    mp, words, ldm = lists("mask", mask, _I32, b if mask_row is None else -1, dev)
-    mask_rows = 0
-    if mp is not None:
-        mask_rows = mask.shape[0]
-        if words < (n + 31) // 32:
-            raise ValueError(f"mask has {words} words a row, needs {(n + 31) // 32}")
-    op = ldo = 0
-    if out is not None:
-        op, ot, ldo = rows("out", out, b, n, dev)
-        if ot != 1:
-            raise TypeError("out must be float32")
-    ip = vp = wp = None
-    need = 0
-    if top1:
-        if idx is None:
-            idx = _empty(b, _torch.int32, y.device, stream)
-        if val is None:
-            val = _empty(b, _torch.float32, y.device, stream)
-        if workspace is None:
-            need = lowbit_logits_workspace_bytes(n, b)
-            workspace = _empty(max(need, 16), _torch.uint8, y.device, stream)
-        ip, vp = vector("idx", idx, _I32, b, dev), vector("val", val, _F32, b, dev)
-        wp, need = vector("workspace", workspace, _U8, 0, dev), workspace.numel()
-    elif idx is not None or val is not None:
-        raise ValueError("idx and val need top1")
-    _call("lowbit_logits_process", dev, stream,
-          (yp, yt, ldy, n, b, tp, tcap, ldt,
-           vector("prompt_len", prompt_len, _I32, b, dev), vector("total_len", total_len, _I32, b, dev),
-           vector("repetition", repetition, _F32, b, dev), vector("frequency", frequency, _F32, b, dev),
-           vector("presence", presence, _F32, b, dev), bp, bv, bcap, ldb,
-           vector("bias_len", bias_len, _I32, b, dev), mp, mask_rows, ldm,
-           vector("mask_row", mask_row, _I32, b, dev), op, ldo, ip, vp, wp, need))
-    return out, idx, val
+    return (_m or _first_use()).logits(y, tokens, prompt_len, total_len, repetition, frequency, presence, bias_ids,
+                                       bias_vals, bias_len, mask, mask_row, out, top1, idx, val, workspace, stream)
 
 
 def lowbit_lora_workspace_bytes(m: int, n: int, k: int, r: int, slots: int) -> int:
@@ -730,27 +645,7 @@ def lowbit_lora_accumulate(x, ids, a, b, y, ranks=None, scales=None, workspace=N
     [slots][r][k] and b [slots][n][r] in x's type, ranks int32 [slots], scales
     FP32 [slots], y [m][n] FP32 (or BF16 with BF16 x); rows of x and y may be
     strided (a slice of a fused projection's output)."""
-    if _torch is None:
-        _first_use()
-    rows, vector = _m.rows, _m.vector
-    m, k, dev = _m.shape("x", x)
-    _same_device(stream, dev)
-    xp, xt, ldx = rows("x", x, m, k, dev)
-    if a.dim() != 3 or b.dim() != 3:
-        raise ValueError("a must be [slots][r][k] and b [slots][n][r]")
-    slots, n, r = b.shape
-    if a.shape != (slots, r, k):
-        raise ValueError(f"a {tuple(a.shape)} does not fit x {tuple(x.shape)} and b {tuple(b.shape)}")
-    yp, yt, ldy = rows("y", y, m, n, dev)
-    if workspace is None:
-        need = lowbit_lora_workspace_bytes(m, n, k, r, slots)
-        workspace = _empty(max(need, 16), _torch.uint8, x.device, stream)
-    _call("lowbit_lora_accumulate", dev, stream,
-          (xp, xt, ldx, vector("ids", ids, _I32, m, dev), m, n, k, r, slots,
-           vector("a", a, xt, 0, dev), vector("b", b, xt, 0, dev),
-           vector("ranks", ranks, _I32, slots, dev), vector("scales", scales, _F32, slots, dev),
-           yp, yt, ldy, vector("workspace", workspace, _U8, 0, dev), workspace.numel()))
-    return y
+    return (_m or _first_use()).lora(x, ids, a, b, y, ranks, scales, workspace, stream)
 
 
 # ---------------------------------------------------------------------------
