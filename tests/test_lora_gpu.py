@@ -55,7 +55,9 @@ SHAPES = [(1, 128, 1, 8, 1), (1, 2048, 6144, 16, 8), (8, 1280, 700, 64, 16), (3,
           (7, 17408, 64, 256, 2), (300, 256, 1025, 32, 300), (1030, 128, 96, 8, 3),
           # one launch with 32 and 64 ranks; several items of one adapter; more rows than a plan keeps in registers
           (9, 512, 300, 32, 4), (12, 256, 700, 64, 5), (16, 640, 129, 48, 16), (40, 384, 300, 128, 3),
-          (64, 256, 100, 16, 1), (5000, 64, 40, 8, 2), (9000, 8, 16, 8, 700)]
+          (64, 256, 100, 16, 1), (5000, 64, 40, 8, 2), (9000, 8, 16, 8, 700),
+          # items of 32 rows with the most ranks; ranks that end inside a 32 at outputs that end inside a wave's
+          (150, 264, 530, 256, 3), (100, 128, 515, 200, 2), (130, 128, 2049, 72, 2)]
 
 
 @pytest.mark.parametrize("m,k,n,r,slots", SHAPES)
