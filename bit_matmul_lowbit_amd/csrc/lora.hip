@@ -26,7 +26,7 @@
 // loads 128 contiguous bytes of a row by eight lanes instead and passes them
 // to the lanes that need them through LDS of its own.
 // expand: y += v B^T, one work-group per (item, share of the outputs, 256 at a
-// time).  v is summed over the slices, scaled, and split into 16-bit pieces
+// time); B goes through LDS in the same manner.  v is summed over the slices, scaled, and split into 16-bit pieces
 // whose sum holds it to FP32's precision or nearly (FP16: two pieces of a row
 // scaled by a power of two, 22 bits; BF16: three pieces, 24 bits), since a
 // single 16-bit v would be the least exact value of the whole sum.  No
@@ -34,11 +34,11 @@
 //
 // What bounds it.  Few rows: the bytes of A and B and the latencies before
 // they can be asked for (ids, then v).  8 rows of 8 adapters, r 64, 5120 ->
-// 34816: 4.0 + 13 us for 7 + 36 MB (three work-groups to a compute unit hold 96
-// KB of B in flight; with B's rows all one expand takes 7.5 us).  Many rows: y,
-// read and written.  4096 rows of 8 adapters, r 32, 5120 -> 17408, BF16: plan
-// 7.1, shrink 20.8, expand 75 us for 285 MB of y (3.8 TB/s; a large copy reaches
-// 4.8).  One row, 2048 -> 6144, r 16: 6.8 us in one launch.
+// 34816: 4.0 + 12.5 us for 7 + 36 MB (more of B in flight changes nothing; with
+// B's rows all one expand takes 7.5 us).  Many rows: y, read and written.  4096
+// rows of 8 adapters, r 32, 5120 -> 17408, BF16: plan 7.1, shrink 20.8, expand
+// 71 us for 285 MB of y (4.0 TB/s; a large copy reaches 4.8).  One row, 2048 ->
+// 6144, r 16: 6.7 us in one launch.
 #include "common.h"
 
 namespace lowbit {
@@ -121,6 +121,7 @@ __device__ __forceinline__ int wave_scan(int v) {
 struct Found {
   Item it;
   int rows[kItemRows];
+  int64_t y_at[kItemRows];  // where they begin in y (64-bit products at each use cost 1 to 2 % of a call)
 };
 
 // Item number `item` (tm rows at most), in every thread: its count is 0 if
@@ -156,7 +157,10 @@ __device__ __forceinline__ Item find_item(const LoraArgs& a, const Plan& plan, i
         it.count = left < tm ? left : tm;
         it.rank = rank_of(a, it.slot);
         const int at = before - first;
-        if (s == it.slot && at >= 0 && at < it.count) found.rows[at] = lane;
+        if (s == it.slot && at >= 0 && at < it.count) {
+          found.rows[at] = lane;
+          found.y_at[at] = lane * a.ldy;
+        }
       }
     } else if (item < plan.most) {
       const int used = *plan.items_used;
@@ -164,7 +168,10 @@ __device__ __forceinline__ Item find_item(const LoraArgs& a, const Plan& plan, i
       const int row = plan.rows[item * tm + (lane & (tm - 1))];
       if (item < used) {
         it = got;
-        if (lane < it.count) found.rows[lane] = row;
+        if (lane < it.count) {
+          found.rows[lane] = row;
+          found.y_at[lane] = row * a.ldy;
+        }
       }
     }
     if (lane == 0) found.it = it;
@@ -463,7 +470,7 @@ __device__ __forceinline__ void store_tail(const Out4<3>& z, bf16_t* p, int n) {
 // is made ready: first() brings about what inner(row, j), four sums of v from
 // rank j on, needs.
 template <int XT, int YT, int SUBS, int WAVES, class First, class Inner>
-__device__ __forceinline__ void expand_item(const LoraArgs& a, const Item& it, const int* rows, float* unscale,
+__device__ __forceinline__ void expand_item(const LoraArgs& a, const Item& it, const Found& found, float* unscale,
                                             typename Elem<XT>::type* pieces, int tm, uint4* staged, int share,
                                             int shares, First first, Inner inner) {
   // Four lanes load 64 contiguous bytes of a row of B and pass them on through
@@ -479,11 +486,10 @@ __device__ __forceinline__ void expand_item(const LoraArgs& a, const Item& it, c
   const float scale = it.scale;
   const int chunks = (rank + 31) / 32, pitch = chunks * 32 + 8;  // 16 bytes past: other banks
   const X* bs = static_cast<const X*>(a.b) + (int64_t)slot * a.n * a.r;
-  // where row 4 q + e of a part has its outputs n0 + 4 c ...; made anew at
-  // each use (kept, the pointers would cost a wave of occupancy)
+  // where row 4 q + e of a part, one of the item's, has its outputs n0 + 4 c
+  // ...; made anew at each use (kept, the pointers would cost a wave of occupancy)
   auto yrow = [&](int s, int e, int64_t n0) __attribute__((always_inline)) {
-    const int at = s * 16 + q * 4 + e;
-    return static_cast<Y*>(a.y) + ((int64_t)rows[at < count ? at : 0] * a.ldy + n0 + c * 4);
+    return static_cast<Y*>(a.y) + (found.y_at[s * 16 + q * 4 + e] + n0 + c * 4);
   };
 
   uint4 w[2][kTilesN];
@@ -651,7 +657,7 @@ __device__ __forceinline__ void expand_item(const LoraArgs& a, const Item& it, c
 
 // One item, every gridDim.x-th 256 outputs.
 template <int XT, int YT, bool INLINE, int SUBS>
-__global__ __launch_bounds__(256, SUBS == 1 || YT == 3 ? 3 : 2) void lora_expand_kernel(
+__global__ __launch_bounds__(256, SUBS == 1 ? 4 : YT == 3 ? 3 : 2) void lora_expand_kernel(
     LoraArgs a, Plan plan, int tm, int slices, const float* __restrict__ v) {
   extern __shared__ uint4 dyn[];  // pieces of v: [pieces][tm][pitch]
   __shared__ Found found;
@@ -677,7 +683,7 @@ __global__ __launch_bounds__(256, SUBS == 1 || YT == 3 ? 3 : 2) void lora_expand
       }
       return sum;
     };
-    expand_item<XT, YT, SUBS, 4>(a, it, rows, unscale,
+    expand_item<XT, YT, SUBS, 4>(a, it, found, unscale,
                                  reinterpret_cast<typename Elem<XT>::type*>(dyn), tm, staged, (int)blockIdx.x,
                                  (int)gridDim.x, [] {}, inner);
     __syncthreads();  // the next item's rows and pieces
@@ -708,7 +714,7 @@ __global__ __launch_bounds__(512) void lora_small_kernel(LoraArgs a) {
   auto inner = [&](int at, int j) __attribute__((always_inline)) {
     return *reinterpret_cast<const f32x4*>(&inner_v[at][j]);
   };
-  expand_item<XT, YT, 1, kWaves>(a, it, rows, unscale,
+  expand_item<XT, YT, 1, kWaves>(a, it, found, unscale,
                                  reinterpret_cast<typename Elem<XT>::type*>(pieces), 16, nullptr, (int)blockIdx.x,
                                  (int)gridDim.x, first, inner);
 }
