@@ -26,11 +26,12 @@
 // loads 128 contiguous bytes of a row by eight lanes instead and passes them
 // to the lanes that need them through LDS of its own.
 // expand: y += v B^T, one work-group per (item, share of the outputs, 256 at a
-// time); B goes through LDS in the same manner.  v is summed over the slices, scaled, and split into 16-bit pieces
-// whose sum holds it to FP32's precision or nearly (FP16: two pieces of a row
-// scaled by a power of two, 22 bits; BF16: three pieces, 24 bits), since a
-// single 16-bit v would be the least exact value of the whole sum.  No
-// atomics anywhere: every value has one writer and its sum one order.
+// time); B goes through LDS in the same manner.  v is summed over the slices,
+// scaled, and split into 16-bit pieces whose sum holds it to FP32's precision
+// or nearly (FP16: two pieces of a row scaled by a power of two, 22 bits; BF16:
+// three pieces, 24 bits), since a single 16-bit v would be the least exact
+// value of the whole sum.  No atomics anywhere: every value has one writer and
+// its sum one order.
 //
 // What bounds it.  Few rows: the bytes of A and B and the latencies before
 // they can be asked for (ids, then v).  8 rows of 8 adapters, r 64, 5120 ->
