@@ -57,7 +57,9 @@ SHAPES = [(1, 128, 1, 8, 1), (1, 2048, 6144, 16, 8), (8, 1280, 700, 64, 16), (3,
           (9, 512, 300, 32, 4), (12, 256, 700, 64, 5), (16, 640, 129, 48, 16), (40, 384, 300, 128, 3),
           (64, 256, 100, 16, 1), (5000, 64, 40, 8, 2), (9000, 8, 16, 8, 700),
           # items of 32 rows with the most ranks; ranks that end inside a 32 at outputs that end inside a wave's
-          (150, 264, 530, 256, 3), (100, 128, 515, 200, 2), (130, 128, 2049, 72, 2)]
+          (150, 264, 530, 256, 3), (100, 128, 515, 200, 2), (130, 128, 2049, 72, 2),
+          # as many adapters as there can be
+          (40, 8, 16, 8, 4096), (100, 16, 24, 16, 4096), (5000, 8, 16, 8, 4096)]
 
 
 @pytest.mark.parametrize("m,k,n,r,slots", SHAPES)

@@ -116,12 +116,22 @@ def test_binding_rejects_host_tensors_and_wrong_types():
 def test_argument_module_counts_its_arguments():
     from bit_matmul_lowbit_amd import _marshal
 
-    for f in (_marshal.shape, _marshal.rows, _marshal.vector, _marshal.lists):
+    for f in (_marshal.bind, _marshal.norm, _marshal.logits, _marshal.lora):
         with pytest.raises(TypeError, match="expected"):
             f("name")
-    assert _marshal.vector("name", None, 1, 5, 0) is None
-    assert _marshal.lists("name", None, 4, 5, 0) == (None, 0, 0)
+
+
+@pytest.mark.parametrize("call", [
+    lambda t: lowbit.lowbit_norm_residual(None, t(2, 8), pre="rms"),
+    lambda t: lowbit.lowbit_norm_residual(None, 3),
+    lambda t: lowbit.lowbit_norm_residual(None, t(2, 8), pre="rms", x_dtype="float16"),
+    lambda t: lowbit.lowbit_norm_residual(None, t(2, 8), scale="a"),
+    lambda t: lowbit.lowbit_logits_process(t(100)),
+    lambda t: lowbit.lowbit_logits_process([1.0]),
+    lambda t: lowbit.lowbit_lora_accumulate(t(1, 8), t(1), t(1, 8, 8), t(1, 8, 8), t(1, 8)),
+])
+def test_the_binding_refuses_host_tensors_and_other_objects(call):
+    import torch
+
     with pytest.raises(TypeError):
-        _marshal.rows("name", None, 1, 1, 0)
-    with pytest.raises(TypeError):
-        _marshal.vector("name", 5, "f32", 1, 0)
+        call(torch.zeros)
