@@ -10,13 +10,16 @@
 // and step, raw, as they were loaded) while its sums are formed: the
 // deviations of a layer norm are summed in a second sweep over the registers,
 // which keeps a small variance beside a large mean.  A row belongs to one
-// work-group, or to one wave where rows are short and many; rows longer than
-// the registers of a work-group hold are read again for every sum.
+// work-group, or to one wave where rows are short and many, and where many rows
+// share weights that weigh as much as a row, a work-group keeps them over
+// several rows; rows longer than the registers of a work-group hold are read
+// again for every sum.
 //
 // What bounds it: memory.  16384 x 5120, everything BF16, a norm on both sides:
-// 141 to 150 us for 671 MB (4.5 to 4.75 TB/s; a large copy reaches 4.8).  Small
-// calls are a launch and two or three latencies: 1 x 2048 2.3 us, 8 x 5120 with
-// a gate 4.5 us, 777 x 1283 with layer norms 7.0 us.
+// 142 to 150 us for 671 MB (4.5 to 4.7 TB/s; a large copy reaches 4.8).  11886 x
+// 1624, FP16, gated: 42 us for 154 MB (3.7).  Small calls are a launch and two
+// or three latencies: 1 x 2048 2.3 us, 8 x 5120 with a gate 4.5 us, 777 x 1283
+// with layer norms 6.2 us.
 #include "common.h"
 
 namespace lowbit {
@@ -28,10 +31,18 @@ struct Raw8 {
   uint32_t d[2 * S];
 };
 
-// Elements [c, c + 8) of a row at p + i0: 16-byte loads at any element
-// alignment; past `k` nothing is read and zeros stand.
+// Eight elements from p[at] on: 16-byte loads at any element alignment
 template <int S>
-__device__ __forceinline__ Raw8<S> load8(const void* p, int64_t i0, int c, int k) {
+__device__ __forceinline__ Raw8<S> load8(const void* p, int64_t at) {
+  Raw8<S> r;
+  __builtin_memcpy(&r, static_cast<const char*>(p) + at * S, sizeof(r));
+  return r;
+}
+
+// Elements [c, c + 8) of a row at p + i0; past `k` nothing is read and zeros
+// stand.
+template <int S>
+__device__ __forceinline__ Raw8<S> load_part8(const void* p, int64_t i0, int c, int k) {
   Raw8<S> r;
   const char* row = static_cast<const char*>(p) + i0 * S;
   if (c + 8 <= k) {
@@ -75,35 +86,26 @@ __device__ __forceinline__ void widen(const Raw8<S>& r, int type, float (&v)[8])
   }
 }
 
+// of the eight elements from `at` on, those from `from` to before `to`
 template <typename T>
-__device__ __forceinline__ void store8_as(void* p, int64_t i0, int c, int k, const float (&v)[8]) {
+__device__ __forceinline__ void store8_as(void* p, int64_t at, int from, int to, const float (&v)[8]) {
   T o[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) o[j] = (T)v[j];
-  T* at = static_cast<T*>(p) + i0 + c;
-  if (c + 8 <= k) {
-    __builtin_memcpy(at, o, sizeof(o));
+  T* out = static_cast<T*>(p) + at;
+  if (from <= 0 && to >= 8) {
+    __builtin_memcpy(out, o, sizeof(o));
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (c + j < k) at[j] = o[j];
+      if (j >= from && j < to) out[j] = o[j];
   }
 }
 
-__device__ __forceinline__ void store8(void* p, int type, int64_t i0, int c, int k, const float (&v)[8]) {
-  if (type == 1) store8_as<float>(p, i0, c, k, v);
-  else if (type == 2) store8_as<_Float16>(p, i0, c, k, v);
-  else store8_as<bf16_t>(p, i0, c, k, v);
-}
-
-// FP32 vector of k elements, or `none` everywhere where it is not given
-__device__ __forceinline__ void vector8(const float* p, float none, int c, int k, float (&v)[8]) {
-  if (p) {
-    widen<4>(load8<4>(p, 0, c, k), 1, v);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = none;
-  }
+__device__ __forceinline__ void store8(void* p, int type, int64_t at, int from, int to, const float (&v)[8]) {
+  if (type == 1) store8_as<float>(p, at, from, to, v);
+  else if (type == 2) store8_as<_Float16>(p, at, from, to, v);
+  else store8_as<bf16_t>(p, at, from, to, v);
 }
 
 // Sum over the wave in every lane: DPP adds within 16 lanes and across the
@@ -146,142 +148,196 @@ __device__ __forceinline__ float row_sum(float v, float (*red)[16], int& turn) {
 }
 
 // Rows of up to threads * NV * 8 elements in registers.  SY, SR: bytes per
-// element of y and r.  AHEAD: weights and gate are fetched with the
-// row, not when they are needed, which takes two memory latencies off a small
-// call and occupancy off a large one.
-template <bool WAVE, int SY, int SR, int NV, bool AHEAD>
+// element of y and r.  MODE: kLazy: weights and gate are fetched when they are
+// needed, which leaves registers for rows of several steps.  kAhead: they are
+// fetched with the row, which takes two memory latencies off a small call.
+// kHeld: a work-group takes every gridDim.x-th row, keeps the weights (and a
+// gate that all rows share), and has the next row on its way while it works on
+// one (11886 x 1621, FP16, a norm on both sides, gated: 78 -> 49 us).
+enum { kLazy, kAhead, kHeld };
+template <int S>
+struct Bytes {
+  static constexpr int value = S;
+};
+// A thread's elements in step n are the eight from c on.  Where fewer are left
+// it holds the row's last eight (k >= 8) and passes over the first `skip` of
+// them, which are another thread's: no load has a short form.  kLazy loads what
+// is left one by one instead, which takes fewer registers (63 for 72: 16384 x
+// 5120, BF16, 143 us for 148).
+template <bool WAVE, int SY, int SR, int NV, int MODE>
 __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(NormArgs a) {
   __shared__ __align__(16) float red[2][16];
   if constexpr (!WAVE) row_sum_init(red);
   const int threads = WAVE ? 64 : (int)blockDim.x;
   const int t = WAVE ? threadIdx.x & 63 : threadIdx.x;
-  const int64_t i = WAVE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : (int64_t)blockIdx.x;
+  int64_t i = WAVE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : (int64_t)blockIdx.x;
+  const int64_t step = WAVE ? (int64_t)gridDim.x * 4 : (int64_t)gridDim.x;
   if (WAVE && i >= a.m) return;
   const int k = (int)a.k;
   const float inv_k = 1.0f / (float)k;
   int turn = 0;
 
-  Raw8<SY> yr[NV];
-  Raw8<SR> rr[NV];
-  float v[NV][8];
+  auto col = [&](int n) __attribute__((always_inline)) { return (n * threads + t) * 8; };
+  int at[NV], skip[NV];
 #pragma unroll
   for (int n = 0; n < NV; ++n) {
-    const int c = (n * threads + t) * 8;
-    if (a.y) yr[n] = load8<SY>(a.y, i * a.ldy, c, k);
-    rr[n] = load8<SR>(a.r, i * a.ldr, c, k);
+    at[n] = MODE == kLazy || col(n) < k - 8 ? col(n) : k - 8;
+    skip[n] = MODE == kLazy ? 0 : col(n) - at[n];
   }
-  float post_w[NV][8], post_b[NV][8], gate[NV][8], pre_w[NV][8], pre_b[NV][8];
-  auto gate8 = [&](int n) __attribute__((always_inline)) {
-    const int c = (n * threads + t) * 8;
-    if (a.gate_type == 1) widen<4>(load8<4>(a.gate, i * a.ldg, c, k), 1, gate[n]);
-    else widen<2>(load8<2>(a.gate, i * a.ldg, c, k), a.gate_type, gate[n]);
+  auto mine = [&](int n, int j) __attribute__((always_inline)) {
+    return MODE == kLazy ? col(n) + j < k : j >= skip[n];
   };
-  if constexpr (AHEAD) {
+  auto any = [&](int n) __attribute__((always_inline)) { return MODE == kLazy ? col(n) < k : skip[n] < 8; };
+  auto load = [&](auto bytes, const void* p, int64_t i0, int n) __attribute__((always_inline)) {
+    constexpr int S = decltype(bytes)::value;
+    if constexpr (MODE == kLazy) return load_part8<S>(p, i0, col(n), k);
+    else return load8<S>(p, i0 + at[n]);
+  };
+  auto store = [&](void* p, int type, int64_t i0, int n, const float (&v)[8]) __attribute__((always_inline)) {
+    if constexpr (MODE == kLazy) store8(p, type, i0 + col(n), 0, k - col(n), v);
+    else store8(p, type, i0 + at[n], skip[n], 8, v);
+  };
+  // from an FP32 vector, or `none` everywhere where it is not given
+  auto vec = [&](const float* p, float none, int n, float (&v)[8]) __attribute__((always_inline)) {
+    if (p) {
+      widen<4>(load(Bytes<4>{}, p, 0, n), 1, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = none;
+    }
+  };
+  Raw8<SY> yr[NV], yn[NV];
+  Raw8<SR> rr[NV], rn[NV];
+  auto load_row = [&](Raw8<SY> (&y)[NV], Raw8<SR> (&r)[NV], int64_t row) __attribute__((always_inline)) {
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
-      const int c = (n * threads + t) * 8;
+      if (a.y) y[n] = load(Bytes<SY>{}, a.y, row * a.ldy, n);
+      r[n] = load(Bytes<SR>{}, a.r, row * a.ldr, n);
+    }
+  };
+  load_row(yr, rr, i);
+  float post_w[NV][8], post_b[NV][8], gate[NV][8], pre_w[NV][8], pre_b[NV][8];
+  auto gate8 = [&](int n, int64_t row) __attribute__((always_inline)) {
+    if (a.gate_type == 1) widen<4>(load(Bytes<4>{}, a.gate, row * a.ldg, n), 1, gate[n]);
+    else widen<2>(load(Bytes<2>{}, a.gate, row * a.ldg, n), a.gate_type, gate[n]);
+  };
+  if constexpr (MODE != kLazy) {
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
       if (a.post != 0) {
-        vector8(a.post_w, 1.0f, c, k, post_w[n]);
-        vector8(a.post_b, 0.0f, c, k, post_b[n]);
+        vec(a.post_w, 1.0f, n, post_w[n]);
+        vec(a.post_b, 0.0f, n, post_b[n]);
       }
       if (a.pre != 0) {
-        vector8(a.pre_w, 1.0f, c, k, pre_w[n]);
-        vector8(a.pre_b, 0.0f, c, k, pre_b[n]);
+        vec(a.pre_w, 1.0f, n, pre_w[n]);
+        vec(a.pre_b, 0.0f, n, pre_b[n]);
       }
-      if (a.gate) gate8(n);
+      if (a.gate) gate8(n, i);
     }
   }
-  if (a.y) {
-    float u[NV][8];
+  for (;;) {
+    const int64_t next = i + step;
+    const bool more = MODE == kHeld && next < a.m;
+    if (more) load_row(yn, rn, next);
+    float v[NV][8];
+    if (a.y) {
+      float u[NV][8];
 #pragma unroll
-    for (int n = 0; n < NV; ++n) widen<SY>(yr[n], a.y_type, u[n]);
-    float mean = 0.0f, rs = 1.0f;
-    if (a.post == 2) {
-      float s = 0.0f;
+      for (int n = 0; n < NV; ++n) widen<SY>(yr[n], a.y_type, u[n]);
+      float mean = 0.0f, rs = 1.0f;
+      if (a.post == 2) {
+        float s = 0.0f;
 #pragma unroll
-      for (int n = 0; n < NV; ++n)
+        for (int n = 0; n < NV; ++n)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s += u[n][j];
-      mean = row_sum<WAVE>(s, red, turn) * inv_k;
-    }
-    if (a.post != 0) {
-      float s = 0.0f;
+          for (int j = 0; j < 8; ++j) s += MODE == kLazy || mine(n, j) ? u[n][j] : 0.0f;
+        mean = row_sum<WAVE>(s, red, turn) * inv_k;
+      }
+      if (a.post != 0) {
+        float s = 0.0f;
 #pragma unroll
-      for (int n = 0; n < NV; ++n)
+        for (int n = 0; n < NV; ++n)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float d = (n * threads + t) * 8 + j < k ? u[n][j] - mean : 0.0f;
-          s += d * d;
+          for (int j = 0; j < 8; ++j) {
+            const float d = mine(n, j) ? u[n][j] - mean : 0.0f;
+            s += d * d;
+          }
+        rs = 1.0f / sqrtf(row_sum<WAVE>(s, red, turn) * inv_k + a.eps);
+      }
+#pragma unroll
+      for (int n = 0; n < NV; ++n) {
+        if (any(n)) {
+          if (a.post != 0) {
+            if constexpr (MODE == kLazy) {
+              vec(a.post_w, 1.0f, n, post_w[n]);
+              vec(a.post_b, 0.0f, n, post_b[n]);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) u[n][j] = (u[n][j] - mean) * rs * post_w[n][j] + post_b[n][j];
+          }
+          if (a.gate) {
+            if constexpr (MODE == kLazy) gate8(n, i);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) u[n][j] *= gate[n][j];
+            if (more && a.ldg != 0) gate8(n, next);
+          }
         }
-      rs = 1.0f / sqrtf(row_sum<WAVE>(s, red, turn) * inv_k + a.eps);
-    }
+        widen<SR>(rr[n], a.r_type, v[n]);
 #pragma unroll
-    for (int n = 0; n < NV; ++n) {
-      const int c = (n * threads + t) * 8;
-      if (c < k) {
-        if (a.post != 0) {
-          if constexpr (!AHEAD) {
-            vector8(a.post_w, 1.0f, c, k, post_w[n]);
-            vector8(a.post_b, 0.0f, c, k, post_b[n]);
+        for (int j = 0; j < 8; ++j) v[n][j] += a.scale * u[n][j];
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < NV; ++n) widen<SR>(rr[n], a.r_type, v[n]);
+    }
+    if (a.r_out) {
+#pragma unroll
+      for (int n = 0; n < NV; ++n) {
+        if (any(n)) store(a.r_out, a.r_type, i * a.ldro, n, v[n]);
+      }
+    }
+    if (a.x_out) {
+      float mean = 0.0f, rs = 1.0f;
+      if (a.pre == 2) {
+        float s = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) s += mine(n, j) ? v[n][j] : 0.0f;
+        mean = row_sum<WAVE>(s, red, turn) * inv_k;
+      }
+      if (a.pre != 0) {
+        float s = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float d = mine(n, j) ? v[n][j] - mean : 0.0f;
+            s += d * d;
+          }
+        rs = 1.0f / sqrtf(row_sum<WAVE>(s, red, turn) * inv_k + a.eps);
+      }
+#pragma unroll
+      for (int n = 0; n < NV; ++n) {
+        if (!any(n)) continue;
+        if (a.pre != 0) {
+          if constexpr (MODE == kLazy) {
+            vec(a.pre_w, 1.0f, n, pre_w[n]);
+            vec(a.pre_b, 0.0f, n, pre_b[n]);
           }
 #pragma unroll
-          for (int j = 0; j < 8; ++j) u[n][j] = (u[n][j] - mean) * rs * post_w[n][j] + post_b[n][j];
+          for (int j = 0; j < 8; ++j) v[n][j] = (v[n][j] - mean) * rs * pre_w[n][j] + pre_b[n][j];
         }
-        if (a.gate) {
-          if constexpr (!AHEAD) gate8(n);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) u[n][j] *= gate[n][j];
-        }
+        store(a.x_out, a.x_type, i * a.ldx, n, v[n]);
       }
-      widen<SR>(rr[n], a.r_type, v[n]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[n][j] += a.scale * u[n][j];
     }
-  } else {
-#pragma unroll
-    for (int n = 0; n < NV; ++n) widen<SR>(rr[n], a.r_type, v[n]);
-  }
-  if (a.r_out) {
+    if (!more) return;
+    i = next;
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
-      const int c = (n * threads + t) * 8;
-      if (c < k) store8(a.r_out, a.r_type, i * a.ldro, c, k, v[n]);
+      yr[n] = yn[n];
+      rr[n] = rn[n];
     }
-  }
-  if (!a.x_out) return;
-  float mean = 0.0f, rs = 1.0f;
-  if (a.pre == 2) {
-    float s = 0.0f;
-#pragma unroll
-    for (int n = 0; n < NV; ++n)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s += (n * threads + t) * 8 + j < k ? v[n][j] : 0.0f;
-    mean = row_sum<WAVE>(s, red, turn) * inv_k;
-  }
-  if (a.pre != 0) {
-    float s = 0.0f;
-#pragma unroll
-    for (int n = 0; n < NV; ++n)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float d = (n * threads + t) * 8 + j < k ? v[n][j] - mean : 0.0f;
-        s += d * d;
-      }
-    rs = 1.0f / sqrtf(row_sum<WAVE>(s, red, turn) * inv_k + a.eps);
-  }
-#pragma unroll
-  for (int n = 0; n < NV; ++n) {
-    const int c = (n * threads + t) * 8;
-    if (c >= k) continue;
-    if (a.pre != 0) {
-      if constexpr (!AHEAD) {
-        vector8(a.pre_w, 1.0f, c, k, pre_w[n]);
-        vector8(a.pre_b, 0.0f, c, k, pre_b[n]);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[n][j] = (v[n][j] - mean) * rs * pre_w[n][j] + pre_b[n][j];
-    }
-    store8(a.x_out, a.x_type, i * a.ldx, c, k, v[n]);
   }
 }
 
@@ -300,8 +356,9 @@ __device__ __forceinline__ void store_any(void* p, int type, int64_t i, float v)
   else static_cast<bf16_t*>(p)[i] = (bf16_t)v;
 }
 
-// Rows longer than a work-group's registers: nothing is kept, each sum reads
-// the row again (a row of 2^22 would not fit a compute unit in any form).
+// Rows longer than a work-group's registers, or shorter than 8: nothing is
+// kept, each sum reads the row again (a row of 2^22 would not fit a compute unit
+// in any form).
 __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
   __shared__ __align__(16) float red[2][16];
   row_sum_init(red);
@@ -314,11 +371,11 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
   if (a.post != 0) {
     if (a.post == 2) {
       float s = 0.0f;
-      for (int64_t c = threadIdx.x; c < a.k; c += 1024) s += load_any(a.y, a.y_type, iy + c);
+      for (int64_t c = threadIdx.x; c < a.k; c += blockDim.x) s += load_any(a.y, a.y_type, iy + c);
       mean_y = row_sum<false>(s, red, turn) * inv_k;
     }
     float s = 0.0f;
-    for (int64_t c = threadIdx.x; c < a.k; c += 1024) {
+    for (int64_t c = threadIdx.x; c < a.k; c += blockDim.x) {
       const float d = load_any(a.y, a.y_type, iy + c) - mean_y;
       s += d * d;
     }
@@ -342,17 +399,17 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
   if (a.pre != 0) {
     if (a.pre == 2) {
       float s = 0.0f;
-      for (int64_t c = threadIdx.x; c < a.k; c += 1024) s += residual(c);
+      for (int64_t c = threadIdx.x; c < a.k; c += blockDim.x) s += residual(c);
       mean_r = row_sum<false>(s, red, turn) * inv_k;
     }
     float s = 0.0f;
-    for (int64_t c = threadIdx.x; c < a.k; c += 1024) {
+    for (int64_t c = threadIdx.x; c < a.k; c += blockDim.x) {
       const float d = residual(c) - mean_r;
       s += d * d;
     }
     rs_r = 1.0f / sqrtf(row_sum<false>(s, red, turn) * inv_k + a.eps);
   }
-  for (int64_t c = threadIdx.x; c < a.k; c += 1024) {
+  for (int64_t c = threadIdx.x; c < a.k; c += blockDim.x) {
     const float v = residual(c);
     if (a.r_out) store_any(a.r_out, a.r_type, i * a.ldro + c, v);
     if (a.x_out) {
@@ -367,13 +424,13 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
   }
 }
 
-template <bool WAVE, int NV, bool AHEAD>
+template <bool WAVE, int NV, int MODE>
 hipError_t launch_as(const NormArgs& a, dim3 grid, dim3 block, hipStream_t st) {
   const bool y4 = a.y_type == 1, r4 = a.r_type == 1;
-  if (y4 && r4) hipLaunchKernelGGL((norm_kernel<WAVE, 4, 4, NV, AHEAD>), grid, block, 0, st, a);
-  else if (y4) hipLaunchKernelGGL((norm_kernel<WAVE, 4, 2, NV, AHEAD>), grid, block, 0, st, a);
-  else if (r4) hipLaunchKernelGGL((norm_kernel<WAVE, 2, 4, NV, AHEAD>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((norm_kernel<WAVE, 2, 2, NV, AHEAD>), grid, block, 0, st, a);
+  if (y4 && r4) hipLaunchKernelGGL((norm_kernel<WAVE, 4, 4, NV, MODE>), grid, block, 0, st, a);
+  else if (y4) hipLaunchKernelGGL((norm_kernel<WAVE, 4, 2, NV, MODE>), grid, block, 0, st, a);
+  else if (r4) hipLaunchKernelGGL((norm_kernel<WAVE, 2, 4, NV, MODE>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((norm_kernel<WAVE, 2, 2, NV, MODE>), grid, block, 0, st, a);
   return hipGetLastError();
 }
 
@@ -381,22 +438,45 @@ hipError_t launch_as(const NormArgs& a, dim3 grid, dim3 block, hipStream_t st) {
 
 hipError_t launch_norm_residual(const NormArgs& a, hipStream_t st) {
   const int64_t chunks = (a.k + 7) / 8;
-  const bool many = a.m >= 1024;
-  // short rows, many of them: one wave each, no barriers
-  if (chunks <= 128 && many) {
-    const dim3 grid((unsigned)((a.m + 3) / 4));
-    return chunks <= 64 ? launch_as<true, 1, false>(a, grid, dim3(256), st)
-                        : launch_as<true, 2, false>(a, grid, dim3(256), st);
-  }
   const dim3 grid((unsigned)a.m);
+  if (a.k < 8) {
+    hipLaunchKernelGGL(norm_long_kernel, grid, dim3(64), 0, st, a);
+    return hipGetLastError();
+  }
+  const bool many = a.m >= 1024;
+  // Many rows: weights are kept where a row would read at least as much of them
+  // as of itself (11886 x 1624, FP16, four of them: 65 us read again, 42 kept;
+  // 4096 x 2048, BF16, one: 15.4 and 14.6; the same in FP32 26 and 28; none but
+  // the residual 37 and 41).  Rows of FP32 on both sides, which take more
+  // registers, need more of them (4096 x 2048, two: 28 and 30; four: 83 and 81).
+  const int vectors = !!a.post_w + !!a.post_b + !!a.pre_w + !!a.pre_b + (a.gate && a.ldg == 0);
+  const int bytes = (a.y ? (a.y_type == 1 ? 4 : 2) : 0) + (a.r_type == 1 ? 4 : 2);
+  const bool keep = 4 * vectors >= (bytes == 8 ? 12 : bytes);
+  // as many work-groups of `waves` waves as run at once (16 waves to a compute
+  // unit), each with as many of the rows
+  const auto running = [](int64_t waves) { return 256 * 16 / waves; };
+  const auto held = [&](int64_t rows, int64_t waves) {
+    const int64_t each = (rows + running(waves) - 1) / running(waves);
+    return dim3((unsigned)((rows + each - 1) / each));
+  };
+  // short rows, many of them: one wave each, no barriers (12030 x 128, one weight
+  // and a gate per row: 8.6 us kept, 12.8 read again)
+  if (chunks <= 64 && many) return launch_as<true, 1, kHeld>(a, held((a.m + 3) / 4, 4), dim3(256), st);
+  if (chunks <= 128 && many)
+    return keep ? launch_as<true, 2, kHeld>(a, held((a.m + 3) / 4, 4), dim3(256), st)
+                : launch_as<true, 2, kLazy>(a, dim3((unsigned)((a.m + 3) / 4)), dim3(256), st);
   auto block = [&](int64_t nv) { return dim3((unsigned)((chunks + nv * 64 - 1) / (nv * 64) * 64)); };
   // Many long rows: 16 elements a thread, so that more work-groups of fewer
-  // waves share a compute unit (16384 x 5120 BF16: 144 us, with 8 elements 184,
-  // with 32 161; 4096 x 4096 27 each way).
-  if (chunks <= 1024 && !(many && chunks > 512))
-    return many ? launch_as<false, 1, false>(a, grid, block(1), st) : launch_as<false, 1, true>(a, grid, block(1), st);
-  if (chunks <= 2048) return launch_as<false, 2, false>(a, grid, block(2), st);
-  if (chunks <= 4096) return launch_as<false, 4, false>(a, grid, block(4), st);
+  // waves share a compute unit (16384 x 5120 BF16: 143 us, with 8 elements 184,
+  // with 32 161; 4096 x 4096 with the weights kept 31, else 38).
+  if (chunks <= 1024 && !(many && chunks > 512)) {
+    const int64_t waves = (chunks + 63) / 64;
+    if (many && !keep) return launch_as<false, 1, kLazy>(a, grid, block(1), st);
+    if (many && a.m >= 2 * running(waves)) return launch_as<false, 1, kHeld>(a, held(a.m, waves), block(1), st);
+    return launch_as<false, 1, kAhead>(a, grid, block(1), st);
+  }
+  if (chunks <= 2048) return launch_as<false, 2, kLazy>(a, grid, block(2), st);
+  if (chunks <= 4096) return launch_as<false, 4, kLazy>(a, grid, block(4), st);
   hipLaunchKernelGGL(norm_long_kernel, grid, dim3(1024), 0, st, a);
   return hipGetLastError();
 }

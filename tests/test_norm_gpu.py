@@ -89,6 +89,31 @@ def test_matches_plain_form(m, k, post, pre, gate):
     _check(d, *got)
 
 
+@pytest.mark.parametrize("m,k", [(1024, 7), (1500, 8), (1031, 9), (9000, 128), (5003, 511), (4100, 514), (5000, 1001),
+                                 (4300, 1025), (1100, 4095), (700, 4096), (1100, 5119), (1030, 8200)])
+@pytest.mark.parametrize("yt,rt,xt", [("f32", "f32", "f16"), ("bf16", "bf16", "bf16"), ("f16", "f32", "bf16")])
+@pytest.mark.parametrize("post,pre,gate,pad", [("none", "none", "none", 0), ("rms", "rms", "none", 3),
+                                               ("layer", "layer", "channel", 0), ("rms", "layer", "row", 8)])
+def test_many_rows(m, k, yt, rt, xt, post, pre, gate, pad):
+    """Work-groups and waves that take several rows and keep the weights, in
+    place and not, at row strides of their own."""
+    import torch
+
+    say(f"norm m={m} k={k} y={yt} r={rt} x={xt} {post} {pre} {gate} pad={pad}")
+    d = _case(m, k, yt, rt, xt, post, pre, gate, m + k + pad)
+    wide = torch.full((m + 1, k + pad), 77.0, dtype=d["r"][0].dtype, device="cuda")
+    r = wide[:m, :k]
+    r.copy_(d["r"][0])
+    r_out, x_out = _call(d, r=r)
+    torch.cuda.synchronize()
+    assert r_out is r
+    _check(d, r_out, x_out)
+    assert bool((wide[:m, k:] == 77.0).all()) and bool((wide[m] == 77.0).all())
+    r2 = torch.empty_like(d["r"][0])
+    _, x2 = _call(d, r_out=r2)
+    assert torch.equal(r2, r_out) and torch.equal(x2, x_out)
+
+
 @pytest.mark.parametrize("yt", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("rt", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("xt", ["f32", "f16", "bf16"])
