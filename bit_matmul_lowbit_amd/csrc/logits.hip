@@ -321,6 +321,10 @@ __global__ __launch_bounds__(256) void logits_top1_kernel(const uint64_t* __rest
 // work-groups of 1024 threads to a compute unit) pays where lists are long:
 // 64 x 151936 with lists of 32768 takes 27 us against 32 with parts of 8192, of
 // 4096 25.2 against 25.3, and 256 x 151936 with lists of 4096 85 against 74.
+// Threads: 512 for parts of 4096 (45 x 44490, lists of 23821: 15.4 us against
+// 18.5 with 256; 64 x 32000, lists of 2048: 11.7 against 13.6), 256 for 2048 (8 x
+// 151936, lists of 4096: 10.1 against 10.4 with 512), 512 for 8192 (64 x 128000,
+// lists of 4096: 24.9 against 27.3 with 1024).
 constexpr int kLargePart = 19456;
 int part_size(int64_t n, int64_t b, int64_t tcap) {
   auto enough = [&](int r) { return (n + r - 1) / r * b >= 384; };
@@ -343,7 +347,7 @@ void launch_part(const LogitsArgs& a, int parts, uint64_t* part, hipStream_t st)
       hipLaunchKernelGGL((logits_kernel<TYPE, 1024, kLargePart>), grid, dim3(1024), 0, st, a, parts, part);
       break;
     case 8192: hipLaunchKernelGGL((logits_kernel<TYPE, 512, 8192>), grid, dim3(512), 0, st, a, parts, part); break;
-    case 4096: hipLaunchKernelGGL((logits_kernel<TYPE, 256, 4096>), grid, dim3(256), 0, st, a, parts, part); break;
+    case 4096: hipLaunchKernelGGL((logits_kernel<TYPE, 512, 4096>), grid, dim3(512), 0, st, a, parts, part); break;
     case 2048: hipLaunchKernelGGL((logits_kernel<TYPE, 256, 2048>), grid, dim3(256), 0, st, a, parts, part); break;
     default: hipLaunchKernelGGL((logits_kernel<TYPE, 256, 1024>), grid, dim3(256), 0, st, a, parts, part); break;
   }
