@@ -18,7 +18,7 @@
 //   D (16 x 16): lane l, register e holds row 4 (l / 16) + e, column l % 16
 //
 // A small call does both in one launch (lora_small_kernel), others in two:
-// shrink: v^T = A x^T, one work-group per (16 rows of an item, up to 64 of
+// shrink: v^T = A x^T, one work-group per (16 rows of an item, up to 48 of
 // its ranks, slice of k); its eight waves split the slice and are summed
 // through LDS.  The slices' FP32 sums go to the workspace.  Operands taken
 // straight from memory would have neighbouring lanes in 16 different rows,
@@ -275,7 +275,7 @@ template <int XT, int RT, int WAVES>
 __device__ __forceinline__ f32x4 shrink16(const LoraArgs& a, int slot, int rank, int r0, const int* rows,
                                           int here, uint4 (*stage)[1 + RT][16][8], int part, int parts) {
   constexpr int T = 1 + RT;                          // 16-row tiles of a step: x, then A's
-  constexpr int U = RT == 4 ? 2 : RT == 2 ? 3 : 4;   // steps in flight
+  constexpr int U = RT >= 3 ? 2 : RT == 2 ? 3 : 4;   // steps in flight
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, q = lane >> 4;    // as an operand's lane
   const int lr = lane >> 3, lp = lane & 7;   // as a loading lane: rows lr and lr + 8, piece lp
@@ -744,18 +744,22 @@ int64_t shrink_units(int64_t m, int64_t slots) {
 
 // Ranks a work-group of the first product takes, in 16s.  Few rows: 16, for
 // many work-groups, each reading x again (from the cache); many rows: x, the
-// larger operand, is read once per 64 ranks.
+// larger operand, is read once per 48 ranks, which are shared out evenly (with
+// 64 one work-group fills a compute unit's LDS: 4096 x 5120 -> 5120, r 40: 66 us a
+// call against 57, r 64 75 and 71, r 128 103 and 98; 1302 x 13568 -> 6355, ranks
+// 56, 28, 53 and 0: 38 against 41).
 int ranks_per_block(int64_t m, int64_t r, int64_t slots) {
   if (r <= 16 || shrink_units(m, slots) * ((r + 15) / 16) <= 256) return 1;
-  return r <= 32 ? 2 : 4;
+  const int tiles = (int)((r + 15) / 16), groups = (tiles + 2) / 3;
+  return (tiles + groups - 1) / groups;
 }
 
-// k in slices as long as all work-groups run at once (two to a compute unit,
-// one where each takes 64 ranks); a wave keeps at least 64 of k
+// k in slices as long as all work-groups run at once (two to a compute unit); a
+// wave keeps at least 64 of k
 int64_t slices_of(int64_t m, int64_t k, int64_t r, int64_t slots) {
   const int rt = ranks_per_block(m, r, slots);
   const int64_t groups = shrink_units(m, slots) * ((r + rt * 16 - 1) / (rt * 16));
-  int64_t s = (rt == 4 ? 256 : 512) / groups;
+  int64_t s = 512 / groups;
   const int64_t most = k / (64 * kShrinkWaves);
   s = s < most ? s : most;
   return s < 1 ? 1 : (s > kMaxSlices ? kMaxSlices : s);
@@ -795,7 +799,7 @@ hipError_t launch(const LoraArgs& a, const Plan& plan, float* v, hipStream_t st)
   else if (rt == 2)
     hipLaunchKernelGGL((lora_shrink_kernel<XT, 2, INLINE>), gs, dim3(512), 0, st, a, plan, tm, subs, v);
   else
-    hipLaunchKernelGGL((lora_shrink_kernel<XT, 4, INLINE>), gs, dim3(512), 0, st, a, plan, tm, subs, v);
+    hipLaunchKernelGGL((lora_shrink_kernel<XT, 3, INLINE>), gs, dim3(512), 0, st, a, plan, tm, subs, v);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   // Work-groups: as many as run at once (three to a compute unit) where two
