@@ -39,37 +39,6 @@ __device__ __forceinline__ Raw8<S> load8(const void* p, int64_t at) {
   return r;
 }
 
-// Elements [c, c + 8) of a row at p + i0; past `k` nothing is read and zeros
-// stand.
-template <int S>
-__device__ __forceinline__ Raw8<S> load_part8(const void* p, int64_t i0, int c, int k) {
-  Raw8<S> r;
-  const char* row = static_cast<const char*>(p) + i0 * S;
-  if (c + 8 <= k) {
-    __builtin_memcpy(&r, row + (int64_t)c * S, sizeof(r));
-  } else {
-    // one by one, all on their way together; past the row its last element is
-    // read again and dropped
-    uint32_t e[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int64_t at = (int64_t)(c + j < k ? c + j : k - 1) * S;
-      if constexpr (S == 4) {
-        __builtin_memcpy(&e[j], row + at, 4);
-      } else {
-        uint16_t h;
-        __builtin_memcpy(&h, row + at, 2);
-        e[j] = h;
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) e[j] = c + j < k ? e[j] : 0u;
-#pragma unroll
-    for (int j = 0; j < 2 * S; ++j) r.d[j] = S == 4 ? e[j] : e[2 * (j & 3)] | (e[2 * (j & 3) + 1] << 16);
-  }
-  return r;
-}
-
 template <int S>
 __device__ __forceinline__ void widen(const Raw8<S>& r, int type, float (&v)[8]) {
   if constexpr (S == 4) {
@@ -86,26 +55,36 @@ __device__ __forceinline__ void widen(const Raw8<S>& r, int type, float (&v)[8])
   }
 }
 
-// of the eight elements from `at` on, those from `from` to before `to`
+// all eight, or those from `skip` on
 template <typename T>
-__device__ __forceinline__ void store8_as(void* p, int64_t at, int from, int to, const float (&v)[8]) {
+__device__ __forceinline__ void store8_as(void* p, int64_t at, int skip, const float (&v)[8]) {
   T o[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) o[j] = (T)v[j];
   T* out = static_cast<T*>(p) + at;
-  if (from <= 0 && to >= 8) {
+  if (skip == 0) {
     __builtin_memcpy(out, o, sizeof(o));
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (j >= from && j < to) out[j] = o[j];
+      if (j >= skip) out[j] = o[j];
   }
 }
 
-__device__ __forceinline__ void store8(void* p, int type, int64_t at, int from, int to, const float (&v)[8]) {
-  if (type == 1) store8_as<float>(p, at, from, to, v);
-  else if (type == 2) store8_as<_Float16>(p, at, from, to, v);
-  else store8_as<bf16_t>(p, at, from, to, v);
+__device__ __forceinline__ void store8(void* p, int type, int64_t at, int skip, const float (&v)[8]) {
+  if (type == 1) store8_as<float>(p, at, skip, v);
+  else if (type == 2) store8_as<_Float16>(p, at, skip, v);
+  else store8_as<bf16_t>(p, at, skip, v);
+}
+
+// from FP32 vector p, or `none` everywhere where it is not given
+__device__ __forceinline__ void vector8(const float* p, float none, int at, float (&v)[8]) {
+  if (p) {
+    widen<4>(load8<4>(p, at), 1, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = none;
+  }
 }
 
 // Sum over the wave in every lane: DPP adds within 16 lanes and across the
@@ -148,22 +127,20 @@ __device__ __forceinline__ float row_sum(float v, float (*red)[16], int& turn) {
 }
 
 // Rows of up to threads * NV * 8 elements in registers.  SY, SR: bytes per
-// element of y and r.  MODE: kLazy: weights and gate are fetched when they are
-// needed, which leaves registers for rows of several steps.  kAhead: they are
-// fetched with the row, which takes two memory latencies off a small call.
-// kHeld: a work-group takes every gridDim.x-th row, keeps the weights (and a
-// gate that all rows share), and has the next row on its way while it works on
-// one (11886 x 1621, FP16, a norm on both sides, gated: 78 -> 49 us).
-enum { kLazy, kAhead, kHeld };
-template <int S>
-struct Bytes {
-  static constexpr int value = S;
-};
+// element of y and r.  MODE:
+//   kLate : weights and gate are fetched when they are needed, which leaves
+//           registers for rows of several steps
+//   kExact: the same for rows that fill every step of every thread
+//   kAhead: they are fetched with the row, which takes two memory latencies off
+//           a small call
+//   kHeld : a work-group takes every gridDim.x-th row, keeps the weights (and a
+//           gate that all rows share), and has the next row on its way while it
+//           works on one (11886 x 1621, FP16, a norm on both sides, gated: 78 ->
+//           50 us)
 // A thread's elements in step n are the eight from c on.  Where fewer are left
 // it holds the row's last eight (k >= 8) and passes over the first `skip` of
-// them, which are another thread's: no load has a short form.  kLazy loads what
-// is left one by one instead, which takes fewer registers (63 for 72: 16384 x
-// 5120, BF16, 143 us for 148).
+// them, which are another thread's: no load has a short form.
+enum { kLate, kExact, kAhead, kHeld };
 template <bool WAVE, int SY, int SR, int NV, int MODE>
 __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(NormArgs a) {
   __shared__ __align__(16) float red[2][16];
@@ -177,60 +154,39 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(NormArgs a) {
   const float inv_k = 1.0f / (float)k;
   int turn = 0;
 
-  auto col = [&](int n) __attribute__((always_inline)) { return (n * threads + t) * 8; };
+  constexpr bool kLater = MODE == kLate || MODE == kExact;
   int at[NV], skip[NV];
 #pragma unroll
   for (int n = 0; n < NV; ++n) {
-    at[n] = MODE == kLazy || col(n) < k - 8 ? col(n) : k - 8;
-    skip[n] = MODE == kLazy ? 0 : col(n) - at[n];
+    const int c = (n * threads + t) * 8;
+    at[n] = MODE == kExact || c < k - 8 ? c : k - 8;
+    skip[n] = c - at[n];
   }
-  auto mine = [&](int n, int j) __attribute__((always_inline)) {
-    return MODE == kLazy ? col(n) + j < k : j >= skip[n];
-  };
-  auto any = [&](int n) __attribute__((always_inline)) { return MODE == kLazy ? col(n) < k : skip[n] < 8; };
-  auto load = [&](auto bytes, const void* p, int64_t i0, int n) __attribute__((always_inline)) {
-    constexpr int S = decltype(bytes)::value;
-    if constexpr (MODE == kLazy) return load_part8<S>(p, i0, col(n), k);
-    else return load8<S>(p, i0 + at[n]);
-  };
-  auto store = [&](void* p, int type, int64_t i0, int n, const float (&v)[8]) __attribute__((always_inline)) {
-    if constexpr (MODE == kLazy) store8(p, type, i0 + col(n), 0, k - col(n), v);
-    else store8(p, type, i0 + at[n], skip[n], 8, v);
-  };
-  // from an FP32 vector, or `none` everywhere where it is not given
-  auto vec = [&](const float* p, float none, int n, float (&v)[8]) __attribute__((always_inline)) {
-    if (p) {
-      widen<4>(load(Bytes<4>{}, p, 0, n), 1, v);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = none;
-    }
-  };
   Raw8<SY> yr[NV], yn[NV];
   Raw8<SR> rr[NV], rn[NV];
   auto load_row = [&](Raw8<SY> (&y)[NV], Raw8<SR> (&r)[NV], int64_t row) __attribute__((always_inline)) {
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
-      if (a.y) y[n] = load(Bytes<SY>{}, a.y, row * a.ldy, n);
-      r[n] = load(Bytes<SR>{}, a.r, row * a.ldr, n);
+      if (a.y) y[n] = load8<SY>(a.y, row * a.ldy + at[n]);
+      r[n] = load8<SR>(a.r, row * a.ldr + at[n]);
     }
   };
   load_row(yr, rr, i);
   float post_w[NV][8], post_b[NV][8], gate[NV][8], pre_w[NV][8], pre_b[NV][8];
   auto gate8 = [&](int n, int64_t row) __attribute__((always_inline)) {
-    if (a.gate_type == 1) widen<4>(load(Bytes<4>{}, a.gate, row * a.ldg, n), 1, gate[n]);
-    else widen<2>(load(Bytes<2>{}, a.gate, row * a.ldg, n), a.gate_type, gate[n]);
+    if (a.gate_type == 1) widen<4>(load8<4>(a.gate, row * a.ldg + at[n]), 1, gate[n]);
+    else widen<2>(load8<2>(a.gate, row * a.ldg + at[n]), a.gate_type, gate[n]);
   };
-  if constexpr (MODE != kLazy) {
+  if constexpr (!kLater) {
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
       if (a.post != 0) {
-        vec(a.post_w, 1.0f, n, post_w[n]);
-        vec(a.post_b, 0.0f, n, post_b[n]);
+        vector8(a.post_w, 1.0f, at[n], post_w[n]);
+        vector8(a.post_b, 0.0f, at[n], post_b[n]);
       }
       if (a.pre != 0) {
-        vec(a.pre_w, 1.0f, n, pre_w[n]);
-        vec(a.pre_b, 0.0f, n, pre_b[n]);
+        vector8(a.pre_w, 1.0f, at[n], pre_w[n]);
+        vector8(a.pre_b, 0.0f, at[n], pre_b[n]);
       }
       if (a.gate) gate8(n, i);
     }
@@ -250,7 +206,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(NormArgs a) {
 #pragma unroll
         for (int n = 0; n < NV; ++n)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) s += MODE == kLazy || mine(n, j) ? u[n][j] : 0.0f;
+          for (int j = 0; j < 8; ++j) s += j >= skip[n] ? u[n][j] : 0.0f;
         mean = row_sum<WAVE>(s, red, turn) * inv_k;
       }
       if (a.post != 0) {
@@ -259,24 +215,24 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(NormArgs a) {
         for (int n = 0; n < NV; ++n)
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float d = mine(n, j) ? u[n][j] - mean : 0.0f;
+            const float d = j >= skip[n] ? u[n][j] - mean : 0.0f;
             s += d * d;
           }
         rs = 1.0f / sqrtf(row_sum<WAVE>(s, red, turn) * inv_k + a.eps);
       }
 #pragma unroll
       for (int n = 0; n < NV; ++n) {
-        if (any(n)) {
+        if (skip[n] < 8) {
           if (a.post != 0) {
-            if constexpr (MODE == kLazy) {
-              vec(a.post_w, 1.0f, n, post_w[n]);
-              vec(a.post_b, 0.0f, n, post_b[n]);
+            if constexpr (kLater) {
+              vector8(a.post_w, 1.0f, at[n], post_w[n]);
+              vector8(a.post_b, 0.0f, at[n], post_b[n]);
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) u[n][j] = (u[n][j] - mean) * rs * post_w[n][j] + post_b[n][j];
           }
           if (a.gate) {
-            if constexpr (MODE == kLazy) gate8(n, i);
+            if constexpr (kLater) gate8(n, i);
 #pragma unroll
             for (int j = 0; j < 8; ++j) u[n][j] *= gate[n][j];
             if (more && a.ldg != 0) gate8(n, next);
@@ -293,7 +249,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(NormArgs a) {
     if (a.r_out) {
 #pragma unroll
       for (int n = 0; n < NV; ++n) {
-        if (any(n)) store(a.r_out, a.r_type, i * a.ldro, n, v[n]);
+        if (skip[n] < 8) store8(a.r_out, a.r_type, i * a.ldro + at[n], skip[n], v[n]);
       }
     }
     if (a.x_out) {
@@ -303,7 +259,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(NormArgs a) {
 #pragma unroll
         for (int n = 0; n < NV; ++n)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) s += mine(n, j) ? v[n][j] : 0.0f;
+          for (int j = 0; j < 8; ++j) s += j >= skip[n] ? v[n][j] : 0.0f;
         mean = row_sum<WAVE>(s, red, turn) * inv_k;
       }
       if (a.pre != 0) {
@@ -312,23 +268,23 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(NormArgs a) {
         for (int n = 0; n < NV; ++n)
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float d = mine(n, j) ? v[n][j] - mean : 0.0f;
+            const float d = j >= skip[n] ? v[n][j] - mean : 0.0f;
             s += d * d;
           }
         rs = 1.0f / sqrtf(row_sum<WAVE>(s, red, turn) * inv_k + a.eps);
       }
 #pragma unroll
       for (int n = 0; n < NV; ++n) {
-        if (!any(n)) continue;
+        if (skip[n] >= 8) continue;
         if (a.pre != 0) {
-          if constexpr (MODE == kLazy) {
-            vec(a.pre_w, 1.0f, n, pre_w[n]);
-            vec(a.pre_b, 0.0f, n, pre_b[n]);
+          if constexpr (kLater) {
+            vector8(a.pre_w, 1.0f, at[n], pre_w[n]);
+            vector8(a.pre_b, 0.0f, at[n], pre_b[n]);
           }
 #pragma unroll
           for (int j = 0; j < 8; ++j) v[n][j] = (v[n][j] - mean) * rs * pre_w[n][j] + pre_b[n][j];
         }
-        store(a.x_out, a.x_type, i * a.ldx, n, v[n]);
+        store8(a.x_out, a.x_type, i * a.ldx + at[n], skip[n], v[n]);
       }
     }
     if (!more) return;
@@ -452,6 +408,12 @@ hipError_t launch_norm_residual(const NormArgs& a, hipStream_t st) {
   const int vectors = !!a.post_w + !!a.post_b + !!a.pre_w + !!a.pre_b + (a.gate && a.ldg == 0);
   const int bytes = (a.y ? (a.y_type == 1 ? 4 : 2) : 0) + (a.r_type == 1 ? 4 : 2);
   const bool keep = 4 * vectors >= (bytes == 8 ? 12 : bytes);
+  // nv steps of every thread filled, and little besides the row: there is
+  // something to gain (16384 x 5120, BF16: 143 us for 151; 4096 x 5120 with two
+  // layer norms and a gate 54 for 49, 16384 x 5121 202 for 197)
+  const auto exact = [&](int nv) {
+    return many && a.k % (nv * 512) == 0 && vectors + (a.gate && a.ldg != 0) <= 2;
+  };
   // as many work-groups of `waves` waves as run at once (16 waves to a compute
   // unit), each with as many of the rows
   const auto running = [](int64_t waves) { return 256 * 16 / waves; };
@@ -462,21 +424,27 @@ hipError_t launch_norm_residual(const NormArgs& a, hipStream_t st) {
   // short rows, many of them: one wave each, no barriers (12030 x 128, one weight
   // and a gate per row: 8.6 us kept, 12.8 read again)
   if (chunks <= 64 && many) return launch_as<true, 1, kHeld>(a, held((a.m + 3) / 4, 4), dim3(256), st);
-  if (chunks <= 128 && many)
-    return keep ? launch_as<true, 2, kHeld>(a, held((a.m + 3) / 4, 4), dim3(256), st)
-                : launch_as<true, 2, kLazy>(a, dim3((unsigned)((a.m + 3) / 4)), dim3(256), st);
+  if (chunks <= 128 && many) {
+    if (keep) return launch_as<true, 2, kHeld>(a, held((a.m + 3) / 4, 4), dim3(256), st);
+    const dim3 g((unsigned)((a.m + 3) / 4));
+    return exact(2) ? launch_as<true, 2, kExact>(a, g, dim3(256), st) : launch_as<true, 2, kLate>(a, g, dim3(256), st);
+  }
   auto block = [&](int64_t nv) { return dim3((unsigned)((chunks + nv * 64 - 1) / (nv * 64) * 64)); };
   // Many long rows: 16 elements a thread, so that more work-groups of fewer
   // waves share a compute unit (16384 x 5120 BF16: 143 us, with 8 elements 184,
   // with 32 161; 4096 x 4096 with the weights kept 31, else 38).
   if (chunks <= 1024 && !(many && chunks > 512)) {
     const int64_t waves = (chunks + 63) / 64;
-    if (many && !keep) return launch_as<false, 1, kLazy>(a, grid, block(1), st);
+    if (many && !keep)
+      return exact(1) ? launch_as<false, 1, kExact>(a, grid, block(1), st)
+                      : launch_as<false, 1, kLate>(a, grid, block(1), st);
     if (many && a.m >= 2 * running(waves)) return launch_as<false, 1, kHeld>(a, held(a.m, waves), block(1), st);
     return launch_as<false, 1, kAhead>(a, grid, block(1), st);
   }
-  if (chunks <= 2048) return launch_as<false, 2, kLazy>(a, grid, block(2), st);
-  if (chunks <= 4096) return launch_as<false, 4, kLazy>(a, grid, block(4), st);
+  if (chunks <= 2048)
+    return exact(2) ? launch_as<false, 2, kExact>(a, grid, block(2), st) : launch_as<false, 2, kLate>(a, grid, block(2), st);
+  if (chunks <= 4096)
+    return exact(4) ? launch_as<false, 4, kExact>(a, grid, block(4), st) : launch_as<false, 4, kLate>(a, grid, block(4), st);
   hipLaunchKernelGGL(norm_long_kernel, grid, dim3(1024), 0, st, a);
   return hipGetLastError();
 }
