@@ -10,16 +10,14 @@
 // and step, raw, as they were loaded) while its sums are formed: the
 // deviations of a layer norm are summed in a second sweep over the registers,
 // which keeps a small variance beside a large mean.  A row belongs to one
-// work-group, or to one wave where rows are short and many, and where many rows
-// share weights that weigh as much as a row, a work-group keeps them over
-// several rows; rows longer than the registers of a work-group hold are read
-// again for every sum.
+// work-group, or to one wave where rows are short and many; rows longer than the
+// registers of a work-group hold are read again for every sum.
 //
 // What bounds it: memory.  16384 x 5120, everything BF16, a norm on both sides:
-// 142 to 150 us for 671 MB (4.5 to 4.7 TB/s; a large copy reaches 4.8).  11886 x
-// 1624, FP16, gated: 42 us for 154 MB (3.7).  Small calls are a launch and two
-// or three latencies: 1 x 2048 2.3 us, 8 x 5120 with a gate 4.5 us, 777 x 1283
-// with layer norms 6.2 us.
+// 125 us for 671 MB (5.4 TB/s; a large copy of torch's reaches 4.8); 4096 x 4096
+// 28 us (4.8); 11886 x 1621, FP16, gated, 46 us for 154 MB (3.3).  Small calls
+// are a launch and two or three latencies: 1 x 2048 2.3 us, 8 x 5120 with a gate
+// 4.5 us, 777 x 1283 with layer norms 6.2 us.
 #include "common.h"
 
 namespace lowbit {
@@ -130,7 +128,8 @@ __device__ __forceinline__ float row_sum(float v, float (*red)[16], int& turn) {
 // element of y and r.  MODE:
 //   kLate : weights and gate are fetched when they are needed, which leaves
 //           registers for rows of several steps
-//   kExact: the same for rows that fill every step of every thread
+//   kExact: the same for rows of whole eights: no masks but one a step, no
+//           short stores (16384 x 5120: 143 -> 125 us, 8192 x 7000 107 -> 90)
 //   kAhead: they are fetched with the row, which takes two memory latencies off
 //           a small call
 //   kHeld : a work-group takes every gridDim.x-th row, keeps the weights (and a
@@ -159,9 +158,25 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(NormArgs a) {
 #pragma unroll
   for (int n = 0; n < NV; ++n) {
     const int c = (n * threads + t) * 8;
-    at[n] = MODE == kExact || c < k - 8 ? c : k - 8;
-    skip[n] = c - at[n];
+    at[n] = c < k - 8 ? c : k - 8;
+    skip[n] = MODE == kExact ? (c < k ? 0 : 8) : c - at[n];
   }
+  // sums over this thread's elements of step n
+  auto sum8 = [&](const float (&w)[8], int n) __attribute__((always_inline)) {
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s += MODE == kExact || j >= skip[n] ? w[j] : 0.0f;
+    return MODE == kExact && skip[n] != 0 ? 0.0f : s;
+  };
+  auto square8 = [&](const float (&w)[8], float mean, int n) __attribute__((always_inline)) {
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float d = MODE == kExact || j >= skip[n] ? w[j] - mean : 0.0f;
+      s += d * d;
+    }
+    return MODE == kExact && skip[n] != 0 ? 0.0f : s;
+  };
   Raw8<SY> yr[NV], yn[NV];
   Raw8<SR> rr[NV], rn[NV];
   auto load_row = [&](Raw8<SY> (&y)[NV], Raw8<SR> (&r)[NV], int64_t row) __attribute__((always_inline)) {
@@ -204,20 +219,13 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(NormArgs a) {
       if (a.post == 2) {
         float s = 0.0f;
 #pragma unroll
-        for (int n = 0; n < NV; ++n)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) s += j >= skip[n] ? u[n][j] : 0.0f;
+        for (int n = 0; n < NV; ++n) s += sum8(u[n], n);
         mean = row_sum<WAVE>(s, red, turn) * inv_k;
       }
       if (a.post != 0) {
         float s = 0.0f;
 #pragma unroll
-        for (int n = 0; n < NV; ++n)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float d = j >= skip[n] ? u[n][j] - mean : 0.0f;
-            s += d * d;
-          }
+        for (int n = 0; n < NV; ++n) s += square8(u[n], mean, n);
         rs = 1.0f / sqrtf(row_sum<WAVE>(s, red, turn) * inv_k + a.eps);
       }
 #pragma unroll
@@ -249,7 +257,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(NormArgs a) {
     if (a.r_out) {
 #pragma unroll
       for (int n = 0; n < NV; ++n) {
-        if (skip[n] < 8) store8(a.r_out, a.r_type, i * a.ldro + at[n], skip[n], v[n]);
+        if (skip[n] < 8) store8(a.r_out, a.r_type, i * a.ldro + at[n], MODE == kExact ? 0 : skip[n], v[n]);
       }
     }
     if (a.x_out) {
@@ -257,20 +265,13 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(NormArgs a) {
       if (a.pre == 2) {
         float s = 0.0f;
 #pragma unroll
-        for (int n = 0; n < NV; ++n)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) s += j >= skip[n] ? v[n][j] : 0.0f;
+        for (int n = 0; n < NV; ++n) s += sum8(v[n], n);
         mean = row_sum<WAVE>(s, red, turn) * inv_k;
       }
       if (a.pre != 0) {
         float s = 0.0f;
 #pragma unroll
-        for (int n = 0; n < NV; ++n)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float d = j >= skip[n] ? v[n][j] - mean : 0.0f;
-            s += d * d;
-          }
+        for (int n = 0; n < NV; ++n) s += square8(v[n], mean, n);
         rs = 1.0f / sqrtf(row_sum<WAVE>(s, red, turn) * inv_k + a.eps);
       }
 #pragma unroll
@@ -284,7 +285,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_kernel(NormArgs a) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) v[n][j] = (v[n][j] - mean) * rs * pre_w[n][j] + pre_b[n][j];
         }
-        store8(a.x_out, a.x_type, i * a.ldx + at[n], skip[n], v[n]);
+        store8(a.x_out, a.x_type, i * a.ldx + at[n], MODE == kExact ? 0 : skip[n], v[n]);
       }
     }
     if (!more) return;
@@ -400,20 +401,15 @@ hipError_t launch_norm_residual(const NormArgs& a, hipStream_t st) {
     return hipGetLastError();
   }
   const bool many = a.m >= 1024;
-  // Many rows: weights are kept where a row would read at least as much of them
-  // as of itself (11886 x 1624, FP16, four of them: 65 us read again, 42 kept;
-  // 4096 x 2048, BF16, one: 15.4 and 14.6; the same in FP32 26 and 28; none but
-  // the residual 37 and 41).  Rows of FP32 on both sides, which take more
-  // registers, need more of them (4096 x 2048, two: 28 and 30; four: 83 and 81).
+  const bool exact = a.k % 8 == 0;
+  // Many rows: those of whole eights need nothing else to come near the memory's
+  // rate; of others the weights are kept where a row would read at least as much
+  // of them as of itself (11886 x 1621, FP16, four of them: 78 us read again, 50
+  // kept).  Rows of FP32 on both sides, which take more registers, need more of
+  // them (4096 x 2048, two: 28 and 30; four: 83 and 81).
   const int vectors = !!a.post_w + !!a.post_b + !!a.pre_w + !!a.pre_b + (a.gate && a.ldg == 0);
   const int bytes = (a.y ? (a.y_type == 1 ? 4 : 2) : 0) + (a.r_type == 1 ? 4 : 2);
-  const bool keep = 4 * vectors >= (bytes == 8 ? 12 : bytes);
-  // nv steps of every thread filled, and little besides the row: there is
-  // something to gain (16384 x 5120, BF16: 143 us for 151; 4096 x 5120 with two
-  // layer norms and a gate 54 for 49, 16384 x 5121 202 for 197)
-  const auto exact = [&](int nv) {
-    return many && a.k % (nv * 512) == 0 && vectors + (a.gate && a.ldg != 0) <= 2;
-  };
+  const bool keep = !exact && 4 * vectors >= (bytes == 8 ? 12 : bytes);
   // as many work-groups of `waves` waves as run at once (16 waves to a compute
   // unit), each with as many of the rows
   const auto running = [](int64_t waves) { return 256 * 16 / waves; };
@@ -427,24 +423,29 @@ hipError_t launch_norm_residual(const NormArgs& a, hipStream_t st) {
   if (chunks <= 128 && many) {
     if (keep) return launch_as<true, 2, kHeld>(a, held((a.m + 3) / 4, 4), dim3(256), st);
     const dim3 g((unsigned)((a.m + 3) / 4));
-    return exact(2) ? launch_as<true, 2, kExact>(a, g, dim3(256), st) : launch_as<true, 2, kLate>(a, g, dim3(256), st);
+    return exact ? launch_as<true, 2, kExact>(a, g, dim3(256), st) : launch_as<true, 2, kLate>(a, g, dim3(256), st);
   }
   auto block = [&](int64_t nv) { return dim3((unsigned)((chunks + nv * 64 - 1) / (nv * 64) * 64)); };
   // Many long rows: 16 elements a thread, so that more work-groups of fewer
-  // waves share a compute unit (16384 x 5120 BF16: 143 us, with 8 elements 184,
-  // with 32 161; 4096 x 4096 with the weights kept 31, else 38).
+  // waves share a compute unit (16384 x 5120 BF16: 125 us, with 8 elements 137).
   if (chunks <= 1024 && !(many && chunks > 512)) {
     const int64_t waves = (chunks + 63) / 64;
     if (many && !keep)
-      return exact(1) ? launch_as<false, 1, kExact>(a, grid, block(1), st)
-                      : launch_as<false, 1, kLate>(a, grid, block(1), st);
+      return exact ? launch_as<false, 1, kExact>(a, grid, block(1), st)
+                   : launch_as<false, 1, kLate>(a, grid, block(1), st);
     if (many && a.m >= 2 * running(waves)) return launch_as<false, 1, kHeld>(a, held(a.m, waves), block(1), st);
     return launch_as<false, 1, kAhead>(a, grid, block(1), st);
   }
-  if (chunks <= 2048)
-    return exact(2) ? launch_as<false, 2, kExact>(a, grid, block(2), st) : launch_as<false, 2, kLate>(a, grid, block(2), st);
+  // Above 12288 a work-group of 16 elements a thread no longer has a second one
+  // beside it, unless y and r are FP32 with its fewer conversions (4096 x 16384,
+  // BF16: 32 elements 109 us, 16 117; 2048 x 16384, FP32: 100 and 95).
+  const bool whole = many && exact;
+  if (chunks <= (whole && bytes < 8 ? 1536 : 2048))
+    return whole ? launch_as<false, 2, kExact>(a, grid, block(2), st)
+                 : launch_as<false, 2, kLate>(a, grid, block(2), st);
   if (chunks <= 4096)
-    return exact(4) ? launch_as<false, 4, kExact>(a, grid, block(4), st) : launch_as<false, 4, kLate>(a, grid, block(4), st);
+    return whole ? launch_as<false, 4, kExact>(a, grid, block(4), st)
+                 : launch_as<false, 4, kLate>(a, grid, block(4), st);
   hipLaunchKernelGGL(norm_long_kernel, grid, dim3(1024), 0, st, a);
   return hipGetLastError();
 }
