@@ -90,7 +90,8 @@ def test_matches_plain_form(m, k, post, pre, gate):
 
 
 @pytest.mark.parametrize("m,k", [(1024, 7), (1500, 8), (1031, 9), (9000, 128), (5003, 511), (4100, 514), (5000, 1001),
-                                 (4300, 1025), (1100, 4095), (700, 4096), (1100, 5119), (1030, 8200)])
+                                 (4300, 1025), (1100, 4095), (700, 4096), (1100, 5119), (1030, 8200),
+                                 (1100, 640), (1030, 1024), (1500, 1032), (1100, 4096), (1024, 12296)])
 @pytest.mark.parametrize("yt,rt,xt", [("f32", "f32", "f16"), ("bf16", "bf16", "bf16"), ("f16", "f32", "bf16")])
 @pytest.mark.parametrize("post,pre,gate,pad", [("none", "none", "none", 0), ("rms", "rms", "none", 3),
                                                ("layer", "layer", "channel", 0), ("rms", "layer", "row", 8)])
