@@ -12,7 +12,8 @@
 // wave of every work-group for itself (no launch, no memory); more are sorted
 // by one work-group first (lora_plan_kernel).
 //
-// Both products run on v_mfma_f32_16x16x32.
+// The first product runs on v_mfma_f32_16x16x32, the second on that (BF16) or on
+// v_mfma_f32_16x16x4 (FP16; a lane holds one value of an operand's four columns).
 //   A operand (16 x 32): lane l holds row l % 16, 8 values at 8 (l / 16)
 //   B operand (32 x 16): lane l holds column l % 16, 8 values at 8 (l / 16)
 //   D (16 x 16): lane l, register e holds row 4 (l / 16) + e, column l % 16
@@ -26,10 +27,10 @@
 // loads 128 contiguous bytes of a row by eight lanes instead and passes them
 // to the lanes that need them through LDS of its own.
 // expand: y += v B^T, one work-group per (item, share of the outputs, 256 at a
-// time); B goes through LDS in the same manner.  v is summed over the slices,
-// scaled, and split into 16-bit pieces whose sum holds it to FP32's precision
-// or nearly (FP16: two pieces of a row scaled by a power of two, 22 bits; BF16:
-// three pieces, 24 bits), since a single 16-bit v would be the least exact
+// time); B goes through LDS in the same manner.  v is summed over the slices and
+// scaled.  With BF16 it is split into three pieces whose sum holds its 24 bits,
+// with FP16, which reaches less far than a row's inner values may lie apart, it
+// stays FP32 and B is widened: a single 16-bit v would be the least exact
 // value of the whole sum.  No atomics anywhere: every value has one writer and
 // its sum one order.
 //
@@ -55,24 +56,41 @@ constexpr int kShrinkWaves = 8;
 constexpr int kTilesN = 4;                 // 16-output tiles of a wave in expand
 constexpr int kWaveN = 16 * kTilesN;       // 64 outputs per wave
 constexpr int kBlockN = 4 * kWaveN;        // 256 outputs per work-group
+constexpr int kFewRows = 4;                // rows of an FP16 item that go without matrix instructions
 constexpr int kMaxSlots = 4096;
 constexpr int kMaxSlices = 8;              // slices of k at most
 
 template <int XT> struct Mma;
 template <> struct Mma<2> {
-  static constexpr int pieces = 2;
   static __device__ __forceinline__ f32x4 run(uint4 a, uint4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
                                                   __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
   }
 };
 template <> struct Mma<3> {
-  static constexpr int pieces = 3;
   static __device__ __forceinline__ f32x4 run(uint4 a, uint4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
   }
 };
+
+// How v stands in LDS for the second product: as FP32, or as BF16 pieces, each
+// [tm][pitch]; the pad after a row's ranks moves the next one to other banks.
+template <int XT> struct Held;
+template <> struct Held<2> {
+  typedef float type;
+  static constexpr int pieces = 1, pad = 4;
+};
+template <> struct Held<3> {
+  typedef bf16_t type;
+  static constexpr int pieces = 3, pad = 8;
+};
+template <int XT>
+constexpr int inner_pitch(int r) { return (r + 31) / 32 * 32 + Held<XT>::pad; }
+template <int XT>
+constexpr size_t inner_bytes(int tm, int r) {
+  return sizeof(typename Held<XT>::type) * Held<XT>::pieces * tm * inner_pitch<XT>(r);
+}
 
 __device__ __forceinline__ int rank_of(const LoraArgs& a, int64_t s) {
   if (!a.ranks) return (int)a.r;
@@ -382,14 +400,9 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs a, Plan plan,
     *reinterpret_cast<f32x4*>(v + ((int64_t)blockIdx.z * a.m + rows[sub * 16 + c]) * a.r + j) = sum;
 }
 
-// FP32 value -> its pieces; `scale` is a power of two (1 for BF16)
-__device__ __forceinline__ void split(float v, float scale, _Float16 (&p)[2]) {
-  v *= scale;
-  p[0] = (_Float16)v;
-  const float rest = v - (float)p[0];
-  p[1] = __builtin_isfinite((float)p[0]) ? (_Float16)rest : (_Float16)0.0f;
-}
-__device__ __forceinline__ void split(float v, float, bf16_t (&p)[3]) {
+// FP32 value -> its pieces
+__device__ __forceinline__ void split(float v, float (&p)[1]) { p[0] = v; }
+__device__ __forceinline__ void split(float v, bf16_t (&p)[3]) {
   p[0] = (bf16_t)v;
   const bool fine = __builtin_isfinite((float)p[0]);
   const float rest = fine ? v - (float)p[0] : 0.0f;
@@ -397,20 +410,86 @@ __device__ __forceinline__ void split(float v, float, bf16_t (&p)[3]) {
   p[2] = (bf16_t)(rest - (float)p[1]);
 }
 
-// largest of 16 consecutive lanes, in each of them
-template <int ROR>
-__device__ __forceinline__ float max_ror(float v) {
-  return fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x120 + ROR,
-                                                                        0xF, 0xF, true)));
-}
-__device__ __forceinline__ float max16(float v) { return max_ror<1>(max_ror<2>(max_ror<4>(max_ror<8>(v)))); }
-
-// largest magnitude of the finite ones of four values
-__device__ __forceinline__ float finite_max(f32x4 v) {
-  float top = 0.0f;
+// acc[s][t] += the products of 32 ranks: of v's rows (`v`: at this lane's first
+// rank, in its row of the first of SUBS 16-row parts) and of B's in `w`.
+//
+// FP16: FP32 products, a quarter of the rate of two FP16 pieces, but a piece's
+// smallest step (2^-38 of the row's largest value) and what its zeros make of an
+// infinite entry of B do not show in y.  HALVES: a lane's ranks are four of the
+// first 16 and, if `both`, four of the others, so that 16 ranks take half of the
+// instructions (342 rows, r 16, 768 -> 12378: 27.9 -> 24.7 us a call; FP16 pieces
+// 22.7).  4096 rows, r 128, 5120 -> 5120: 139 us, FP16 pieces 112.
+template <int SUBS, bool HALVES>
+__device__ __forceinline__ void multiply(const float* v, int pitch, int, int count, bool both,
+                                         const uint4 (&w)[kTilesN], f32x4 (&acc)[SUBS][kTilesN]) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) top = fabsf(v[e]) <= 3.4028235e38f ? fmaxf(top, fabsf(v[e])) : top;
-  return top;
+  for (int h = 0; h < 2; ++h) {
+    if (h == 1 && !both) break;
+    f32x4 a[SUBS];
+#pragma unroll
+    for (int s = 0; s < SUBS; ++s)
+      if (s * 16 < count) a[s] = *reinterpret_cast<const f32x4*>(v + s * 16 * pitch + h * (HALVES ? 16 : 4));
+#pragma unroll
+    for (int t = 0; t < kTilesN; ++t) {
+      const f16x8 b = __builtin_bit_cast(f16x8, w[t]);
+#pragma unroll
+      for (int s = 0; s < SUBS; ++s) {
+        if (s * 16 < count) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            acc[s][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[s][i], (float)b[h * 4 + i], acc[s][t], 0, 0, 0);
+        }
+      }
+    }
+  }
+}
+template <int SUBS, bool>
+__device__ __forceinline__ void multiply(const bf16_t* v, int pitch, int tm, int count, bool,
+                                         const uint4 (&w)[kTilesN], f32x4 (&acc)[SUBS][kTilesN]) {
+#pragma unroll
+  for (int s = 0; s < SUBS; ++s) {
+    if (s * 16 < count) {
+#pragma unroll
+      for (int p = 0; p < Held<3>::pieces; ++p) {
+        const uint4 a = *reinterpret_cast<const uint4*>(v + (p * tm + s * 16) * pitch);
+#pragma unroll
+        for (int t = 0; t < kTilesN; ++t) acc[s][t] = Mma<3>::run(a, w[t], acc[s][t]);
+      }
+    }
+  }
+}
+
+// FP16, up to kFewRows rows, for which a matrix instruction's 16 would be mostly
+// empty: each lane sums its own 8 ranks (`v`: at the first of them, of the first
+// row), and few_end() joins the four lanes of an output.  8 rows of 8 adapters, r
+// 64, 5120 -> 34816: 16.8 us a call, 19.9 by matrix instructions; 1 x 2048 -> 6144,
+// r 16: 6.8 and 7.5.
+__device__ __forceinline__ void few(const float* v, int pitch, int count, const uint4 (&w)[kTilesN],
+                                    f32x4 (&acc)[kTilesN]) {
+#pragma unroll
+  for (int e = 0; e < kFewRows; ++e) {
+    if (e < count) {
+      float a[8];
+      __builtin_memcpy(a, __builtin_assume_aligned(v + e * pitch, 16), 32);
+#pragma unroll
+      for (int t = 0; t < kTilesN; ++t) {
+        const f16x8 b = __builtin_bit_cast(f16x8, w[t]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[t][e] = __builtin_fmaf((float)b[i], a[i], acc[t][e]);
+      }
+    }
+  }
+}
+__device__ __forceinline__ void few_end(int count, f32x4 (&acc)[kTilesN]) {
+#pragma unroll
+  for (int e = 0; e < kFewRows; ++e)
+    if (e < count) {
+#pragma unroll
+      for (int t = 0; t < kTilesN; ++t) {
+        const float half = acc[t][e] + __shfl_xor(acc[t][e], 16, 64);
+        acc[t][e] = half + __shfl_xor(half, 32, 64);
+      }
+    }
 }
 
 // four consecutive outputs of a row, as they are stored
@@ -419,7 +498,7 @@ struct Out4 {
   uint32_t d[YT == 1 ? 4 : 2];
 };
 
-// + add * un, rounded once
+// + what is added, rounded once
 __device__ __forceinline__ Out4<1> add4(Out4<1> z, float a0, float a1, float a2, float a3) {
   const float add[4] = {a0, a1, a2, a3};
 #pragma unroll
@@ -470,22 +549,24 @@ __device__ __forceinline__ void store_tail(const Out4<3>& z, bf16_t* p, int n) {
 // BF16).  The first outputs and the first ranks of B are on their way while v
 // is made ready: first() brings about what inner(row, j), four sums of v from
 // rank j on, needs.
-template <int XT, int YT, int SUBS, int WAVES, class First, class Inner>
-__device__ __forceinline__ void expand_item(const LoraArgs& a, const Item& it, const Found& found, float* unscale,
-                                            typename Elem<XT>::type* pieces, int tm, uint4* staged, int share,
+template <int XT, int YT, bool INLINE, int SUBS, int WAVES, class First, class Inner>
+__device__ __forceinline__ void expand_item(const LoraArgs& a, const Item& it, const Found& found,
+                                            typename Held<XT>::type* pieces, int tm, uint4* staged, int share,
                                             int shares, First first, Inner inner) {
   // Four lanes load 64 contiguous bytes of a row of B and pass them on through
   // LDS, as in shrink: 8 rows of 8 adapters 17.8 -> 16.8 us a call, 4096 rows
   // 101.4 -> 97.8 (not in the small kernel, whose first product holds that LDS).
   constexpr bool kStaged = WAVES == 4;
-  constexpr int P = Mma<XT>::pieces;
+  constexpr int P = Held<XT>::pieces;
+  constexpr bool kHalves = XT == 2 && !INLINE;  // a lane's ranks of 32: 4 q .. + 3 and those 16 on; else 8 q .. + 7
+  typedef typename Held<XT>::type V;
   typedef typename Elem<XT>::type X;
   typedef typename Elem<YT>::type Y;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 15, q = lane >> 4;
   const int slot = it.slot, count = it.count, rank = it.rank;
   const float scale = it.scale;
-  const int chunks = (rank + 31) / 32, pitch = chunks * 32 + 8;  // 16 bytes past: other banks
+  const int chunks = (rank + 31) / 32, pitch = inner_pitch<XT>(rank);
   const X* bs = static_cast<const X*>(a.b) + (int64_t)slot * a.n * a.r;
   // where row 4 q + e of a part, one of the item's, has its outputs n0 + 4 c
   // ...; made anew at each use (kept, the pointers would cost a wave of occupancy)
@@ -493,6 +574,9 @@ __device__ __forceinline__ void expand_item(const LoraArgs& a, const Item& it, c
     return static_cast<Y*>(a.y) + (found.y_at[s * 16 + q * 4 + e] + n0 + c * 4);
   };
 
+  // by how much the four pieces of row `r` of B change places in LDS, so that 32
+  // lanes that read 8 bytes of 16 rows find them in different banks
+  auto turn = [](int r) __attribute__((always_inline)) { return (r >> 2 & 1) * 2 + (r >> 3 & 1); };
   uint4 w[2][kTilesN];
   // B's rows from n0 on: a uniform base and 32-bit offsets
   auto load_w = [&](uint4 (&d)[kTilesN], int64_t n0, int rc) __attribute__((always_inline)) {
@@ -553,34 +637,25 @@ __device__ __forceinline__ void expand_item(const LoraArgs& a, const Item& it, c
       }
       return sum;
     };
-    const f32x4 head = scaled(j0);
-    float up = 1.0f;
-    if constexpr (XT == 2) {
-      float top = finite_max(head);
-#pragma unroll 1
-      for (int j = j0 + 64; j < rank; j += 64) top = fmaxf(top, finite_max(scaled(j)));
-      top = max16(top);
-      // the row's largest value to [2^13, 2^14): far from FP16's ends on both sides
-      int ex = top > 0.0f ? 13 - ilogbf(top) : 0;
-      ex = ex > 120 ? 120 : ex;
-      up = ldexpf(1.0f, ex);
-      if ((tid & 15) == 0 && live) unscale[at] = ldexpf(1.0f, -ex);
-    }
 #pragma unroll 1
     for (int j = j0; j < chunks * 32; j += 64) {
-      const f32x4 val = j == j0 ? head : scaled(j);
-      X p[4][P];
+      const f32x4 val = scaled(j);
+      V p[4][P];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) split(val[e], up, p[e]);
+      for (int e = 0; e < 4; ++e) split(val[e], p[e]);
 #pragma unroll
       for (int u = 0; u < P; ++u) {
-        X o[4] = {p[0][u], p[1][u], p[2][u], p[3][u]};
-        __builtin_memcpy(pieces + (u * tm + at) * pitch + j, o, 8);
+        V o[4] = {p[0][u], p[1][u], p[2][u], p[3][u]};
+        __builtin_memcpy(__builtin_assume_aligned(pieces + (u * tm + at) * pitch + j, sizeof(o)), o, sizeof(o));
       }
     }
   }
   __syncthreads();
 
+  // (Only where an adapter's rows are dealt to its items in their order, so that
+  // which form a row goes through depends on nothing but the call's arguments.)
+  constexpr bool kFew = XT == 2 && INLINE;
+  const bool is_few = kFew && count <= kFewRows;
   f32x4 acc[SUBS][kTilesN];
   int rc = 0;
   // one piece of B; with the last ranks of an output, y is written
@@ -591,21 +666,30 @@ __device__ __forceinline__ void expand_item(const LoraArgs& a, const Item& it, c
 #pragma unroll
         for (int t = 0; t < kTilesN; ++t) acc[s][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
     }
-    const int j = rc * 32 + q * 8;
+    const int j = rc * 32 + q * (kHalves ? 4 : 8);
+    const bool both = !kHalves || rank - rc * 32 > 16;
     if constexpr (kStaged) {
       uint4* own = staged + wave * (kTilesN * 64);
 #pragma unroll
-      for (int t = 0; t < kTilesN; ++t) own[t * 64 + lane] = d[t];
+      for (int t = 0; t < kTilesN; ++t) own[t * 64 + (lane ^ (kHalves ? turn(lane >> 2) : 0))] = d[t];
       __builtin_amdgcn_wave_barrier();
 #pragma unroll
-      for (int t = 0; t < kTilesN; ++t) d[t] = own[t * 64 + c * 4 + q];
+      for (int t = 0; t < kTilesN; ++t) {
+        if constexpr (kHalves) {
+          const uint2* row = reinterpret_cast<const uint2*>(own + t * 64 + c * 4);
+          const uint2 lo = row[q ^ (2 * turn(c))], hi = row[(4 + q) ^ (2 * turn(c))];
+          d[t] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        } else {
+          d[t] = own[t * 64 + c * 4 + q];
+        }
+      }
       __builtin_amdgcn_wave_barrier();
     }
     if (rc * 32 + 32 > rank) {  // entries past the rank may hold anything
       uint32_t keep[4];
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
-        const int left = rank - j - 2 * h;
+        const int left = rank - j - 2 * h - (kHalves && h >= 2 ? 12 : 0);
         keep[h] = left >= 2 ? 0xFFFFFFFFu : (left == 1 ? 0xFFFFu : 0u);
       }
 #pragma unroll
@@ -616,27 +700,23 @@ __device__ __forceinline__ void expand_item(const LoraArgs& a, const Item& it, c
         d[t].w &= keep[3];
       }
     }
-#pragma unroll
-    for (int s = 0; s < SUBS; ++s) {
-      if (s * 16 < count) {
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-          const uint4 b = *reinterpret_cast<const uint4*>(pieces + (p * tm + s * 16 + c) * pitch + j);
-#pragma unroll
-          for (int t = 0; t < kTilesN; ++t) acc[s][t] = Mma<XT>::run(b, d[t], acc[s][t]);
-        }
-      }
+    if constexpr (kFew) {
+      if (is_few) few(pieces + j, pitch, count, d, acc[0]);
+      else multiply<SUBS, kHalves>(pieces + c * pitch + j, pitch, tm, count, both, d, acc);
+    } else {
+      multiply<SUBS, kHalves>(pieces + c * pitch + j, pitch, tm, count, both, d, acc);
     }
     request(d);
     if (++rc < chunks) return;
     rc = 0;
+    if constexpr (kFew) {
+      if (is_few) few_end(count, acc[0]);
+    }
 #pragma unroll
     for (int s = 0; s < SUBS; ++s)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float un = XT == 2 ? unscale[s * 16 + q * 4 + e] : 1.0f;
-        z[s][e] = add4(z[s][e], acc[s][0][e] * un, acc[s][1][e] * un, acc[s][2][e] * un, acc[s][3][e] * un);
-      }
+      for (int e = 0; e < 4; ++e)
+        z[s][e] = add4(z[s][e], acc[s][0][e], acc[s][1][e], acc[s][2][e], acc[s][3][e]);
     const int64_t left = a.n - n0 - c * 4;
 #pragma unroll
     for (int s = 0; s < SUBS; ++s)
@@ -660,10 +740,9 @@ __device__ __forceinline__ void expand_item(const LoraArgs& a, const Item& it, c
 template <int XT, int YT, bool INLINE, int SUBS>
 __global__ __launch_bounds__(256, SUBS == 1 ? 4 : YT == 3 ? 3 : 2) void lora_expand_kernel(
     LoraArgs a, Plan plan, int tm, int slices, const float* __restrict__ v) {
-  extern __shared__ uint4 dyn[];  // pieces of v: [pieces][tm][pitch]
+  extern __shared__ uint4 dyn[];  // v (Held)
   __shared__ Found found;
   const int* rows = found.rows;
-  __shared__ float unscale[kItemRows];
   __shared__ uint4 staged[4 * kTilesN * 64];
   for (int item = blockIdx.y;; item += gridDim.y) {
     const Item it = find_item<INLINE>(a, plan, item, tm, found);
@@ -679,14 +758,15 @@ __global__ __launch_bounds__(256, SUBS == 1 ? 4 : YT == 3 ? 3 : 2) void lora_exp
         for (int u = 0; u < 4; ++u)
           part[u] = *reinterpret_cast<const f32x4*>(vr + (int64_t)(u0 + u < slices ? u0 + u : u0) * a.m * a.r);
 #pragma unroll
+        for (int u = 0; u < 4; ++u) __asm__ volatile("" : "+v"(part[u]));  // not one by one, as they are added
+#pragma unroll
         for (int u = 0; u < 4; ++u)
           if (u0 + u < slices) sum += part[u];
       }
       return sum;
     };
-    expand_item<XT, YT, SUBS, 4>(a, it, found, unscale,
-                                 reinterpret_cast<typename Elem<XT>::type*>(dyn), tm, staged, (int)blockIdx.x,
-                                 (int)gridDim.x, [] {}, inner);
+    expand_item<XT, YT, INLINE, SUBS, 4>(a, it, found, reinterpret_cast<typename Held<XT>::type*>(dyn), tm, staged,
+                                         (int)blockIdx.x, (int)gridDim.x, [] {}, inner);
     __syncthreads();  // the next item's rows and pieces
   }
 }
@@ -699,10 +779,9 @@ __global__ __launch_bounds__(512) void lora_small_kernel(LoraArgs a) {
   constexpr int kWaves = 8, kPitch = RT * 16 + 4;
   __shared__ Found found;
   const int* rows = found.rows;
-  __shared__ float unscale[16];
   __shared__ uint4 stage[kWaves][1 + RT][16][8];
   __shared__ __align__(16) float inner_v[16][kPitch];
-  __shared__ uint4 pieces[Mma<XT>::pieces * 16 * ((RT * 16 + 31) / 32 * 32 + 8) / 8];
+  __shared__ uint4 pieces[inner_bytes<XT>(16, RT * 16) / 16];
   const Item it = find_item<true>(a, Plan{}, (int)blockIdx.y, 16, found);
   if (!it.count) return;
   auto first = [&]() __attribute__((always_inline)) {
@@ -715,9 +794,8 @@ __global__ __launch_bounds__(512) void lora_small_kernel(LoraArgs a) {
   auto inner = [&](int at, int j) __attribute__((always_inline)) {
     return *reinterpret_cast<const f32x4*>(&inner_v[at][j]);
   };
-  expand_item<XT, YT, 1, kWaves>(a, it, found, unscale,
-                                 reinterpret_cast<typename Elem<XT>::type*>(pieces), 16, nullptr, (int)blockIdx.x,
-                                 (int)gridDim.x, first, inner);
+  expand_item<XT, YT, true, 1, kWaves>(a, it, found, reinterpret_cast<typename Held<XT>::type*>(pieces), 16, nullptr,
+                                       (int)blockIdx.x, (int)gridDim.x, first, inner);
 }
 
 int64_t round256(int64_t v) { return (v + 255) / 256 * 256; }
@@ -810,7 +888,7 @@ hipError_t launch(const LoraArgs& a, const Plan& plan, float* v, hipStream_t st)
   int64_t each = all <= 1536 ? (all + 767) / 768 : (all + 2999) / 3000;
   each = each < tiles ? each : tiles;
   const dim3 ge((unsigned)((tiles + each - 1) / each), (unsigned)(items < 32768 ? items : 32768));
-  const size_t lds = (size_t)Mma<XT>::pieces * tm * ((a.r + 31) / 32 * 32 + 8) * 2;
+  const size_t lds = inner_bytes<XT>(tm, (int)a.r);
   if (tm == 16)
     hipLaunchKernelGGL((lora_expand_kernel<XT, YT, INLINE, 1>), ge, dim3(256), lds, st, a, plan, tm, slices, v);
   else

@@ -483,9 +483,9 @@ size_t lowbit_lora_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_t r, i
  *   scales : [slots] FP32 or NULL (1)
  *   y      : [m] rows of n at stride ldy, read and written in place: FP32,
  *            or, with BF16 x, BF16
- * Products are of the stored values, sums and the result of the first
- * product are FP32 (or pairs that hold as much), and y is rounded once.  No
- * atomics; equal inputs give equal bits.  Rows may come in any order and
+ * Products are of the stored values; sums, the result of the first product
+ * and its products with B are FP32 (or pieces that hold as much), and y is
+ * rounded once.  No atomics; equal inputs give equal bits.  Rows may come in any order and
  * adapters be shared by any of them.
  * 1 <= m <= 2^22, n < 2^31, k a multiple of 8, r a multiple of 8 up to 256,
  * 1 <= slots <= 4096, every extent below 2^40 elements.  x, a, b and

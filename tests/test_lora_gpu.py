@@ -235,3 +235,59 @@ def test_two_streams_with_their_own_workspaces():
     torch.cuda.synchronize()
     for d, want in zip(cases, wants):
         _check(d["y"], *want)
+
+
+# rows: one launch; grouped in every work-group; sorted first
+ROWS = [3, 30, 70, 200]
+
+
+@pytest.mark.parametrize("m", ROWS)
+@pytest.mark.parametrize("xt,yt", [("f16", "f32"), ("bf16", "f32"), ("bf16", "bf16")])
+def test_small_inner_values_beside_large_ones(m, xt, yt):
+    """Inner values 2^27 apart in one row, and outputs that take only the small
+    ones: their products are as exact as any."""
+    import torch
+
+    g = np.random.default_rng(m)
+    k, n, r = 64, 90, 40
+    d = _case(m, k, n, r, 2, xt, yt, ids=np.arange(m) % 2, seed=50 + m)
+    a = g.standard_normal((2, r, k))
+    a[:, :24] *= 2.0 ** 13
+    a[:, 24:] *= 2.0 ** -14
+    b = g.standard_normal((2, n, r)) * 0.3
+    b[:, ::2, :24] = 0.0
+    d["a"], d["b"] = _t(a, xt), _t(b, xt)
+    d["y"].zero_()
+    got = lowbit.lowbit_lora_accumulate(**d)
+    torch.cuda.synchronize()
+    _check(got, *_want(d, np.zeros((m, n)), yt))
+
+
+@pytest.mark.parametrize("m", ROWS)
+@pytest.mark.parametrize("xt,yt", [("f16", "f32")])
+def test_infinite_weights_follow_the_formula(m, xt, yt):
+    """An infinite entry of B gives an infinity of the product's sign, whatever
+    bits the inner value has; times an inner value of zero, NaN."""
+    import torch
+
+    k, n, r = 64, 70, 24
+    d = _case(m, k, n, r, 2, xt, yt, ids=np.arange(m) % 2, seed=60 + m)
+    d["x"][0] = 0.0
+    d["x"][1] = 0.0
+    d["x"][1, 5] = 1.0
+    d["a"][1, 3, 5] = -2.0   # an inner value of one bit
+    d["scales"][1] = 0.5
+    d["x"][2] = 0.0          # a row of zeros
+    d["a"][0, 20, 0] = 1.0
+    d["x"][0, 0] = 1.0
+    d["b"][1, 3, 3] = float("inf")
+    d["b"][1, 4, 3] = -float("inf")
+    d["b"][0, 64, 20] = float("inf")
+    y0 = d["y"].cpu().double().numpy()
+    got = lowbit.lowbit_lora_accumulate(**d).cpu().double().numpy()
+    with np.errstate(invalid="ignore"):
+        want, bound = _want(d, y0, yt)
+    assert want[1, 3] == -np.inf and want[1, 4] == np.inf and want[0, 64] == np.inf and np.isnan(want[2, 64])
+    fine = np.isfinite(want)
+    assert np.array_equal(got[~fine], want[~fine], equal_nan=True)
+    assert (np.abs(got - want)[fine] <= bound[fine]).all()
