@@ -400,14 +400,33 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs a, Plan plan,
     *reinterpret_cast<f32x4*>(v + ((int64_t)blockIdx.z * a.m + rows[sub * 16 + c]) * a.r + j) = sum;
 }
 
-// FP32 value -> its pieces
+// FP32 value -> its pieces.  The three are cut, not rounded, 8 bits each: they
+// hold the value's 24, none of a finite value is infinite, and all have its
+// sign.  One that nothing is left for takes half of the one before, so that an
+// infinite entry of B meets no zero unless the value is one.
 __device__ __forceinline__ void split(float v, float (&p)[1]) { p[0] = v; }
 __device__ __forceinline__ void split(float v, bf16_t (&p)[3]) {
-  p[0] = (bf16_t)v;
-  const bool fine = __builtin_isfinite((float)p[0]);
-  const float rest = fine ? v - (float)p[0] : 0.0f;
-  p[1] = (bf16_t)rest;
-  p[2] = (bf16_t)(rest - (float)p[1]);
+  const auto cut = [](float f) __attribute__((always_inline)) {
+    return __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, f) & 0xFFFF0000u);
+  };
+  float hi = v, mid = v, lo = v;
+  if (__builtin_isfinite(v)) {
+    hi = cut(v);
+    mid = cut(v - hi);
+    lo = v - hi - mid;
+    if (mid == 0.0f) {
+      hi *= 0.5f;
+      mid = hi;
+      lo = 0.0f;
+    }
+    if (lo == 0.0f) {
+      mid *= 0.5f;
+      lo = mid;
+    }
+  }
+  p[0] = (bf16_t)hi;
+  p[1] = (bf16_t)mid;
+  p[2] = (bf16_t)lo;
 }
 
 // acc[s][t] += the products of 32 ranks: of v's rows (`v`: at this lane's first

@@ -264,7 +264,7 @@ def test_small_inner_values_beside_large_ones(m, xt, yt):
 
 
 @pytest.mark.parametrize("m", ROWS)
-@pytest.mark.parametrize("xt,yt", [("f16", "f32")])
+@pytest.mark.parametrize("xt,yt", [("f16", "f32"), ("bf16", "f32"), ("bf16", "bf16")])
 def test_infinite_weights_follow_the_formula(m, xt, yt):
     """An infinite entry of B gives an infinity of the product's sign, whatever
     bits the inner value has; times an inner value of zero, NaN."""
@@ -291,3 +291,19 @@ def test_infinite_weights_follow_the_formula(m, xt, yt):
     fine = np.isfinite(want)
     assert np.array_equal(got[~fine], want[~fine], equal_nan=True)
     assert (np.abs(got - want)[fine] <= bound[fine]).all()
+
+
+@pytest.mark.parametrize("m", ROWS)
+@pytest.mark.parametrize("xt,yt", [("f16", "f32"), ("bf16", "f32"), ("bf16", "bf16")])
+def test_inner_values_at_the_end_of_fp32(m, xt, yt):
+    """Finite inner values that a 16-bit type rounds to infinity."""
+    import torch
+
+    d = _case(m, 8, 40, 8, 1, xt, yt, ids=np.zeros(m), seed=70 + m)
+    d["x"].zero_()
+    d["x"][:, 0] = 1.0
+    d["a"][0, :, 0] = torch.tensor([1.0, -1.0, 0.5, 0.0, 1.0, 1.0, -0.25, 0.0])
+    d["scales"][0] = 3.4e38
+    d["b"] = _t(np.random.default_rng(m).uniform(1.0, 2.0, (1, 40, 8)) * 2.0 ** -14, xt)
+    y0 = d["y"].cpu().double().numpy()
+    _check(lowbit.lowbit_lora_accumulate(**d), *_want(d, y0, yt))
