@@ -893,10 +893,10 @@ hipError_t launch(const LoraArgs& a, const Plan& plan, float* v, hipStream_t st)
   const dim3 gs((unsigned)(items * subs), (unsigned)((a.r + rt * 16 - 1) / (rt * 16)), (unsigned)slices);
   if (rt == 1)
     hipLaunchKernelGGL((lora_shrink_kernel<XT, 1, INLINE>), gs, dim3(512), 0, st, a, plan, tm, subs, v);
-  else if (rt == 2)
-    hipLaunchKernelGGL((lora_shrink_kernel<XT, 2, INLINE>), gs, dim3(512), 0, st, a, plan, tm, subs, v);
-  else
+  else if (INLINE || rt == 3)  // (up to 64 rows take more than 16 ranks at once above 64 alone: in threes)
     hipLaunchKernelGGL((lora_shrink_kernel<XT, 3, INLINE>), gs, dim3(512), 0, st, a, plan, tm, subs, v);
+  else if constexpr (!INLINE)
+    hipLaunchKernelGGL((lora_shrink_kernel<XT, 2, false>), gs, dim3(512), 0, st, a, plan, tm, subs, v);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   // Work-groups: as many as run at once (three to a compute unit) where two
@@ -908,10 +908,11 @@ hipError_t launch(const LoraArgs& a, const Plan& plan, float* v, hipStream_t st)
   each = each < tiles ? each : tiles;
   const dim3 ge((unsigned)((tiles + each - 1) / each), (unsigned)(items < 32768 ? items : 32768));
   const size_t lds = inner_bytes<XT>(tm, (int)a.r);
-  if (tm == 16)
+  if (INLINE || tm == 16) {
     hipLaunchKernelGGL((lora_expand_kernel<XT, YT, INLINE, 1>), ge, dim3(256), lds, st, a, plan, tm, slices, v);
-  else
-    hipLaunchKernelGGL((lora_expand_kernel<XT, YT, INLINE, 2>), ge, dim3(256), lds, st, a, plan, tm, slices, v);
+  } else if constexpr (!INLINE) {  // rows not sorted first make no items of 32
+    hipLaunchKernelGGL((lora_expand_kernel<XT, YT, false, 2>), ge, dim3(256), lds, st, a, plan, tm, slices, v);
+  }
   return hipGetLastError();
 }
 
