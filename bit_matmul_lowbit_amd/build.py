@@ -1,6 +1,6 @@
 """Build liblowbit.so (HIP, gfx950) in-tree with hipcc, and the Python
 binding's compiled part (_marshal.so, host code against torch's headers)
-with g++.
+with g++; where torch is absent the library alone.
 
 Run ``python -m bit_matmul_lowbit_amd.build`` or call ``build()``.  Every call
 recompiles.  Both are placed next to this file so that they travel with the
@@ -8,6 +8,7 @@ source tree.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import subprocess
 import sys
@@ -65,9 +66,14 @@ def build_marshal(verbose: bool = False) -> str:
 
 
 def build(verbose: bool = False) -> str:
-    build_marshal(verbose)
+    """The library, which takes hipcc alone, and then, where there is a torch to
+    call it from, the binding's compiled part."""
     srcs = [os.path.join(CSRC, s) for s in SOURCES]
     _run([HIPCC, *FLAGS, "-I", os.path.join(ROOT, "include"), "-o", LIB + ".tmp", *srcs], LIB, verbose)
+    if importlib.util.find_spec("torch") is None:
+        print("no torch here: _marshal.so, which the Python binding loads, is not built", file=sys.stderr)
+    else:
+        build_marshal(verbose)
     return LIB
 
 
