@@ -309,3 +309,76 @@ def test_long_lists_of_tokens(b, n):
     _same(idx[rows], widx)
     _same(val[rows], wval)
     assert torch.equal(idx.long(), out.max(dim=1).indices) or torch.equal(out.max(dim=1).values, val)
+
+
+# (b, n, tokens, biases): parts of 4096, 8192, 19456, 2048 and 2048 tokens; in batches of 8 of 1024 or 2048
+@pytest.mark.parametrize("b,n,hist,nbias", [(64, 32000, 2048, 1500), (64, 50001, 300, 700), (64, 120001, 16400, 1100),
+                                            (24, 32003, 700, 600), (47, 32000, 500, 300)])
+@pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
+def test_every_part_size_with_everything(b, n, hist, nbias, dtype):
+    """More biases than threads, and than LDS holds for one part, shared mask
+    rows, each type, in place where that can be: sampled rows against the plain
+    form, all rows against themselves in small batches, every token against its
+    row."""
+    import torch
+
+    say(f"logits b={b} n={n} hist={hist} bias={nbias} {dtype}")
+    d = _case(b, n, hist, nbias, True, b + n, mask_rows=5)
+    g = np.random.default_rng(n)
+    crowd = g.random((b, nbias)) < 0.5
+    d["bias_ids"][crowd] = g.integers(0, 700, crowd.sum())
+    y = torch.from_numpy(d["y"]).to(getattr(torch, dtype)).cuda()
+    t = {k: _dev(v) for k, v in d.items() if k != "y"}
+    parts = []
+    for i in range(0, b, 8):
+        rows = {k: v if k == "mask" else v[i:i + 8] for k, v in t.items()}
+        out = torch.empty(y[i:i + 8].shape, dtype=torch.float32, device="cuda")
+        parts.append(lowbit.lowbit_logits_process(y[i:i + 8], out=out, **rows))
+    out = y if dtype == "float32" else torch.empty((b, n), dtype=torch.float32, device="cuda")
+    out, idx, val = lowbit.lowbit_logits_process(y, out=out, **t)
+    for at, got in enumerate((out, idx, val)):
+        assert torch.equal(got, torch.cat([p[at] for p in parts])), at
+    # the lowest of a row's largest; -1 where nothing is allowed
+    first = torch.where(out == val[:, None], torch.arange(n, device="cuda"), n).amin(dim=1)
+    none = torch.isneginf(val)
+    assert torch.equal(val, out.amax(dim=1)) and torch.equal(idx.long(), torch.where(none, -1, first))
+    rows = np.unique(np.concatenate([[0, b - 1], g.choice(b, 3, replace=False)]))
+    want, widx, wval, _ = plain64.logits_process(**{k: v if k == "mask" else v[rows] for k, v in d.items()})
+    _same(out[rows], want)
+    _same(idx[rows], widx)
+    _same(val[rows], wval)
+
+
+@pytest.mark.parametrize("b,n", [(64, 151936), (400, 20001), (70, 60000)])
+def test_tokens_of_every_row_with_long_lists(b, n):
+    """The lowest of a row's largest, in rows full of ties."""
+    import torch
+
+    g = np.random.default_rng(b + 1)
+    hist = 16500
+    y = torch.from_numpy((g.integers(-40, 41, (b, n)) / 8).astype(np.float32)).cuda()
+    out = torch.empty_like(y)
+    _, idx, val = lowbit.lowbit_logits_process(
+        y, tokens=_dev((g.random((b, hist)) ** 4 * n).astype(np.int32)),
+        total_len=_dev(g.integers(0, hist + 1, b).astype(np.int32)), repetition=_dev(np.full(b, 2.0, np.float32)), out=out)
+    assert torch.equal(val, out.amax(dim=1))
+    first = torch.where(out == val[:, None], torch.arange(n, device="cuda"), n).amin(dim=1)
+    assert torch.equal(idx.long(), first)
+
+
+@pytest.mark.parametrize("same", [False, True])
+def test_the_longest_list_of_biases_in_one_part(same):
+    """16384 entries that fall together, every id once or one id for all."""
+    import torch
+
+    n, nbias = 32000, 16384
+    g = np.random.default_rng(3)
+    d = _case(3, n, 50, 0, False, 3)
+    d["bias_ids"] = np.stack([np.full(nbias, 77) if same else g.permutation(nbias) % 1000 for _ in range(3)]).astype(np.int32)
+    d["bias_vals"] = (g.integers(-8, 9, (3, nbias)) / 8).astype(np.float32)
+    out = torch.empty((3, n), dtype=torch.float32, device="cuda")
+    _, idx, val = _run(d, out=out)
+    want, widx, wval, _ = plain64.logits_process(**d)
+    _same(out, want)
+    _same(idx, widx)
+    _same(val, wval)
