@@ -307,3 +307,39 @@ def test_inner_values_at_the_end_of_fp32(m, xt, yt):
     d["b"] = _t(np.random.default_rng(m).uniform(1.0, 2.0, (1, 40, 8)) * 2.0 ** -14, xt)
     y0 = d["y"].cpu().double().numpy()
     _check(lowbit.lowbit_lora_accumulate(**d), *_want(d, y0, yt))
+
+
+@pytest.mark.parametrize("m,k,n,r,slots", [
+    (4100, 136, 300, 32, 8),      # 32 ranks to a work-group of the first product, items of 32 rows
+    (4100, 136, 2049, 128, 8),    # 48 ranks; two shares of the outputs one after the other, four pieces of ranks each
+    (2100, 264, 4099, 72, 5), (4100, 128, 2800, 256, 3),
+    (600, 64, 5000, 72, 300),     # items of 16 rows, three shares of the outputs
+    (1500, 1032, 515, 64, 20)])
+@pytest.mark.parametrize("xt,yt", [("f16", "f32"), ("bf16", "f32"), ("bf16", "bf16")])
+def test_many_rows(m, k, n, r, slots, xt, yt):
+    import torch
+
+    say(f"lora many rows m={m} k={k} n={n} r={r} slots={slots} {xt} {yt}")
+    d = _case(m, k, n, r, slots, xt, yt, ragged=True, seed=m + n)
+    y0 = d["y"].clone()
+    got = lowbit.lowbit_lora_accumulate(**d)
+    again = lowbit.lowbit_lora_accumulate(**{**d, "y": y0.clone()})
+    torch.cuda.synchronize()
+    assert torch.equal(again, got)
+    ids = d["ids"].cpu().numpy()
+    none = torch.from_numpy((ids < 0) | (ids >= slots)).cuda()
+    assert bool(none.any()) and torch.equal(got[none], y0[none])
+    g = np.random.default_rng(r)
+    rows = np.unique(np.concatenate([[0, m - 1], g.choice(m, 60, replace=False)]))
+    part = {**d, "x": d["x"][rows], "ids": d["ids"][rows]}
+    _check(got[rows], *_want(part, y0[rows].cpu().double().numpy(), yt))
+    # rows in calls of few rows: the same sums in another order.  The inner values
+    # are sums of some 20 in magnitudes, y's of at most 256 * 0.24 * 2 * 20 < 2500, in
+    # (k / 32 + 130) + (r + 16) < 500 roundings: 0.075 for each call; another row's
+    # sums would be off by more than that nearly everywhere.
+    for i in range(0, m, 64 * 16):
+        at = slice(i, min(i + 64, m))
+        few = lowbit.lowbit_lora_accumulate(**{**d, "x": d["x"][at], "ids": d["ids"][at].contiguous(), "y": y0[at].clone()})
+        off = (few.double() - got[at].double()).abs()
+        step = 2.0 ** -7 if yt == "bf16" else 2.0 ** -23
+        assert bool((off <= 0.15 + step * few.double().abs()).all())
