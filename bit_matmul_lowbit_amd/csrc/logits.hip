@@ -206,7 +206,10 @@ __global__ __launch_bounds__(THREADS, THREADS == 1024 ? 8 : 1) void logits_kerne
   int best_c = 0;
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    const int c = g * kStep + tid * 4;
+    int t4 = tid * 4;
+    // (made anew: kept since the loads, the places are more than 64 registers hold)
+    if constexpr (THREADS == 1024) __asm__ volatile("" : "+v"(t4));
+    const int c = g * kStep + t4;
     if (c >= size) continue;
     const uint4 k4 = *reinterpret_cast<const uint4*>(cnt + c);
     const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
@@ -270,18 +273,51 @@ __global__ __launch_bounds__(THREADS, THREADS == 1024 ? 8 : 1) void logits_kerne
     };
     if (my_off < (uint32_t)size) entry(my_at, (int)my_off, my_val, my_y);
     for (int i = nkept + tid; i < nb; i += THREADS) entry(i, bias_at[i], bias_val[i], (float)y[bias_at[i]]);
-  } else {  // more than LDS holds: the same from the list itself
-    for (int i = tid; i < nlist; i += THREADS) {
-      const int32_t id = ids[i];
-      const uint32_t off = (uint32_t)id - (uint32_t)lo;
-      if (off >= (uint32_t)size) continue;
-      bool first = true;
-      for (int j = 0; first && j < i; ++j) first = ids[j] != id;
-      if (!first) continue;
-      float bias = vals[i];
-      for (int j = i + 1; j < nlist; ++j)
-        if (ids[j] == id) bias += vals[j];
-      biased((int)off, (float)y[off], bias);
+  } else {
+    // More than LDS holds: a wave takes 256 tokens at a time, four to a lane in
+    // registers, and walks the list once for them; its entries are added one by
+    // one, in the list's order.  64 x 151936 with 16384 biases a row: 0.45 ms
+    // (127 with a walk for each entry); all of one id 1.0 ms (2.5).
+    const int lane = tid & 63;
+    for (int base = (tid >> 6) * 256; base < size; base += 4 * THREADS) {
+      bool mine[4];
+      float sum[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int off = base + e * 64 + lane;
+        mine[e] = off < size && (cnt[off] & kBias);
+        sum[e] = -0.0f;  // the first entry added to it keeps its bits
+      }
+      if (!__ballot(mine[0] || mine[1] || mine[2] || mine[3])) continue;
+      constexpr int U = 4;
+      for (int j0 = 0; j0 < nlist; j0 += U * 64) {
+        uint32_t at[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int j = j0 + u * 64 + lane;
+          at[u] = j < nlist ? (uint32_t)ids[j] - (uint32_t)lo - (uint32_t)base : ~0u;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          uint64_t hit = __ballot(at[u] < 256u);  // (places past the part's end are nobody's)
+          if (!hit) continue;
+          const float val = at[u] < 256u ? vals[j0 + u * 64 + lane] : 0.0f;
+          while (hit) {
+            const int l = __builtin_ctzll(hit);
+            hit &= hit - 1;
+            const int place = __builtin_amdgcn_readlane((int)at[u], l);
+            const float v = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, val), l));
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (place == e * 64 + lane) sum[e] += v;
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int off = base + e * 64 + lane;
+        if (mine[e]) biased(off, (float)y[off], sum[e]);
+      }
     }
   }
   if (part) {

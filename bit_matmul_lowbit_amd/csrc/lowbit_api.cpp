@@ -431,7 +431,7 @@ int lowbit_logits_process(const void* y, int y_type, int64_t ldy, int64_t n, int
     return LOWBIT_ERR_SHAPE;
   constexpr int64_t kMaxList = int64_t(1) << 30;
   if (tokens && (tcap < 0 || tcap >= kMaxList || !rows_ok(b, tcap, ldt))) return LOWBIT_ERR_SHAPE;
-  // where many ids fall together each is compared with the whole list: a bound on that work
+  // where many ids fall together the list is walked for every 256 tokens: a bound on that work
   constexpr int64_t kMaxBiases = 16384;
   if (bias_ids && (bcap < 0 || bcap > kMaxBiases || !rows_ok(b, bcap, ldb))) return LOWBIT_ERR_SHAPE;
   if (mask) {

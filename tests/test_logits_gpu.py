@@ -382,3 +382,25 @@ def test_the_longest_list_of_biases_in_one_part(same):
     _same(out, want)
     _same(idx, widx)
     _same(val, wval)
+
+
+@pytest.mark.parametrize("b,n,top", [(64, 151936, 151936), (8, 151936, 151936), (64, 32000, 1000), (3, 32000, 1)])
+def test_long_lists_of_biases_are_bounded_work(b, n, top):
+    """16384 biases a row: a walk over the list for each group of tokens, not
+    for each token (that was 127 ms for the first of these calls)."""
+    import torch
+
+    nbias = 16384
+    ids = torch.stack([torch.randperm(top, device="cuda").repeat((nbias + top - 1) // top)[:nbias] for _ in range(b)]).int()
+    y = torch.randn(b, n, device="cuda")
+    args = dict(bias_ids=ids, bias_vals=torch.randn(b, nbias, device="cuda"), out=torch.empty_like(y))
+    lowbit.lowbit_logits_process(y, **args)
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    out, _, _ = lowbit.lowbit_logits_process(y, **args)
+    end.record()
+    end.synchronize()
+    want = y[0].double().index_add(0, ids[0].long(), args["bias_vals"][0].double())
+    # at most 16384 additions of values below 6
+    assert bool(((out[0].double() - want).abs() <= nbias * 2.0 ** -24 * 6 * (nbias / min(top, nbias))).all())
+    assert start.elapsed_time(end) < 20
