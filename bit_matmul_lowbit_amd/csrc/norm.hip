@@ -410,18 +410,21 @@ hipError_t launch_norm_residual(const NormArgs& a, hipStream_t st) {
   const int vectors = !!a.post_w + !!a.post_b + !!a.pre_w + !!a.pre_b + (a.gate && a.ldg == 0);
   const int bytes = (a.y ? (a.y_type == 1 ? 4 : 2) : 0) + (a.r_type == 1 ? 4 : 2);
   const bool keep = !exact && 4 * vectors >= (bytes == 8 ? 12 : bytes);
-  // as many work-groups of `waves` waves as run at once (16 waves to a compute
-  // unit), each with as many of the rows
-  const auto running = [](int64_t waves) { return 256 * 16 / waves; };
-  const auto held = [&](int64_t rows, int64_t waves) {
-    const int64_t each = (rows + running(waves) - 1) / running(waves);
+  // As many work-groups of `waves` waves as run at once, `simd` waves to a SIMD, each
+  // with as many of the rows.  Four run with up to 128 registers; two steps of one
+  // wave take 163 to 165 with a 16-bit y (three), 171 to 173 with an FP32 one (two):
+  // 40000 x 601, FP16, four weights and a gate 75.6 -> 65.8 us, 5000 x 1001, FP32 24.3
+  // -> 20.0 against four; 16384 x 1001, BF16 y, FP32 r 55.6 -> 58.1.
+  const auto running = [](int64_t waves, int64_t simd) { return 256 * 4 * simd / waves; };
+  const auto held = [&](int64_t rows, int64_t waves, int64_t simd) {
+    const int64_t each = (rows + running(waves, simd) - 1) / running(waves, simd);
     return dim3((unsigned)((rows + each - 1) / each));
   };
   // short rows, many of them: one wave each, no barriers (12030 x 128, one weight
   // and a gate per row: 8.6 us kept, 12.8 read again)
-  if (chunks <= 64 && many) return launch_as<true, 1, kHeld>(a, held((a.m + 3) / 4, 4), dim3(256), st);
+  if (chunks <= 64 && many) return launch_as<true, 1, kHeld>(a, held((a.m + 3) / 4, 4, 4), dim3(256), st);
   if (chunks <= 128 && many) {
-    if (keep) return launch_as<true, 2, kHeld>(a, held((a.m + 3) / 4, 4), dim3(256), st);
+    if (keep) return launch_as<true, 2, kHeld>(a, held((a.m + 3) / 4, 4, a.y_type == 1 ? 2 : 3), dim3(256), st);
     const dim3 g((unsigned)((a.m + 3) / 4));
     return exact ? launch_as<true, 2, kExact>(a, g, dim3(256), st) : launch_as<true, 2, kLate>(a, g, dim3(256), st);
   }
@@ -433,7 +436,7 @@ hipError_t launch_norm_residual(const NormArgs& a, hipStream_t st) {
     if (many && !keep)
       return exact ? launch_as<false, 1, kExact>(a, grid, block(1), st)
                    : launch_as<false, 1, kLate>(a, grid, block(1), st);
-    if (many && a.m >= 2 * running(waves)) return launch_as<false, 1, kHeld>(a, held(a.m, waves), block(1), st);
+    if (many && a.m >= 2 * running(waves, 4)) return launch_as<false, 1, kHeld>(a, held(a.m, waves, 4), block(1), st);
     return launch_as<false, 1, kAhead>(a, grid, block(1), st);
   }
   // Above 12288 a work-group of 16 elements a thread no longer has a second one
