@@ -135,7 +135,7 @@ __device__ __forceinline__ float row_sum(float v, float (*red)[16], int& turn) {
 //   kHeld : a work-group takes every gridDim.x-th row, keeps the weights (and a
 //           gate that all rows share), and has the next row on its way while it
 //           works on one (11886 x 1621, FP16, a norm on both sides, gated: 78 ->
-//           50 us)
+//           46 us)
 // A thread's elements in step n are the eight from c on.  Where fewer are left
 // it holds the row's last eight (k >= 8) and passes over the first `skip` of
 // them, which are another thread's: no load has a short form.
@@ -404,7 +404,7 @@ hipError_t launch_norm_residual(const NormArgs& a, hipStream_t st) {
   const bool exact = a.k % 8 == 0;
   // Many rows: those of whole eights need nothing else to come near the memory's
   // rate; of others the weights are kept where a row would read at least as much
-  // of them as of itself (11886 x 1621, FP16, four of them: 78 us read again, 50
+  // of them as of itself (11886 x 1621, FP16, four of them: 78 us read again, 46
   // kept).  Rows of FP32 on both sides, which take more registers, need more of
   // them (4096 x 2048, two: 28 and 30; four: 83 and 81).
   const int vectors = !!a.post_w + !!a.post_b + !!a.pre_w + !!a.pre_b + (a.gate && a.ldg == 0);

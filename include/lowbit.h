@@ -405,9 +405,7 @@ int lowbit_lm_head(int fmt, const void* codes, const uint16_t* scales, int64_t n
  *            rows at stride ldg; or NULL
  * Strides count elements and are at least k (or 0 for ldg).  1 <= m <= 2^21,
  * 1 <= k <= 2^22, m * stride < 2^40.  At least one of r_out and x_out is
- * given.  Pointers need their element's alignment only; rows whose
- * pointers and strides are multiples of 16 bytes are read 16 bytes at a
- * time.  eps >= 0. */
+ * given.  Pointers need their element's alignment only.  eps >= 0. */
 int lowbit_norm_residual(const void* y, int y_type, int64_t ldy, const void* r, int r_type,
                          int64_t ldr, void* r_out, int64_t ldro, void* x_out, int x_type,
                          int64_t ldx, int64_t m, int64_t k, int post, const float* post_w,
