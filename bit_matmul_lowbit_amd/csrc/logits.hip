@@ -15,10 +15,10 @@
 //
 // What bounds it.  Large calls: the logits read and written, and the tokens,
 // read once by every part.  64 x 151936 with lists of up to 32768, 300 biases, a
-// mask, logits written: 29.5 us and 4 to 5 for the rows' ends (86 MB of logits,
-// mask and lists; without tokens 24 in all, without biases too 20).  Small calls:
+// mask, logits written: 28 us and 4 to 5 for the rows' ends (86 MB of logits,
+// mask and lists; counting the tokens is some 10 of them, the biases 3).  Small calls:
 // a launch and the latencies of lengths, tokens and logits: 1 x 151936, the token
-// alone, 4.4 + 1.5 us; 8 x 151936 with everything 8.7 + 2.2 us.
+// alone, 4.5 + 1.6 us; 8 x 151936 with everything 8 to 9.6 + 1.5 to 3.9 us.
 #include "argmax.h"
 #include "common.h"
 

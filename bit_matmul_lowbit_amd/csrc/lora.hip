@@ -36,11 +36,12 @@
 //
 // What bounds it.  Few rows: the bytes of A and B and the latencies before
 // they can be asked for (ids, then v).  8 rows of 8 adapters, r 64, 5120 ->
-// 34816: 4.0 + 12.5 us for 7 + 36 MB (more of B in flight changes nothing; with
-// B's rows all one expand takes 7.5 us).  Many rows: y, read and written.  4096
-// rows of 8 adapters, r 32, 5120 -> 17408, BF16: plan 7.1, shrink 20.8, expand
-// 71 us for 285 MB of y (4.0 TB/s; a large copy reaches 4.8).  One row, 2048 ->
-// 6144, r 16: 6.7 us in one launch.
+// 34816: 4.0 + 13 us for 7 + 36 MB (more of B in flight changes nothing; with
+// B's rows all one expand takes 9.2 us).  Many rows: y, read and written.  4096
+// rows of 8 adapters, r 32, 5120 -> 17408, BF16: plan 7.2, shrink 21, expand
+// 71 us for 285 MB of y (4.0 TB/s; a large copy reaches 4.8); with FP16 and many
+// ranks the FP32 matrix instructions as well (4096 rows, r 128, 5120 -> 5120: 139 us
+// a call).  One row, 2048 -> 6144, r 16: 6.8 us in one launch.
 #include "common.h"
 
 namespace lowbit {
@@ -432,7 +433,7 @@ __device__ __forceinline__ void split(float v, bf16_t (&p)[3]) {
 // acc[s][t] += the products of 32 ranks: of v's rows (`v`: at this lane's first
 // rank, in its row of the first of SUBS 16-row parts) and of B's in `w`.
 //
-// FP16: FP32 products, a quarter of the rate of two FP16 pieces, but a piece's
+// FP16: FP32 products, an eighth of the rate of two FP16 pieces, but a piece's
 // smallest step (2^-38 of the row's largest value) and what its zeros make of an
 // infinite entry of B do not show in y.  HALVES: a lane's ranks are four of the
 // first 16 and, if `both`, four of the others, so that 16 ranks take half of the
