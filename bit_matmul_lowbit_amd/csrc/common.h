@@ -270,6 +270,65 @@ struct LoraArgs {
 size_t lora_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_t r, int64_t slots);
 hipError_t launch_lora_accumulate(const LoraArgs& a, void* ws, hipStream_t st);
 
+// rotary positions; the 4-bit cache and attention over it (arguments as in the C ABI)
+struct RopeArgs {
+  const void* x;
+  void* out;
+  const int32_t* positions;
+  const uint64_t* turns;
+  int64_t ldx, ldxh, ldo, ldoh, m, heads, d, rot;
+  double gain;
+  int inter, x_type, out_type;
+};
+hipError_t launch_rope(const RopeArgs& a, hipStream_t st);
+
+struct KvStoreArgs {
+  const void *k, *v, *q;
+  void* q_out;
+  const int32_t *slots, *positions;
+  const uint64_t* turns;
+  uint8_t* pages;
+  int64_t ldk, ldkh, ldv, ldvh, ldq, ldqh, ldqo, ldqoh, m, hq, heads, d, page, n_pages, rot;
+  double gain;
+  int inter, in_type, qo_type;
+};
+hipError_t launch_kv_store(const KvStoreArgs& a, hipStream_t st);
+
+struct KvLoadArgs {
+  const uint8_t* pages;
+  const int32_t* slots;
+  void *k, *v;
+  int64_t ldk, ldkh, ldv, ldvh, m, heads, d, page, n_pages;
+  int out_type;
+};
+hipError_t launch_kv_load(const KvLoadArgs& a, hipStream_t st);
+
+struct AttnArgs {
+  const void* q;
+  const uint8_t* pages;
+  const int32_t *table, *lengths, *q_start;
+  void* out;
+  float* lse;
+  int64_t ldq, ldqh, ldo, ldoh, m, hq, heads, d, page, n_pages, tcap, ldt, b, max_q;
+  float scale;
+  int q_type, out_type;
+};
+size_t attention_workspace_bytes(int64_t hq, int64_t heads, int64_t d, int64_t max_q);
+hipError_t launch_attention(const AttnArgs& a, void* ws, hipStream_t st);
+
+// a token drawn from each row of logits (arguments as in the C ABI)
+struct SampleArgs {
+  const void* y;
+  const float *temperature, *top_p, *min_p, *u;
+  const int32_t* top_k;
+  int32_t* idx;
+  float* prob;
+  int64_t ldy, n, b;
+  int y_type;
+};
+size_t sample_workspace_bytes(int64_t n, int64_t b);
+hipError_t launch_sample(const SampleArgs& a, void* ws, hipStream_t st);
+
 hipError_t launch_gemm(int fmt, const uint8_t* codes, const uint16_t* scales, int64_t n,
                        int64_t k, const uint16_t* x, int64_t m, void* y, bool out_f32,
                        hipStream_t st);

@@ -5,6 +5,7 @@
 #include "common.h"
 
 #include <atomic>
+#include <cmath>
 
 namespace lowbit {
 
@@ -54,6 +55,34 @@ bool rows_ok(int64_t m, int64_t k, int64_t ld) { return ld >= k && ld <= kMaxEle
 int64_t padded(int64_t n) { return (n + 15) / 16 * 16; }
 
 int hip_status(hipError_t e) { return e == hipSuccess ? LOWBIT_OK : LOWBIT_ERR_HIP; }
+
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+constexpr int64_t kMaxSlots = (int64_t(1) << 31) - 1;
+
+// [m][heads][d] at strides ld and ldh: no two heads of all tokens overlap, and
+// every offset is below 2^40
+bool heads_ok(int64_t m, int64_t heads, int64_t d, int64_t ld, int64_t ldh) {
+  if (ld < 0 || ldh < 0 || ld > kMaxElems / m || ldh > kMaxElems / heads) return false;
+  const int64_t all_heads = (heads - 1) * ldh + d, all_tokens = (m - 1) * ld + d;
+  return ((heads == 1 || ldh >= d) && (m == 1 || ld >= all_heads)) ||
+         ((m == 1 || ld >= d) && (heads == 1 || ldh >= all_tokens));
+}
+
+bool cache_ok(int64_t heads, int64_t d, int64_t page, int64_t pages) {
+  if (heads < 1 || heads > 1024 || (d != 64 && d != 128 && d != 256)) return false;
+  if (page < 16 || page > 256 || (page & (page - 1)) != 0) return false;
+  return pages >= 1 && pages <= kMaxSlots / page;
+}
+
+bool attention_ok(int64_t m, int64_t b, int64_t hq, int64_t heads, int64_t d, int64_t max_q) {
+  if (m < 1 || m > kMaxRows || b < 1 || b > 65535 || max_q < 1 || max_q > kMaxRows) return false;
+  if (heads < 1 || hq < heads || hq > 1024 || hq % heads != 0) return false;
+  return d == 64 || d == 128 || d == 256;
+}
+
+// a part's place in the sampler's lists has 20 bits
+bool sample_ok(int64_t n, int64_t b) { return n >= 1 && n <= (int64_t(1) << 20) && b >= 1 && b <= 65535; }
 
 bool logits_shape_ok(int64_t n, int64_t b) {
   // the grid's threads (one per 16 logits) stay below 2^32
@@ -523,6 +552,237 @@ int lowbit_lora_accumulate(const void* x, int x_type, int64_t ldx, const int32_t
   q.x_type = x_type;
   q.y_type = y_type;
   return hip_status(lowbit::launch_lora_accumulate(q, workspace, stream));
+}
+
+int lowbit_rope_turns(int64_t rot, double theta, int scaling, double factor, int64_t trained,
+                      double beta_fast, double beta_slow, uint64_t* turns, double* gain) {
+  if (!turns || !(theta > 1.0) || !std::isfinite(theta)) return LOWBIT_ERR_ARG;
+  if (scaling < LOWBIT_ROPE_PLAIN || scaling > LOWBIT_ROPE_YARN) return LOWBIT_ERR_ARG;
+  if (scaling != LOWBIT_ROPE_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor))) return LOWBIT_ERR_ARG;
+  if (scaling == LOWBIT_ROPE_YARN &&
+      (trained < 1 || !(beta_slow > 0.0) || !(beta_fast > beta_slow) || !std::isfinite(beta_fast)))
+    return LOWBIT_ERR_ARG;
+  if (rot < 2 || rot > 1024 || rot % 2 != 0) return LOWBIT_ERR_SHAPE;
+  if (scaling == LOWBIT_ROPE_NTK && rot == 2) return LOWBIT_ERR_SHAPE;
+  const double pi = 3.14159265358979323846, half = 0.5 * (double)rot;
+  if (scaling == LOWBIT_ROPE_NTK) theta *= std::pow(factor, (double)rot / (double)(rot - 2));
+  double low = 0.0, high = 1.0;
+  if (scaling == LOWBIT_ROPE_YARN) {
+    // the pair that turns `beta` times within the trained length
+    auto pair = [&](double beta) { return half * std::log((double)trained / (beta * 2.0 * pi)) / std::log(theta); };
+    low = std::fmax(std::floor(pair(beta_fast)), 0.0);
+    high = std::fmin(std::ceil(pair(beta_slow)), (double)(rot - 1));
+  }
+  for (int64_t i = 0; i < rot / 2; ++i) {
+    double f = std::pow(theta, -(double)i / half);
+    if (scaling == LOWBIT_ROPE_LINEAR) f /= factor;
+    if (scaling == LOWBIT_ROPE_YARN) {
+      const double ramp = std::fmin(std::fmax(((double)i - low) / std::fmax(high - low, 0.001), 0.0), 1.0);
+      f = f / factor * ramp + f * (1.0 - ramp);
+    }
+    turns[i] = (uint64_t)(f / (2.0 * pi) * 18446744073709551616.0);  // f <= 1: below 2^64
+  }
+  if (gain) *gain = scaling == LOWBIT_ROPE_YARN ? 0.1 * std::log(factor) + 1.0 : 1.0;
+  return LOWBIT_OK;
+}
+
+int lowbit_rope(const void* x, int x_type, int64_t ldx, int64_t ldxh, const int32_t* positions,
+                const uint64_t* turns, int64_t m, int64_t heads, int64_t d, int64_t rot,
+                int interleaved, double gain, void* out, int out_type, int64_t ldo, int64_t ldoh,
+                hipStream_t stream) {
+  if (!x || !positions || !turns || !out || !type_ok(x_type) || !type_ok(out_type)) return LOWBIT_ERR_ARG;
+  if (!std::isfinite(gain)) return LOWBIT_ERR_ARG;
+  if (m < 1 || m > kMaxRows || heads < 1 || heads > 65535 || d < 2 || d > 1024) return LOWBIT_ERR_SHAPE;
+  if (rot < 2 || rot > d || rot % 2 != 0) return LOWBIT_ERR_SHAPE;
+  if (!heads_ok(m, heads, d, ldx, ldxh) || !heads_ok(m, heads, d, ldo, ldoh)) return LOWBIT_ERR_SHAPE;
+  if (out == x && (out_type != x_type || ldo != ldx || ldoh != ldxh)) return LOWBIT_ERR_ARG;
+  if (!aligned_to_elem(x, x_type) || !aligned_to_elem(out, out_type) || !aligned4(positions) || !aligned8(turns))
+    return LOWBIT_ERR_ALIGN;
+  lowbit::RopeArgs a = {};
+  a.x = x;
+  a.out = out;
+  a.positions = positions;
+  a.turns = turns;
+  a.ldx = ldx;
+  a.ldxh = ldxh;
+  a.ldo = ldo;
+  a.ldoh = ldoh;
+  a.m = m;
+  a.heads = heads;
+  a.d = d;
+  a.rot = rot;
+  a.gain = gain;
+  a.inter = interleaved != 0;
+  a.x_type = x_type;
+  a.out_type = out_type;
+  return hip_status(lowbit::launch_rope(a, stream));
+}
+
+size_t lowbit_kv_page_bytes(int64_t heads, int64_t d, int64_t page) {
+  return cache_ok(heads, d, page, 1) ? (size_t)(heads * d * page * 5 / 4) : 0;
+}
+
+int lowbit_kv_store(const void* k, int64_t ldk, int64_t ldkh, const void* v, int64_t ldv,
+                    int64_t ldvh, int type, const int32_t* slots, int64_t m, int64_t heads,
+                    int64_t d, void* pages, int64_t n_pages, int64_t page,
+                    const int32_t* positions, const uint64_t* turns, int64_t rot, int interleaved,
+                    double gain, const void* q, int64_t ldq, int64_t ldqh, int64_t hq,
+                    void* q_out, int q_type, int64_t ldqo, int64_t ldqoh, hipStream_t stream) {
+  if (!k || !v || !slots || !pages || !type_ok(type)) return LOWBIT_ERR_ARG;
+  if (!positions != !turns || !q != !q_out || (q && (!turns || !type_ok(q_type)))) return LOWBIT_ERR_ARG;
+  if (turns && !std::isfinite(gain)) return LOWBIT_ERR_ARG;
+  if (m < 1 || m > kMaxRows || !cache_ok(heads, d, page, n_pages)) return LOWBIT_ERR_SHAPE;
+  if (!heads_ok(m, heads, d, ldk, ldkh) || !heads_ok(m, heads, d, ldv, ldvh)) return LOWBIT_ERR_SHAPE;
+  if (turns && (rot < 16 || rot > d || rot % 16 != 0)) return LOWBIT_ERR_SHAPE;
+  if (q && (hq < 1 || hq > 1024 || !heads_ok(m, hq, d, ldq, ldqh) || !heads_ok(m, hq, d, ldqo, ldqoh)))
+    return LOWBIT_ERR_SHAPE;
+  if (q && q_out == q && (q_type != type || ldqo != ldq || ldqoh != ldqh)) return LOWBIT_ERR_ARG;
+  if (!aligned_to_elem(k, type) || !aligned_to_elem(v, type) || !aligned4(slots) || !aligned16(pages) ||
+      !aligned4(positions) || !aligned8(turns) || (q && (!aligned_to_elem(q, type) || !aligned_to_elem(q_out, q_type))))
+    return LOWBIT_ERR_ALIGN;
+  lowbit::KvStoreArgs a = {};
+  a.k = k;
+  a.v = v;
+  a.slots = slots;
+  a.pages = static_cast<uint8_t*>(pages);
+  a.ldk = ldk;
+  a.ldkh = ldkh;
+  a.ldv = ldv;
+  a.ldvh = ldvh;
+  a.m = m;
+  a.heads = heads;
+  a.d = d;
+  a.page = page;
+  a.n_pages = n_pages;
+  a.in_type = type;
+  if (turns) {
+    a.positions = positions;
+    a.turns = turns;
+    a.rot = rot;
+    a.inter = interleaved != 0;
+    a.gain = gain;
+  }
+  if (q) {
+    a.q = q;
+    a.q_out = q_out;
+    a.ldq = ldq;
+    a.ldqh = ldqh;
+    a.ldqo = ldqo;
+    a.ldqoh = ldqoh;
+    a.hq = hq;
+    a.qo_type = q_type;
+  }
+  return hip_status(lowbit::launch_kv_store(a, stream));
+}
+
+int lowbit_kv_load(const void* pages, int64_t n_pages, int64_t heads, int64_t d, int64_t page,
+                   const int32_t* slots, int64_t m, void* k, int64_t ldk, int64_t ldkh, void* v,
+                   int64_t ldv, int64_t ldvh, int type, hipStream_t stream) {
+  if (!pages || !slots || (!k && !v) || !type_ok(type)) return LOWBIT_ERR_ARG;
+  if (k == v) return LOWBIT_ERR_ARG;
+  if (m < 1 || m > kMaxRows || !cache_ok(heads, d, page, n_pages)) return LOWBIT_ERR_SHAPE;
+  if ((k && !heads_ok(m, heads, d, ldk, ldkh)) || (v && !heads_ok(m, heads, d, ldv, ldvh))) return LOWBIT_ERR_SHAPE;
+  if (!aligned16(pages) || !aligned4(slots) || !aligned_to_elem(k, type) || !aligned_to_elem(v, type))
+    return LOWBIT_ERR_ALIGN;
+  lowbit::KvLoadArgs a = {};
+  a.pages = static_cast<const uint8_t*>(pages);
+  a.slots = slots;
+  a.k = k;
+  a.v = v;
+  a.ldk = ldk;
+  a.ldkh = ldkh;
+  a.ldv = ldv;
+  a.ldvh = ldvh;
+  a.m = m;
+  a.heads = heads;
+  a.d = d;
+  a.page = page;
+  a.n_pages = n_pages;
+  a.out_type = type;
+  return hip_status(lowbit::launch_kv_load(a, stream));
+}
+
+size_t lowbit_attention_workspace_bytes(int64_t m, int64_t b, int64_t hq, int64_t heads, int64_t d,
+                                        int64_t max_q) {
+  return attention_ok(m, b, hq, heads, d, max_q) ? lowbit::attention_workspace_bytes(hq, heads, d, max_q) : 0;
+}
+
+int lowbit_attention(const void* q, int q_type, int64_t ldq, int64_t ldqh, int64_t m, int64_t hq,
+                     const void* pages, int64_t n_pages, int64_t heads, int64_t d, int64_t page,
+                     const int32_t* table, int64_t tcap, int64_t ldt, const int32_t* lengths,
+                     const int32_t* q_start, int64_t b, int64_t max_q, float scale, void* out,
+                     int out_type, int64_t ldo, int64_t ldoh, float* lse, void* workspace,
+                     size_t workspace_bytes, hipStream_t stream) {
+  if (!q || !pages || !table || !lengths || !out || !type_ok(out_type)) return LOWBIT_ERR_ARG;
+  if (q_type != LOWBIT_F16 && q_type != LOWBIT_BF16) return LOWBIT_ERR_ARG;
+  if (!std::isfinite(scale) || out == q) return LOWBIT_ERR_ARG;
+  if (!q_start && (m != b || max_q != 1)) return LOWBIT_ERR_ARG;
+  if (!attention_ok(m, b, hq, heads, d, max_q) || !cache_ok(heads, d, page, n_pages)) return LOWBIT_ERR_SHAPE;
+  if (tcap < 1 || tcap > (int64_t(1) << 30) / page || !rows_ok(b, tcap, ldt)) return LOWBIT_ERR_SHAPE;
+  if (!heads_ok(m, hq, d, ldq, ldqh) || !heads_ok(m, hq, d, ldo, ldoh)) return LOWBIT_ERR_SHAPE;
+  if (!aligned_to_elem(q, q_type) || !aligned16(pages) || !aligned4(table) || !aligned4(lengths) ||
+      !aligned4(q_start) || !aligned_to_elem(out, out_type) || !aligned4(lse))
+    return LOWBIT_ERR_ALIGN;
+  if (!workspace || workspace_bytes < lowbit::attention_workspace_bytes(hq, heads, d, max_q))
+    return LOWBIT_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return LOWBIT_ERR_ALIGN;
+  lowbit::AttnArgs a = {};
+  a.q = q;
+  a.pages = static_cast<const uint8_t*>(pages);
+  a.table = table;
+  a.lengths = lengths;
+  a.q_start = q_start;
+  a.out = out;
+  a.lse = lse;
+  a.ldq = ldq;
+  a.ldqh = ldqh;
+  a.ldo = ldo;
+  a.ldoh = ldoh;
+  a.m = m;
+  a.hq = hq;
+  a.heads = heads;
+  a.d = d;
+  a.page = page;
+  a.n_pages = n_pages;
+  a.tcap = tcap;
+  a.ldt = ldt;
+  a.b = b;
+  a.max_q = max_q;
+  a.scale = scale;
+  a.q_type = q_type;
+  a.out_type = out_type;
+  return hip_status(lowbit::launch_attention(a, workspace, stream));
+}
+
+size_t lowbit_sample_workspace_bytes(int64_t n, int64_t b) {
+  return sample_ok(n, b) ? lowbit::sample_workspace_bytes(n, b) : 0;
+}
+
+int lowbit_sample(const void* y, int y_type, int64_t ldy, int64_t n, int64_t b,
+                  const float* temperature, const int32_t* top_k, const float* top_p,
+                  const float* min_p, const float* u, int32_t* idx, float* prob, void* workspace,
+                  size_t workspace_bytes, hipStream_t stream) {
+  if (!y || !u || !idx || !type_ok(y_type)) return LOWBIT_ERR_ARG;
+  if (!sample_ok(n, b) || !rows_ok(b, n, ldy)) return LOWBIT_ERR_SHAPE;
+  if (!aligned_to_elem(y, y_type) || !aligned4(temperature) || !aligned4(top_k) || !aligned4(top_p) ||
+      !aligned4(min_p) || !aligned4(u) || !aligned4(idx) || !aligned4(prob))
+    return LOWBIT_ERR_ALIGN;
+  if (!workspace || workspace_bytes < lowbit::sample_workspace_bytes(n, b)) return LOWBIT_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return LOWBIT_ERR_ALIGN;
+  lowbit::SampleArgs a = {};
+  a.y = y;
+  a.temperature = temperature;
+  a.top_k = top_k;
+  a.top_p = top_p;
+  a.min_p = min_p;
+  a.u = u;
+  a.idx = idx;
+  a.prob = prob;
+  a.ldy = ldy;
+  a.n = n;
+  a.b = b;
+  a.y_type = y_type;
+  return hip_status(lowbit::launch_sample(a, workspace, stream));
 }
 
 }  // extern "C"

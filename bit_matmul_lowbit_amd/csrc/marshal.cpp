@@ -9,12 +9,15 @@
 #include <c10/core/DeviceGuard.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
+#include <cmath>
+
 #include "lowbit.h"
 
 namespace {
 
 // as lowbit_type, and what else the calls take
-enum Code { kNone = 0, kF32 = 1, kF16 = 2, kBF16 = 3, kI32 = 4, kU8 = 5 };
+enum Code { kNone = 0, kF32 = 1, kF16 = 2, kBF16 = 3, kI32 = 4, kU8 = 5, kI64 = 6 };
 
 int code_of(const at::Tensor& t) {
   switch (t.scalar_type()) {
@@ -23,13 +26,14 @@ int code_of(const at::Tensor& t) {
     case at::kBFloat16: return kBF16;
     case at::kInt: return kI32;
     case at::kByte: return kU8;
+    case at::kLong: return kI64;
     default: return kNone;
   }
 }
 
 const char* name_of(long code) {
-  static const char* const names[] = {"?", "float32", "float16", "bfloat16", "int32", "uint8"};
-  return names[code >= 1 && code <= 5 ? code : 0];
+  static const char* const names[] = {"?", "float32", "float16", "bfloat16", "int32", "uint8", "int64"};
+  return names[code >= 1 && code <= 6 ? code : 0];
 }
 
 // the tensor of argument `o`, on a GPU, or NULL with the error set
@@ -89,6 +93,14 @@ struct {
   decltype(&lowbit_logits_process) logits;
   decltype(&lowbit_lora_workspace_bytes) lora_bytes;
   decltype(&lowbit_lora_accumulate) lora;
+  decltype(&lowbit_rope) rope;
+  decltype(&lowbit_kv_page_bytes) page_bytes;
+  decltype(&lowbit_kv_store) kv_store;
+  decltype(&lowbit_kv_load) kv_load;
+  decltype(&lowbit_attention_workspace_bytes) attention_bytes;
+  decltype(&lowbit_attention) attention;
+  decltype(&lowbit_sample_workspace_bytes) sample_bytes;
+  decltype(&lowbit_sample) sample;
   PyObject* raw_stream;  // device -> address of its current stream
   PyObject* empty;       // (shape, type code or dtype, device of, stream) -> tensor
   PyObject* error;       // LowbitError
@@ -257,17 +269,22 @@ bool address(PyObject* o, T* out) {
   return !PyErr_Occurred();
 }
 
-// bind(norm, logits_bytes, logits, lora_bytes, lora, raw_stream, empty, error)
+// bind(norm, logits_bytes, logits, lora_bytes, lora, rope, page_bytes, kv_store,
+// kv_load, attention_bytes, attention, sample_bytes, sample, raw_stream, empty,
+// error)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!count_ok(n, 8)) return nullptr;
+  if (!count_ok(n, 16)) return nullptr;
   if (!address(a[0], &bound.norm) || !address(a[1], &bound.logits_bytes) || !address(a[2], &bound.logits) ||
-      !address(a[3], &bound.lora_bytes) || !address(a[4], &bound.lora))
+      !address(a[3], &bound.lora_bytes) || !address(a[4], &bound.lora) || !address(a[5], &bound.rope) ||
+      !address(a[6], &bound.page_bytes) || !address(a[7], &bound.kv_store) || !address(a[8], &bound.kv_load) ||
+      !address(a[9], &bound.attention_bytes) || !address(a[10], &bound.attention) ||
+      !address(a[11], &bound.sample_bytes) || !address(a[12], &bound.sample))
     return nullptr;
   PyObject** const keep[] = {&bound.raw_stream, &bound.empty, &bound.error};
   for (int i = 0; i < 3; ++i) {
-    Py_INCREF(a[5 + i]);
+    Py_INCREF(a[13 + i]);
     Py_XDECREF(*keep[i]);
-    *keep[i] = a[5 + i];
+    *keep[i] = a[13 + i];
   }
   Py_RETURN_NONE;
 }
@@ -478,10 +495,374 @@ PyObject* lora(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// a tensor [m][heads][d] whose heads are contiguous; -1: any size
+struct Heads {
+  void* p = nullptr;
+  int type = 0;
+  int64_t m = 0, heads = 0, d = 0, ld = 0, ldh = 0;
+};
+bool get_heads(PyObject* o, const char* name, int64_t m, int64_t heads, int64_t d, int dev, Heads* out) {
+  const at::Tensor* t = tensor(o, name);
+  if (!t) return false;
+  const int code = code_of(*t);
+  if (code < kF32 || code > kBF16) {
+    PyErr_Format(PyExc_TypeError, "%s must be float32, float16 or bfloat16", name);
+    return false;
+  }
+  if (dev >= 0 && !on_device(*t, dev, name)) return false;
+  const auto size = t->sizes(), stride = t->strides();
+  if (size.size() != 3) {
+    PyErr_Format(PyExc_ValueError, "%s must have three dimensions [m][heads][d], not %zd", name,
+                 (Py_ssize_t)size.size());
+    return false;
+  }
+  if ((m >= 0 && size[0] != m) || (heads >= 0 && size[1] != heads) || (d >= 0 && size[2] != d)) {
+    PyErr_Format(PyExc_ValueError, "%s has shape [%lld, %lld, %lld], expected [%lld, %lld, %lld]", name,
+                 (long long)size[0], (long long)size[1], (long long)size[2], (long long)(m >= 0 ? m : size[0]),
+                 (long long)(heads >= 0 ? heads : size[1]), (long long)(d >= 0 ? d : size[2]));
+    return false;
+  }
+  if (size[2] > 1 && stride[2] != 1) {
+    PyErr_Format(PyExc_ValueError, "%s: the elements of a head must be contiguous", name);
+    return false;
+  }
+  // the stride of a dimension of one is not used; it may be anything
+  const int64_t ldh = size[1] > 1 ? stride[1] : size[2];
+  const int64_t ld = size[0] > 1 ? stride[0] : size[1] * size[2];
+  *out = {t->data_ptr(), code, size[0], size[1], size[2], ld, ldh};
+  return true;
+}
+
+bool device_of(PyObject* o, const char* name, int* dev) {
+  const at::Tensor* t = tensor(o, name);
+  if (t) *dev = t->get_device();
+  return t != nullptr;
+}
+
+at::ScalarType scalar_of(int code) {
+  return code == kF32 ? at::kFloat : code == kF16 ? at::kHalf : at::kBFloat16;
+}
+
+// the pages of a cache: uint8 [pages][page_bytes], contiguous
+bool get_pages(PyObject* o, int dev, int64_t* n, int64_t* bytes, uint8_t** p) {
+  if (o == Py_None) {
+    PyErr_SetString(PyExc_TypeError, "pages must be a CUDA (HIP) tensor");
+    return false;
+  }
+  if (!get_vector(o, "pages", kU8, 0, dev, p)) return false;
+  const at::Tensor& t = THPVariable_Unpack(o);
+  if (t.dim() != 2) {
+    PyErr_SetString(PyExc_ValueError, "pages must be [pages][bytes of a page]");
+    return false;
+  }
+  *n = t.size(0);
+  *bytes = t.size(1);
+  return true;
+}
+bool fits_page(int64_t bytes, int64_t heads, int64_t d, int64_t page) {
+  const int64_t want = (int64_t)bound.page_bytes(heads, d, page);
+  if (want == 0 || bytes == want) return true;  // a bad shape is the library's to refuse
+  PyErr_Format(PyExc_ValueError, "pages of %lld bytes do not hold %lld tokens of %lld heads of %lld (%lld bytes)",
+               (long long)bytes, (long long)page, (long long)heads, (long long)d, (long long)want);
+  return false;
+}
+
+template <class T>
+bool need_vector(PyObject* o, const char* name, int code, long long count, int dev, T** out) {
+  if (o == Py_None) {
+    PyErr_Format(PyExc_TypeError, "%s must be a CUDA (HIP) tensor", name);
+    return false;
+  }
+  return get_vector(o, name, code, count, dev, out);
+}
+
+// rope(x, positions, turns, out, out_code, interleaved, gain, stream) -> out
+PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_ok(n, 8) || !ready()) return nullptr;
+  return guarded([&]() -> PyObject* {
+    PyObject *x = a[0], *out = a[3], *stream = a[7];
+    const long code = PyLong_AsLong(a[4]);
+    const int inter = PyObject_IsTrue(a[5]);
+    const double gain = PyFloat_AsDouble(a[6]);
+    if (PyErr_Occurred()) return nullptr;
+    int dev;
+    hipStream_t st;
+    Heads hx, ho;
+    if (!device_of(x, "x", &dev) || !get_stream(stream, dev, &st) || !get_heads(x, "x", -1, -1, -1, dev, &hx))
+      return nullptr;
+    const int32_t* positions;
+    const uint64_t* turns;
+    if (!need_vector(a[1], "positions", kI32, hx.m, dev, &positions) ||
+        !need_vector(a[2], "turns", kI64, 0, dev, &turns))
+      return nullptr;
+    const int64_t rot = 2 * THPVariable_Unpack(a[2]).numel();
+    Ref made;
+    if (out == Py_None) {
+      const int type = code ? (int)code : hx.type;
+      if (!make(THPVariable_Unpack(x), THPVariable_Unpack(x).sizes(), scalar_of(type), type, stream, &made))
+        return nullptr;
+      out = made.o;
+    }
+    if (!get_heads(out, "out", hx.m, hx.heads, hx.d, dev, &ho)) return nullptr;
+    if (!launch(dev, "lowbit_rope", [&] {
+          return bound.rope(hx.p, hx.type, hx.ld, hx.ldh, positions, turns, hx.m, hx.heads, hx.d, rot, inter, gain,
+                            ho.p, ho.type, ho.ld, ho.ldh, st);
+        }))
+      return nullptr;
+    Py_INCREF(out);
+    return out;
+  });
+}
+
+// kv_store(k, v, slots, pages, page, positions, turns, interleaved, gain, q,
+// q_out, q_code, stream) -> q_out or None
+PyObject* kv_store(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_ok(n, 13) || !ready()) return nullptr;
+  return guarded([&]() -> PyObject* {
+    PyObject *k = a[0], *v = a[1], *q = a[9], *q_out = a[10], *stream = a[12];
+    const int64_t page = PyLong_AsLongLong(a[4]);
+    const int inter = PyObject_IsTrue(a[7]);
+    const double gain = PyFloat_AsDouble(a[8]);
+    const long code = PyLong_AsLong(a[11]);
+    if (PyErr_Occurred()) return nullptr;
+    int dev;
+    hipStream_t st;
+    Heads hk, hv, hq, ho;
+    if (!device_of(k, "k", &dev) || !get_stream(stream, dev, &st) || !get_heads(k, "k", -1, -1, -1, dev, &hk) ||
+        !get_heads(v, "v", hk.m, hk.heads, hk.d, dev, &hv))
+      return nullptr;
+    if (hv.type != hk.type) {
+      PyErr_SetString(PyExc_TypeError, "k, v and q must have one type");
+      return nullptr;
+    }
+    const int32_t *slots, *positions;
+    const uint64_t* turns;
+    uint8_t* pages;
+    int64_t n_pages, bytes, rot = 0;
+    if (!need_vector(a[2], "slots", kI32, hk.m, dev, &slots) || !get_pages(a[3], dev, &n_pages, &bytes, &pages) ||
+        !fits_page(bytes, hk.heads, hk.d, page) || !get_vector(a[5], "positions", kI32, hk.m, dev, &positions) ||
+        !get_vector(a[6], "turns", kI64, 0, dev, &turns))
+      return nullptr;
+    if ((a[5] == Py_None) != (a[6] == Py_None)) {
+      PyErr_SetString(PyExc_ValueError, "positions and turns go together");
+      return nullptr;
+    }
+    if (a[6] != Py_None) rot = 2 * THPVariable_Unpack(a[6]).numel();
+    Ref made;
+    if (q != Py_None) {
+      if (a[6] == Py_None) {
+        PyErr_SetString(PyExc_ValueError, "q needs positions and turns");
+        return nullptr;
+      }
+      if (!get_heads(q, "q", hk.m, -1, hk.d, dev, &hq)) return nullptr;
+      if (hq.type != hk.type) {
+        PyErr_SetString(PyExc_TypeError, "k, v and q must have one type");
+        return nullptr;
+      }
+      if (q_out == Py_None) {
+        const int type = code ? (int)code : hq.type == kF32 ? (int)kF16 : hq.type;
+        if (!make(THPVariable_Unpack(q), THPVariable_Unpack(q).sizes(), scalar_of(type), type, stream, &made))
+          return nullptr;
+        q_out = made.o;
+      }
+      if (!get_heads(q_out, "q_out", hk.m, hq.heads, hk.d, dev, &ho)) return nullptr;
+    } else if (q_out != Py_None) {
+      PyErr_SetString(PyExc_ValueError, "q_out needs q");
+      return nullptr;
+    }
+    if (!launch(dev, "lowbit_kv_store", [&] {
+          return bound.kv_store(hk.p, hk.ld, hk.ldh, hv.p, hv.ld, hv.ldh, hk.type, slots, hk.m, hk.heads, hk.d, pages,
+                                n_pages, page, positions, turns, rot, inter, gain, hq.p, hq.ld, hq.ldh, hq.heads,
+                                ho.p, ho.type, ho.ld, ho.ldh, st);
+        }))
+      return nullptr;
+    Py_INCREF(q_out);
+    return q_out;
+  });
+}
+
+// kv_load(pages, page, slots, heads, d, k_out, v_out, code, stream) -> (k, v)
+PyObject* kv_load(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_ok(n, 9) || !ready()) return nullptr;
+  return guarded([&]() -> PyObject* {
+    PyObject *k = a[5], *v = a[6], *stream = a[8];
+    const int64_t page = PyLong_AsLongLong(a[1]), heads = PyLong_AsLongLong(a[3]), d = PyLong_AsLongLong(a[4]);
+    const long code = PyLong_AsLong(a[7]);
+    if (PyErr_Occurred()) return nullptr;
+    int dev;
+    hipStream_t st;
+    uint8_t* pages;
+    int64_t n_pages, bytes;
+    const int32_t* slots;
+    if (!device_of(a[0], "pages", &dev) || !get_stream(stream, dev, &st) ||
+        !get_pages(a[0], dev, &n_pages, &bytes, &pages) || !fits_page(bytes, heads, d, page) ||
+        !need_vector(a[2], "slots", kI32, 0, dev, &slots))
+      return nullptr;
+    const int64_t m = THPVariable_Unpack(a[2]).numel();
+    if (heads < 0 || d < 0) {
+      PyErr_SetString(PyExc_ValueError, "heads and d must not be negative");
+      return nullptr;
+    }
+    Ref made_k, made_v;
+    const at::Tensor& like = THPVariable_Unpack(a[0]);
+    const bool both = k == Py_None && v == Py_None;
+    if (both) {
+      if (!make(like, {m, heads, d}, scalar_of((int)code), (int)code, stream, &made_k) ||
+          !make(like, {m, heads, d}, scalar_of((int)code), (int)code, stream, &made_v))
+        return nullptr;
+      k = made_k.o;
+      v = made_v.o;
+    }
+    Heads hk, hv;
+    if ((k != Py_None && !get_heads(k, "k_out", m, heads, d, dev, &hk)) ||
+        (v != Py_None && !get_heads(v, "v_out", m, heads, d, dev, &hv)))
+      return nullptr;
+    if (k != Py_None && v != Py_None && hk.type != hv.type) {
+      PyErr_SetString(PyExc_TypeError, "k_out and v_out must have one type");
+      return nullptr;
+    }
+    if (!launch(dev, "lowbit_kv_load", [&] {
+          return bound.kv_load(pages, n_pages, heads, d, page, slots, m, hk.p, hk.ld, hk.ldh, hv.p, hv.ld, hv.ldh,
+                               k != Py_None ? hk.type : hv.type, st);
+        }))
+      return nullptr;
+    return PyTuple_Pack(2, k, v);
+  });
+}
+
+// attention(q, pages, page, table, lengths, q_start, max_q, scale or None, out,
+// out_code, lse, workspace, stream) -> out
+PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_ok(n, 13) || !ready()) return nullptr;
+  return guarded([&]() -> PyObject* {
+    PyObject *q = a[0], *out = a[8], *workspace = a[11], *stream = a[12];
+    const int64_t page = PyLong_AsLongLong(a[2]);
+    const long code = PyLong_AsLong(a[9]);
+    if (PyErr_Occurred()) return nullptr;
+    int dev;
+    hipStream_t st;
+    Heads hq, ho;
+    uint8_t* pages;
+    int64_t n_pages, bytes;
+    if (!device_of(q, "q", &dev) || !get_stream(stream, dev, &st) || !get_heads(q, "q", -1, -1, -1, dev, &hq) ||
+        !get_pages(a[1], dev, &n_pages, &bytes, &pages))
+      return nullptr;
+    // as many KV heads as a page has room for
+    const int64_t one = (int64_t)bound.page_bytes(1, hq.d, page);
+    const int64_t heads = one ? bytes / one : 1;
+    if (one && (heads < 1 || heads * one != bytes)) {
+      PyErr_Format(PyExc_ValueError, "pages of %lld bytes do not hold %lld tokens of heads of %lld", (long long)bytes,
+                   (long long)page, (long long)hq.d);
+      return nullptr;
+    }
+    if (a[3] == Py_None) {
+      PyErr_SetString(PyExc_TypeError, "table must be a CUDA (HIP) tensor");
+      return nullptr;
+    }
+    Lists<const int32_t> table;
+    const int32_t *lengths, *q_start;
+    if (!get_lists(a[3], "table", kI32, -1, dev, &table) ||
+        !need_vector(a[4], "lengths", kI32, table.rows, dev, &lengths) ||
+        !get_vector(a[5], "q_start", kI32, table.rows + 1, dev, &q_start))
+      return nullptr;
+    int64_t max_q = 1;
+    if (a[5] != Py_None) {
+      max_q = a[6] == Py_None ? hq.m : PyLong_AsLongLong(a[6]);
+      if (PyErr_Occurred()) return nullptr;
+    } else if (a[6] != Py_None) {
+      max_q = PyLong_AsLongLong(a[6]);
+      if (PyErr_Occurred()) return nullptr;
+    }
+    const double scale = a[7] == Py_None ? 1.0 / std::sqrt((double)std::max<int64_t>(hq.d, 1)) : PyFloat_AsDouble(a[7]);
+    if (PyErr_Occurred()) return nullptr;
+    Ref made, made_ws;
+    if (out == Py_None) {
+      const int type = code ? (int)code : hq.type;
+      if (!make(THPVariable_Unpack(q), THPVariable_Unpack(q).sizes(), scalar_of(type), type, stream, &made))
+        return nullptr;
+      out = made.o;
+    }
+    float* lse;
+    uint8_t* ws;
+    if (!get_heads(out, "out", hq.m, hq.heads, hq.d, dev, &ho) ||
+        !get_vector(a[10], "lse", kF32, hq.m * hq.heads, dev, &lse))
+      return nullptr;
+    if (workspace == Py_None) {
+      const int64_t need = (int64_t)bound.attention_bytes(hq.m, table.rows, hq.heads, heads, hq.d, max_q);
+      if (!make(THPVariable_Unpack(q), {need > 16 ? need : 16}, at::kByte, kU8, stream, &made_ws)) return nullptr;
+      workspace = made_ws.o;
+    }
+    if (!get_vector(workspace, "workspace", kU8, 0, dev, &ws)) return nullptr;
+    const int64_t ws_bytes = THPVariable_Unpack(workspace).numel();
+    if (!launch(dev, "lowbit_attention", [&] {
+          return bound.attention(hq.p, hq.type, hq.ld, hq.ldh, hq.m, hq.heads, pages, n_pages, heads, hq.d, page,
+                                 table.p, table.columns, table.ld, lengths, q_start, table.rows, max_q, (float)scale,
+                                 ho.p, ho.type, ho.ld, ho.ldh, lse, ws, (size_t)ws_bytes, st);
+        }))
+      return nullptr;
+    Py_INCREF(out);
+    return out;
+  });
+}
+
+// sample(y, u, temperature, top_k, top_p, min_p, idx, prob, workspace, stream)
+// -> (idx, prob)
+PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_ok(n, 10) || !ready()) return nullptr;
+  return guarded([&]() -> PyObject* {
+    PyObject *y = a[0], *idx = a[6], *prob = a[7], *workspace = a[8], *stream = a[9];
+    long long b, v;
+    int dev;
+    hipStream_t st;
+    Rows ry;
+    if (!get_shape(y, "y", &b, &v, &dev) || !get_stream(stream, dev, &st) || !get_rows(y, "y", b, v, dev, &ry))
+      return nullptr;
+    const float *u, *temperature, *top_p, *min_p;
+    const int32_t* top_k;
+    if (!need_vector(a[1], "u", kF32, b, dev, &u) || !get_vector(a[2], "temperature", kF32, b, dev, &temperature) ||
+        !get_vector(a[3], "top_k", kI32, b, dev, &top_k) || !get_vector(a[4], "top_p", kF32, b, dev, &top_p) ||
+        !get_vector(a[5], "min_p", kF32, b, dev, &min_p))
+      return nullptr;
+    const at::Tensor& t = THPVariable_Unpack(y);
+    Ref made_idx, made_prob, made_ws;
+    if (idx == Py_None) {
+      if (!make(t, {b}, at::kInt, kI32, stream, &made_idx)) return nullptr;
+      idx = made_idx.o;
+    }
+    if (prob == Py_None) {
+      if (!make(t, {b}, at::kFloat, kF32, stream, &made_prob)) return nullptr;
+      prob = made_prob.o;
+    }
+    if (workspace == Py_None) {
+      const int64_t need = (int64_t)bound.sample_bytes(v, b);
+      if (!make(t, {need > 16 ? need : 16}, at::kByte, kU8, stream, &made_ws)) return nullptr;
+      workspace = made_ws.o;
+    }
+    int32_t* idx_p;
+    float* prob_p;
+    uint8_t* ws;
+    if (!get_vector(idx, "idx", kI32, b, dev, &idx_p) || !get_vector(prob, "prob", kF32, b, dev, &prob_p) ||
+        !get_vector(workspace, "workspace", kU8, 0, dev, &ws))
+      return nullptr;
+    const int64_t ws_bytes = THPVariable_Unpack(workspace).numel();
+    if (!launch(dev, "lowbit_sample", [&] {
+          return bound.sample(ry.p, ry.type, ry.ld, v, b, temperature, top_k, top_p, min_p, u, idx_p, prob_p, ws,
+                              (size_t)ws_bytes, st);
+        }))
+      return nullptr;
+    return PyTuple_Pack(2, idx, prob);
+  });
+}
+
 PyMethodDef methods[] = {{"bind", (PyCFunction)(void (*)())bind, METH_FASTCALL, nullptr},
                          {"norm", (PyCFunction)(void (*)())norm, METH_FASTCALL, nullptr},
                          {"logits", (PyCFunction)(void (*)())logits, METH_FASTCALL, nullptr},
                          {"lora", (PyCFunction)(void (*)())lora, METH_FASTCALL, nullptr},
+                         {"rope", (PyCFunction)(void (*)())rope, METH_FASTCALL, nullptr},
+                         {"kv_store", (PyCFunction)(void (*)())kv_store, METH_FASTCALL, nullptr},
+                         {"kv_load", (PyCFunction)(void (*)())kv_load, METH_FASTCALL, nullptr},
+                         {"attention", (PyCFunction)(void (*)())attention, METH_FASTCALL, nullptr},
+                         {"sample", (PyCFunction)(void (*)())sample, METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -30,9 +30,12 @@ SYMBOLS = [
     "lowbit_argmax", "lowbit_lm_head_workspace_bytes", "lowbit_lm_head",
     "lowbit_norm_residual", "lowbit_logits_workspace_bytes", "lowbit_logits_process",
     "lowbit_lora_workspace_bytes", "lowbit_lora_accumulate",
+    "lowbit_rope_turns", "lowbit_rope", "lowbit_kv_page_bytes", "lowbit_kv_store", "lowbit_kv_load",
+    "lowbit_attention_workspace_bytes", "lowbit_attention", "lowbit_sample_workspace_bytes", "lowbit_sample",
 ]
 
 NORMS = {"none": 0, "rms": 1, "layer": 2}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 
 # ceiling probes (include/lowbit_probes.h): context for the roofline only
@@ -66,7 +69,7 @@ def load() -> ctypes.CDLL:
 
     lib = ctypes.CDLL(LIB_PATH)
     p, i64, sz, i = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
-    f = ctypes.c_float
+    f, dbl = ctypes.c_float, ctypes.c_double
     sig = {
         "lowbit_version": ([], i),
         "lowbit_status_str": ([i], ctypes.c_char_p),
@@ -99,6 +102,17 @@ def load() -> ctypes.CDLL:
         "lowbit_lora_workspace_bytes": ([i64, i64, i64, i64, i64], sz),
         "lowbit_lora_accumulate": ([p, i, i64, p, i64, i64, i64, i64, i64, p, p, p, p, p, i, i64, p, sz,
                                     p], i),
+        "lowbit_rope_turns": ([i64, dbl, i, dbl, i64, dbl, dbl, p, p], i),
+        "lowbit_rope": ([p, i, i64, i64, p, p, i64, i64, i64, i64, i, dbl, p, i, i64, i64, p], i),
+        "lowbit_kv_page_bytes": ([i64, i64, i64], sz),
+        "lowbit_kv_store": ([p, i64, i64, p, i64, i64, i, p, i64, i64, i64, p, i64, i64, p, p, i64, i, dbl, p, i64,
+                             i64, i64, p, i, i64, i64, p], i),
+        "lowbit_kv_load": ([p, i64, i64, i64, i64, p, i64, p, i64, i64, p, i64, i64, i, p], i),
+        "lowbit_attention_workspace_bytes": ([i64, i64, i64, i64, i64, i64], sz),
+        "lowbit_attention": ([p, i, i64, i64, i64, i64, p, i64, i64, i64, i64, p, i64, i64, p, p, i64, i64, f, p, i,
+                              i64, i64, p, p, sz, p], i),
+        "lowbit_sample_workspace_bytes": ([i64, i64], sz),
+        "lowbit_sample": ([p, i, i64, i64, i64, p, p, p, p, p, p, p, p, sz, p], i),
         "lowbit_quantize_t2": ([p, i64, i64, p, p, p], i),
         "lowbit_base3_bytes": ([i64, i64], sz),
         "lowbit_t2_to_base3": ([p, p, i64, i64, p, p, p], i),
@@ -588,7 +602,9 @@ def _first_use():
     _codes.update({torch.float32: 1, torch.float16: 2, torch.bfloat16: 3, torch.int32: 4, torch.uint8: 5})
     _marshal.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in
                     ("lowbit_norm_residual", "lowbit_logits_workspace_bytes", "lowbit_logits_process",
-                     "lowbit_lora_workspace_bytes", "lowbit_lora_accumulate")),
+                     "lowbit_lora_workspace_bytes", "lowbit_lora_accumulate", "lowbit_rope", "lowbit_kv_page_bytes",
+                     "lowbit_kv_store", "lowbit_kv_load", "lowbit_attention_workspace_bytes", "lowbit_attention",
+                     "lowbit_sample_workspace_bytes", "lowbit_sample")),
                   torch._C._cuda_getCurrentRawStream, _empty, LowbitError)
     _m = _marshal
     return _m
@@ -646,6 +662,100 @@ def lowbit_lora_accumulate(x, ids, a, b, y, ranks=None, scales=None, workspace=N
     FP32 [slots], y [m][n] FP32 (or BF16 with BF16 x); rows of x and y may be
     strided (a slice of a fused projection's output)."""
     return (_m or _first_use()).lora(x, ids, a, b, y, ranks, scales, workspace, stream)
+
+
+def _type_code(dtype, name, none=0):
+    """The library's number of an FP type; `none` for None."""
+    code = none if dtype is None else _codes.get(dtype, 9)
+    if code > 3:
+        raise TypeError(f"{name} must be float32, float16 or bfloat16")
+    return code
+
+
+def lowbit_rope_turns(rot: int, theta: float = 10000.0, scaling="none", factor: float = 1.0, trained: int = 1,
+                      beta_fast: float = 32.0, beta_slow: float = 1.0, device=None):
+    """Frequencies of rotary positions for a head of which `rot` values turn:
+    (turns int64 [rot / 2] on `device`, gain).
+
+    scaling for contexts longer than the `trained` length: "none", "linear" (f /
+    factor), "ntk" (a larger base) or "yarn" (by parts, with a gain).  Made once
+    and kept; device None: the current GPU."""
+    import torch
+
+    turns, gain = (ctypes.c_uint64 * max(1, rot // 2))(), ctypes.c_double()
+    _check(load().lowbit_rope_turns(rot, theta, ROPE_SCALINGS[scaling], factor, trained, beta_fast, beta_slow, turns,
+                                    ctypes.byref(gain)), "lowbit_rope_turns")
+    signed = [v - 2 ** 64 if v >= 2 ** 63 else v for v in turns]
+    return torch.tensor(signed, dtype=torch.int64, device="cuda" if device is None else device), gain.value
+
+
+def lowbit_rope(x, positions, turns, out=None, interleaved=False, gain=1.0, out_dtype=None, stream=None):
+    """Rotary positions: x [m][heads][d] turned by positions int32 [m] with
+    `turns` of lowbit_rope_turns (the first 2 * len(turns) values of a head;
+    the others are copied); returns out (x itself: in place; made with out_dtype,
+    or x's type, if not given).  Tokens and heads of x and out may be strided (a slice
+    of a fused product's output)."""
+    m = _m or _first_use()
+    return m.rope(x, positions, turns, out, _type_code(out_dtype, "out_dtype"), interleaved, gain, stream)
+
+
+def lowbit_kv_page_bytes(heads: int, d: int, page: int) -> int:
+    return int(load().lowbit_kv_page_bytes(heads, d, page))
+
+
+def lowbit_kv_store(k, v, slots, pages, page: int, positions=None, turns=None, interleaved=False, gain=1.0, q=None,
+                    q_out=None, q_dtype=None, stream=None):
+    """k and v [m][heads][d] written to a cache held in 4 bits, at slots int32
+    [m] (outside the cache: not written) of pages uint8
+    [pages][lowbit_kv_page_bytes(heads, d, page)].
+
+    With positions and turns the keys are turned first, and q [m][hq][d] is
+    turned beside them into q_out, which is returned (made with q_dtype, or FP16
+    for FP32 and else q's type, if not given)."""
+    m = _m or _first_use()
+    return m.kv_store(k, v, slots, pages, page, positions, turns, interleaved, gain, q, q_out,
+                      _type_code(q_dtype, "q_dtype"), stream)
+
+
+def lowbit_kv_load(pages, page: int, slots, heads: int, d: int, k_out=None, v_out=None, dtype=None, stream=None):
+    """(k, v) [m][heads][d] as the cache holds them at slots int32 [m] (zeros
+    where one is outside).  Without k_out and v_out both are made, with dtype
+    (FP16 if not given); with one of them only that one is read."""
+    m = _m or _first_use()
+    return m.kv_load(pages, page, slots, heads, d, k_out, v_out, _type_code(dtype, "dtype", 2), stream)
+
+
+def lowbit_attention_workspace_bytes(m: int, b: int, hq: int, heads: int, d: int, max_q: int = 1) -> int:
+    return int(load().lowbit_attention_workspace_bytes(m, b, hq, heads, d, max_q))
+
+
+def lowbit_attention(q, pages, page: int, table, lengths, q_start=None, max_q=None, scale=None, out=None,
+                     out_dtype=None, lse=None, workspace=None, stream=None):
+    """Attention of q [m][hq][d] (FP16 or BF16) over a cache held in 4 bits;
+    returns out [m][hq][d] (made with out_dtype, or q's type, if not given).
+
+    Sequence i has lengths[i] tokens in the pages table[i] (int32 [b][.]), and its
+    queries are the last of them: one each (m = b), or rows q_start[i] ..
+    q_start[i + 1] - 1 (int32 [b + 1]; max_q: the most of a sequence, m if not
+    given).  scale: d^-0.5 if not given.  lse FP32 [m][hq] takes the logarithm of the
+    sums."""
+    m = _m or _first_use()
+    return m.attention(q, pages, page, table, lengths, q_start, max_q, scale, out, _type_code(out_dtype, "out_dtype"),
+                       lse, workspace, stream)
+
+
+def lowbit_sample_workspace_bytes(n: int, b: int) -> int:
+    return int(load().lowbit_sample_workspace_bytes(n, b))
+
+
+def lowbit_sample(y, u, temperature=None, top_k=None, top_p=None, min_p=None, idx=None, prob=None, workspace=None,
+                  stream=None):
+    """A token from each row of logits y [b][n] (those of lowbit_logits_process)
+    by the random numbers u FP32 [b]; returns (idx int32 [b], prob FP32 [b]).
+
+    temperature, top_p, min_p FP32 [b], top_k int32 [b]; None: 1, 1, 0 and 0,
+    which filter nothing."""
+    return (_m or _first_use()).sample(y, u, temperature, top_k, top_p, min_p, idx, prob, workspace, stream)
 
 
 # ---------------------------------------------------------------------------

@@ -129,6 +129,16 @@ typedef enum {
                            var(v) = mean((v - mean(v))^2)                     */
 } lowbit_norm;
 
+/* Scaling of lowbit_rope_turns for contexts longer than the trained one. */
+typedef enum {
+  LOWBIT_ROPE_PLAIN = 0,  /* f                                                */
+  LOWBIT_ROPE_LINEAR = 1, /* f / factor                                       */
+  LOWBIT_ROPE_NTK = 2,    /* theta * factor^(rot / (rot - 2)) as the base      */
+  LOWBIT_ROPE_YARN = 3    /* f for pairs that turn often within the trained
+                             length, f / factor for those that turn little, a
+                             ramp between                                     */
+} lowbit_rope_scaling;
+
 /* Library ABI version (this header describes version 1). */
 int lowbit_version(void);
 
@@ -494,6 +504,175 @@ int lowbit_lora_accumulate(const void* x, int x_type, int64_t ldx, const int32_t
                            const void* b, const int32_t* ranks, const float* scales, void* y,
                            int y_type, int64_t ldy, void* workspace, size_t workspace_bytes,
                            hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * BETWEEN THE QKV PRODUCT AND THE OUTPUT PRODUCT
+ *
+ * Rotary positions, a cache of keys and values in 4 bits, and attention over
+ * it  [P2 "La memoria es la restriccion vinculante": the cache of 262144
+ * tokens takes a quarter in 4 bits of what it takes in FP16].
+ *
+ * THE CACHE.  Pages of `page` tokens (16, 32, 64, 128 or 256) for `heads` KV
+ * heads of d values (64, 128 or 256); slot s is token s % page of page
+ * s / page.  32 neighbouring values x of a head share two FP16 numbers a, b and
+ * have a code c in 0..15 each, which stands for
+ *     FP16(a * (1 + c / 16) + b)                      (one rounding)
+ * Written by, with FP32 operations, each rounded, and nearest-even throughout:
+ *     x    cut to [-16384, 16384]; NaN and -0 count as 0 (what is held is
+ *          finite)
+ *     a    = FP16((max x - min x) * (16 / 15)),  b = FP16(min x - a)
+ *     c    = the whole number nearest to (x - (a + b)) / (a / 16), ties to
+ *            even, cut to 0..15; 0 where a is 0
+ * A page holds for each head, one after another (5/4 d bytes a token):
+ *     K codes   [page][d / 2]           value 2i in the low half of byte i
+ *     K params  [page][d / 32]{a, b}    FP16
+ *     V codes   [page / 4][d / 2][4]    of tokens 0, 1, 2, 3 of four the bytes
+ *                                       0, 2, 1, 3
+ *     V params  [page / 4][d / 32]{a of four tokens, b of four tokens}
+ * ------------------------------------------------------------------------ */
+
+/* Frequencies of rotary positions as the kernels take them, host only:
+ * pair i of rot / 2 turns by f_i = theta^(-2 i / rot) radians a position,
+ * scaled; turns[i] = f_i / (2 pi) * 2^64 mod 2^64 (a fraction of a turn, so
+ * that position * turns wraps by itself).
+ *   rot       : values of a head that turn, even, 2..1024
+ *   scaling   : lowbit_rope_scaling; factor >= 1 (NTK: rot > 2), trained >= 1
+ *               (YaRN) the length that the frequencies were trained at
+ *   beta_fast, beta_slow : YaRN: pairs that turn more often than beta_fast
+ *               times within `trained` positions stay, those that turn less than
+ *               beta_slow times are divided by factor (usual: 32 and 1)
+ *   turns     : HOST [rot / 2], written; to be copied to the device
+ *   gain      : HOST, written, or NULL: what rotated values are multiplied
+ *               by (YaRN: 0.1 ln(factor) + 1, else 1) */
+int lowbit_rope_turns(int64_t rot, double theta, int scaling, double factor, int64_t trained,
+                      double beta_fast, double beta_slow, uint64_t* turns, double* gain);
+
+/* Rotary positions.  Pair i of a head turns by angle = positions[t] * f_i:
+ *   (x1, x2) -> (x1 c - x2 s, x2 c + x1 s),  c = FP32(gain cos angle), s alike
+ * with FP32 products and sums, each rounded, and one rounding to out_type.
+ *   x    : [m][heads][d], x_type, token stride ldx, head stride ldxh
+ *   out  : the same in out_type, strides ldo and ldoh; may be x itself (same
+ *          type and strides); otherwise the two do not overlap
+ *   rot  : the first rot values of a head turn, the others are copied.
+ *          interleaved 0: pair i is (x[i], x[rot / 2 + i]), else
+ *          (x[2 i], x[2 i + 1])
+ *   positions : [m] int32 (any value);  turns : [rot / 2]
+ * 1 <= m <= 2^22, 1 <= heads <= 65535, 2 <= d <= 1024, rot even, 2..d.  Strides
+ * count elements: heads of a token or tokens of a head do not overlap.  Pointers
+ * need their element's alignment only (turns: 8 bytes). */
+int lowbit_rope(const void* x, int x_type, int64_t ldx, int64_t ldxh, const int32_t* positions,
+                const uint64_t* turns, int64_t m, int64_t heads, int64_t d, int64_t rot,
+                int interleaved, double gain, void* out, int out_type, int64_t ldo, int64_t ldoh,
+                hipStream_t stream);
+
+/* Bytes of a page of the cache; 0 on a bad shape. */
+size_t lowbit_kv_page_bytes(int64_t heads, int64_t d, int64_t page);
+
+/* Writes keys and values into the cache, the keys turned on the way, and
+ * turns the queries beside them, in one launch.
+ *   k, v   : [m][heads][d], type, strides ldk / ldkh and ldv / ldvh (what a
+ *            fused QKV product gave)
+ *   slots  : [m] int32; a token whose slot is outside the cache is not
+ *            written.  The slots of a call differ from each other (the content
+ *            of one that is named twice is not specified)
+ *   pages  : n_pages pages, 16-byte aligned, written at the slots only
+ *   positions, turns, rot, interleaved, gain : as for lowbit_rope, rot a
+ *            multiple of 16; turns NULL: the keys are stored as they come
+ *   q      : [m][hq][d], type, strides ldq / ldqh, or NULL; needs turns.  Every
+ *            row is turned, whatever its slot
+ *   q_out  : [m][hq][d], q_type, strides ldqo / ldqoh; may be q itself
+ * n_pages * page < 2^31, heads and hq <= 1024.  Alignment as for lowbit_rope. */
+int lowbit_kv_store(const void* k, int64_t ldk, int64_t ldkh, const void* v, int64_t ldv,
+                    int64_t ldvh, int type, const int32_t* slots, int64_t m, int64_t heads,
+                    int64_t d, void* pages, int64_t n_pages, int64_t page,
+                    const int32_t* positions, const uint64_t* turns, int64_t rot, int interleaved,
+                    double gain, const void* q, int64_t ldq, int64_t ldqh, int64_t hq,
+                    void* q_out, int q_type, int64_t ldqo, int64_t ldqoh, hipStream_t stream);
+
+/* Reads keys and values back.
+ *   slots  : [m] int32, in any order, also more than once; one outside the
+ *            cache gives zeros
+ *   k, v   : [m][heads][d], type (one rounding more unless FP16), strides ldk /
+ *            ldkh and ldv / ldvh; one of them may be NULL */
+int lowbit_kv_load(const void* pages, int64_t n_pages, int64_t heads, int64_t d, int64_t page,
+                   const int32_t* slots, int64_t m, void* k, int64_t ldk, int64_t ldkh, void* v,
+                   int64_t ldv, int64_t ldvh, int type, hipStream_t stream);
+
+/* Workspace bytes lowbit_attention needs; 0 on a bad shape. */
+size_t lowbit_attention_workspace_bytes(int64_t m, int64_t b, int64_t hq, int64_t heads, int64_t d,
+                                        int64_t max_q);
+
+/* Attention of b sequences over the cache.  Sequence i has lengths[i] tokens
+ * in the cache, its queries' own among them, and its queries are the last of them:
+ * row j of its nq rows sees tokens 0 .. lengths[i] - nq + j.
+ *   out[r][h] = sum_t p_t V[t][h / (hq / heads)] / sum_t p_t,
+ *   p_t = exp(scale * q[r][h] . K[t][h / (hq / heads)])
+ *   lse[r][h] = ln sum_t p_t
+ * A row that sees nothing gives zeros, and -inf.
+ *   q       : [m][hq][d], q_type FP16 or BF16, strides ldq / ldqh
+ *   pages   : n_pages pages as lowbit_kv_store leaves them (a slot below a
+ *             length that was never written: any finite or other value)
+ *   table   : [b] rows of tcap int32 at stride ldt: token t of sequence i is in
+ *             page table[i][t / page].  Tokens of an entry outside
+ *             [0, n_pages) are passed over as if masked
+ *   lengths : [b] int32, cut to [0, tcap * page]
+ *   q_start : [b + 1] int32: the rows of sequence i are q_start[i] ..
+ *             q_start[i + 1] - 1 (none is allowed); rows of no sequence
+ *             are left as they are.  Ascending, and cut to [0, m].  NULL: one
+ *             row each, m = b
+ *   max_q   : the most rows of a sequence (it picks the kernel; more are
+ *             computed too, slower), 1 without q_start
+ *   out     : [m][hq][d], out_type, strides ldo / ldoh
+ *   lse     : [m][hq] FP32, or NULL
+ *   workspace : lowbit_attention_workspace_bytes(m, b, hq, heads, d, max_q)
+ *             bytes, contents ignored on entry
+ * The scores, their maximum and all sums are FP32; p is rounded to FP16 for the
+ * product with V, and the sum that divides is that of the rounded p.  No
+ * atomics; equal inputs give equal bits.
+ * 1 <= m <= 2^22, 1 <= b <= 65535, hq a multiple of heads, hq <= 1024, d 64,
+ * 128 or 256, tcap * page <= 2^30, n_pages * page < 2^31.  Alignment as for
+ * lowbit_rope; pages and workspace 16 bytes.  scale is finite. */
+int lowbit_attention(const void* q, int q_type, int64_t ldq, int64_t ldqh, int64_t m, int64_t hq,
+                     const void* pages, int64_t n_pages, int64_t heads, int64_t d, int64_t page,
+                     const int32_t* table, int64_t tcap, int64_t ldt, const int32_t* lengths,
+                     const int32_t* q_start, int64_t b, int64_t max_q, float scale, void* out,
+                     int out_type, int64_t ldo, int64_t ldoh, float* lse, void* workspace,
+                     size_t workspace_bytes, hipStream_t stream);
+
+/* Workspace bytes lowbit_sample needs for (n, b); 0 on a bad shape. */
+size_t lowbit_sample_workspace_bytes(int64_t n, int64_t b);
+
+/* A token from each row of logits, with the filters of a preset  [P1 "9 Chat"
+ * and "10 Parametros de muestreo": temperature 0.5, top-p 0.85, top-k 20],
+ * from one random number a row.
+ * With w[t] = exp((y[t] - max y) / temperature) and the tokens in the order of
+ * their values, equal ones by number, a token is kept if
+ *   it is among the first top_k                       (0 or less: all), and
+ *   the w of those before it that top-k keeps add up to less than top_p times
+ *   the w of all that top-k keeps                     (1 or more: all), and
+ *   w >= min_p                                        (0 or less: all).
+ * The first token is always kept.  The result is the first kept token, in the
+ * order of the tokens' numbers, at which the running sum of the kept w is over u
+ * times their sum.
+ *   y           : [b] rows of n logits at stride ldy, y_type (read-only): those
+ *                 of lowbit_logits_process, -inf where a token is not allowed
+ *   temperature : [b] FP32 or NULL (1); below 2^-20, or NaN: the token of the
+ *                 largest value, the lowest number among equals
+ *   top_k       : [b] int32 or NULL;  top_p, min_p : [b] FP32 or NULL (NaN: not
+ *                 used; min_p above 1 counts as 1)
+ *   u           : [b] FP32, cut to [0, 1); NaN counts as 0
+ *   idx         : [b] int32 (device, written); -1 if every logit is -inf
+ *   prob        : [b] FP32 or NULL: w at idx over the sum of the kept w
+ *   workspace   : lowbit_sample_workspace_bytes(n, b) bytes, contents ignored
+ *                 on entry
+ * A row that has NaN or +inf: the lowest token of the largest value (NaN
+ * counting as largest), prob 1.  w is kept to 2^-40 relative and, below
+ * 2^(ceil(log2 n) - 62) of the largest, counts as 0.  Equal inputs give equal bits.
+ * 1 <= n <= 2^20, 1 <= b <= 65535.  Alignment: elements; workspace 16 bytes. */
+int lowbit_sample(const void* y, int y_type, int64_t ldy, int64_t n, int64_t b,
+                  const float* temperature, const int32_t* top_k, const float* top_p,
+                  const float* min_p, const float* u, int32_t* idx, float* prob, void* workspace,
+                  size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }
