@@ -60,6 +60,11 @@ __device__ __forceinline__ int64_t uniform64(int64_t v) {
   return (int64_t)((uint64_t)(uint32_t)uniform((int)v) | ((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32));
 }
 
+// What a kernel reads of the call's lists: nothing writes them meanwhile, so
+// they come through the scalar cache
+typedef const __attribute__((address_space(4))) int32_t* list_t;
+__device__ __forceinline__ list_t list_of(const int32_t* p) { return (list_t)(uintptr_t)p; }
+
 // How rows and tokens are cut; made on the host.
 struct Shape {
   int group;        // query heads of a KV head
@@ -89,12 +94,13 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& a, const Shape& s, int i) 
   Seq q;
   int64_t q0 = i, q1 = i + 1;
   if (a.q_start) {
-    q0 = min(max((int64_t)a.q_start[i], (int64_t)0), a.m);
-    q1 = min(max((int64_t)a.q_start[i + 1], q0), a.m);
+    const list_t start = list_of(a.q_start);
+    q0 = min(max((int64_t)start[i], (int64_t)0), a.m);
+    q1 = min(max((int64_t)start[i + 1], q0), a.m);
   }
   q.q0 = (int)q0;
   q.nq = (int)(q1 - q0);
-  q.len = min(max(a.lengths[i], 0), (int)a.tcap << s.page_shift);
+  q.len = min(max(list_of(a.lengths)[i], 0), (int)a.tcap << s.page_shift);
   q.off = q.len - q.nq;
   const int tt = 1 << s.tok_shift;
   q.before = (max(q.off, 0) + tt - 1) >> s.tok_shift;
@@ -104,17 +110,24 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& a, const Shape& s, int i) 
   return q;
 }
 
-// Which work-group does what, found by every work-group for itself.
-struct Walk {
-  int seq;          // of the first unit of this work-group
-  int64_t base;     // first unit of that sequence
-  int64_t total;
+// Even shares of all units: the first `more` work-groups have one unit more.
+// Work-groups without a unit come last.
+struct Shares {
+  int64_t each, more;
+  __device__ __forceinline__ int64_t begin(int64_t i) const { return i * each + min(i, more); }
 };
 
-// Sum of all units, and the sequence that unit `share(total)` is of: the threads
-// take neighbouring sequences each, and add up.
+// Which work-group does what, found by every work-group for itself.
+struct Walk {
+  int seq;          // of the unit that was asked for
+  int64_t base;     // first unit of that sequence
+  Shares share;
+};
+
+// The shares, and the sequence that unit `pick(shares)` is of: the threads take
+// neighbouring sequences each, and add up.
 template <class F>
-__device__ __forceinline__ Walk find_walk(const AttnArgs& a, const Shape& s, int64_t* red, F share) {
+__device__ __forceinline__ Walk find_walk(const AttnArgs& a, const Shape& s, int64_t* red, int64_t wgs, F pick) {
   const int t = threadIdx.x, n = (int)a.b;
   const int chunk = (n + kThreads - 1) / kThreads, lo = min(n, t * chunk), hi = min(n, lo + chunk);
   int64_t mine = 0;
@@ -135,7 +148,12 @@ __device__ __forceinline__ Walk find_walk(const AttnArgs& a, const Shape& s, int
     total += red[w];
   }
   int64_t at = before + sum - mine;
-  const int64_t want = share(total);
+  Shares share;
+  total = uniform64(total);
+  // few units: no 64-bit division (its hundred instructions in a row)
+  share.each = total <= INT32_MAX ? (int64_t)((uint32_t)total / (uint32_t)wgs) : total / wgs;
+  share.more = total - share.each * wgs;
+  const int64_t want = pick(share);
   if (want >= at && want < at + mine) {
     for (int i = lo; i < hi; ++i) {
       const int64_t u = seq_of(a, s, i).units;
@@ -148,10 +166,8 @@ __device__ __forceinline__ Walk find_walk(const AttnArgs& a, const Shape& s, int
     }
   }
   __syncthreads();
-  return {uniform((int)red[4]), uniform64(red[5]), uniform64(total)};
+  return {uniform((int)red[4]), uniform64(red[5]), share};
 }
-
-__device__ __forceinline__ int64_t share_of(int64_t total, int64_t i, int64_t n) { return total * i / n; }
 
 // one item: a tile of a KV head of a sequence
 struct Item {
@@ -178,61 +194,86 @@ __device__ __forceinline__ Item item_of(const Seq& q, const Shape& s, int64_t un
   return it;
 }
 
-// Codes and params of 32 tokens as a lane needs them
+// Codes and params of 32 tokens' keys, and of their values, as a lane needs them
 template <int D>
-struct Raw {
-  static constexpr int kW = D / 32;               // dwords of a lane
-  static constexpr int kP = D / 32 >= 8 ? 2 : 1;  // groups of 32 values that a lane's K falls into
-  uint32_t k[2][kW], kp[2][kP], v[2][kW];
-  uint4 vp[2];
+struct Keys {
+  static constexpr int kP = D / 32 >= 8 ? 2 : 1;  // groups of 32 values that a lane's part falls into
+  uint32_t code[2][D / 32], param[2][kP];
+};
+template <int D>
+struct Values {
+  uint32_t code[2][D / 32], param[2][4];
 };
 
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
 template <int W>
-__device__ __forceinline__ void load_words(uint32_t (&out)[W], const uint8_t* p) {
-  if constexpr (W == 2) {
-    const uint2 x = *reinterpret_cast<const uint2*>(p);
-    out[0] = x.x, out[1] = x.y;
+__device__ __forceinline__ void load_words(uint32_t (&out)[W], __amdgpu_buffer_rsrc_t part, uint32_t lane, int at) {
+  if constexpr (W == 1) {
+    out[0] = __builtin_amdgcn_raw_buffer_load_b32(part, lane, at, 0);
+  } else if constexpr (W == 2) {
+    const u32x2 x = __builtin_amdgcn_raw_buffer_load_b64(part, lane, at, 0);
+    out[0] = x[0], out[1] = x[1];
   } else {
 #pragma unroll
     for (int i = 0; i < W / 4; ++i) {
-      const uint4 x = reinterpret_cast<const uint4*>(p)[i];
-      out[4 * i] = x.x, out[4 * i + 1] = x.y, out[4 * i + 2] = x.z, out[4 * i + 3] = x.w;
+      const u32x4 x = __builtin_amdgcn_raw_buffer_load_b128(part, lane, at + 16 * i, 0);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) out[4 * i + e] = x[e];
     }
   }
 }
 
-// where 16 tokens lie, or that they do not (then somewhere that can be read)
+// Where the two halves of 32 tokens lie: the part of the page that belongs to the
+// head, as a buffer (of no bytes if there is no such page: loads give zeros)
 struct Place {
-  const uint8_t* head;
-  int in;
-  bool there;
+  __amdgpu_buffer_rsrc_t part[2];
+  int in[2];
+  bool there[2];
 };
-__device__ __forceinline__ Place place16(const AttnArgs& a, const Shape& s, const int32_t* table, int len, int t,
-                                         int head, int head_bytes, int64_t page_bytes) {
+__device__ __forceinline__ Place place_of(list_t table, int page_shift, const uint8_t* head, int64_t page_bytes,
+                                          int part_bytes, int pages, int end, int t) {
   Place p;
-  int id = -1;
-  if (t < len) id = table[t >> s.page_shift];
-  id = uniform(id);
-  p.there = id >= 0 && id < a.n_pages;
-  p.head = a.pages + (p.there ? id : 0) * page_bytes + (int64_t)head * head_bytes;
-  p.in = t & ((1 << s.page_shift) - 1);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int u = t + 16 * h;
+    const int id = u < end ? table[u >> page_shift] : -1;
+    p.there[h] = id >= 0 && id < pages;
+    p.part[h] = buffer_rsrc(head + (p.there[h] ? id : 0) * page_bytes, p.there[h] ? part_bytes : 0);
+    p.in[h] = u & ((1 << page_shift) - 1);
+  }
   return p;
 }
 
+// a lane's places in the codes and params of 16 tokens
 template <int D>
-__device__ __forceinline__ void load_raw(Raw<D>& r, int h, const Place& p, const KvHead& lay, int lane) {
-  const int m = lane & 15, g = lane >> 4;
-  load_words(r.k[h], p.head + (p.in + m) * (D / 2) + g * (D / 8));
-  const uint32_t* kp = reinterpret_cast<const uint32_t*>(p.head + lay.k_params()) + (p.in + m) * (D / 32);
-  if constexpr (Raw<D>::kP == 2) {
-    const uint2 x = *reinterpret_cast<const uint2*>(kp + 2 * g);
-    r.kp[h][0] = x.x, r.kp[h][1] = x.y;
-  } else {
-    r.kp[h][0] = kp[D == 64 ? g >> 1 : g];
+struct Lane {
+  uint32_t k, kp, v, vp;
+  __device__ __forceinline__ explicit Lane(int lane) {
+    const int m = lane & 15, g = lane >> 4;
+    k = m * (D / 2) + g * (D / 8);
+    kp = (m * (D / 32) + g * (D / 32) / 4) * 4;
+    v = g * (D * 2) + m * (D / 8);
+    vp = (g * (D / 32) + m * D / 512) * 16;
   }
-  const int quad = (p.in >> 2) + g;
-  load_words(r.v[h], p.head + lay.v_codes() + quad * (D * 2) + m * (D / 8));
-  r.vp[h] = reinterpret_cast<const uint4*>(p.head + lay.v_params())[quad * (D / 32) + m * D / 512];
+};
+
+template <int D>
+__device__ __forceinline__ void load_keys(Keys<D>& r, const Place& p, const KvHead& lay, const Lane<D>& at) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    load_words(r.code[h], p.part[h], at.k, p.in[h] * (D / 2));
+    load_words(r.param[h], p.part[h], at.kp, lay.k_params() + p.in[h] * (D / 8));
+  }
+}
+template <int D>
+__device__ __forceinline__ void load_values(Values<D>& r, const Place& p, const KvHead& lay, const Lane<D>& at) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    load_words(r.code[h], p.part[h], at.v, lay.v_codes() + p.in[h] * (D / 2));
+    load_words(r.param[h], p.part[h], at.vp, lay.v_params() + p.in[h] * (D / 8));
+  }
 }
 
 __device__ __forceinline__ f16x2 splat_lo(uint32_t w) {
@@ -253,41 +294,40 @@ struct State {
   float m[NR];
 };
 
-// `p` of 32 tokens joins the state.  mask (the same in the whole wave): tokens
-// past the row's last one, or past the end, or not there, are passed over.
+// S^T of 32 tokens: two tiles of 16 of them, four to a lane
 template <int D, int NR>
-__device__ __forceinline__ void step(State<D, NR>& st, const Raw<D>& r, const f16x8 (&q)[NR][D / 32],
-                                     const float (&c)[NR], const int (&last)[NR], bool mask, int t0, int len,
-                                     bool there0, bool there1, int lane) {
-  const int g = lane >> 4;
-  f32x4 s[NR][2];
+__device__ __forceinline__ void scores(f32x4 (&s)[NR][2], const Keys<D>& r, const f16x8 (&q)[NR][D / 32],
+                                       uint32_t ones) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int n = 0; n < NR; ++n) s[n][h] = (f32x4){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int w = 0; w < D / 32; ++w) {
-      const uint32_t ab = r.kp[h][Raw<D>::kP == 2 ? w / 4 : 0];
+  for (int w = 0; w < D / 32; ++w) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t ab = r.param[h][Keys<D>::kP == 2 ? w / 4 : 0], x = r.code[h][w];
       const f16x2 a = splat_lo(ab), b = splat_hi(ab);
-      const uint32_t x = r.k[h][w];
-      const f16x8 key = join(fma2(nibbles<0>(x), a, b), fma2(nibbles<1>(x), a, b), fma2(nibbles<2>(x), a, b),
-                             fma2(nibbles<3>(x), a, b));
+      const f16x8 key = join(fma2(nibbles<0>(x, ones), a, b), fma2(nibbles<1>(x, ones), a, b),
+                             fma2(nibbles<2>(x, ones), a, b), fma2(nibbles<3>(x, ones), a, b));
 #pragma unroll
       for (int n = 0; n < NR; ++n) s[n][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(key, q[n][w], s[n][h], 0, 0, 0);
     }
   }
-  f16x8 p[NR];
+}
+
+// p of the 32 tokens in the order of the product with V, and the state's maximum
+// and sum with them
+template <int D, int NR>
+__device__ __forceinline__ void weigh(State<D, NR>& st, f16x8 (&p)[NR], const f32x4 (&s)[NR][2], const float (&c)[NR],
+                                      uint32_t ones) {
+  const f16x2 one = __builtin_bit_cast(f16x2, ones);
 #pragma unroll
   for (int n = 0; n < NR; ++n) {
-    float x[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = s[n][e >> 2][e & 3] * c[n];
-    if (mask) {
-      const int see0 = there0 ? last[n] - (t0 + 4 * g) : -1, see1 = there1 ? last[n] - (t0 + 16 + 4 * g) : -1;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = (e & 3) <= (e < 4 ? see0 : see1) ? x[e] : -INFINITY;
-    }
-    float most = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+    // scaled first, the maximum taken away after: the largest gives exactly 1
+    // however large it is
+    const f32x4 x = s[n][0] * c[n], y = s[n][1] * c[n];
+    const float most = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])));
     if (__builtin_amdgcn_ballot_w64(most > st.m[n] + kRaise) != 0) {
       const float m = fmaxf(st.m[n], max_groups(most));
       const float f = exp2_fast(st.m[n] - m);
@@ -298,38 +338,35 @@ __device__ __forceinline__ void step(State<D, NR>& st, const Raw<D>& r, const f1
     }
     f16x2 pk[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      auto two = __builtin_amdgcn_cvt_pkrtz(exp2_fast(x[2 * e] - st.m[n]), exp2_fast(x[2 * e + 1] - st.m[n]));
-      pk[e] = __builtin_bit_cast(f16x2, two);
+    for (int e = 0; e < 2; ++e) {
+      pk[e] = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_pkrtz(exp2_fast(x[2 * e] - st.m[n]),
+                                                                   exp2_fast(x[2 * e + 1] - st.m[n])));
+      pk[e + 2] = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_pkrtz(exp2_fast(y[2 * e] - st.m[n]),
+                                                                       exp2_fast(y[2 * e + 1] - st.m[n])));
     }
     p[n] = join(pk[0], pk[1], pk[2], pk[3]);
-    const _Float16 one = (_Float16)1.0f;
-    st.l[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16((f16x8){one, one, one, one, one, one, one, one}, p[n], st.l[n], 0, 0,
-                                                     0);
+    st.l[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(join(one, one, one, one), p[n], st.l[n], 0, 0, 0);
   }
+}
+
+// O^T += V^T P^T
+template <int D, int NR>
+__device__ __forceinline__ void gather(State<D, NR>& st, const Values<D>& r, const f16x8 (&p)[NR], uint32_t ones) {
   f16x2 a[2][2], b[2][2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    uint4 w = r.vp[h];
-    if (mask) {
-      // what is not there counts 0 times p = 0, whatever its bits say
-      const int have = (h ? there1 : there0) ? len - (t0 + 16 * h + 4 * g) : 0;
-      const uint32_t m01 = have >= 2 ? 0xFFFFFFFFu : have == 1 ? 0x0000FFFFu : 0u;
-      const uint32_t m23 = have >= 4 ? 0xFFFFFFFFu : have == 3 ? 0x0000FFFFu : 0u;
-      w = make_uint4(w.x & m01, w.y & m23, w.z & m01, w.w & m23);
-    }
-    a[h][0] = __builtin_bit_cast(f16x2, w.x);
-    a[h][1] = __builtin_bit_cast(f16x2, w.y);
-    b[h][0] = __builtin_bit_cast(f16x2, w.z);
-    b[h][1] = __builtin_bit_cast(f16x2, w.w);
+    a[h][0] = __builtin_bit_cast(f16x2, r.param[h][0]);
+    a[h][1] = __builtin_bit_cast(f16x2, r.param[h][1]);
+    b[h][0] = __builtin_bit_cast(f16x2, r.param[h][2]);
+    b[h][1] = __builtin_bit_cast(f16x2, r.param[h][3]);
   }
 #pragma unroll
   for (int e = 0; e < D / 32; ++e) {
-    const uint32_t x = r.v[0][e], y = r.v[1][e];
-    const f16x8 even = join(fma2(nibbles<0>(x), a[0][0], b[0][0]), fma2(nibbles<2>(x), a[0][1], b[0][1]),
-                            fma2(nibbles<0>(y), a[1][0], b[1][0]), fma2(nibbles<2>(y), a[1][1], b[1][1]));
-    const f16x8 odd = join(fma2(nibbles<1>(x), a[0][0], b[0][0]), fma2(nibbles<3>(x), a[0][1], b[0][1]),
-                           fma2(nibbles<1>(y), a[1][0], b[1][0]), fma2(nibbles<3>(y), a[1][1], b[1][1]));
+    const uint32_t x = r.code[0][e], y = r.code[1][e];
+    const f16x8 even = join(fma2(nibbles<0>(x, ones), a[0][0], b[0][0]), fma2(nibbles<2>(x, ones), a[0][1], b[0][1]),
+                            fma2(nibbles<0>(y, ones), a[1][0], b[1][0]), fma2(nibbles<2>(y, ones), a[1][1], b[1][1]));
+    const f16x8 odd = join(fma2(nibbles<1>(x, ones), a[0][0], b[0][0]), fma2(nibbles<3>(x, ones), a[0][1], b[0][1]),
+                           fma2(nibbles<1>(y, ones), a[1][0], b[1][0]), fma2(nibbles<3>(y, ones), a[1][1], b[1][1]));
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
       st.o[n][2 * e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(even, p[n], st.o[n][2 * e], 0, 0, 0);
@@ -343,11 +380,22 @@ __device__ __forceinline__ void step(State<D, NR>& st, const Raw<D>& r, const f1
 template <int D, int ROWS>
 constexpr int kPartFloats = ROWS * (D + 2);
 
-__device__ __forceinline__ void store_out(void* out, int type, int64_t at, float v) {
-  if (type == 1) static_cast<float*>(out)[at] = v;
-  else if (type == 2) static_cast<_Float16*>(out)[at] = (_Float16)v;
-  else static_cast<bf16_t*>(out)[at] = (bf16_t)v;
+// What a work-group that began an item and did not end it leaves for the join:
+// the number of parts (in a list of its own, 0: nothing to join), which of its own
+// two is the first, and where the item's rows go.
+struct alignas(16) Join {
+  int slot;
+  int token, tokens;  // first row of q, and how many there are
+  int head, heads;    // first head, and how many
+  int pad[3];
+};
+// The work-group whose share holds unit `to` - 1, counted from the first
+__device__ __forceinline__ int64_t holder(const Shares& h, int64_t to) {
+  const int64_t longer = h.more * (h.each + 1);  // units of the work-groups that have one more
+  if (to <= longer) return (to - 1) / (h.each + 1);
+  return h.more + (to - 1 - longer) / h.each;
 }
+
 template <int N>
 __device__ __forceinline__ void store_row(void* out, int type, int64_t at, const float (&v)[N]) {
   if (type == 1) {
@@ -365,6 +413,8 @@ __device__ __forceinline__ void store_row(void* out, int type, int64_t at, const
   }
 }
 
+__device__ __forceinline__ float inverse_of(float l) { return l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l; }  // NaN stays
+
 // row `row` of an item: its row of q and its head; false if it has none
 __device__ __forceinline__ bool row_of(const Seq& q, const Item& it, const Shape& s, int row, int* token, int* head) {
   const int t = row / s.part, h = row - t * s.part;
@@ -378,18 +428,23 @@ __device__ __forceinline__ bool row_of(const Seq& q, const Item& it, const Shape
 // SPLIT: the four waves take a unit's tokens in turn for the same rows and are
 // joined through LDS; otherwise each has rows of its own.
 template <int D, int NR, bool SPLIT>
-__global__ __launch_bounds__(kThreads, NR == 1 ? 2 : 1) void attn_kernel(AttnArgs a, Shape s, float* parts) {
+__global__ __launch_bounds__(kThreads, NR == 1 ? 2 : 1) void attn_kernel(AttnArgs a, Shape s, float* parts, int* counts, Join* joins) {
   constexpr int kM = D / 16;
   constexpr int kRows = SPLIT ? 16 * NR : 64 * NR;
   __shared__ int64_t red[6];
   __shared__ f32x4 swap[SPLIT ? 2 * NR * kM * 64 : 1];
   __shared__ float stat[SPLIT ? 4 * 2 * 16 * NR : 1];
   const int64_t wg = blockIdx.x, wgs = gridDim.x;
-  Walk walk = find_walk(a, s, red, [&](int64_t total) { return share_of(total, wg, wgs); });
-  const int64_t end = share_of(walk.total, wg + 1, wgs);
-  int64_t at = share_of(walk.total, wg, wgs);
-  if (at >= end) return;
+  const Walk walk = find_walk(a, s, red, wgs, [&](const Shares& h) { return h.begin(wg); });
+  const int64_t end = walk.share.begin(wg + 1);
+  int64_t at = walk.share.begin(wg);
+  if (at >= end) {
+    if (threadIdx.x == 0) counts[wg] = 0;
+    return;
+  }
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), g = lane >> 4;
+  const Lane<D> place(lane);
+  const uint32_t ones = ones_of();
   const KvHead lay(1 << s.page_shift, D);
   const int64_t page_bytes = a.heads * lay.bytes();
   const int unit_tokens_shift = s.unit_shift + s.tok_shift;
@@ -398,15 +453,41 @@ __global__ __launch_bounds__(kThreads, NR == 1 ? 2 : 1) void attn_kernel(AttnArg
   bool first = true;
   while (at < end) {
     Seq q = seq_of(a, s, i);
+    q.q0 = uniform(q.q0);
+    q.nq = uniform(q.nq);
+    q.off = uniform(q.off);
+    q.len = uniform(q.len);
     if (at >= base + q.units) {
       base += q.units;
       ++i;
       continue;
     }
-    const Item it = item_of(q, s, at - base);
+    Item it = item_of(q, s, at - base);
+    // one item for the whole work-group: its numbers belong into scalar registers
+    it.head = uniform(it.head);
+    it.part = uniform(it.part);
+    it.tile = uniform(it.tile);
+    const int seq = uniform(i);
     const int u0 = uniform((int)(at - base - it.first)), u1 = uniform((int)min(end - base - it.first, it.units));
+    // the tokens that any of its rows sees, and those that all of them see (rows
+    // that are not there may count what they like)
+    const int tile_end = uniform(min(q.len, q.off + ((it.tile + 1) << s.tok_shift)));
+    const int open = uniform(min(q.len, q.off + (it.tile << s.tok_shift) + 1));
+    const list_t table = list_of(a.table + (int64_t)seq * a.ldt);
+    const uint8_t* head_base = a.pages + (int64_t)it.head * lay.bytes();
+    const int t_end = uniform((int)min((int64_t)tile_end, (int64_t)u1 << unit_tokens_shift));
+    constexpr int kStep = SPLIT ? 128 : 32;
+    int t = uniform((u0 << unit_tokens_shift) + (SPLIT ? wave * 32 : 0));
+    auto find = [&](int from) __attribute__((always_inline)) {
+      return place_of(table, s.page_shift, head_base, page_bytes, lay.bytes(), (int)a.n_pages, t_end, from);
+    };
+    // keys and values are on their way before q is; page numbers go a step ahead
+    Place now = find(t), then = find(t + kStep);
+    Keys<D> keys;
+    Values<D> values;
+    load_keys<D>(keys, now, lay, place);
+    load_values<D>(values, now, lay, place);
     // its rows
-    const int tile_end = uniform(min(q.len, q.off + ((it.tile + 1) << s.tok_shift)));  // tokens that any of them sees
     f16x8 qf[NR][D / 32];
     float c[NR];
     int last[NR];
@@ -422,7 +503,10 @@ __global__ __launch_bounds__(kThreads, NR == 1 ? 2 : 1) void attn_kernel(AttnArg
 #pragma unroll
       for (int j = 0; j < D / 8; ++j) w[j] = 0;
       if (have) __builtin_memcpy(w, static_cast<const uint16_t*>(a.q) + from, sizeof(w));
-      c[n] = a.scale * 1.44269504088896340736f;
+      const uint32_t sign = a.scale < 0.0f ? 0x80008000u : 0u;  // a negative scale turns q around
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j) w[j] ^= sign;
+      c[n] = fabsf(a.scale) * 1.44269504088896340736f;
       if (a.q_type == 3) {
         // BF16: times the power of two that puts the row's largest near 2^14
         uint32_t big = 0;
@@ -439,6 +523,7 @@ __global__ __launch_bounds__(kThreads, NR == 1 ? 2 : 1) void attn_kernel(AttnArg
           w[j] = __builtin_bit_cast(uint32_t, (f16x2){(_Float16)lo, (_Float16)hi});
         }
       }
+      c[n] = fmaxf(c[n], 1e-37f);  // never 0: a hidden score is -inf times this
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) {
         const f16x2 x = __builtin_bit_cast(f16x2, w[4 * j]), y = __builtin_bit_cast(f16x2, w[4 * j + 1]),
@@ -450,32 +535,42 @@ __global__ __launch_bounds__(kThreads, NR == 1 ? 2 : 1) void attn_kernel(AttnArg
 #pragma unroll
       for (int j = 0; j < kM; ++j) st.o[n][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
     }
-    // the token up to which every row that there is sees everything; rows that
-    // are not there may count what they like
-    const int open = uniform(min(q.len, q.off + (it.tile << s.tok_shift) + 1));
-    const int32_t* table = a.table + (int64_t)i * a.ldt;
-    const int t_end = (int)min((int64_t)tile_end, (int64_t)u1 << unit_tokens_shift);
-    constexpr int kStep = SPLIT ? 128 : 32;
-    int t = (u0 << unit_tokens_shift) + (SPLIT ? wave * 32 : 0);
-    Raw<D> cur, next;
-    bool c0 = false, c1 = false, n0 = false, n1 = false;
-    auto fetch = [&](Raw<D>& r, int from, bool& h0, bool& h1) __attribute__((always_inline)) {
-      const Place p0 = place16(a, s, table, q.len, from, it.head, lay.bytes(), page_bytes);
-      const Place p1 = place16(a, s, table, q.len, from + 16, it.head, lay.bytes(), page_bytes);
-      h0 = p0.there;
-      h1 = p1.there;
-      load_raw(r, 0, p0, lay, lane);
-      load_raw(r, 1, p1, lay, lane);
-    };
-    if (t < t_end) fetch(cur, t, c0, c1);
-    while (t < t_end) {
-      const int then = t + kStep;
-      if (then < t_end) fetch(next, then, n0, n1);
-      step<D, NR>(st, cur, qf, c, last, t + 32 > open || !c0 || !c1, t, q.len, c0, c1, lane);
-      cur = next;
-      c0 = n0;
-      c1 = n1;
-      t = then;
+    // (a step past the last one loads nothing: there is no page for it)
+    for (int steps = uniform(max(0, (t_end - t + kStep - 1) / kStep)); steps > 0; --steps) {
+      f32x4 sc[NR][2];
+      f16x8 p[NR];
+      scores<D, NR>(sc, keys, qf, ones);
+      __builtin_amdgcn_sched_barrier(0);
+      load_keys<D>(keys, then, lay, place);
+      const bool there = now.there[0] && now.there[1];
+      if (t + 32 > open || !there) {
+        // tokens past the row's last one or past the end, or of no page: a score of
+        // -inf, and where nothing may be, zeros for the values, whatever the bits say
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int first = t + 16 * h + 4 * g;
+#pragma unroll
+          for (int n = 0; n < NR; ++n) {
+            const int sees = now.there[h] ? last[n] - first : -1;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[n][h][e] = e <= sees ? sc[n][h][e] : -INFINITY;
+          }
+          const int have = now.there[h] ? q.len - first : 0;
+          const uint32_t m01 = have >= 2 ? 0xFFFFFFFFu : have == 1 ? 0x0000FFFFu : 0u;
+          const uint32_t m23 = have >= 4 ? 0xFFFFFFFFu : have == 3 ? 0x0000FFFFu : 0u;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) values.param[h][e] &= e & 1 ? m23 : m01;
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      weigh<D, NR>(st, p, sc, c, ones);
+      __builtin_amdgcn_sched_barrier(0);
+      gather<D, NR>(st, values, p, ones);
+      __builtin_amdgcn_sched_barrier(0);
+      load_values<D>(values, then, lay, place);
+      t += kStep;
+      now = then;
+      then = find(t + kStep);
     }
     if constexpr (SPLIT) {
       // one maximum for the four waves, then their sums
@@ -531,7 +626,7 @@ __global__ __launch_bounds__(kThreads, NR == 1 ? 2 : 1) void attn_kernel(AttnArg
         for (int n = 0; n < NR; ++n) {
           int token, head;
           if (!row_of(q, it, s, row0 + n * 16 + (lane & 15), &token, &head)) continue;
-          const float l = st.l[n][0], f = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;  // NaN stays NaN
+          const float l = st.l[n][0], f = inverse_of(l);
           const int64_t to = token * a.ldo + head * a.ldoh + g * (D / 4);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -551,76 +646,219 @@ __global__ __launch_bounds__(kThreads, NR == 1 ? 2 : 1) void attn_kernel(AttnArg
           for (int j = 0; j < kM; ++j)
             reinterpret_cast<f32x4*>(part)[((row0 / 16 + n) * kM + j) * 64 + lane] = st.o[n][j];
           if (g == 0) {
-            part[kRows * D + row0 + n * 16 + lane] = st.m[n];
-            part[kRows * D + kRows + row0 + n * 16 + lane] = st.l[n][0];
+            reinterpret_cast<float2*>(part + kRows * D)[row0 + n * 16 + lane] = make_float2(st.m[n], st.l[n][0]);
           }
         }
       }
+    }
+    if (threadIdx.x == 0 && base + it.first + u1 == end) {  // its last item
+      const bool more = u0 == 0 && u1 < it.units;
+      counts[wg] = more ? (int)(holder(walk.share, base + it.first + it.units) - wg) + 1 : 0;
+      Join j = {};
+      j.slot = first ? 0 : 1;
+      j.token = q.q0 + (it.tile << s.tok_shift);
+      j.tokens = min(1 << s.tok_shift, q.nq - (it.tile << s.tok_shift));
+      j.head = it.head * s.group + it.part * s.part;
+      j.heads = min(s.part, s.group - it.part * s.part);
+      joins[wg] = j;
     }
     first = false;
     at = base + it.first + u1;
   }
 }
 
-// Joins the parts of the item that work-group blockIdx.x began and did not end.
-// blockIdx.y: 16 rows of it.
-template <int D, int ROWS>
-__global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, Shape s, const float* parts, int wgs) {
-  constexpr int kM = D / 16;
-  __shared__ int64_t red[6];
-  __shared__ float rows[16][D + 4];
-  const int64_t wg = blockIdx.x;
-  // the last unit of work-group wg is of the item
-  const Walk walk = find_walk(a, s, red, [&](int64_t total) { return share_of(total, wg + 1, wgs) - 1; });
-  const int64_t begin = share_of(walk.total, wg, wgs), end = share_of(walk.total, wg + 1, wgs);
-  if (begin >= end) return;
-  const Seq q = seq_of(a, s, walk.seq);
-  const Item it = item_of(q, s, end - 1 - walk.base);
-  const int64_t from = walk.base + it.first, to = from + it.units;
-  if (from < begin || to <= end) return;  // begun before, or ended here
-  const int tile = (int)blockIdx.y;
-  const float* own = parts + (wg * 2 + (from > begin ? 1 : 0)) * kPartFloats<D, ROWS>;
-  const int n = threadIdx.x & 15;
-  const float* stats = own + ROWS * D + tile * 16 + n;
-  // the parts that follow are the first ones of their work-groups; those without
-  // units are passed over
-  float m = stats[0];
-  int64_t w_end = wg + 1;
-  while (w_end < wgs && share_of(walk.total, w_end, wgs) < to) ++w_end;
-  for (int64_t w = wg + 1; w < w_end; ++w)
-    if (share_of(walk.total, w + 1, wgs) > share_of(walk.total, w, wgs))
-      m = fmaxf(m, parts[w * 2 * kPartFloats<D, ROWS> + ROWS * D + tile * 16 + n]);
-  f32x4 o[(kM + 3) / 4];
-  float l = 0.0f;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-  for (int j = 0; j < (kM + 3) / 4; ++j) o[j] = (f32x4){0.f, 0.f, 0.f, 0.f};
-  for (int64_t w = wg; w < w_end; ++w) {
-    const float* p = w == wg ? own : parts + w * 2 * kPartFloats<D, ROWS>;
-    if (w != wg && share_of(walk.total, w + 1, wgs) == share_of(walk.total, w, wgs)) continue;
-    const float f = exp2_fast(p[ROWS * D + tile * 16 + n] - m);
-    l += p[ROWS * D + ROWS + tile * 16 + n] * f;
-#pragma unroll
-    for (int j = 0; j < kM / 4; ++j)
-      o[j] += reinterpret_cast<const f32x4*>(p)[(tile * kM + wave + 4 * j) * 64 + lane] * f;
+constexpr int kMostParts = 512;  // work-groups of the first launch
+
+// The work-group that began the `nth` item whose parts are to be joined, and how
+// many they are; {.., 0} if there are not so many.  Every thread of a
+// work-group of at least 256 calls it.
+struct Owner {
+  int wg, parts;
+};
+__device__ __forceinline__ Owner find_owner(const int* counts, int wgs, int nth, int* lds) {
+  // lds: [0..7] owners of a wave's work-groups, [8] and [9] the result
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  int c[2] = {0, 0};
+  if (t < 256) {
+    c[0] = counts[t];
+    if (wgs > 256) c[1] = counts[t + 256];
   }
-  const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
-#pragma unroll
-  for (int j = 0; j < kM / 4; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) rows[n][(lane >> 4) * (D / 4) + e * kM + wave + 4 * j] = o[j][e] * inv;
+  if (t == 0) lds[9] = 0;
+  const uint64_t b0 = __builtin_amdgcn_ballot_w64(c[0] != 0), b1 = __builtin_amdgcn_ballot_w64(c[1] != 0);
+  if (lane == 0 && wave < 4) {
+    lds[wave] = __popcll(b0);
+    lds[wave + 4] = __popcll(b1);
+  }
   __syncthreads();
-  for (int r = wave; r < 16; r += 4) {
-    int token, head;
-    if (!row_of(q, it, s, tile * 16 + r, &token, &head)) continue;
-    for (int d = lane; d < D; d += 64)
-      store_out(a.out, a.out_type, token * a.ldo + head * a.ldoh + d, rows[r][d]);
+  if (wave < 4) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      int before = 0;
+      for (int w = 0; w < h * 4 + wave; ++w) before += lds[w];
+      const uint64_t b = h ? b1 : b0;
+      if (c[h] != 0 && before + __popcll(b & (((uint64_t)1 << lane) - 1)) == nth) {
+        lds[8] = h * 256 + t;
+        lds[9] = c[h];
+      }
+    }
   }
-  if (a.lse && threadIdx.x < 16) {
-    int token, head;
-    if (row_of(q, it, s, tile * 16 + n, &token, &head))
-      a.lse[token * a.hq + head] = l == 0.0f ? -INFINITY : 0.69314718055994530942f * (m + __log2f(l));
+  __syncthreads();
+  return {uniform(lds[8]), uniform(lds[9])};
+}
+
+// Joins the parts of item blockIdx.x of those that are to be joined, of a kernel
+// whose waves split the tokens.  blockIdx.y: 16 rows of it and kJ of the head's
+// tiles.  Eight waves take the parts in turn; all that is loaded first goes out
+// at once.
+constexpr int kJoinThreads = 512, kJoinWaves = kJoinThreads / 64, kJ = 2;
+template <int D, int ROWS>
+__global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int part, const float* parts,
+                                                                 const int* counts, const Join* joins, int wgs) {
+  constexpr int kM = D / 16, kY = kM / kJ;
+  __shared__ float weight[kMostParts][16];
+  __shared__ f32x4 swap[kJoinWaves - 1][kJ * 64];
+  __shared__ float most8[kJoinWaves][16], sum8[kJoinWaves][16];
+  __shared__ int lds[10];
+  const Owner own = find_owner(counts, wgs, (int)blockIdx.x, lds);
+  if (own.parts == 0) return;
+  const int count = own.parts;
+  const int tile = (int)blockIdx.y / kY, column = ((int)blockIdx.y % kY) * kJ;
+  const int t = threadIdx.x, lane = t & 63, wave = uniform(t >> 6), n = lane & 15;
+  const Join* jp = joins + own.wg;
+  const int slot = uniform(jp->slot), tokens = uniform(jp->tokens), heads = uniform(jp->heads);
+  if (tile * 16 / part >= tokens) return;  // no row of the tile is there
+  // a part's floats; those that follow the first are the first ones of their work-groups
+  auto at = [&](int k) {
+    return parts + ((int64_t)(own.wg + k) * 2 + (k == 0 ? slot : 0)) * kPartFloats<D, ROWS>;
+  };
+  const int row = tile * 16 + n;
+  constexpr int kAhead = 8, kRound = kJoinThreads / 16;
+  f32x4 x[kAhead][kJ];
+  auto fetch = [&](int k0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) {
+      const int k = k0 + e * kJoinWaves;
+      if (k < count) {
+#pragma unroll
+        for (int c = 0; c < kJ; ++c)
+          x[e][c] = reinterpret_cast<const f32x4*>(at(k))[(tile * kM + column + c) * 64 + lane];
+      }
+    }
+  };
+  fetch(wave);
+  float2 ml[kMostParts / kRound];
+#pragma unroll
+  for (int e = 0; e < kMostParts / kRound; ++e) {
+    ml[e] = make_float2(kEmpty, 0.0f);
+    const int k = (t >> 4) + e * kRound;
+    if (e * kRound < count && k < count) ml[e] = reinterpret_cast<const float2*>(at(k) + ROWS * D)[row];
   }
+  float m = kEmpty;
+#pragma unroll
+  for (int e = 0; e < kMostParts / kRound; ++e) m = fmaxf(m, ml[e].x);
+  m = max_groups(m);
+  if (lane < 16) most8[wave][n] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinWaves; ++w) m = fmaxf(m, most8[w][n]);
+  float l = 0.0f;
+#pragma unroll
+  for (int e = 0; e < kMostParts / kRound; ++e) {
+    if (e * kRound < count) {
+      const float g = exp2_fast(ml[e].x - m);
+      weight[(t >> 4) + e * kRound][n] = g;
+      l += g * ml[e].y;
+    }
+  }
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+  if (lane < 16) sum8[wave][n] = l;
+  __syncthreads();
+  f32x4 o[kJ];
+#pragma unroll
+  for (int c = 0; c < kJ; ++c) o[c] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  for (int k0 = wave; k0 < count; k0 += kJoinWaves * kAhead) {
+    if (k0 != wave) fetch(k0);
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) {
+      const int k = k0 + e * kJoinWaves;
+      if (k < count) {
+        const float g = weight[k][n];
+#pragma unroll
+        for (int c = 0; c < kJ; ++c) o[c] += x[e][c] * g;
+      }
+    }
+  }
+  if (wave > 0)
+#pragma unroll
+    for (int c = 0; c < kJ; ++c) swap[wave - 1][c * 64 + lane] = o[c];
+  __syncthreads();
+  if (wave > 0) return;
+  l = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kJoinWaves; ++w) l += sum8[w][n];
+#pragma unroll
+  for (int w = 0; w < kJoinWaves - 1; ++w)
+#pragma unroll
+    for (int c = 0; c < kJ; ++c) o[c] += swap[w][c * 64 + lane];
+  const int tok = row / part, h = row - tok * part;
+  if (tok >= tokens || h >= heads) return;
+  const float inv = inverse_of(l);
+  const int token = jp->token + tok, head = jp->head + h;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float v[kJ];
+#pragma unroll
+    for (int c = 0; c < kJ; ++c) v[c] = o[c][e] * inv;
+    store_row(a.out, a.out_type, token * a.ldo + head * a.ldoh + (lane >> 4) * (D / 4) + e * kM + column, v);
+  }
+  if (a.lse && column == 0 && lane < 16)
+    a.lse[token * a.hq + head] = l == 0.0f ? -INFINITY : 0.69314718055994530942f * (m + __log2f(l));
+}
+
+// The same for a kernel whose waves have rows of their own: items have many rows
+// and few parts, so a wave takes 16 rows and walks their parts.
+template <int D, int ROWS>
+__global__ __launch_bounds__(kThreads) void attn_join_rows_kernel(AttnArgs a, int part, const float* parts,
+                                                                  const int* counts, const Join* joins, int wgs) {
+  constexpr int kM = D / 16;
+  __shared__ int lds[10];
+  const Owner own = find_owner(counts, wgs, (int)blockIdx.x, lds);
+  if (own.parts == 0) return;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 15;
+  const int tile = (int)blockIdx.y * 4 + wave, row = tile * 16 + n;
+  const Join* jp = joins + own.wg;
+  const int slot = uniform(jp->slot), tokens = uniform(jp->tokens), heads = uniform(jp->heads);
+  if (tile * 16 / part >= tokens) return;  // no row of the tile is there
+  float m = kEmpty, l = 0.0f;
+  f32x4 o[kM];
+#pragma unroll
+  for (int c = 0; c < kM; ++c) o[c] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  for (int k = 0; k < own.parts; ++k) {
+    const float* p = parts + ((int64_t)(own.wg + k) * 2 + (k == 0 ? slot : 0)) * kPartFloats<D, ROWS>;
+    const float2 ml = reinterpret_cast<const float2*>(p + ROWS * D)[row];
+    f32x4 x[kM];
+#pragma unroll
+    for (int c = 0; c < kM; ++c) x[c] = reinterpret_cast<const f32x4*>(p)[(tile * kM + c) * 64 + lane];
+    const float most = fmaxf(m, ml.x), f = exp2_fast(m - most), g = exp2_fast(ml.x - most);
+    m = most;
+    l = l * f + ml.y * g;
+#pragma unroll
+    for (int c = 0; c < kM; ++c) o[c] = o[c] * f + x[c] * g;
+  }
+  const int tok = row / part, h = row - tok * part;
+  if (tok >= tokens || h >= heads) return;
+  const float inv = inverse_of(l);
+  const int token = jp->token + tok, head = jp->head + h;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float v[kM];
+#pragma unroll
+    for (int c = 0; c < kM; ++c) v[c] = o[c][e] * inv;
+    store_row(a.out, a.out_type, token * a.ldo + head * a.ldoh + (lane >> 4) * (D / 4) + e * kM, v);
+  }
+  if (a.lse && lane < 16)
+    a.lse[token * a.hq + head] = l == 0.0f ? -INFINITY : 0.69314718055994530942f * (m + __log2f(l));
 }
 
 int log2_of(int64_t v) {
@@ -650,21 +888,32 @@ Variant variant_of(int64_t group, int64_t d, int64_t max_q) {
 }
 
 template <int D, int NR, bool SPLIT>
-void launch_one(const AttnArgs& a, const Shape& s, const Variant& v, float* parts, hipStream_t st) {
-  attn_kernel<D, NR, SPLIT><<<v.wgs, kThreads, 0, st>>>(a, s, parts);
+void launch_one(const AttnArgs& a, const Shape& s, const Variant& v, void* ws, hipStream_t st) {
   constexpr int kRows = SPLIT ? 16 * NR : 64 * NR;
-  attn_join_kernel<D, kRows><<<dim3(v.wgs, kRows / 16), kThreads, 0, st>>>(a, s, parts, v.wgs);
+  int* counts = static_cast<int*>(ws);
+  Join* joins = reinterpret_cast<Join*>(counts + v.wgs);
+  float* parts = reinterpret_cast<float*>(joins + v.wgs);
+  attn_kernel<D, NR, SPLIT><<<v.wgs, kThreads, 0, st>>>(a, s, parts, counts, joins);
+  // no more items than this, and of a work-group one at most
+  const int64_t items = min(a.m, a.b + (a.m >> s.tok_shift)) * a.heads * s.parts;
+  const unsigned most = (unsigned)min((int64_t)v.wgs, items);
+  if constexpr (SPLIT)
+    attn_join_kernel<D, kRows><<<dim3(most, kRows / 16 * (D / 16 / kJ)), kJoinThreads, 0, st>>>(
+        a, s.part, parts, counts, joins, v.wgs);
+  else
+    attn_join_rows_kernel<D, kRows><<<dim3(most, kRows / 64), kThreads, 0, st>>>(a, s.part, parts, counts, joins,
+                                                                                v.wgs);
 }
 
 template <int D>
-void launch_d(const AttnArgs& a, const Shape& s, const Variant& v, float* parts, hipStream_t st) {
-  if (v.split && v.nr == 1) launch_one<D, 1, true>(a, s, v, parts, st);
-  else if (v.split && v.nr == 2) launch_one<D, 2, true>(a, s, v, parts, st);
+void launch_d(const AttnArgs& a, const Shape& s, const Variant& v, void* ws, hipStream_t st) {
+  if (v.split && v.nr == 1) launch_one<D, 1, true>(a, s, v, ws, st);
+  else if (v.split && v.nr == 2) launch_one<D, 2, true>(a, s, v, ws, st);
   if constexpr (D == 256) {
-    if (!v.split) launch_one<D, 2, false>(a, s, v, parts, st);
+    if (!v.split) launch_one<D, 2, false>(a, s, v, ws, st);
   } else {
-    if (v.split && v.nr == 4) launch_one<D, 4, true>(a, s, v, parts, st);
-    else if (!v.split) launch_one<D, 4, false>(a, s, v, parts, st);
+    if (v.split && v.nr == 4) launch_one<D, 4, true>(a, s, v, ws, st);
+    else if (!v.split) launch_one<D, 4, false>(a, s, v, ws, st);
   }
 }
 
@@ -672,7 +921,7 @@ void launch_d(const AttnArgs& a, const Shape& s, const Variant& v, float* parts,
 
 size_t attention_workspace_bytes(int64_t hq, int64_t heads, int64_t d, int64_t max_q) {
   const Variant v = variant_of(hq / heads, d, max_q);
-  return (size_t)v.wgs * 2 * v.rows * (size_t)(d + 2) * sizeof(float);
+  return (size_t)v.wgs * (sizeof(int) + sizeof(Join) + 2 * v.rows * (size_t)(d + 2) * sizeof(float));
 }
 
 hipError_t launch_attention(const AttnArgs& a, void* ws, hipStream_t st) {
@@ -686,9 +935,9 @@ hipError_t launch_attention(const AttnArgs& a, void* ws, hipStream_t st) {
   // a unit: 128 tokens, or the tile's tokens where they are more
   s.unit_shift = max(0, 7 - s.tok_shift);
   s.page_shift = log2_of(a.page);
-  if (a.d == 64) launch_d<64>(a, s, v, static_cast<float*>(ws), st);
-  else if (a.d == 128) launch_d<128>(a, s, v, static_cast<float*>(ws), st);
-  else launch_d<256>(a, s, v, static_cast<float*>(ws), st);
+  if (a.d == 64) launch_d<64>(a, s, v, ws, st);
+  else if (a.d == 128) launch_d<128>(a, s, v, ws, st);
+  else launch_d<256>(a, s, v, ws, st);
   return hipGetLastError();
 }
 

@@ -392,8 +392,9 @@ __global__ __launch_bounds__(kThreads) void kv_store_kernel(KvStoreArgs a, KvGri
 __device__ __forceinline__ void values8(uint32_t w, uint32_t params, float (&v)[8]) {
   const f16x2 ab = __builtin_bit_cast(f16x2, params);
   const f16x2 a = {ab.x, ab.x}, b = {ab.y, ab.y};
-  const f16x2 x[4] = {fma2(nibbles<0>(w), a, b), fma2(nibbles<1>(w), a, b), fma2(nibbles<2>(w), a, b),
-                      fma2(nibbles<3>(w), a, b)};
+  const uint32_t ones = ones_of();
+  const f16x2 x[4] = {fma2(nibbles<0>(w, ones), a, b), fma2(nibbles<1>(w, ones), a, b),
+                      fma2(nibbles<2>(w, ones), a, b), fma2(nibbles<3>(w, ones), a, b)};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     v[j] = (float)x[j].x;

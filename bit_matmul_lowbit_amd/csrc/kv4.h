@@ -26,12 +26,19 @@ struct KvHead {
 __device__ __forceinline__ int v_byte(int t) { return ((t & 1) << 1) | (t >> 1); }
 
 // Nibbles N and N + 4 of w as the FP16 pair 1 + code / 16: the code is put at
-// the top of the mantissa of 1.0 (no conversion and no subtraction).
+// the top of the mantissa of 1.0 (no conversion and no subtraction).  `ones` is a
+// pair of 1.0 in a register (ones_of), which makes mask and insertion one
+// instruction: it takes one constant from outside the vector registers, not two.
+__device__ __forceinline__ uint32_t ones_of() {
+  uint32_t ones;
+  __asm__("v_mov_b32 %0, 0x3c003c00" : "=v"(ones));
+  return ones;
+}
 template <int N>
-__device__ __forceinline__ f16x2 nibbles(uint32_t w) {
+__device__ __forceinline__ f16x2 nibbles(uint32_t w, uint32_t ones) {
   constexpr int kShift = 6 - 4 * N;  // to bits 6..9 of both halves
   const uint32_t s = kShift >= 0 ? w << (kShift & 31) : w >> (-kShift & 31);
-  return __builtin_bit_cast(f16x2, (s & 0x03C003C0u) | 0x3C003C00u);
+  return __builtin_bit_cast(f16x2, (s & 0x03C003C0u) | ones);
 }
 
 __device__ __forceinline__ f16x2 fma2(f16x2 x, f16x2 a, f16x2 b) { return __builtin_elementwise_fma(x, a, b); }
