@@ -290,43 +290,55 @@ __device__ __forceinline__ f16x8 join(f16x2 a, f16x2 b, f16x2 c, f16x2 d) {
 template <int D, int NR>
 struct State {
   static constexpr int kM = D / 16;
-  f32x4 o[NR][kM], l[NR];  // l: the sum of p, the same in all four
-  float m[NR];
+  f32x4 o[NR][kM];
+  float l[NR], m[NR];  // l: of the tokens that this lane had
 };
 
-// S^T of 32 tokens: two tiles of 16 of them, four to a lane
+// Q of a wave's rows as the B operand.  Where it would take more than 32
+// registers it stays in LDS (which leaves o in the vector registers and two waves
+// a SIMD: o in accumulation registers was copied back and forth every step).
 template <int D, int NR>
-__device__ __forceinline__ void scores(f32x4 (&s)[NR][2], const Keys<D>& r, const f16x8 (&q)[NR][D / 32],
-                                       uint32_t ones) {
+constexpr bool kQInLds = NR * D > 256;
+
+// S^T of 32 tokens: two tiles of 16 of them, four to a lane.  q(n, w): the
+// operand of tile n's rows, step w
+template <int D, int NR, class Q>
+__device__ __forceinline__ void scores(f32x4 (&s)[NR][2], const Keys<D>& r, Q q, uint32_t ones) {
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int n = 0; n < NR; ++n) s[n][h] = (f32x4){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int w = 0; w < D / 32; ++w) {
+    if (kQInLds<D, NR>) __builtin_amdgcn_sched_barrier(0);  // registers: one step's keys at a time
+    f16x8 key[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const uint32_t ab = r.param[h][Keys<D>::kP == 2 ? w / 4 : 0], x = r.code[h][w];
       const f16x2 a = splat_lo(ab), b = splat_hi(ab);
-      const f16x8 key = join(fma2(nibbles<0>(x, ones), a, b), fma2(nibbles<1>(x, ones), a, b),
-                             fma2(nibbles<2>(x, ones), a, b), fma2(nibbles<3>(x, ones), a, b));
+      key[h] = join(fma2(nibbles<0>(x, ones), a, b), fma2(nibbles<1>(x, ones), a, b),
+                    fma2(nibbles<2>(x, ones), a, b), fma2(nibbles<3>(x, ones), a, b));
+    }
 #pragma unroll
-      for (int n = 0; n < NR; ++n) s[n][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(key, q[n][w], s[n][h], 0, 0, 0);
+    for (int n = 0; n < NR; ++n) {
+      const f16x8 qn = q(n, w);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) s[n][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(key[h], qn, s[n][h], 0, 0, 0);
     }
   }
 }
 
 // p of the 32 tokens in the order of the product with V, and the state's maximum
 // and sum with them
-template <int D, int NR>
-__device__ __forceinline__ void weigh(State<D, NR>& st, f16x8 (&p)[NR], const f32x4 (&s)[NR][2], const float (&c)[NR],
-                                      uint32_t ones) {
+template <int D, int NR, class C>
+__device__ __forceinline__ void weigh(State<D, NR>& st, f16x8 (&p)[NR], const f32x4 (&s)[NR][2], C c, uint32_t ones) {
   const f16x2 one = __builtin_bit_cast(f16x2, ones);
 #pragma unroll
   for (int n = 0; n < NR; ++n) {
     // scaled first, the maximum taken away after: the largest gives exactly 1
     // however large it is
-    const f32x4 x = s[n][0] * c[n], y = s[n][1] * c[n];
+    const float f0 = c(n);
+    const f32x4 x = s[n][0] * f0, y = s[n][1] * f0;
     const float most = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])));
     if (__builtin_amdgcn_ballot_w64(most > st.m[n] + kRaise) != 0) {
       const float m = fmaxf(st.m[n], max_groups(most));
@@ -345,7 +357,9 @@ __device__ __forceinline__ void weigh(State<D, NR>& st, f16x8 (&p)[NR], const f3
                                                                        exp2_fast(y[2 * e + 1] - st.m[n])));
     }
     p[n] = join(pk[0], pk[1], pk[2], pk[3]);
-    st.l[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(join(one, one, one, one), p[n], st.l[n], 0, 0, 0);
+    // the sum of the rounded p, as the product with V takes them
+#pragma unroll
+    for (int e = 0; e < 4; ++e) st.l[n] = __builtin_amdgcn_fdot2(pk[e], one, st.l[n], false);
   }
 }
 
@@ -362,6 +376,7 @@ __device__ __forceinline__ void gather(State<D, NR>& st, const Values<D>& r, con
   }
 #pragma unroll
   for (int e = 0; e < D / 32; ++e) {
+    if (kQInLds<D, NR>) __builtin_amdgcn_sched_barrier(0);
     const uint32_t x = r.code[0][e], y = r.code[1][e];
     const f16x8 even = join(fma2(nibbles<0>(x, ones), a[0][0], b[0][0]), fma2(nibbles<2>(x, ones), a[0][1], b[0][1]),
                             fma2(nibbles<0>(y, ones), a[1][0], b[1][0]), fma2(nibbles<2>(y, ones), a[1][1], b[1][1]));
@@ -428,14 +443,25 @@ __device__ __forceinline__ bool row_of(const Seq& q, const Item& it, const Shape
 // SPLIT: the four waves take a unit's tokens in turn for the same rows and are
 // joined through LDS; otherwise each has rows of its own.
 template <int D, int NR, bool SPLIT>
-__global__ __launch_bounds__(kThreads, NR == 1 ? 2 : 1) void attn_kernel(AttnArgs a, Shape s, float* parts, int* counts, Join* joins) {
+__global__ __launch_bounds__(kThreads, 2) void attn_kernel(AttnArgs a, Shape s, float* parts, int* counts, Join* joins) {
   constexpr int kM = D / 16;
   constexpr int kRows = SPLIT ? 16 * NR : 64 * NR;
   __shared__ int64_t red[6];
-  __shared__ f32x4 swap[SPLIT ? 2 * NR * kM * 64 : 1];
+  constexpr bool kLds = kQInLds<D, NR>;
+  __shared__ f32x4 swap[SPLIT ? 2 * kM * 64 : 1];
+  // a wave's own, or one for the four waves that share their rows
+  __shared__ f16x8 q_lds[kLds ? (SPLIT ? 1 : 4) * NR * (D / 32) * 64 : 1];
+  __shared__ float c_lds[kLds ? kRows : 1];
+  __shared__ int last_lds[kLds ? kRows : 1];
   __shared__ float stat[SPLIT ? 4 * 2 * 16 * NR : 1];
-  const int64_t wg = blockIdx.x, wgs = gridDim.x;
-  const Walk walk = find_walk(a, s, red, wgs, [&](const Shares& h) { return h.begin(wg); });
+  // where every work-group has work, neighbouring shares go to one of the eight
+  // dies, whose L2 then holds few heads
+  const int64_t wgs = gridDim.x;
+  auto number = [&](const Shares& h) {
+    return h.each > 0 ? (int64_t)(blockIdx.x & 7) * (wgs / 8) + (blockIdx.x >> 3) : (int64_t)blockIdx.x;
+  };
+  const Walk walk = find_walk(a, s, red, wgs, [&](const Shares& h) { return h.begin(number(h)); });
+  const int64_t wg = number(walk.share);
   const int64_t end = walk.share.begin(wg + 1);
   int64_t at = walk.share.begin(wg);
   if (at >= end) {
@@ -488,16 +514,20 @@ __global__ __launch_bounds__(kThreads, NR == 1 ? 2 : 1) void attn_kernel(AttnArg
     load_keys<D>(keys, now, lay, place);
     load_values<D>(values, now, lay, place);
     // its rows
-    f16x8 qf[NR][D / 32];
-    float c[NR];
-    int last[NR];
+    f16x8 qf[kLds ? 1 : NR][D / 32];
+    f16x8* q_own = q_lds + (SPLIT ? 0 : wave * NR * (D / 32) * 64) + lane;
+    if (kLds && SPLIT) __syncthreads();  // the last item's rows are done with
+    // a row's factor of the scores and the last token that it sees
+    float c_of[kLds ? 1 : NR];
+    int last_of[kLds ? 1 : NR];
+    const int row0 = SPLIT ? 0 : wave * 16 * NR;
     State<D, NR> st;
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
-      const int row = (SPLIT ? 0 : wave * 16 * NR) + n * 16 + (lane & 15);
+      const int row = row0 + n * 16 + (lane & 15);
       int token, head;
       const bool have = row_of(q, it, s, row, &token, &head);
-      last[n] = have ? q.off + (token - q.q0) : -1;
+      const int last = have ? q.off + (token - q.q0) : -1;
       const int64_t from = have ? token * a.ldq + head * a.ldqh + g * (D / 4) : 0;
       uint32_t w[D / 8];
 #pragma unroll
@@ -506,7 +536,7 @@ __global__ __launch_bounds__(kThreads, NR == 1 ? 2 : 1) void attn_kernel(AttnArg
       const uint32_t sign = a.scale < 0.0f ? 0x80008000u : 0u;  // a negative scale turns q around
 #pragma unroll
       for (int j = 0; j < D / 8; ++j) w[j] ^= sign;
-      c[n] = fabsf(a.scale) * 1.44269504088896340736f;
+      float c = fabsf(a.scale) * 1.44269504088896340736f;
       if (a.q_type == 3) {
         // BF16: times the power of two that puts the row's largest near 2^14
         uint32_t big = 0;
@@ -516,30 +546,57 @@ __global__ __launch_bounds__(kThreads, NR == 1 ? 2 : 1) void attn_kernel(AttnArg
         const int up = min(127 + 14 - e, 126);
         const float f = __builtin_bit_cast(float, (uint32_t)(127 + max(up, -126)) << 23);
         const float back = __builtin_bit_cast(float, (uint32_t)(127 - max(up, -126)) << 23);
-        c[n] *= back;
+        c *= back;
 #pragma unroll
         for (int j = 0; j < D / 8; ++j) {
           const float lo = __builtin_bit_cast(float, w[j] << 16) * f, hi = __builtin_bit_cast(float, w[j] & 0xFFFF0000u) * f;
           w[j] = __builtin_bit_cast(uint32_t, (f16x2){(_Float16)lo, (_Float16)hi});
         }
       }
-      c[n] = fmaxf(c[n], 1e-37f);  // never 0: a hidden score is -inf times this
+      c = fmaxf(c, 1e-37f);  // never 0: a hidden score is -inf times this
+      if constexpr (kLds) {
+        if (g == 0) {
+          c_lds[row] = c;
+          last_lds[row] = last;
+        }
+      } else {
+        c_of[n] = c;
+        last_of[n] = last;
+      }
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) {
         const f16x2 x = __builtin_bit_cast(f16x2, w[4 * j]), y = __builtin_bit_cast(f16x2, w[4 * j + 1]),
                     z = __builtin_bit_cast(f16x2, w[4 * j + 2]), u = __builtin_bit_cast(f16x2, w[4 * j + 3]);
-        qf[n][j] = (f16x8){x.x, z.x, x.y, z.y, y.x, u.x, y.y, u.y};  // 0 4 1 5 2 6 3 7
+        const f16x8 b = {x.x, z.x, x.y, z.y, y.x, u.x, y.y, u.y};  // 0 4 1 5 2 6 3 7
+        if constexpr (kLds) {
+          if (!SPLIT || wave == n % 4) q_own[(n * (D / 32) + j) * 64] = b;
+        } else {
+          qf[n][j] = b;
+        }
       }
       st.m[n] = kEmpty;
-      st.l[n] = (f32x4){0.f, 0.f, 0.f, 0.f};
+      st.l[n] = 0.0f;
 #pragma unroll
       for (int j = 0; j < kM; ++j) st.o[n][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
     }
+    if (kLds && SPLIT) __syncthreads();
+    auto q_of = [&](int n, int w) __attribute__((always_inline)) {
+      if constexpr (kLds) return q_own[(n * (D / 32) + w) * 64];
+      else return qf[n][w];
+    };
+    auto c_at = [&](int n) __attribute__((always_inline)) {
+      if constexpr (kLds) return c_lds[row0 + n * 16 + (lane & 15)];
+      else return c_of[n];
+    };
+    auto last_at = [&](int n) __attribute__((always_inline)) {
+      if constexpr (kLds) return last_lds[row0 + n * 16 + (lane & 15)];
+      else return last_of[n];
+    };
     // (a step past the last one loads nothing: there is no page for it)
     for (int steps = uniform(max(0, (t_end - t + kStep - 1) / kStep)); steps > 0; --steps) {
       f32x4 sc[NR][2];
       f16x8 p[NR];
-      scores<D, NR>(sc, keys, qf, ones);
+      scores<D, NR>(sc, keys, q_of, ones);
       __builtin_amdgcn_sched_barrier(0);
       load_keys<D>(keys, then, lay, place);
       const bool there = now.there[0] && now.there[1];
@@ -551,7 +608,7 @@ __global__ __launch_bounds__(kThreads, NR == 1 ? 2 : 1) void attn_kernel(AttnArg
           const int first = t + 16 * h + 4 * g;
 #pragma unroll
           for (int n = 0; n < NR; ++n) {
-            const int sees = now.there[h] ? last[n] - first : -1;
+            const int sees = now.there[h] ? last_at(n) - first : -1;
 #pragma unroll
             for (int e = 0; e < 4; ++e) sc[n][h][e] = e <= sees ? sc[n][h][e] : -INFINITY;
           }
@@ -563,7 +620,7 @@ __global__ __launch_bounds__(kThreads, NR == 1 ? 2 : 1) void attn_kernel(AttnArg
         }
       }
       __builtin_amdgcn_sched_barrier(0);
-      weigh<D, NR>(st, p, sc, c, ones);
+      weigh<D, NR>(st, p, sc, c_at, ones);
       __builtin_amdgcn_sched_barrier(0);
       gather<D, NR>(st, values, p, ones);
       __builtin_amdgcn_sched_barrier(0);
@@ -571,6 +628,11 @@ __global__ __launch_bounds__(kThreads, NR == 1 ? 2 : 1) void attn_kernel(AttnArg
       t += kStep;
       now = then;
       then = find(t + kStep);
+    }
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {  // over the four groups of lanes
+      st.l[n] += __shfl_xor(st.l[n], 16);
+      st.l[n] += __shfl_xor(st.l[n], 32);
     }
     if constexpr (SPLIT) {
       // one maximum for the four waves, then their sums
@@ -589,25 +651,24 @@ __global__ __launch_bounds__(kThreads, NR == 1 ? 2 : 1) void attn_kernel(AttnArg
         st.l[n] *= f;
 #pragma unroll
         for (int j = 0; j < kM; ++j) st.o[n][j] *= f;
-        if (g == 0) stat[64 * NR + wave * 16 * NR + n * 16 + lane] = st.l[n][0];
+        if (g == 0) stat[64 * NR + wave * 16 * NR + n * 16 + lane] = st.l[n];
       }
       // waves 2 and 3 hand over to 0 and 1, then 1 to 0
 #pragma unroll
-      for (int half = 2; half >= 1; half >>= 1) {
-        if (wave >= half && wave < 2 * half) {
+      for (int n = 0; n < NR; ++n) {
 #pragma unroll
-          for (int n = 0; n < NR; ++n)
+        for (int half = 2; half >= 1; half >>= 1) {
+          if (wave >= half && wave < 2 * half) {
 #pragma unroll
-            for (int j = 0; j < kM; ++j) swap[(((wave - half) * NR + n) * kM + j) * 64 + lane] = st.o[n][j];
+            for (int j = 0; j < kM; ++j) swap[((wave - half) * kM + j) * 64 + lane] = st.o[n][j];
+          }
+          __syncthreads();
+          if (wave < half) {
+#pragma unroll
+            for (int j = 0; j < kM; ++j) st.o[n][j] += swap[(wave * kM + j) * 64 + lane];
+          }
+          __syncthreads();
         }
-        __syncthreads();
-        if (wave < half) {
-#pragma unroll
-          for (int n = 0; n < NR; ++n)
-#pragma unroll
-            for (int j = 0; j < kM; ++j) st.o[n][j] += swap[((wave * NR + n) * kM + j) * 64 + lane];
-        }
-        __syncthreads();
       }
       if (wave == 0) {
 #pragma unroll
@@ -615,18 +676,17 @@ __global__ __launch_bounds__(kThreads, NR == 1 ? 2 : 1) void attn_kernel(AttnArg
           float l = 0.0f;
 #pragma unroll
           for (int w = 0; w < 4; ++w) l += stat[64 * NR + w * 16 * NR + n * 16 + (lane & 15)];
-          st.l[n][0] = l;
+          st.l[n] = l;
         }
       }
     }
     if (!SPLIT || wave == 0) {
-      const int row0 = SPLIT ? 0 : wave * 16 * NR;
       if (u0 == 0 && u1 == it.units) {
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
           int token, head;
           if (!row_of(q, it, s, row0 + n * 16 + (lane & 15), &token, &head)) continue;
-          const float l = st.l[n][0], f = inverse_of(l);
+          const float l = st.l[n], f = inverse_of(l);
           const int64_t to = token * a.ldo + head * a.ldoh + g * (D / 4);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -646,7 +706,7 @@ __global__ __launch_bounds__(kThreads, NR == 1 ? 2 : 1) void attn_kernel(AttnArg
           for (int j = 0; j < kM; ++j)
             reinterpret_cast<f32x4*>(part)[((row0 / 16 + n) * kM + j) * 64 + lane] = st.o[n][j];
           if (g == 0) {
-            reinterpret_cast<float2*>(part + kRows * D)[row0 + n * 16 + lane] = make_float2(st.m[n], st.l[n][0]);
+            reinterpret_cast<float2*>(part + kRows * D)[row0 + n * 16 + lane] = make_float2(st.m[n], st.l[n]);
           }
         }
       }
@@ -880,10 +940,10 @@ Variant variant_of(int64_t group, int64_t d, int64_t max_q) {
   const int64_t rows = group * max_q;
   Variant v;
   if (rows <= 16) v = {1, true, 16, 512};
-  else if (rows <= 32 || (d == 256 && rows <= 64)) v = {2, true, 32, 256};
-  else if (rows <= 64) v = {4, true, 64, 256};
-  else if (d == 256) v = {2, false, 128, 256};
-  else v = {4, false, 256, 256};
+  else if (rows <= 32 || (d == 256 && rows <= 64)) v = {2, true, 32, 512};
+  else if (rows <= 64) v = {4, true, 64, 512};
+  else if (d == 256) v = {2, false, 128, 512};
+  else v = {4, false, 256, 512};
   return v;
 }
 
