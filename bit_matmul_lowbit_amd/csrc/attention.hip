@@ -440,20 +440,101 @@ __device__ __forceinline__ bool row_of(const Seq& q, const Item& it, const Shape
   return t < (1 << s.tok_shift) && tok < q.nq && in < s.group;
 }
 
-// SPLIT: the four waves take a unit's tokens in turn for the same rows and are
-// joined through LDS; otherwise each has rows of its own.
-template <int D, int NR, bool SPLIT>
+// A quarter of a row of q, as the B operand of the scores, FP16, the values in
+// the order of the nibbles.  Returns what the row's scores are to be multiplied
+// by (with log2 e, for 2^x), never 0: a hidden score is -inf times this.
+template <int D>
+__device__ __forceinline__ float load_q(f16x8 (&out)[D / 32], const AttnArgs& a, bool have, int token, int head, int g) {
+  uint32_t w[D / 8];
+#pragma unroll
+  for (int j = 0; j < D / 8; ++j) w[j] = 0;
+  if (have)
+    __builtin_memcpy(w, static_cast<const uint16_t*>(a.q) + token * a.ldq + head * a.ldqh + g * (D / 4), sizeof(w));
+  const uint32_t sign = a.scale < 0.0f ? 0x80008000u : 0u;  // a negative scale turns q around
+#pragma unroll
+  for (int j = 0; j < D / 8; ++j) w[j] ^= sign;
+  float c = fabsf(a.scale) * 1.44269504088896340736f;
+  if (a.q_type == 3) {
+    // BF16: times the power of two that puts the row's largest near 2^14
+    uint32_t big = 0;
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j) big = max(big, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
+    const int e = (int)(__builtin_bit_cast(uint32_t, max_groups(__builtin_bit_cast(float, big << 16))) >> 23);
+    const int up = max(min(127 + 14 - e, 126), -126);
+    const float f = __builtin_bit_cast(float, (uint32_t)(127 + up) << 23);
+    c *= __builtin_bit_cast(float, (uint32_t)(127 - up) << 23);
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j) {
+      const float lo = __builtin_bit_cast(float, w[j] << 16) * f, hi = __builtin_bit_cast(float, w[j] & 0xFFFF0000u) * f;
+      w[j] = __builtin_bit_cast(uint32_t, (f16x2){(_Float16)lo, (_Float16)hi});
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j) {
+    const f16x2 x = __builtin_bit_cast(f16x2, w[4 * j]), y = __builtin_bit_cast(f16x2, w[4 * j + 1]),
+                z = __builtin_bit_cast(f16x2, w[4 * j + 2]), u = __builtin_bit_cast(f16x2, w[4 * j + 3]);
+    out[j] = (f16x8){x.x, z.x, x.y, z.y, y.x, u.x, y.y, u.y};  // 0 4 1 5 2 6 3 7
+  }
+  return fmaxf(c, 1e-37f);
+}
+
+// What the rows of a wave came to: their results, where the item is whole, or a
+// part for the join.
+template <int D, int NR, int ROWS>
+__device__ __forceinline__ void finish(const State<D, NR>& st, const AttnArgs& a, const Shape& s, const Seq& q,
+                                       const Item& it, int row0, bool whole, float* part, int lane) {
+  constexpr int kM = D / 16;
+  const int g = lane >> 4;
+#pragma unroll
+  for (int n = 0; n < NR; ++n) {
+    if (whole) {
+      int token, head;
+      if (!row_of(q, it, s, row0 + n * 16 + (lane & 15), &token, &head)) continue;
+      const float l = st.l[n], f = inverse_of(l);
+      const int64_t to = token * a.ldo + head * a.ldoh + g * (D / 4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float v[kM];
+#pragma unroll
+        for (int j = 0; j < kM; ++j) v[j] = st.o[n][j][e] * f;
+        store_row(a.out, a.out_type, to + e * kM, v);
+      }
+      if (a.lse && g == 0)
+        a.lse[token * a.hq + head] = l == 0.0f ? -INFINITY : 0.69314718055994530942f * (st.m[n] + __log2f(l));
+    } else {
+#pragma unroll
+      for (int j = 0; j < kM; ++j) reinterpret_cast<f32x4*>(part)[((row0 / 16 + n) * kM + j) * 64 + lane] = st.o[n][j];
+      if (g == 0) reinterpret_cast<float2*>(part + ROWS * D)[row0 + n * 16 + lane] = make_float2(st.m[n], st.l[n]);
+    }
+  }
+}
+
+// A work-group's note on its last item for the join
+__device__ __forceinline__ void leave(int* counts, Join* joins, const Shares& share, int64_t wg, bool first,
+                                      const Shape& s, const Seq& q, const Item& it, int64_t base, bool more) {
+  counts[wg] = more ? (int)(holder(share, base + it.first + it.units) - wg) + 1 : 0;
+  Join j = {};
+  j.slot = first ? 0 : 1;
+  j.token = q.q0 + (it.tile << s.tok_shift);
+  j.tokens = min(1 << s.tok_shift, q.nq - (it.tile << s.tok_shift));
+  j.head = it.head * s.group + it.part * s.part;
+  j.heads = min(s.part, s.group - it.part * s.part);
+  joins[wg] = j;
+}
+
+// Few rows: the four waves take a unit's tokens in turn for the same rows and are
+// joined through LDS.
+template <int D, int NR>
 __global__ __launch_bounds__(kThreads, 2) void attn_kernel(AttnArgs a, Shape s, float* parts, int* counts, Join* joins) {
   constexpr int kM = D / 16;
-  constexpr int kRows = SPLIT ? 16 * NR : 64 * NR;
+  constexpr int kRows = 16 * NR;
   __shared__ int64_t red[6];
   constexpr bool kLds = kQInLds<D, NR>;
-  __shared__ f32x4 swap[SPLIT ? 2 * kM * 64 : 1];
-  // a wave's own, or one for the four waves that share their rows
-  __shared__ f16x8 q_lds[kLds ? (SPLIT ? 1 : 4) * NR * (D / 32) * 64 : 1];
+  __shared__ f32x4 swap[2 * kM * 64];
+  __shared__ f16x8 q_lds[kLds ? NR * (D / 32) * 64 : 1];
   __shared__ float c_lds[kLds ? kRows : 1];
   __shared__ int last_lds[kLds ? kRows : 1];
-  __shared__ float stat[SPLIT ? 4 * 2 * 16 * NR : 1];
+  __shared__ float stat[4 * 2 * 16 * NR];
   // where every work-group has work, neighbouring shares go to one of the eight
   // dies, whose L2 then holds few heads
   const int64_t wgs = gridDim.x;
@@ -502,8 +583,8 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(AttnArgs a, Shape s, 
     const list_t table = list_of(a.table + (int64_t)seq * a.ldt);
     const uint8_t* head_base = a.pages + (int64_t)it.head * lay.bytes();
     const int t_end = uniform((int)min((int64_t)tile_end, (int64_t)u1 << unit_tokens_shift));
-    constexpr int kStep = SPLIT ? 128 : 32;
-    int t = uniform((u0 << unit_tokens_shift) + (SPLIT ? wave * 32 : 0));
+    constexpr int kStep = 128;
+    int t = uniform((u0 << unit_tokens_shift) + wave * 32);
     auto find = [&](int from) __attribute__((always_inline)) {
       return place_of(table, s.page_shift, head_base, page_bytes, lay.bytes(), (int)a.n_pages, t_end, from);
     };
@@ -515,45 +596,20 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(AttnArgs a, Shape s, 
     load_values<D>(values, now, lay, place);
     // its rows
     f16x8 qf[kLds ? 1 : NR][D / 32];
-    f16x8* q_own = q_lds + (SPLIT ? 0 : wave * NR * (D / 32) * 64) + lane;
-    if (kLds && SPLIT) __syncthreads();  // the last item's rows are done with
+    f16x8* q_own = q_lds + lane;
+    if (kLds) __syncthreads();  // the last item's rows are done with
     // a row's factor of the scores and the last token that it sees
     float c_of[kLds ? 1 : NR];
     int last_of[kLds ? 1 : NR];
-    const int row0 = SPLIT ? 0 : wave * 16 * NR;
     State<D, NR> st;
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
-      const int row = row0 + n * 16 + (lane & 15);
+      const int row = n * 16 + (lane & 15);
       int token, head;
       const bool have = row_of(q, it, s, row, &token, &head);
       const int last = have ? q.off + (token - q.q0) : -1;
-      const int64_t from = have ? token * a.ldq + head * a.ldqh + g * (D / 4) : 0;
-      uint32_t w[D / 8];
-#pragma unroll
-      for (int j = 0; j < D / 8; ++j) w[j] = 0;
-      if (have) __builtin_memcpy(w, static_cast<const uint16_t*>(a.q) + from, sizeof(w));
-      const uint32_t sign = a.scale < 0.0f ? 0x80008000u : 0u;  // a negative scale turns q around
-#pragma unroll
-      for (int j = 0; j < D / 8; ++j) w[j] ^= sign;
-      float c = fabsf(a.scale) * 1.44269504088896340736f;
-      if (a.q_type == 3) {
-        // BF16: times the power of two that puts the row's largest near 2^14
-        uint32_t big = 0;
-#pragma unroll
-        for (int j = 0; j < D / 8; ++j) big = max(big, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
-        const int e = (int)(__builtin_bit_cast(uint32_t, max_groups(__builtin_bit_cast(float, big << 16))) >> 23);
-        const int up = min(127 + 14 - e, 126);
-        const float f = __builtin_bit_cast(float, (uint32_t)(127 + max(up, -126)) << 23);
-        const float back = __builtin_bit_cast(float, (uint32_t)(127 - max(up, -126)) << 23);
-        c *= back;
-#pragma unroll
-        for (int j = 0; j < D / 8; ++j) {
-          const float lo = __builtin_bit_cast(float, w[j] << 16) * f, hi = __builtin_bit_cast(float, w[j] & 0xFFFF0000u) * f;
-          w[j] = __builtin_bit_cast(uint32_t, (f16x2){(_Float16)lo, (_Float16)hi});
-        }
-      }
-      c = fmaxf(c, 1e-37f);  // never 0: a hidden score is -inf times this
+      f16x8 qr[D / 32];
+      const float c = load_q<D>(qr, a, have, token, head, g);
       if constexpr (kLds) {
         if (g == 0) {
           c_lds[row] = c;
@@ -565,13 +621,10 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(AttnArgs a, Shape s, 
       }
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) {
-        const f16x2 x = __builtin_bit_cast(f16x2, w[4 * j]), y = __builtin_bit_cast(f16x2, w[4 * j + 1]),
-                    z = __builtin_bit_cast(f16x2, w[4 * j + 2]), u = __builtin_bit_cast(f16x2, w[4 * j + 3]);
-        const f16x8 b = {x.x, z.x, x.y, z.y, y.x, u.x, y.y, u.y};  // 0 4 1 5 2 6 3 7
         if constexpr (kLds) {
-          if (!SPLIT || wave == n % 4) q_own[(n * (D / 32) + j) * 64] = b;
+          if (wave == n % 4) q_own[(n * (D / 32) + j) * 64] = qr[j];
         } else {
-          qf[n][j] = b;
+          qf[n][j] = qr[j];
         }
       }
       st.m[n] = kEmpty;
@@ -579,17 +632,17 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(AttnArgs a, Shape s, 
 #pragma unroll
       for (int j = 0; j < kM; ++j) st.o[n][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
     }
-    if (kLds && SPLIT) __syncthreads();
+    if (kLds) __syncthreads();
     auto q_of = [&](int n, int w) __attribute__((always_inline)) {
       if constexpr (kLds) return q_own[(n * (D / 32) + w) * 64];
       else return qf[n][w];
     };
     auto c_at = [&](int n) __attribute__((always_inline)) {
-      if constexpr (kLds) return c_lds[row0 + n * 16 + (lane & 15)];
+      if constexpr (kLds) return c_lds[n * 16 + (lane & 15)];
       else return c_of[n];
     };
     auto last_at = [&](int n) __attribute__((always_inline)) {
-      if constexpr (kLds) return last_lds[row0 + n * 16 + (lane & 15)];
+      if constexpr (kLds) return last_lds[n * 16 + (lane & 15)];
       else return last_of[n];
     };
     // (a step past the last one loads nothing: there is no page for it)
@@ -634,7 +687,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(AttnArgs a, Shape s, 
       st.l[n] += __shfl_xor(st.l[n], 16);
       st.l[n] += __shfl_xor(st.l[n], 32);
     }
-    if constexpr (SPLIT) {
+    {
       // one maximum for the four waves, then their sums
       __syncthreads();
       if (g == 0)
@@ -680,48 +733,228 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(AttnArgs a, Shape s, 
         }
       }
     }
-    if (!SPLIT || wave == 0) {
-      if (u0 == 0 && u1 == it.units) {
+    if (wave == 0) {
+      finish<D, NR, kRows>(st, a, s, q, it, 0, u0 == 0 && u1 == it.units,
+                           parts + (wg * 2 + (first ? 0 : 1)) * kPartFloats<D, kRows>, lane);
+    }
+    if (threadIdx.x == 0 && base + it.first + u1 == end)  // its last item
+      leave(counts, joins, walk.share, wg, first, s, q, it, base, u0 == 0 && u1 < it.units);
+    first = false;
+    at = base + it.first + u1;
+  }
+}
+
+// A wave's share of 32 tokens' operands: kPer of the D / 16 operands of K (16
+// tokens, 32 values) and as many of V (32 tokens, 16 values)
+template <int D>
+struct Shared {
+  static constexpr int kPer = D / 64, kOps = D / 16;  // a wave's, all
+  static constexpr int kW = D == 64 ? 1 : D / 128;    // dwords of K, and of V, that they are of
+  uint32_t k[kPer], kp[kPer], v[kW][2], vp[2][4];
+  bool there[2];
+  int at;
+};
+template <int D>
+__device__ __forceinline__ void load_shared(Shared<D>& r, const Place& p, int t, const KvHead& lay, const Lane<D>& at,
+                                            int wave) {
+  constexpr int kPer = Shared<D>::kPer;
+  r.at = t;
 #pragma unroll
-        for (int n = 0; n < NR; ++n) {
-          int token, head;
-          if (!row_of(q, it, s, row0 + n * 16 + (lane & 15), &token, &head)) continue;
-          const float l = st.l[n], f = inverse_of(l);
-          const int64_t to = token * a.ldo + head * a.ldoh + g * (D / 4);
+  for (int h = 0; h < 2; ++h) r.there[h] = p.there[h];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float v[kM];
+  for (int j = 0; j < kPer; ++j) {
+    const int f = wave * kPer + j, w = f >> 1;
+    const auto part = D == 64 ? ((f & 1) ? p.part[1] : p.part[0]) : p.part[j & 1];
+    const int in = D == 64 ? ((f & 1) ? p.in[1] : p.in[0]) : p.in[j & 1];
+    r.k[j] = __builtin_amdgcn_raw_buffer_load_b32(part, at.k, in * (D / 2) + 4 * w, 0);
+    r.kp[j] = __builtin_amdgcn_raw_buffer_load_b32(part, at.kp, lay.k_params() + in * (D / 8) + (w / 4) * 4, 0);
+  }
 #pragma unroll
-            for (int j = 0; j < kM; ++j) v[j] = st.o[n][j][e] * f;
-            store_row(a.out, a.out_type, to + e * kM, v);
-          }
-          if (a.lse && g == 0)
-            a.lse[token * a.hq + head] = l == 0.0f ? -INFINITY : 0.69314718055994530942f * (st.m[n] + __log2f(l));
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int e = 0; e < Shared<D>::kW; ++e) {
+      const int w = (wave * kPer) / 2 + e;
+      r.v[e][h] = __builtin_amdgcn_raw_buffer_load_b32(p.part[h], at.v, lay.v_codes() + p.in[h] * (D / 2) + 4 * w, 0);
+    }
+    load_words(r.vp[h], p.part[h], at.vp, lay.v_params() + p.in[h] * (D / 8));
+  }
+}
+// ... as FP16 into LDS, where a lane of any wave finds its 16 bytes of them
+template <int D>
+__device__ __forceinline__ void spread_shared(f16x8* lds, Shared<D>& r, int len, int lane, int wave, uint32_t ones) {
+  constexpr int kPer = Shared<D>::kPer;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const uint32_t x = r.k[j];
+    const f16x2 a = splat_lo(r.kp[j]), b = splat_hi(r.kp[j]);
+    lds[(wave * kPer + j) * 64 + lane] = join(fma2(nibbles<0>(x, ones), a, b), fma2(nibbles<1>(x, ones), a, b),
+                                              fma2(nibbles<2>(x, ones), a, b), fma2(nibbles<3>(x, ones), a, b));
+  }
+  f16x2 a[2][2], b[2][2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    // what is not there counts 0 times p = 0, whatever its bits say
+    const int have = r.there[h] ? len - (r.at + 16 * h + 4 * (lane >> 4)) : 0;
+    const uint32_t m01 = have >= 2 ? 0xFFFFFFFFu : have == 1 ? 0x0000FFFFu : 0u;
+    const uint32_t m23 = have >= 4 ? 0xFFFFFFFFu : have == 3 ? 0x0000FFFFu : 0u;
+    a[h][0] = __builtin_bit_cast(f16x2, r.vp[h][0] & m01);
+    a[h][1] = __builtin_bit_cast(f16x2, r.vp[h][1] & m23);
+    b[h][0] = __builtin_bit_cast(f16x2, r.vp[h][2] & m01);
+    b[h][1] = __builtin_bit_cast(f16x2, r.vp[h][3] & m23);
+  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int f = wave * kPer + j;
+    const uint32_t x = r.v[j >> 1][0], y = r.v[j >> 1][1];
+    // even operands: nibbles 0 and 2, odd ones: 1 and 3
+    const int down = D == 64 ? (f & 1) * 4 : (j & 1) * 4;
+    const uint32_t xs = x >> down, ys = y >> down;
+    lds[(Shared<D>::kOps + f) * 64 + lane] =
+        join(fma2(nibbles<0>(xs, ones), a[0][0], b[0][0]), fma2(nibbles<2>(xs, ones), a[0][1], b[0][1]),
+             fma2(nibbles<0>(ys, ones), a[1][0], b[1][0]), fma2(nibbles<2>(ys, ones), a[1][1], b[1][1]));
+  }
+}
+
+// Many rows: every wave has kWaveRows of its own, and the four make the operands
+// of 32 tokens together, one step ahead, in two LDS buffers in turn (each wave
+// making all of them for itself, 64 rows a wave, was bound by that: 589 us where
+// this takes @@).
+constexpr int kTiles = 2, kWaveRows = 16 * kTiles, kManyRows = 4 * kWaveRows;
+template <int D>
+__global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(AttnArgs a, Shape s, float* parts, int* counts,
+                                                                Join* joins) {
+  constexpr int kM = D / 16, kOps = Shared<D>::kOps;
+  __shared__ int64_t red[6];
+  __shared__ f16x8 lds[2][2 * kOps * 64];
+  // where every work-group has work, neighbouring shares go to one of the eight
+  // dies, whose L2 then holds few heads
+  const int64_t wgs = gridDim.x;
+  auto number = [&](const Shares& h) {
+    return h.each > 0 ? (int64_t)(blockIdx.x & 7) * (wgs / 8) + (blockIdx.x >> 3) : (int64_t)blockIdx.x;
+  };
+  const Walk walk = find_walk(a, s, red, wgs, [&](const Shares& h) { return h.begin(number(h)); });
+  const int64_t wg = number(walk.share);
+  const int64_t end = walk.share.begin(wg + 1);
+  int64_t at = walk.share.begin(wg);
+  if (at >= end) {
+    if (threadIdx.x == 0) counts[wg] = 0;
+    return;
+  }
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), g = lane >> 4;
+  const Lane<D> place(lane);
+  const uint32_t ones = ones_of();
+  const KvHead lay(1 << s.page_shift, D);
+  const int64_t page_bytes = a.heads * lay.bytes();
+  const int unit_tokens_shift = s.unit_shift + s.tok_shift;
+  int i = walk.seq;
+  int64_t base = walk.base;
+  bool first = true;
+  while (at < end) {
+    Seq q = seq_of(a, s, i);
+    q.q0 = uniform(q.q0);
+    q.nq = uniform(q.nq);
+    q.off = uniform(q.off);
+    q.len = uniform(q.len);
+    if (at >= base + q.units) {
+      base += q.units;
+      ++i;
+      continue;
+    }
+    Item it = item_of(q, s, at - base);
+    it.head = uniform(it.head);
+    it.part = uniform(it.part);
+    it.tile = uniform(it.tile);
+    const int seq = uniform(i);
+    const int u0 = uniform((int)(at - base - it.first)), u1 = uniform((int)min(end - base - it.first, it.units));
+    const int tile_end = uniform(min(q.len, q.off + ((it.tile + 1) << s.tok_shift)));
+    const int open = uniform(min(q.len, q.off + (it.tile << s.tok_shift) + 1));
+    const list_t table = list_of(a.table + (int64_t)seq * a.ldt);
+    const uint8_t* head_base = a.pages + (int64_t)it.head * lay.bytes();
+    const int t_end = uniform((int)min((int64_t)tile_end, (int64_t)u1 << unit_tokens_shift));
+    int t = uniform(u0 << unit_tokens_shift);
+    auto find = [&](int from) __attribute__((always_inline)) {
+      return place_of(table, s.page_shift, head_base, page_bytes, lay.bytes(), (int)a.n_pages, t_end, from);
+    };
+    Shared<D> raw;
+    load_shared<D>(raw, find(t), t, lay, place, wave);
+    Place then = find(t + 32);
+    f16x8 q_op[kTiles][D / 32];
+    float c[kTiles];
+    int last[kTiles];
+    State<D, kTiles> st;
+#pragma unroll
+    for (int n = 0; n < kTiles; ++n) {
+      int token, head;
+      const bool have = row_of(q, it, s, wave * kWaveRows + n * 16 + (lane & 15), &token, &head);
+      last[n] = have ? q.off + (token - q.q0) : -1;
+      c[n] = load_q<D>(q_op[n], a, have, token, head, g);
+      st.m[n] = kEmpty;
+      st.l[n] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kM; ++j) st.o[n][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    }
+    bool there0 = raw.there[0], there1 = raw.there[1];
+    spread_shared<D>(lds[0], raw, q.len, lane, wave, ones);
+    load_shared<D>(raw, then, t + 32, lay, place, wave);
+    then = find(t + 64);
+    __syncthreads();
+    int turn = 0;
+    for (int steps = uniform(max(0, (t_end - t + 31) / 32)); steps > 0; --steps) {
+      const f16x8* ops = lds[turn];
+      f32x4 sc[kTiles][2];
+      f16x8 p[kTiles];
+#pragma unroll
+      for (int n = 0; n < kTiles; ++n) sc[n][0] = sc[n][1] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < D / 32; ++w)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const f16x8 key = ops[(2 * w + h) * 64 + lane];
+#pragma unroll
+          for (int n = 0; n < kTiles; ++n)
+            sc[n][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(key, q_op[n][w], sc[n][h], 0, 0, 0);
         }
-      } else {
-        float* part = parts + (wg * 2 + (first ? 0 : 1)) * kPartFloats<D, kRows>;
+      __builtin_amdgcn_sched_barrier(0);
+      const bool now0 = there0, now1 = there1;
+      there0 = raw.there[0];
+      there1 = raw.there[1];
+      // the next step's operands, and the codes of the one after it
+      spread_shared<D>(lds[turn ^ 1], raw, q.len, lane, wave, ones);
+      load_shared<D>(raw, then, t + 64, lay, place, wave);
+      then = find(t + 96);
+      __builtin_amdgcn_sched_barrier(0);
+      if (t + 32 > open || !now0 || !now1) {
 #pragma unroll
-        for (int n = 0; n < NR; ++n) {
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int j = 0; j < kM; ++j)
-            reinterpret_cast<f32x4*>(part)[((row0 / 16 + n) * kM + j) * 64 + lane] = st.o[n][j];
-          if (g == 0) {
-            reinterpret_cast<float2*>(part + kRows * D)[row0 + n * 16 + lane] = make_float2(st.m[n], st.l[n]);
+          for (int n = 0; n < kTiles; ++n) {
+            const int sees = (h ? now1 : now0) ? last[n] - (t + 16 * h + 4 * g) : -1;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[n][h][e] = e <= sees ? sc[n][h][e] : -INFINITY;
           }
-        }
       }
+      weigh<D, kTiles>(st, p, sc, [&](int n) { return c[n]; }, ones);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < kM; ++j) {
+        const f16x8 value = ops[(kOps + j) * 64 + lane];
+#pragma unroll
+        for (int n = 0; n < kTiles; ++n)
+          st.o[n][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value, p[n], st.o[n][j], 0, 0, 0);
+      }
+      __syncthreads();
+      t += 32;
+      turn ^= 1;
     }
-    if (threadIdx.x == 0 && base + it.first + u1 == end) {  // its last item
-      const bool more = u0 == 0 && u1 < it.units;
-      counts[wg] = more ? (int)(holder(walk.share, base + it.first + it.units) - wg) + 1 : 0;
-      Join j = {};
-      j.slot = first ? 0 : 1;
-      j.token = q.q0 + (it.tile << s.tok_shift);
-      j.tokens = min(1 << s.tok_shift, q.nq - (it.tile << s.tok_shift));
-      j.head = it.head * s.group + it.part * s.part;
-      j.heads = min(s.part, s.group - it.part * s.part);
-      joins[wg] = j;
+#pragma unroll
+    for (int n = 0; n < kTiles; ++n) {  // over the four groups of lanes
+      st.l[n] += __shfl_xor(st.l[n], 16);
+      st.l[n] += __shfl_xor(st.l[n], 32);
     }
+    finish<D, kTiles, kManyRows>(st, a, s, q, it, wave * kWaveRows, u0 == 0 && u1 == it.units,
+                                 parts + (wg * 2 + (first ? 0 : 1)) * kPartFloats<D, kManyRows>, lane);
+    if (threadIdx.x == 0 && base + it.first + u1 == end)  // its last item
+      leave(counts, joins, walk.share, wg, first, s, q, it, base, u0 == 0 && u1 < it.units);
     first = false;
     at = base + it.first + u1;
   }
@@ -928,60 +1161,54 @@ int log2_of(int64_t v) {
 }
 
 // Which kernel, by the rows that a KV head's queries have at most in a sequence:
-// four waves split the tokens while a wave can hold the rows (NR tiles of 16),
+// the waves split the tokens while one of them can hold the rows (nr tiles of 16),
 // beyond they split the rows.
 struct Variant {
-  int nr;
-  bool split;
+  int nr;  // 0: attn_rows_kernel
   int rows;
-  int wgs;
 };
+constexpr int kWgs = 512;  // two a unit
 Variant variant_of(int64_t group, int64_t d, int64_t max_q) {
   const int64_t rows = group * max_q;
-  Variant v;
-  if (rows <= 16) v = {1, true, 16, 512};
-  else if (rows <= 32 || (d == 256 && rows <= 64)) v = {2, true, 32, 512};
-  else if (rows <= 64) v = {4, true, 64, 512};
-  else if (d == 256) v = {2, false, 128, 512};
-  else v = {4, false, 256, 512};
-  return v;
+  if (rows <= 16) return {1, 16};
+  if (rows <= 32) return {2, 32};
+  if (rows <= 64 && d < 256) return {4, 64};
+  return {0, kManyRows};
 }
 
-template <int D, int NR, bool SPLIT>
-void launch_one(const AttnArgs& a, const Shape& s, const Variant& v, void* ws, hipStream_t st) {
-  constexpr int kRows = SPLIT ? 16 * NR : 64 * NR;
+template <int D, int NR>
+void launch_one(const AttnArgs& a, const Shape& s, void* ws, hipStream_t st) {
+  constexpr int kRows = NR ? 16 * NR : kManyRows;
   int* counts = static_cast<int*>(ws);
-  Join* joins = reinterpret_cast<Join*>(counts + v.wgs);
-  float* parts = reinterpret_cast<float*>(joins + v.wgs);
-  attn_kernel<D, NR, SPLIT><<<v.wgs, kThreads, 0, st>>>(a, s, parts, counts, joins);
+  Join* joins = reinterpret_cast<Join*>(counts + kWgs);
+  float* parts = reinterpret_cast<float*>(joins + kWgs);
   // no more items than this, and of a work-group one at most
   const int64_t items = min(a.m, a.b + (a.m >> s.tok_shift)) * a.heads * s.parts;
-  const unsigned most = (unsigned)min((int64_t)v.wgs, items);
-  if constexpr (SPLIT)
+  const unsigned most = (unsigned)min((int64_t)kWgs, items);
+  if constexpr (NR > 0) {
+    attn_kernel<D, NR><<<kWgs, kThreads, 0, st>>>(a, s, parts, counts, joins);
     attn_join_kernel<D, kRows><<<dim3(most, kRows / 16 * (D / 16 / kJ)), kJoinThreads, 0, st>>>(
-        a, s.part, parts, counts, joins, v.wgs);
-  else
+        a, s.part, parts, counts, joins, kWgs);
+  } else {
+    attn_rows_kernel<D><<<kWgs, kThreads, 0, st>>>(a, s, parts, counts, joins);
     attn_join_rows_kernel<D, kRows><<<dim3(most, kRows / 64), kThreads, 0, st>>>(a, s.part, parts, counts, joins,
-                                                                                v.wgs);
+                                                                                kWgs);
+  }
 }
 
 template <int D>
 void launch_d(const AttnArgs& a, const Shape& s, const Variant& v, void* ws, hipStream_t st) {
-  if (v.split && v.nr == 1) launch_one<D, 1, true>(a, s, v, ws, st);
-  else if (v.split && v.nr == 2) launch_one<D, 2, true>(a, s, v, ws, st);
-  if constexpr (D == 256) {
-    if (!v.split) launch_one<D, 2, false>(a, s, v, ws, st);
-  } else {
-    if (v.split && v.nr == 4) launch_one<D, 4, true>(a, s, v, ws, st);
-    else if (!v.split) launch_one<D, 4, false>(a, s, v, ws, st);
-  }
+  if (v.nr == 1) launch_one<D, 1>(a, s, ws, st);
+  else if (v.nr == 2) launch_one<D, 2>(a, s, ws, st);
+  else if (v.nr == 0) launch_one<D, 0>(a, s, ws, st);
+  else if constexpr (D < 256) launch_one<D, 4>(a, s, ws, st);
 }
 
 }  // namespace
 
 size_t attention_workspace_bytes(int64_t hq, int64_t heads, int64_t d, int64_t max_q) {
   const Variant v = variant_of(hq / heads, d, max_q);
-  return (size_t)v.wgs * (sizeof(int) + sizeof(Join) + 2 * v.rows * (size_t)(d + 2) * sizeof(float));
+  return (size_t)kWgs * (sizeof(int) + sizeof(Join) + 2 * v.rows * (size_t)(d + 2) * sizeof(float));
 }
 
 hipError_t launch_attention(const AttnArgs& a, void* ws, hipStream_t st) {
