@@ -333,33 +333,48 @@ __device__ __forceinline__ void scores(f32x4 (&s)[NR][2], const Keys<D>& r, Q q,
 template <int D, int NR, class C>
 __device__ __forceinline__ void weigh(State<D, NR>& st, f16x8 (&p)[NR], const f32x4 (&s)[NR][2], C c, uint32_t ones) {
   const f16x2 one = __builtin_bit_cast(f16x2, ones);
+  // two tiles at a time, for which there is one question whether a maximum rises
+  constexpr int kTogether = NR < 2 ? 1 : 2;
 #pragma unroll
-  for (int n = 0; n < NR; ++n) {
+  for (int n0 = 0; n0 < NR; n0 += kTogether) {
     // scaled first, the maximum taken away after: the largest gives exactly 1
     // however large it is
-    const float f0 = c(n);
-    const f32x4 x = s[n][0] * f0, y = s[n][1] * f0;
-    const float most = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])));
-    if (__builtin_amdgcn_ballot_w64(most > st.m[n] + kRaise) != 0) {
-      const float m = fmaxf(st.m[n], max_groups(most));
-      const float f = exp2_fast(st.m[n] - m);
-      st.m[n] = m;
-      st.l[n] *= f;
+    f32x4 x[kTogether][2];
+    float most[kTogether];
+    bool rises = false;
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) st.o[n][i] *= f;
+    for (int n = 0; n < kTogether; ++n) {
+      const float f = c(n0 + n);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) x[n][h] = s[n0 + n][h] * f;
+      const f32x4 u = x[n][0], v = x[n][1];
+      most[n] = fmaxf(fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3])), fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])));
+      rises = rises || most[n] > st.m[n0 + n] + kRaise;
     }
-    f16x2 pk[4];
+    if (__builtin_amdgcn_ballot_w64(rises) != 0) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      pk[e] = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_pkrtz(exp2_fast(x[2 * e] - st.m[n]),
-                                                                   exp2_fast(x[2 * e + 1] - st.m[n])));
-      pk[e + 2] = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_pkrtz(exp2_fast(y[2 * e] - st.m[n]),
-                                                                       exp2_fast(y[2 * e + 1] - st.m[n])));
+      for (int n = 0; n < kTogether; ++n) {
+        const float m = fmaxf(st.m[n0 + n], max_groups(most[n]));
+        const float f = exp2_fast(st.m[n0 + n] - m);
+        st.m[n0 + n] = m;
+        st.l[n0 + n] *= f;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) st.o[n0 + n][i] *= f;
+      }
     }
-    p[n] = join(pk[0], pk[1], pk[2], pk[3]);
-    // the sum of the rounded p, as the product with V takes them
 #pragma unroll
-    for (int e = 0; e < 4; ++e) st.l[n] = __builtin_amdgcn_fdot2(pk[e], one, st.l[n], false);
+    for (int n = 0; n < kTogether; ++n) {
+      f16x2 pk[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        pk[e] = __builtin_bit_cast(
+            f16x2, __builtin_amdgcn_cvt_pkrtz(exp2_fast(x[n][e >> 1][2 * (e & 1)] - st.m[n0 + n]),
+                                              exp2_fast(x[n][e >> 1][2 * (e & 1) + 1] - st.m[n0 + n])));
+      p[n0 + n] = join(pk[0], pk[1], pk[2], pk[3]);
+      // the sum of the rounded p, as the product with V takes them
+#pragma unroll
+      for (int e = 0; e < 4; ++e) st.l[n0 + n] = __builtin_amdgcn_fdot2(pk[e], one, st.l[n0 + n], false);
+    }
   }
 }
 
@@ -791,16 +806,24 @@ __device__ __forceinline__ void spread_shared(f16x8* lds, Shared<D>& r, int len,
                                               fma2(nibbles<2>(x, ones), a, b), fma2(nibbles<3>(x, ones), a, b));
   }
   f16x2 a[2][2], b[2][2];
+  if (r.at + 32 > len) {
+    // tokens past the end count 0 times p = 0, whatever their bits say (those of
+    // no page are zeros already)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int have = len - (r.at + 16 * h + 4 * (lane >> 4));
+      const uint32_t m01 = have >= 2 ? 0xFFFFFFFFu : have == 1 ? 0x0000FFFFu : 0u;
+      const uint32_t m23 = have >= 4 ? 0xFFFFFFFFu : have == 3 ? 0x0000FFFFu : 0u;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r.vp[h][e] &= e & 1 ? m23 : m01;
+    }
+  }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    // what is not there counts 0 times p = 0, whatever its bits say
-    const int have = r.there[h] ? len - (r.at + 16 * h + 4 * (lane >> 4)) : 0;
-    const uint32_t m01 = have >= 2 ? 0xFFFFFFFFu : have == 1 ? 0x0000FFFFu : 0u;
-    const uint32_t m23 = have >= 4 ? 0xFFFFFFFFu : have == 3 ? 0x0000FFFFu : 0u;
-    a[h][0] = __builtin_bit_cast(f16x2, r.vp[h][0] & m01);
-    a[h][1] = __builtin_bit_cast(f16x2, r.vp[h][1] & m23);
-    b[h][0] = __builtin_bit_cast(f16x2, r.vp[h][2] & m01);
-    b[h][1] = __builtin_bit_cast(f16x2, r.vp[h][3] & m23);
+    a[h][0] = __builtin_bit_cast(f16x2, r.vp[h][0]);
+    a[h][1] = __builtin_bit_cast(f16x2, r.vp[h][1]);
+    b[h][0] = __builtin_bit_cast(f16x2, r.vp[h][2]);
+    b[h][1] = __builtin_bit_cast(f16x2, r.vp[h][3]);
   }
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
@@ -903,17 +926,12 @@ __global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(AttnArgs a, Shap
       const f16x8* ops = lds[turn];
       f32x4 sc[kTiles][2];
       f16x8 p[kTiles];
+      // operands leave LDS kAhead at a time, before what stands between them and
+      // their products: the next step's operands, and the weights
+      constexpr int kAhead = kOps < 8 ? kOps : 8;
+      f16x8 op[kAhead];
 #pragma unroll
-      for (int n = 0; n < kTiles; ++n) sc[n][0] = sc[n][1] = (f32x4){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int w = 0; w < D / 32; ++w)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const f16x8 key = ops[(2 * w + h) * 64 + lane];
-#pragma unroll
-          for (int n = 0; n < kTiles; ++n)
-            sc[n][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(key, q_op[n][w], sc[n][h], 0, 0, 0);
-        }
+      for (int j = 0; j < kAhead; ++j) op[j] = ops[j * 64 + lane];
       __builtin_amdgcn_sched_barrier(0);
       const bool now0 = there0, now1 = there1;
       there0 = raw.there[0];
@@ -922,6 +940,20 @@ __global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(AttnArgs a, Shap
       spread_shared<D>(lds[turn ^ 1], raw, q.len, lane, wave, ones);
       load_shared<D>(raw, then, t + 64, lay, place, wave);
       then = find(t + 96);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int n = 0; n < kTiles; ++n) sc[n][0] = sc[n][1] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j0 = 0; j0 < kOps; j0 += kAhead) {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+#pragma unroll
+          for (int n = 0; n < kTiles; ++n)
+            sc[n][j & 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(op[j], q_op[n][(j0 + j) >> 1], sc[n][j & 1], 0, 0, 0);
+          // then the operands that follow: of K, and after them the first of V
+          op[j] = ops[(j0 + kAhead + j) * 64 + lane];
+        }
+      }
       __builtin_amdgcn_sched_barrier(0);
       if (t + 32 > open || !now0 || !now1) {
 #pragma unroll
@@ -936,11 +968,14 @@ __global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(AttnArgs a, Shap
       weigh<D, kTiles>(st, p, sc, [&](int n) { return c[n]; }, ones);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int j = 0; j < kM; ++j) {
-        const f16x8 value = ops[(kOps + j) * 64 + lane];
+      for (int j0 = 0; j0 < kM; j0 += kAhead) {
 #pragma unroll
-        for (int n = 0; n < kTiles; ++n)
-          st.o[n][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value, p[n], st.o[n][j], 0, 0, 0);
+        for (int j = 0; j < kAhead; ++j) {
+#pragma unroll
+          for (int n = 0; n < kTiles; ++n)
+            st.o[n][j0 + j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(op[j], p[n], st.o[n][j0 + j], 0, 0, 0);
+          if (j0 + kAhead < kM) op[j] = ops[(kOps + j0 + kAhead + j) * 64 + lane];
+        }
       }
       __syncthreads();
       t += 32;
