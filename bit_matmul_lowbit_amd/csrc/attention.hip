@@ -65,6 +65,11 @@ __device__ __forceinline__ int64_t uniform64(int64_t v) {
 typedef const __attribute__((address_space(4))) int32_t* list_t;
 __device__ __forceinline__ list_t list_of(const int32_t* p) { return (list_t)(uintptr_t)p; }
 
+// What beginning an item costs, in units: an item counts as so many units more
+// than its tokens are.  (Three prompts of 8192, 2729 and 510 tokens, chunks of up to
+// 2048: 541 us without, @@ with one.)
+constexpr int kBegin = 1;
+
 // How rows and tokens are cut; made on the host.
 struct Shape {
   int group;        // query heads of a KV head
@@ -75,10 +80,12 @@ struct Shape {
   int page_shift;
 };
 
-// sum of ceil(y / r) for y = 1..x, r = 1 << shift
-__device__ __forceinline__ int64_t units_up_to(int64_t x, int shift) {
-  const int64_t a = x >> shift, b = x & (((int64_t)1 << shift) - 1);
-  return ((a * (a + 1) / 2) << shift) + b * (a + 1);
+// sum of kBegin + ceil(y / r) for y = 1..x, r = 1 << shift: the units of the tiles
+// whose last row sees up to x tiles' worth of tokens
+template <class T>
+__device__ __forceinline__ T units_up_to(T x, int shift) {
+  const T a = x >> shift, b = x & (((T)1 << shift) - 1);
+  return ((a * (a + 1) / 2) << shift) + b * (a + 1) + kBegin * x;
 }
 
 // one sequence of the call
@@ -105,7 +112,7 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& a, const Shape& s, int i) 
   const int tt = 1 << s.tok_shift;
   q.before = (max(q.off, 0) + tt - 1) >> s.tok_shift;
   const int tiles = (q.nq + tt - 1) >> s.tok_shift;
-  q.per = units_up_to(q.before + tiles, s.unit_shift) - units_up_to(q.before, s.unit_shift);
+  q.per = units_up_to((int64_t)q.before + tiles, s.unit_shift) - units_up_to((int64_t)q.before, s.unit_shift);
   q.units = q.per * a.heads * s.parts;
   return q;
 }
@@ -116,6 +123,14 @@ struct Shares {
   int64_t each, more;
   __device__ __forceinline__ int64_t begin(int64_t i) const { return i * each + min(i, more); }
 };
+
+__device__ __forceinline__ Shares shares_of(int64_t total, int64_t wgs) {
+  Shares h;
+  // few units: no 64-bit division (a hundred instructions in a row)
+  h.each = total <= INT32_MAX ? (int64_t)((uint32_t)total / (uint32_t)wgs) : total / wgs;
+  h.more = total - h.each * wgs;
+  return h;
+}
 
 // Which work-group does what, found by every work-group for itself.
 struct Walk {
@@ -129,6 +144,10 @@ struct Walk {
 template <class F>
 __device__ __forceinline__ Walk find_walk(const AttnArgs& a, const Shape& s, int64_t* red, int64_t wgs, F pick) {
   const int t = threadIdx.x, n = (int)a.b;
+  if (n == 1) {
+    const int64_t total = uniform64(seq_of(a, s, 0).units);
+    return {0, 0, shares_of(total, wgs)};
+  }
   const int chunk = (n + kThreads - 1) / kThreads, lo = min(n, t * chunk), hi = min(n, lo + chunk);
   int64_t mine = 0;
   for (int i = lo; i < hi; ++i) mine += seq_of(a, s, i).units;
@@ -148,11 +167,7 @@ __device__ __forceinline__ Walk find_walk(const AttnArgs& a, const Shape& s, int
     total += red[w];
   }
   int64_t at = before + sum - mine;
-  Shares share;
-  total = uniform64(total);
-  // few units: no 64-bit division (its hundred instructions in a row)
-  share.each = total <= INT32_MAX ? (int64_t)((uint32_t)total / (uint32_t)wgs) : total / wgs;
-  share.more = total - share.each * wgs;
+  const Shares share = shares_of(uniform64(total), wgs);
   const int64_t want = pick(share);
   if (want >= at && want < at + mine) {
     for (int i = lo; i < hi; ++i) {
@@ -172,26 +187,39 @@ __device__ __forceinline__ Walk find_walk(const AttnArgs& a, const Shape& s, int
 // one item: a tile of a KV head of a sequence
 struct Item {
   int head, part, tile;
-  int64_t first, units;  // its units, from the start of the sequence's
+  int64_t first;   // its units begin there, counted from the start of the sequence's
+  int units;
 };
-__device__ __forceinline__ Item item_of(const Seq& q, const Shape& s, int64_t unit) {
+template <class T>
+__device__ __forceinline__ Item item_by(const Seq& q, const Shape& s, T unit) {
   Item it;
-  const int64_t which = unit / q.per, rest = unit - which * q.per;
-  it.head = (int)(which / s.parts);
-  it.part = (int)(which - (int64_t)it.head * s.parts);
+  const T per = (T)q.per, which = unit / per, rest = unit - which * per;
+  it.head = (int)which / s.parts;
+  it.part = (int)which - it.head * s.parts;
   // the tile that unit `rest` is of: the last one whose units begin at or before it
-  const int64_t zero = units_up_to(q.before, s.unit_shift);
+  const T zero = units_up_to((T)q.before, s.unit_shift);
   int lo = 0, hi = (q.nq + (1 << s.tok_shift) - 1) >> s.tok_shift;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (units_up_to(q.before + mid, s.unit_shift) - zero <= rest) lo = mid;
+    if (units_up_to((T)(q.before + mid), s.unit_shift) - zero <= rest) lo = mid;
     else hi = mid;
   }
   it.tile = lo;
-  const int64_t begin = units_up_to(q.before + lo, s.unit_shift) - zero;
-  it.units = units_up_to(q.before + lo + 1, s.unit_shift) - zero - begin;
-  it.first = which * q.per + begin;
+  const T begin = units_up_to((T)(q.before + lo), s.unit_shift) - zero;
+  it.units = (int)(units_up_to((T)(q.before + lo + 1), s.unit_shift) - zero - begin);
+  it.first = (int64_t)(which * per + begin);
   return it;
+}
+// Scalar 32-bit arithmetic wherever the numbers allow it: 64-bit divisions and
+// products cost some microseconds an item.
+__device__ __forceinline__ Item item_of(const Seq& q, const Shape& s, int64_t unit) {
+  const int64_t most = units_up_to((int64_t)q.before + ((q.nq + (1 << s.tok_shift) - 1) >> s.tok_shift), s.unit_shift);
+  if (uniform(most <= INT32_MAX && q.units <= INT32_MAX)) {
+    Seq u = q;
+    u.per = uniform((int)q.per);
+    return item_by<uint32_t>(u, s, (uint32_t)uniform((int)unit));
+  }
+  return item_by<int64_t>(q, s, unit);
 }
 
 // Codes and params of 32 tokens' keys, and of their values, as a lane needs them
@@ -590,7 +618,9 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(AttnArgs a, Shape s, 
     it.part = uniform(it.part);
     it.tile = uniform(it.tile);
     const int seq = uniform(i);
-    const int u0 = uniform((int)(at - base - it.first)), u1 = uniform((int)min(end - base - it.first, it.units));
+    // its units of this work-group, and those of them that have tokens
+    const int v0 = uniform((int)(at - base - it.first)), v1 = uniform((int)min(end - base - it.first, (int64_t)it.units));
+    const int u0 = max(v0 - kBegin, 0), u1 = max(v1 - kBegin, 0);
     // the tokens that any of its rows sees, and those that all of them see (rows
     // that are not there may count what they like)
     const int tile_end = uniform(min(q.len, q.off + ((it.tile + 1) << s.tok_shift)));
@@ -749,13 +779,13 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(AttnArgs a, Shape s, 
       }
     }
     if (wave == 0) {
-      finish<D, NR, kRows>(st, a, s, q, it, 0, u0 == 0 && u1 == it.units,
+      finish<D, NR, kRows>(st, a, s, q, it, 0, v0 == 0 && v1 == it.units,
                            parts + (wg * 2 + (first ? 0 : 1)) * kPartFloats<D, kRows>, lane);
     }
-    if (threadIdx.x == 0 && base + it.first + u1 == end)  // its last item
-      leave(counts, joins, walk.share, wg, first, s, q, it, base, u0 == 0 && u1 < it.units);
+    if (threadIdx.x == 0 && base + it.first + v1 == end)  // its last item
+      leave(counts, joins, walk.share, wg, first, s, q, it, base, v0 == 0 && v1 < it.units);
     first = false;
-    at = base + it.first + u1;
+    at = base + it.first + v1;
   }
 }
 
@@ -842,11 +872,15 @@ __device__ __forceinline__ void spread_shared(f16x8* lds, Shared<D>& r, int len,
 // of 32 tokens together, one step ahead, in two LDS buffers in turn (each wave
 // making all of them for itself, 64 rows a wave, was bound by that: 589 us where
 // this takes @@).
-constexpr int kTiles = 2, kWaveRows = 16 * kTiles, kManyRows = 4 * kWaveRows;
+// A wave has 32 rows, or 16 of 256 values (32 of those and their q do not fit its registers).
+template <int D>
+constexpr int kManyTiles = D == 256 ? 1 : 2;
+template <int D>
+constexpr int kManyRows = 64 * kManyTiles<D>;
 template <int D>
 __global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(AttnArgs a, Shape s, float* parts, int* counts,
                                                                 Join* joins) {
-  constexpr int kM = D / 16, kOps = Shared<D>::kOps;
+  constexpr int kM = D / 16, kOps = Shared<D>::kOps, kTiles = kManyTiles<D>, kWaveRows = 16 * kTiles;
   __shared__ int64_t red[6];
   __shared__ f16x8 lds[2][2 * kOps * 64];
   // where every work-group has work, neighbouring shares go to one of the eight
@@ -888,7 +922,9 @@ __global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(AttnArgs a, Shap
     it.part = uniform(it.part);
     it.tile = uniform(it.tile);
     const int seq = uniform(i);
-    const int u0 = uniform((int)(at - base - it.first)), u1 = uniform((int)min(end - base - it.first, it.units));
+    // its units of this work-group, and those of them that have tokens
+    const int v0 = uniform((int)(at - base - it.first)), v1 = uniform((int)min(end - base - it.first, (int64_t)it.units));
+    const int u0 = max(v0 - kBegin, 0), u1 = max(v1 - kBegin, 0);
     const int tile_end = uniform(min(q.len, q.off + ((it.tile + 1) << s.tok_shift)));
     const int open = uniform(min(q.len, q.off + (it.tile << s.tok_shift) + 1));
     const list_t table = list_of(a.table + (int64_t)seq * a.ldt);
@@ -986,12 +1022,12 @@ __global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(AttnArgs a, Shap
       st.l[n] += __shfl_xor(st.l[n], 16);
       st.l[n] += __shfl_xor(st.l[n], 32);
     }
-    finish<D, kTiles, kManyRows>(st, a, s, q, it, wave * kWaveRows, u0 == 0 && u1 == it.units,
-                                 parts + (wg * 2 + (first ? 0 : 1)) * kPartFloats<D, kManyRows>, lane);
-    if (threadIdx.x == 0 && base + it.first + u1 == end)  // its last item
-      leave(counts, joins, walk.share, wg, first, s, q, it, base, u0 == 0 && u1 < it.units);
+    finish<D, kTiles, kManyRows<D>>(st, a, s, q, it, wave * kWaveRows, v0 == 0 && v1 == it.units,
+                                 parts + (wg * 2 + (first ? 0 : 1)) * kPartFloats<D, kManyRows<D>>, lane);
+    if (threadIdx.x == 0 && base + it.first + v1 == end)  // its last item
+      leave(counts, joins, walk.share, wg, first, s, q, it, base, v0 == 0 && v1 < it.units);
     first = false;
-    at = base + it.first + u1;
+    at = base + it.first + v1;
   }
 }
 
@@ -1208,12 +1244,12 @@ Variant variant_of(int64_t group, int64_t d, int64_t max_q) {
   if (rows <= 16) return {1, 16};
   if (rows <= 32) return {2, 32};
   if (rows <= 64 && d < 256) return {4, 64};
-  return {0, kManyRows};
+  return {0, d == 256 ? kManyRows<256> : kManyRows<128>};
 }
 
 template <int D, int NR>
 void launch_one(const AttnArgs& a, const Shape& s, void* ws, hipStream_t st) {
-  constexpr int kRows = NR ? 16 * NR : kManyRows;
+  constexpr int kRows = NR ? 16 * NR : kManyRows<D>;
   int* counts = static_cast<int*>(ws);
   Join* joins = reinterpret_cast<Join*>(counts + kWgs);
   float* parts = reinterpret_cast<float*>(joins + kWgs);
