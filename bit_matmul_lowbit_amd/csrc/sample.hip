@@ -14,9 +14,10 @@
 // on one scale for all parts, so parts are added without being read again.  The second
 // launch, a work-group a row, adds the histograms and finds the bin in which
 // each filter ends.  Where few tokens come before that (kList), they are
-// gathered, sorted and drawn from in LDS.  Otherwise the bin is narrowed by the
-// bits of its values until its end is one token, the kept mass of every part
-// is known, and only the part in which the draw falls is walked.
+// gathered into LDS.  A filter's last token is found by narrowing an interval of
+// (value, number) by 256 at a time, over the list or over the row; no sort.  The
+// draw goes by parts, blocks of 64 tokens and tokens, or, where the kept tokens
+// are many, by the parts' histograms and one part of the row.
 //
 // Weights are exact to 2^-40 (FP64, which runs at the rate of FP32 here) and
 // masses are 64-bit whole numbers, so that sums have no order: LDS atomics may come as
@@ -28,11 +29,15 @@ namespace lowbit {
 namespace {
 
 constexpr int kPart = 4096;      // logits of a part
-constexpr int kPartThreads = 256;
+constexpr int kBlock = 512;      // logits of a block: eight a lane
+constexpr int kBlocks = kPart / kBlock;
+constexpr int kPartThreads = 64 * kBlocks;
 constexpr int kBins = 256;       // quarters of an octave; the last one: everything below
 constexpr int kRowThreads = 1024;
 constexpr int kMostParts = 256;
-constexpr int kList = 2048;      // tokens that are sorted in LDS
+constexpr int kAhead = 4;        // blocks that a wave loads ahead
+constexpr int kList = 2048;      // tokens that are held in LDS
+constexpr int kMostK = 1024;     // up to which top-k rows go without the parts' masses
 constexpr int kUnit = 51;        // a part's weights are whole numbers of 2^-51: 4096 of them stay below 2^64
 
 // Order of values as whole numbers: NaN above all, both zeros alike
@@ -76,11 +81,17 @@ __device__ __forceinline__ float temperature_of(const SampleArgs& a, int64_t row
   return t >= 0x1p-20f ? t : 0.0f;
 }
 __device__ __forceinline__ double octaves(float t) { return 1.4426950408889634074 / (double)t; }
+// A value in octaves, c of them to one.  Rounded before a base is taken off: bases are rounded
+// likewise, and at 1e38 an exact product less a rounded one is no small number.
+__device__ __forceinline__ double in_octaves(float y, double c) {
+#pragma clang fp contract(off)
+  return (double)y * c;
+}
 
 // what the first launch leaves of a part
 struct Parts {
   double* base;      // [rows][parts]: weights are relative to 2^base
-  uint32_t* top;     // [rows][parts]: the largest key
+  uint32_t* top;     // [rows][parts][kPart / kBlock]: the largest key of a block
   uint64_t* mass;    // [rows][parts][kBins]
   uint16_t* count;   // [rows][parts][kBins]
 };
@@ -88,7 +99,7 @@ __host__ __device__ inline size_t align_up(size_t v) { return (v + 255) / 256 * 
 inline size_t parts_layout(int64_t rows, int64_t parts, void* ws, Parts* p) {
   char* at = static_cast<char*>(ws);
   const size_t n = (size_t)(rows * parts);
-  const size_t mass = align_up(n * kBins * 8), count = align_up(n * kBins * 2), base = align_up(n * 8), top = align_up(n * 4);
+  const size_t mass = align_up(n * kBins * 8), count = align_up(n * kBins * 2), base = align_up(n * 8), top = align_up(n * kBlocks * 4);
   if (p) {
     p->mass = reinterpret_cast<uint64_t*>(at);
     p->count = reinterpret_cast<uint16_t*>(at + mass);
@@ -122,100 +133,117 @@ __device__ __forceinline__ void load_logits(const void* y, int type, int64_t at,
   }
 }
 
+// Whether a row's filters are likely to need the masses of the histograms: with
+// few tokens by top-k the kept ones are weighed one by one
+__device__ __forceinline__ int64_t top_k_of(const SampleArgs& a, int64_t row) {
+  const int64_t k = a.top_k ? a.top_k[row] : 0;
+  return k <= 0 || k > a.n ? a.n : k;
+}
+__device__ __forceinline__ bool without_mass(const SampleArgs& a, int64_t k) { return k < a.n && k <= kMostK; }
+
 template <int S>
 __global__ __launch_bounds__(kPartThreads) void sample_parts_kernel(SampleArgs a, Parts out) {
   __shared__ unsigned long long mass[kBins];
   __shared__ uint32_t count[kBins];
-  __shared__ uint32_t top4[4];
+  __shared__ uint32_t tops[kBlocks];
   const int64_t row = blockIdx.y, part = blockIdx.x, slot = row * gridDim.x + part;
-  const int64_t from = part * kPart;
   const int t = threadIdx.x;
-  mass[t] = 0;
-  count[t] = 0;
-  float v[2][8];
+  const int64_t at = part * kPart + t * 8;
+  float v[8];
+  load_logits<S>(a.y, a.y_type, row * a.ldy + at, a.n - at, v);
+  const float temp = temperature_of(a, row);
+  const bool only_count = without_mass(a, top_k_of(a, row));
+  if (t < kBins) {
+    mass[t] = 0;
+    count[t] = 0;
+  }
   uint32_t top = kKeyNegInf;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int64_t at = from + (h * kPartThreads + t) * 8;
-    load_logits<S>(a.y, a.y_type, row * a.ldy + at, a.n - at, v[h]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) top = max(top, key_of(v[h][j]));
-  }
+  for (int j = 0; j < 8; ++j) top = max(top, key_of(v[j]));
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
-  if ((t & 63) == 0) top4[t >> 6] = top;
+  if ((t & 63) == 0) {
+    tops[t >> 6] = top;
+    out.top[slot * kBlocks + (t >> 6)] = top;
+  }
   __syncthreads();
-  top = max(max(top4[0], top4[1]), max(top4[2], top4[3]));
-  const float temp = temperature_of(a, row);
+#pragma unroll
+  for (int w = 0; w < kBlocks; ++w) top = max(top, tops[w]);
   // greedy rows, and rows with NaN or infinity, go by the maximum alone
   const bool plain = temp != 0.0f && top < kKeyInf && top > kKeyNegInf;
   const double c = plain ? octaves(temp) : 0.0;
-  const double base = plain ? __builtin_ceil((double)value_of(top) * c) : -1e300;
+  const double base = plain ? __builtin_ceil(in_octaves(value_of(top), c)) : -1e300;
   if (plain) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const double v2 = (double)v[h][j] * c;
-        const int bin = bin_of(quarter(v2), base);
-        if (bin < kBins - 1) {  // what is below counts nothing, and is counted from the others
-          atomicAdd(&count[bin], 1u);
-          atomicAdd(&mass[bin], (unsigned long long)fixed_of(exp2_of(v2 - base)));
-        }
+    for (int j = 0; j < 8; ++j) {
+      const double v2 = in_octaves(v[j], c);
+      const int bin = bin_of(quarter(v2), base);
+      if (bin < kBins - 1) {  // what is below counts nothing, and is counted from the others
+        atomicAdd(&count[bin], 1u);
+        if (!only_count) atomicAdd(&mass[bin], (unsigned long long)fixed_of(exp2_of(v2 - base)));
       }
+    }
   }
   __syncthreads();
-  out.mass[slot * kBins + t] = mass[t];
-  out.count[slot * kBins + t] = (uint16_t)count[t];
-  if (t == 0) {
-    out.base[slot] = base;
-    out.top[slot] = top;
+  if (t < kBins) {
+    out.mass[slot * kBins + t] = mass[t];
+    out.count[slot * kBins + t] = (uint16_t)count[t];
   }
+  if (t == 0) out.base[slot] = base;
 }
 
 // ---------------------------------------------------------------------------
 // one work-group a row
 
-__device__ __forceinline__ uint64_t shfl_up64(uint64_t v, int d) { return (uint64_t)__shfl_up((unsigned long long)v, d); }
-
-// Sum of v over the threads before this one; *total: over all (1024 threads).
-__device__ __forceinline__ uint64_t scan64(uint64_t v, uint64_t* red, uint64_t* total) {
-  const int t = threadIdx.x;
-  uint64_t s = v;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint64_t o = shfl_up64(s, d);
-    if ((t & 63) >= d) s += o;
-  }
-  __syncthreads();
-  if ((t & 63) == 63) red[t >> 6] = s;
-  __syncthreads();
-  uint64_t before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < kRowThreads / 64; ++w) {
-    if (w < (t >> 6)) before += red[w];
-    all += red[w];
-  }
-  *total = all;
-  return before + s - v;
+// The lanes' sums up to and with each, by DPP (no LDS round trips)
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint64_t dpp_add64(uint64_t v) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, CTRL, ROWS, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), CTRL, ROWS, 0xF, false);
+  return v + (((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ uint64_t wave_scan64(uint64_t v) {
+  v = dpp_add64<0x111, 0xF>(v);  // row_shr:1
+  v = dpp_add64<0x112, 0xF>(v);
+  v = dpp_add64<0x114, 0xF>(v);
+  v = dpp_add64<0x118, 0xF>(v);
+  v = dpp_add64<0x142, 0xA>(v);  // row_bcast:15 into rows 1 and 3
+  v = dpp_add64<0x143, 0xC>(v);  // row_bcast:31 into rows 2 and 3
+  return v;
 }
 
-// Descending (or ascending) order of size = a power of two entries in LDS
-template <typename T, bool DESCENDING>
-__device__ __forceinline__ void sort_lds(T* v, int size) {
-  for (int k = 2; k <= size; k <<= 1)
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      for (int i = threadIdx.x; i < size / 2; i += kRowThreads) {
-        const int lo = 2 * j * (i / j) + i % j, hi = lo + j;
-        const bool up = ((lo & k) == 0) != DESCENDING;
-        const T x = v[lo], y = v[hi];
-        if ((x > y) == up) {
-          v[lo] = y;
-          v[hi] = x;
-        }
-      }
-      __syncthreads();
+// Sums of v over the threads before this one; total: over all (1024 threads).
+template <int N>
+__device__ __forceinline__ void scan64(const uint64_t (&v)[N], uint64_t (&before)[N], uint64_t (&total)[N],
+                                       uint64_t (*red)[16]) {
+  const int t = threadIdx.x;
+  uint64_t sum[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n) sum[n] = wave_scan64(v[n]);
+  __syncthreads();
+  if ((t & 63) == 63)
+#pragma unroll
+    for (int n = 0; n < N; ++n) red[n][t >> 6] = sum[n];
+  __syncthreads();
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    uint64_t b = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kRowThreads / 64; ++w) {
+      const uint64_t r = red[n][w];
+      if (w < (t >> 6)) b += r;
+      all += r;
     }
+    before[n] = b + sum[n] - v[n];
+    total[n] = all;
+  }
+}
+__device__ __forceinline__ uint64_t scan64(uint64_t v, uint64_t (*red)[16], uint64_t* total) {
+  const uint64_t in[1] = {v};
+  uint64_t before[1], all[1];
+  scan64<1>(in, before, all, red);
+  *total = all[0];
+  return before[0];
 }
 
 // A token's place in the order: value first, then its number
@@ -225,35 +253,103 @@ __device__ __forceinline__ uint64_t place_of(uint32_t key, int token) {
 
 struct RowShared {
   double base[kMostParts];          // of the parts
-  uint64_t kept[kMostParts];        // mass of a part's kept tokens, in its own unit
+  uint32_t top[kMostParts * kBlocks];  // of their blocks
+  uint16_t todo[kMostParts * kBlocks];  // blocks to walk over
   int down[kMostParts];             // octaves from the row's base down to the part's
-  unsigned long long mass[kBins];   // in the row's unit
+  unsigned long long kept[kMostParts];  // mass of a part's kept tokens
+  unsigned long long mass[kBins];   // in the row's unit, up to and with the bin
   uint32_t count[kBins];
-  uint64_t red[16];
-  uint64_t list[kList], weight[kList];
-  uint32_t order[kList];
-  uint32_t fill;
-  uint32_t found;
-  uint64_t found64;
+  unsigned long long sub_mass[kBins];
+  uint32_t sub_count[kBins];
+  uint64_t red[2][16];
+  uint64_t list[kList], few[64], few_mass[64];
+  uint64_t out[4];
+  uint32_t fill, found, walk;
   int pick;
 };
 
-// Calls f(part, token, value) for the tokens of the parts that use(part) names
-template <int S, class U, class F>
-__device__ __forceinline__ void walk_row(const SampleArgs& a, int64_t row, int parts, U use, F f) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int p = wave; p < parts; p += kRowThreads / 64) {
-    if (!use(p)) continue;
-    for (int i = 0; i < kPart / 512; ++i) {
-      const int64_t at = (int64_t)p * kPart + i * 512 + lane * 8;
-      if (at >= a.n) break;
-      float v[8];
-      load_logits<S>(a.y, a.y_type, row * a.ldy + at, a.n - at, v);
+template <int S>
+__device__ __forceinline__ float one_logit(const SampleArgs& a, int64_t row, int64_t at) {
+  const int64_t o = row * a.ldy + at;
+  if constexpr (S == 4) return static_cast<const float*>(a.y)[o];
+  else if (a.y_type == 2) return (float)static_cast<const _Float16*>(a.y)[o];
+  else return (float)static_cast<const bf16_t*>(a.y)[o];
+}
+
+// which of eight values from `at` on are tokens of the row with lo <= value < hi (a NaN hi:
+// all from lo on)
+__device__ __forceinline__ uint32_t hits_of(const float (&v)[8], float lo, float hi, int64_t left) {
+  uint32_t hits = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (at + j < a.n) f(p, (int)at + j, v[j]);
+  for (int j = 0; j < 8; ++j) hits |= v[j] >= lo && !(v[j] >= hi) && j < left ? 1u << j : 0;
+  return hits;
+}
+__device__ __forceinline__ float pick(const float (&v)[8], int j) {
+  const float a = j & 1 ? v[1] : v[0], b = j & 1 ? v[3] : v[2], c = j & 1 ? v[5] : v[4], d = j & 1 ? v[7] : v[6];
+  const float e = j & 2 ? b : a, f = j & 2 ? d : c;
+  return j & 4 ? f : e;
+}
+
+// Calls f(from, values) for the blocks that have values of lo and above; a lane has eight
+// values, from `from` on
+template <int S, class F>
+__device__ __forceinline__ void walk_blocks(const SampleArgs& a, int64_t row, int blocks, RowShared& s, float lo, F f) {
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const uint32_t least = key_of(lo);
+  if (t == 0) s.walk = 0;
+  __syncthreads();
+  for (int b = t; b < blocks; b += kRowThreads)
+    if (s.top[b] >= least) s.todo[atomicAdd(&s.walk, 1u)] = (uint16_t)b;
+  __syncthreads();
+  const int n = (int)s.walk;
+#pragma unroll 1
+  for (int i = wave; i < n; i += kRowThreads / 64 * kAhead) {
+    float v[kAhead][8];
+    int64_t from[kAhead];
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) {
+      const int k = i + e * (kRowThreads / 64);
+      from[e] = k < n ? (int64_t)s.todo[k] * kBlock + lane * 8 : a.n;
+      load_logits<S>(a.y, a.y_type, row * a.ldy + from[e], a.n - from[e], v[e]);
     }
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) f(from[e], v[e]);
   }
+}
+
+// Calls f(token, value) for the tokens with lo <= value < hi
+template <int S, class F>
+__device__ __forceinline__ void walk_row(const SampleArgs& a, int64_t row, int blocks, RowShared& s, float lo, float hi,
+                                         F f) {
+  walk_blocks<S>(a, row, blocks, s, lo, [&](int64_t from, float (&v)[8]) {
+    for (uint32_t hits = hits_of(v, lo, hi, a.n - from); hits; hits &= hits - 1) {
+      const int j = __builtin_ctz(hits);
+      f((int)from + j, pick(v, j));
+    }
+  });
+}
+
+// The places of those tokens into s.list, which has room for kList; returns their number
+template <int S>
+__device__ __forceinline__ int gather_row(const SampleArgs& a, int64_t row, int blocks, RowShared& s, float lo,
+                                          float hi) {
+  if (threadIdx.x == 0) s.fill = 0;
+  walk_blocks<S>(a, row, blocks, s, lo, [&](int64_t from, float (&v)[8]) {
+    uint32_t hits = hits_of(v, lo, hi, a.n - from);
+    // one atomic a wave and block
+    const uint32_t mine = __builtin_popcount(hits), before = (uint32_t)wave_scan64(mine) - mine;
+    const uint32_t all = (uint32_t)__builtin_amdgcn_readlane((int)(before + mine), 63);
+    if (all == 0) return;
+    uint32_t at = 0;
+    if ((threadIdx.x & 63) == 0) at = atomicAdd(&s.fill, all);
+    at = (uint32_t)__builtin_amdgcn_readfirstlane((int)at) + before;
+    for (; hits; hits &= hits - 1, ++at) {
+      const int j = __builtin_ctz(hits);
+      if (at < kList) s.list[at] = place_of(key_of(pick(v, j)), (int)from + j);
+    }
+  });
+  __syncthreads();
+  return (int)s.fill < kList ? (int)s.fill : kList;
 }
 
 // u in [0, 1) of w, rounded down
@@ -262,43 +358,49 @@ __device__ __forceinline__ uint64_t share_of(uint64_t w, float u) {
   return __umul64hi(w, (uint64_t)((double)x * 0x1p64));
 }
 
-// The last token that a filter keeps: `place` within `bin`.  Tokens up to and with
-// it have the mass `mass` and the number `count`.
-struct Cut {
-  int bin;
-  uint64_t place, mass;
-};
-
 template <int S>
 __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, Parts in, int parts, int unit) {
   __shared__ RowShared s;
   const int64_t row = blockIdx.x;
-  const int t = threadIdx.x;
-  const uint32_t* tops = in.top + row * parts;
-  const double* bases = in.base + row * parts;
+  const int t = threadIdx.x, lane = t & 63;
 
-  // the row's maximum and base
+  // the parts' maxima and bases, and the row's
+  const float temp = temperature_of(a, row);
+  const int64_t k = top_k_of(a, row);
+  const float top_p = a.top_p ? a.top_p[row] : 1.0f, min_p = a.min_p ? a.min_p[row] : 0.0f, u = a.u[row];
+  const int blocks = parts * kBlocks;
+  for (int b = t; b < blocks; b += kRowThreads) s.top[b] = in.top[row * blocks + b];
+  for (int p = t; p < parts; p += kRowThreads) {
+    s.base[p] = in.base[row * parts + p];
+    s.kept[p] = 0;
+  }
+  if (t < kBins) {
+    s.mass[t] = 0;
+    s.count[t] = 0;
+  }
+  if (t == 0) s.found = 0xFFFFFFFFu;
+  __syncthreads();
   uint32_t top = kKeyNegInf;
   double base = -1e300;
-  for (int p = t & 63; p < parts; p += 64) {
-    top = max(top, tops[p]);
-    base = fmax(base, bases[p]);
-  }
+  for (int b = lane; b < blocks; b += 64) top = max(top, s.top[b]);
+  for (int p = lane; p < parts; p += 64) base = fmax(base, s.base[p]);
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     top = max(top, (uint32_t)__shfl_xor((int)top, d));
     base = fmax(base, __shfl_xor(base, d));
   }
-  const float temp = temperature_of(a, row);
   if (temp == 0.0f || top >= kKeyInf || top == kKeyNegInf) {
     // the lowest token of the largest value
-    if (t == 0) s.found = 0xFFFFFFFFu;
-    __syncthreads();
-    if (top != kKeyNegInf)
-      walk_row<S>(a, row, parts, [&](int p) { return tops[p] == top; },
-                  [&](int, int token, float y) {
-                    if (key_of(y) == top) atomicMin(&s.found, (uint32_t)token);
-                  });
+    if (top == 0xFFFFFFFFu) {  // NaN, which no comparison finds
+      for (int b = t >> 6; b < blocks; b += kRowThreads / 64) {
+        if (s.top[b] != top) continue;
+        for (int64_t at = (int64_t)b * kBlock + lane; at < (int64_t)(b + 1) * kBlock && at < a.n; at += 64)
+          if (key_of(one_logit<S>(a, row, at)) == top) atomicMin(&s.found, (uint32_t)at);
+      }
+    } else if (top != kKeyNegInf) {
+      walk_row<S>(a, row, blocks, s, value_of(top), __builtin_nanf(""),
+                  [&](int token, float) { atomicMin(&s.found, (uint32_t)token); });
+    }
     __syncthreads();
     if (t == 0) {
       a.idx[row] = (int32_t)s.found;
@@ -309,394 +411,346 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
 
   const double c = octaves(temp);
   const int up = kUnit - unit;  // from the row's unit to a part's, at the same base
+  // a token's weight in the unit of its part, and a part's mass in the row's
+  auto weigh = [&](int p, float y) { return fixed_of(exp2_of(in_octaves(y, c) - s.base[p])); };
+  auto to_row = [&](int p, uint64_t w) { return s.down[p] + up < 64 ? w >> (s.down[p] + up) : 0; };
+  // of a place in the list
+  auto token_of = [](uint64_t place) { return (int)~(uint32_t)place; };
+  auto logit_of = [](uint64_t place) { return value_of((uint32_t)(place >> 32)); };
+  auto mass_of = [&](uint64_t place) {
+    const int p = token_of(place) / kPart;
+    return to_row(p, weigh(p, logit_of(place)));
+  };
   for (int p = t; p < parts; p += kRowThreads) {
-    const double d = base - bases[p];
-    s.base[p] = bases[p];
+    const double d = base - s.base[p];
     s.down[p] = d < 1000.0 ? (int)d : 1000;
-  }
-  if (t < kBins) {
-    s.mass[t] = 0;
-    s.count[t] = 0;
   }
   __syncthreads();
   // the row's histogram: four threads a bin
-  {
+  auto add_parts = [&](bool counts) {
     const int r = t & (kBins - 1);
     uint64_t m = 0;
     uint32_t n = 0;
     if (r < kBins - 1)
+#pragma unroll 10
       for (int p = t / kBins; p < parts; p += kRowThreads / kBins) {
-        const int j = r - 4 * s.down[p];
-        if (j < 0) continue;
-        const int64_t at = (row * parts + p) * kBins + j;
-        m += s.down[p] + up < 64 ? in.mass[at] >> (s.down[p] + up) : 0;
-        n += in.count[at];
+        const int down = s.down[p], j = r - 4 * down;
+        const int64_t at = (row * parts + p) * kBins + max(j, 0);
+        const uint64_t pm = in.mass[at];
+        const uint32_t pn = in.count[at];
+        m += j >= 0 && down + up < 64 ? pm >> ((down + up) & 63) : 0;
+        n += j >= 0 ? pn : 0;
       }
-    if (n) atomicAdd(&s.count[r], n);
+    if (n && counts) atomicAdd(&s.count[r], n);
     if (m) atomicAdd(&s.mass[r], (unsigned long long)m);
-  }
+  };
+  add_parts(true);
   __syncthreads();
   // sums up to and with each bin (the last bin has the rest of the tokens, and no mass)
-  uint64_t all_mass;
-  {
-    const uint64_t m = t < kBins ? s.mass[t] : 0, n = t < kBins ? s.count[t] : 0;
-    const uint64_t bm = scan64(m, s.red, &all_mass);
-    uint64_t dummy;
-    const uint64_t bn = scan64(n, s.red, &dummy);
-    __syncthreads();
+  uint64_t full;
+  auto add_bins = [&](bool counts) {
+    const uint64_t mn[2] = {t < kBins ? s.mass[t] : 0, t < kBins ? s.count[t] : 0};
+    uint64_t before[2], total[2];
+    scan64<2>(mn, before, total, s.red);
+    full = total[0];
     if (t < kBins) {
-      s.mass[t] = bm + m;
-      s.count[t] = t == kBins - 1 ? (uint32_t)a.n : (uint32_t)(bn + n);
+      s.mass[t] = before[0] + mn[0];
+      if (counts) s.count[t] = t == kBins - 1 ? (uint32_t)a.n : (uint32_t)(before[1] + mn[1]);
     }
     __syncthreads();
-  }
-  const uint64_t full = all_mass;
+  };
+  add_bins(true);
 
-  int64_t k = a.top_k ? a.top_k[row] : 0;
-  if (k <= 0 || k > a.n) k = a.n;
-  const float top_p = a.top_p ? a.top_p[row] : 1.0f;
-  const bool by_p = top_p < 1.0f;
-  const float min_p = a.min_p ? a.min_p[row] : 0.0f;
-  const bool by_min = min_p > 0.0f;
-  const double v2_top = (double)value_of(top) * c;
+  const bool by_k = k < a.n, by_p = top_p < 1.0f, by_min = min_p > 0.0f;
+  const double v2_top = in_octaves(value_of(top), c);
   const double least = by_min ? v2_top + log2((double)fminf(min_p, 1.0f)) : -1e308;  // of v2
   const int bin_min = by_min ? bin_of(quarter(least), base) : kBins - 1;
 
+  // the smallest value that lies in `bin` or above; all values are in the last bin or above
+  auto lowest = [&](int bin) {
+    if (bin >= kBins - 1) return -INFINITY;
+    if (bin < 0) return INFINITY;
+    const double least2 = (base * 4.0 - 1.0 - bin) * 0.25;  // of v2
+    const double guess = fmin(fmax(least2 / c, -3.4028234e38), 3.4028234e38);
+    uint32_t key = key_of((float)guess);
+    while (key < kKeyInf - 1 && !(in_octaves(value_of(key), c) >= least2)) ++key;
+    while (key > kKeyNegInf + 1 && in_octaves(value_of(key - 1), c) >= least2) --key;
+    return value_of(key);
+  };
   // first bin at which a sum (which never falls) reaches what is wanted, or the last
   auto first_bin = [&](auto reaches) {
-    __syncthreads();
     if (t == 0) s.pick = kBins - 1;
     __syncthreads();
     if (t < kBins - 1 && reaches(t) && (t == 0 || !reaches(t - 1))) s.pick = t;
     __syncthreads();
-    return s.pick;
+    const int bin = s.pick;
+    __syncthreads();
+    return bin;
   };
   auto bin_at_count = [&](uint64_t want) { return first_bin([&](int b) { return s.count[b] >= want; }); };
   auto bin_at_mass = [&](uint64_t want) { return first_bin([&](int b) { return s.mass[b] >= want; }); };
   // kept: a token with less mass before it than this, top-p's share of w rounded up
   auto mass_wanted = [&](uint64_t w) {
     const uint64_t p = top_p > 0.0f ? (uint64_t)((double)top_p * 0x1p64) : 0;
-    return max((uint64_t)1, __umul64hi(w, p) + (w * p != 0 ? 1 : 0));
+    const uint64_t want = (uint64_t)__umul64hi(w, p) + (w * p != 0 ? 1 : 0);
+    return want ? want : 1;
   };
 
-  int bin_k = kBins - 1, bin_last = kBins - 1;
-  if (k < a.n) bin_k = bin_last = bin_at_count((uint64_t)k);
-  if (by_p && k == a.n) bin_last = bin_at_mass(mass_wanted(full));
-  if (!by_p || k == a.n) bin_last = min(bin_last, bin_min);
-
-  if (s.count[bin_last] <= kList) {
-    // few tokens: in LDS
-    if (t == 0) s.fill = 0;
+  int bin_last = kBins - 1;
+  if (by_k) bin_last = bin_at_count((uint64_t)k);
+  if (by_p && !by_k) bin_last = bin_at_mass(mass_wanted(full));
+  if (!by_p || !by_k) bin_last = min(bin_last, bin_min);
+  // few tokens: in LDS
+  const bool few = s.count[bin_last] <= kList;
+  int have = 0;
+  if (few) {
+    have = gather_row<S>(a, row, blocks, s, lowest(bin_last), INFINITY);
+  } else if (without_mass(a, k)) {
+    // very many tokens at the end of a small top-k (they share one value, or nearly):
+    // the masses that the first launch left out
+    walk_row<S>(a, row, blocks, s, lowest(bin_last), INFINITY, [&](int token, float y) {
+      const int p = token / kPart, bin = bin_of(quarter(in_octaves(y, c)), s.base[p]);
+      atomicAdd(reinterpret_cast<unsigned long long*>(&in.mass[(row * parts + p) * kBins + bin]),
+                (unsigned long long)weigh(p, y));
+    });
+    __threadfence();
     __syncthreads();
-    walk_row<S>(a, row, parts, [&](int p) { return bin_of(quarter((double)value_of(tops[p]) * c), base) <= bin_last; },
-                [&](int, int token, float y) {
-                  if (bin_of(quarter((double)y * c), base) <= bin_last) {
-                    const uint32_t at = atomicAdd(&s.fill, 1u);
-                    if (at < kList) s.list[at] = place_of(key_of(y), token);
-                  }
-                });
+    if (t < kBins) s.mass[t] = 0;
     __syncthreads();
-    const int have = min((int)s.fill, kList);
-    int size = 2;
-    while (size < have) size <<= 1;
-    for (int i = have + t; i < size; i += kRowThreads) s.list[i] = 0;
+    add_parts(false);
     __syncthreads();
-    sort_lds<uint64_t, true>(s.list, size);
-    // two neighbours a thread, weights in units of 2^-51 of the row's base
-    uint64_t w[2], sum = 0, before, ignored;
-    double v2[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int i = 2 * t + e;
-      v2[e] = i < have ? (double)value_of((uint32_t)(s.list[i] >> 32)) * c : -1e308;
-      w[e] = i < have && i < k ? fixed_of(exp2_of(v2[e] - base)) : 0;
-      sum += w[e];
-    }
-    uint64_t total;
-    before = scan64(sum, s.red, &total);
-    uint64_t want = mass_wanted(k < a.n ? total : full);
-    if (k == a.n) want = want >> (63 - up) ? UINT64_MAX : want << up;
-    uint64_t kept_sum = 0;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int i = 2 * t + e;
-      const bool keep = i < have && i < k && (i == 0 || ((!by_p || before < want) && (!by_min || v2[e] >= least)));
-      before += w[e];
-      if (!keep) w[e] = 0;
-      kept_sum += w[e];
-      if (i < kList) {
-        s.weight[i] = w[e];
-        // by number: those that are not kept weigh nothing wherever they are
-        if (i < size) s.order[i] = i < have ? ((~(uint32_t)s.list[i]) << 11) | (uint32_t)i : 0xFFFFFFFFu;
-      }
-    }
-    uint64_t kept;
-    scan64(kept_sum, s.red, &kept);
-    __syncthreads();
-    sort_lds<uint32_t, false>(s.order, size);
-    uint64_t x[2] = {0, 0};
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int i = 2 * t + e;
-      if (i < have) x[e] = s.weight[s.order[i] & 2047u];
-    }
-    uint64_t at = scan64(x[0] + x[1], s.red, &ignored);
-    const uint64_t target = share_of(kept, a.u[row]);
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int i = 2 * t + e;
-      if (i < have && target >= at && target < at + x[e]) {
-        a.idx[row] = (int32_t)(s.order[i] >> 11);
-        if (a.prob) a.prob[row] = (float)((double)x[e] / (double)kept);
-      }
-      at += x[e];
-    }
-    return;
+    add_bins(false);
   }
 
-  // many tokens: the place of the last kept one
-  auto in_bin = [&](int bin, float y) { return bin_of(quarter((double)y * c), base) == bin; };
-  auto part_has = [&](int bin, int p) {
-    const int j = bin - 4 * s.down[p];
-    return j >= 0 && in.count[(row * parts + p) * kBins + j] != 0;
-  };
-  // a token's weight in the unit of its part
-  auto weigh = [&](int p, float y) { return fixed_of(exp2_of((double)y * c - s.base[p])); };
-  auto to_row = [&](int p, uint64_t w) { return s.down[p] + up < 64 ? w >> (s.down[p] + up) : 0; };
-  // by_count: the want-th token in order; else the first at which the mass reaches want
-  auto cut_at = [&](bool by_count, uint64_t want) {
-    Cut r;
-    r.bin = by_count ? bin_at_count(want) : bin_at_mass(want);
-    if (r.bin == kBins - 1) {  // only what weighs nothing is cut off
-      r.place = 0;
-      r.mass = full;
-      return r;
+  // Places of the last tokens that top-k and top-p keep, the earlier of them in `cut` (0:
+  // everything that weighs), and the mass of what is kept.
+  uint64_t cut = 0, mass = full;
+#pragma unroll 1
+  for (int filter = 0; filter < 2; ++filter) {
+    const bool by_count = filter == 0;
+    if (!(by_count ? by_k : by_p)) continue;
+    if (few && by_count && k >= have) {  // all of the list; of its bin, others may be there that weigh nothing
+      uint64_t sum = 0;
+      for (int i = t; i < have; i += kRowThreads) sum += mass_of(s.list[i]);
+      scan64(sum, s.red, &mass);
+      continue;
     }
-    uint64_t n_before = r.bin ? s.count[r.bin - 1] : 0, m_before = r.bin ? s.mass[r.bin - 1] : 0;
-    uint32_t hi = 0xFFFFFFFFu, lo = 0;  // keys of the bin
-    {
-      // the values of the bin, and a little more on both sides
-      const double q = base * 4.0 - 1.0 - r.bin;
-      lo = key_of((float)(q * 0.25 / c));
-      if (r.bin > 0) hi = key_of((float)((q + 1.0) * 0.25 / c));
-      lo = lo > 4 ? lo - 4 : 0;
-      hi = hi < 0xFFFFFFFBu ? hi + 4 : 0xFFFFFFFFu;
+    const uint64_t want = by_count ? (uint64_t)k : mass_wanted(mass);
+    // the interval of places from lo to hi, and the tokens there and before it
+    int bin = bin_last;
+    uint64_t inside = have, n_before = 0, m_before = 0;
+    if (!few) {
+      bin = by_count ? bin_at_count(want) : bin_at_mass(want);
+      if (bin == kBins - 1) continue;  // only what weighs nothing is cut off
+      n_before = bin ? s.count[bin - 1] : 0;
+      m_before = bin ? s.mass[bin - 1] : 0;
+      inside = s.count[bin] - n_before;
+      if (inside <= kList) have = gather_row<S>(a, row, blocks, s, lowest(bin), lowest(bin - 1));
     }
-    uint64_t inside = s.count[r.bin] - n_before;
-    unsigned long long* sub_mass = reinterpret_cast<unsigned long long*>(s.weight);
-    uint32_t* sub_count = s.order;
-    while (inside > kList && hi > lo) {
+    const bool in_list = inside <= kList;
+    uint64_t lo = (uint64_t)key_of(lowest(bin)) << 32;
+    uint64_t hi = ((uint64_t)(few ? top : key_of(lowest(bin - 1)) - 1) << 32) | 0xFFFFFFFFu;
+    // narrower by 256 at a time, until a wave can order the few that are left
+    while (true) {
+      const bool order = inside <= 64;
+      // numbers go no further than n; where the key is known, they alone differ
+      if ((lo >> 32) == (hi >> 32)) {
+        const uint64_t last_place = place_of((uint32_t)(hi >> 32), (int)(a.n - 1));
+        lo = lo > last_place ? lo : last_place;
+      }
       int shift = 0;
       while (((hi - lo) >> shift) >= kBins) ++shift;
       __syncthreads();
       if (t < kBins) {
-        sub_mass[t] = 0;
-        sub_count[t] = 0;
+        s.sub_mass[t] = 0;
+        s.sub_count[t] = 0;
       }
-      __syncthreads();
-      walk_row<S>(a, row, parts, [&](int p) { return part_has(r.bin, p); },
-                  [&](int p, int, float y) {
-                    const uint32_t key = key_of(y);
-                    if (key > hi || key < lo || !in_bin(r.bin, y)) return;
-                    const uint32_t j = (hi - key) >> shift;
-                    atomicAdd(&sub_count[j], 1u);
-                    atomicAdd(&sub_mass[j], (unsigned long long)to_row(p, weigh(p, y)));
-                  });
-      __syncthreads();
-      // the first that reaches it, or the last that has any
-      uint64_t ignored;
-      const uint64_t n0 = t < kBins ? sub_count[t] : 0, m0 = t < kBins ? sub_mass[t] : 0;
-      const uint64_t n = n_before + scan64(n0, s.red, &ignored), m = m_before + scan64(m0, s.red, &ignored);
       if (t == 0) {
         s.found = 0xFFFFFFFFu;
+        s.pick = 0;
         s.fill = 0;
       }
       __syncthreads();
-      if (n0 && (by_count ? n + n0 >= want : m + m0 >= want)) atomicMin(&s.found, (uint32_t)t);
-      if (n0) atomicMax(&s.fill, (uint32_t)t);
-      __syncthreads();
-      const uint32_t found = s.found != 0xFFFFFFFFu ? s.found : s.fill;
-      if (t == (int)found) {
-        s.red[0] = n0;
-        s.red[1] = n;
-        s.red[2] = m;
-      }
-      __syncthreads();
-      inside = s.red[0];
-      n_before = s.red[1];
-      m_before = s.red[2];
-      const uint32_t top_key = hi - (found << shift);
-      const uint32_t span = ((uint32_t)1 << shift) - 1;
-      lo = top_key - lo > span ? top_key - span : lo;
-      hi = top_key;
-    }
-    __syncthreads();
-    if (inside <= kList) {
-      if (t == 0) {
-        s.fill = 0;
-        s.found = 0xFFFFFFFFu;
-      }
-      __syncthreads();
-      walk_row<S>(a, row, parts, [&](int p) { return part_has(r.bin, p); },
-                  [&](int, int token, float y) {
-                    const uint32_t key = key_of(y);
-                    if (key > hi || key < lo || !in_bin(r.bin, y)) return;
-                    const uint32_t at = atomicAdd(&s.fill, 1u);
-                    if (at < kList) s.list[at] = place_of(key, token);
-                  });
-      __syncthreads();
-      const int have = min((int)s.fill, kList);
-      int size = 2;
-      while (size < have) size <<= 1;
-      for (int i = have + t; i < size; i += kRowThreads) s.list[i] = 0;
-      __syncthreads();
-      sort_lds<uint64_t, true>(s.list, size);
-      uint64_t w[2], total;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int i = 2 * t + e;
-        w[e] = 0;
-        if (i < have) {
-          const int token = (int)~(uint32_t)s.list[i];
-          w[e] = to_row(token / kPart, weigh(token / kPart, value_of((uint32_t)(s.list[i] >> 32))));
-        }
-      }
-      uint64_t m = m_before + scan64(w[0] + w[1], s.red, &total);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int i = 2 * t + e;
-        m += w[e];
-        if (i < have && (by_count ? n_before + i + 1 >= want : m >= want)) atomicMin(&s.found, (uint32_t)i);
-        if (i < have) s.weight[i] = m;
-      }
-      __syncthreads();
-      const int at = s.found != 0xFFFFFFFFu ? (int)s.found : have - 1;
-      r.place = s.list[at];
-      r.mass = s.weight[at];
-    } else {
-      // one value that very many tokens have: the one of them that is wanted, by number
-      if (t < kMostParts) s.order[t] = 0;
-      __syncthreads();
-      walk_row<S>(a, row, parts, [&](int p) { return part_has(r.bin, p); },
-                  [&](int p, int, float y) {
-                    if (key_of(y) == hi) atomicAdd(&s.order[p], 1u);
-                  });
-      __syncthreads();
-      uint64_t left = by_count ? want - n_before : 0, m = m_before;
-      int part = 0;
-      uint32_t nth = 0;  // from 0, within the part
-      for (int p = 0; p < parts; ++p) {
-        const uint32_t n = s.order[p];
-        if (n == 0) continue;
-        const uint64_t w = to_row(p, weigh(p, value_of(hi)));
-        part = p;
-        if (by_count) {
-          nth = (uint32_t)(left < n ? left : n) - 1;
-          if (left <= n) {
-            m += w * (nth + 1);
-            break;
+      auto add = [&](uint64_t place) {
+        if (place < lo || place > hi) return;
+        const uint64_t w = mass_of(place);
+        if (order) {
+          const uint32_t at = atomicAdd(&s.fill, 1u);
+          if (at < 64) {
+            s.few[at] = place;
+            s.few_mass[at] = w;
           }
-          left -= n;
         } else {
-          const uint64_t need = m >= want ? 1 : w ? (want - m + w - 1) / w : (uint64_t)n + 1;
-          nth = (uint32_t)(need < n ? need : n) - 1;
-          if (need <= n) {
-            m += w * (nth + 1);
-            break;
-          }
+          const uint32_t j = (uint32_t)((hi - place) >> shift);
+          atomicAdd(&s.sub_count[j], 1u);
+          if (w) atomicAdd(&s.sub_mass[j], (unsigned long long)w);
         }
-        m += w * n;
-      }
-      // its number: counted through the part, four tokens a thread
-      const int64_t at = (int64_t)part * kPart + t * 4;
-      uint32_t mine = 0;
-      uint64_t ignored;
-      bool is[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float y = 0.0f;
-        const bool there = at + e < a.n;
-        if (there) {
-          const int64_t o = row * a.ldy + at + e;
-          if constexpr (S == 4) y = static_cast<const float*>(a.y)[o];
-          else if (a.y_type == 2) y = (float)static_cast<const _Float16*>(a.y)[o];
-          else y = (float)static_cast<const bf16_t*>(a.y)[o];
-        }
-        is[e] = there && key_of(y) == hi;
-        mine += is[e];
-      }
-      uint64_t n = scan64(mine, s.red, &ignored);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (is[e] && n == nth) s.found64 = place_of(hi, (int)(at + e));
-        n += is[e];
+      };
+      if (in_list) {
+        for (int i = t; i < have; i += kRowThreads) add(s.list[i]);
+      } else {
+        walk_row<S>(a, row, blocks, s, value_of((uint32_t)(lo >> 32)), value_of((uint32_t)(hi >> 32) + 1),
+                    [&](int token, float y) { add(place_of(key_of(y), token)); });
       }
       __syncthreads();
-      r.place = s.found64;
-      r.mass = m;
+      if (order) break;
+      // the first that reaches it, or the last that has any
+      const uint64_t nm[2] = {t < kBins ? s.sub_count[t] : 0, t < kBins ? s.sub_mass[t] : 0};
+      uint64_t before[2], ignored[2];
+      scan64<2>(nm, before, ignored, s.red);
+      const uint64_t n = n_before + before[0], m = m_before + before[1];
+      if (nm[0] && (by_count ? n + nm[0] >= want : m + nm[1] >= want)) atomicMin(&s.found, (uint32_t)t);
+      if (nm[0]) atomicMax(&s.pick, t);
+      __syncthreads();
+      const uint32_t found = s.found != 0xFFFFFFFFu ? s.found : (uint32_t)s.pick;
+      if (t == (int)found) {
+        s.out[0] = nm[0];
+        s.out[1] = n;
+        s.out[2] = m;
+      }
+      __syncthreads();
+      inside = s.out[0];
+      n_before = s.out[1];
+      m_before = s.out[2];
+      hi -= (uint64_t)found << shift;
+      const uint64_t span = ((uint64_t)1 << shift) - 1;
+      lo = hi - lo > span ? hi - span : lo;
+    }
+    if (t < 64) {
+      const int left = min((int)s.fill, 64);
+      const uint64_t place = t < left ? s.few[t] : 0, w = t < left ? s.few_mass[t] : 0;
+      uint64_t n = n_before + 1, m = m_before + w;
+      for (int i = 0; i < left; ++i) {
+        const bool first = s.few[i] > place;
+        n += first ? 1 : 0;
+        m += first ? s.few_mass[i] : 0;
+      }
+      // the first in their order that reaches it, else the last
+      const bool reaches = t < left && (by_count ? n >= want : m >= want);
+      const bool none = __builtin_amdgcn_ballot_w64(reaches) == 0;
+      const uint64_t rank = t >= left || !(none || reaches) ? UINT64_MAX : none ? UINT64_MAX - n : n;
+      uint64_t least_rank = rank;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1)
+      {
+        const uint64_t other = __shfl_xor((unsigned long long)least_rank, d);
+        least_rank = other < least_rank ? other : least_rank;
+      }
+      if (rank == least_rank && t < left) {
+        s.out[0] = place;
+        s.out[1] = m;
+      }
     }
     __syncthreads();
-    return r;
-  };
-
-  Cut cut = {kBins, 0, full};  // everything
-  if (k < a.n) cut = cut_at(true, (uint64_t)k);
-  if (by_p) {
-    const Cut p = cut_at(false, mass_wanted(cut.mass));
-    if (p.bin < cut.bin || (p.bin == cut.bin && p.place > cut.place)) cut = p;
+    cut = s.out[0] > cut ? s.out[0] : cut;
+    if (by_count) mass = s.out[1];
   }
+
+  if (few) {
+    // the kept tokens' masses: of parts, of the drawn part's blocks, of its tokens
+    uint64_t w[kList / kRowThreads];
+#pragma unroll
+    for (int e = 0; e < kList / kRowThreads; ++e) {
+      const int i = e * kRowThreads + t;
+      const uint64_t place = i < have ? s.list[i] : 0;
+      const bool keep = i < have && place >= cut &&
+                        (!by_min || in_octaves(logit_of(place), c) >= least || (uint32_t)(place >> 32) == top);
+      w[e] = keep ? mass_of(place) : 0;
+      if (w[e]) atomicAdd(&s.kept[token_of(place) / kPart], (unsigned long long)w[e]);
+    }
+    if (t < 64) {
+      s.sub_mass[t] = 0;
+      s.few_mass[t] = 0;
+    }
+    __syncthreads();
+    uint64_t total;
+    const uint64_t mine = t < parts ? s.kept[t] : 0, before = scan64(mine, s.red, &total);
+    const uint64_t target = share_of(total, u);
+    if (target >= before && target < before + mine) {
+      s.pick = t;
+      s.out[2] = target - before;
+    }
+    __syncthreads();
+    const int part = s.pick;
+#pragma unroll
+    for (int e = 0; e < kList / kRowThreads; ++e) {
+      const int token = w[e] ? token_of(s.list[e * kRowThreads + t]) : -1;
+      if (w[e] && token / kPart == part) atomicAdd(&s.sub_mass[token % kPart / 64], (unsigned long long)w[e]);
+    }
+    __syncthreads();
+    if (t < 64) {
+      const uint64_t m = s.sub_mass[t], sum = wave_scan64(m), rest = s.out[2];
+      if (rest >= sum - m && rest < sum) {
+        s.found = (uint32_t)t;
+        s.out[3] = rest - (sum - m);
+      }
+    }
+    __syncthreads();
+    const int block = part * (kPart / 64) + (int)s.found;
+#pragma unroll
+    for (int e = 0; e < kList / kRowThreads; ++e) {
+      const int token = w[e] ? token_of(s.list[e * kRowThreads + t]) : -1;
+      if (w[e] && token / 64 == block) s.few_mass[token % 64] = w[e];
+    }
+    __syncthreads();
+    if (t < 64) {
+      const uint64_t m = s.few_mass[t], sum = wave_scan64(m), rest = s.out[3];
+      if (rest >= sum - m && rest < sum) {
+        const int token = block * 64 + t;
+        a.idx[row] = token;
+        if (a.prob)
+          a.prob[row] = (float)(exp2_of(in_octaves(one_logit<S>(a, row, token), c) - base) /
+                                __builtin_ldexp((double)total, -unit));
+      }
+    }
+    return;
+  }
+
+  // Many tokens.
+  const int bin_cut = cut ? bin_of(quarter(in_octaves(logit_of(cut), c)), base) : kBins;
   // kept: the bins before `last`, and in it what both the cut and min-p leave
-  const int last = min(cut.bin, by_min ? bin_min : kBins);
+  const int last = min(bin_cut, by_min ? bin_min : kBins);
+  const float last_lo = lowest(min(last, kBins - 2)), last_hi = lowest(last - 1);
   auto kept = [&](int token, float y) {
-    const double v2 = (double)y * c;
-    const int b = bin_of(quarter(v2), base);
-    if (b == kBins - 1) return false;  // weighs nothing
-    if (b != last) return b < last;
-    if (b == cut.bin && place_of(key_of(y), token) < cut.place) return false;
-    return !by_min || v2 >= least || key_of(y) == top;
+    if (!(y >= last_lo)) return false;
+    if (y >= last_hi || last > kBins - 2) return true;
+    if (place_of(key_of(y), token) < cut) return false;
+    return !by_min || in_octaves(y, c) >= least || key_of(y) == top;
   };
-  for (int p = t; p < parts; p += kRowThreads) s.kept[p] = 0;
-  __syncthreads();
-  // a wave a part: the bins before the last one
+  // a wave a part: the bins before the last one, in the part's own unit
   for (int p = t >> 6; p < parts; p += kRowThreads / 64) {
     uint64_t m = 0;
-    for (int j = t & 63; j < kBins; j += 64)
-      if (j + 4 * s.down[p] < last) m += in.mass[(row * parts + p) * kBins + j];
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) m += (uint64_t)__shfl_xor((unsigned long long)m, d);
-    if ((t & 63) == 0) s.kept[p] = m;
+    for (int j = 0; j < kBins; j += 64)
+      if (j + lane + 4 * s.down[p] < last) m += in.mass[(row * parts + p) * kBins + j + lane];
+    m = wave_scan64(m);
+    if (lane == 63) s.kept[p] = m;
   }
   __syncthreads();
   if (last < kBins - 1)
-    walk_row<S>(a, row, parts, [&](int p) { return part_has(last, p); },
-                [&](int p, int token, float y) {
-                  if (in_bin(last, y) && kept(token, y))
-                    atomicAdd(reinterpret_cast<unsigned long long*>(&s.kept[p]), (unsigned long long)weigh(p, y));
-                });
+    walk_row<S>(a, row, blocks, s, last_lo, last_hi, [&](int token, float y) {
+      if (kept(token, y)) atomicAdd(&s.kept[token / kPart], (unsigned long long)weigh(token / kPart, y));
+    });
   __syncthreads();
   // the part that the draw falls into, and what is left of it there
-  uint64_t w = t < parts ? to_row(t, s.kept[t]) : 0, total;
-  uint64_t before = scan64(w, s.red, &total);
-  const uint64_t target = share_of(total, a.u[row]);
-  if (t < parts && target >= before && target < before + w) {
+  uint64_t total;
+  const uint64_t w = t < parts ? to_row(t, s.kept[t]) : 0, before = scan64(w, s.red, &total);
+  const uint64_t target = share_of(total, u);
+  if (target >= before && target < before + w) {
     s.pick = t;
-    s.found64 = (target - before) << (s.down[t] + up);
+    s.out[2] = (target - before) << (s.down[t] + up);
   }
   __syncthreads();
   const int part = s.pick;
-  const uint64_t rest = s.found64;
+  const uint64_t rest = s.out[2];
   const int64_t at = (int64_t)part * kPart + t * 4;
   uint64_t x[4], sum = 0, ignored;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     x[e] = 0;
     if (at + e < a.n) {
-      const int64_t o = row * a.ldy + at + e;
-      float y;
-      if constexpr (S == 4) y = static_cast<const float*>(a.y)[o];
-      else if (a.y_type == 2) y = (float)static_cast<const _Float16*>(a.y)[o];
-      else y = (float)static_cast<const bf16_t*>(a.y)[o];
-      if (kept((int)(at + e), y) && bin_of(quarter((double)y * c), s.base[part]) < kBins - 1) x[e] = weigh(part, y);
+      const float y = one_logit<S>(a, row, at + e);
+      if (kept((int)(at + e), y) && bin_of(quarter(in_octaves(y, c)), s.base[part]) < kBins - 1) x[e] = weigh(part, y);
     }
     sum += x[e];
   }
@@ -705,7 +759,9 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
   for (int e = 0; e < 4; ++e) {
     if (rest >= run && rest < run + x[e]) {
       a.idx[row] = (int32_t)(at + e);
-      if (a.prob) a.prob[row] = (float)(__builtin_ldexp((double)x[e], -(s.down[part] + up)) / (double)total);
+      if (a.prob)
+        a.prob[row] = (float)(exp2_of(in_octaves(one_logit<S>(a, row, at + e), c) - base) /
+                              __builtin_ldexp((double)total, -unit));
     }
     run += x[e];
   }
