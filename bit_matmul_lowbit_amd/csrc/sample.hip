@@ -186,7 +186,7 @@ __global__ __launch_bounds__(kPartThreads) void sample_parts_kernel(SampleArgs a
   }
   __syncthreads();
   if (t < kBins) {
-    out.mass[slot * kBins + t] = mass[t];
+    if (!only_count) out.mass[slot * kBins + t] = mass[t];
     out.count[slot * kBins + t] = (uint16_t)count[t];
   }
   if (t == 0) out.base[slot] = base;
@@ -276,12 +276,12 @@ __device__ __forceinline__ float one_logit(const SampleArgs& a, int64_t row, int
   else return (float)static_cast<const bf16_t*>(a.y)[o];
 }
 
-// which of eight values from `at` on are tokens of the row with lo <= value < hi (a NaN hi:
-// all from lo on)
-__device__ __forceinline__ uint32_t hits_of(const float (&v)[8], float lo, float hi, int64_t left) {
+// Which of eight values have lo <= value < hi (a NaN hi: lo and above).  lo is above -inf, which
+// fills up the row's last eight.
+__device__ __forceinline__ uint32_t hits_of(const float (&v)[8], float lo, float hi) {
   uint32_t hits = 0;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) hits |= v[j] >= lo && !(v[j] >= hi) && j < left ? 1u << j : 0;
+  for (int j = 0; j < 8; ++j) hits |= v[j] >= lo && !(v[j] >= hi) ? 1u << j : 0;
   return hits;
 }
 __device__ __forceinline__ float pick(const float (&v)[8], int j) {
@@ -322,7 +322,7 @@ template <int S, class F>
 __device__ __forceinline__ void walk_row(const SampleArgs& a, int64_t row, int blocks, RowShared& s, float lo, float hi,
                                          F f) {
   walk_blocks<S>(a, row, blocks, s, lo, [&](int64_t from, float (&v)[8]) {
-    for (uint32_t hits = hits_of(v, lo, hi, a.n - from); hits; hits &= hits - 1) {
+    for (uint32_t hits = hits_of(v, lo, hi); hits; hits &= hits - 1) {
       const int j = __builtin_ctz(hits);
       f((int)from + j, pick(v, j));
     }
@@ -335,18 +335,12 @@ __device__ __forceinline__ int gather_row(const SampleArgs& a, int64_t row, int 
                                           float hi) {
   if (threadIdx.x == 0) s.fill = 0;
   walk_blocks<S>(a, row, blocks, s, lo, [&](int64_t from, float (&v)[8]) {
-    uint32_t hits = hits_of(v, lo, hi, a.n - from);
-    // one atomic a wave and block
-    const uint32_t mine = __builtin_popcount(hits), before = (uint32_t)wave_scan64(mine) - mine;
-    const uint32_t all = (uint32_t)__builtin_amdgcn_readlane((int)(before + mine), 63);
-    if (all == 0) return;
-    uint32_t at = 0;
-    if ((threadIdx.x & 63) == 0) at = atomicAdd(&s.fill, all);
-    at = (uint32_t)__builtin_amdgcn_readfirstlane((int)at) + before;
-    for (; hits; hits &= hits - 1, ++at) {
-      const int j = __builtin_ctz(hits);
-      if (at < kList) s.list[at] = place_of(key_of(pick(v, j)), (int)from + j);
-    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (v[j] >= lo && !(v[j] >= hi)) {
+        const uint32_t at = atomicAdd(&s.fill, 1u);
+        if (at < kList) s.list[at] = place_of(key_of(v[j]), (int)from + j);
+      }
   });
   __syncthreads();
   return (int)s.fill < kList ? (int)s.fill : kList;
@@ -426,8 +420,38 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
     s.down[p] = d < 1000.0 ? (int)d : 1000;
   }
   __syncthreads();
+  const bool by_k = k < a.n, by_p = top_p < 1.0f, by_min = min_p > 0.0f;
+  bool few = false;  // all that may be kept is in the list
+  int have = 0;      // tokens there
+  uint32_t key_lo = 0;
+
+  // A small top-k: the tokens from the k-th largest block's maximum on, which are k at least
+  // and hardly more.  Each block against half of them a thread.
+  if (by_k && k <= blocks / 2 && blocks <= kRowThreads / 2) {
+    uint32_t* rank = reinterpret_cast<uint32_t*>(s.list);
+    const int b = t % (kRowThreads / 2);
+    if (t < kRowThreads / 2) rank[t] = 0;
+    __syncthreads();
+    if (b < blocks) {
+      const uint32_t own = s.top[b];
+      const int from = t < kRowThreads / 2 ? 0 : blocks / 2, to = t < kRowThreads / 2 ? blocks / 2 : blocks;
+      uint32_t larger = 0;
+#pragma unroll 8
+      for (int i = from; i < to; ++i) larger += s.top[i] > own || (s.top[i] == own && i < b) ? 1 : 0;
+      atomicAdd(&rank[b], larger);
+    }
+    __syncthreads();
+    if (t < blocks && rank[t] == (uint32_t)k - 1) s.pick = t;
+    __syncthreads();
+    const uint32_t key = s.top[s.pick];
+    key_lo = key > kKeyNegInf ? key : kKeyNegInf + 1;
+    have = gather_row<S>(a, row, blocks, s, value_of(key_lo), INFINITY);
+    few = s.fill <= kList;
+  }
+
   // the row's histogram: four threads a bin
-  auto add_parts = [&](bool counts) {
+  const bool only_count = without_mass(a, k);
+  auto add_parts = [&](bool counts, bool masses) {
     const int r = t & (kBins - 1);
     uint64_t m = 0;
     uint32_t n = 0;
@@ -436,18 +460,16 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
       for (int p = t / kBins; p < parts; p += kRowThreads / kBins) {
         const int down = s.down[p], j = r - 4 * down;
         const int64_t at = (row * parts + p) * kBins + max(j, 0);
-        const uint64_t pm = in.mass[at];
-        const uint32_t pn = in.count[at];
+        const uint64_t pm = masses ? in.mass[at] : 0;
+        const uint32_t pn = counts ? in.count[at] : 0;
         m += j >= 0 && down + up < 64 ? pm >> ((down + up) & 63) : 0;
         n += j >= 0 ? pn : 0;
       }
-    if (n && counts) atomicAdd(&s.count[r], n);
+    if (n) atomicAdd(&s.count[r], n);
     if (m) atomicAdd(&s.mass[r], (unsigned long long)m);
   };
-  add_parts(true);
-  __syncthreads();
   // sums up to and with each bin (the last bin has the rest of the tokens, and no mass)
-  uint64_t full;
+  uint64_t full = 0;
   auto add_bins = [&](bool counts) {
     const uint64_t mn[2] = {t < kBins ? s.mass[t] : 0, t < kBins ? s.count[t] : 0};
     uint64_t before[2], total[2];
@@ -459,9 +481,6 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
     }
     __syncthreads();
   };
-  add_bins(true);
-
-  const bool by_k = k < a.n, by_p = top_p < 1.0f, by_min = min_p > 0.0f;
   const double v2_top = in_octaves(value_of(top), c);
   const double least = by_min ? v2_top + log2((double)fminf(min_p, 1.0f)) : -1e308;  // of v2
   const int bin_min = by_min ? bin_of(quarter(least), base) : kBins - 1;
@@ -496,70 +515,95 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
     return want ? want : 1;
   };
 
-  int bin_last = kBins - 1;
-  if (by_k) bin_last = bin_at_count((uint64_t)k);
-  if (by_p && !by_k) bin_last = bin_at_mass(mass_wanted(full));
-  if (!by_p || !by_k) bin_last = min(bin_last, bin_min);
-  // few tokens: in LDS
-  const bool few = s.count[bin_last] <= kList;
-  int have = 0;
-  if (few) {
-    have = gather_row<S>(a, row, blocks, s, lowest(bin_last), INFINITY);
-  } else if (without_mass(a, k)) {
-    // very many tokens at the end of a small top-k (they share one value, or nearly):
-    // the masses that the first launch left out
-    walk_row<S>(a, row, blocks, s, lowest(bin_last), INFINITY, [&](int token, float y) {
-      const int p = token / kPart, bin = bin_of(quarter(in_octaves(y, c)), s.base[p]);
-      atomicAdd(reinterpret_cast<unsigned long long*>(&in.mass[(row * parts + p) * kBins + bin]),
-                (unsigned long long)weigh(p, y));
-    });
-    __threadfence();
+  if (!few) {
+    add_parts(true, !only_count);
     __syncthreads();
-    if (t < kBins) s.mass[t] = 0;
-    __syncthreads();
-    add_parts(false);
-    __syncthreads();
-    add_bins(false);
+    add_bins(true);
+    int bin_last = kBins - 1;
+    if (by_k) bin_last = bin_at_count((uint64_t)k);
+    if (by_p && !by_k) bin_last = bin_at_mass(mass_wanted(full));
+    if (!by_p || !by_k) bin_last = min(bin_last, bin_min);
+    bin_last = min(bin_last, kBins - 2);  // what is below weighs nothing
+    const float lo = lowest(bin_last);
+    few = s.count[bin_last] <= kList;
+    if (few) {
+      key_lo = key_of(lo);
+      have = gather_row<S>(a, row, blocks, s, lo, INFINITY);
+    } else if (only_count) {
+      // very many tokens at the end of a top-k (they share one value, or nearly): the masses
+      // that the first launch left out
+      for (int i = t; i < parts * kBins; i += kRowThreads) in.mass[row * parts * kBins + i] = 0;
+      __threadfence();
+      __syncthreads();
+      walk_row<S>(a, row, blocks, s, lo, INFINITY, [&](int token, float y) {
+        const int p = token / kPart, bin = bin_of(quarter(in_octaves(y, c)), s.base[p]);
+        atomicAdd(reinterpret_cast<unsigned long long*>(&in.mass[(row * parts + p) * kBins + bin]),
+                  (unsigned long long)weigh(p, y));
+      });
+      __threadfence();
+      __syncthreads();
+      if (t < kBins) s.mass[t] = 0;
+      __syncthreads();
+      add_parts(false, true);
+      __syncthreads();
+      add_bins(false);
+    }
   }
+
+  // A thread's tokens of the list, and their masses
+  uint64_t mine[kList / kRowThreads], w[kList / kRowThreads];
+  auto take_list = [&]() {
+#pragma unroll
+    for (int e = 0; e < kList / kRowThreads; ++e) {
+      const int i = e * kRowThreads + t;
+      mine[e] = i < have ? s.list[i] : 0;
+      w[e] = i < have ? mass_of(mine[e]) : 0;
+    }
+  };
+  take_list();
 
   // Places of the last tokens that top-k and top-p keep, the earlier of them in `cut` (0:
   // everything that weighs), and the mass of what is kept.
   uint64_t cut = 0, mass = full;
+  bool ranked = false;  // the list is few enough to be in s.few, with its sums
 #pragma unroll 1
   for (int filter = 0; filter < 2; ++filter) {
     const bool by_count = filter == 0;
     if (!(by_count ? by_k : by_p)) continue;
-    if (few && by_count && k >= have) {  // all of the list; of its bin, others may be there that weigh nothing
+    if (few && by_count && k >= have) continue;  // all that weighs
+    if (few && !by_count && by_k && !ranked) {  // of the tokens of the list that top-k keeps
       uint64_t sum = 0;
-      for (int i = t; i < have; i += kRowThreads) sum += mass_of(s.list[i]);
+#pragma unroll
+      for (int e = 0; e < kList / kRowThreads; ++e) sum += mine[e] >= cut ? w[e] : 0;
       scan64(sum, s.red, &mass);
-      continue;
     }
     const uint64_t want = by_count ? (uint64_t)k : mass_wanted(mass);
     // the interval of places from lo to hi, and the tokens there and before it
-    int bin = bin_last;
     uint64_t inside = have, n_before = 0, m_before = 0;
+    uint64_t lo = (uint64_t)key_lo << 32, hi = ((uint64_t)top << 32) | 0xFFFFFFFFu;
     if (!few) {
-      bin = by_count ? bin_at_count(want) : bin_at_mass(want);
+      const int bin = by_count ? bin_at_count(want) : bin_at_mass(want);
       if (bin == kBins - 1) continue;  // only what weighs nothing is cut off
       n_before = bin ? s.count[bin - 1] : 0;
       m_before = bin ? s.mass[bin - 1] : 0;
       inside = s.count[bin] - n_before;
-      if (inside <= kList) have = gather_row<S>(a, row, blocks, s, lowest(bin), lowest(bin - 1));
+      if (inside <= kList) {
+        have = gather_row<S>(a, row, blocks, s, lowest(bin), lowest(bin - 1));
+        take_list();
+      }
+      lo = (uint64_t)key_of(lowest(bin)) << 32;
+      hi = ((uint64_t)(key_of(lowest(bin - 1)) - 1) << 32) | 0xFFFFFFFFu;
     }
     const bool in_list = inside <= kList;
-    uint64_t lo = (uint64_t)key_of(lowest(bin)) << 32;
-    uint64_t hi = ((uint64_t)(few ? top : key_of(lowest(bin - 1)) - 1) << 32) | 0xFFFFFFFFu;
     // narrower by 256 at a time, until a wave can order the few that are left
-    while (true) {
+    while (!ranked) {
       const bool order = inside <= 64;
       // numbers go no further than n; where the key is known, they alone differ
       if ((lo >> 32) == (hi >> 32)) {
         const uint64_t last_place = place_of((uint32_t)(hi >> 32), (int)(a.n - 1));
         lo = lo > last_place ? lo : last_place;
       }
-      int shift = 0;
-      while (((hi - lo) >> shift) >= kBins) ++shift;
+      const int shift = hi - lo < kBins ? 0 : 64 - 8 - __builtin_clzll(hi - lo);
       __syncthreads();
       if (t < kBins) {
         s.sub_mass[t] = 0;
@@ -571,9 +615,8 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
         s.fill = 0;
       }
       __syncthreads();
-      auto add = [&](uint64_t place) {
+      auto add = [&](uint64_t place, uint64_t w) {
         if (place < lo || place > hi) return;
-        const uint64_t w = mass_of(place);
         if (order) {
           const uint32_t at = atomicAdd(&s.fill, 1u);
           if (at < 64) {
@@ -587,10 +630,15 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
         }
       };
       if (in_list) {
-        for (int i = t; i < have; i += kRowThreads) add(s.list[i]);
+#pragma unroll
+        for (int e = 0; e < kList / kRowThreads; ++e)
+          if (e * kRowThreads + t < have) add(mine[e], w[e]);
       } else {
         walk_row<S>(a, row, blocks, s, value_of((uint32_t)(lo >> 32)), value_of((uint32_t)(hi >> 32) + 1),
-                    [&](int token, float y) { add(place_of(key_of(y), token)); });
+                    [&](int token, float y) {
+                      const int p = token / kPart;
+                      add(place_of(key_of(y), token), to_row(p, weigh(p, y)));
+                    });
       }
       __syncthreads();
       if (order) break;
@@ -616,27 +664,32 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
       const uint64_t span = ((uint64_t)1 << shift) - 1;
       lo = hi - lo > span ? hi - span : lo;
     }
-    if (t < 64) {
-      const int left = min((int)s.fill, 64);
-      const uint64_t place = t < left ? s.few[t] : 0, w = t < left ? s.few_mass[t] : 0;
-      uint64_t n = n_before + 1, m = m_before + w;
-      for (int i = 0; i < left; ++i) {
-        const bool first = s.few[i] > place;
-        n += first ? 1 : 0;
-        m += first ? s.few_mass[i] : 0;
+    // each of the few against four of them a wave
+    const int left = min((int)s.fill, 64);
+    const uint64_t place = lane < left ? s.few[lane] : 0;
+    if (!ranked) {
+      uint32_t up_to = 0;
+      uint64_t mass_up_to = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = (t >> 6) * 4 + e;
+        const bool first = i < left && s.few[i] >= place;
+        up_to += first ? 1 : 0;
+        mass_up_to += first ? s.few_mass[i] : 0;
       }
+      if (lane < left && up_to) {
+        atomicAdd(&s.sub_count[lane], up_to);
+        atomicAdd(&s.sub_mass[lane], (unsigned long long)mass_up_to);
+      }
+      ranked = few && have <= 64;
+    }
+    __syncthreads();
+    if (t < 64) {
+      const uint64_t n = n_before + s.sub_count[t], m = m_before + s.sub_mass[t];
       // the first in their order that reaches it, else the last
       const bool reaches = t < left && (by_count ? n >= want : m >= want);
-      const bool none = __builtin_amdgcn_ballot_w64(reaches) == 0;
-      const uint64_t rank = t >= left || !(none || reaches) ? UINT64_MAX : none ? UINT64_MAX - n : n;
-      uint64_t least_rank = rank;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1)
-      {
-        const uint64_t other = __shfl_xor((unsigned long long)least_rank, d);
-        least_rank = other < least_rank ? other : least_rank;
-      }
-      if (rank == least_rank && t < left) {
+      const int reaching = __builtin_popcountll(__builtin_amdgcn_ballot_w64(reaches));
+      if (t < left && (int)s.sub_count[t] == left - (reaching ? reaching - 1 : 0)) {
         s.out[0] = place;
         s.out[1] = m;
       }
@@ -647,16 +700,13 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
   }
 
   if (few) {
-    // the kept tokens' masses: of parts, of the drawn part's blocks, of its tokens
-    uint64_t w[kList / kRowThreads];
+    // the kept tokens' masses: of parts, of the drawn part's blocks of 64, of its tokens
 #pragma unroll
     for (int e = 0; e < kList / kRowThreads; ++e) {
-      const int i = e * kRowThreads + t;
-      const uint64_t place = i < have ? s.list[i] : 0;
-      const bool keep = i < have && place >= cut &&
-                        (!by_min || in_octaves(logit_of(place), c) >= least || (uint32_t)(place >> 32) == top);
-      w[e] = keep ? mass_of(place) : 0;
-      if (w[e]) atomicAdd(&s.kept[token_of(place) / kPart], (unsigned long long)w[e]);
+      const bool keep = mine[e] >= cut && (!by_min || in_octaves(logit_of(mine[e]), c) >= least ||
+                                           (uint32_t)(mine[e] >> 32) == top);
+      w[e] = keep ? w[e] : 0;
+      if (w[e]) atomicAdd(&s.kept[token_of(mine[e]) / kPart], (unsigned long long)w[e]);
     }
     if (t < 64) {
       s.sub_mass[t] = 0;
@@ -664,9 +714,9 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
     }
     __syncthreads();
     uint64_t total;
-    const uint64_t mine = t < parts ? s.kept[t] : 0, before = scan64(mine, s.red, &total);
+    const uint64_t m = t < parts ? s.kept[t] : 0, before = scan64(m, s.red, &total);
     const uint64_t target = share_of(total, u);
-    if (target >= before && target < before + mine) {
+    if (target >= before && target < before + m) {
       s.pick = t;
       s.out[2] = target - before;
     }
@@ -674,7 +724,7 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
     const int part = s.pick;
 #pragma unroll
     for (int e = 0; e < kList / kRowThreads; ++e) {
-      const int token = w[e] ? token_of(s.list[e * kRowThreads + t]) : -1;
+      const int token = w[e] ? token_of(mine[e]) : -1;
       if (w[e] && token / kPart == part) atomicAdd(&s.sub_mass[token % kPart / 64], (unsigned long long)w[e]);
     }
     __syncthreads();
@@ -689,7 +739,7 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
     const int block = part * (kPart / 64) + (int)s.found;
 #pragma unroll
     for (int e = 0; e < kList / kRowThreads; ++e) {
-      const int token = w[e] ? token_of(s.list[e * kRowThreads + t]) : -1;
+      const int token = w[e] ? token_of(mine[e]) : -1;
       if (w[e] && token / 64 == block) s.few_mass[token % 64] = w[e];
     }
     __syncthreads();
@@ -734,9 +784,9 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
   __syncthreads();
   // the part that the draw falls into, and what is left of it there
   uint64_t total;
-  const uint64_t w = t < parts ? to_row(t, s.kept[t]) : 0, before = scan64(w, s.red, &total);
+  const uint64_t m = t < parts ? to_row(t, s.kept[t]) : 0, before = scan64(m, s.red, &total);
   const uint64_t target = share_of(total, u);
-  if (target >= before && target < before + w) {
+  if (target >= before && target < before + m) {
     s.pick = t;
     s.out[2] = (target - before) << (s.down[t] + up);
   }
