@@ -36,7 +36,7 @@ constexpr int kBins = 256;       // quarters of an octave; the last one: everyth
 constexpr int kRowThreads = 1024;
 constexpr int kMostParts = 256;
 constexpr int kAhead = 4;        // blocks that a wave loads ahead
-constexpr int kList = 2048;      // tokens that are held in LDS
+constexpr int kList = 8192;      // tokens that are held in LDS
 constexpr int kMostK = 1024;     // up to which top-k rows go without the parts' masses
 constexpr int kUnit = 51;        // a part's weights are whole numbers of 2^-51: 4096 of them stay below 2^64
 
@@ -262,7 +262,7 @@ struct RowShared {
   unsigned long long sub_mass[kBins];
   uint32_t sub_count[kBins];
   uint64_t red[2][16];
-  uint64_t list[kList], few[64], few_mass[64];
+  uint64_t list[kList], list_mass[kList], few[64], few_mass[64];
   uint64_t out[4];
   uint32_t fill, found, walk;
   int pick;
@@ -290,6 +290,24 @@ __device__ __forceinline__ float pick(const float (&v)[8], int j) {
   return j & 4 ? f : e;
 }
 
+// Eight values of a row, from `from` on or the row's last; a row of fewer is filled up with -inf
+template <int S>
+__device__ __forceinline__ Raw8<S> load_inside(const SampleArgs& a, int64_t row, int from) {
+  if (a.n >= 8) return load8<S>(a.y, row * a.ldy + min(from, (int)a.n - 8));
+  Raw8<S> r;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int64_t at = row * a.ldy + j;
+    if constexpr (S == 4) {
+      r.d[j] = j < a.n ? static_cast<const uint32_t*>(a.y)[at] : 0xFF800000u;
+    } else {
+      const uint32_t h = j < a.n ? static_cast<const uint16_t*>(a.y)[at] : a.y_type == 2 ? 0xFC00u : 0xFF80u;
+      r.d[j >> 1] = j & 1 ? r.d[j >> 1] | h << 16 : h;
+    }
+  }
+  return r;
+}
+
 // Calls f(from, values) for the blocks that have values of lo and above; a lane has eight
 // values, from `from` on
 template <int S, class F>
@@ -304,16 +322,29 @@ __device__ __forceinline__ void walk_blocks(const SampleArgs& a, int64_t row, in
   const int n = (int)s.walk;
 #pragma unroll 1
   for (int i = wave; i < n; i += kRowThreads / 64 * kAhead) {
-    float v[kAhead][8];
-    int64_t from[kAhead];
+    // loads without a branch, which would wait for each: at the row's end its last eight
+    Raw8<S> raw[kAhead];
+    int block[kAhead];
 #pragma unroll
     for (int e = 0; e < kAhead; ++e) {
       const int k = i + e * (kRowThreads / 64);
-      from[e] = k < n ? (int64_t)s.todo[k] * kBlock + lane * 8 : a.n;
-      load_logits<S>(a.y, a.y_type, row * a.ldy + from[e], a.n - from[e], v[e]);
+      block[e] = __builtin_amdgcn_readfirstlane((int)s.todo[k < n ? k : i]);
+      raw[e] = load_inside<S>(a, row, block[e] * kBlock + lane * 8);
     }
 #pragma unroll
-    for (int e = 0; e < kAhead; ++e) f(from[e], v[e]);
+    for (int e = 0; e < kAhead; ++e) {
+      if (i + e * (kRowThreads / 64) >= n) break;
+      const int from = block[e] * kBlock + lane * 8;
+      int at = from;
+      float v[8];
+      widen<S>(raw[e], a.y_type, v);
+      if ((int64_t)(block[e] + 1) * kBlock > a.n) {
+        at = min(from, max((int)a.n - 8, 0));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = j < from - at ? -INFINITY : v[j];
+      }
+      f(at, v);
+    }
   }
 }
 
@@ -321,10 +352,10 @@ __device__ __forceinline__ void walk_blocks(const SampleArgs& a, int64_t row, in
 template <int S, class F>
 __device__ __forceinline__ void walk_row(const SampleArgs& a, int64_t row, int blocks, RowShared& s, float lo, float hi,
                                          F f) {
-  walk_blocks<S>(a, row, blocks, s, lo, [&](int64_t from, float (&v)[8]) {
+  walk_blocks<S>(a, row, blocks, s, lo, [&](int from, float (&v)[8]) {
     for (uint32_t hits = hits_of(v, lo, hi); hits; hits &= hits - 1) {
       const int j = __builtin_ctz(hits);
-      f((int)from + j, pick(v, j));
+      f(from + j, pick(v, j));
     }
   });
 }
@@ -334,13 +365,28 @@ template <int S>
 __device__ __forceinline__ int gather_row(const SampleArgs& a, int64_t row, int blocks, RowShared& s, float lo,
                                           float hi) {
   if (threadIdx.x == 0) s.fill = 0;
-  walk_blocks<S>(a, row, blocks, s, lo, [&](int64_t from, float (&v)[8]) {
+  walk_blocks<S>(a, row, blocks, s, lo, [&](int from, float (&v)[8]) {
+    // one atomic a wave and block
+    uint64_t hits[8];
+    uint32_t all = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (v[j] >= lo && !(v[j] >= hi)) {
-        const uint32_t at = atomicAdd(&s.fill, 1u);
-        if (at < kList) s.list[at] = place_of(key_of(v[j]), (int)from + j);
-      }
+    for (int j = 0; j < 8; ++j) {
+      hits[j] = __builtin_amdgcn_ballot_w64(v[j] >= lo && !(v[j] >= hi));
+      all += __builtin_popcountll(hits[j]);
+    }
+    if (all == 0) return;
+    uint32_t at = 0;
+    if ((threadIdx.x & 63) == 0) at = atomicAdd(&s.fill, all);
+    at = (uint32_t)__builtin_amdgcn_readfirstlane((int)at);
+    if (at + all > kList) return;  // too many: the list is of no use
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (v[j] >= lo && !(v[j] >= hi))
+        s.list[at + __builtin_amdgcn_mbcnt_hi((uint32_t)(hits[j] >> 32),
+                                              __builtin_amdgcn_mbcnt_lo((uint32_t)hits[j], 0))] =
+            place_of(key_of(v[j]), from + j);
+      at += __builtin_popcountll(hits[j]);
+    }
   });
   __syncthreads();
   return (int)s.fill < kList ? (int)s.fill : kList;
@@ -455,15 +501,19 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
     const int r = t & (kBins - 1);
     uint64_t m = 0;
     uint32_t n = 0;
-    if (r < kBins - 1)
+    if (r < kBins - 1 && counts)
+#pragma unroll 10
+      for (int p = t / kBins; p < parts; p += kRowThreads / kBins) {
+        const int j = r - 4 * s.down[p];
+        const uint32_t pn = in.count[(row * parts + p) * kBins + max(j, 0)];
+        n += j >= 0 ? pn : 0;
+      }
+    if (r < kBins - 1 && masses)
 #pragma unroll 10
       for (int p = t / kBins; p < parts; p += kRowThreads / kBins) {
         const int down = s.down[p], j = r - 4 * down;
-        const int64_t at = (row * parts + p) * kBins + max(j, 0);
-        const uint64_t pm = masses ? in.mass[at] : 0;
-        const uint32_t pn = counts ? in.count[at] : 0;
+        const uint64_t pm = in.mass[(row * parts + p) * kBins + max(j, 0)];
         m += j >= 0 && down + up < 64 ? pm >> ((down + up) & 63) : 0;
-        n += j >= 0 ? pn : 0;
       }
     if (n) atomicAdd(&s.count[r], n);
     if (m) atomicAdd(&s.mass[r], (unsigned long long)m);
@@ -550,21 +600,16 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
     }
   }
 
-  // A thread's tokens of the list, and their masses
-  uint64_t mine[kList / kRowThreads], w[kList / kRowThreads];
-  auto take_list = [&]() {
-#pragma unroll
-    for (int e = 0; e < kList / kRowThreads; ++e) {
-      const int i = e * kRowThreads + t;
-      mine[e] = i < have ? s.list[i] : 0;
-      w[e] = i < have ? mass_of(mine[e]) : 0;
-    }
+  // the masses of the list
+  auto weigh_list = [&]() {
+    for (int i = t; i < have; i += kRowThreads) s.list_mass[i] = mass_of(s.list[i]);
   };
-  take_list();
+  weigh_list();
 
   // Places of the last tokens that top-k and top-p keep, the earlier of them in `cut` (0:
   // everything that weighs), and the mass of what is kept.
   uint64_t cut = 0, mass = full;
+  int list_bin = -1;    // whose tokens the list has, where it has not all
   bool ranked = false;  // the list is few enough to be in s.few, with its sums
 #pragma unroll 1
   for (int filter = 0; filter < 2; ++filter) {
@@ -573,8 +618,7 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
     if (few && by_count && k >= have) continue;  // all that weighs
     if (few && !by_count && by_k && !ranked) {  // of the tokens of the list that top-k keeps
       uint64_t sum = 0;
-#pragma unroll
-      for (int e = 0; e < kList / kRowThreads; ++e) sum += mine[e] >= cut ? w[e] : 0;
+      for (int i = t; i < have; i += kRowThreads) sum += s.list[i] >= cut ? s.list_mass[i] : 0;
       scan64(sum, s.red, &mass);
     }
     const uint64_t want = by_count ? (uint64_t)k : mass_wanted(mass);
@@ -589,7 +633,8 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
       inside = s.count[bin] - n_before;
       if (inside <= kList) {
         have = gather_row<S>(a, row, blocks, s, lowest(bin), lowest(bin - 1));
-        take_list();
+        weigh_list();
+        list_bin = bin;
       }
       lo = (uint64_t)key_of(lowest(bin)) << 32;
       hi = ((uint64_t)(key_of(lowest(bin - 1)) - 1) << 32) | 0xFFFFFFFFu;
@@ -630,9 +675,7 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
         }
       };
       if (in_list) {
-#pragma unroll
-        for (int e = 0; e < kList / kRowThreads; ++e)
-          if (e * kRowThreads + t < have) add(mine[e], w[e]);
+        for (int i = t; i < have; i += kRowThreads) add(s.list[i], s.list_mass[i]);
       } else {
         walk_row<S>(a, row, blocks, s, value_of((uint32_t)(lo >> 32)), value_of((uint32_t)(hi >> 32) + 1),
                     [&](int token, float y) {
@@ -701,12 +744,12 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
 
   if (few) {
     // the kept tokens' masses: of parts, of the drawn part's blocks of 64, of its tokens
-#pragma unroll
-    for (int e = 0; e < kList / kRowThreads; ++e) {
-      const bool keep = mine[e] >= cut && (!by_min || in_octaves(logit_of(mine[e]), c) >= least ||
-                                           (uint32_t)(mine[e] >> 32) == top);
-      w[e] = keep ? w[e] : 0;
-      if (w[e]) atomicAdd(&s.kept[token_of(mine[e]) / kPart], (unsigned long long)w[e]);
+    for (int i = t; i < have; i += kRowThreads) {
+      const uint64_t place = s.list[i], w = s.list_mass[i];
+      const bool keep = place >= cut && (!by_min || in_octaves(logit_of(place), c) >= least ||
+                                         (uint32_t)(place >> 32) == top);
+      if (!keep) s.list_mass[i] = 0;
+      else if (w) atomicAdd(&s.kept[token_of(place) / kPart], (unsigned long long)w);
     }
     if (t < 64) {
       s.sub_mass[t] = 0;
@@ -722,10 +765,9 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
     }
     __syncthreads();
     const int part = s.pick;
-#pragma unroll
-    for (int e = 0; e < kList / kRowThreads; ++e) {
-      const int token = w[e] ? token_of(mine[e]) : -1;
-      if (w[e] && token / kPart == part) atomicAdd(&s.sub_mass[token % kPart / 64], (unsigned long long)w[e]);
+    for (int i = t; i < have; i += kRowThreads) {
+      const int token = token_of(s.list[i]);
+      if (token / kPart == part) atomicAdd(&s.sub_mass[token % kPart / 64], (unsigned long long)s.list_mass[i]);
     }
     __syncthreads();
     if (t < 64) {
@@ -737,10 +779,9 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
     }
     __syncthreads();
     const int block = part * (kPart / 64) + (int)s.found;
-#pragma unroll
-    for (int e = 0; e < kList / kRowThreads; ++e) {
-      const int token = w[e] ? token_of(mine[e]) : -1;
-      if (w[e] && token / 64 == block) s.few_mass[token % 64] = w[e];
+    for (int i = t; i < have; i += kRowThreads) {
+      const int token = token_of(s.list[i]);
+      if (token / 64 == block) s.few_mass[token % 64] = s.list_mass[i];
     }
     __syncthreads();
     if (t < 64) {
@@ -777,10 +818,16 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
     if (lane == 63) s.kept[p] = m;
   }
   __syncthreads();
-  if (last < kBins - 1)
-    walk_row<S>(a, row, blocks, s, last_lo, last_hi, [&](int token, float y) {
+  if (last < kBins - 1) {
+    auto add = [&](int token, float y) {
       if (kept(token, y)) atomicAdd(&s.kept[token / kPart], (unsigned long long)weigh(token / kPart, y));
-    });
+    };
+    if (last == list_bin) {
+      for (int i = t; i < have; i += kRowThreads) add(token_of(s.list[i]), logit_of(s.list[i]));
+    } else {
+      walk_row<S>(a, row, blocks, s, last_lo, last_hi, add);
+    }
+  }
   __syncthreads();
   // the part that the draw falls into, and what is left of it there
   uint64_t total;
