@@ -37,7 +37,6 @@ constexpr int kRowThreads = 1024;
 constexpr int kMostParts = 256;
 constexpr int kAhead = 4;        // blocks that a wave loads ahead
 constexpr int kList = 8192;      // tokens that are held in LDS
-constexpr int kMostK = 1024;     // up to which top-k rows go without the parts' masses
 constexpr int kUnit = 51;        // a part's weights are whole numbers of 2^-51: 4096 of them stay below 2^64
 
 // Order of values as whole numbers: NaN above all, both zeros alike
@@ -92,21 +91,24 @@ __device__ __forceinline__ double in_octaves(float y, double c) {
 struct Parts {
   double* base;      // [rows][parts]: weights are relative to 2^base
   uint32_t* top;     // [rows][parts][kPart / kBlock]: the largest key of a block
-  uint64_t* mass;    // [rows][parts][kBins]
-  uint16_t* count;   // [rows][parts][kBins]
+  uint64_t* mass;    // [rows][parts][kBins]: up to and with the bin
+  uint16_t* count;   // [rows][parts][kBins]: likewise
+  uint16_t* order;   // [rows][parts][kPart]: the part's tokens by their bins
 };
 __host__ __device__ inline size_t align_up(size_t v) { return (v + 255) / 256 * 256; }
 inline size_t parts_layout(int64_t rows, int64_t parts, void* ws, Parts* p) {
   char* at = static_cast<char*>(ws);
   const size_t n = (size_t)(rows * parts);
   const size_t mass = align_up(n * kBins * 8), count = align_up(n * kBins * 2), base = align_up(n * 8), top = align_up(n * kBlocks * 4);
+  const size_t order = align_up(n * kPart * 2);
   if (p) {
     p->mass = reinterpret_cast<uint64_t*>(at);
     p->count = reinterpret_cast<uint16_t*>(at + mass);
     p->base = reinterpret_cast<double*>(at + mass + count);
     p->top = reinterpret_cast<uint32_t*>(at + mass + count + base);
+    p->order = reinterpret_cast<uint16_t*>(at + mass + count + base + top);
   }
-  return mass + count + base + top;
+  return mass + count + base + top + order;
 }
 
 // the quarter octave of v2 = y log2(e) / T on the scale of all parts
@@ -131,65 +133,6 @@ __device__ __forceinline__ void load_logits(const void* y, int type, int64_t at,
       }
     }
   }
-}
-
-// Whether a row's filters are likely to need the masses of the histograms: with
-// few tokens by top-k the kept ones are weighed one by one
-__device__ __forceinline__ int64_t top_k_of(const SampleArgs& a, int64_t row) {
-  const int64_t k = a.top_k ? a.top_k[row] : 0;
-  return k <= 0 || k > a.n ? a.n : k;
-}
-__device__ __forceinline__ bool without_mass(const SampleArgs& a, int64_t k) { return k < a.n && k <= kMostK; }
-
-template <int S>
-__global__ __launch_bounds__(kPartThreads) void sample_parts_kernel(SampleArgs a, Parts out) {
-  __shared__ unsigned long long mass[kBins];
-  __shared__ uint32_t count[kBins];
-  __shared__ uint32_t tops[kBlocks];
-  const int64_t row = blockIdx.y, part = blockIdx.x, slot = row * gridDim.x + part;
-  const int t = threadIdx.x;
-  const int64_t at = part * kPart + t * 8;
-  float v[8];
-  load_logits<S>(a.y, a.y_type, row * a.ldy + at, a.n - at, v);
-  const float temp = temperature_of(a, row);
-  const bool only_count = without_mass(a, top_k_of(a, row));
-  if (t < kBins) {
-    mass[t] = 0;
-    count[t] = 0;
-  }
-  uint32_t top = kKeyNegInf;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) top = max(top, key_of(v[j]));
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
-  if ((t & 63) == 0) {
-    tops[t >> 6] = top;
-    out.top[slot * kBlocks + (t >> 6)] = top;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kBlocks; ++w) top = max(top, tops[w]);
-  // greedy rows, and rows with NaN or infinity, go by the maximum alone
-  const bool plain = temp != 0.0f && top < kKeyInf && top > kKeyNegInf;
-  const double c = plain ? octaves(temp) : 0.0;
-  const double base = plain ? __builtin_ceil(in_octaves(value_of(top), c)) : -1e300;
-  if (plain) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const double v2 = in_octaves(v[j], c);
-      const int bin = bin_of(quarter(v2), base);
-      if (bin < kBins - 1) {  // what is below counts nothing, and is counted from the others
-        atomicAdd(&count[bin], 1u);
-        if (!only_count) atomicAdd(&mass[bin], (unsigned long long)fixed_of(exp2_of(v2 - base)));
-      }
-    }
-  }
-  __syncthreads();
-  if (t < kBins) {
-    if (!only_count) out.mass[slot * kBins + t] = mass[t];
-    out.count[slot * kBins + t] = (uint16_t)count[t];
-  }
-  if (t == 0) out.base[slot] = base;
 }
 
 // ---------------------------------------------------------------------------
@@ -246,6 +189,94 @@ __device__ __forceinline__ uint64_t scan64(uint64_t v, uint64_t (*red)[16], uint
   return before[0];
 }
 
+// Where top-k keeps no more than the list has room for, no histogram of masses is needed
+__device__ __forceinline__ int64_t top_k_of(const SampleArgs& a, int64_t row) {
+  const int64_t k = a.top_k ? a.top_k[row] : 0;
+  return k <= 0 || k > a.n ? a.n : k;
+}
+__device__ __forceinline__ bool without_mass(const SampleArgs& a, int64_t k) { return k < a.n && k <= kList; }
+
+template <int S>
+__global__ __launch_bounds__(kPartThreads) void sample_parts_kernel(SampleArgs a, Parts out) {
+  __shared__ unsigned long long mass[kBins];
+  __shared__ uint32_t count[kBins], before[kBins];
+  __shared__ uint32_t tops[kBlocks], waves[kBins / 64];
+  __shared__ unsigned long long wave_mass[kBins / 64];
+  __shared__ __align__(16) uint16_t order[kPart];
+  const int64_t row = blockIdx.y, part = blockIdx.x, slot = row * gridDim.x + part;
+  const int t = threadIdx.x;
+  const int64_t at = part * kPart + t * 8;
+  float v[8];
+  load_logits<S>(a.y, a.y_type, row * a.ldy + at, a.n - at, v);
+  const float temp = temperature_of(a, row);
+  const bool only_count = without_mass(a, top_k_of(a, row));
+  if (t < kBins) {
+    mass[t] = 0;
+    count[t] = 0;
+  }
+  uint32_t top = kKeyNegInf;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) top = max(top, key_of(v[j]));
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
+  if ((t & 63) == 0) {
+    tops[t >> 6] = top;
+    out.top[slot * kBlocks + (t >> 6)] = top;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kBlocks; ++w) top = max(top, tops[w]);
+  // greedy rows, and rows with NaN or infinity, go by the maximum alone
+  const bool plain = temp != 0.0f && top < kKeyInf && top > kKeyNegInf;
+  if (temp == 0.0f || top >= kKeyInf) return;
+  const double c = octaves(temp);
+  const double base = plain ? __builtin_ceil(in_octaves(value_of(top), c)) : -1e300;
+  if (t == 0) out.base[slot] = base;
+  int bin[8];
+  uint32_t place[8];
+  if (plain) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const double v2 = in_octaves(v[j], c);
+      bin[j] = bin_of(quarter(v2), base);
+      if (bin[j] < kBins - 1) {  // what is below counts nothing
+        place[j] = atomicAdd(&count[bin[j]], 1u);
+        if (!only_count) atomicAdd(&mass[bin[j]], (unsigned long long)fixed_of(exp2_of(v2 - base)));
+      }
+    }
+  }
+  __syncthreads();
+  // sums up to and with each bin
+  uint32_t n = 0;
+  uint64_t m = 0;
+  if (t < kBins) {
+    n = (uint32_t)wave_scan64(count[t]);
+    m = wave_scan64(mass[t]);
+    if ((t & 63) == 63) {
+      waves[t >> 6] = n;
+      wave_mass[t >> 6] = m;
+    }
+  }
+  __syncthreads();
+  if (t < kBins) {
+    for (int w = 0; w < (t >> 6); ++w) {
+      n += waves[w];
+      m += wave_mass[w];
+    }
+    before[t] = n - count[t];
+    out.count[slot * kBins + t] = (uint16_t)n;
+    if (!only_count) out.mass[slot * kBins + t] = m;
+  }
+  __syncthreads();
+  if (!plain) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (bin[j] < kBins - 1) order[before[bin[j]] + place[j]] = (uint16_t)(t * 8 + j);
+  __syncthreads();
+  if ((uint32_t)t * 8 < before[kBins - 1])
+    *reinterpret_cast<uint4*>(out.order + slot * kPart + t * 8) = *reinterpret_cast<const uint4*>(order + t * 8);
+}
+
 // A token's place in the order: value first, then its number
 __device__ __forceinline__ uint64_t place_of(uint32_t key, int token) {
   return ((uint64_t)key << 32) | (uint32_t)~token;
@@ -256,6 +287,7 @@ struct RowShared {
   uint32_t top[kMostParts * kBlocks];  // of their blocks
   uint16_t todo[kMostParts * kBlocks];  // blocks to walk over
   int down[kMostParts];             // octaves from the row's base down to the part's
+  int first[kMostParts], until[kMostParts];  // of the parts' tokens in a walk: in their order, and summed up
   unsigned long long kept[kMostParts];  // mass of a part's kept tokens
   unsigned long long mass[kBins];   // in the row's unit, up to and with the bin
   uint32_t count[kBins];
@@ -467,6 +499,7 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
   }
   __syncthreads();
   const bool by_k = k < a.n, by_p = top_p < 1.0f, by_min = min_p > 0.0f;
+  uint64_t full = 0;
   bool few = false;  // all that may be kept is in the list
   int have = 0;      // tokens there
   uint32_t key_lo = 0;
@@ -497,18 +530,18 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
 
   // the row's histogram: four threads a bin
   const bool only_count = without_mass(a, k);
-  auto add_parts = [&](bool counts, bool masses) {
+  auto add_parts = [&]() {
     const int r = t & (kBins - 1);
     uint64_t m = 0;
     uint32_t n = 0;
-    if (r < kBins - 1 && counts)
+    if (r < kBins - 1)
 #pragma unroll 10
       for (int p = t / kBins; p < parts; p += kRowThreads / kBins) {
         const int j = r - 4 * s.down[p];
         const uint32_t pn = in.count[(row * parts + p) * kBins + max(j, 0)];
         n += j >= 0 ? pn : 0;
       }
-    if (r < kBins - 1 && masses)
+    if (r < kBins - 1 && !only_count)
 #pragma unroll 10
       for (int p = t / kBins; p < parts; p += kRowThreads / kBins) {
         const int down = s.down[p], j = r - 4 * down;
@@ -517,19 +550,6 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
       }
     if (n) atomicAdd(&s.count[r], n);
     if (m) atomicAdd(&s.mass[r], (unsigned long long)m);
-  };
-  // sums up to and with each bin (the last bin has the rest of the tokens, and no mass)
-  uint64_t full = 0;
-  auto add_bins = [&](bool counts) {
-    const uint64_t mn[2] = {t < kBins ? s.mass[t] : 0, t < kBins ? s.count[t] : 0};
-    uint64_t before[2], total[2];
-    scan64<2>(mn, before, total, s.red);
-    full = total[0];
-    if (t < kBins) {
-      s.mass[t] = before[0] + mn[0];
-      if (counts) s.count[t] = t == kBins - 1 ? (uint32_t)a.n : (uint32_t)(before[1] + mn[1]);
-    }
-    __syncthreads();
   };
   const double v2_top = in_octaves(value_of(top), c);
   const double least = by_min ? v2_top + log2((double)fminf(min_p, 1.0f)) : -1e308;  // of v2
@@ -565,38 +585,69 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
     return want ? want : 1;
   };
 
-  if (!few) {
-    add_parts(true, !only_count);
+  // Tokens of the bins from b0 to b1: where each part has its own, and how many there are
+  auto set_walk = [&](int b0, int b1) {
+    uint64_t n = 0;
+    if (t < parts) {
+      const int64_t at = (row * parts + t) * kBins;
+      const int j0 = b0 - 4 * s.down[t] - 1, j1 = b1 - 4 * s.down[t];
+      const int first = j0 >= 0 ? in.count[at + j0] : 0;
+      n = j1 >= 0 ? in.count[at + j1] - first : 0;
+      s.first[t] = first;
+    }
+    uint64_t all;
+    const uint64_t before = scan64(n, s.red, &all);
+    if (t < parts) {
+      s.first[t] -= (int)before;
+      s.until[t] = (int)(before + n);
+    }
     __syncthreads();
-    add_bins(true);
+    return (int)all;
+  };
+  // the i-th of them
+  auto token_at = [&](int i) {
+    int p = 0;
+    for (int step = kMostParts / 2; step; step >>= 1)
+      if (p + step <= parts - 1 && s.until[p + step - 1] <= i) p += step;
+    return p * kPart + in.order[(row * parts + p) * kPart + s.first[p] + i];
+  };
+  auto walk_bins = [&](int n, auto f) {
+    for (int i = t; i < n; i += kRowThreads * kAhead) {
+      int token[kAhead];
+      float y[kAhead];
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e) token[e] = token_at(min(i + e * kRowThreads, n - 1));
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e) y[e] = one_logit<S>(a, row, token[e]);
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e)
+        if (i + e * kRowThreads < n) f(i + e * kRowThreads, token[e], y[e]);
+    }
+  };
+  // into the list, which has room
+  auto gather_bins = [&](int b0, int b1) {
+    const int n = set_walk(b0, b1);
+    walk_bins(min(n, kList), [&](int i, int token, float y) { s.list[i] = place_of(key_of(y), token); });
+    __syncthreads();
+    return min(n, kList);
+  };
+
+  if (!few) {
+    add_parts();
+    __syncthreads();
+    if (t == kBins - 1) s.count[t] = (uint32_t)a.n;
+    if (t == kBins - 1) s.mass[t] = s.mass[t - 1];
+    __syncthreads();
+    full = s.mass[kBins - 1];
     int bin_last = kBins - 1;
     if (by_k) bin_last = bin_at_count((uint64_t)k);
     if (by_p && !by_k) bin_last = bin_at_mass(mass_wanted(full));
     if (!by_p || !by_k) bin_last = min(bin_last, bin_min);
     bin_last = min(bin_last, kBins - 2);  // what is below weighs nothing
-    const float lo = lowest(bin_last);
     few = s.count[bin_last] <= kList;
     if (few) {
-      key_lo = key_of(lo);
-      have = gather_row<S>(a, row, blocks, s, lo, INFINITY);
-    } else if (only_count) {
-      // very many tokens at the end of a top-k (they share one value, or nearly): the masses
-      // that the first launch left out
-      for (int i = t; i < parts * kBins; i += kRowThreads) in.mass[row * parts * kBins + i] = 0;
-      __threadfence();
-      __syncthreads();
-      walk_row<S>(a, row, blocks, s, lo, INFINITY, [&](int token, float y) {
-        const int p = token / kPart, bin = bin_of(quarter(in_octaves(y, c)), s.base[p]);
-        atomicAdd(reinterpret_cast<unsigned long long*>(&in.mass[(row * parts + p) * kBins + bin]),
-                  (unsigned long long)weigh(p, y));
-      });
-      __threadfence();
-      __syncthreads();
-      if (t < kBins) s.mass[t] = 0;
-      __syncthreads();
-      add_parts(false, true);
-      __syncthreads();
-      add_bins(false);
+      key_lo = key_of(lowest(bin_last));
+      have = gather_bins(0, bin_last);
     }
   }
 
@@ -609,6 +660,7 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
   // Places of the last tokens that top-k and top-p keep, the earlier of them in `cut` (0:
   // everything that weighs), and the mass of what is kept.
   uint64_t cut = 0, mass = full;
+  int cut_bin = kBins - 1;
   int list_bin = -1;    // whose tokens the list has, where it has not all
   bool ranked = false;  // the list is few enough to be in s.few, with its sums
 #pragma unroll 1
@@ -626,13 +678,15 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
     uint64_t inside = have, n_before = 0, m_before = 0;
     uint64_t lo = (uint64_t)key_lo << 32, hi = ((uint64_t)top << 32) | 0xFFFFFFFFu;
     if (!few) {
-      const int bin = by_count ? bin_at_count(want) : bin_at_mass(want);
+      const int bin = cut_bin = by_count ? bin_at_count(want) : bin_at_mass(want);
       if (bin == kBins - 1) continue;  // only what weighs nothing is cut off
       n_before = bin ? s.count[bin - 1] : 0;
       m_before = bin ? s.mass[bin - 1] : 0;
       inside = s.count[bin] - n_before;
-      if (inside <= kList) {
-        have = gather_row<S>(a, row, blocks, s, lowest(bin), lowest(bin - 1));
+      if (inside > kList) {
+        set_walk(bin, bin);
+      } else {
+        have = gather_bins(bin, bin);
         weigh_list();
         list_bin = bin;
       }
@@ -640,6 +694,7 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
       hi = ((uint64_t)(key_of(lowest(bin - 1)) - 1) << 32) | 0xFFFFFFFFu;
     }
     const bool in_list = inside <= kList;
+    const int in_bin = (int)inside;
     // narrower by 256 at a time, until a wave can order the few that are left
     while (!ranked) {
       const bool order = inside <= 64;
@@ -677,11 +732,10 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
       if (in_list) {
         for (int i = t; i < have; i += kRowThreads) add(s.list[i], s.list_mass[i]);
       } else {
-        walk_row<S>(a, row, blocks, s, value_of((uint32_t)(lo >> 32)), value_of((uint32_t)(hi >> 32) + 1),
-                    [&](int token, float y) {
-                      const int p = token / kPart;
-                      add(place_of(key_of(y), token), to_row(p, weigh(p, y)));
-                    });
+        walk_bins(in_bin, [&](int, int token, float y) {
+          const int p = token / kPart;
+          add(place_of(key_of(y), token), to_row(p, weigh(p, y)));
+        });
       }
       __syncthreads();
       if (order) break;
@@ -740,6 +794,22 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
     __syncthreads();
     cut = s.out[0] > cut ? s.out[0] : cut;
     if (by_count) mass = s.out[1];
+    if (!few && only_count) {  // what top-k keeps: there was no room for all of its last bin
+      if (t == 0) s.fill = 0;
+      const int n = set_walk(0, cut_bin);
+      walk_bins(n, [&](int, int token, float y) {
+        const uint64_t place = place_of(key_of(y), token);
+        if (place < cut) return;
+        const uint32_t at = atomicAdd(&s.fill, 1u);
+        if (at < kList) s.list[at] = place;
+      });
+      __syncthreads();
+      have = min((int)s.fill, kList);
+      few = true;
+      key_lo = (uint32_t)(cut >> 32);
+      weigh_list();
+      __syncthreads();
+    }
   }
 
   if (few) {
@@ -808,14 +878,10 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
     if (place_of(key_of(y), token) < cut) return false;
     return !by_min || in_octaves(y, c) >= least || key_of(y) == top;
   };
-  // a wave a part: the bins before the last one, in the part's own unit
-  for (int p = t >> 6; p < parts; p += kRowThreads / 64) {
-    uint64_t m = 0;
-#pragma unroll
-    for (int j = 0; j < kBins; j += 64)
-      if (j + lane + 4 * s.down[p] < last) m += in.mass[(row * parts + p) * kBins + j + lane];
-    m = wave_scan64(m);
-    if (lane == 63) s.kept[p] = m;
+  // the bins before the last one, in the part's own unit
+  if (t < parts) {
+    const int b = min(last, kBins - 1) - 1 - 4 * s.down[t];
+    s.kept[t] = b >= 0 ? in.mass[(row * parts + t) * kBins + b] : 0;
   }
   __syncthreads();
   if (last < kBins - 1) {
@@ -825,7 +891,7 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
     if (last == list_bin) {
       for (int i = t; i < have; i += kRowThreads) add(token_of(s.list[i]), logit_of(s.list[i]));
     } else {
-      walk_row<S>(a, row, blocks, s, last_lo, last_hi, add);
+      walk_bins(set_walk(last, last), [&](int, int token, float y) { add(token, y); });
     }
   }
   __syncthreads();
