@@ -41,9 +41,18 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256;
 constexpr float kEmpty = -1e30f;   // a maximum of nothing
-constexpr float kRaise = 8.0f;     // log2 of what p may reach
+// log2 of what p may reach.  Where scores are so large that this is less than a step of
+// theirs, it may come to twice as much, which FP16 still holds.
+constexpr float kRaise = 7.0f;
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// To the nearest: cut off, p would put the result 2.5e-4 off (relative, FP16's own rounding being
+// 2.1e-4), so 2e-4 at most
+__device__ __forceinline__ f16x2 to_f16x2(float a, float b) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  return __builtin_convertvector((f32x2{a, b}), f16x2);
+}
 
 // over the four groups of 16 lanes
 __device__ __forceinline__ float as_float(uint32_t v) { return __builtin_bit_cast(float, v); }
@@ -395,9 +404,8 @@ __device__ __forceinline__ void weigh(State<D, NR>& st, f16x8 (&p)[NR], const f3
       f16x2 pk[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        pk[e] = __builtin_bit_cast(
-            f16x2, __builtin_amdgcn_cvt_pkrtz(exp2_fast(x[n][e >> 1][2 * (e & 1)] - st.m[n0 + n]),
-                                              exp2_fast(x[n][e >> 1][2 * (e & 1) + 1] - st.m[n0 + n])));
+        pk[e] = to_f16x2(exp2_fast(x[n][e >> 1][2 * (e & 1)] - st.m[n0 + n]),
+                         exp2_fast(x[n][e >> 1][2 * (e & 1) + 1] - st.m[n0 + n]));
       p[n0 + n] = join(pk[0], pk[1], pk[2], pk[3]);
       // the sum of the rounded p, as the product with V takes them
 #pragma unroll
