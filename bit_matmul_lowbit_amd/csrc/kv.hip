@@ -402,6 +402,8 @@ __device__ __forceinline__ void values8(uint32_t w, uint32_t params, float (&v)[
   }
 }
 
+constexpr int kAhead = 4;  // pieces of K that a thread has on their way
+
 template <bool FOUR>
 __global__ __launch_bounds__(kThreads) void kv_load_kernel(KvLoadArgs a, KvGrid g) {
   const int64_t first = (int64_t)blockIdx.x * g.tokens;
@@ -415,6 +417,42 @@ __global__ __launch_bounds__(kThreads) void kv_load_kernel(KvLoadArgs a, KvGrid 
   const int64_t page_bytes = a.heads * lay.bytes();
   const int kTok = values && FOUR ? 4 : 1;
   const int items = (tokens + kTok - 1) / kTok * per_token;
+  if (!values) {
+    for (int i0 = threadIdx.x; i0 < items; i0 += kAhead * kThreads) {
+      int64_t to[kAhead];
+      int slot[kAhead], head[kAhead], piece[kAhead];
+      uint32_t codes[kAhead], params[kAhead];
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e) {
+        const int i = min(i0 + e * kThreads, items - 1);
+        const int t = quotient(i, g.by_token), r = i - t * per_token;
+        const int h = quotient(r, g.by_head);
+        piece[e] = r - h * per_head;
+        head[e] = i0 + e * kThreads < items && h < heads ? head0 + h : -1;
+        slot[e] = a.slots[first + t];
+        to[e] = (first + t) * a.ldk + (head0 + h) * a.ldkh + piece[e] * 8;
+      }
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e) {
+        int64_t at;
+        int in;
+        codes[e] = params[e] = 0;
+        if (place_of(slot[e], g.shift, a.n_pages, &at, &in) && head[e] >= 0) {
+          const uint8_t* from = a.pages + at * page_bytes + (int64_t)head[e] * lay.bytes();
+          codes[e] = reinterpret_cast<const uint32_t*>(from)[in * (d / 8) + piece[e]];
+          params[e] = reinterpret_cast<const uint32_t*>(from + lay.k_params())[in * (d / 32) + (piece[e] >> 2)];
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e) {
+        if (head[e] < 0) continue;
+        float v[8];
+        values8(codes[e], params[e], v);
+        store8(a.k, a.out_type, to[e], 0, v);
+      }
+    }
+    return;
+  }
   for (int i = threadIdx.x; i < items; i += kThreads) {
     const int t = quotient(i, g.by_token), r = i - t * per_token;
     const int h = quotient(r, g.by_head), p = r - h * per_head;
@@ -423,18 +461,6 @@ __global__ __launch_bounds__(kThreads) void kv_load_kernel(KvLoadArgs a, KvGrid 
     int64_t at;
     int in;
     float v[8];
-    if (!values) {
-      const int64_t to = (first + t) * a.ldk + (head0 + h) * a.ldkh + p * 8;
-      uint32_t codes = 0, params = 0;
-      if (place_of(a.slots[first + t], g.shift, a.n_pages, &at, &in)) {
-        const uint8_t* head = a.pages + at * page_bytes + off;
-        codes = reinterpret_cast<const uint32_t*>(head)[in * (d / 8) + p];
-        params = reinterpret_cast<const uint32_t*>(head + lay.k_params())[in * (d / 32) + (p >> 2)];
-      }
-      values8(codes, params, v);
-      store8(a.k, a.out_type, to, 0, v);
-      continue;
-    }
     const int64_t token = first + t * kTok;
     const int have = min(kTok, tokens - t * kTok);
     if constexpr (FOUR) {
@@ -518,9 +544,12 @@ hipError_t launch_kv_store(const KvStoreArgs& a, hipStream_t st) {
     r.rot = a.rot;
     r.inter = a.inter;
     g.q = rope_grid(r, a.q_out == a.q);
-    // the token groups of the cache's part; as many heads as make up its pieces
+    // The token groups of the cache's part, and as many heads as make up its pieces; four times
+    // as many where there is work for all, since each work-group has the cosines to make (4096
+    // tokens, 32 heads of 128: 29.7 -> 28.6 us; 61 tokens, 24 heads of 256 would take 14 for 6)
     g.q.tokens = g.tokens;
-    const int64_t target = max((int64_t)kSmall, (int64_t)g.tokens * g.heads * a.d / 8);
+    const bool many = a.m * (a.heads * a.d / 8) > 512 * kSmall;
+    const int64_t target = many ? 16 * kThreads : max((int64_t)kSmall, (int64_t)g.tokens * g.heads * a.d / 8);
     g.q.heads = (int)max((int64_t)1, min(a.hq, target / ((int64_t)g.tokens * g.q.pieces.all)));
     g.q.by_token = divide(g.q.heads * g.q.pieces.all);
     g.q_parts = (int)((a.hq + g.q.heads - 1) / g.q.heads);
