@@ -29,13 +29,10 @@ namespace lowbit {
 namespace {
 
 constexpr int kPart = 4096;      // logits of a part
-constexpr int kBlock = 512;      // logits of a block: eight a lane
-constexpr int kBlocks = kPart / kBlock;
-constexpr int kPartThreads = 64 * kBlocks;
+constexpr int kPartThreads = kPart / 8;
 constexpr int kBins = 256;       // quarters of an octave; the last one: everything below
 constexpr int kRowThreads = 1024;
 constexpr int kMostParts = 256;
-constexpr int kAhead = 4;        // blocks that a wave loads ahead
 constexpr int kList = 8192;      // tokens that are held in LDS
 constexpr int kUnit = 51;        // a part's weights are whole numbers of 2^-51: 4096 of them stay below 2^64
 
@@ -90,7 +87,7 @@ __device__ __forceinline__ double in_octaves(float y, double c) {
 // what the first launch leaves of a part
 struct Parts {
   double* base;      // [rows][parts]: weights are relative to 2^base
-  uint32_t* top;     // [rows][parts][kPart / kBlock]: the largest key of a block
+  uint32_t* top;     // [rows][parts]: the largest key
   uint64_t* mass;    // [rows][parts][kBins]: up to and with the bin
   uint16_t* count;   // [rows][parts][kBins]: likewise
   uint16_t* order;   // [rows][parts][kPart]: the part's tokens by their bins
@@ -99,7 +96,7 @@ __host__ __device__ inline size_t align_up(size_t v) { return (v + 255) / 256 * 
 inline size_t parts_layout(int64_t rows, int64_t parts, void* ws, Parts* p) {
   char* at = static_cast<char*>(ws);
   const size_t n = (size_t)(rows * parts);
-  const size_t mass = align_up(n * kBins * 8), count = align_up(n * kBins * 2), base = align_up(n * 8), top = align_up(n * kBlocks * 4);
+  const size_t mass = align_up(n * kBins * 8), count = align_up(n * kBins * 2), base = align_up(n * 8), top = align_up(n * 4);
   const size_t order = align_up(n * kPart * 2);
   if (p) {
     p->mass = reinterpret_cast<uint64_t*>(at);
@@ -134,9 +131,6 @@ __device__ __forceinline__ void load_logits(const void* y, int type, int64_t at,
     }
   }
 }
-
-// ---------------------------------------------------------------------------
-// one work-group a row
 
 // The lanes' sums up to and with each, by DPP (no LDS round trips)
 template <int CTRL, int ROWS>
@@ -200,7 +194,7 @@ template <int S>
 __global__ __launch_bounds__(kPartThreads) void sample_parts_kernel(SampleArgs a, Parts out) {
   __shared__ unsigned long long mass[kBins];
   __shared__ uint32_t count[kBins], before[kBins];
-  __shared__ uint32_t tops[kBlocks], waves[kBins / 64];
+  __shared__ uint32_t tops[kPartThreads / 64], waves[kBins / 64];
   __shared__ unsigned long long wave_mass[kBins / 64];
   __shared__ __align__(16) uint16_t order[kPart];
   const int64_t row = blockIdx.y, part = blockIdx.x, slot = row * gridDim.x + part;
@@ -219,13 +213,11 @@ __global__ __launch_bounds__(kPartThreads) void sample_parts_kernel(SampleArgs a
   for (int j = 0; j < 8; ++j) top = max(top, key_of(v[j]));
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
-  if ((t & 63) == 0) {
-    tops[t >> 6] = top;
-    out.top[slot * kBlocks + (t >> 6)] = top;
-  }
+  if ((t & 63) == 0) tops[t >> 6] = top;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kBlocks; ++w) top = max(top, tops[w]);
+  for (int w = 0; w < kPartThreads / 64; ++w) top = max(top, tops[w]);
+  if (t == 0) out.top[slot] = top;
   // greedy rows, and rows with NaN or infinity, go by the maximum alone
   const bool plain = temp != 0.0f && top < kKeyInf && top > kKeyNegInf;
   if (temp == 0.0f || top >= kKeyInf) return;
@@ -284,8 +276,7 @@ __device__ __forceinline__ uint64_t place_of(uint32_t key, int token) {
 
 struct RowShared {
   double base[kMostParts];          // of the parts
-  uint32_t top[kMostParts * kBlocks];  // of their blocks
-  uint16_t todo[kMostParts * kBlocks];  // blocks to walk over
+  uint32_t top[kMostParts];
   int down[kMostParts];             // octaves from the row's base down to the part's
   int first[kMostParts], until[kMostParts];  // of the parts' tokens in a walk: in their order, and summed up
   unsigned long long kept[kMostParts];  // mass of a part's kept tokens
@@ -296,7 +287,7 @@ struct RowShared {
   uint64_t red[2][16];
   uint64_t list[kList], list_mass[kList], few[64], few_mass[64];
   uint64_t out[4];
-  uint32_t fill, found, walk;
+  uint32_t fill, found;
   int pick;
 };
 
@@ -308,127 +299,14 @@ __device__ __forceinline__ float one_logit(const SampleArgs& a, int64_t row, int
   else return (float)static_cast<const bf16_t*>(a.y)[o];
 }
 
-// Which of eight values have lo <= value < hi (a NaN hi: lo and above).  lo is above -inf, which
-// fills up the row's last eight.
-__device__ __forceinline__ uint32_t hits_of(const float (&v)[8], float lo, float hi) {
-  uint32_t hits = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) hits |= v[j] >= lo && !(v[j] >= hi) ? 1u << j : 0;
-  return hits;
-}
-__device__ __forceinline__ float pick(const float (&v)[8], int j) {
-  const float a = j & 1 ? v[1] : v[0], b = j & 1 ? v[3] : v[2], c = j & 1 ? v[5] : v[4], d = j & 1 ? v[7] : v[6];
-  const float e = j & 2 ? b : a, f = j & 2 ? d : c;
-  return j & 4 ? f : e;
-}
-
-// Eight values of a row, from `from` on or the row's last; a row of fewer is filled up with -inf
-template <int S>
-__device__ __forceinline__ Raw8<S> load_inside(const SampleArgs& a, int64_t row, int from) {
-  if (a.n >= 8) return load8<S>(a.y, row * a.ldy + min(from, (int)a.n - 8));
-  Raw8<S> r;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int64_t at = row * a.ldy + j;
-    if constexpr (S == 4) {
-      r.d[j] = j < a.n ? static_cast<const uint32_t*>(a.y)[at] : 0xFF800000u;
-    } else {
-      const uint32_t h = j < a.n ? static_cast<const uint16_t*>(a.y)[at] : a.y_type == 2 ? 0xFC00u : 0xFF80u;
-      r.d[j >> 1] = j & 1 ? r.d[j >> 1] | h << 16 : h;
-    }
-  }
-  return r;
-}
-
-// Calls f(from, values) for the blocks that have values of lo and above; a lane has eight
-// values, from `from` on
-template <int S, class F>
-__device__ __forceinline__ void walk_blocks(const SampleArgs& a, int64_t row, int blocks, RowShared& s, float lo, F f) {
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  const uint32_t least = key_of(lo);
-  if (t == 0) s.walk = 0;
-  __syncthreads();
-  for (int b = t; b < blocks; b += kRowThreads)
-    if (s.top[b] >= least) s.todo[atomicAdd(&s.walk, 1u)] = (uint16_t)b;
-  __syncthreads();
-  const int n = (int)s.walk;
-#pragma unroll 1
-  for (int i = wave; i < n; i += kRowThreads / 64 * kAhead) {
-    // loads without a branch, which would wait for each: at the row's end its last eight
-    Raw8<S> raw[kAhead];
-    int block[kAhead];
-#pragma unroll
-    for (int e = 0; e < kAhead; ++e) {
-      const int k = i + e * (kRowThreads / 64);
-      block[e] = __builtin_amdgcn_readfirstlane((int)s.todo[k < n ? k : i]);
-      raw[e] = load_inside<S>(a, row, block[e] * kBlock + lane * 8);
-    }
-#pragma unroll
-    for (int e = 0; e < kAhead; ++e) {
-      if (i + e * (kRowThreads / 64) >= n) break;
-      const int from = block[e] * kBlock + lane * 8;
-      int at = from;
-      float v[8];
-      widen<S>(raw[e], a.y_type, v);
-      if ((int64_t)(block[e] + 1) * kBlock > a.n) {
-        at = min(from, max((int)a.n - 8, 0));
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = j < from - at ? -INFINITY : v[j];
-      }
-      f(at, v);
-    }
-  }
-}
-
-// Calls f(token, value) for the tokens with lo <= value < hi
-template <int S, class F>
-__device__ __forceinline__ void walk_row(const SampleArgs& a, int64_t row, int blocks, RowShared& s, float lo, float hi,
-                                         F f) {
-  walk_blocks<S>(a, row, blocks, s, lo, [&](int from, float (&v)[8]) {
-    for (uint32_t hits = hits_of(v, lo, hi); hits; hits &= hits - 1) {
-      const int j = __builtin_ctz(hits);
-      f(from + j, pick(v, j));
-    }
-  });
-}
-
-// The places of those tokens into s.list, which has room for kList; returns their number
-template <int S>
-__device__ __forceinline__ int gather_row(const SampleArgs& a, int64_t row, int blocks, RowShared& s, float lo,
-                                          float hi) {
-  if (threadIdx.x == 0) s.fill = 0;
-  walk_blocks<S>(a, row, blocks, s, lo, [&](int from, float (&v)[8]) {
-    // one atomic a wave and block
-    uint64_t hits[8];
-    uint32_t all = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      hits[j] = __builtin_amdgcn_ballot_w64(v[j] >= lo && !(v[j] >= hi));
-      all += __builtin_popcountll(hits[j]);
-    }
-    if (all == 0) return;
-    uint32_t at = 0;
-    if ((threadIdx.x & 63) == 0) at = atomicAdd(&s.fill, all);
-    at = (uint32_t)__builtin_amdgcn_readfirstlane((int)at);
-    if (at + all > kList) return;  // too many: the list is of no use
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (v[j] >= lo && !(v[j] >= hi))
-        s.list[at + __builtin_amdgcn_mbcnt_hi((uint32_t)(hits[j] >> 32),
-                                              __builtin_amdgcn_mbcnt_lo((uint32_t)hits[j], 0))] =
-            place_of(key_of(v[j]), from + j);
-      at += __builtin_popcountll(hits[j]);
-    }
-  });
-  __syncthreads();
-  return (int)s.fill < kList ? (int)s.fill : kList;
-}
-
 // u in [0, 1) of w, rounded down
 __device__ __forceinline__ uint64_t share_of(uint64_t w, float u) {
   const float x = u > 0.0f ? fminf(u, 0x1.fffffep-1f) : 0.0f;
   return __umul64hi(w, (uint64_t)((double)x * 0x1p64));
 }
+
+// ---------------------------------------------------------------------------
+// a row's draw
 
 template <int S>
 __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, Parts in, int parts, int unit) {
@@ -440,9 +318,8 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
   const float temp = temperature_of(a, row);
   const int64_t k = top_k_of(a, row);
   const float top_p = a.top_p ? a.top_p[row] : 1.0f, min_p = a.min_p ? a.min_p[row] : 0.0f, u = a.u[row];
-  const int blocks = parts * kBlocks;
-  for (int b = t; b < blocks; b += kRowThreads) s.top[b] = in.top[row * blocks + b];
   for (int p = t; p < parts; p += kRowThreads) {
+    s.top[p] = in.top[row * parts + p];
     s.base[p] = in.base[row * parts + p];
     s.kept[p] = 0;
   }
@@ -454,24 +331,22 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
   __syncthreads();
   uint32_t top = kKeyNegInf;
   double base = -1e300;
-  for (int b = lane; b < blocks; b += 64) top = max(top, s.top[b]);
-  for (int p = lane; p < parts; p += 64) base = fmax(base, s.base[p]);
+  for (int p = lane; p < parts; p += 64) {
+    top = max(top, s.top[p]);
+    base = fmax(base, s.base[p]);
+  }
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     top = max(top, (uint32_t)__shfl_xor((int)top, d));
     base = fmax(base, __shfl_xor(base, d));
   }
   if (temp == 0.0f || top >= kKeyInf || top == kKeyNegInf) {
-    // the lowest token of the largest value
-    if (top == 0xFFFFFFFFu) {  // NaN, which no comparison finds
-      for (int b = t >> 6; b < blocks; b += kRowThreads / 64) {
-        if (s.top[b] != top) continue;
-        for (int64_t at = (int64_t)b * kBlock + lane; at < (int64_t)(b + 1) * kBlock && at < a.n; at += 64)
-          if (key_of(one_logit<S>(a, row, at)) == top) atomicMin(&s.found, (uint32_t)at);
-      }
-    } else if (top != kKeyNegInf) {
-      walk_row<S>(a, row, blocks, s, value_of(top), __builtin_nanf(""),
-                  [&](int token, float) { atomicMin(&s.found, (uint32_t)token); });
+    // the lowest token of the largest value, in the first part that has it
+    if (top > kKeyNegInf) {
+      int p = 0;
+      while (s.top[p] != top) ++p;
+      for (int64_t at = (int64_t)p * kPart + t; at < (int64_t)(p + 1) * kPart && at < a.n; at += kRowThreads)
+        if (key_of(one_logit<S>(a, row, at)) == top) atomicMin(&s.found, (uint32_t)at);
     }
     __syncthreads();
     if (t == 0) {
@@ -498,59 +373,33 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
     s.down[p] = d < 1000.0 ? (int)d : 1000;
   }
   __syncthreads();
-  const bool by_k = k < a.n, by_p = top_p < 1.0f, by_min = min_p > 0.0f;
-  uint64_t full = 0;
-  bool few = false;  // all that may be kept is in the list
-  int have = 0;      // tokens there
-  uint32_t key_lo = 0;
-
-  // A small top-k: the tokens from the k-th largest block's maximum on, which are k at least
-  // and hardly more.  Each block against half of them a thread.
-  if (by_k && k <= blocks / 2 && blocks <= kRowThreads / 2) {
-    uint32_t* rank = reinterpret_cast<uint32_t*>(s.list);
-    const int b = t % (kRowThreads / 2);
-    if (t < kRowThreads / 2) rank[t] = 0;
-    __syncthreads();
-    if (b < blocks) {
-      const uint32_t own = s.top[b];
-      const int from = t < kRowThreads / 2 ? 0 : blocks / 2, to = t < kRowThreads / 2 ? blocks / 2 : blocks;
-      uint32_t larger = 0;
-#pragma unroll 8
-      for (int i = from; i < to; ++i) larger += s.top[i] > own || (s.top[i] == own && i < b) ? 1 : 0;
-      atomicAdd(&rank[b], larger);
-    }
-    __syncthreads();
-    if (t < blocks && rank[t] == (uint32_t)k - 1) s.pick = t;
-    __syncthreads();
-    const uint32_t key = s.top[s.pick];
-    key_lo = key > kKeyNegInf ? key : kKeyNegInf + 1;
-    have = gather_row<S>(a, row, blocks, s, value_of(key_lo), INFINITY);
-    few = s.fill <= kList;
-  }
-
-  // the row's histogram: four threads a bin
-  const bool only_count = without_mass(a, k);
-  auto add_parts = [&]() {
+  // the row's sums up to and with each bin, four threads a bin; in the last bin there are
+  // the other tokens, without mass
+  const bool by_k = k < a.n, by_p = top_p < 1.0f, by_min = min_p > 0.0f, only_count = without_mass(a, k);
+  {
     const int r = t & (kBins - 1);
     uint64_t m = 0;
     uint32_t n = 0;
-    if (r < kBins - 1)
 #pragma unroll 10
-      for (int p = t / kBins; p < parts; p += kRowThreads / kBins) {
-        const int j = r - 4 * s.down[p];
-        const uint32_t pn = in.count[(row * parts + p) * kBins + max(j, 0)];
-        n += j >= 0 ? pn : 0;
-      }
-    if (r < kBins - 1 && !only_count)
+    for (int p = t / kBins; p < parts; p += kRowThreads / kBins) {
+      const int j = r - 4 * s.down[p];
+      const uint32_t pn = in.count[(row * parts + p) * kBins + max(j, 0)];
+      n += j >= 0 ? pn : 0;
+    }
+    if (!only_count)
 #pragma unroll 10
       for (int p = t / kBins; p < parts; p += kRowThreads / kBins) {
         const int down = s.down[p], j = r - 4 * down;
         const uint64_t pm = in.mass[(row * parts + p) * kBins + max(j, 0)];
         m += j >= 0 && down + up < 64 ? pm >> ((down + up) & 63) : 0;
       }
-    if (n) atomicAdd(&s.count[r], n);
+    if (n && r < kBins - 1) atomicAdd(&s.count[r], n);
     if (m) atomicAdd(&s.mass[r], (unsigned long long)m);
-  };
+    if (t == kBins - 1) s.count[t] = (uint32_t)a.n;
+  }
+  __syncthreads();
+  const uint64_t full = s.mass[kBins - 2];
+
   const double v2_top = in_octaves(value_of(top), c);
   const double least = by_min ? v2_top + log2((double)fminf(min_p, 1.0f)) : -1e308;  // of v2
   const int bin_min = by_min ? bin_of(quarter(least), base) : kBins - 1;
@@ -612,16 +461,9 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
     return p * kPart + in.order[(row * parts + p) * kPart + s.first[p] + i];
   };
   auto walk_bins = [&](int n, auto f) {
-    for (int i = t; i < n; i += kRowThreads * kAhead) {
-      int token[kAhead];
-      float y[kAhead];
-#pragma unroll
-      for (int e = 0; e < kAhead; ++e) token[e] = token_at(min(i + e * kRowThreads, n - 1));
-#pragma unroll
-      for (int e = 0; e < kAhead; ++e) y[e] = one_logit<S>(a, row, token[e]);
-#pragma unroll
-      for (int e = 0; e < kAhead; ++e)
-        if (i + e * kRowThreads < n) f(i + e * kRowThreads, token[e], y[e]);
+    for (int i = t; i < n; i += kRowThreads) {
+      const int token = token_at(i);
+      f(i, token, one_logit<S>(a, row, token));
     }
   };
   // into the list, which has room
@@ -632,23 +474,17 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
     return min(n, kList);
   };
 
-  if (!few) {
-    add_parts();
-    __syncthreads();
-    if (t == kBins - 1) s.count[t] = (uint32_t)a.n;
-    if (t == kBins - 1) s.mass[t] = s.mass[t - 1];
-    __syncthreads();
-    full = s.mass[kBins - 1];
-    int bin_last = kBins - 1;
-    if (by_k) bin_last = bin_at_count((uint64_t)k);
-    if (by_p && !by_k) bin_last = bin_at_mass(mass_wanted(full));
-    if (!by_p || !by_k) bin_last = min(bin_last, bin_min);
-    bin_last = min(bin_last, kBins - 2);  // what is below weighs nothing
-    few = s.count[bin_last] <= kList;
-    if (few) {
-      key_lo = key_of(lowest(bin_last));
-      have = gather_bins(0, bin_last);
-    }
+  int bin_last = kBins - 1;
+  if (by_k) bin_last = bin_at_count((uint64_t)k);
+  if (by_p && !by_k) bin_last = bin_at_mass(mass_wanted(full));
+  if (!by_p || !by_k) bin_last = min(bin_last, bin_min);
+  bin_last = min(bin_last, kBins - 2);  // what is below weighs nothing
+  bool few = s.count[bin_last] <= kList;  // all that may be kept is in the list
+  int have = 0;                           // tokens there
+  uint32_t key_lo = 0;
+  if (few) {
+    key_lo = key_of(lowest(bin_last));
+    have = gather_bins(0, bin_last);
   }
 
   // the masses of the list
