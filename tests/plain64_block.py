@@ -177,8 +177,7 @@ def attention(q, k, v, last, scale, out_dtype):
     A score is a sum of d products in FP32 in any order, scaled and reduced by
     the maximum: off by at most (d + 4) U of the sum of its terms' magnitudes.  p is
     then off by that much relative, by 2^-21 of the exponential, and by its
-    rounding to FP16 towards zero: 2^-10 relative, or all of what is below 2^-24 of
-    the largest.  Both sums are of the rounded p, so what is common to all p
+    rounding to FP16: 2^-11 relative, or 2^-25 of the largest where it is small.  Both sums are of the rounded p, so what is common to all p
     cancels: an error e of p_t moves the quotient by e |v_t - out|.  The sums over
     n tokens pass no term through more than n / 32 + 600 additions."""
     nq, hq, d = q.shape
@@ -198,7 +197,7 @@ def attention(q, k, v, last, scale, out_dtype):
             p = np.exp(s - s.max())
             total = p.sum()
             o = p @ vv / total
-            e = p * (es + 2.0 ** -21 + 2.0 ** -10) + np.minimum(p, 2.0 ** -24)
+            e = p * (es + 2.0 ** -21 + 2.0 ** -11) + np.minimum(p, 2.0 ** -25)
             depth = (m / 32 + 600) * U
             out[j, h] = o
             lse[j, h] = s.max() + np.log(total)
