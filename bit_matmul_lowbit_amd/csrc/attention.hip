@@ -6,10 +6,11 @@
 // unnormalised o stay in registers, FP32.
 //
 // Rows.  The queries of a KV head's `group` query heads read the same keys: a
-// tile is TT tokens (a power of two) by the group, up to RT = 16 NR or 64 NR rows.
+// tile is a power of two of tokens by the group (or a part of it), up to 16, 32 or 64
+// rows where the four waves of a work-group have the same rows and take the cache's tokens in
+// turn, and up to 128 (64 of 256 values) where each has rows of its own.
 //
-// Products.  Both are v_mfma_f32_16x16x32_f16 with the cache as the A operand
-// straight from memory, never through LDS:
+// Products.  Both are v_mfma_f32_16x16x32_f16 with the cache as the A operand:
 //   S^T = K Q^T : a lane holds, of one token, the quarter of the head that its
 //     16 lanes belong to -- d / 8 neighbouring bytes; Q is put in the order of
 //     the nibbles once.
@@ -17,21 +18,33 @@
 //     dword, so a lane has four tokens of d / 16 values in one load, and the
 //     tokens that it needs of P are those that S^T gave it: P is rounded to FP16
 //     and used where it is.
+// With few rows the codes go straight from memory to the lane that needs them, never
+// through LDS; with many, the four waves make an operand each and hand it round in LDS.
 // A code becomes FP16(a (1 + c / 16) + b) with a shift, a mask and half a packed
 // FMA: it is put into the mantissa of 1.0.  Keys and values of the cache are FP16
 // numbers by definition, so nothing is lost there; BF16 queries are scaled by a power
 // of two a row, which is exact.  The sum of p is a product with ones, of the same
 // rounded p.
 //
-// The maximum is raised only where a score passes it by 2^8 (p stays far
+// The maximum is raised only where a score passes it by 2^7 (p stays far
 // inside FP16), so most steps neither exchange lanes nor rescale o.
 //
-// Work.  All (sequence, KV head, tile) items are cut into units of kUnit
-// tokens, and the units of all items, one after another, are shared out evenly
-// over the work-groups from the lengths on the device: a work-group may end one item and
-// begin others.  An item that does not end where it began leaves its parts (m,
-// sum, o) in the workspace, and a second launch joins them in the order of their
-// work-groups.  No atomics; equal inputs give equal bits.
+// Work.  All (sequence, KV head, tile) items are cut into units of 128 tokens (or as
+// many as a tile has, if they are more), and the units of all items, one after another, are
+// shared out evenly over the work-groups from the lengths on the device: a work-group may
+// end one item and begin others.  An item that does not end where it began leaves its
+// parts (m, sum, o) in the workspace, and a second launch joins them in the order of
+// their work-groups.  No atomics; equal inputs give equal bits.
+//
+// Measured (a 1 GiB copy moves 5.2 TB/s, an 8192^3 product of the library 1.2 PFLOP/s here):
+//   one token over 262144, 24 heads on 4 of 256: 65 us and 8 for the join, 335 MB, the
+//     cache read at 5.2 TB/s: bound by memory
+//   16 chats, 1 to 32767 tokens, the same heads: 56 and 8 us
+//   one token over 4096, 16 heads on 8 of 128: 8.6 and 4.5 us: latency (the lists, q, three
+//     steps of loads and products, the join's launch)
+//   chunks of up to 2048 on three prompts, 32 heads on 8 of 128: 428 us, 700 TFLOP/s of the
+//     two products: what the exponentials and the rounding of p take from the matrix units' issue,
+//     with two waves a SIMD for the registers of o
 #include "kv4.h"
 
 namespace lowbit {
@@ -76,7 +89,7 @@ __device__ __forceinline__ list_t list_of(const int32_t* p) { return (list_t)(ui
 
 // What beginning an item costs, in units: an item counts as so many units more
 // than its tokens are.  (Three prompts of 8192, 2729 and 510 tokens, chunks of up to
-// 2048: 541 us without, @@ with one.)
+// 2048: 541 us without, 442 with one.)
 constexpr int kBegin = 1;
 
 // How rows and tokens are cut; made on the host.
@@ -878,8 +891,8 @@ __device__ __forceinline__ void spread_shared(f16x8* lds, Shared<D>& r, int len,
 
 // Many rows: every wave has kWaveRows of its own, and the four make the operands
 // of 32 tokens together, one step ahead, in two LDS buffers in turn (each wave
-// making all of them for itself, 64 rows a wave, was bound by that: 589 us where
-// this takes @@).
+// making all of them for itself, 64 rows a wave, was bound by that: three prompts in chunks of
+// 2048 took 1025 us, now 438).
 // A wave has 32 rows, or 16 of 256 values (32 of those and their q do not fit its registers).
 template <int D>
 constexpr int kManyTiles = D == 256 ? 1 : 2;
@@ -1241,12 +1254,23 @@ int log2_of(int64_t v) {
 
 // Which kernel, by the rows that a KV head's queries have at most in a sequence:
 // the waves split the tokens while one of them can hold the rows (nr tiles of 16),
-// beyond they split the rows.
+// beyond they split the rows.  Both sides, us a call replayed from a graph:
+//   up to 16 rows, for 16 or 32: one chat of 4096 14.5 and 16.7, of 262144 84 and 97,
+//     16 mixed chats 72 and 84
+//   17 to 32, for 32 or 64: 8 tokens of a chat of 4096 18 and 27, of 16 chats 49 and 74;
+//     4 tokens of 16 mixed chats, heads of 256, 94 and 158
+//   33 to 64, split by tokens or by rows: 16 tokens of a chat of 4096 29 and 39, of 32768 52
+//     and 74, of four of those 93 and 125; but of 16 chats of 4096 90 and 73.  The lengths are on
+//     the device; the longer ones decide.  (Heads of 256 would need 64 more registers.)
+//   beyond: chunks of 2048 of three prompts 438 by rows, 1025 by tokens; 128 rows of a chat of
+//     4096 39 and 36
 struct Variant {
   int nr;  // 0: attn_rows_kernel
   int rows;
 };
-constexpr int kWgs = 512;  // two a unit
+// Two a unit.  Half as many take 641 us for those chunks, 768 take 470 (and 90 for the chat of
+// 262144, whose parts are more).
+constexpr int kWgs = 512;
 Variant variant_of(int64_t group, int64_t d, int64_t max_q) {
   const int64_t rows = group * max_q;
   if (rows <= 16) return {1, 16};
