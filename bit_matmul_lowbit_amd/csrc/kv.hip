@@ -265,13 +265,19 @@ struct KvGrid {
   Divide by_head, by_token;  // pieces of a head, of a work-group's heads of one token
 };
 
-// Eight elements of head h of token t, turned where they have to be
+// Eight elements of a head from `c` on, and those that they turn with in the half layout
 template <int S>
-__device__ __forceinline__ void key_piece(const KvStoreArgs& a, int64_t token, int h, int p, const float2* cs,
-                                          float (&v)[8]) {
-  const int64_t at = token * a.ldk + h * a.ldkh;
-  const int c = p * 8, half = (int)a.rot / 2;
-  widen<S>(load8<S>(a.k, at + c), a.in_type, v);
+__device__ __forceinline__ void load_key(const KvStoreArgs& a, int64_t at, int c, Raw8<S>* own, Raw8<S>* other) {
+  const int half = (int)a.rot / 2;
+  *own = load8<S>(a.k, at + c);
+  *other = load8<S>(a.k, at + (c >= a.rot || a.inter ? c : c < half ? c + half : c - half));
+}
+// ... turned where they have to be
+template <int S>
+__device__ __forceinline__ void turn_key(const KvStoreArgs& a, const Raw8<S>& own, const Raw8<S>& other, int c,
+                                         const float2* cs, float (&v)[8]) {
+  const int half = (int)a.rot / 2;
+  widen<S>(own, a.in_type, v);
   if (c >= a.rot) return;  // rot is a multiple of 16: a piece turns or does not
   if (a.inter) {
 #pragma unroll
@@ -283,7 +289,7 @@ __device__ __forceinline__ void key_piece(const KvStoreArgs& a, int64_t token, i
   } else {
     const bool low = c < half;
     float w[8];
-    widen<S>(load8<S>(a.k, at + (low ? c + half : c - half)), a.in_type, w);
+    widen<S>(other, a.in_type, w);
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       v[j] = low ? turned(v[j], w[j], cs[c + j]).x : turned(w[j], v[j], cs[c - half + j]).y;
@@ -337,19 +343,37 @@ __global__ __launch_bounds__(kThreads) void kv_store_kernel(KvStoreArgs a, KvGri
       fill_turns(shared_turns, a.positions, a.turns, first, tokens, half, g.q.by_half, a.gain);
       __syncthreads();
     }
-    for (int i = threadIdx.x; i < tokens * per_token; i += kThreads) {
-      const int t = quotient(i, g.by_token), r = i - t * per_token;
-      const int h = quotient(r, g.by_head), p = r - h * per_head;
-      int64_t at;
-      int in;
-      if (h >= heads || !place_of(a.slots[first + t], g.shift, a.n_pages, &at, &in)) continue;
-      float v[8];
-      key_piece<S>(a, first + t, head0 + h, p, shared_turns + t * half, v);
-      uint32_t params;
-      const uint32_t codes = quantise8(v, &params);
-      uint8_t* head = a.pages + at * page_bytes + (int64_t)(head0 + h) * lay.bytes();
-      reinterpret_cast<uint32_t*>(head)[in * (d / 8) + p] = codes;
-      if ((p & 3) == 0) reinterpret_cast<uint32_t*>(head + lay.k_params())[in * (d / 32) + (p >> 2)] = params;
+    constexpr int kPieces = FOUR ? 4 : 1;
+    for (int i0 = threadIdx.x; i0 < tokens * per_token; i0 += kPieces * kThreads) {
+      Raw8<S> own[kPieces], other[kPieces];
+      int token[kPieces], head[kPieces], piece[kPieces], slot[kPieces];
+#pragma unroll
+      for (int e = 0; e < kPieces; ++e) {
+        const int i = i0 + e * kThreads;
+        const int t = quotient(i, g.by_token), r = i - t * per_token, h = quotient(r, g.by_head);
+        token[e] = t;
+        head[e] = head0 + h;
+        piece[e] = r - h * per_head;
+        slot[e] = -1;
+        if (i < tokens * per_token && h < heads) {
+          slot[e] = a.slots[first + t];
+          load_key<S>(a, (first + t) * a.ldk + head[e] * a.ldkh, piece[e] * 8, &own[e], &other[e]);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < kPieces; ++e) {
+        int64_t at;
+        int in;
+        if (!place_of(slot[e], g.shift, a.n_pages, &at, &in)) continue;
+        const int p = piece[e];
+        float v[8];
+        turn_key<S>(a, own[e], other[e], p * 8, shared_turns + token[e] * half, v);
+        uint32_t params;
+        const uint32_t codes = quantise8(v, &params);
+        uint8_t* to = a.pages + at * page_bytes + (int64_t)head[e] * lay.bytes();
+        reinterpret_cast<uint32_t*>(to)[in * (d / 8) + p] = codes;
+        if ((p & 3) == 0) reinterpret_cast<uint32_t*>(to + lay.k_params())[in * (d / 32) + (p >> 2)] = params;
+      }
     }
     return;
   }
