@@ -551,9 +551,9 @@ __device__ __forceinline__ void finish(const State<D, NR>& st, const AttnArgs& a
   const int g = lane >> 4;
 #pragma unroll
   for (int n = 0; n < NR; ++n) {
+    int token, head;
+    if (!row_of(q, it, s, row0 + n * 16 + (lane & 15), &token, &head)) continue;
     if (whole) {
-      int token, head;
-      if (!row_of(q, it, s, row0 + n * 16 + (lane & 15), &token, &head)) continue;
       const float l = st.l[n], f = inverse_of(l);
       const int64_t to = token * a.ldo + head * a.ldoh + g * (D / 4);
 #pragma unroll
@@ -1116,14 +1116,15 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int
   auto at = [&](int k) {
     return parts + ((int64_t)(own.wg + k) * 2 + (k == 0 ? slot : 0)) * kPartFloats<D, ROWS>;
   };
-  const int row = tile * 16 + n;
+  const int row = tile * 16 + n, tok = row / part, h = row - tok * part;
+  const bool there = tok < tokens && h < heads;  // the parts have no other rows
   constexpr int kAhead = 8, kRound = kJoinThreads / 16;
   f32x4 x[kAhead][kJ];
   auto fetch = [&](int k0) __attribute__((always_inline)) {
 #pragma unroll
     for (int e = 0; e < kAhead; ++e) {
       const int k = k0 + e * kJoinWaves;
-      if (k < count) {
+      if (k < count && there) {
 #pragma unroll
         for (int c = 0; c < kJ; ++c)
           x[e][c] = reinterpret_cast<const f32x4*>(at(k))[(tile * kM + column + c) * 64 + lane];
@@ -1186,8 +1187,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int
   for (int w = 0; w < kJoinWaves - 1; ++w)
 #pragma unroll
     for (int c = 0; c < kJ; ++c) o[c] += swap[w][c * 64 + lane];
-  const int tok = row / part, h = row - tok * part;
-  if (tok >= tokens || h >= heads) return;
+  if (!there) return;
   const float inv = inverse_of(l);
   const int token = jp->token + tok, head = jp->head + h;
 #pragma unroll
@@ -1214,7 +1214,8 @@ __global__ __launch_bounds__(kThreads) void attn_join_rows_kernel(AttnArgs a, in
   const int tile = (int)blockIdx.y * 4 + wave, row = tile * 16 + n;
   const Join* jp = joins + own.wg;
   const int slot = uniform(jp->slot), tokens = uniform(jp->tokens), heads = uniform(jp->heads);
-  if (tile * 16 / part >= tokens) return;  // no row of the tile is there
+  const int tok = row / part, h = row - tok * part;
+  if (tok >= tokens || h >= heads) return;  // the parts have no such row
   float m = kEmpty, l = 0.0f;
   f32x4 o[kM];
 #pragma unroll
@@ -1231,8 +1232,6 @@ __global__ __launch_bounds__(kThreads) void attn_join_rows_kernel(AttnArgs a, in
 #pragma unroll
     for (int c = 0; c < kM; ++c) o[c] = o[c] * f + x[c] * g;
   }
-  const int tok = row / part, h = row - tok * part;
-  if (tok >= tokens || h >= heads) return;
   const float inv = inverse_of(l);
   const int token = jp->token + tok, head = jp->head + h;
 #pragma unroll
