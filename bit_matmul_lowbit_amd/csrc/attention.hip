@@ -1011,7 +1011,6 @@ __global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(AttnArgs a, Shap
           op[j] = ops[(j0 + kAhead + j) * 64 + lane];
         }
       }
-      __builtin_amdgcn_sched_barrier(0);
       if (t + 32 > open || !now0 || !now1) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -1022,8 +1021,12 @@ __global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(AttnArgs a, Shap
             for (int e = 0; e < 4; ++e) sc[n][h][e] = e <= sees ? sc[n][h][e] : -INFINITY;
           }
       }
+      // ahead of the other work-group's waves, whose products go on beside it (the three prompts
+      // above, replayed from a graph: 430 to 439 us, 443 to 458 without)
+      __builtin_amdgcn_s_setprio(1);
       weigh<D, kTiles>(st, p, sc, [&](int n) { return c[n]; }, ones);
       __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_setprio(0);
 #pragma unroll
       for (int j0 = 0; j0 < kM; j0 += kAhead) {
 #pragma unroll
