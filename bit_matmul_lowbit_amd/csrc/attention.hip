@@ -989,7 +989,6 @@ __global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(AttnArgs a, Shap
       f16x8 op[kAhead];
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) op[j] = ops[j * 64 + lane];
-      __builtin_amdgcn_sched_barrier(0);
       const bool now0 = there0, now1 = there1;
       there0 = raw.there[0];
       there1 = raw.there[1];
@@ -997,7 +996,6 @@ __global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(AttnArgs a, Shap
       spread_shared<D>(lds[turn ^ 1], raw, q.len, lane, wave, ones);
       load_shared<D>(raw, then, t + 64, lay, place, wave);
       then = find(t + 96);
-      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int n = 0; n < kTiles; ++n) sc[n][0] = sc[n][1] = (f32x4){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
