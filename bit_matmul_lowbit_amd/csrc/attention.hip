@@ -42,7 +42,7 @@
 //   16 chats, 1 to 32767 tokens, the same heads: 56 and 8 us
 //   one token over 4096, 16 heads on 8 of 128: 8.6 and 4.5 us: latency (the lists, q, three
 //     steps of loads and products, the join's launch)
-//   chunks of up to 2048 on three prompts, 32 heads on 8 of 128: 428 us, 700 TFLOP/s of the
+//   chunks of up to 2048 on three prompts, 32 heads on 8 of 128: 412 us, 727 TFLOP/s of the
 //     two products: what the exponentials and the rounding of p take from the matrix units' issue,
 //     with two waves a SIMD for the registers of o
 #include "kv4.h"
@@ -892,7 +892,7 @@ __device__ __forceinline__ void spread_shared(f16x8* lds, Shared<D>& r, int len,
 // Many rows: every wave has kWaveRows of its own, and the four make the operands
 // of 32 tokens together, one step ahead, in two LDS buffers in turn (each wave
 // making all of them for itself, 64 rows a wave, was bound by that: three prompts in chunks of
-// 2048 took 1025 us, now 438).
+// 2048 took 1025 us replayed, now 424).
 // A wave has 32 rows, or 16 of 256 values (32 of those and their q do not fit its registers).
 template <int D>
 constexpr int kManyTiles = D == 256 ? 1 : 2;
