@@ -23,8 +23,8 @@
 // What bounds it: the steps of the second launch, one after another (sums, a filter's end, its
 // list, its narrowing, the draw: one to four microseconds each for their loads and barriers);
 // a work-group reads 30 GB/s, so it must not read a row.  Measured, 151936 FP32 logits: one row
-// with top-k 20 and top-p 0.85 4.5 and 16 us, 64 rows of mixed settings 20 us (2.0 TB/s: FP64
-// weights and LDS atomics) and 55, most for those that keep 20000 tokens.
+// with top-k 20 and top-p 0.85 4.5 and 15 us, 64 rows of mixed settings 20 us (2.0 TB/s: FP64
+// weights and LDS atomics) and 53, most for those that keep 20000 tokens.
 //
 // Weights are exact to 2^-40 (FP64, which runs at the rate of FP32 here) and
 // masses are 64-bit whole numbers, so that sums have no order: LDS atomics may come as
@@ -39,6 +39,7 @@ constexpr int kPart = 4096;      // logits of a part
 constexpr int kPartThreads = kPart / 8;
 constexpr int kBins = 256;       // quarters of an octave; the last one: everything below
 constexpr int kRowThreads = 1024;
+constexpr int kEarly = 10;       // parts whose sums a thread has on their way early: of 163840 logits
 constexpr int kMostParts = 256;
 constexpr int kList = 8192;      // tokens that are held in LDS (64 mixed rows 80 us, 84 with 2048)
 constexpr int kUnit = 51;        // a part's weights are whole numbers of 2^-51: 4096 of them stay below 2^64
@@ -331,6 +332,23 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
     s.base[p] = in.base[row * parts + p];
     s.kept[p] = 0;
   }
+  // Four threads a bin have a part's sums on their way before it is known where they belong (one
+  // row 16.0 us, 14.7 with them; garbage where the row goes by its maximum)
+  const bool only_count = without_mass(a, k);
+  const int own_bin = t & (kBins - 1), part0 = t / kBins;
+  uint32_t early_n[kEarly];
+  uint64_t early_m[kEarly];
+#pragma unroll
+  for (int e = 0; e < kEarly; ++e) {
+    const int p = min(part0 + e * (kRowThreads / kBins), parts - 1);
+    early_n[e] = in.count[(row * parts + p) * kBins + own_bin];
+  }
+  if (!only_count)
+#pragma unroll
+    for (int e = 0; e < kEarly; ++e) {
+      const int p = min(part0 + e * (kRowThreads / kBins), parts - 1);
+      early_m[e] = in.mass[(row * parts + p) * kBins + own_bin];
+    }
   if (t < kBins) {
     s.mass[t] = 0;
     s.count[t] = 0;
@@ -381,30 +399,25 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
     s.down[p] = d < 1000.0 ? (int)d : 1000;
   }
   __syncthreads();
-  // the row's sums up to and with each bin, four threads a bin; in the last bin there are
-  // the other tokens, without mass
-  const bool by_k = k < a.n, by_p = top_p < 1.0f, by_min = min_p > 0.0f, only_count = without_mass(a, k);
-  {
-    const int r = t & (kBins - 1);
-    uint64_t m = 0;
-    uint32_t n = 0;
-#pragma unroll 10
-    for (int p = t / kBins; p < parts; p += kRowThreads / kBins) {
-      const int j = r - 4 * s.down[p];
-      const uint32_t pn = in.count[(row * parts + p) * kBins + max(j, 0)];
-      n += j >= 0 ? pn : 0;
-    }
-    if (!only_count)
-#pragma unroll 10
-      for (int p = t / kBins; p < parts; p += kRowThreads / kBins) {
-        const int down = s.down[p], j = r - 4 * down;
-        const uint64_t pm = in.mass[(row * parts + p) * kBins + max(j, 0)];
-        m += j >= 0 && down + up < 64 ? pm >> ((down + up) & 63) : 0;
-      }
-    if (n && r < kBins - 1) atomicAdd(&s.count[r], n);
-    if (m) atomicAdd(&s.mass[r], (unsigned long long)m);
-    if (t == kBins - 1) s.count[t] = (uint32_t)a.n;
+  // the row's sums up to and with each bin; in the last bin there are the other tokens, without
+  // mass
+  const bool by_k = k < a.n, by_p = top_p < 1.0f, by_min = min_p > 0.0f;
+  auto add_part = [&](int p, uint32_t n, uint64_t m) {
+    const int down = s.down[p], r = own_bin + 4 * down;
+    if (r >= kBins - 1) return;
+    if (n) atomicAdd(&s.count[r], n);
+    if (m) atomicAdd(&s.mass[r], (unsigned long long)to_row(p, m));
+  };
+#pragma unroll
+  for (int e = 0; e < kEarly; ++e) {
+    const int p = part0 + e * (kRowThreads / kBins);
+    if (p < parts) add_part(p, early_n[e], only_count ? 0 : early_m[e]);
   }
+  for (int p = part0 + kEarly * (kRowThreads / kBins); p < parts; p += kRowThreads / kBins) {
+    const int64_t at = (row * parts + p) * kBins + own_bin;
+    add_part(p, in.count[at], only_count ? 0 : in.mass[at]);
+  }
+  if (t == kBins - 1) s.count[t] = (uint32_t)a.n;
   __syncthreads();
   const uint64_t full = s.mass[kBins - 2];
 
