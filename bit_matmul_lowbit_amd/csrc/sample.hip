@@ -84,7 +84,9 @@ __device__ __forceinline__ float temperature_of(const SampleArgs& a, int64_t row
   const float t = a.temperature ? a.temperature[row] : 1.0f;
   return t >= 0x1p-20f ? t : 0.0f;
 }
-__device__ __forceinline__ double octaves(float t) { return 1.4426950408889634074 / (double)t; }
+// (not 0 where the temperature is infinite: a masked logit, -inf, has to stay that; and no
+// less than what leaves 2^-149 times it above FP64's smallest)
+__device__ __forceinline__ double octaves(float t) { return fmax(1.4426950408889634074 / (double)t, 0x1p-400); }
 // A value in octaves, c of them to one.  Rounded before a base is taken off: bases are rounded
 // likewise, and at 1e38 an exact product less a rounded one is no small number.
 __device__ __forceinline__ double in_octaves(float y, double c) {
@@ -432,8 +434,9 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
     const double least2 = (base * 4.0 - 1.0 - bin) * 0.25;  // of v2
     const double guess = fmin(fmax(least2 / c, -3.4028234e38), 3.4028234e38);
     uint32_t key = key_of((float)guess);
-    while (key < kKeyInf - 1 && !(in_octaves(value_of(key), c) >= least2)) ++key;
-    while (key > kKeyNegInf + 1 && in_octaves(value_of(key - 1), c) >= least2) --key;
+    // the guess is off by a step at most (two where a zero of either sign lies there)
+    for (int i = 0; i < 4 && key < kKeyInf && !(in_octaves(value_of(key), c) >= least2); ++i) ++key;
+    for (int i = 0; i < 4 && key > kKeyNegInf + 1 && in_octaves(value_of(key - 1), c) >= least2; ++i) --key;
     return value_of(key);
   };
   // first bin at which a sum (which never falls) reaches what is wanted, or the last

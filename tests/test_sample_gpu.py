@@ -110,6 +110,22 @@ def test_edges_of_the_random_number_and_settings():
     check(y, [0.7] * 12, temperature=[1e-6, 2e-6, 1e-3, 0.05, 1e3, 1e30, 3e38, 1.0, 1.0, 1.0, 1.0, 1.0], least=12)
 
 
+@pytest.mark.parametrize("size", [1.0, 1e-30, 1e6, 1e37])
+def test_temperatures_of_all_magnitudes(size):
+    """From one that leaves a single token to one that makes all alike, over logits of all sizes;
+    the smallest is 2^-20, where neighbouring FP32 logits of 10 are an octave apart."""
+    say("sample temperatures", size)
+    g = np.random.default_rng(41)
+    t = [float("inf"), 3e38, 1e30, 1e6, 50.0, 1.0, 0.02, 1e-3, 2.0 ** -19, 2.0 ** -20]
+    y = logits(g, len(t), 9001, 2.0) * size
+    y[:, 17::5] = -float("inf")
+    for kw in ({}, dict(top_k=[700] * len(t)), dict(top_p=[0.7] * len(t)), dict(min_p=[0.3] * len(t)),
+               dict(top_k=[8500] * len(t), top_p=[0.9] * len(t), min_p=[1e-3] * len(t))):
+        check(y, g.random(len(t)), t, **kw)
+    greedy, _ = lowbit.lowbit_sample(y, dev(g.random(len(t))), dev([0.0, -1.0, float("nan"), 9e-7, -0.0] * 2))
+    assert np.array_equal(greedy.cpu().numpy(), y.cpu().numpy().argmax(1))
+
+
 @pytest.mark.parametrize("n", [5, 5000, 151936])
 def test_what_is_not_finite(n):
     say("sample not finite", n)
