@@ -265,7 +265,8 @@ def test_outputs_on_another_stream_do_not_reuse_its_memory(op):
     (_store, lambda: dict(pages=_pages(0))),
     (_load, lambda: dict(slots=_f(0, dtype="int32"))),
     (_load, lambda: dict(pages=_pages(0))),
-    (_attention, lambda: dict(q=_f(0, 4, D, dtype="float16"), table=_f(0, 2, dtype="int32"), lengths=_f(0, dtype="int32"))),
+    (_attention, lambda: dict(q=_f(0, 4, D, dtype="float16"), table=_f(0, 2, dtype="int32"),
+                              lengths=_f(0, dtype="int32"))),
     (_attention, lambda: dict(table=_f(3, 0, dtype="int32"))),
     (_attention, lambda: dict(pages=_pages(0))),
     (_sample, lambda: dict(y=_f(0, 1000), u=_f(0))),

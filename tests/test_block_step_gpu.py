@@ -122,7 +122,8 @@ def _check_stages(m, pages_before, position):
     assert np.array_equal(held_v[live], P.held(fused[:, HQ + KV:])[live])
     x = fused[:, HQ:HQ + KV]
     turned = P.rope(x, position, turns, False, m.gain)
-    bound = P.held_bound(turned.astype(np.float32)) + 2 * P.rope_bound(x, position, turns, False, m.gain, "float32")[..., None].max(-2)
+    err = P.rope_bound(x, position, turns, False, m.gain, "float32").max(-1, keepdims=True)
+    bound = P.held_bound(turned.astype(np.float32)) + 2 * err
     assert (np.abs(held_k.astype(np.float64) - turned) <= bound)[live].all()
     x = fused[:, :HQ]
     q = P.rope(x, position, turns, False, m.gain)
