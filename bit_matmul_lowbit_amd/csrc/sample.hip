@@ -120,9 +120,12 @@ inline size_t parts_layout(int64_t rows, int64_t parts, void* ws, Parts* p) {
 
 // the quarter octave of v2 = y log2(e) / T on the scale of all parts
 __device__ __forceinline__ double quarter(double v2) { return __builtin_floor(v2 * 4.0); }
+// Quarters from the base down.  A base is a whole number of octaves that no value of its parts
+// passes; one that lies on it is in bin 0, alone.  4 base - q is exact whatever the size, so a
+// part's bin and the octaves from the row's base down to the part's add up to the row's bin.
 __device__ __forceinline__ int bin_of(double q, double base) {
-  const double b = base * 4.0 - 1.0 - q;
-  return b < 0.0 ? 0 : b >= kBins - 1 ? kBins - 1 : (int)b;
+  const double b = base * 4.0 - q;
+  return b >= kBins - 1 ? kBins - 1 : (int)b;
 }
 
 template <int S>
@@ -431,7 +434,7 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a, 
   auto lowest = [&](int bin) {
     if (bin >= kBins - 1) return -INFINITY;
     if (bin < 0) return INFINITY;
-    const double least2 = (base * 4.0 - 1.0 - bin) * 0.25;  // of v2
+    const double least2 = (base * 4.0 - bin) * 0.25;  // of v2
     const double guess = fmin(fmax(least2 / c, -3.4028234e38), 3.4028234e38);
     uint32_t key = key_of((float)guess);
     // the guess is off by a step at most (two where a zero of either sign lies there)
