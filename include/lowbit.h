@@ -627,7 +627,8 @@ size_t lowbit_attention_workspace_bytes(int64_t m, int64_t b, int64_t hq, int64_
  *   workspace : lowbit_attention_workspace_bytes(m, b, hq, heads, d, max_q)
  *             bytes, contents ignored on entry
  * The scores, their maximum and all sums are FP32; p is rounded to FP16 for the
- * product with V, and the sum that divides is that of the rounded p.  No
+ * product with V (off by 2^-11 of itself or 2^-32 of the row's largest p,
+ * whichever is more), and the sum that divides is that of the rounded p.  No
  * atomics; equal inputs give equal bits.
  * 1 <= m <= 2^22, 1 <= b <= 65535, hq a multiple of heads, hq <= 1024, d 64,
  * 128 or 256, tcap * page <= 2^30, n_pages * page < 2^31.  Alignment as for
