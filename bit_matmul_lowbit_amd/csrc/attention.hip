@@ -57,7 +57,7 @@ namespace {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256;
-constexpr float kEmpty = -1e30f;   // a maximum of nothing
+constexpr float kEmpty = -3.4028234663852886e38f;  // m of nothing: no score lies below it
 // log2 of the largest p where m is set, and of what p may reach before it is set again (FP16 holds
 // less than 2^16).  Where a step of the scores is 8, m may lie 8 below instead of 7; where it is
 // larger, m is the maximum.
