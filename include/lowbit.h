@@ -610,8 +610,9 @@ size_t lowbit_attention_workspace_bytes(int64_t m, int64_t b, int64_t hq, int64_
  *   lse[r][h] = ln sum_t p_t
  * A row that sees nothing gives zeros, and -inf.
  *   q       : [m][hq][d], q_type FP16 or BF16, strides ldq / ldqh
- *   pages   : n_pages pages as lowbit_kv_store leaves them (a slot below a
- *             length that was never written: any finite or other value)
+ *   pages   : n_pages pages as lowbit_kv_store leaves them.  A slot below a
+ *             length that was never written: the rows that see it may come to
+ *             anything, the others do not depend on it
  *   table   : [b] rows of tcap int32 at stride ldt: token t of sequence i is in
  *             page table[i][t / page].  Tokens of an entry outside
  *             [0, n_pages) are passed over as if masked

@@ -1,4 +1,5 @@
-"""Attention over the 4-bit cache on the GPU: scores of every magnitude that FP32 holds."""
+"""Attention over the 4-bit cache on the GPU: scores of every magnitude that FP32 holds, slots
+that were never written."""
 import numpy as np
 import pytest
 
@@ -6,6 +7,7 @@ from bit_matmul_lowbit_amd import lowbit
 from tests import plain64_block as P
 from tests.helpers import say
 from tests.plain64 import U, rounding
+from tests.test_attention_gpu import Case
 from tests.test_kv_gpu import dt, host, i32
 
 pytestmark = pytest.mark.gpu
@@ -51,3 +53,39 @@ def test_rows_whose_scores_are_all_far_from_zero(d, group, nq, sign, size):
             assert (np.abs(got[row] - want) <= bound).all(), (scale, row)
             wlse = s.max() + np.log(p.sum())
             assert (np.abs(glse[row] - wlse) <= abs(wlse) * 8 * U + 2.0 ** -10).all(), (scale, row)
+
+
+def never_written(c, token, params):
+    """All bits of a token's codes set, and FP16 patterns `params` as its a and b."""
+    import torch
+
+    page, t = divmod(token, c.page)
+    part = c.pages[int(c.table[0, page])].view(c.heads, -1)
+    g, size = c.d // 32, c.page * c.d // 2
+    a, b = (torch.tensor([v & 255, v >> 8], dtype=torch.uint8, device="cuda") for v in params)
+    part[:, :size].view(c.heads, c.page, -1)[:, t] = 255
+    part[:, size:size + c.page * g * 4].view(c.heads, c.page, g, 2, 2)[:, t] = torch.stack([a, b])
+    base = size + c.page * g * 4
+    part[:, base:base + size].view(c.heads, c.page // 4, c.d // 2, 4)[:, t // 4, :, P.V_BYTE[t % 4]] = 255
+    vp = part[:, base + size:].view(c.heads, c.page // 4, g, 2, 4, 2)
+    vp[:, t // 4, :, 0, t % 4], vp[:, t // 4, :, 1, t % 4] = a, b
+
+
+@pytest.mark.parametrize("params", [(0xFFFF, 0xFFFF), (0x7C00, 0xFC00), (0x7BFF, 0x7BFF), (0x7BFF, 0x0000), (0xFBFF, 0xFBFF),
+                                    (0x0000, 0x7C00), (0x7E00, 0x0000)])
+@pytest.mark.parametrize("hq,heads,d,nq", [(1, 1, 64, 4), (4, 2, 128, 8), (6, 1, 256, 3), (2, 1, 64, 16), (4, 2, 256, 12), (1, 1, 128, 33),
+                                           (8, 2, 64, 12), (4, 1, 128, 16), (4, 1, 64, 60), (2, 2, 128, 130), (3, 1, 256, 70)])
+def test_rows_do_not_depend_on_slots_that_only_later_ones_see(hq, heads, d, nq, params):
+    """A padded chunk: the last tokens' keys and values were not written, and the pages came as
+    they were."""
+    import torch
+
+    say("attention never written", hq, heads, d, nq, params)
+    for n, last in ((nq, 1), (150, 2), (262, 1)):
+        c = Case([max(n, nq)], [nq], hq, heads, d, 32, seed=nq)
+        want, wlse = c.run()
+        for token in range(c.lens[0] - last, c.lens[0]):
+            never_written(c, token, params)
+        got, lse = c.run()
+        assert torch.isfinite(want).all()
+        assert torch.equal(got[:nq - last], want[:nq - last]) and torch.equal(lse[:nq - last], wlse[:nq - last])
