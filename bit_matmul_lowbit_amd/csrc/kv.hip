@@ -7,7 +7,7 @@
 //
 // Angles: a pair turns by position * frequency.  The frequency is held as a 64-bit
 // fraction of a turn, so the product wraps by itself and no position is too far:
-// the angle is exact to 2^-63 of a half turn times the position.  Sine and
+// the angle is off by 2^-62 of a half turn times the position at most.  Sine and
 // cosine are FP64 (which runs at the rate of FP32 here), rounded once to FP32, one
 // pair per token and frequency, kept in LDS for all heads.
 //

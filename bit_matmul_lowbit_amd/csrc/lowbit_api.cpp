@@ -564,23 +564,28 @@ int lowbit_rope_turns(int64_t rot, double theta, int scaling, double factor, int
     return LOWBIT_ERR_ARG;
   if (rot < 2 || rot > 1024 || rot % 2 != 0) return LOWBIT_ERR_SHAPE;
   if (scaling == LOWBIT_ROPE_NTK && rot == 2) return LOWBIT_ERR_SHAPE;
-  const double pi = 3.14159265358979323846, half = 0.5 * (double)rot;
-  if (scaling == LOWBIT_ROPE_NTK) theta *= std::pow(factor, (double)rot / (double)(rot - 2));
-  double low = 0.0, high = 1.0;
+  // 64 bits of mantissa: FP64's 53 would leave the fastest pairs 2^-57 of a turn off a position,
+  // 1e-7 radians at position 10^9
+  const long double two_pi = 6.28318530717958647692528676655900577L, half = 0.5L * (long double)rot, by = factor;
+  long double base = theta;
+  if (scaling == LOWBIT_ROPE_NTK) base *= std::pow(by, (long double)rot / (long double)(rot - 2));
+  long double low = 0.0L, high = 1.0L;
   if (scaling == LOWBIT_ROPE_YARN) {
     // the pair that turns `beta` times within the trained length
-    auto pair = [&](double beta) { return half * std::log((double)trained / (beta * 2.0 * pi)) / std::log(theta); };
-    low = std::fmax(std::floor(pair(beta_fast)), 0.0);
-    high = std::fmin(std::ceil(pair(beta_slow)), (double)(rot - 1));
+    auto pair = [&](long double beta) {
+      return half * std::log((long double)trained / (beta * two_pi)) / std::log(base);
+    };
+    low = std::fmax(std::floor(pair(beta_fast)), 0.0L);
+    high = std::fmin(std::ceil(pair(beta_slow)), (long double)(rot - 1));
   }
   for (int64_t i = 0; i < rot / 2; ++i) {
-    double f = std::pow(theta, -(double)i / half);
-    if (scaling == LOWBIT_ROPE_LINEAR) f /= factor;
+    long double f = std::pow(base, -(long double)i / half);
+    if (scaling == LOWBIT_ROPE_LINEAR) f /= by;
     if (scaling == LOWBIT_ROPE_YARN) {
-      const double ramp = std::fmin(std::fmax(((double)i - low) / std::fmax(high - low, 0.001), 0.0), 1.0);
-      f = f / factor * ramp + f * (1.0 - ramp);
+      const long double ramp = std::fmin(std::fmax(((long double)i - low) / std::fmax(high - low, 0.001L), 0.0L), 1.0L);
+      f = f / by * ramp + f * (1.0L - ramp);
     }
-    turns[i] = (uint64_t)(f / (2.0 * pi) * 18446744073709551616.0);  // f <= 1: below 2^64
+    turns[i] = (uint64_t)(f / two_pi * 0x1p64L + 0.5L);  // f <= 1: below 2^62
   }
   if (gain) *gain = scaling == LOWBIT_ROPE_YARN ? 0.1 * std::log(factor) + 1.0 : 1.0;
   return LOWBIT_OK;

@@ -534,7 +534,7 @@ int lowbit_lora_accumulate(const void* x, int x_type, int64_t ldx, const int32_t
 /* Frequencies of rotary positions as the kernels take them, host only:
  * pair i of rot / 2 turns by f_i = theta^(-2 i / rot) radians a position,
  * scaled; turns[i] = f_i / (2 pi) * 2^64 mod 2^64 (a fraction of a turn, so
- * that position * turns wraps by itself).
+ * that position * turns wraps by itself), off by less than 2.
  *   rot       : values of a head that turn, even, 2..1024
  *   scaling   : lowbit_rope_scaling; factor >= 1 (NTK: rot > 2), trained >= 1
  *               (YaRN) the length that the frequencies were trained at
