@@ -26,10 +26,11 @@
 // with top-k 20 and top-p 0.85 4.5 and 15 us, 64 rows of mixed settings 20 us (2.0 TB/s: FP64
 // weights and LDS atomics) and 53, most for those that keep 20000 tokens.
 //
-// Weights are exact to 2^-40 (FP64, which runs at the rate of FP32 here) and
-// masses are 64-bit whole numbers, so that sums have no order: LDS atomics may come as
-// they like, equal inputs give equal bits, and a draw among 150000 tokens finds the
-// token that 64-bit arithmetic finds.
+// Weights are made to 2^-40 relative (FP64, which runs at the rate of FP32 here) and rounded to whole
+// numbers of 2^-51 of a part's base.  Where a row's are added they are cut to 2^-49 of its base, or to
+// what leaves room for n of them in 62 bits (2^-44 for 151936; a weight below that counts nothing).
+// So sums have no order: LDS atomics may come as they like, equal inputs give equal bits, and a
+// draw among 150000 tokens finds the token that 64-bit arithmetic finds unless it is that close.
 #include "pieces.h"
 
 namespace lowbit {

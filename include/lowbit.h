@@ -668,9 +668,10 @@ size_t lowbit_sample_workspace_bytes(int64_t n, int64_t b);
  *   workspace   : lowbit_sample_workspace_bytes(n, b) bytes, contents ignored
  *                 on entry
  * A row that has NaN or +inf: the lowest token of the largest value (NaN
- * counting as largest), prob 1.  w is kept to 2^-40 relative (or 2^-52 |y| /
- * temperature, where that is more) and, below 2^(ceil(log2 n) - 62) of the largest,
- * counts as 0.  Equal inputs give equal bits.
+ * counting as largest), prob 1.  w is exact to 2^-40 relative (or 2^-52 |y| /
+ * temperature, where that is more), and counts as a multiple of a step s of at most
+ * 2^(1 - min(49, 62 - ceil(log2 n))), off by less than s: one below s may count as 0.
+ * Equal inputs give equal bits.
  * 1 <= n <= 2^20, 1 <= b <= 65535.  Alignment: elements; workspace 16 bytes. */
 int lowbit_sample(const void* y, int y_type, int64_t ldy, int64_t n, int64_t b,
                   const float* temperature, const int32_t* top_k, const float* top_p,

@@ -107,3 +107,40 @@ def test_parts_of_zeros_and_others(sign):
     for shift in range(3):  # the parts in other orders
         check_rows([np.roll(r, shift * 4096) for r in rows], settings, g.random(len(rows)))
     check_rows([r[::-1].copy() for r in rows], settings, g.random(len(rows)))
+
+
+@pytest.mark.parametrize("n,behind", [(2, [-33.9, -34.0, -34.2]), (4096, [-33.9, -34.0, -34.2]), (1 << 14, [-33.2, -33.3]),
+                                      (151936, [-30.45, -30.55]), (1 << 20, [-29.1, -29.2])])
+def test_the_least_weights_that_count(n, behind):
+    """One logit behind another, which is a whole octave: with u = 0 it is drawn if it weighs
+    something.  A weight is cut to a whole number of 2^-unit.  In the part of the largest it has been
+    rounded to one of 2^-51 before, so it counts from 1 - 2^(unit - 52) of 2^-unit on there, which is
+    7/8 at unit 49 (a logit of -34.098); in another part its own base is 48 octaves lower, and that
+    rounding no matter."""
+    unit = min(49, 62 - int(np.ceil(np.log2(n))))
+    for first, last in ((0, n - 1), (n // 2 - 1, n // 2)):
+        least = (1 - (2.0 ** (unit - 52) if first // 4096 == last // 4096 else 0.0)) * 2.0 ** -unit
+        rows = np.full((len(behind), n), -np.inf)
+        rows[:, last] = 0.0
+        rows[:, first] = behind
+        idx, prob = lowbit.lowbit_sample(dev(rows), dev([0.0] * len(behind)))
+        w = np.exp(np.float32(behind).astype(np.float64))
+        assert (np.abs(w / least - 1) > 1e-3).all() and w[0] > least > w[-1]
+        assert idx.tolist() == [first if v > least else last for v in w]
+        assert abs(float(prob[0]) / w[0] - 1) < 1e-5
+
+
+@pytest.mark.parametrize("sigma", [4.0, 15.0, 60.0])
+def test_every_token_is_one_that_the_filters_keep(sigma):
+    """Rows so uneven that the nearest decision is often closer than the weights' steps."""
+    say("sample uneven", sigma)
+    g = np.random.default_rng(int(sigma))
+    n = 20000
+    rows, settings = [], []
+    for i in range(48):
+        y = g.standard_normal(n) * sigma
+        y[g.integers(0, n, 4000)] = np.float32(y.max() - (i % 8))
+        rows.append(y.astype(np.float32))
+        settings.append(dict(temperature=float(g.choice([0.3, 1.0, 2.0])), top_k=int(g.choice([0, 3, 700, 4001, 9000])),
+                             top_p=float(g.choice([0.2, 0.9, 0.9999, 1.0])), min_p=float(g.choice([0.0, 0.01, 0.5]))))
+    check_rows(rows, settings, g.choice([0.0, 1e-7, 0.5, 1.0], 48))
