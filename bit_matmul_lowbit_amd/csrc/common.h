@@ -317,6 +317,7 @@ size_t attention_workspace_bytes(int64_t hq, int64_t heads, int64_t d, int64_t m
 hipError_t launch_attention(const AttnArgs& a, void* ws, hipStream_t st);
 
 // a token drawn from each row of logits (arguments as in the C ABI)
+constexpr int64_t kSampleMost = int64_t(1) << 20;  // logits of a row
 struct SampleArgs {
   const void* y;
   const float *temperature, *top_p, *min_p, *u;

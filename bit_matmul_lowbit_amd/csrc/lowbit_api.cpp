@@ -81,8 +81,7 @@ bool attention_ok(int64_t m, int64_t b, int64_t hq, int64_t heads, int64_t d, in
   return d == 64 || d == 128 || d == 256;
 }
 
-// a part's place in the sampler's lists has 20 bits
-bool sample_ok(int64_t n, int64_t b) { return n >= 1 && n <= (int64_t(1) << 20) && b >= 1 && b <= 65535; }
+bool sample_ok(int64_t n, int64_t b) { return n >= 1 && n <= lowbit::kSampleMost && b >= 1 && b <= 65535; }
 
 bool logits_shape_ok(int64_t n, int64_t b) {
   // the grid's threads (one per 16 logits) stay below 2^32

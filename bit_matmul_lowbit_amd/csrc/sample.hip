@@ -42,6 +42,7 @@ constexpr int kBins = 256;       // quarters of an octave; the last one: everyth
 constexpr int kRowThreads = 1024;
 constexpr int kEarly = 10;       // parts whose sums a thread has on their way early: of 163840 logits
 constexpr int kMostParts = 256;
+static_assert((int64_t)kMostParts * kPart >= kSampleMost, "a row's parts have their places in LDS");
 constexpr int kList = 8192;      // tokens that are held in LDS (64 mixed rows 80 us, 84 with 2048)
 constexpr int kUnit = 51;        // a part's weights are whole numbers of 2^-51: 4096 of them stay below 2^64
 
