@@ -23,7 +23,8 @@
 // A code becomes FP16(a (1 + c / 16) + b) with a shift, a mask and half a packed
 // FMA: it is put into the mantissa of 1.0.  Keys and values of the cache are FP16
 // numbers by definition, so nothing is lost there; BF16 queries are scaled by a power
-// of two a row, which is exact.  The sum of p is a product with ones, of the same
+// of two a row, which is exact down to 2^-31 of the row's largest (FP16's least numbers: what is
+// smaller is off by 2^-39 of the largest).  The sum of p is a product with ones, of the same
 // rounded p.
 //
 // m is not the maximum but lies 7 below the one that set it, and is set again only where a score
@@ -31,7 +32,7 @@
 // the largest and is off by 2^-32 of that at most below (with m at the maximum: 2^-14 and 2^-25,
 // and what many tokens have together behind one of most of the mass was 25 % off, or gone).  Most
 // steps neither exchange lanes nor rescale o.  m lower still takes away from what a score may rise:
-// 10 below, chunks of three prompts take 420 us for 416, 12 below 434.
+// 10 below costs chunks of three prompts 1 %, 12 below 4 %.
 //
 // Work.  All (sequence, KV head, tile) items are cut into units of 128 tokens (or as
 // many as a tile has, if they are more), and the units of all items, one after another, are
@@ -43,10 +44,12 @@
 // Measured (a 1 GiB copy moves 5.2 TB/s, an 8192^3 product of the library 1.2 PFLOP/s here):
 //   one token over 262144, 24 heads on 4 of 256: 65 us and 8 for the join, 335 MB, the
 //     cache read at 5.2 TB/s: bound by memory
-//   16 chats, 1 to 32767 tokens, the same heads: 56 and 8 us
-//   one token over 4096, 16 heads on 8 of 128: 8.6 and 4.5 us: latency (the lists, q, three
+//   16 chats, 1 to 32767 tokens, the same heads: 57 and 8 us
+//   one token over 4096, 16 heads on 8 of 128: 8.0 and 5.4 us: latency (the lists, q, three
 //     steps of loads and products, the join's launch)
-//   chunks of up to 2048 on three prompts, 32 heads on 8 of 128: 412 us, 727 TFLOP/s of the
+//   four tokens of those 16 chats: 86 us for the same bytes.  attn_kernel<256, 2> keeps 12 registers in
+//     memory, <128, 4> 47 and <64, 4> 13
+//   chunks of up to 2048 on three prompts, 32 heads on 8 of 128: 420 us, 713 TFLOP/s of the
 //     two products: what the exponentials and the rounding of p take from the matrix units' issue,
 //     with two waves a SIMD for the registers of o
 #include "kv4.h"
@@ -911,7 +914,7 @@ __device__ __forceinline__ void spread_shared(f16x8* lds, Shared<D>& r, int open
 // Many rows: every wave has kWaveRows of its own, and the four make the operands
 // of 32 tokens together, one step ahead, in two LDS buffers in turn (each wave
 // making all of them for itself, 64 rows a wave, was bound by that: three prompts in chunks of
-// 2048 took 1025 us replayed, now 424).
+// 2048 take 967 us by that kernel, 420 by this one).
 // A wave has 32 rows, or 16 of 256 values (32 of those and their q do not fit its registers).
 template <int D>
 constexpr int kManyTiles = D == 256 ? 1 : 2;
@@ -1039,7 +1042,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(AttnArgs a, Shap
           }
       }
       // ahead of the other work-group's waves, whose products go on beside it (the three prompts
-      // above, replayed from a graph: 430 to 439 us, 443 to 458 without)
+      // above: 4 % less time)
       __builtin_amdgcn_s_setprio(1);
       weigh<D, kTiles>(st, p, sc, [&](int n) { return c[n]; }, ones);
       __builtin_amdgcn_sched_barrier(0);
@@ -1274,15 +1277,15 @@ int log2_of(int64_t v) {
 // Which kernel, by the rows that a KV head's queries have at most in a sequence:
 // the waves split the tokens while one of them can hold the rows (nr tiles of 16),
 // beyond they split the rows.  Both sides, us a call replayed from a graph:
-//   up to 16 rows, for 16 or 32: one chat of 4096 14.5 and 16.7, of 262144 84 and 97,
-//     16 mixed chats 72 and 84
-//   17 to 32, for 32 or 64: 8 tokens of a chat of 4096 18 and 27, of 16 chats 49 and 74;
-//     4 tokens of 16 mixed chats, heads of 256, 94 and 158
-//   33 to 64, split by tokens or by rows: 16 tokens of a chat of 4096 29 and 39, of 32768 52
-//     and 74, of four of those 93 and 125; but of 16 chats of 4096 90 and 73.  The lengths are on
+//   up to 16 rows, for 16 or 32: one chat of 4096 13.7 and 15.9, of 262144 81 and 83,
+//     16 mixed chats 57 and 67
+//   17 to 32, for 32 or 64: 8 tokens of a chat of 4096 18 and 26, of 16 chats 49 and 71;
+//     4 tokens of 16 mixed chats, heads of 256, for 32 or by rows 82 and 150
+//   33 to 64, split by tokens or by rows: 16 tokens of a chat of 4096 29 and 38, of 32768 54
+//     and 71, of four of those 90 and 109; but of 16 chats of 4096 89 and 63.  The lengths are on
 //     the device; the longer ones decide.  (Heads of 256 would need 64 more registers.)
-//   beyond: chunks of 2048 of three prompts 438 by rows, 1025 by tokens; 128 rows of a chat of
-//     4096 39 and 36
+//   beyond: chunks of 2048 of three prompts 420 by rows, 967 by tokens; 128 rows of a chat of
+//     4096 40 and 37
 struct Variant {
   int nr;  // 0: attn_rows_kernel
   int rows;

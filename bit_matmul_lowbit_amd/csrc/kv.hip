@@ -1,9 +1,9 @@
-// Rotary positions, and a cache of keys and values in 4 bits as it is written
+// Rotary positions, and a cache of keys and values in 4-bit codes as it is written
 // and read back.
 //
 // [P2] 7minutos.es, "PrismML lanza Bonsai 27B ...", "La memoria es la
 //      restriccion vinculante": the cache of 262144 tokens takes a quarter in 4
-//      bits of what it takes in FP16.
+//      bits of what it takes in FP16.  With a and b here it is 5 bits, 5/16.
 //
 // Angles: a pair turns by position * frequency.  The frequency is held as a 64-bit
 // fraction of a turn, so the product wraps by itself and no position is too far:
@@ -18,10 +18,11 @@
 // What bounds them: memory where tokens are many, a launch and two latencies
 // where they are few.  Measured (a 1 GiB copy moves 5.2 TB/s here):
 //   8192 tokens of 32 heads of 128 turned: 28.5 us, 4.7 TB/s
-//   4096 tokens written, 32 heads of q turned beside 8 of K and V: 28.6 us, 3.1 TB/s (the q's part
-//     alone takes 14, K and V 10: their groups of four tokens and heads leave threads idle)
-//   32768 tokens of 4 heads of 256 read back: 41 us, 4.3 TB/s
-//   one token written and read back: 3.6 and 2.0 us
+//   4096 tokens written, 32 heads of q turned beside 8 of K and V: 27.1 us, 3.3 TB/s (the q's part
+//     alone takes 14, K and V 10; a row's loads wait for the cosines and their barrier, one
+//     memory latency after another in work-groups as short as these)
+//   32768 tokens of 4 heads of 256 read back: 40.6 us, 4.3 TB/s
+//   one token written and read back: 3.6 and 2.1 us
 #include "kv4.h"
 #include "pieces.h"
 
@@ -316,9 +317,11 @@ __device__ __forceinline__ uint32_t gather_bytes(const uint32_t (&w)[4], int e) 
 }
 
 // FOUR: an item of V is four tokens, which is one 16-byte store where they
-// are four neighbours of a page that start at a multiple of four.  (4096 tokens in order: 29.0 us,
-// one by one 30.0, and read back 43.7 against 56 for 32768; scattered 40.8 against 37.2.)  The host
-// does not see the slots: for four tokens and more, of which a prompt's are the many.
+// are four neighbours of a page that start at a multiple of four; the others go byte by byte.  The
+// host does not see the slots: for four tokens and more, of which a prompt's are the many.  Both
+// sides, us, by fours and one by one (inputs from memory; 8 heads of 128, BF16, 32 of q): 4096 tokens in
+// order 27.6 and 28.2, in order from another slot 29.6 and 28.7, scattered 34.9 and 33.1; 500 in order 8.0
+// and 8.0.  4 heads of 256, FP32: single tokens of 61 chats 6.6 and 6.6, of 1000 20.0 and 17.6.
 template <int S, bool FOUR>
 __global__ __launch_bounds__(kThreads) void kv_store_kernel(KvStoreArgs a, KvGrid g) {
   const int64_t first = (int64_t)blockIdx.x * g.tokens;
@@ -438,6 +441,9 @@ __device__ __forceinline__ void values8(uint32_t w, uint32_t params, float (&v)[
 // Pieces of K that a thread has on their way (32768 tokens, 4 heads of 256: 43.7 us, 50 with one)
 constexpr int kAhead = 4;
 
+// FOUR as above, us by fours and one by one (a graph's calls): 4096 tokens of 8 heads of 128 in order 6.5
+// and 8.7, from another slot 8.1 and 8.4; 32768 of 4 of 256 28.8 and 34.7, from another slot 35.0 and
+// 35.4; 64 in order 3.2 and 3.4, but single tokens of 61 chats 4.1 and 3.4.
 template <bool FOUR>
 __global__ __launch_bounds__(kThreads) void kv_load_kernel(KvLoadArgs a, KvGrid g) {
   const int64_t first = (int64_t)blockIdx.x * g.tokens;

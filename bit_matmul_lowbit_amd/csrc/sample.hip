@@ -23,8 +23,8 @@
 // What bounds it: the steps of the second launch, one after another (sums, a filter's end, its
 // list, its narrowing, the draw: one to four microseconds each for their loads and barriers);
 // a work-group reads 30 GB/s, so it must not read a row.  Measured, 151936 FP32 logits: one row
-// with top-k 20 and top-p 0.85 4.5 and 15 us, 64 rows of mixed settings 20 us (2.0 TB/s: FP64
-// weights and LDS atomics) and 53, most for those that keep 20000 tokens.
+// with top-k 20 and top-p 0.85 4.4 and 14.4 us, 64 rows of mixed settings 21 us (1.9 TB/s: FP64
+// weights and LDS atomics) and 52, most for those that keep 20000 tokens.
 //
 // Weights are made to 2^-40 relative (FP64, which runs at the rate of FP32 here) and rounded to whole
 // numbers of 2^-51 of a part's base.  Where a row's are added they are cut to 2^-49 of its base, or to
@@ -40,7 +40,9 @@ constexpr int kPart = 4096;      // logits of a part
 constexpr int kPartThreads = kPart / 8;
 constexpr int kBins = 256;       // quarters of an octave; the last one: everything below
 constexpr int kRowThreads = 1024;
-constexpr int kEarly = 10;       // parts whose sums a thread has on their way early: of 163840 logits
+// parts whose sums a thread has on their way early (of 163840 logits; one row with top-k 20: 151936
+// 18.7 us, 163841 19.2, 262144 21.1)
+constexpr int kEarly = 10;
 constexpr int kMostParts = 256;
 static_assert((int64_t)kMostParts * kPart >= kSampleMost, "a row's parts have their places in LDS");
 constexpr int kList = 8192;      // tokens that are held in LDS (64 mixed rows 80 us, 84 with 2048)

@@ -705,7 +705,7 @@ def lowbit_kv_page_bytes(heads: int, d: int, page: int) -> int:
 
 def lowbit_kv_store(k, v, slots, pages, page: int, positions=None, turns=None, interleaved=False, gain=1.0, q=None,
                     q_out=None, q_dtype=None, stream=None):
-    """k and v [m][heads][d] written to a cache held in 4 bits, at slots int32
+    """k and v [m][heads][d] written to a cache in 4-bit codes (5 bits a value), at slots int32
     [m] (outside the cache: not written) of pages uint8
     [pages][lowbit_kv_page_bytes(heads, d, page)].
 
@@ -731,7 +731,7 @@ def lowbit_attention_workspace_bytes(m: int, b: int, hq: int, heads: int, d: int
 
 def lowbit_attention(q, pages, page: int, table, lengths, q_start=None, max_q=None, scale=None, out=None,
                      out_dtype=None, lse=None, workspace=None, stream=None):
-    """Attention of q [m][hq][d] (FP16 or BF16) over a cache held in 4 bits;
+    """Attention of q [m][hq][d] (FP16 or BF16) over a cache in 4-bit codes;
     returns out [m][hq][d] (made with out_dtype, or q's type, if not given).
 
     Sequence i has lengths[i] tokens in the pages table[i] (int32 [b][.]), and its

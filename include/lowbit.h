@@ -508,9 +508,11 @@ int lowbit_lora_accumulate(const void* x, int x_type, int64_t ldx, const int32_t
 /* ---------------------------------------------------------------------------
  * BETWEEN THE QKV PRODUCT AND THE OUTPUT PRODUCT
  *
- * Rotary positions, a cache of keys and values in 4 bits, and attention over
- * it  [P2 "La memoria es la restriccion vinculante": the cache of 262144
- * tokens takes a quarter in 4 bits of what it takes in FP16].
+ * Rotary positions, a cache of keys and values in 4-bit codes, and attention
+ * over it  [P2 "La memoria es la restriccion vinculante": the cache of 262144
+ * tokens takes a quarter in 4 bits of what it takes in FP16].  With the two
+ * numbers that 32 codes share it is 5 bits a value here, 5/16 of FP16: 5.4 GB
+ * for the 262144 tokens of 16 layers of 4 heads of 256.
  *
  * THE CACHE.  Pages of `page` tokens (16, 32, 64, 128 or 256) for `heads` KV
  * heads of d values (64, 128 or 256); slot s is token s % page of page
@@ -609,7 +611,8 @@ size_t lowbit_attention_workspace_bytes(int64_t m, int64_t b, int64_t hq, int64_
  *   p_t = exp(scale * q[r][h] . K[t][h / (hq / heads)])
  *   lse[r][h] = ln sum_t p_t
  * A row that sees nothing gives zeros, and -inf.
- *   q       : [m][hq][d], q_type FP16 or BF16, strides ldq / ldqh
+ *   q       : [m][hq][d], q_type FP16 or BF16, strides ldq / ldqh (BF16: what is
+ *             below 2^-31 of a row's largest is off by up to 2^-39 of that)
  *   pages   : n_pages pages as lowbit_kv_store leaves them.  A slot below a
  *             length that was never written: the rows that see it may come to
  *             anything, the others do not depend on it
